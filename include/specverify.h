@@ -76,6 +76,7 @@ typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype_t;
 #define SV_DEV_DUP_SIBLING 32u   /* target-only tree: a sibling repeats a token; the repeat is skipped    */
 #define SV_DEV_TIMEOUT 64u       /* a bounded wait inside a kernel gave up (never expected): this call's   */
                                  /* outputs are undefined and the workspace must be zero-filled again      */
+#define SV_DEV_SLOT_RANGE 128u   /* a page id, slot or position lies outside the KV cache: it is skipped   */
 
 /*
  * Outputs of one call (all DEVICE pointers, caller-owned).  max_len is the
@@ -377,6 +378,156 @@ sv_status_t spec_verify_build_tree(const int32_t* parents, const int64_t* seq_le
                                    int64_t* positions, uint8_t* mask, int32_t* retrieve_index,
                                    int32_t* first_child, int32_t* next_sibling, uint32_t* status,
                                    cudaStream_t stream);
+
+/*
+ * A paged KV cache, as the attention and commit calls below take it.  (The
+ * pages describe verification on top of such a cache - [E2D] §2.4 the tree
+ * mask over committed history and draft nodes, §5.6.6 and §8.1 the committed
+ * KV slots - without fixing its layout.)
+ *
+ * k and v are [layers, pages, page_size, heads, head_dim] arrays with the same
+ * strides (in elements); head_dim is dense, every other axis may have any
+ * stride (head-major pages are a matter of strides).  Slot s is entry
+ * s % page_size of page s / page_size.  Position x of request b is entry
+ * x % page_size of page page_table[b * ld_table + x / page_size]; the table
+ * has max_pages entries a request, so positions [0, max_pages * page_size)
+ * exist.  Base pointers must be 16-byte aligned; head_dim and every stride,
+ * in bytes, multiples of 16; head_dim <= 256.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  sv_dtype_t dtype;
+  int32_t layers;
+  int32_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int64_t layer_stride;
+  int64_t page_stride;
+  int64_t slot_stride;
+  int64_t head_stride;
+  const int32_t* page_table; /* [batch, ld_table], device */
+  int32_t max_pages;
+  int64_t ld_table;
+} sv_kv_cache_t;
+
+/*
+ * Attention of each request's new rows (a single decoded token, a draft chain,
+ * a ragged block or a draft tree) over its committed history in the paged
+ * cache and over the new rows themselves ([E2D] §2.4: each node sees the
+ * committed history, its ancestors and itself).
+ *
+ * Request b owns rows [b * max_len, (b + 1) * max_len), or, with cu_seqlens,
+ * [cu_seqlens[b], cu_seqlens[b+1]) of length 1..max_len.  Its row i has query
+ * heads q[row * q_row_stride + h * q_head_stride + d] (cache dtype), h <
+ * num_heads, a multiple of the cache's heads; query head h reads cache head
+ * h / (num_heads / heads).  The row sees positions [0, seq_lens[b]) and, of the
+ * request's own rows, row j iff mask[b][i][j] != 0 (mask: [batch, max_len,
+ * max_len] uint8, the format spec_verify_build_tree writes), or j <= i when
+ * mask is NULL.  The K/V of the request's rows are already in the cache, at
+ * row_slots[row], or at positions seq_lens[b] + j when row_slots is NULL.
+ *
+ *   s_x = scale * (q . k_x)   out = sum_x softmax(s)_x v_x   lse = ln sum_x exp(s_x)
+ *
+ * with fp32 statistics and sums; out (cache dtype, its own row and head
+ * strides) is rounded once.  lse [total_rows, num_heads] fp32 may be NULL.  A
+ * row that sees nothing, or only scores of -inf, has out 0 and lse -inf.  K/V
+ * of entries a row does not see do not influence it, whatever they hold.
+ *
+ * dev_status [batch]: SV_DEV_BAD_LAYOUT for an invalid row range (the request's
+ * rows are left unwritten) or a negative seq_lens[b] (taken as 0);
+ * SV_DEV_SLOT_RANGE when a page, slot or position lies outside the cache (its
+ * entry is not seen).  max_len * num_heads may be at most 2^24, batch at most
+ * 65535.  ws: at least spec_verify_attention_workspace_bytes(...)
+ * bytes, zero-filled before its first use and left zeroed where it matters by
+ * every call; a workspace that served another entry point is zero-filled again.
+ */
+size_t spec_verify_attention_workspace_bytes(int32_t batch, int32_t max_len, int32_t num_heads, int32_t kv_heads,
+                                             int32_t head_dim);
+
+sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                        int32_t num_heads, const sv_kv_cache_t* cache, int32_t layer, int32_t batch,
+                                        int64_t total_rows, int32_t max_len, const int32_t* cu_seqlens,
+                                        const int64_t* seq_lens, const int64_t* row_slots, const uint8_t* mask,
+                                        float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                                        float* lse, uint32_t* dev_status, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
+/*
+ * The KV move that a verification's commit lists describe ([E2D] §5.6.6,
+ * §8.1): for every request b and entry e in [commit_cu[b], commit_cu[b+1]), in
+ * every layer, K and V of slot commit_src_slot[e] are copied to position
+ * commit_dst_pos[e] of the request.  All of a request's reads come before its
+ * writes, so its sources and destinations may overlap (drafts staged in
+ * place); those of different requests must not.  A request commits at most
+ * max_len (<= 1024) entries, and the lists hold list_len entries.
+ * dev_status [batch] (may be NULL): SV_DEV_BAD_LAYOUT when the request's range
+ * is invalid (nothing is moved), SV_DEV_SLOT_RANGE when an entry's slot or
+ * position lies outside the cache (that entry is not moved).
+ */
+sv_status_t spec_verify_kv_commit(const sv_kv_cache_t* cache, int32_t batch, int32_t max_len, int64_t list_len,
+                                  const int32_t* commit_cu, const int64_t* commit_src_slot,
+                                  const int64_t* commit_dst_pos, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Log probabilities of given tokens, with each row's entropy and its most
+ * likely alternatives ([E2D] §6.2: the target distribution softmax(l / T)).
+ * (What serving returns beside committed tokens, and what draft training takes
+ * its loss from.)
+ *
+ * Output i of n describes logits row row_index[i] (row i when row_index is
+ * NULL; -1 is padding, so a verification's accept_rows can be passed as it is;
+ * any other index outside [0, rows) is treated as padding and flagged
+ * SV_DEV_BAD_LAYOUT).  With T = row_temp[i] (1 when row_temp is NULL, or for a
+ * greedy temperature: the unscaled distribution) and M the largest usable
+ * logit (NaN and +inf are ignored and flagged SV_DEV_NONFINITE, as is an all
+ * -inf row):
+ *   row_max[i] = M,  log_z[i] = ln sum_v exp((l_v - M) / T)
+ *   logprob[i][j] = (l_id - M) / T - log_z   for id = ids[i * ldi + j]
+ *   entropy[i] = - sum_v p_v ln p_v
+ *   top_ids / top_logprob [i][k]: the k-th most likely token, equal logits
+ *     resolving to the lowest index; -1 and -inf where fewer than top_k tokens
+ *     have a logit above -inf
+ * logprob is 0 for id -1 (padding), -inf for a token without probability and
+ * for an id outside [0, vocab) (flagged SV_DEV_TOKEN_RANGE).  A padding output
+ * has logprob 0 for every id, entropy 0, row_max -inf, log_z 0, top_ids -1; an
+ * all -inf row has entropy 0, row_max -inf, log_z -inf, logprob -inf.
+ * entropy, row_max, log_z and flags may be NULL, as may logprob when num_ids is
+ * 0 and the top arrays when top_k is 0.  num_ids <= 1024, top_k <= 64.  Sums
+ * and statistics are held in fp32, joined over a row in a fixed order.
+ * ws: at least spec_verify_logprobs_workspace_bytes(n, vocab, top_k) bytes,
+ * zero-filled before its first use, left zeroed where it matters (zero-fill a
+ * workspace that served another entry point).
+ */
+size_t spec_verify_logprobs_workspace_bytes(int64_t n, int32_t vocab, int32_t top_k);
+
+sv_status_t spec_verify_token_logprobs(const void* logits, sv_dtype_t dtype, int64_t ld, int64_t rows, int32_t vocab,
+                                       int64_t n, const int32_t* row_index, const int32_t* ids, int32_t num_ids,
+                                       int64_t ldi, const float* row_temp, int32_t top_k, float* logprob,
+                                       float* entropy, float* row_max, float* log_z, int32_t* top_ids,
+                                       float* top_logprob, uint32_t* flags, void* ws, size_t ws_bytes,
+                                       cudaStream_t stream);
+
+/*
+ * The gradient of spec_verify_token_logprobs (row i describing logits row i)
+ * by the logits, given g_logprob [rows, num_ids], g_entropy [rows] (or NULL)
+ * and g_top [rows, top_k] (or NULL), with what the forward call kept: row_max,
+ * log_z, entropy (needed with g_entropy) and top_ids (needed with g_top):
+ *   dlogits_v = 1/T ( sum_{j: id_j = v} g_j + sum_{k: top_k = v} gt_k - p_v G
+ *                     - g_entropy p_v (ln p_v + entropy) ),  G = sum g + sum gt
+ * over ids that are usable tokens; -1, ids outside [0, vocab) and tokens with
+ * a NaN or +inf logit have no part in it, and neither such logits nor an all
+ * -inf row receive a gradient.  dlogits [rows, ldd] has the logits' dtype (16-byte
+ * aligned rows), is rounded once, and must not overlap the logits
+ * (SV_ERR_UNSUPPORTED).  Either of num_ids and top_k may be 0.  No workspace.
+ */
+sv_status_t spec_verify_token_logprobs_backward(const void* logits, sv_dtype_t dtype, int64_t ld, int64_t rows,
+                                                int32_t vocab, const int32_t* ids, int32_t num_ids, int64_t ldi,
+                                                const float* row_temp, const float* row_max, const float* log_z,
+                                                const float* entropy, const int32_t* top_ids, int32_t top_k,
+                                                const float* g_logprob, const float* g_entropy, const float* g_top,
+                                                void* dlogits, int64_t ldd, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

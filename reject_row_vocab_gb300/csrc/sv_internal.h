@@ -21,6 +21,7 @@ constexpr uint32_t kStBadLayout = SV_DEV_BAD_LAYOUT;
 constexpr uint32_t kStResidualEmpty = SV_DEV_RESIDUAL_EMPTY;
 constexpr uint32_t kStDupSibling = SV_DEV_DUP_SIBLING;
 constexpr uint32_t kStTimeout = SV_DEV_TIMEOUT;
+constexpr uint32_t kStSlotRange = SV_DEV_SLOT_RANGE;
 
 // Final statistics of one logits row, written by the row-statistics kernel.
 // M is the row maximum over usable entries (finite or -inf), argmax its lowest

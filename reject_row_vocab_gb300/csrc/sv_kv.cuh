@@ -1,0 +1,61 @@
+// The paged KV cache as the kernels see it: host checks of the caller's
+// description and the address of a position or slot.
+#pragma once
+
+#include <cstdint>
+
+#include "sv_device.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+
+// Strides in elements, as the caller gives them.
+struct KvView {
+  char* k;
+  char* v;
+  int32_t es;  // bytes an element
+  int32_t layers, pages, page_size, heads, head_dim;
+  int64_t layer_stride, page_stride, slot_stride, head_stride;
+  const int32_t* table;
+  int32_t max_pages;
+  int64_t ld_table;
+};
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+inline sv_status_t check_cache(const sv_kv_cache_t* c, KvView* v) {
+  if (!c) return SV_ERR_NULL_ARG;
+  if (!c->k || !c->v || !c->page_table) return SV_ERR_NULL_ARG;
+  if (c->dtype != SV_F32 && c->dtype != SV_BF16) return SV_ERR_BAD_DTYPE;
+  if (c->layers < 1 || c->pages < 1 || c->page_size < 1 || c->heads < 1 || c->heads > 65535 || c->head_dim < 1 ||
+      c->head_dim > 256 || c->max_pages < 1 || c->ld_table < c->max_pages)
+    return SV_ERR_BAD_SHAPE;
+  if (c->layer_stride < 0 || c->page_stride < 0 || c->slot_stride < 0 || c->head_stride < 0) return SV_ERR_BAD_SHAPE;
+  // positions and slots are 31-bit numbers inside the kernels
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX / 2 ||
+      static_cast<int64_t>(c->pages) * c->page_size > INT32_MAX / 2)
+    return SV_ERR_BAD_SHAPE;
+  const int32_t es = c->dtype == SV_BF16 ? 2 : 4;
+  if (!aligned16(c->k) || !aligned16(c->v) || (c->head_dim * es) % 16 != 0 || (c->layer_stride * es) % 16 != 0 ||
+      (c->page_stride * es) % 16 != 0 || (c->slot_stride * es) % 16 != 0 || (c->head_stride * es) % 16 != 0)
+    return SV_ERR_MISALIGNED;
+  *v = KvView{static_cast<char*>(c->k), static_cast<char*>(c->v), es,          c->layers,      c->pages,
+              c->page_size,             c->heads,                 c->head_dim, c->layer_stride, c->page_stride,
+              c->slot_stride,           c->head_stride,           c->page_table, c->max_pages, c->ld_table};
+  return SV_OK;
+}
+
+// Element offset (within a layer and head 0) of a slot, or -1 outside the cache.
+__device__ __forceinline__ int64_t kv_slot_offset(const KvView& c, int64_t slot) {
+  if (slot < 0 || slot >= static_cast<int64_t>(c.pages) * c.page_size) return -1;
+  const uint32_t s = static_cast<uint32_t>(slot), page = s / static_cast<uint32_t>(c.page_size);
+  return page * c.page_stride + static_cast<int64_t>(s - page * c.page_size) * c.slot_stride;
+}
+
+// Element offset of entry `off` of page `page` (a page table's word), or -1 outside the cache.
+__device__ __forceinline__ int64_t kv_page_offset(const KvView& c, int32_t page, uint32_t off) {
+  if (page < 0 || page >= c.pages) return -1;
+  return page * c.page_stride + static_cast<int64_t>(off) * c.slot_stride;
+}
+
+}  // namespace sv

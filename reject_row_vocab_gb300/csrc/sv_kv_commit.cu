@@ -1,0 +1,109 @@
+// The KV move of a verification's commit lists ([E2D] §5.6.6, §8.1): K and V
+// of every committed entry, from its slot to its position, in every layer.
+//
+//   cache[l][dst(e)] <- cache[l][src(e)]   for e in [commit_cu[b], commit_cu[b+1])
+//
+// Bound by the bytes: each moved row is read once and written once.  The rows
+// of one request may overlap (drafts staged in place move towards the front),
+// so a block owns whole columns of one request's rows: it reads the 16-byte
+// column pieces of all its entries into registers, waits for the block, and
+// only then writes them.  Columns are independent, so blocks of one request
+// (one for each layer and for K and V) need no order among themselves.
+//
+//   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
+#include <cstdint>
+
+#include "sv_kv.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRegs = 8;  // 16-byte pieces a thread holds between the reads and the writes
+
+__global__ void __launch_bounds__(kMoveThreads) k_kv_commit(KvView c, int32_t max_len, int64_t list_len,
+                                                            const int32_t* cu, const int64_t* src_slot,
+                                                            const int64_t* dst_pos, uint32_t* status) {
+  __shared__ int64_t s_src[kMaxNodes], s_dst[kMaxNodes];  // element offsets, -1 for an entry that is not moved
+  __shared__ uint32_t s_status;
+  const int b = blockIdx.x, t = threadIdx.x;
+  const int layer = blockIdx.y >> 1, which = blockIdx.y & 1;
+  grid_dependency_wait();
+  allow_dependents();
+  if (t == 0) s_status = 0u;
+  __syncthreads();
+  const int64_t lo = cu[b];
+  const int64_t n64 = static_cast<int64_t>(cu[b + 1]) - lo;
+  const bool bad = lo < 0 || n64 < 0 || n64 > max_len || lo + n64 > list_len;
+  const int n = bad ? 0 : static_cast<int>(n64);
+  for (int e = t; e < n; e += kMoveThreads) {
+    const int64_t pos = dst_pos[lo + e];
+    const int64_t src = kv_slot_offset(c, src_slot[lo + e]);
+    int64_t dst = -1;
+    if (pos >= 0 && pos < static_cast<int64_t>(c.max_pages) * c.page_size) {
+      const uint32_t p = static_cast<uint32_t>(pos) / static_cast<uint32_t>(c.page_size);
+      dst = kv_page_offset(c, c.table[b * c.ld_table + p], static_cast<uint32_t>(pos) - p * c.page_size);
+    }
+    const bool ok = src >= 0 && dst >= 0;
+    if (!ok) atomicOr(&s_status, kStSlotRange);
+    s_src[e] = ok ? src : -1;
+    s_dst[e] = ok && src != dst ? dst : -1;  // an entry already in place is not moved
+  }
+  __syncthreads();
+  if (blockIdx.y == 0 && t == 0 && status) status[b] = bad ? kStBadLayout : s_status;
+  char* base = (which ? c.v : c.k) + layer * c.layer_stride * c.es;
+  const int per_head = c.head_dim * c.es / 16;
+  const int cols = c.heads * per_head;  // 16-byte pieces of one row
+  if (n == 0) return;
+  // As many columns at a time as fit the registers of the block (n <= 1024: two at least).
+  const int width = min(cols, kMoveThreads * kMoveRegs / n);
+  for (int c0 = 0; c0 < cols; c0 += width) {
+    const int w = min(width, cols - c0);
+    const int pieces = w * n;
+    uint4 r[kMoveRegs];
+#pragma unroll
+    for (int i = 0; i < kMoveRegs; ++i) {
+      const int x = t + i * kMoveThreads;
+      if (x < pieces) {
+        const int e = x / w, col = c0 + x % w;
+        if (s_dst[e] >= 0)
+          r[i] = *reinterpret_cast<const uint4*>(base + (s_src[e] + (col / per_head) * c.head_stride) * c.es +
+                                                 (col % per_head) * 16);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMoveRegs; ++i) {
+      const int x = t + i * kMoveThreads;
+      if (x < pieces) {
+        const int e = x / w, col = c0 + x % w;
+        if (s_dst[e] >= 0)
+          *reinterpret_cast<uint4*>(base + (s_dst[e] + (col / per_head) * c.head_stride) * c.es +
+                                    (col % per_head) * 16) = r[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" sv_status_t spec_verify_kv_commit(const sv_kv_cache_t* cache, int32_t batch, int32_t max_len,
+                                             int64_t list_len, const int32_t* commit_cu,
+                                             const int64_t* commit_src_slot, const int64_t* commit_dst_pos,
+                                             uint32_t* dev_status, cudaStream_t stream) {
+  if (batch < 0 || batch > 65535 || max_len < 1 || max_len > kMaxNodes || list_len < 0) return SV_ERR_BAD_SHAPE;
+  KvView c{};
+  const sv_status_t s = check_cache(cache, &c);
+  if (s != SV_OK) return s;
+  if (c.layers > 32767) return SV_ERR_BAD_SHAPE;
+  if (batch == 0) return SV_OK;
+  if (!commit_cu || (list_len > 0 && (!commit_src_slot || !commit_dst_pos))) return SV_ERR_NULL_ARG;
+  const cudaError_t e =
+      launch_pdl(k_kv_commit, dim3(static_cast<unsigned>(batch), static_cast<unsigned>(c.layers) * 2u),
+                 dim3(kMoveThreads), 0, stream, c, max_len, list_len, commit_cu, commit_src_slot, commit_dst_pos,
+                 dev_status);
+  return e == cudaSuccess ? SV_OK : cuda_failure(e);
+}

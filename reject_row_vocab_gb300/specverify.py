@@ -23,6 +23,7 @@ SV_F32, SV_BF16 = 0, 1
 STATUS = {0: "SV_OK", 1: "SV_ERR_NULL_ARG", 2: "SV_ERR_BAD_SHAPE", 3: "SV_ERR_BAD_DTYPE", 4: "SV_ERR_MISALIGNED",
           5: "SV_ERR_UNSUPPORTED", 6: "SV_ERR_WORKSPACE_TOO_SMALL", 7: "SV_ERR_CUDA"}
 DEV_TOKEN_RANGE, DEV_NONFINITE, DEV_BAD_TREE, DEV_BAD_LAYOUT, DEV_RESIDUAL_EMPTY, DEV_DUP_SIBLING = 1, 2, 4, 8, 16, 32
+DEV_TIMEOUT, DEV_SLOT_RANGE = 64, 128
 
 ENTRY_POINTS = ("spec_verify_workspace_bytes", "spec_verify_status_string", "spec_verify_greedy_chain",
                 "spec_verify_greedy_tree", "spec_verify_rejection_chain", "spec_verify_rejection_ragged",
@@ -30,7 +31,9 @@ ENTRY_POINTS = ("spec_verify_workspace_bytes", "spec_verify_status_string", "spe
                 "spec_verify_last_cuda_error", "spec_verify_rejection_chain_noalloc",
                 "spec_verify_dspark_workspace_bytes", "spec_verify_dspark_budget", "spec_verify_dspark_verify_lens",
                 "spec_verify_sparse_workspace_bytes", "spec_verify_rejection_chain_sparse", "spec_verify_build_tree",
-                "spec_verify_sample_match_chain")
+                "spec_verify_sample_match_chain", "spec_verify_attention_workspace_bytes",
+                "spec_verify_paged_attention", "spec_verify_kv_commit", "spec_verify_logprobs_workspace_bytes",
+                "spec_verify_token_logprobs", "spec_verify_token_logprobs_backward")
 
 
 class SpecVerifyError(RuntimeError):
@@ -43,6 +46,14 @@ class SvOut(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "accept_len", "num_out", "out_tokens", "bonus", "accept_rows", "commit_cu", "commit_src_slot",
         "commit_dst_pos", "dev_status")]
+
+
+class SvKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("layers", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32), ("ld_table", ctypes.c_int64)]
 
 
 _lib = None
@@ -82,6 +93,15 @@ def load_library():
         "spec_verify_dspark_workspace_bytes": ([I32], SZ),
         "spec_verify_dspark_budget": ([P, I64, I32, P, I32, F, P], ctypes.c_int),
         "spec_verify_dspark_verify_lens": ([P, I32, I32, I64, I32, I32, I32, F, P, P, SZ, P], ctypes.c_int),
+        "spec_verify_attention_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+        "spec_verify_paged_attention": ([P, I64, I64, I32, P, I32, I32, I64, I32, P, P, P, P, F, P, I64, I64, P, P, P,
+                                         SZ, P], ctypes.c_int),
+        "spec_verify_kv_commit": ([P, I32, I32, I64, P, P, P, P, P], ctypes.c_int),
+        "spec_verify_logprobs_workspace_bytes": ([I64, I32, I32], SZ),
+        "spec_verify_token_logprobs": ([P, ctypes.c_int, I64, I64, I32, I64, P, P, I32, I64, P, I32, P, P, P, P, P, P,
+                                        P, P, SZ, P], ctypes.c_int),
+        "spec_verify_token_logprobs_backward": ([P, ctypes.c_int, I64, I64, I32, P, I32, I64, P, P, P, P, P, I32, P, P,
+                                                 P, P, I64, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -513,3 +533,312 @@ def build_tree(parents, seq_lens=None, stream=None, out: Optional[dict] = None) 
         _ptr(parents), _ptr(seq_lens), B, N, _ptr(res["positions"]), _ptr(res["mask"]), _ptr(res["retrieve_index"]),
         _ptr(res["first_child"]), _ptr(res["next_sibling"]), _ptr(res["status"]), _stream(stream)))
     return res
+
+
+# Serving-side operators around the verification: attention over the paged KV
+# cache, the KV move of the commit lists, and token log probabilities.
+
+
+class _NoStream:
+    """The current stream: nothing to enter."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_CURRENT = _NoStream()
+
+
+def _on(stream):
+    """Context for the tensors a call allocates: they belong to the stream the call runs on."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _call_stream(stream, device) -> int:
+    """The handle of the given stream, or of the device's current one."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _row_step(t: torch.Tensor) -> int:
+    """Row stride of [rows, cols]; of a single row, its own length up to whole 16-byte pieces."""
+    if t.shape[0] > 1:
+        return t.stride(0)
+    per = 16 // t.element_size()
+    return -(-t.shape[1] // per) * per
+
+
+class PagedKvCache:
+    """A paged KV cache: k, v [layers, pages, page_size, heads, head_dim] (bf16 or fp32, head_dim dense, any other
+    strides, the same for both) and page_table [batch, max_pages] int32 (dense rows).
+
+    Holds the tensors and the library's description of them; make it once and use it for every call."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 5:
+                raise ValueError("%s must be a 5-D torch tensor [layers, pages, page_size, heads, head_dim]" % name)
+            if t.shape[4] > 1 and t.stride(4) != 1:
+                raise ValueError("%s: head_dim must be dense" % name)
+        if k.dtype not in (torch.bfloat16, torch.float32) or v.dtype != k.dtype:
+            raise TypeError("k and v must both be bfloat16 or float32, got %s and %s" % (k.dtype, v.dtype))
+        if v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+            raise ValueError("k and v must have the same shape, strides and device")
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be a 2-D torch tensor")
+        batch, pages = page_table.shape
+        _rows_arg(page_table, "page_table", torch.int32, batch, pages, k.device)
+        self.k, self.v, self.page_table = k, v, page_table
+        self.device, self.dtype, self.batch = k.device, k.dtype, batch
+        self.heads, self.head_dim = k.shape[3], k.shape[4]
+        st = [x if n > 1 else 0 for x, n in zip(k.stride(), k.shape)]  # an axis of one entry has no step
+        self.struct = SvKvCache(k.data_ptr(), v.data_ptr(), SV_BF16 if k.dtype == torch.bfloat16 else SV_F32,
+                                k.shape[0], k.shape[1], k.shape[2], k.shape[3], k.shape[4], st[0], st[1], st[2], st[3],
+                                page_table.data_ptr(), pages, page_table.stride(0) if batch > 1 else max(pages, 1))
+        self.ref = ctypes.byref(self.struct)
+
+
+def _require_cache(cache: PagedKvCache):
+    if not isinstance(cache, PagedKvCache):
+        raise TypeError("cache must be a PagedKvCache")
+    if not cache.k.is_cuda:
+        raise ValueError("the cache must be on a CUDA device (got %s): the library has no CPU path" % cache.device)
+
+
+@dataclass
+class AttentionOutputs:
+    out: torch.Tensor              # [rows, heads, head_dim], the cache's type
+    lse: Optional[torch.Tensor]    # [rows, heads] fp32
+    dev_status: torch.Tensor       # [batch] int32 storage of uint32 bits
+
+    @staticmethod
+    def allocate(rows: int, heads: int, head_dim: int, batch: int, dtype=torch.bfloat16, device=None,
+                 lse: bool = True) -> "AttentionOutputs":
+        d = device or "cuda"
+        return AttentionOutputs(out=torch.empty(rows, heads, head_dim, dtype=dtype, device=d),
+                                lse=torch.empty(rows, heads, dtype=torch.float32, device=d) if lse else None,
+                                dev_status=torch.empty(batch, dtype=torch.int32, device=d))
+
+
+def attention_workspace(batch: int, max_len: int, cache: PagedKvCache, num_heads: int) -> torch.Tensor:
+    """A zero-filled workspace of paged_attention calls (the library keeps its counters zero between calls)."""
+    n = int(load_library().spec_verify_attention_workspace_bytes(batch, max_len, num_heads, cache.heads,
+                                                                 cache.head_dim))
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def _head_rows(t, name, rows, heads, dim, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError("%s must be a 3-D torch tensor [rows, heads, head_dim]" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s; the call runs on %s (the cache's device)" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (the cache's type), got %s" % (name, dtype, t.dtype))
+    if t.shape[0] < rows or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError("%s is %s; the call needs [%d, %d, %d]" % (name, tuple(t.shape), rows, heads, dim))
+    if dim > 1 and t.stride(2) != 1:
+        raise ValueError("%s: head_dim must be dense" % name)
+
+
+def _steps(t):
+    """Row and head strides; an axis of one entry has no step."""
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len: Optional[int] = None,
+                    cu_seqlens=None, row_slots=None, mask=None, scale: Optional[float] = None, out=None, ws=None,
+                    stream=None) -> AttentionOutputs:
+    """Attention of each request's new rows q [rows, heads, head_dim] over its committed positions in the cache and
+    over the new rows themselves.
+
+    seq_lens [batch] int64: committed positions, without the new rows.  A request has max_len new rows
+    (rows / batch when not given; 1 is plain decoding), or cu_seqlens [batch + 1] int32 gives ragged ones of 1..max_len.
+    row_slots [rows] int64: where the new rows' K/V lie (None: at positions seq_lens + j).  mask [batch, max_len,
+    max_len] uint8: which new rows a row sees (None: itself and earlier ones), as build_tree returns it.
+    scale defaults to 1 / sqrt(head_dim)."""
+    lib = load_library()
+    _require_cache(cache)
+    dev = cache.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a 3-D torch tensor [rows, heads, head_dim]")
+    rows, heads, dim = q.shape
+    _head_rows(q, "q", rows, heads, cache.head_dim, cache.dtype, dev)
+    _arg(seq_lens, "seq_lens", torch.int64, 0, dev)
+    if seq_lens is None:
+        raise ValueError("seq_lens is required")
+    batch = seq_lens.numel()
+    if cache.batch < batch:
+        raise ValueError("page_table has %d rows; the call reads %d" % (cache.batch, batch))
+    if max_len is None:
+        if cu_seqlens is not None:
+            raise ValueError("max_len is required with cu_seqlens")
+        max_len = rows // batch if batch else 1
+    if cu_seqlens is None and batch and rows < batch * max_len:
+        raise ValueError("q has %d rows; the call reads %d" % (rows, batch * max_len))
+    _arg(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, dev)
+    _arg(row_slots, "row_slots", torch.int64, rows, dev)
+    _arg(mask, "mask", torch.uint8, batch * max_len * max_len, dev)
+    if out is None or ws is None:
+        with _on(stream):
+            if out is None:
+                out = AttentionOutputs.allocate(rows, heads, dim, batch, cache.dtype, dev)
+            if ws is None:
+                ws = attention_workspace(batch, max_len, cache, heads)
+    _head_rows(out.out, "out.out", rows, heads, dim, cache.dtype, dev)
+    _arg(out.lse, "out.lse", torch.float32, rows * heads, dev)
+    _arg(out.dev_status, "out.dev_status", torch.int32, batch, dev)
+    _check_ws(ws, dev)
+    _check("spec_verify_paged_attention", lib.spec_verify_paged_attention(
+        q.data_ptr(), *_steps(q), heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
+        seq_lens.data_ptr(), _addr(row_slots), _addr(mask), dim ** -0.5 if scale is None else scale,
+        out.out.data_ptr(), *_steps(out.out), _addr(out.lse), _addr(out.dev_status),
+        ws.data_ptr(), ws.numel(), _call_stream(stream, dev)))
+    return out
+
+
+def kv_commit(cache: PagedKvCache, commit_cu, commit_src_slot, commit_dst_pos, *, max_len: int, dev_status=None,
+              stream=None) -> torch.Tensor:
+    """Moves the committed rows' K/V to their positions, in every layer, from a verification's commit lists
+    (VerifyOutputs.commit_cu / commit_src_slot / commit_dst_pos).  Returns the requests' status bits [batch]."""
+    lib = load_library()
+    _require_cache(cache)
+    dev = cache.device
+    if commit_cu is None or commit_src_slot is None or commit_dst_pos is None:
+        raise ValueError("commit_cu, commit_src_slot and commit_dst_pos are required")
+    _arg(commit_cu, "commit_cu", torch.int32, 1, dev)
+    batch = commit_cu.numel() - 1
+    if cache.batch < batch:
+        raise ValueError("page_table has %d rows; the call reads %d" % (cache.batch, batch))
+    _arg(commit_src_slot, "commit_src_slot", torch.int64, 0, dev)
+    _arg(commit_dst_pos, "commit_dst_pos", torch.int64, 0, dev)
+    if dev_status is None:
+        with _on(stream):
+            dev_status = torch.empty(batch, dtype=torch.int32, device=dev)
+    _arg(dev_status, "dev_status", torch.int32, batch, dev)
+    _check("spec_verify_kv_commit", lib.spec_verify_kv_commit(
+        cache.ref, batch, max_len, min(commit_src_slot.numel(), commit_dst_pos.numel()), commit_cu.data_ptr(),
+        _addr(commit_src_slot), _addr(commit_dst_pos), _addr(dev_status), _call_stream(stream, dev)))
+    return dev_status
+
+
+@dataclass
+class LogprobOutputs:
+    logprob: Optional[torch.Tensor]      # [n, num_ids] fp32
+    entropy: Optional[torch.Tensor]      # [n] fp32
+    row_max: Optional[torch.Tensor]      # [n] fp32, the rows' largest logits
+    log_z: Optional[torch.Tensor]        # [n] fp32, ln sum exp((l - row_max) / T)
+    top_ids: Optional[torch.Tensor]      # [n, top_k] int32
+    top_logprob: Optional[torch.Tensor]  # [n, top_k] fp32
+    flags: Optional[torch.Tensor]        # [n] int32 storage of uint32 bits
+
+    @staticmethod
+    def allocate(n: int, num_ids: int, top_k: int = 0, device=None) -> "LogprobOutputs":
+        f32 = dict(dtype=torch.float32, device=device or "cuda")
+        i32 = dict(dtype=torch.int32, device=device or "cuda")
+        return LogprobOutputs(logprob=torch.empty(n, num_ids, **f32), entropy=torch.empty(n, **f32),
+                              row_max=torch.empty(n, **f32), log_z=torch.empty(n, **f32),
+                              top_ids=torch.empty(n, top_k, **i32) if top_k else None,
+                              top_logprob=torch.empty(n, top_k, **f32) if top_k else None,
+                              flags=torch.empty(n, **i32))
+
+
+def logprobs_workspace(n: int, vocab: int, top_k: int = 0, device=None) -> torch.Tensor:
+    """A zero-filled workspace of token_logprobs calls (the library keeps its counters zero between calls)."""
+    b = int(load_library().spec_verify_logprobs_workspace_bytes(n, vocab, top_k))
+    return torch.zeros(b, dtype=torch.uint8, device=device or "cuda")
+
+
+def _given_ids(ids, n, device):
+    """ids as [n, num_ids] with dense rows; a 1-D array is one id a row."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() not in (1, 2):
+        raise ValueError("ids must be a 1-D or 2-D torch tensor")
+    if ids.dim() == 1:
+        ids = ids.unsqueeze(1)
+    _rows_arg(ids, "ids", torch.int32, n, 0, device)
+    return ids, ids.shape[1], (ids.stride(0) if n > 1 else max(ids.shape[1], 1))
+
+
+def token_logprobs(logits, ids, *, top_k: int = 0, row_index=None, row_temp=None, out=None, ws=None,
+                   stream=None) -> LogprobOutputs:
+    """Log probabilities of the given tokens ids [n, num_ids] (or [n]) under softmax(logits / T), with each row's
+    entropy and its top_k most likely tokens.
+
+    Output i describes logits row row_index[i] (int32, -1 is padding; None: row i), so that a verification's
+    accept_rows and out_tokens can be passed as they are.  row_temp [n] fp32 (None: 1)."""
+    lib = load_library()
+    _require_cuda(logits)
+    rows, V = logits.shape
+    dev = logits.device
+    if row_index is None:
+        n = rows
+    else:
+        _arg(row_index, "row_index", torch.int32, 0, dev)
+        n = row_index.numel()
+    ids, num_ids, ldi = _given_ids(ids, n, dev)
+    _arg(row_temp, "row_temp", torch.float32, n, dev)
+    if out is None or ws is None:
+        with _on(stream):
+            if out is None:
+                out = LogprobOutputs.allocate(n, num_ids, top_k, dev)
+            if ws is None:
+                ws = logprobs_workspace(n, V, top_k, dev)
+    f32 = torch.float32
+    _arg(out.logprob, "out.logprob", f32, n * num_ids, dev)
+    _arg(out.entropy, "out.entropy", f32, n, dev)
+    _arg(out.row_max, "out.row_max", f32, n, dev)
+    _arg(out.log_z, "out.log_z", f32, n, dev)
+    _arg(out.top_ids, "out.top_ids", torch.int32, n * top_k, dev)
+    _arg(out.top_logprob, "out.top_logprob", f32, n * top_k, dev)
+    _arg(out.flags, "out.flags", torch.int32, n, dev)
+    _check_ws(ws, dev)
+    _check("spec_verify_token_logprobs", lib.spec_verify_token_logprobs(
+        logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, n, _addr(row_index), ids.data_ptr(), num_ids,
+        ldi, _addr(row_temp), top_k, _addr(out.logprob), _addr(out.entropy), _addr(out.row_max), _addr(out.log_z),
+        _addr(out.top_ids), _addr(out.top_logprob), _addr(out.flags), ws.data_ptr(), ws.numel(),
+        _call_stream(stream, dev)))
+    return out
+
+
+def token_logprobs_backward(logits, ids, kept: LogprobOutputs, g_logprob, *, g_entropy=None, g_top=None, row_temp=None,
+                            out=None, stream=None) -> torch.Tensor:
+    """The gradient by logits [rows, V] of token_logprobs (called without row_index), given the gradients of its
+    logprob [rows, num_ids], entropy [rows] and top_logprob [rows, top_k].
+
+    kept: the forward call's outputs (row_max and log_z; entropy with g_entropy; top_ids with g_top).  out: a tensor
+    like logits (rows of a multiple of 16 bytes) that does not overlap them."""
+    lib = load_library()
+    _require_cuda(logits)
+    rows, V = logits.shape
+    dev, f32 = logits.device, torch.float32
+    ids, num_ids, ldi = _given_ids(ids, rows, dev)
+    _arg(g_logprob, "g_logprob", f32, rows * num_ids, dev)
+    _arg(g_entropy, "g_entropy", f32, rows, dev)
+    top_k = 0
+    if g_top is not None:
+        if not isinstance(g_top, torch.Tensor) or g_top.dim() != 2:
+            raise ValueError("g_top must be a 2-D torch tensor")
+        top_k = g_top.shape[1]
+        _arg(g_top, "g_top", f32, rows * top_k, dev)
+        _arg(kept.top_ids, "kept.top_ids", torch.int32, rows * top_k, dev)
+        if kept.top_ids is not None and (kept.top_ids.dim() != 2 or kept.top_ids.shape[1] != top_k):
+            raise ValueError("kept.top_ids must have g_top's %d columns" % top_k)
+    _arg(row_temp, "row_temp", f32, rows, dev)
+    _arg(kept.row_max, "kept.row_max", f32, rows, dev)
+    _arg(kept.log_z, "kept.log_z", f32, rows, dev)
+    _arg(kept.entropy, "kept.entropy", f32, rows, dev)
+    if out is None:
+        per = 16 // logits.element_size()
+        with _on(stream):
+            out = torch.empty(rows, -(-V // per) * per, dtype=logits.dtype, device=dev)[:, :V]
+    _rows_arg(out, "out", logits.dtype, rows, V, dev)
+    _check("spec_verify_token_logprobs_backward", lib.spec_verify_token_logprobs_backward(
+        logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, ids.data_ptr(), num_ids, ldi, _addr(row_temp),
+        _addr(kept.row_max), _addr(kept.log_z), _addr(kept.entropy), _addr(kept.top_ids) if top_k else None, top_k,
+        _addr(g_logprob), _addr(g_entropy), _addr(g_top), out.data_ptr(), _row_step(out), _call_stream(stream, dev)))
+    return out
