@@ -17,27 +17,18 @@
 namespace sv {
 namespace {
 
-constexpr float kLn2 = 0.693147180559945309417f;
-
 // ---------------------------------------------------------------------------------------------------------------------
 // Engine: plain fp32 arithmetic.  Four warps of four rows each; a lane scores one key of the tile, then gathers columns.
 // ---------------------------------------------------------------------------------------------------------------------
 
-template <bool BF16>
-__device__ __forceinline__ float4 load4(const char* p) {  // four elements as floats
-  if (BF16) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-  }
-  return *reinterpret_cast<const float4*>(p);
-}
+__device__ __forceinline__ float4 load4(const char* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <bool BF16, int DP>
+template <int DP>
 struct SimtEngine {
-  static constexpr bool kBf16 = BF16;
+  static constexpr bool kBf16 = false;
   static constexpr int kDP = DP;
   static constexpr int MT = 16, KT = 32, WK = 1, THREADS = 128;
-  static constexpr int ES = BF16 ? 2 : 4;
+  static constexpr int ES = 4;
   static constexpr int ROW = DP * ES;              // bytes of a staged row
   static constexpr int STAGE = 2 * KT * ROW;       // K then V
   static constexpr int STAGES = STAGE > 32768 ? 2 : 3;
@@ -62,7 +53,7 @@ struct SimtEngine {
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < rows && d < p.c.head_dim) {
         const int64_t at = (r.row0 + row / p.group) * p.q_row + (hkv * p.group + row % p.group) * p.q_head + d;
-        f = load4<BF16>(p.q + at * ES);
+        f = load4(p.q + at * ES);
       }
       f.x *= p.scale_log2, f.y *= p.scale_log2, f.z *= p.scale_log2, f.w *= p.scale_log2;
       *reinterpret_cast<float4*>(q + x * 4) = f;
@@ -85,18 +76,14 @@ struct SimtEngine {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c = 0; c < DP * ES / 16; ++c) {
       const char* kp = ks + piece(lane, c);
+      const float4 k = load4(kp);
 #pragma unroll
-      for (int h = 0; h < 16 / (4 * ES); ++h) {
-        const float4 k = load4<BF16>(kp + h * 4 * ES);
-        const int d = c * (16 / ES) + h * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 a = *reinterpret_cast<const float4*>(q + (warp * 4 + i) * DP + d);
-          s[i] = fmaf(a.x, k.x, s[i]);
-          s[i] = fmaf(a.y, k.y, s[i]);
-          s[i] = fmaf(a.z, k.z, s[i]);
-          s[i] = fmaf(a.w, k.w, s[i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(q + (warp * 4 + i) * DP + c * 4);
+        s[i] = fmaf(a.x, k.x, s[i]);
+        s[i] = fmaf(a.y, k.y, s[i]);
+        s[i] = fmaf(a.z, k.z, s[i]);
+        s[i] = fmaf(a.w, k.w, s[i]);
       }
     }
     const bool masked = valid[0] != 0xffffffffu || x0 + KT > r.len;
@@ -136,7 +123,7 @@ struct SimtEngine {
       for (int j = 0; j < NQ; ++j) {
         const int d = KS == 1 ? (lane + 32 * j) * 4 : (lane & 15) * 4;
         const int byte = d * ES;
-        const float4 v = load4<BF16>(vs + piece(key, byte >> 4) + (byte & 15));
+        const float4 v = load4(vs + piece(key, byte >> 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (!masked || !(w[i] < 0.0f)) {
@@ -176,6 +163,238 @@ struct SimtEngine {
 };
 
 // ---------------------------------------------------------------------------------------------------------------------
+// Engine: bf16 matrix instructions (16 x 8 x 16, fp32 accumulators).  WR row groups of 16 rows times WK key groups of
+// KT / WK keys, a warp each; a warp keeps the scores, weights and O of its rows in registers, so the only exchange is
+// the join of the key groups at the end of a unit.  Few rows are spread over the keys, many over the rows.
+// ---------------------------------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// A pair of bf16 with NaN and infinities replaced by 0.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int DP, int WR>
+struct MmaEngine {
+  static constexpr bool kBf16 = true;
+  static constexpr int kDP = DP;
+  static constexpr int WK = 4 / WR, MT = 16 * WR, KT = 64, THREADS = 128;
+  static constexpr int ROW = DP * 2, STAGE = 2 * KT * ROW;
+  static constexpr int STAGES = DP == 64 ? 5 : 3;
+  static constexpr int EXTRA = MT * ROW;  // Q
+  static constexpr int NK = KT / WK;      // keys of a warp
+  static constexpr int NT = NK / 8, DT = DP / 8, KS = DP / 16;
+  static constexpr bool kQRegs = DP <= 128;  // Q stays in registers (wider heads fetch it from shared memory)
+
+  float m[2], l[2];
+  float o[DT][4];
+  uint32_t qf[kQRegs ? KS : 1][4];
+  uint32_t q_addr;  // this lane's row of Q for ldmatrix
+
+  __device__ static int piece(int row, int c) { return row * ROW + ((c ^ (row & 7)) << 4); }
+  __device__ static int row_group() { return (threadIdx.x >> 5) % WR; }
+  __device__ static int key_group() { return (threadIdx.x >> 5) / WR; }
+
+  __device__ void load_q(int ks, uint32_t (&a)[4]) const {
+    const int lane = threadIdx.x & 31;
+    const int row = row_group() * 16 + (lane & 15);
+    ldmatrix4(q_addr + piece(row, ks * 2 + (lane >> 4)), a);
+  }
+
+  __device__ void init(const AttnParams& p, const AttnRequest& r, int hkv, int rt, char* extra) {
+    const int rows = r.n * p.group;
+    for (int x = threadIdx.x; x < MT * (DP / 8); x += THREADS) {
+      const int row = x / (DP / 8), c = x % (DP / 8), grow = rt * MT + row;
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (grow < rows && c * 8 < p.c.head_dim) {
+        const int64_t at = (r.row0 + grow / p.group) * p.q_row + (hkv * p.group + grow % p.group) * p.q_head + c * 8;
+        u = *reinterpret_cast<const uint4*>(p.q + at * 2);
+      }
+      *reinterpret_cast<uint4*>(extra + piece(row, c)) = u;
+    }
+    q_addr = smem_addr(extra);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i] = -kInfF, l[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    __syncthreads();
+    if (kQRegs)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) load_q(ks, qf[kQRegs ? ks : 0]);
+  }
+
+  __device__ void tile(const AttnParams& p, const AttnRequest& r, int b, int rt, int x0, const char* stage,
+                       const uint32_t* valid) {
+    const int lane = threadIdx.x & 31;
+    const int k0 = key_group() * NK;  // first key of the warp within the tile
+    const uint32_t ks_addr = smem_addr(stage), vs_addr = ks_addr + KT * ROW;
+    const int mi = lane >> 3, mr = lane & 7;
+    float s[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t a[4];
+      if (kQRegs) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = qf[kQRegs ? ks : 0][i];
+      } else {
+        load_q(ks, a);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; nt += 2) {
+        uint32_t kb[4];
+        ldmatrix4(ks_addr + piece(k0 + nt * 8 + (mi >> 1) * 8 + mr, ks * 2 + (mi & 1)), kb);
+        mma_bf16(s[nt], a, kb[0], kb[1]);
+        mma_bf16(s[nt + 1], a, kb[2], kb[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[i][c] *= p.scale_log2;
+    const int row_lo = row_group() * 16 + (lane >> 2);
+    // valid: a bit for each of the tile's keys
+    const bool masked = (valid[0] & valid[1]) != 0xffffffffu || x0 + KT > r.len;
+    if (masked) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = (rt * MT + row_lo + h * 8) / p.group;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int key = k0 + i * 8 + (lane & 3) * 2 + c;
+            bool see = (valid[key >> 5] >> (key & 31) & 1u) != 0u && row < r.n;
+            if (see && x0 + key >= r.len) see = row_sees(p, b, row, x0 + key - r.len);
+            if (!see) s[i][h * 2 + c] = -kInfF;
+          }
+      }
+    }
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = m[h];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) mx = fmax_nan(mx, fmax_nan(s[i][h * 2], s[i][h * 2 + 1]));
+      mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float ref = mx == -kInfF ? 0.0f : mx;
+      alpha[h] = ex2_fast(m[h] - ref);
+      m[h] = mx;
+      l[h] *= alpha[h];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float x = ex2_fast(s[i][h * 2 + c] - ref);
+          s[i][h * 2 + c] = x;
+          l[h] += x;
+        }
+    }
+    // O moves to the new maximum only when one of the warp's rows has a new one.
+    if (__any_sync(0xffffffffu, !(alpha[0] == 1.0f && alpha[1] == 1.0f))) {
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        o[i][0] *= alpha[0], o[i][1] *= alpha[0];
+        o[i][2] *= alpha[1], o[i][3] *= alpha[1];
+      }
+    }
+    // A weight of 0 does not silence a V that is NaN or infinite.  Only new rows can be seen by some rows of the tile
+    // and not by others; where one of them holds such a V, it is taken out of the products and added by itself.
+    bool careful = false;
+    if (masked && r.n > 1) {
+      for (int x = lane; x < NK * (DP / 8); x += 32) {
+        const uint4 u = *reinterpret_cast<const uint4*>(stage + KT * ROW + piece(k0 + x / (DP / 8), x % (DP / 8)));
+        careful = careful || nonfinite_pair(u.x) || nonfinite_pair(u.y) || nonfinite_pair(u.z) || nonfinite_pair(u.w);
+      }
+      careful = __any_sync(0xffffffffu, careful);
+    }
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) {
+      const uint32_t a[4] = {pack_bf16(s[2 * j][0], s[2 * j][1]), pack_bf16(s[2 * j][2], s[2 * j][3]),
+                             pack_bf16(s[2 * j + 1][0], s[2 * j + 1][1]), pack_bf16(s[2 * j + 1][2], s[2 * j + 1][3])};
+#pragma unroll
+      for (int dt = 0; dt < DT; dt += 2) {
+        uint32_t vb[4];
+        ldmatrix4_trans(vs_addr + piece(k0 + j * 16 + (mi & 1) * 8 + mr, dt + (mi >> 1)), vb);
+        if (careful) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vb[i] = finite_pair(vb[i]);
+        }
+        mma_bf16(o[dt], a, vb[0], vb[1]);
+        mma_bf16(o[dt + 1], a, vb[2], vb[3]);
+      }
+    }
+    if (careful) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        for (int kk = 0; kk < 8; ++kk) {
+          const int src = (lane & ~3) | (kk >> 1);
+          const float w0 = __shfl_sync(0xffffffffu, (kk & 1) ? s[i][1] : s[i][0], src);
+          const float w1 = __shfl_sync(0xffffffffu, (kk & 1) ? s[i][3] : s[i][2], src);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(stage + KT * ROW + piece(k0 + i * 8 + kk, dt) +
+                                                                  (lane & 3) * 4);
+            if (!nonfinite_pair(v)) continue;
+            const float lo = bf16_lo(v), hi = bf16_hi(v);
+            if (finite_pair(v & 0xffffu) != (v & 0xffffu)) {
+              if (w0 != 0.0f) o[dt][0] = fmaf(w0, lo, o[dt][0]);
+              if (w1 != 0.0f) o[dt][2] = fmaf(w1, lo, o[dt][2]);
+            }
+            if (finite_pair(v & 0xffff0000u) != (v & 0xffff0000u)) {
+              if (w0 != 0.0f) o[dt][1] = fmaf(w0, hi, o[dt][1]);
+              if (w1 != 0.0f) o[dt][3] = fmaf(w1, hi, o[dt][3]);
+            }
+          }
+        }
+    }
+  }
+
+  __device__ void dump(float* so, float* sm, float* sl) {
+    const int lane = threadIdx.x & 31, wk = key_group();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float sum = l[h];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int row = wk * MT + row_group() * 16 + (lane >> 2) + h * 8;
+      if ((lane & 3) == 0) sm[row] = m[h], sl[row] = sum;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+        *reinterpret_cast<float2*>(so + row * DP + dt * 8 + (lane & 3) * 2) = make_float2(o[dt][h * 2], o[dt][h * 2 + 1]);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------------------------------------------------
 
@@ -183,39 +402,10 @@ struct SimtEngine {
 // engine's own, the keys' offsets and validity, and the rows' m, l and weights at the end of a unit.
 template <class E>
 struct Lay {
-  static constexpr int kPart = E::MT * (E::kDP + 2) + 4;  // floats of a part: O, m, l, status
   static constexpr int kFinish = E::WK * E::MT * E::kDP * 4;
   static constexpr int kRing = E::STAGES * E::STAGE > kFinish ? E::STAGES * E::STAGE : kFinish;
   static constexpr int kSmem = kRing + E::EXTRA + (E::STAGES + 1) * (E::KT * 8 + 16) + E::WK * E::MT * 3 * 4;
 };
-
-template <bool BF16>
-__device__ __forceinline__ void store4(char* p, float4 v) {
-  if (BF16) {
-    uint2 u;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(v.y), "f"(v.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(v.w), "f"(v.z));
-    *reinterpret_cast<uint2*>(p) = u;
-  } else {
-    *reinterpret_cast<float4*>(p) = v;
-  }
-}
-
-// One query row's quad of columns, normalised, and its lse.
-template <class E>
-__device__ __forceinline__ void write_row(const AttnParams& p, const AttnRequest& r, int hkv, int row, int d, float4 o,
-                                          float m, float l) {
-  if (row >= r.n * p.group) return;
-  const int64_t grow = r.row0 + row / p.group;
-  const int head = hkv * p.group + row % p.group;
-  const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
-  const float inv = none ? 0.0f : 1.0f / l;
-  if (d < p.c.head_dim) {
-    o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    store4<E::kBf16>(p.out + (grow * p.o_row + head * p.o_head + d) * (E::kBf16 ? 2 : 4), o);
-  }
-  if (d == 0 && p.lse) p.lse[grow * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
-}
 
 template <class E>
 __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
@@ -236,80 +426,16 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
   __shared__ int64_t s_find[2];
   __shared__ int s_last;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int block = blockIdx.x;
+  auto sync = [] { __syncthreads(); };
 
   grid_dependency_wait();
   allow_dependents();
-
-  // The line of tiles: its length, and the request this block starts in.
-  auto tiles_of = [&](const AttnRequest& r) -> int64_t {
-    if (r.n == 0) return 0;
-    const int64_t row_tiles = (static_cast<int64_t>(r.n) * p.group + MT - 1) / MT;
-    return p.c.heads * row_tiles * ((r.len + r.n + KT - 1) / KT);
-  };
-  int64_t mine = 0;
-  for (int b = t; b < p.batch; b += T) mine += tiles_of(attn_request(p, b));
-  int64_t sum = mine;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) s_sum[warp] = sum;
-  if (t == 0) s_find[0] = -1;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < T / 32; ++w) total += s_sum[w];
-  __syncthreads();
-  const int64_t g = total < gridDim.x ? (total > 0 ? total : 1) : gridDim.x;  // blocks that have work
-  // Requests without rows have no tiles: their status is written here.
-  for (int b = block * T + t; b < p.batch; b += gridDim.x * T) {
-    const AttnRequest r = attn_request(p, b);
-    if (r.n == 0) p.status[b] = r.status;
-  }
-  if (block >= g || total == 0) return;
-  const int64_t start = block * total / g, end = (block + 1) * total / g;
-  int64_t before = 0;  // tiles of the requests before the chunk
-  for (int b0 = 0; b0 < p.batch; b0 += T) {
-    const int b = b0 + t;
-    int64_t own = b < p.batch ? tiles_of(attn_request(p, b)) : 0;
-    int64_t inc = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    int64_t base = before, chunk = 0;
-#pragma unroll
-    for (int w = 0; w < T / 32; ++w) {
-      if (w < warp) base += s_sum[w];
-      chunk += s_sum[w];
-    }
-    if (own > 0 && base + inc - own <= start && start < base + inc) {
-      s_find[0] = b;
-      s_find[1] = base + inc - own;
-    }
-    __syncthreads();
-    before += chunk;
-    if (s_find[0] >= 0) break;
-  }
-  int b = static_cast<int>(s_find[0]);
-  int64_t first = s_find[1];  // first tile of request b
-
-  for (int64_t pos = start; pos < end;) {
-    AttnRequest r = attn_request(p, b);
-    const int64_t have = tiles_of(r);
-    if (pos >= first + have) {  // next request
-      first += have;
-      ++b;
-      continue;
-    }
-    const int nt = (r.len + r.n + KT - 1) / KT;
-    const int row_tiles = (r.n * p.group + MT - 1) / MT;
-    const int unit = static_cast<int>((pos - first) / nt);
-    const int t0 = static_cast<int>((pos - first) - static_cast<int64_t>(unit) * nt);
-    const int rt = unit % row_tiles, hkv = unit / row_tiles;
-    const int cnt = static_cast<int>(min(static_cast<int64_t>(nt - t0), end - pos));
+  const AttnSpan span = attn_span<MT, KT, T>(p, t, s_sum, s_find, sync);
+  AttnWalk<MT, KT> walk(p, span);
+  AttnSegment s;
+  while (walk.next(s)) {
+    const AttnRequest& r = s.r;
+    const int end = s.t0 + s.cnt;
     const int keys = r.len + r.n;
     uint32_t bad = 0u;  // this thread placed a key outside the cache
 
@@ -317,26 +443,26 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
     // Offsets of a tile's keys: fetched as raw words two tiles before they are needed.
     int64_t word = -1;
     auto fetch = [&](int tile) {
-      if (t < KT) word = tile < t0 + cnt ? key_word(p, r, b, tile * KT + t) : -1;
+      if (t < KT) word = tile < end ? key_word(p, r, s.b, tile * KT + t) : -1;
     };
     auto place = [&](int tile) {
       if (t < KT) {
         const int x = tile * KT + t;
-        const int64_t off = tile < t0 + cnt ? key_offset(p, r, x, word) : -1;
+        const int64_t off = tile < end ? key_offset(p, r, x, word) : -1;
         const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
-        if (tile < t0 + cnt && x < keys && off < 0) bad |= kStSlotRange;
+        if (tile < end && x < keys && off < 0) bad |= kStSlotRange;
         s_off[(tile % RING) * KT + t] = off;
         if (lane == 0) s_valid[(tile % RING) * 4 + warp] = ok;
       }
     };
     auto load = [&](int tile) {
-      if (tile < t0 + cnt) {
+      if (tile < end) {
         const uint32_t dst = smem_addr(ring + (tile % S) * E::STAGE);
         for (int x = t; x < KT * PIECES; x += T) {
           const int key = x / PIECES, c = x % PIECES;
           const int64_t off = s_off[(tile % RING) * KT + key];
           const bool ok = off >= 0 && c * 16 < p.c.head_dim * ES;
-          const int64_t byte = ok ? (off + hkv * p.c.head_stride) * ES + c * 16 : 0;
+          const int64_t byte = ok ? (off + s.hkv * p.c.head_stride) * ES + c * 16 : 0;
           cp_async16(dst + E::piece(key, c), p.c.k + byte, ok);
           cp_async16(dst + KT * E::ROW + E::piece(key, c), p.c.v + byte, ok);
         }
@@ -344,20 +470,20 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
       cp_async_commit();
     };
     for (int i = 0; i < S; ++i) {
-      fetch(t0 + i);
-      place(t0 + i);
+      fetch(s.t0 + i);
+      place(s.t0 + i);
     }
-    fetch(t0 + S);
+    fetch(s.t0 + S);
     __syncthreads();
-    for (int i = 0; i < S - 1; ++i) load(t0 + i);
-    eng.init(p, r, hkv, rt, extra);
-    for (int tile = t0; tile < t0 + cnt; ++tile) {
+    for (int i = 0; i < S - 1; ++i) load(s.t0 + i);
+    eng.init(p, r, s.hkv, s.rt, extra);
+    for (int tile = s.t0; tile < end; ++tile) {
       cp_async_wait<S - 2>();
       __syncthreads();
       load(tile + S - 1);
       place(tile + S);
       fetch(tile + S + 1);
-      eng.tile(p, r, b, rt, tile * KT, ring + (tile % S) * E::STAGE, s_valid + (tile % RING) * 4);
+      eng.tile(p, r, s.b, s.rt, tile * KT, ring + (tile % S) * E::STAGE, s_valid + (tile % RING) * 4);
     }
     cp_async_wait<0>();
     bad = (__syncthreads_or(static_cast<int>(bad)) ? kStSlotRange : 0u) | r.status;
@@ -366,19 +492,19 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
     float* s_o = reinterpret_cast<float*>(ring);
     eng.dump(s_o, s_m, s_l);
     __syncthreads();
-    if (t < MT) {
+    for (int row = t; row < MT; row += T) {
       float M = -kInfF;
 #pragma unroll
-      for (int k = 0; k < WK; ++k) M = fmax_nan(M, s_m[k * MT + t]);
+      for (int k = 0; k < WK; ++k) M = fmax_nan(M, s_m[k * MT + row]);
       float L = 0.0f;
 #pragma unroll
       for (int k = 0; k < WK; ++k) {
-        const float w = M == -kInfF ? 0.0f : ex2_fast(s_m[k * MT + t] - M);
-        s_w[k * MT + t] = w;
-        L = fmaf(w, s_l[k * MT + t], L);
+        const float w = M == -kInfF ? 0.0f : ex2_fast(s_m[k * MT + row] - M);
+        s_w[k * MT + row] = w;
+        L = fmaf(w, s_l[k * MT + row], L);
       }
-      s_m[t] = M;
-      s_l[t] = L;
+      s_m[row] = M;
+      s_l[row] = L;
     }
     __syncthreads();
     auto joined = [&](int row, int d) {
@@ -391,71 +517,23 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
       }
       return a;
     };
-    const bool whole = cnt == nt;
-    const bool reports = hkv == 0 && rt == row_tiles - 1;  // this unit's keys are all of the request's
-    if (whole) {
+    if (s.cnt == s.nt) {
       for (int x = t; x < MT * QUADS; x += T) {
         const int row = x / QUADS, d = (x % QUADS) * 4;
-        write_row<E>(p, r, hkv, rt * MT + row, d, joined(row, d), s_m[row], s_l[row]);
+        write_row<E::kBf16>(p, r, s.hkv, s.rt * MT + row, d, joined(row, d), s_m[row], s_l[row]);
       }
-      if (reports && t == 0) p.status[b] = bad;
+      if (s.reports && t == 0) p.status[s.b] = bad;
     } else {
-      // A part: slot 0 for the block's first tiles, 1 for a unit that begins inside the block.
-      float* part = p.parts + (static_cast<int64_t>(block) * 2 + (pos == start ? 0 : 1)) * Lay<E>::kPart;
+      float* part = attn_part<MT, DP>(p, blockIdx.x, s.at_start);
       for (int x = t; x < MT * QUADS; x += T) {
         const int row = x / QUADS, d = (x % QUADS) * 4;
         *reinterpret_cast<float4*>(part + row * DP + d) = joined(row, d);
       }
-      if (t < MT) part[MT * DP + t] = s_m[t], part[MT * DP + MT + t] = s_l[t];
+      for (int row = t; row < MT; row += T) part[MT * DP + row] = s_m[row], part[MT * DP + MT + row] = s_l[row];
       if (t == 0) part[MT * (DP + 2)] = __uint_as_float(bad);
-      __syncthreads();
-      // The unit's blocks: those that own its first and its last tile.
-      const int64_t u0 = first + static_cast<int64_t>(unit) * nt, u1 = u0 + nt - 1;
-      const int c0 = static_cast<int>(((u0 + 1) * g - 1) / total), c1 = static_cast<int>(((u1 + 1) * g - 1) / total);
-      if (t == 0) {
-        const bool last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0);
-        if (last) p.tickets[c0] = 0u;
-        s_last = last ? 1 : 0;
-      }
-      __syncthreads();
-      if (s_last) {
-        const int64_t begin0 = c0 * total / g;
-        auto part_of = [&](int c) {
-          return p.parts + (static_cast<int64_t>(c) * 2 + (c == c0 && begin0 != u0 ? 1 : 0)) * Lay<E>::kPart;
-        };
-        uint32_t any = 0u;
-        if (t < MT) {
-          float M = -kInfF, L = 0.0f;
-          for (int c = c0; c <= c1; ++c) M = fmax_nan(M, __ldcg(part_of(c) + MT * DP + t));
-          if (M > -kInfF || M != M)
-            for (int c = c0; c <= c1; ++c)
-              L = fmaf(ex2_fast(__ldcg(part_of(c) + MT * DP + t) - M), __ldcg(part_of(c) + MT * DP + MT + t), L);
-          s_m[t] = M;
-          s_l[t] = L;
-        }
-        if (t == 0)
-          for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(part_of(c) + MT * (DP + 2)));
-        __syncthreads();
-        for (int x = t; x < MT * QUADS; x += T) {
-          const int row = x / QUADS, d = (x % QUADS) * 4;
-          const float M = s_m[row];
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (M != -kInfF) {
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float* q = part_of(c);
-              const float w = ex2_fast(__ldcg(q + MT * DP + row) - M);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(q + row * DP + d));
-              a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
-            }
-          }
-          write_row<E>(p, r, hkv, rt * MT + row, d, a, M, s_l[row]);
-        }
-        if (reports && t == 0) p.status[b] = any;
-      }
+      attn_join<E::kBf16, MT, DP, T>(p, span, s, t, s_m, s_l, &s_last, sync);
     }
     __syncthreads();  // the ring and the offsets are free again
-    pos += cnt;
   }
 }
 
@@ -491,11 +569,24 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
   return launch_pdl(k_attention<E>, dim3(static_cast<unsigned>(grid)), dim3(E::THREADS), Lay<E>::kSmem, stream, p);
 }
 
-template <bool BF16>
-cudaError_t launch_dim(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  if (p.c.head_dim <= 64) return launch<SimtEngine<BF16, 64>>(p, dev, stream);
-  if (p.c.head_dim <= 128) return launch<SimtEngine<BF16, 128>>(p, dev, stream);
-  return launch<SimtEngine<BF16, 256>>(p, dev, stream);
+// Row tiles of 16, 32 or 64: the smallest that holds a request's rows, so that few rows leave their warps to the keys.
+template <int DP>
+cudaError_t launch_mma(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
+  if (rows <= 16) return launch<MmaEngine<DP, 1>>(p, dev, stream);
+  if (rows <= 32) return launch<MmaEngine<DP, 2>>(p, dev, stream);
+  return launch<MmaEngine<DP, 4>>(p, dev, stream);
+}
+
+cudaError_t launch_attention(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  const int dim = p.c.head_dim;
+  if (p.c.es == 2 && dim <= 128 && static_cast<int64_t>(p.max_len) * p.group > 32)
+    return launch_attention_wide(p, dev, stream);
+  if (p.c.es == 2)
+    return dim <= 64 ? launch_mma<64>(p, dev, stream)
+                     : dim <= 128 ? launch_mma<128>(p, dev, stream) : launch_mma<256>(p, dev, stream);
+  return dim <= 64 ? launch<SimtEngine<64>>(p, dev, stream)
+                   : dim <= 128 ? launch<SimtEngine<128>>(p, dev, stream) : launch<SimtEngine<256>>(p, dev, stream);
 }
 
 // Floats of one part: the largest row tile any engine has for this head size.
@@ -550,7 +641,7 @@ sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int
                      cu_seqlens, seq_lens, row_slots, mask, dev_status, batch, max_len, num_heads,
                      num_heads / c.heads, total_rows, scale * 1.44269504088896340736f,
                      reinterpret_cast<uint32_t*>(base), reinterpret_cast<float*>(base + kAttnCounterBytes)};
-  e = c.es == 2 ? launch_dim<true>(p, dev, stream) : launch_dim<false>(p, dev, stream);
+  e = launch_attention(p, dev, stream);
   return e == cudaSuccess ? SV_OK : cuda_failure(e);
 }
 

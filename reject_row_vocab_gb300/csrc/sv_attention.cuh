@@ -104,4 +104,231 @@ __device__ __forceinline__ bool row_sees(const AttnParams& p, int b, int i, int 
   return p.mask[(static_cast<int64_t>(b) * p.max_len + i) * p.max_len + j] != 0;
 }
 
+constexpr float kLn2 = 0.693147180559945309417f;
+
+template <bool BF16>
+__device__ __forceinline__ void store4(char* p, float4 v) {
+  if (BF16) {
+    uint2 u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(v.y), "f"(v.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(v.w), "f"(v.z));
+    *reinterpret_cast<uint2*>(p) = u;
+  } else {
+    *reinterpret_cast<float4*>(p) = v;
+  }
+}
+
+// One query row's quad of columns, normalised, and its lse.
+template <bool BF16>
+__device__ __forceinline__ void write_row(const AttnParams& p, const AttnRequest& r, int hkv, int row, int d, float4 o,
+                                          float m, float l) {
+  if (row >= r.n * p.group) return;
+  const int64_t grow = r.row0 + row / p.group;
+  const int head = hkv * p.group + row % p.group;
+  const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
+  const float inv = none ? 0.0f : 1.0f / l;
+  if (d < p.c.head_dim) {
+    o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    store4<BF16>(p.out + (grow * p.o_row + head * p.o_head + d) * (BF16 ? 2 : 4), o);
+  }
+  if (d == 0 && p.lse) p.lse[grow * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
+}
+
+
+// ---------------------------------------------------------------------------------------------------------------------
+// The line of tiles
+// ---------------------------------------------------------------------------------------------------------------------
+
+template <int MT, int KT>
+__device__ __forceinline__ int64_t attn_tiles(const AttnParams& p, const AttnRequest& r) {
+  if (r.n == 0) return 0;
+  const int64_t row_tiles = (static_cast<int64_t>(r.n) * p.group + MT - 1) / MT;
+  return p.c.heads * row_tiles * ((r.len + r.n + KT - 1) / KT);
+}
+
+// A block's stretch of the line, and the request it starts in.
+struct AttnSpan {
+  int64_t total, g;     // all tiles; blocks that have work
+  int64_t start, end;   // this block's tiles (start == end: none)
+  int32_t b;            // request of the first one
+  int64_t first;        // that request's first tile
+};
+
+// Computed by every block for itself (one pass over the requests for the total, one to find the start), by T threads
+// of which this is thread t; sync() is a barrier among them.  s_sum [T / 32] and s_find [2] are shared.
+template <int MT, int KT, int T, class Sync>
+__device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_t* s_sum, int64_t* s_find, Sync sync) {
+  const int lane = t & 31, warp = t >> 5;
+  AttnSpan sp{};
+  int64_t sum = 0;
+  for (int b = t; b < p.batch; b += T) sum += attn_tiles<MT, KT>(p, attn_request(p, b));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) s_sum[warp] = sum;
+  if (t == 0) s_find[0] = -1;
+  sync();
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) sp.total += s_sum[w];
+  sync();
+  const int64_t blocks = gridDim.x;
+  sp.g = sp.total < blocks ? (sp.total > 0 ? sp.total : 1) : blocks;
+  // Requests without rows have no tiles: their status is written here.
+  for (int b = blockIdx.x * T + t; b < p.batch; b += gridDim.x * T) {
+    const AttnRequest r = attn_request(p, b);
+    if (r.n == 0) p.status[b] = r.status;
+  }
+  if (blockIdx.x >= sp.g || sp.total == 0) return sp;
+  sp.start = blockIdx.x * sp.total / sp.g;
+  sp.end = (blockIdx.x + 1) * sp.total / sp.g;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += T) {
+    const int b = b0 + t;
+    const int64_t own = b < p.batch ? attn_tiles<MT, KT>(p, attn_request(p, b)) : 0;
+    int64_t inc = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    sync();
+    int64_t base = before, chunk = 0;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) {
+      if (w < warp) base += s_sum[w];
+      chunk += s_sum[w];
+    }
+    if (own > 0 && base + inc - own <= sp.start && sp.start < base + inc) {
+      s_find[0] = b;
+      s_find[1] = base + inc - own;
+    }
+    sync();
+    before += chunk;
+    if (s_find[0] >= 0) break;
+  }
+  sp.b = static_cast<int32_t>(s_find[0]);
+  sp.first = s_find[1];
+  return sp;
+}
+
+// The block's next segment: consecutive key tiles of one unit.
+struct AttnSegment {
+  AttnRequest r;
+  int32_t b, hkv, rt;
+  int32_t t0, cnt, nt;  // its key tiles [t0, t0 + cnt) of nt
+  int64_t u0;           // the unit's first tile in the line
+  bool at_start;        // it begins the block's stretch
+  bool reports;         // its unit sees all of the request's keys: it carries the request's status
+};
+
+template <int MT, int KT>
+struct AttnWalk {
+  const AttnParams& p;
+  AttnSpan sp;
+  int64_t pos;
+
+  __device__ AttnWalk(const AttnParams& params, const AttnSpan& s) : p(params), sp(s), pos(s.start) {}
+
+  __device__ bool next(AttnSegment& s) {
+    while (pos < sp.end) {
+      s.r = attn_request(p, sp.b);
+      const int64_t have = attn_tiles<MT, KT>(p, s.r);
+      if (pos >= sp.first + have) {
+        sp.first += have;
+        ++sp.b;
+        continue;
+      }
+      s.b = sp.b;
+      s.nt = (s.r.len + s.r.n + KT - 1) / KT;
+      const int row_tiles = (s.r.n * p.group + MT - 1) / MT;
+      const int unit = static_cast<int>((pos - sp.first) / s.nt);
+      s.u0 = sp.first + static_cast<int64_t>(unit) * s.nt;
+      s.t0 = static_cast<int>(pos - s.u0);
+      s.rt = unit % row_tiles;
+      s.hkv = unit / row_tiles;
+      s.cnt = static_cast<int>(min(static_cast<int64_t>(s.nt - s.t0), sp.end - pos));
+      s.at_start = pos == sp.start;
+      s.reports = s.hkv == 0 && s.rt == row_tiles - 1;
+      pos += s.cnt;
+      return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------------------------------------------------------------
+// Parts of a unit that several blocks share
+// ---------------------------------------------------------------------------------------------------------------------
+
+// Floats of a part: O [MT][DP], m [MT], l [MT], status.
+template <int MT, int DP>
+struct AttnPart {
+  static constexpr int kFloats = MT * (DP + 2) + 4;
+};
+
+// Where this block leaves its part of a segment: slot 0 for its first tiles, 1 for a unit that begins inside it.
+template <int MT, int DP>
+__device__ __forceinline__ float* attn_part(const AttnParams& p, int block, bool at_start) {
+  return p.parts + (static_cast<int64_t>(block) * 2 + (at_start ? 0 : 1)) * AttnPart<MT, DP>::kFloats;
+}
+
+// After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
+// writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_m, s_l [MT] and s_last
+// are shared.
+template <bool BF16, int MT, int DP, int T, class Sync>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
+                                          float* s_m, float* s_l, int* s_last, Sync sync) {
+  constexpr int QUADS = DP / 4;
+  sync();
+  const int64_t u1 = s.u0 + s.nt - 1;  // the unit's blocks are those that own its first and its last tile
+  const int c0 = static_cast<int>(((s.u0 + 1) * sp.g - 1) / sp.total);
+  const int c1 = static_cast<int>(((u1 + 1) * sp.g - 1) / sp.total);
+  if (t == 0) {
+    const bool last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0);
+    if (last) p.tickets[c0] = 0u;
+    *s_last = last ? 1 : 0;
+  }
+  sync();
+  if (!*s_last) return;
+  const bool inside = c0 * sp.total / sp.g != s.u0;  // the unit begins inside its first block's stretch
+  const float* first = attn_part<MT, DP>(p, c0, !inside);
+  auto part_of = [&](int c) { return c == c0 ? first : attn_part<MT, DP>(p, c, true); };
+  for (int row = t; row < MT; row += T) {
+    float M = -kInfF, L = 0.0f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) M = fmax_nan(M, __ldcg(part_of(c) + MT * DP + row));
+    if (M != -kInfF) {
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c)
+        L = fmaf(ex2_fast(__ldcg(part_of(c) + MT * DP + row) - M), __ldcg(part_of(c) + MT * DP + MT + row), L);
+    }
+    s_m[row] = M;
+    s_l[row] = L;
+  }
+  uint32_t any = 0u;
+  if (t == 0 && s.reports)
+    for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(part_of(c) + MT * (DP + 2)));
+  sync();
+  const int live = min(MT, s.r.n * p.group - s.rt * MT);
+  for (int x = t; x < live * QUADS; x += T) {
+    const int row = x / QUADS, d = (x % QUADS) * 4;
+    const float M = s_m[row];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (M != -kInfF) {
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float* q = part_of(c);
+        const float w = ex2_fast(__ldcg(q + MT * DP + row) - M);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + row * DP + d));
+        a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+      }
+    }
+    write_row<BF16>(p, s.r, s.hkv, s.rt * MT + row, d, a, M, s_l[row]);
+  }
+  if (s.reports && t == 0) p.status[s.b] = any;
+}
+
+// The tensor-memory kernel (bf16, head_dim <= 128).
+cudaError_t launch_attention_wide(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
+
 }  // namespace sv

@@ -1,0 +1,571 @@
+// Attention over the paged cache for many query rows, on the fifth-generation
+// tensor cores: bf16, heads of up to 128, tiles of 128 rows and 128 keys.
+//
+//   S = Q K^T (128 x 128, tensor memory)     one thread issues the products
+//   P = 2^(c S - m), l += sum P              one thread a row: no exchange
+//   O += P V  (P from tensor memory)         accumulated in tensor memory
+//
+// Four softmax warps, four loading warps and one warp that issues the matrix
+// instructions, connected by mbarriers.  The loading warps gather K and V rows
+// through the page table with 16-byte asynchronous copies into a ring of
+// tiles in the 128-byte swizzle the matrix unit reads, and run ahead over the
+// ends of units.  S has two buffers, so the next tile's scores are computed
+// while this one's weights are taken; P overwrites its own S.  The reference m
+// moves (and O is rescaled) only when a row's maximum has grown by more than
+// 2^8: the weights stay below 2^8, the sums in fp32, and the result does not
+// depend on the reference.
+//
+// Every wait is bounded; a wait that gives up raises SV_DEV_TIMEOUT, lets all
+// warps leave, and the block frees its tensor memory.
+//
+//   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
+#include <cstdint>
+#include <mutex>
+
+#include "sv_attention.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;  // a tile
+constexpr int kSoftmaxThreads = 128, kLoadThreads = 128;
+constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 32;
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr float kSlack = 8.0f;  // log2 units a row's maximum may pass its reference by
+
+// ---------------------------------------------------------------------------------------------------------------------
+// Tensor memory and matrix instructions
+// ---------------------------------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of the calling warp's 32 lanes: one row's values a thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand in the 128-byte swizzle.  Stride: bytes between groups of eight rows (1024); lead: bytes between
+// 64-element blocks of the contiguous axis (used where that axis is the operand's M or N).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lead >> 4) & 0x3fffu) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, 128 rows, n columns; b_mn: B's contiguous axis is N (V as it lies), not K.
+__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // NaN and infinities replaced by 0
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// ---------------------------------------------------------------------------------------------------------------------
+// Layout
+// ---------------------------------------------------------------------------------------------------------------------
+
+template <int DP>
+struct Wide {
+  static constexpr int kBlock = kKeys * 128;          // 128 rows of 64 elements
+  static constexpr int kTile = kBlock * (DP / 64);    // a K or V tile, or Q
+  static constexpr int kRing = DP == 128 ? 6 : 8;     // tiles in the ring
+  static constexpr int kFlight = 4;                   // of them, copies a thread leaves unfinished
+  static constexpr int kInfo = 8;                     // tiles whose validity is kept
+  static constexpr int kPieces = DP / 8;              // 16-byte pieces of a row
+  static constexpr int kS = 0, kO = 256;              // tensor memory columns: two S of 128, then O
+  // shared memory
+  static constexpr int kQ = 0;
+  static constexpr int kTiles = kTile;
+  static constexpr int kOff = kTiles + kRing * kTile;             // int64 [2][kKeys]
+  static constexpr int kValid = kOff + 2 * kKeys * 8;             // uint32 [kInfo][8]: four valid words, four bad
+  static constexpr int kBars = kValid + kInfo * 8 * 4;            // full, empty [kRing], s [2], p [2], pv, q, two meets
+  static constexpr int kMisc = kBars + (2 * kRing + 8) * 8;       // sums [9], find [2]; tmem, abort, last, careful
+  static constexpr int kSmem = kMisc + 11 * 8 + 4 * 4;
+  // 16-byte piece c of row r of a tile
+  __device__ static uint32_t piece(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  }
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p) {
+  using W = Wide<DP>;
+  constexpr int NB = W::kRing;
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t base = smem_addr(smem);
+  int64_t* s_off = reinterpret_cast<int64_t*>(smem + W::kOff);
+  volatile uint32_t* s_valid = reinterpret_cast<volatile uint32_t*>(smem + W::kValid);
+  int64_t* s_sum = reinterpret_cast<int64_t*>(smem + W::kMisc);
+  int64_t* s_find = s_sum + 9;
+  int* s_misc = reinterpret_cast<int*>(s_find + 2);
+  volatile int* s_abort = s_misc + 1;
+  int* s_last = s_misc + 2;
+  volatile int* s_careful = s_misc + 3;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  auto bar_full = [&](int i) { return base + W::kBars + i * 8; };
+  auto bar_empty = [&](int i) { return base + W::kBars + (NB + i) * 8; };
+  auto bar_s = [&](int i) { return base + W::kBars + (2 * NB + i) * 8; };
+  auto bar_p = [&](int i) { return base + W::kBars + (2 * NB + 2 + i) * 8; };
+  const uint32_t bar_pv = base + W::kBars + (2 * NB + 4) * 8, bar_q = bar_pv + 8;
+  const uint32_t bar_load = bar_pv + 16, bar_soft = bar_pv + 24;  // the loading warps, the softmax warps meet
+
+  if (t == 0) {
+    for (int i = 0; i < NB; ++i) mbar_init(bar_full(i), kLoadThreads), mbar_init(bar_empty(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar_s(i), 2), mbar_init(bar_p(i), kSoftmaxThreads);
+    mbar_init(bar_pv, 1);
+    mbar_init(bar_q, kSoftmaxThreads);
+    mbar_init(bar_load, kLoadThreads);
+    mbar_init(bar_soft, kSoftmaxThreads);
+    mbar_fence_init();
+    *s_abort = 0;
+    *s_careful = 0;
+  }
+  if (warp == 8) {
+    tmem_alloc(base + W::kMisc + 11 * 8, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(s_misc[0]);
+
+  grid_dependency_wait();
+  allow_dependents();
+  const AttnSpan span = attn_span<kRows, kKeys, kWideThreads>(p, t, s_sum, s_find, [] { __syncthreads(); });
+  AttnWalk<kRows, kKeys> walk(p, span);
+
+  // A wait that gives up ends every role; the lanes of a warp leave together.
+  auto wait_one = [&](uint32_t bar, uint32_t parity) {
+    if (mbar_wait_bounded(bar, parity, s_abort, kWaitNs)) return true;
+    *s_abort = 1;
+    return false;
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
+
+  if (warp >= 4 && warp < 8) {
+    // ---- Loading warps: tile g's K is group 2 g of the ring, its V group 2 g + 1.
+    const int lt = t - kSoftmaxThreads;
+    AttnSegment s{};
+    bool more = walk.next(s);
+    int tile = s.t0;
+    int64_t word = more ? key_word(p, s.r, s.b, tile * kKeys + lt) : -1;
+    uint32_t q = 0;  // groups issued
+    bool ok = true;
+    auto landed = [&](uint32_t group) {  // this thread's copies of the group are in place
+      fence_async();
+      mbar_arrive(bar_full(group % NB));
+    };
+    while (more && ok) {
+      const AttnSegment cur = s;
+      const int x = tile * kKeys + lt;
+      const int64_t off = key_offset(p, cur.r, x, word);
+      const bool outside = x < cur.r.len + cur.r.n && off < 0;
+      // the next tile's word is on its way while this tile is copied
+      if (++tile >= s.t0 + s.cnt) {
+        more = walk.next(s);
+        tile = s.t0;
+      }
+      if (more) word = key_word(p, s.r, s.b, tile * kKeys + lt);
+      const uint32_t g = q >> 1;
+      if (q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) break;
+      s_off[(g & 1) * kKeys + lt] = off;
+      const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
+      const uint32_t bad = __ballot_sync(0xffffffffu, outside);
+      if (lane == 0) {
+        s_valid[(g % W::kInfo) * 8 + (warp - 4)] = valid;
+        s_valid[(g % W::kInfo) * 8 + 4 + (warp - 4)] = bad;
+      }
+      mbar_arrive(bar_load);
+      if (!wait(bar_load, g & 1)) break;
+      for (int which = 0; which < 2; ++which, ++q) {
+        if (which == 1 && q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const char* src = which ? p.c.v : p.c.k;
+        const uint32_t dst = base + W::kTiles + (q % NB) * W::kTile;
+        const int c = lt % W::kPieces;
+        const bool in_head = c * 8 < p.c.head_dim;
+        const int64_t shift = static_cast<int64_t>(cur.hkv) * p.c.head_stride + c * 8;
+#pragma unroll 8
+        for (int r = lt / W::kPieces; r < kKeys; r += kLoadThreads / W::kPieces) {
+          const int64_t o = s_off[(g & 1) * kKeys + r];
+          const bool live = o >= 0 && in_head;
+          cp_async16(dst + W::piece(r, c), src + (live ? (o + shift) * 2 : 0), live);
+        }
+        cp_async_commit();
+        if (q + 1 >= W::kFlight) {
+          cp_async_wait<W::kFlight - 1>();
+          landed(q + 1 - W::kFlight);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (ok)
+      for (uint32_t i = q >= W::kFlight - 1 ? q - (W::kFlight - 1) : 0; i < q; ++i) landed(i);
+  } else if (warp == 8) {
+    // ---- The issuing thread.
+    if (lane == 0) {
+      AttnSegment s;
+      uint32_t g = 0, units = 0;
+      bool ok = true;
+      auto scores = [&](uint32_t n) {
+        const uint32_t group = 2 * n;
+        if (!wait_one(bar_full(group % NB), (group / NB) & 1)) return false;
+        tc_fence_after();
+        mbar_arrive(bar_s(n & 1));  // hands the tile's validity on
+        const uint32_t k = base + W::kTiles + (group % NB) * W::kTile;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          const uint32_t at = (i >> 2) * W::kBlock + (i & 3) * 32;
+          mma_ss(tmem + W::kS + (n & 1) * 128, operand(base + W::kQ + at, 16), operand(k + at, 16),
+                 instruction(kKeys, false), i > 0);
+        }
+        tc_commit(bar_empty(group % NB));
+        tc_commit(bar_s(n & 1));
+        return true;
+      };
+      while (ok && walk.next(s)) {
+        if (!wait_one(bar_q, units & 1)) break;
+        tc_fence_after();
+        ok = scores(g);
+        for (int i = 0; ok && i < s.cnt; ++i) {
+          const uint32_t n = g + i, group = 2 * n + 1;
+          if (i + 1 < s.cnt && !scores(n + 1)) {
+            ok = false;
+            break;
+          }
+          if (!wait_one(bar_full(group % NB), (group / NB) & 1) || !wait_one(bar_p(n & 1), (n >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t v = base + W::kTiles + (group % NB) * W::kTile;
+#pragma unroll
+          for (int j = 0; j < kKeys / 16; ++j)
+            mma_ts(tmem + W::kO, tmem + W::kS + (n & 1) * 128 + j * 8, operand(v + j * 2048, W::kBlock),
+                   instruction(DP, true), i > 0 || j > 0);
+          tc_commit(bar_empty(group % NB));
+          tc_commit(bar_pv);
+        }
+        g += s.cnt;
+        ++units;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- Softmax warps: thread t has row t of the unit's tile.
+    uint32_t meets = 0;
+    auto meet = [&] {  // a barrier of the softmax warps, bounded like every wait
+      mbar_arrive(bar_soft);
+      wait(bar_soft, meets++ & 1);
+    };
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // scale < 0 is carried by Q's signs; a scale of 0 by one that is too small to tell (0 times a masked -inf is NaN)
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    const float c = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    AttnSegment s;
+    uint32_t g = 0;
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
+      const bool idle = warp * 32 >= rows;              // none of the warp's rows exists
+      for (int x = t; x < kRows * W::kPieces; x += kSoftmaxThreads) {
+        const int row = x / W::kPieces, col = x % W::kPieces, grow = s.rt * kRows + row;
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows && col * 8 < p.c.head_dim) {
+          const int64_t at = (s.r.row0 + grow / p.group) * p.q_row + (s.hkv * p.group + grow % p.group) * p.q_head + col * 8;
+          u = *reinterpret_cast<const uint4*>(p.q + at * 2);
+          u.x ^= flip, u.y ^= flip, u.z ^= flip, u.w ^= flip;
+        }
+        *reinterpret_cast<uint4*>(smem + W::kQ + W::piece(row, col)) = u;
+      }
+      fence_async();
+      mbar_arrive(bar_q);
+      const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread
+      float m = -kInfF, l = 0.0f;
+      uint32_t bad = 0u;
+      bool mixed = false;  // a tile whose keys some rows see and others do not
+      for (int i = 0; i < s.cnt; ++i, ++g) {
+        const int x0 = (s.t0 + i) * kKeys;
+        const uint32_t st = tmem + lanes + W::kS + (g & 1) * 128;
+        if (!wait(bar_s(g & 1), (g >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t vw[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          vw[w] = s_valid[(g % W::kInfo) * 8 + w];
+          bad |= s_valid[(g % W::kInfo) * 8 + 4 + w];
+        }
+        const bool masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xffffffffu || x0 + kKeys > s.r.len;
+        if (masked && s.r.n > 1 && x0 + kKeys > s.r.len) {
+          // A weight of 0 does not silence a V that is NaN or infinite: such values of new rows are taken out of the
+          // products here, and added to the rows that see them at the end.
+          mixed = true;
+          const uint32_t group = 2 * g + 1;
+          if (!wait(bar_full(group % NB), (group / NB) & 1)) {
+            ok = false;
+            break;
+          }
+          char* v = smem + W::kTiles + (group % NB) * W::kTile;
+          const int from = max(s.r.len - x0, 0);
+          bool found = false;
+          for (int x = from * W::kPieces + t; x < kKeys * W::kPieces; x += kSoftmaxThreads) {
+            uint4* at = reinterpret_cast<uint4*>(v + W::piece(x / W::kPieces, x % W::kPieces));
+            const uint4 u = *at;
+            const uint4 f = make_uint4(finite_pair(u.x), finite_pair(u.y), finite_pair(u.z), finite_pair(u.w));
+            if (f.x != u.x || f.y != u.y || f.z != u.z || f.w != u.w) {
+              *at = f;
+              found = true;
+            }
+          }
+          if (found) *s_careful = 1;
+          fence_async();
+        }
+        if (!idle) {
+          if (masked) {
+            // what this row sees of the tile: valid keys, history, and new rows up to itself or as the mask says
+            if (x0 + kKeys > s.r.len) {
+              const int first = max(s.r.len - x0, 0);  // first new row's place in the tile
+              const bool none = t >= rows;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                uint32_t see = 0u;
+                if (!p.mask) {
+                  const int upto = s.r.len + my_row + 1 - x0 - w * 32;  // keys seen of these 32
+                  see = none || upto <= 0 ? 0u : upto >= 32 ? 0xffffffffu : (1u << upto) - 1u;
+                } else if (!none) {
+                  const int hist = first - w * 32;
+                  see = hist <= 0 ? 0u : hist >= 32 ? 0xffffffffu : (1u << hist) - 1u;
+                  const int j0 = x0 + w * 32 - s.r.len;
+                  for (int b = max(-j0, 0); b < min(32, s.r.n - j0); ++b)
+                    if (row_sees(p, s.b, my_row, j0 + b)) see |= 1u << b;
+                }
+                vw[w] &= see;
+              }
+            }
+          }
+          // The scores are read twice, for the maximum and for the weights: 128 of them do not fit beside the rest.
+          float mx[4] = {-kInfF, -kInfF, -kInfF, -kInfF};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[64];
+            tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
+            tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j] = (vw[h * 2 + (j >> 5)] >> (j & 31) & 1u) ? v[j] : -kInfF;
+            }
+#pragma unroll
+            for (int j = 0; j < 64; ++j) mx[j & 3] = fmax_nan(mx[j & 3], v[j]);
+          }
+          const float top = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3])) * c;
+          const bool grow = !(top <= m + kSlack);  // also a first finite maximum, and NaN
+          if (i == 0) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, grow)) {
+            const float a = grow ? ex2_fast(m - top) : 1.0f;
+            if (grow) m = top;
+            l *= a;
+            if (!wait(bar_pv, (g - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < DP / 32; ++h) {
+              float o[32];
+              tmem_ld32(tmem + lanes + W::kO + h * 32, reinterpret_cast<uint32_t*>(o));
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= a;
+              tmem_st32(tmem + lanes + W::kO + h * 32, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          const float ref = m == -kInfF ? 0.0f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[64];
+            uint32_t pk[32];
+            tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
+            tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j] = (vw[h * 2 + (j >> 5)] >> (j & 31) & 1u) ? v[j] : -kInfF;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float a = ex2_fast(fmaf(v[2 * j], c, -ref));
+              const float b = ex2_fast(fmaf(v[2 * j + 1], c, -ref));
+              sum[(2 * j) & 3] += a;
+              sum[(2 * j + 1) & 3] += b;
+              pk[j] = pack_bf16(a, b);
+            }
+            tmem_st32(st + h * 32, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(bar_p(g & 1));
+      }
+      if (!ok) break;
+      // The unit's last product is done: this thread's row of O.
+      if (!wait(bar_pv, (g - 1) & 1)) break;
+      tc_fence_after();
+      bool careful = false;
+      if (mixed) {
+        meet();
+        careful = *s_careful != 0;
+        meet();
+        if (t == 0) *s_careful = 0;
+      }
+      bad = (bad ? kStSlotRange : 0u) | s.r.status;
+      const bool whole = s.cnt == s.nt;
+      float* part = whole ? nullptr : attn_part<kRows, DP>(p, blockIdx.x, s.at_start);
+      if (!idle) {
+#pragma unroll
+        for (int h = 0; h < DP / 32; ++h) {
+          float o[32];
+          tmem_ld32(tmem + lanes + W::kO + h * 32, reinterpret_cast<uint32_t*>(o));
+          tmem_wait_ld();
+          if (t < rows) {
+            if (careful) {
+              for (int j = 0; j < s.r.n; ++j) {
+                const int x = s.r.len + j;
+                if (x < s.t0 * kKeys || x >= (s.t0 + s.cnt) * kKeys || !row_sees(p, s.b, my_row, j)) continue;
+                const int64_t off = key_offset(p, s.r, x, key_word(p, s.r, s.b, x));
+                if (off < 0) continue;
+                const uint16_t* vr = reinterpret_cast<const uint16_t*>(p.c.v) + off + s.hkv * p.c.head_stride + h * 32;
+#pragma unroll
+                for (int d = 0; d < 32; ++d)
+                  if (h * 32 + d < p.c.head_dim) {
+                    const float f = __uint_as_float(static_cast<uint32_t>(vr[d]) << 16);
+                    if (!(fabsf(f) < kInfF)) o[d] += f;
+                  }
+              }
+            }
+#pragma unroll
+            for (int d = 0; d < 32; d += 4) {
+              const float4 v = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+              if (whole)
+                write_row<true>(p, s.r, s.hkv, s.rt * kRows + t, h * 32 + d, v, m, l);
+              else
+                *reinterpret_cast<float4*>(part + t * DP + h * 32 + d) = v;
+            }
+          }
+        }
+      }
+      if (whole) {
+        if (s.reports && t == 0) p.status[s.b] = bad;
+      } else {
+        // shared arrays of the join: this unit's Q is no longer read
+        float* s_m = reinterpret_cast<float*>(smem + W::kQ);
+        part[kRows * DP + t] = m;
+        part[kRows * DP + kRows + t] = l;
+        if (t == 0) part[kRows * (DP + 2)] = __uint_as_float(bad);
+        attn_join<true, kRows, DP, kSoftmaxThreads>(p, span, s, t, s_m, s_m + kRows, s_last, meet);
+        meet();
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (*s_abort) {  // never expected: see SV_DEV_TIMEOUT
+    for (int b = t; b < p.batch; b += kWideThreads) p.status[b] = kStTimeout;
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <int DP>
+cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool have[64] = {};
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return e;
+  if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!have[d]) {
+      e = cudaFuncSetAttribute(k_attention_wide<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<DP>::kSmem);
+      if (e != cudaSuccess) return e;
+      have[d] = true;
+    }
+  }
+  static_assert(Wide<DP>::kSmem <= 227 * 1024, "shared memory of a block");
+  const int grid = dev.sms < kAttnMaxBlocks / 2 ? dev.sms : kAttnMaxBlocks / 2;  // parts are laid out for 64-row tiles
+  return launch_pdl(k_attention_wide<DP>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<DP>::kSmem,
+                    stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_wide(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  return p.c.head_dim <= 64 ? launch<64>(p, dev, stream) : launch<128>(p, dev, stream);
+}
+
+}  // namespace sv
