@@ -407,6 +407,9 @@ struct Lay {
   static constexpr int kSmem = kRing + E::EXTRA + (E::STAGES + 1) * (E::KT * 8 + 16) + E::WK * E::MT * 3 * 4;
 };
 
+// What a unit costs beside its key tiles (loading Q, the join of the key groups, the first tiles' latency), in tiles.
+constexpr int kUnitPlaces = 2;
+
 template <class E>
 __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
   constexpr int T = E::THREADS, KT = E::KT, MT = E::MT, S = E::STAGES, DP = E::kDP, WK = E::WK;
@@ -430,8 +433,8 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
 
   grid_dependency_wait();
   allow_dependents();
-  const AttnSpan span = attn_span<MT, KT, T>(p, t, s_sum, s_find, sync);
-  AttnWalk<MT, KT> walk(p, span);
+  const AttnSpan span = attn_span<MT, KT, kUnitPlaces, T>(p, t, s_sum, s_find, sync);
+  AttnWalk<MT, KT, kUnitPlaces> walk(p, span);
   AttnSegment s;
   while (walk.next(s)) {
     const AttnRequest& r = s.r;
@@ -524,13 +527,14 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
       }
       if (s.reports && t == 0) p.status[s.b] = bad;
     } else {
-      float* part = attn_part<MT, DP>(p, blockIdx.x, s.at_start);
+      using P = AttnPart<MT, DP>;
+      float* part = attn_part<MT, DP>(p, blockIdx.x, s.t0 == 0);
       for (int x = t; x < MT * QUADS; x += T) {
-        const int row = x / QUADS, d = (x % QUADS) * 4;
-        *reinterpret_cast<float4*>(part + row * DP + d) = joined(row, d);
+        const int row = x % MT, quad = x / MT;
+        *reinterpret_cast<float4*>(part + x * 4) = joined(row, quad * 4);
       }
-      for (int row = t; row < MT; row += T) part[MT * DP + row] = s_m[row], part[MT * DP + MT + row] = s_l[row];
-      if (t == 0) part[MT * (DP + 2)] = __uint_as_float(bad);
+      for (int row = t; row < MT; row += T) part[P::kM + row] = s_m[row], part[P::kL + row] = s_l[row];
+      if (t == 0) part[P::kStatus] = __uint_as_float(bad);
       attn_join<E::kBf16, MT, DP, T>(p, span, s, t, s_m, s_l, &s_last, sync);
     }
     __syncthreads();  // the ring and the offsets are free again
@@ -580,7 +584,7 @@ cudaError_t launch_mma(const AttnParams& p, const DeviceInfo& dev, cudaStream_t 
 
 cudaError_t launch_attention(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   const int dim = p.c.head_dim;
-  if (p.c.es == 2 && dim <= 128 && static_cast<int64_t>(p.max_len) * p.group > 32)
+  if (p.c.es == 2 && dim <= 128 && static_cast<int64_t>(p.max_len) * p.group > 32 && p.scale_log2 >= 0.0f)
     return launch_attention_wide(p, dev, stream);
   if (p.c.es == 2)
     return dim <= 64 ? launch_mma<64>(p, dev, stream)

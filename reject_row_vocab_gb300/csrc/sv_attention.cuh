@@ -4,10 +4,11 @@
 // A unit is one request, one cache head and one tile of MT query rows (a
 // request's new rows times the query heads that share the cache head).  Its
 // keys are the request's committed positions followed by its new rows, cut
-// into tiles of KT keys.  All units' tiles form one line; block c of g works
-// on tiles [c T / g, (c + 1) T / g) of it.  So every block gets the same
-// number of tiles whatever the requests' lengths are, a long history is split
-// over many blocks and a short one is not split at all.  A unit that lies in
+// into tiles of KT keys.  All units' tiles form one line, each unit's preceded
+// by U places that stand for what a unit costs beside its tiles; block c of g
+// has places [c T / g, (c + 1) T / g) of it.  So every block gets the same
+// work whatever the requests' lengths are, a long history is split over many
+// blocks and a short one is not split at all.  A unit that lies in
 // one block is finished there; otherwise each block leaves its part (m, l, O)
 // and the unit's last block to arrive joins the parts in block order.
 #pragma once
@@ -139,29 +140,30 @@ __device__ __forceinline__ void write_row(const AttnParams& p, const AttnRequest
 // The line of tiles
 // ---------------------------------------------------------------------------------------------------------------------
 
-template <int MT, int KT>
-__device__ __forceinline__ int64_t attn_tiles(const AttnParams& p, const AttnRequest& r) {
+// Places of a request: its units times (U + key tiles).
+template <int MT, int KT, int U>
+__device__ __forceinline__ int64_t attn_places(const AttnParams& p, const AttnRequest& r) {
   if (r.n == 0) return 0;
   const int64_t row_tiles = (static_cast<int64_t>(r.n) * p.group + MT - 1) / MT;
-  return p.c.heads * row_tiles * ((r.len + r.n + KT - 1) / KT);
+  return p.c.heads * row_tiles * ((r.len + r.n + KT - 1) / KT + U);
 }
 
 // A block's stretch of the line, and the request it starts in.
 struct AttnSpan {
-  int64_t total, g;     // all tiles; blocks that have work
-  int64_t start, end;   // this block's tiles (start == end: none)
+  int64_t total, g;     // all places; blocks that have work
+  int64_t start, end;   // this block's places (start == end: none)
   int32_t b;            // request of the first one
-  int64_t first;        // that request's first tile
+  int64_t first;        // that request's first place
 };
 
 // Computed by every block for itself (one pass over the requests for the total, one to find the start), by T threads
 // of which this is thread t; sync() is a barrier among them.  s_sum [T / 32] and s_find [2] are shared.
-template <int MT, int KT, int T, class Sync>
+template <int MT, int KT, int U, int T, class Sync>
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_t* s_sum, int64_t* s_find, Sync sync) {
   const int lane = t & 31, warp = t >> 5;
   AttnSpan sp{};
   int64_t sum = 0;
-  for (int b = t; b < p.batch; b += T) sum += attn_tiles<MT, KT>(p, attn_request(p, b));
+  for (int b = t; b < p.batch; b += T) sum += attn_places<MT, KT, U>(p, attn_request(p, b));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane == 0) s_sum[warp] = sum;
@@ -172,7 +174,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_
   sync();
   const int64_t blocks = gridDim.x;
   sp.g = sp.total < blocks ? (sp.total > 0 ? sp.total : 1) : blocks;
-  // Requests without rows have no tiles: their status is written here.
+  // Requests without rows have no places: their status is written here.
   for (int b = blockIdx.x * T + t; b < p.batch; b += gridDim.x * T) {
     const AttnRequest r = attn_request(p, b);
     if (r.n == 0) p.status[b] = r.status;
@@ -183,7 +185,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_
   int64_t before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += T) {
     const int b = b0 + t;
-    const int64_t own = b < p.batch ? attn_tiles<MT, KT>(p, attn_request(p, b)) : 0;
+    const int64_t own = b < p.batch ? attn_places<MT, KT, U>(p, attn_request(p, b)) : 0;
     int64_t inc = own;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -216,12 +218,11 @@ struct AttnSegment {
   AttnRequest r;
   int32_t b, hkv, rt;
   int32_t t0, cnt, nt;  // its key tiles [t0, t0 + cnt) of nt
-  int64_t u0;           // the unit's first tile in the line
-  bool at_start;        // it begins the block's stretch
+  int64_t u0;           // the place of the unit's first tile
   bool reports;         // its unit sees all of the request's keys: it carries the request's status
 };
 
-template <int MT, int KT>
+template <int MT, int KT, int U>
 struct AttnWalk {
   const AttnParams& p;
   AttnSpan sp;
@@ -232,7 +233,7 @@ struct AttnWalk {
   __device__ bool next(AttnSegment& s) {
     while (pos < sp.end) {
       s.r = attn_request(p, sp.b);
-      const int64_t have = attn_tiles<MT, KT>(p, s.r);
+      const int64_t have = attn_places<MT, KT, U>(p, s.r);
       if (pos >= sp.first + have) {
         sp.first += have;
         ++sp.b;
@@ -241,15 +242,15 @@ struct AttnWalk {
       s.b = sp.b;
       s.nt = (s.r.len + s.r.n + KT - 1) / KT;
       const int row_tiles = (s.r.n * p.group + MT - 1) / MT;
-      const int unit = static_cast<int>((pos - sp.first) / s.nt);
-      s.u0 = sp.first + static_cast<int64_t>(unit) * s.nt;
-      s.t0 = static_cast<int>(pos - s.u0);
+      const int unit = static_cast<int>((pos - sp.first) / (s.nt + U));
+      s.u0 = sp.first + static_cast<int64_t>(unit) * (s.nt + U) + U;
+      s.t0 = static_cast<int>(max(pos - s.u0, static_cast<int64_t>(0)));
+      s.cnt = static_cast<int>(min(static_cast<int64_t>(s.nt), sp.end - s.u0)) - s.t0;
+      pos = s.u0 + s.nt;
+      if (s.cnt <= 0) continue;  // the block's places end before the unit's first tile
       s.rt = unit % row_tiles;
       s.hkv = unit / row_tiles;
-      s.cnt = static_cast<int>(min(static_cast<int64_t>(s.nt - s.t0), sp.end - pos));
-      s.at_start = pos == sp.start;
       s.reports = s.hkv == 0 && s.rt == row_tiles - 1;
-      pos += s.cnt;
       return true;
     }
     return false;
@@ -260,29 +261,30 @@ struct AttnWalk {
 // Parts of a unit that several blocks share
 // ---------------------------------------------------------------------------------------------------------------------
 
-// Floats of a part: O [MT][DP], m [MT], l [MT], status.
+// Floats of a part: O as [DP / 4][MT] quads of columns, m [MT], l [MT], status.
 template <int MT, int DP>
 struct AttnPart {
-  static constexpr int kFloats = MT * (DP + 2) + 4;
+  static constexpr int kM = MT * DP, kL = kM + MT, kStatus = kL + MT, kFloats = kStatus + 4;
 };
 
-// Where this block leaves its part of a segment: slot 0 for its first tiles, 1 for a unit that begins inside it.
+// A block leaves at most two parts: of a unit that began before it, and of one that goes on behind it.
 template <int MT, int DP>
-__device__ __forceinline__ float* attn_part(const AttnParams& p, int block, bool at_start) {
-  return p.parts + (static_cast<int64_t>(block) * 2 + (at_start ? 0 : 1)) * AttnPart<MT, DP>::kFloats;
+__device__ __forceinline__ float* attn_part(const AttnParams& p, int block, bool begins) {
+  return p.parts + (static_cast<int64_t>(block) * 2 + (begins ? 1 : 0)) * AttnPart<MT, DP>::kFloats;
 }
 
 // After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
 // writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_m, s_l [MT] and s_last
-// are shared.
+// are shared.  Eight quads a thread are joined at a time, so that the loads of a part do not wait for one another.
 template <bool BF16, int MT, int DP, int T, class Sync>
 __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
                                           float* s_m, float* s_l, int* s_last, Sync sync) {
-  constexpr int QUADS = DP / 4;
+  using P = AttnPart<MT, DP>;
+  constexpr int E = 8;
   sync();
-  const int64_t u1 = s.u0 + s.nt - 1;  // the unit's blocks are those that own its first and its last tile
+  // the unit's blocks are those that own its first and its last tile
   const int c0 = static_cast<int>(((s.u0 + 1) * sp.g - 1) / sp.total);
-  const int c1 = static_cast<int>(((u1 + 1) * sp.g - 1) / sp.total);
+  const int c1 = static_cast<int>(((s.u0 + s.nt) * sp.g - 1) / sp.total);
   if (t == 0) {
     const bool last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0);
     if (last) p.tickets[c0] = 0u;
@@ -290,40 +292,60 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
   }
   sync();
   if (!*s_last) return;
-  const bool inside = c0 * sp.total / sp.g != s.u0;  // the unit begins inside its first block's stretch
-  const float* first = attn_part<MT, DP>(p, c0, !inside);
-  auto part_of = [&](int c) { return c == c0 ? first : attn_part<MT, DP>(p, c, true); };
-  for (int row = t; row < MT; row += T) {
+  const float* first = attn_part<MT, DP>(p, c0, true);
+  const float* rest = attn_part<MT, DP>(p, 0, false);
+  auto part_of = [&](int c) { return c == c0 ? first : rest + static_cast<int64_t>(c) * 2 * P::kFloats; };
+  const int live = min(MT, s.r.n * p.group - s.rt * MT);
+  for (int row = t; row < live; row += T) {
     float M = -kInfF, L = 0.0f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) M = fmax_nan(M, __ldcg(part_of(c) + MT * DP + row));
+#pragma unroll 8
+    for (int c = c0; c <= c1; ++c) M = fmax_nan(M, __ldcg(part_of(c) + P::kM + row));
     if (M != -kInfF) {
-#pragma unroll 4
+#pragma unroll 8
       for (int c = c0; c <= c1; ++c)
-        L = fmaf(ex2_fast(__ldcg(part_of(c) + MT * DP + row) - M), __ldcg(part_of(c) + MT * DP + MT + row), L);
+        L = fmaf(ex2_fast(__ldcg(part_of(c) + P::kM + row) - M), __ldcg(part_of(c) + P::kL + row), L);
     }
     s_m[row] = M;
     s_l[row] = L;
   }
   uint32_t any = 0u;
   if (t == 0 && s.reports)
-    for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(part_of(c) + MT * (DP + 2)));
+    for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(part_of(c) + P::kStatus));
   sync();
-  const int live = min(MT, s.r.n * p.group - s.rt * MT);
-  for (int x = t; x < live * QUADS; x += T) {
-    const int row = x / QUADS, d = (x % QUADS) * 4;
-    const float M = s_m[row];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -kInfF) {
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float* q = part_of(c);
-        const float w = ex2_fast(__ldcg(q + MT * DP + row) - M);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + row * DP + d));
-        a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+  const int quads = live * (DP / 4);
+  for (int x0 = t; x0 < quads; x0 += T * E) {
+    float4 a[E];
+    int at[E], row[E];
+    float M[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int x = x0 + e * T < quads ? x0 + e * T : x0;
+      row[e] = x % live;
+      at[e] = (x / live) * MT + row[e];
+      M[e] = s_m[row[e]] == -kInfF ? 0.0f : s_m[row[e]];
+      a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+      const float* q = part_of(c);
+      float w[E];
+      float4 v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        w[e] = __ldcg(q + P::kM + row[e]);
+        v[e] = __ldcg(reinterpret_cast<const float4*>(q) + at[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float f = ex2_fast(w[e] - M[e]);
+        a[e].x = fmaf(f, v[e].x, a[e].x), a[e].y = fmaf(f, v[e].y, a[e].y);
+        a[e].z = fmaf(f, v[e].z, a[e].z), a[e].w = fmaf(f, v[e].w, a[e].w);
       }
     }
-    write_row<BF16>(p, s.r, s.hkv, s.rt * MT + row, d, a, M, s_l[row]);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (x0 + e * T < quads)
+        write_row<BF16>(p, s.r, s.hkv, s.rt * MT + row[e], at[e] / MT * 4, a[e], s_m[row[e]], s_l[row[e]]);
   }
   if (s.reports && t == 0) p.status[s.b] = any;
 }

@@ -5,8 +5,8 @@
 //   P = 2^(c S - m), l += sum P              one thread a row: no exchange
 //   O += P V  (P from tensor memory)         accumulated in tensor memory
 //
-// Four softmax warps, four loading warps and one warp that issues the matrix
-// instructions, connected by mbarriers.  The loading warps gather K and V rows
+// Four softmax warps, four loading warps, one warp that issues the matrix
+// instructions and one that loads the next unit's Q, connected by mbarriers.  The loading warps gather K and V rows
 // through the page table with 16-byte asynchronous copies into a ring of
 // tiles in the 128-byte swizzle the matrix unit reads, and run ahead over the
 // ends of units.  S has two buffers, so the next tile's scores are computed
@@ -29,7 +29,8 @@ namespace {
 
 constexpr int kRows = 128, kKeys = 128;  // a tile
 constexpr int kSoftmaxThreads = 128, kLoadThreads = 128;
-constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 32;
+constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 64;  // and a warp to issue, a warp to load Q
+constexpr int kUnitPlaces = 1;  // what a unit costs beside its key tiles, in tiles
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kSlack = 8.0f;  // log2 units a row's maximum may pass its reference by
 
@@ -130,11 +131,11 @@ struct Wide {
   // shared memory
   static constexpr int kQ = 0;
   static constexpr int kTiles = kTile;
-  static constexpr int kOff = kTiles + kRing * kTile;             // int64 [2][kKeys]
-  static constexpr int kValid = kOff + 2 * kKeys * 8;             // uint32 [kInfo][8]: four valid words, four bad
-  static constexpr int kBars = kValid + kInfo * 8 * 4;            // full, empty [kRing], s [2], p [2], pv, q, two meets
-  static constexpr int kMisc = kBars + (2 * kRing + 8) * 8;       // sums [9], find [2]; tmem, abort, last, careful
-  static constexpr int kSmem = kMisc + 11 * 8 + 4 * 4;
+  static constexpr int kValid = kTiles + kRing * kTile;     // uint32 [kInfo][8]: four valid words, four bad
+  static constexpr int kJoin = kValid + kInfo * 8 * 4;      // m, l [kRows] of a join
+  static constexpr int kBars = kJoin + 2 * kRows * 4;       // full, empty [kRing], s [2], p [2], pv, q, q free, soft
+  static constexpr int kMisc = kBars + (2 * kRing + 8) * 8; // sums [10], find [2]; tmem, abort, last, careful
+  static constexpr int kSmem = kMisc + 12 * 8 + 4 * 4;
   // 16-byte piece c of row r of a tile
   __device__ static uint32_t piece(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -147,10 +148,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   constexpr int NB = W::kRing;
   extern __shared__ __align__(1024) char smem[];
   const uint32_t base = smem_addr(smem);
-  int64_t* s_off = reinterpret_cast<int64_t*>(smem + W::kOff);
-  volatile uint32_t* s_valid = reinterpret_cast<volatile uint32_t*>(smem + W::kValid);
+  uint32_t* s_valid = reinterpret_cast<uint32_t*>(smem + W::kValid);
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem + W::kMisc);
-  int64_t* s_find = s_sum + 9;
+  int64_t* s_find = s_sum + 10;
   int* s_misc = reinterpret_cast<int*>(s_find + 2);
   volatile int* s_abort = s_misc + 1;
   int* s_last = s_misc + 2;
@@ -161,21 +161,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   auto bar_s = [&](int i) { return base + W::kBars + (2 * NB + i) * 8; };
   auto bar_p = [&](int i) { return base + W::kBars + (2 * NB + 2 + i) * 8; };
   const uint32_t bar_pv = base + W::kBars + (2 * NB + 4) * 8, bar_q = bar_pv + 8;
-  const uint32_t bar_load = bar_pv + 16, bar_soft = bar_pv + 24;  // the loading warps, the softmax warps meet
+  const uint32_t bar_qfree = bar_pv + 16, bar_soft = bar_pv + 24;  // Q may be replaced; the softmax warps meet
 
   if (t == 0) {
     for (int i = 0; i < NB; ++i) mbar_init(bar_full(i), kLoadThreads), mbar_init(bar_empty(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(bar_s(i), 2), mbar_init(bar_p(i), kSoftmaxThreads);
     mbar_init(bar_pv, 1);
-    mbar_init(bar_q, kSoftmaxThreads);
-    mbar_init(bar_load, kLoadThreads);
+    mbar_init(bar_q, 32);
+    mbar_init(bar_qfree, 1);
     mbar_init(bar_soft, kSoftmaxThreads);
     mbar_fence_init();
     *s_abort = 0;
     *s_careful = 0;
   }
   if (warp == 8) {
-    tmem_alloc(base + W::kMisc + 11 * 8, 512);
+    tmem_alloc(base + W::kMisc + 12 * 8, 512);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -185,11 +185,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
 
   grid_dependency_wait();
   allow_dependents();
-  const AttnSpan span = attn_span<kRows, kKeys, kWideThreads>(p, t, s_sum, s_find, [] { __syncthreads(); });
-  AttnWalk<kRows, kKeys> walk(p, span);
+  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kWideThreads>(p, t, s_sum, s_find, [] { __syncthreads(); });
+  AttnWalk<kRows, kKeys, kUnitPlaces> walk(p, span);
 
   // A wait that gives up ends every role; the lanes of a warp leave together.
   auto wait_one = [&](uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < 64; ++i)  // the clock is read only by waits that are long
+      if (mbar_try_wait(bar, parity)) return true;
     if (mbar_wait_bounded(bar, parity, s_abort, kWaitNs)) return true;
     *s_abort = 1;
     return false;
@@ -197,55 +199,65 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
 
   if (warp >= 4 && warp < 8) {
-    // ---- Loading warps: tile g's K is group 2 g of the ring, its V group 2 g + 1.
-    const int lt = t - kSoftmaxThreads;
-    AttnSegment s{};
-    bool more = walk.next(s);
-    int tile = s.t0;
-    int64_t word = more ? key_word(p, s.r, s.b, tile * kKeys + lt) : -1;
+    // ---- Loading warps: tile g's K is group 2 g of the ring, its V group 2 g + 1.  A warp has 32 of a tile's keys, a
+    // lane one key's place, handed round by shuffles; the words that place the keys are fetched two tiles ahead.
+    const int lw = warp - 4;
+    struct Ahead {
+      AttnSegment s;
+      int tile;
+      bool more;
+      int64_t word;
+    } cur, one, two;
+    auto place_word = [&](Ahead& a) {
+      a.word = a.more ? key_word(p, a.s.r, a.s.b, a.tile * kKeys + lw * 32 + lane) : -1;
+    };
+    auto advance = [&](Ahead& a) {
+      if (++a.tile >= a.s.t0 + a.s.cnt) {
+        a.more = walk.next(a.s);
+        a.tile = a.s.t0;
+      }
+    };
+    cur.s = AttnSegment{};
+    cur.more = walk.next(cur.s);
+    cur.tile = cur.s.t0;
+    place_word(cur);
+    one = cur;
+    if (one.more) advance(one);
+    place_word(one);
     uint32_t q = 0;  // groups issued
     bool ok = true;
     auto landed = [&](uint32_t group) {  // this thread's copies of the group are in place
       fence_async();
       mbar_arrive(bar_full(group % NB));
     };
-    while (more && ok) {
-      const AttnSegment cur = s;
-      const int x = tile * kKeys + lt;
-      const int64_t off = key_offset(p, cur.r, x, word);
-      const bool outside = x < cur.r.len + cur.r.n && off < 0;
-      // the next tile's word is on its way while this tile is copied
-      if (++tile >= s.t0 + s.cnt) {
-        more = walk.next(s);
-        tile = s.t0;
-      }
-      if (more) word = key_word(p, s.r, s.b, tile * kKeys + lt);
-      const uint32_t g = q >> 1;
-      if (q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) break;
-      s_off[(g & 1) * kKeys + lt] = off;
+    const int c = lane % W::kPieces, sub = lane / W::kPieces;
+    constexpr int kStep = 32 / W::kPieces;  // rows a warp copies at once
+    const bool in_head = c * 8 < p.c.head_dim;
+    while (cur.more && ok) {
+      two = one;
+      if (two.more) advance(two);
+      place_word(two);
+      const int x = cur.tile * kKeys + lw * 32 + lane;
+      const int64_t off = key_offset(p, cur.s.r, x, cur.word);
       const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
-      const uint32_t bad = __ballot_sync(0xffffffffu, outside);
-      if (lane == 0) {
-        s_valid[(g % W::kInfo) * 8 + (warp - 4)] = valid;
-        s_valid[(g % W::kInfo) * 8 + 4 + (warp - 4)] = bad;
-      }
-      mbar_arrive(bar_load);
-      if (!wait(bar_load, g & 1)) break;
+      const uint32_t bad = __ballot_sync(0xffffffffu, x < cur.s.r.len + cur.s.r.n && off < 0);
+      const uint32_t g = q >> 1;
       for (int which = 0; which < 2; ++which, ++q) {
-        if (which == 1 && q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) {
+        if (q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) {
           ok = false;
           break;
         }
-        const char* src = which ? p.c.v : p.c.k;
+        if (which == 0 && lane == 0) {
+          s_valid[(g % W::kInfo) * 8 + lw] = valid;
+          s_valid[(g % W::kInfo) * 8 + 4 + lw] = bad;
+        }
+        const char* src = (which ? p.c.v : p.c.k) + (static_cast<int64_t>(cur.s.hkv) * p.c.head_stride + c * 8) * 2;
         const uint32_t dst = base + W::kTiles + (q % NB) * W::kTile;
-        const int c = lt % W::kPieces;
-        const bool in_head = c * 8 < p.c.head_dim;
-        const int64_t shift = static_cast<int64_t>(cur.hkv) * p.c.head_stride + c * 8;
 #pragma unroll 8
-        for (int r = lt / W::kPieces; r < kKeys; r += kLoadThreads / W::kPieces) {
-          const int64_t o = s_off[(g & 1) * kKeys + r];
+        for (int i = 0; i < 32; i += kStep) {
+          const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
           const bool live = o >= 0 && in_head;
-          cp_async16(dst + W::piece(r, c), src + (live ? (o + shift) * 2 : 0), live);
+          cp_async16(dst + W::piece(lw * 32 + i + sub, c), live ? src + o * 2 : p.c.k, live);
         }
         cp_async_commit();
         if (q + 1 >= W::kFlight) {
@@ -253,17 +265,40 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           landed(q + 1 - W::kFlight);
         }
       }
+      cur = one;
+      one = two;
     }
     cp_async_wait<0>();
     if (ok)
       for (uint32_t i = q >= W::kFlight - 1 ? q - (W::kFlight - 1) : 0; i < q; ++i) landed(i);
+  } else if (warp == 9) {
+    // ---- Q of the next unit, as soon as this unit's last scores are done.  Rows that do not exist are 0.
+    AttnSegment s;
+    for (uint32_t units = 0; walk.next(s); ++units) {
+      if (units > 0 && !wait(bar_qfree, (units - 1) & 1)) break;
+      const int rows = s.r.n * p.group - s.rt * kRows;
+      const int warps = min(kRows, (rows + 31) & ~31);  // rows of the warps that have any
+      const int c = lane % W::kPieces;
+      for (int row = lane / W::kPieces; row < warps; row += 32 / W::kPieces) {
+        const int grow = s.rt * kRows + row;
+        const bool live = row < rows && c * 8 < p.c.head_dim;
+        const int i = grow / p.group;
+        const int64_t at = (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head + c * 8;
+        cp_async16(base + W::kQ + W::piece(row, c), p.q + (live ? at * 2 : 0), live);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_async();
+      mbar_arrive(bar_q);
+    }
+    cp_async_wait<0>();
   } else if (warp == 8) {
     // ---- The issuing thread.
     if (lane == 0) {
       AttnSegment s;
       uint32_t g = 0, units = 0;
       bool ok = true;
-      auto scores = [&](uint32_t n) {
+      auto scores = [&](uint32_t n, bool last) {
         const uint32_t group = 2 * n;
         if (!wait_one(bar_full(group % NB), (group / NB) & 1)) return false;
         tc_fence_after();
@@ -277,15 +312,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
         }
         tc_commit(bar_empty(group % NB));
         tc_commit(bar_s(n & 1));
+        if (last) tc_commit(bar_qfree);
         return true;
       };
       while (ok && walk.next(s)) {
         if (!wait_one(bar_q, units & 1)) break;
         tc_fence_after();
-        ok = scores(g);
+        ok = scores(g, s.cnt == 1);
         for (int i = 0; ok && i < s.cnt; ++i) {
           const uint32_t n = g + i, group = 2 * n + 1;
-          if (i + 1 < s.cnt && !scores(n + 1)) {
+          if (i + 1 < s.cnt && !scores(n + 1, i + 2 == s.cnt)) {
             ok = false;
             break;
           }
@@ -315,27 +351,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       wait(bar_soft, meets++ & 1);
     };
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    // scale < 0 is carried by Q's signs; a scale of 0 by one that is too small to tell (0 times a masked -inf is NaN)
-    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-    const float c = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    const float c = fmaxf(p.scale_log2, 1e-30f);  // a scale of 0 by one too small to tell: 0 times a masked -inf is NaN
     AttnSegment s;
     uint32_t g = 0;
     bool ok = true;
     while (ok && walk.next(s)) {
       const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
       const bool idle = warp * 32 >= rows;              // none of the warp's rows exists
-      for (int x = t; x < kRows * W::kPieces; x += kSoftmaxThreads) {
-        const int row = x / W::kPieces, col = x % W::kPieces, grow = s.rt * kRows + row;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows && col * 8 < p.c.head_dim) {
-          const int64_t at = (s.r.row0 + grow / p.group) * p.q_row + (s.hkv * p.group + grow % p.group) * p.q_head + col * 8;
-          u = *reinterpret_cast<const uint4*>(p.q + at * 2);
-          u.x ^= flip, u.y ^= flip, u.z ^= flip, u.w ^= flip;
-        }
-        *reinterpret_cast<uint4*>(smem + W::kQ + W::piece(row, col)) = u;
-      }
-      fence_async();
-      mbar_arrive(bar_q);
       const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread
       float m = -kInfF, l = 0.0f;
       uint32_t bad = 0u;
@@ -348,12 +370,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           break;
         }
         tc_fence_after();
-        uint32_t vw[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          vw[w] = s_valid[(g % W::kInfo) * 8 + w];
-          bad |= s_valid[(g % W::kInfo) * 8 + 4 + w];
-        }
+        const uint4 vv = *reinterpret_cast<const uint4*>(s_valid + (g % W::kInfo) * 8);
+        const uint4 vb = *reinterpret_cast<const uint4*>(s_valid + (g % W::kInfo) * 8 + 4);
+        uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
+        bad |= vb.x | vb.y | vb.z | vb.w;
         const bool masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xffffffffu || x0 + kKeys > s.r.len;
         if (masked && s.r.n > 1 && x0 + kKeys > s.r.len) {
           // A weight of 0 does not silence a V that is NaN or infinite: such values of new rows are taken out of the
@@ -482,7 +502,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       }
       bad = (bad ? kStSlotRange : 0u) | s.r.status;
       const bool whole = s.cnt == s.nt;
-      float* part = whole ? nullptr : attn_part<kRows, DP>(p, blockIdx.x, s.at_start);
+      using P = AttnPart<kRows, DP>;
+      float* part = whole ? nullptr : attn_part<kRows, DP>(p, blockIdx.x, s.t0 == 0);
+      const int head = s.hkv * p.group + (s.rt * kRows + t) % p.group;
+      char* out = p.out + ((s.r.row0 + my_row) * p.o_row + head * p.o_head) * 2;
+      const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
+      const float inv = none ? 0.0f : 1.0f / l;
       if (!idle) {
 #pragma unroll
         for (int h = 0; h < DP / 32; ++h) {
@@ -505,27 +530,34 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
                   }
               }
             }
+            if (whole) {
 #pragma unroll
-            for (int d = 0; d < 32; d += 4) {
-              const float4 v = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
-              if (whole)
-                write_row<true>(p, s.r, s.hkv, s.rt * kRows + t, h * 32 + d, v, m, l);
-              else
-                *reinterpret_cast<float4*>(part + t * DP + h * 32 + d) = v;
+              for (int d = 0; d < 32; d += 8)
+                if (h * 32 + d < p.c.head_dim) {
+                  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                  if (!none)
+                    u = make_uint4(pack_bf16(o[d] * inv, o[d + 1] * inv), pack_bf16(o[d + 2] * inv, o[d + 3] * inv),
+                                   pack_bf16(o[d + 4] * inv, o[d + 5] * inv), pack_bf16(o[d + 6] * inv, o[d + 7] * inv));
+                  *reinterpret_cast<uint4*>(out + (h * 32 + d) * 2) = u;
+                }
+            } else {
+#pragma unroll
+              for (int d = 0; d < 32; d += 4)
+                reinterpret_cast<float4*>(part)[(h * 8 + d / 4) * kRows + t] =
+                    make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
             }
           }
         }
       }
       if (whole) {
+        if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
         if (s.reports && t == 0) p.status[s.b] = bad;
       } else {
-        // shared arrays of the join: this unit's Q is no longer read
-        float* s_m = reinterpret_cast<float*>(smem + W::kQ);
-        part[kRows * DP + t] = m;
-        part[kRows * DP + kRows + t] = l;
-        if (t == 0) part[kRows * (DP + 2)] = __uint_as_float(bad);
+        float* s_m = reinterpret_cast<float*>(smem + W::kJoin);
+        part[P::kM + t] = m;
+        part[P::kL + t] = l;
+        if (t == 0) part[P::kStatus] = __uint_as_float(bad);
         attn_join<true, kRows, DP, kSoftmaxThreads>(p, span, s, t, s_m, s_m + kRows, s_last, meet);
-        meet();
       }
       tc_fence_before();
     }
