@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
       }
       for (int row = t; row < MT; row += T) part[P::kM + row] = s_m[row], part[P::kL + row] = s_l[row];
       if (t == 0) part[P::kStatus] = __uint_as_float(bad);
-      attn_join<E::kBf16, MT, DP, T>(p, span, s, t, s_m, s_l, &s_last, sync);
+      attn_join<E::kBf16, MT, DP, T>(p, span, s, t, &s_last, sync);
     }
     __syncthreads();  // the ring and the offsets are free again
   }

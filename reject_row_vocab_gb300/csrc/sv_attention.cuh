@@ -81,6 +81,18 @@ __device__ __forceinline__ int64_t key_word(const AttnParams& p, const AttnReque
   if (page >= static_cast<uint32_t>(p.c.max_pages)) return -1;
   return p.c.table[b * p.c.ld_table + page];
 }
+__device__ __forceinline__ void key_prefetch(const AttnParams& p, const AttnRequest& r, int b, int x) {
+  if (x < 0 || x >= r.len + r.n) return;
+  const void* at;
+  if (x >= r.len && p.row_slots) {
+    at = p.row_slots + r.row0 + (x - r.len);
+  } else {
+    const uint32_t page = static_cast<uint32_t>(x) / static_cast<uint32_t>(p.c.page_size);
+    if (page >= static_cast<uint32_t>(p.c.max_pages)) return;
+    at = p.c.table + b * p.c.ld_table + page;
+  }
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+}
 __device__ __forceinline__ int64_t key_offset(const AttnParams& p, const AttnRequest& r, int x, int64_t word) {
   if (x < 0 || x >= r.len + r.n) return -1;
   if (x >= r.len && p.row_slots) return kv_slot_offset(p.c, word);
@@ -274,13 +286,15 @@ __device__ __forceinline__ float* attn_part(const AttnParams& p, int block, bool
 }
 
 // After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
-// writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_m, s_l [MT] and s_last
-// are shared.  Eight quads a thread are joined at a time, so that the loads of a part do not wait for one another.
+// writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_last is shared.  At the end
+// of a call every trip to L2 counts, so a part's m, l and O are fetched together (eight quads of columns a thread, two
+// parts at a time) and the running maximum moves as they come.
 template <bool BF16, int MT, int DP, int T, class Sync>
 __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
-                                          float* s_m, float* s_l, int* s_last, Sync sync) {
+                                          int* s_last, Sync sync) {
   using P = AttnPart<MT, DP>;
-  constexpr int E = 8;
+  constexpr int E = 8, ES = BF16 ? 2 : 4;
+  __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
   sync();
   // the unit's blocks are those that own its first and its last tile
   const int c0 = static_cast<int>(((s.u0 + 1) * sp.g - 1) / sp.total);
@@ -296,56 +310,47 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
   const float* rest = attn_part<MT, DP>(p, 0, false);
   auto part_of = [&](int c) { return c == c0 ? first : rest + static_cast<int64_t>(c) * 2 * P::kFloats; };
   const int live = min(MT, s.r.n * p.group - s.rt * MT);
-  for (int row = t; row < live; row += T) {
-    float M = -kInfF, L = 0.0f;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) M = fmax_nan(M, __ldcg(part_of(c) + P::kM + row));
-    if (M != -kInfF) {
-#pragma unroll 8
-      for (int c = c0; c <= c1; ++c)
-        L = fmaf(ex2_fast(__ldcg(part_of(c) + P::kM + row) - M), __ldcg(part_of(c) + P::kL + row), L);
-    }
-    s_m[row] = M;
-    s_l[row] = L;
-  }
+  int wide = 1;  // threads side by side on the rows: a power of two
+  while (wide < live) wide *= 2;
+  const int row = t & (wide - 1), step = T / wide;
+  const int grow = s.rt * MT + row, i = grow / p.group;
+  const int head = s.hkv * p.group + grow - i * p.group;
+  char* out = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head) * ES;
   uint32_t any = 0u;
-  if (t == 0 && s.reports)
-    for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(part_of(c) + P::kStatus));
-  sync();
-  const int quads = live * (DP / 4);
-  for (int x0 = t; x0 < quads; x0 += T * E) {
+  for (int q0 = t / wide; q0 < DP / 4 && row < live; q0 += step * E) {
     float4 a[E];
-    int at[E], row[E];
-    float M[E];
+    float M = -kInfF, L = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int x = x0 + e * T < quads ? x0 + e * T : x0;
-      row[e] = x % live;
-      at[e] = (x / live) * MT + row[e];
-      M[e] = s_m[row[e]] == -kInfF ? 0.0f : s_m[row[e]];
-      a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    for (int e = 0; e < E; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
       const float* q = part_of(c);
-      float w[E];
+      const float m = __ldcg(q + P::kM + row), l = __ldcg(q + P::kL + row);
       float4 v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        w[e] = __ldcg(q + P::kM + row[e]);
-        v[e] = __ldcg(reinterpret_cast<const float4*>(q) + at[e]);
-      }
+      for (int e = 0; e < E; ++e)
+        if (q0 + e * step < DP / 4) v[e] = __ldcg(reinterpret_cast<const float4*>(q) + (q0 + e * step) * MT + row);
+      if (t == 0 && q0 == 0) any |= __float_as_uint(__ldcg(q + P::kStatus));
+      if (m == -kInfF) continue;  // nothing seen in this part
+      const float N = fmax_nan(M, m), wa = ex2_fast(M - N), wb = ex2_fast(m - N);
+      M = N;
+      L = fmaf(L, wa, l * wb);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float f = ex2_fast(w[e] - M[e]);
-        a[e].x = fmaf(f, v[e].x, a[e].x), a[e].y = fmaf(f, v[e].y, a[e].y);
-        a[e].z = fmaf(f, v[e].z, a[e].z), a[e].w = fmaf(f, v[e].w, a[e].w);
+        a[e].x = fmaf(a[e].x, wa, v[e].x * wb), a[e].y = fmaf(a[e].y, wa, v[e].y * wb);
+        a[e].z = fmaf(a[e].z, wa, v[e].z * wb), a[e].w = fmaf(a[e].w, wa, v[e].w * wb);
       }
     }
+    const bool none = M == -kInfF;
+    const float inv = none ? 0.0f : 1.0f / L;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (x0 + e * T < quads)
-        write_row<BF16>(p, s.r, s.hkv, s.rt * MT + row[e], at[e] / MT * 4, a[e], s_m[row[e]], s_l[row[e]]);
+    for (int e = 0; e < E; ++e) {
+      const int d = (q0 + e * step) * 4;
+      if (d < p.c.head_dim)
+        store4<BF16>(out + d * ES, none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                        : make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv));
+    }
+    if (q0 == 0 && p.lse) p.lse[(s.r.row0 + i) * p.heads + head] = none ? -kInfF : fmaf(M, kLn2, logf(L));
   }
   if (s.reports && t == 0) p.status[s.b] = any;
 }

@@ -132,9 +132,8 @@ struct Wide {
   static constexpr int kQ = 0;
   static constexpr int kTiles = kTile;
   static constexpr int kValid = kTiles + kRing * kTile;     // uint32 [kInfo][8]: four valid words, four bad
-  static constexpr int kJoin = kValid + kInfo * 8 * 4;      // m, l [kRows] of a join
-  static constexpr int kBars = kJoin + 2 * kRows * 4;       // full, empty [kRing], s [2], p [2], pv, q, q free, soft
-  static constexpr int kMisc = kBars + (2 * kRing + 8) * 8; // sums [10], find [2]; tmem, abort, last, careful
+  static constexpr int kBars = kValid + kInfo * 8 * 4;       // full, empty [kRing], s, p, q, q free, pv [2], soft
+  static constexpr int kMisc = kBars + (2 * kRing + 12) * 8; // sums [10], find [2]; tmem, abort, last, careful
   static constexpr int kSmem = kMisc + 12 * 8 + 4 * 4;
   // 16-byte piece c of row r of a tile
   __device__ static uint32_t piece(int r, int c) {
@@ -160,15 +159,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   auto bar_empty = [&](int i) { return base + W::kBars + (NB + i) * 8; };
   auto bar_s = [&](int i) { return base + W::kBars + (2 * NB + i) * 8; };
   auto bar_p = [&](int i) { return base + W::kBars + (2 * NB + 2 + i) * 8; };
-  const uint32_t bar_pv = base + W::kBars + (2 * NB + 4) * 8, bar_q = bar_pv + 8;
-  const uint32_t bar_qfree = bar_pv + 16, bar_soft = bar_pv + 24;  // Q may be replaced; the softmax warps meet
+  auto bar_q = [&](int i) { return base + W::kBars + (2 * NB + 4 + i) * 8; };
+  auto bar_qfree = [&](int i) { return base + W::kBars + (2 * NB + 6 + i) * 8; };
+  // Two, in turn: a wait by parity is only good where the barrier's phase before is known to be over, and that S(g) has
+  // come means that O has the products of tile g - 2, not those of g - 1.
+  auto bar_pv = [&](uint32_t g) { return base + W::kBars + (2 * NB + 8 + (g & 1)) * 8; };
+  const uint32_t bar_soft = base + W::kBars + (2 * NB + 10) * 8;
+  // Units of up to 64 rows have two Qs, one in each half of Q's rows: the products of the lower half read on into what
+  // lies behind it, but rows past 64 are nobody's then.
+  const int twin = p.max_len * static_cast<int64_t>(p.group) <= 64 ? 1 : 0;
+  auto q_slot = [&](uint32_t unit) { return twin ? static_cast<int>(unit & 1) : 0; };
+  auto q_phase = [&](uint32_t unit) { return twin ? unit >> 1 : unit; };
 
   if (t == 0) {
     for (int i = 0; i < NB; ++i) mbar_init(bar_full(i), kLoadThreads), mbar_init(bar_empty(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(bar_s(i), 2), mbar_init(bar_p(i), kSoftmaxThreads);
-    mbar_init(bar_pv, 1);
-    mbar_init(bar_q, 32);
-    mbar_init(bar_qfree, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar_pv(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar_q(i), 32), mbar_init(bar_qfree(i), 1);
     mbar_init(bar_soft, kSoftmaxThreads);
     mbar_fence_init();
     *s_abort = 0;
@@ -200,30 +207,35 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
 
   if (warp >= 4 && warp < 8) {
     // ---- Loading warps: tile g's K is group 2 g of the ring, its V group 2 g + 1.  A warp has 32 of a tile's keys, a
-    // lane one key's place, handed round by shuffles; the words that place the keys are fetched two tiles ahead.
+    // lane one key's place, handed round by shuffles; the words that place the keys are called into L1 two tiles ahead
+    // (a register that waits for them would stop the warp at its first copy).
     const int lw = warp - 4;
-    struct Ahead {
+    struct Tile {
       AttnSegment s;
       int tile;
       bool more;
-      int64_t word;
-    } cur, one, two;
-    auto place_word = [&](Ahead& a) {
-      a.word = a.more ? key_word(p, a.s.r, a.s.b, a.tile * kKeys + lw * 32 + lane) : -1;
-    };
-    auto advance = [&](Ahead& a) {
+    } cur, ahead;
+    auto advance = [&](Tile& a) {
       if (++a.tile >= a.s.t0 + a.s.cnt) {
         a.more = walk.next(a.s);
         a.tile = a.s.t0;
       }
     };
+    auto call = [&](const Tile& a) {
+      if (a.more) key_prefetch(p, a.s.r, a.s.b, a.tile * kKeys + lw * 32 + lane);
+    };
+    AttnWalk<kRows, kKeys, kUnitPlaces> mine = walk;  // cur's own walk; `walk` is ahead's
     cur.s = AttnSegment{};
-    cur.more = walk.next(cur.s);
+    cur.more = mine.next(cur.s);
     cur.tile = cur.s.t0;
-    place_word(cur);
-    one = cur;
-    if (one.more) advance(one);
-    place_word(one);
+    ahead.s = AttnSegment{};
+    ahead.more = walk.next(ahead.s);
+    ahead.tile = ahead.s.t0;
+    call(ahead);
+    for (int i = 0; i < 2 && ahead.more; ++i) {
+      advance(ahead);
+      call(ahead);
+    }
     uint32_t q = 0;  // groups issued
     bool ok = true;
     auto landed = [&](uint32_t group) {  // this thread's copies of the group are in place
@@ -234,11 +246,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
     constexpr int kStep = 32 / W::kPieces;  // rows a warp copies at once
     const bool in_head = c * 8 < p.c.head_dim;
     while (cur.more && ok) {
-      two = one;
-      if (two.more) advance(two);
-      place_word(two);
       const int x = cur.tile * kKeys + lw * 32 + lane;
-      const int64_t off = key_offset(p, cur.s.r, x, cur.word);
+      const int64_t off = key_offset(p, cur.s.r, x, key_word(p, cur.s.r, cur.s.b, x));
+      if (ahead.more) advance(ahead);
+      call(ahead);
       const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
       const uint32_t bad = __ballot_sync(0xffffffffu, x < cur.s.r.len + cur.s.r.n && off < 0);
       const uint32_t g = q >> 1;
@@ -265,8 +276,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           landed(q + 1 - W::kFlight);
         }
       }
-      cur = one;
-      one = two;
+      if (++cur.tile >= cur.s.t0 + cur.s.cnt) {
+        cur.more = mine.next(cur.s);
+        cur.tile = cur.s.t0;
+      }
     }
     cp_async_wait<0>();
     if (ok)
@@ -275,7 +288,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
     // ---- Q of the next unit, as soon as this unit's last scores are done.  Rows that do not exist are 0.
     AttnSegment s;
     for (uint32_t units = 0; walk.next(s); ++units) {
-      if (units > 0 && !wait(bar_qfree, (units - 1) & 1)) break;
+      const int slot = q_slot(units);
+      if (q_phase(units) > 0 && !wait(bar_qfree(slot), (q_phase(units) - 1) & 1)) break;
       const int rows = s.r.n * p.group - s.rt * kRows;
       const int warps = min(kRows, (rows + 31) & ~31);  // rows of the warps that have any
       const int c = lane % W::kPieces;
@@ -284,12 +298,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
         const bool live = row < rows && c * 8 < p.c.head_dim;
         const int i = grow / p.group;
         const int64_t at = (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head + c * 8;
-        cp_async16(base + W::kQ + W::piece(row, c), p.q + (live ? at * 2 : 0), live);
+        cp_async16(base + W::kQ + W::piece(slot * 64 + row, c), p.q + (live ? at * 2 : 0), live);
       }
       cp_async_commit();
       cp_async_wait<0>();
       fence_async();
-      mbar_arrive(bar_q);
+      mbar_arrive(bar_q(slot));
     }
     cp_async_wait<0>();
   } else if (warp == 8) {
@@ -299,6 +313,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       uint32_t g = 0, units = 0;
       bool ok = true;
       auto scores = [&](uint32_t n, bool last) {
+        const int slot = q_slot(units);
         const uint32_t group = 2 * n;
         if (!wait_one(bar_full(group % NB), (group / NB) & 1)) return false;
         tc_fence_after();
@@ -307,16 +322,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
           const uint32_t at = (i >> 2) * W::kBlock + (i & 3) * 32;
-          mma_ss(tmem + W::kS + (n & 1) * 128, operand(base + W::kQ + at, 16), operand(k + at, 16),
+          mma_ss(tmem + W::kS + (n & 1) * 128, operand(base + W::kQ + slot * 64 * 128 + at, 16), operand(k + at, 16),
                  instruction(kKeys, false), i > 0);
         }
         tc_commit(bar_empty(group % NB));
         tc_commit(bar_s(n & 1));
-        if (last) tc_commit(bar_qfree);
+        if (last) tc_commit(bar_qfree(slot));
         return true;
       };
       while (ok && walk.next(s)) {
-        if (!wait_one(bar_q, units & 1)) break;
+        if (!wait_one(bar_q(q_slot(units)), q_phase(units) & 1)) break;
         tc_fence_after();
         ok = scores(g, s.cnt == 1);
         for (int i = 0; ok && i < s.cnt; ++i) {
@@ -336,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
             mma_ts(tmem + W::kO, tmem + W::kS + (n & 1) * 128 + j * 8, operand(v + j * 2048, W::kBlock),
                    instruction(DP, true), i > 0 || j > 0);
           tc_commit(bar_empty(group % NB));
-          tc_commit(bar_pv);
+          tc_commit(bar_pv(n));
         }
         g += s.cnt;
         ++units;
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
             const float a = grow ? ex2_fast(m - top) : 1.0f;
             if (grow) m = top;
             l *= a;
-            if (!wait(bar_pv, (g - 1) & 1)) {
+            if (!wait(bar_pv(g - 1), ((g - 1) >> 1) & 1)) {
               ok = false;
               break;
             }
@@ -491,7 +506,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       }
       if (!ok) break;
       // The unit's last product is done: this thread's row of O.
-      if (!wait(bar_pv, (g - 1) & 1)) break;
+      if (!wait(bar_pv(g - 1), ((g - 1) >> 1) & 1)) break;
       tc_fence_after();
       bool careful = false;
       if (mixed) {
@@ -553,11 +568,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
         if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
         if (s.reports && t == 0) p.status[s.b] = bad;
       } else {
-        float* s_m = reinterpret_cast<float*>(smem + W::kJoin);
         part[P::kM + t] = m;
         part[P::kL + t] = l;
         if (t == 0) part[P::kStatus] = __uint_as_float(bad);
-        attn_join<true, kRows, DP, kSoftmaxThreads>(p, span, s, t, s_m, s_m + kRows, s_last, meet);
+        attn_join<true, kRows, DP, kSoftmaxThreads>(p, span, s, t, s_last, meet);
       }
       tc_fence_before();
     }

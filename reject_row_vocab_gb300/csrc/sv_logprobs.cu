@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(LogprobParams p) 
       p.part[at] = r;
       p.part_flags[at] = s_flags;
     }
+    __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
     __syncthreads();
     if (t == 0) s_last = ticket_add(&p.tickets[i], 1u) == static_cast<unsigned>(p.splits - 1) ? 1u : 0u;
     __syncthreads();

@@ -172,6 +172,17 @@ def test_repeats_are_bit_equal_and_the_workspace_rewinds():
     assert torch.equal(first.out, c.run(sv, ws=ws).out)
 
 
+@pytest.mark.parametrize("rows,dim", [(17, 64), (33, 128), (64, 64), (64, 128)])
+def test_many_rows_repeat_bit_equal_with_short_segments(rows, dim):
+    # about two key tiles a block: the end of a unit follows its beginning at once
+    c = AttentionCase([20011], rows, 4, 1, dim, 32, BF16, seed=9)
+    first = c.run(sv)
+    check_attention(c, first)
+    for _ in range(12):
+        again = c.run(sv)
+        assert torch.equal(first.out, again.out) and torch.equal(first.lse, again.lse)
+
+
 def test_side_stream():
     c = AttentionCase([900, 70], 2, 8, 2, 128, 16, BF16, seed=21)
     ref = c.run(sv)
