@@ -77,27 +77,16 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnParams& p, int b) 
 __device__ __forceinline__ int64_t key_word(const AttnParams& p, const AttnRequest& r, int b, int x) {
   if (x < 0 || x >= r.len + r.n) return -1;
   if (x >= r.len && p.row_slots) return p.row_slots[r.row0 + (x - r.len)];
-  const uint32_t page = static_cast<uint32_t>(x) / static_cast<uint32_t>(p.c.page_size);
+  const uint32_t page = divide(static_cast<uint32_t>(x), p.c.div_mul, p.c.div_shift);
   if (page >= static_cast<uint32_t>(p.c.max_pages)) return -1;
   return p.c.table[b * p.c.ld_table + page];
-}
-__device__ __forceinline__ void key_prefetch(const AttnParams& p, const AttnRequest& r, int b, int x) {
-  if (x < 0 || x >= r.len + r.n) return;
-  const void* at;
-  if (x >= r.len && p.row_slots) {
-    at = p.row_slots + r.row0 + (x - r.len);
-  } else {
-    const uint32_t page = static_cast<uint32_t>(x) / static_cast<uint32_t>(p.c.page_size);
-    if (page >= static_cast<uint32_t>(p.c.max_pages)) return;
-    at = p.c.table + b * p.c.ld_table + page;
-  }
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
 }
 __device__ __forceinline__ int64_t key_offset(const AttnParams& p, const AttnRequest& r, int x, int64_t word) {
   if (x < 0 || x >= r.len + r.n) return -1;
   if (x >= r.len && p.row_slots) return kv_slot_offset(p.c, word);
   if (word < 0 || word > INT32_MAX) return -1;
-  return kv_page_offset(p.c, static_cast<int32_t>(word), static_cast<uint32_t>(x) % static_cast<uint32_t>(p.c.page_size));
+  const uint32_t page = divide(static_cast<uint32_t>(x), p.c.div_mul, p.c.div_shift);
+  return kv_page_offset(p.c, static_cast<int32_t>(word), static_cast<uint32_t>(x) - page * p.c.page_size);
 }
 
 // 16-byte asynchronous copy global -> shared; zero-fills when !valid (the source is then not read).
@@ -254,7 +243,9 @@ struct AttnWalk {
       s.b = sp.b;
       s.nt = (s.r.len + s.r.n + KT - 1) / KT;
       const int row_tiles = (s.r.n * p.group + MT - 1) / MT;
-      const int unit = static_cast<int>((pos - sp.first) / (s.nt + U));
+      const int64_t in = pos - sp.first;
+      const int unit = in <= INT32_MAX ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(s.nt + U))
+                                       : static_cast<int>(in / (s.nt + U));
       s.u0 = sp.first + static_cast<int64_t>(unit) * (s.nt + U) + U;
       s.t0 = static_cast<int>(max(pos - s.u0, static_cast<int64_t>(0)));
       s.cnt = static_cast<int>(min(static_cast<int64_t>(s.nt), sp.end - s.u0)) - s.t0;

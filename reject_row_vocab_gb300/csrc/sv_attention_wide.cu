@@ -115,6 +115,19 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // NaN and infini
   return w;
 }
 
+// As mbar_try_wait, the thread suspended for up to about `ns`.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------------------------------------------------------------
 // Layout
 // ---------------------------------------------------------------------------------------------------------------------
@@ -197,8 +210,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
 
   // A wait that gives up ends every role; the lanes of a warp leave together.
   auto wait_one = [&](uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < 64; ++i)  // the clock is read only by waits that are long
-      if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i)  // suspended meanwhile: warps that poll take issue slots from those that work
+      if (mbar_try_wait_for(bar, parity, 10000)) return true;
     if (mbar_wait_bounded(bar, parity, s_abort, kWaitNs)) return true;
     *s_abort = 1;
     return false;
@@ -207,35 +220,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
 
   if (warp >= 4 && warp < 8) {
     // ---- Loading warps: tile g's K is group 2 g of the ring, its V group 2 g + 1.  A warp has 32 of a tile's keys, a
-    // lane one key's place, handed round by shuffles; the words that place the keys are called into L1 two tiles ahead
-    // (a register that waits for them would stop the warp at its first copy).
+    // lane one key's place, handed round by shuffles; the word that places a lane's key of the next tile is on its way
+    // while this tile is copied.
     const int lw = warp - 4;
-    struct Tile {
-      AttnSegment s;
-      int tile;
-      bool more;
-    } cur, ahead;
-    auto advance = [&](Tile& a) {
-      if (++a.tile >= a.s.t0 + a.s.cnt) {
-        a.more = walk.next(a.s);
-        a.tile = a.s.t0;
-      }
-    };
-    auto call = [&](const Tile& a) {
-      if (a.more) key_prefetch(p, a.s.r, a.s.b, a.tile * kKeys + lw * 32 + lane);
-    };
-    AttnWalk<kRows, kKeys, kUnitPlaces> mine = walk;  // cur's own walk; `walk` is ahead's
-    cur.s = AttnSegment{};
-    cur.more = mine.next(cur.s);
-    cur.tile = cur.s.t0;
-    ahead.s = AttnSegment{};
-    ahead.more = walk.next(ahead.s);
-    ahead.tile = ahead.s.t0;
-    call(ahead);
-    for (int i = 0; i < 2 && ahead.more; ++i) {
-      advance(ahead);
-      call(ahead);
-    }
+    AttnSegment s{};
+    bool more = walk.next(s);
+    int tile = s.t0;
+    int64_t word = more ? key_word(p, s.r, s.b, tile * kKeys + lw * 32 + lane) : -1;
     uint32_t q = 0;  // groups issued
     bool ok = true;
     auto landed = [&](uint32_t group) {  // this thread's copies of the group are in place
@@ -245,13 +236,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
     const int c = lane % W::kPieces, sub = lane / W::kPieces;
     constexpr int kStep = 32 / W::kPieces;  // rows a warp copies at once
     const bool in_head = c * 8 < p.c.head_dim;
-    while (cur.more && ok) {
-      const int x = cur.tile * kKeys + lw * 32 + lane;
-      const int64_t off = key_offset(p, cur.s.r, x, key_word(p, cur.s.r, cur.s.b, x));
-      if (ahead.more) advance(ahead);
-      call(ahead);
+    while (more && ok) {
+      const int x = tile * kKeys + lw * 32 + lane;
+      const int64_t off = key_offset(p, s.r, x, word);
       const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
-      const uint32_t bad = __ballot_sync(0xffffffffu, x < cur.s.r.len + cur.s.r.n && off < 0);
+      const uint32_t bad = __ballot_sync(0xffffffffu, x < s.r.len + s.r.n && off < 0);
+      const int64_t shift = (static_cast<int64_t>(s.hkv) * p.c.head_stride + c * 8) * 2;
+      if (++tile >= s.t0 + s.cnt) {
+        more = walk.next(s);
+        tile = s.t0;
+      }
+      if (more) word = key_word(p, s.r, s.b, tile * kKeys + lw * 32 + lane);
       const uint32_t g = q >> 1;
       for (int which = 0; which < 2; ++which, ++q) {
         if (q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) {
@@ -262,7 +257,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           s_valid[(g % W::kInfo) * 8 + lw] = valid;
           s_valid[(g % W::kInfo) * 8 + 4 + lw] = bad;
         }
-        const char* src = (which ? p.c.v : p.c.k) + (static_cast<int64_t>(cur.s.hkv) * p.c.head_stride + c * 8) * 2;
+        const char* src = (which ? p.c.v : p.c.k) + shift;
         const uint32_t dst = base + W::kTiles + (q % NB) * W::kTile;
 #pragma unroll 8
         for (int i = 0; i < 32; i += kStep) {
@@ -275,10 +270,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           cp_async_wait<W::kFlight - 1>();
           landed(q + 1 - W::kFlight);
         }
-      }
-      if (++cur.tile >= cur.s.t0 + cur.s.cnt) {
-        cur.more = mine.next(cur.s);
-        cur.tile = cur.s.t0;
       }
     }
     cp_async_wait<0>();

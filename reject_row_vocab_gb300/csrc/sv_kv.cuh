@@ -19,7 +19,24 @@ struct KvView {
   const int32_t* table;
   int32_t max_pages;
   int64_t ld_table;
+  uint32_t div_mul, div_shift;  // x / page_size = umulhi(x, div_mul) >> div_shift for x < 2^31
 };
+
+// Multiplier and shift of an exact division of 31-bit numbers by d >= 2: with 2^l >= d, m = ceil(2^(31 + l) / d) exceeds
+// 2^(31 + l) / d by less than 1, so x m / 2^(31 + l) exceeds x / d by less than 2^-l <= 1 / d for x < 2^31, which cannot
+// reach the next whole number; m < 2^32 as 2^(l - 1) < d.
+struct Divider {
+  uint32_t mul, shift;
+};
+inline Divider divider(uint32_t d) {
+  if (d < 2) return Divider{0u, 0u};  // the quotient is x itself
+  uint32_t l = 1;
+  while ((1ull << l) < d) ++l;
+  return Divider{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t x, uint32_t mul, uint32_t shift) {
+  return mul ? __umulhi(x, mul) >> shift : x;
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -39,16 +56,18 @@ inline sv_status_t check_cache(const sv_kv_cache_t* c, KvView* v) {
   if (!aligned16(c->k) || !aligned16(c->v) || (c->head_dim * es) % 16 != 0 || (c->layer_stride * es) % 16 != 0 ||
       (c->page_stride * es) % 16 != 0 || (c->slot_stride * es) % 16 != 0 || (c->head_stride * es) % 16 != 0)
     return SV_ERR_MISALIGNED;
+  const Divider d = divider(static_cast<uint32_t>(c->page_size));
   *v = KvView{static_cast<char*>(c->k), static_cast<char*>(c->v), es,          c->layers,      c->pages,
               c->page_size,             c->heads,                 c->head_dim, c->layer_stride, c->page_stride,
-              c->slot_stride,           c->head_stride,           c->page_table, c->max_pages, c->ld_table};
+              c->slot_stride,           c->head_stride,           c->page_table, c->max_pages, c->ld_table,
+              d.mul,                    d.shift};
   return SV_OK;
 }
 
 // Element offset (within a layer and head 0) of a slot, or -1 outside the cache.
 __device__ __forceinline__ int64_t kv_slot_offset(const KvView& c, int64_t slot) {
   if (slot < 0 || slot >= static_cast<int64_t>(c.pages) * c.page_size) return -1;
-  const uint32_t s = static_cast<uint32_t>(slot), page = s / static_cast<uint32_t>(c.page_size);
+  const uint32_t s = static_cast<uint32_t>(slot), page = divide(s, c.div_mul, c.div_shift);
   return page * c.page_stride + static_cast<int64_t>(s - page * c.page_size) * c.slot_stride;
 }
 

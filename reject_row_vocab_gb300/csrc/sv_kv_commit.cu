@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_commit(KvView c, int32_t ma
     const int64_t src = kv_slot_offset(c, src_slot[lo + e]);
     int64_t dst = -1;
     if (pos >= 0 && pos < static_cast<int64_t>(c.max_pages) * c.page_size) {
-      const uint32_t p = static_cast<uint32_t>(pos) / static_cast<uint32_t>(c.page_size);
+      const uint32_t p = divide(static_cast<uint32_t>(pos), c.div_mul, c.div_shift);
       dst = kv_page_offset(c, c.table[b * c.ld_table + p], static_cast<uint32_t>(pos) - p * c.page_size);
     }
     const bool ok = src >= 0 && dst >= 0;
