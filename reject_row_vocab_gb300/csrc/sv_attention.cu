@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
   float* s_m = reinterpret_cast<float*>(s_valid + RING * 4);                  // [WK][MT]
   float* s_l = s_m + WK * MT;
   float* s_w = s_l + WK * MT;
-  __shared__ int64_t s_sum[T / 32];
+  __shared__ int64_t s_sum[2 * T / 32];
   __shared__ int64_t s_find[2];
   __shared__ int s_last;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -522,8 +522,11 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
     };
     if (s.cnt == s.nt) {
       for (int x = t; x < MT * QUADS; x += T) {
-        const int row = x / QUADS, d = (x % QUADS) * 4;
-        write_row<E::kBf16>(p, r, s.hkv, s.rt * MT + row, d, joined(row, d), s_m[row], s_l[row]);
+        const int row = x / QUADS, d = (x % QUADS) * 4, grow = s.rt * MT + row;
+        if (grow < r.n * p.group) {
+          const int i = grow / p.group;
+          write_row<E::kBf16>(p, r.row0 + i, s.hkv * p.group + grow - i * p.group, d, joined(row, d), s_m[row], s_l[row]);
+        }
       }
       if (s.reports && t == 0) p.status[s.b] = bad;
     } else {
@@ -596,7 +599,7 @@ cudaError_t launch_attention(const AttnParams& p, const DeviceInfo& dev, cudaStr
 // Floats of one part: the largest row tile any engine has for this head size.
 size_t part_bytes(int32_t head_dim) {
   const size_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  return (64 * (dp + 2) + 4) * sizeof(float);
+  return (64 * (dp + 2) + 16) * sizeof(float);
 }
 
 }  // namespace
@@ -644,7 +647,8 @@ sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int
                      q_row_stride, q_head_stride, static_cast<char*>(out), out_row_stride, out_head_stride, lse, c,
                      cu_seqlens, seq_lens, row_slots, mask, dev_status, batch, max_len, num_heads,
                      num_heads / c.heads, total_rows, scale * 1.44269504088896340736f,
-                     reinterpret_cast<uint32_t*>(base), reinterpret_cast<float*>(base + kAttnCounterBytes)};
+                     reinterpret_cast<uint32_t*>(base), reinterpret_cast<uint32_t*>(base) + kAttnMaxBlocks,
+                     reinterpret_cast<float*>(base + kAttnCounterBytes)};
   e = launch_attention(p, dev, stream);
   return e == cudaSuccess ? SV_OK : cuda_failure(e);
 }

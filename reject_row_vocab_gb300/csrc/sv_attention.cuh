@@ -20,7 +20,7 @@
 namespace sv {
 
 constexpr int kAttnMaxBlocks = 512;     // upper bound on the grid (the workspace is laid out for it)
-constexpr int kAttnCounterBytes = sizeof(uint32_t) * kAttnMaxBlocks;
+constexpr int kAttnCounterBytes = sizeof(uint32_t) * kAttnMaxBlocks + 256;  // tickets, then the error word
 
 struct AttnParams {
   const char* q;
@@ -38,8 +38,11 @@ struct AttnParams {
   int64_t total_rows;
   float scale_log2;  // scale * log2(e)
   uint32_t* tickets;  // [kAttnMaxBlocks], zero between calls
+  uint32_t* err;      // a wait gave up: reported by every call until the workspace is zero-filled
   float* parts;       // [grid, 2, part_floats]
 };
+
+__device__ __forceinline__ uint32_t attn_timeout(const AttnParams& p) { return __ldcg(p.err) ? kStTimeout : 0u; }
 
 struct AttnRequest {
   int64_t row0;
@@ -120,22 +123,17 @@ __device__ __forceinline__ void store4(char* p, float4 v) {
   }
 }
 
-// One query row's quad of columns, normalised, and its lse.
+// A query row's quad of columns, normalised, and (with the first quad) its lse.
 template <bool BF16>
-__device__ __forceinline__ void write_row(const AttnParams& p, const AttnRequest& r, int hkv, int row, int d, float4 o,
-                                          float m, float l) {
-  if (row >= r.n * p.group) return;
-  const int64_t grow = r.row0 + row / p.group;
-  const int head = hkv * p.group + row % p.group;
+__device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int head, int d, float4 o, float m, float l) {
   const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
   const float inv = none ? 0.0f : 1.0f / l;
   if (d < p.c.head_dim) {
     o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    store4<BF16>(p.out + (grow * p.o_row + head * p.o_head + d) * (BF16 ? 2 : 4), o);
+    store4<BF16>(p.out + (row * p.o_row + head * p.o_head + d) * (BF16 ? 2 : 4), o);
   }
-  if (d == 0 && p.lse) p.lse[grow * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
+  if (d == 0 && p.lse) p.lse[row * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
 }
-
 
 // ---------------------------------------------------------------------------------------------------------------------
 // The line of tiles
@@ -157,57 +155,81 @@ struct AttnSpan {
   int64_t first;        // that request's first place
 };
 
-// Computed by every block for itself (one pass over the requests for the total, one to find the start), by T threads
-// of which this is thread t; sync() is a barrier among them.  s_sum [T / 32] and s_find [2] are shared.
+// a b / c for b c < 2^63, by 32-bit division where the numbers are small.
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  const int64_t n = a * b;
+  if (n <= UINT32_MAX && c <= UINT32_MAX) return static_cast<uint32_t>(n) / static_cast<uint32_t>(c);
+  return n / c;
+}
+
+// Computed by every block for itself, by T threads of which this is thread t; sync() is a barrier among them.  One
+// scan over the first T requests gives the total and finds the start; only larger batches are gone through again.
+// s_sum [2 T / 32] and s_find [2] are shared.
 template <int MT, int KT, int U, int T, class Sync>
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_t* s_sum, int64_t* s_find, Sync sync) {
+  constexpr int W = T / 32;
   const int lane = t & 31, warp = t >> 5;
   AttnSpan sp{};
-  int64_t sum = 0;
-  for (int b = t; b < p.batch; b += T) sum += attn_places<MT, KT, U>(p, attn_request(p, b));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) s_sum[warp] = sum;
-  if (t == 0) s_find[0] = -1;
-  sync();
-#pragma unroll
-  for (int w = 0; w < T / 32; ++w) sp.total += s_sum[w];
-  sync();
-  const int64_t blocks = gridDim.x;
-  sp.g = sp.total < blocks ? (sp.total > 0 ? sp.total : 1) : blocks;
-  // Requests without rows have no places: their status is written here.
-  for (int b = blockIdx.x * T + t; b < p.batch; b += gridDim.x * T) {
+  int64_t own = 0, rest = 0;
+  for (int b = t; b < p.batch; b += T) {
     const AttnRequest r = attn_request(p, b);
-    if (r.n == 0) p.status[b] = r.status;
+    const int64_t places = attn_places<MT, KT, U>(p, r);
+    if (b == t)
+      own = places;
+    else
+      rest += places;
+    // a request without rows has no places: its status is written here
+    if (r.n == 0 && b % gridDim.x == blockIdx.x) p.status[b] = r.status;
   }
-  if (blockIdx.x >= sp.g || sp.total == 0) return sp;
-  sp.start = blockIdx.x * sp.total / sp.g;
-  sp.end = (blockIdx.x + 1) * sp.total / sp.g;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += T) {
-    const int b = b0 + t;
-    const int64_t own = b < p.batch ? attn_places<MT, KT, U>(p, attn_request(p, b)) : 0;
-    int64_t inc = own;
+  auto scan = [&](int64_t x) {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
+      const int64_t o = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += o;
     }
-    if (lane == 31) s_sum[warp] = inc;
-    sync();
-    int64_t base = before, chunk = 0;
+    return x;
+  };
+  int64_t inc = scan(own);
+  if (p.batch > T) {
 #pragma unroll
-    for (int w = 0; w < T / 32; ++w) {
-      if (w < warp) base += s_sum[w];
-      chunk += s_sum[w];
-    }
-    if (own > 0 && base + inc - own <= sp.start && sp.start < base + inc) {
-      s_find[0] = b;
-      s_find[1] = base + inc - own;
+    for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+  }
+  if (lane == 31) s_sum[warp] = inc, s_sum[W + warp] = rest;
+  if (t == 0) s_find[0] = -1;
+  sync();
+  int64_t base = 0, chunk = 0;  // places before this warp, and of this chunk of requests
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) base += s_sum[w];
+    chunk += s_sum[w];
+    sp.total += s_sum[w] + s_sum[W + w];
+  }
+  const int64_t blocks = gridDim.x;
+  sp.g = sp.total < blocks ? (sp.total > 0 ? sp.total : 1) : blocks;
+  if (blockIdx.x >= sp.g || sp.total == 0) return sp;
+  sp.start = mul_div(blockIdx.x, sp.total, sp.g);
+  sp.end = mul_div(blockIdx.x + 1, sp.total, sp.g);
+  int64_t before = 0;
+  for (int b0 = 0;;) {
+    const int64_t at = before + base + inc - own;
+    if (own > 0 && at <= sp.start && sp.start < at + own) {
+      s_find[0] = b0 + t;
+      s_find[1] = at;
     }
     sync();
     before += chunk;
-    if (s_find[0] >= 0) break;
+    b0 += T;
+    if (s_find[0] >= 0 || b0 >= p.batch) break;
+    own = b0 + t < p.batch ? attn_places<MT, KT, U>(p, attn_request(p, b0 + t)) : 0;
+    inc = scan(own);
+    if (lane == 31) s_sum[warp] = inc;
+    sync();
+    base = chunk = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) base += s_sum[w];
+      chunk += s_sum[w];
+    }
   }
   sp.b = static_cast<int32_t>(s_find[0]);
   sp.first = s_find[1];
@@ -264,11 +286,21 @@ struct AttnWalk {
 // Parts of a unit that several blocks share
 // ---------------------------------------------------------------------------------------------------------------------
 
-// Floats of a part: O as [DP / 4][MT] quads of columns, m [MT], l [MT], status.
+// Floats of a part: O as [DP / 4][MT] quads of columns, m [MT], l [MT], status, and an AttnSplit (see there).
 template <int MT, int DP>
 struct AttnPart {
-  static constexpr int kM = MT * DP, kL = kM + MT, kStatus = kL + MT, kFloats = kStatus + 4;
+  static constexpr int kM = MT * DP, kL = kM + MT, kStatus = kL + MT, kSplit = kStatus + 4, kFloats = kSplit + 12;
 };
+
+// What the join kernel needs of a unit that begins in a block and goes on behind it.
+struct AttnSplit {
+  int64_t row0;
+  int32_t n, b, hkv, rt;
+  int32_t last;     // the unit's last block; 0: the block left no such unit
+  int32_t reports;
+  int32_t pad[4];
+};
+static_assert(sizeof(AttnSplit) == 48, "AttnSplit layout");
 
 // A block leaves at most two parts: of a unit that began before it, and of one that goes on behind it.
 template <int MT, int DP>
@@ -276,20 +308,77 @@ __device__ __forceinline__ float* attn_part(const AttnParams& p, int block, bool
   return p.parts + (static_cast<int64_t>(block) * 2 + (begins ? 1 : 0)) * AttnPart<MT, DP>::kFloats;
 }
 
+// The block that owns a place.
+__device__ __forceinline__ int attn_owner(const AttnSpan& sp, int64_t place) {
+  const int64_t n = (place + 1) * sp.g - 1;
+  if (n <= UINT32_MAX && sp.total <= UINT32_MAX) return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(sp.total));
+  return static_cast<int>(n / sp.total);
+}
+
 // After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
-// writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_last is shared.  At the end
-// of a call every trip to L2 counts, so a part's m, l and O are fetched together (eight quads of columns a thread, two
-// parts at a time) and the running maximum moves as they come.
+// writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_last is shared.
+// Joins parts c0 .. c1 of a unit and writes its rows: E quads of columns a thread, PARTS parts in flight; a part's m, l
+// and O are fetched together, and the running maximum moves as they come.
+template <bool BF16, int MT, int DP, int T, int E, int PARTS>
+__device__ __forceinline__ void attn_join_rows(const AttnParams& p, const AttnSegment& s, int c0, int c1, int live,
+                                               int t) {
+  using P = AttnPart<MT, DP>;
+  const float* first = attn_part<MT, DP>(p, c0, true);
+  const float* rest = attn_part<MT, DP>(p, 0, false);
+  auto part_of = [&](int c) { return c == c0 ? first : rest + static_cast<int64_t>(c) * 2 * P::kFloats; };
+  int wide = 1;  // threads side by side on the rows: a power of two
+  while (wide < live) wide *= 2;
+  const int row = t & (wide - 1), step = T / wide;
+  const int grow = s.rt * MT + row, i = grow / p.group;
+  const int head = s.hkv * p.group + grow - i * p.group;
+  for (int q0 = t / wide; q0 < DP / 4 && row < live; q0 += step * E) {
+    float4 a[E];
+    float M = -kInfF, L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int cb = c0; cb <= c1; cb += PARTS) {
+      float m[PARTS], l[PARTS];
+      float4 v[PARTS][E];
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        m[j] = -kInfF, l[j] = 0.0f;
+        if (cb + j <= c1) {
+          const float* q = part_of(cb + j);
+          m[j] = __ldcg(q + P::kM + row), l[j] = __ldcg(q + P::kL + row);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q0 + e * step < DP / 4)
+              v[j][e] = __ldcg(reinterpret_cast<const float4*>(q) + (q0 + e * step) * MT + row);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        if (cb + j > c1) break;
+        const float N = fmax_nan(M, m[j]), ref = N == -kInfF ? 0.0f : N;
+        const float wa = ex2_fast(M - ref), wb = ex2_fast(m[j] - ref);
+        M = N;
+        L = fmaf(L, wa, l[j] * wb);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          a[e].x = fmaf(a[e].x, wa, v[j][e].x * wb), a[e].y = fmaf(a[e].y, wa, v[j][e].y * wb);
+          a[e].z = fmaf(a[e].z, wa, v[j][e].z * wb), a[e].w = fmaf(a[e].w, wa, v[j][e].w * wb);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) write_row<BF16>(p, s.r.row0 + i, head, (q0 + e * step) * 4, a[e], M, L);
+  }
+}
+
 template <bool BF16, int MT, int DP, int T, class Sync>
 __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
                                           int* s_last, Sync sync) {
-  using P = AttnPart<MT, DP>;
-  constexpr int E = 8, ES = BF16 ? 2 : 4;
   __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
   sync();
   // the unit's blocks are those that own its first and its last tile
-  const int c0 = static_cast<int>(((s.u0 + 1) * sp.g - 1) / sp.total);
-  const int c1 = static_cast<int>(((s.u0 + s.nt) * sp.g - 1) / sp.total);
+  const int c0 = attn_owner(sp, s.u0), c1 = attn_owner(sp, s.u0 + s.nt - 1);
   if (t == 0) {
     const bool last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0);
     if (last) p.tickets[c0] = 0u;
@@ -297,53 +386,17 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
   }
   sync();
   if (!*s_last) return;
-  const float* first = attn_part<MT, DP>(p, c0, true);
-  const float* rest = attn_part<MT, DP>(p, 0, false);
-  auto part_of = [&](int c) { return c == c0 ? first : rest + static_cast<int64_t>(c) * 2 * P::kFloats; };
+  // few rows: one quad a thread and eight parts at a time; many: four quads and two parts
   const int live = min(MT, s.r.n * p.group - s.rt * MT);
-  int wide = 1;  // threads side by side on the rows: a power of two
-  while (wide < live) wide *= 2;
-  const int row = t & (wide - 1), step = T / wide;
-  const int grow = s.rt * MT + row, i = grow / p.group;
-  const int head = s.hkv * p.group + grow - i * p.group;
-  char* out = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head) * ES;
-  uint32_t any = 0u;
-  for (int q0 = t / wide; q0 < DP / 4 && row < live; q0 += step * E) {
-    float4 a[E];
-    float M = -kInfF, L = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = c0; c <= c1; ++c) {
-      const float* q = part_of(c);
-      const float m = __ldcg(q + P::kM + row), l = __ldcg(q + P::kL + row);
-      float4 v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (q0 + e * step < DP / 4) v[e] = __ldcg(reinterpret_cast<const float4*>(q) + (q0 + e * step) * MT + row);
-      if (t == 0 && q0 == 0) any |= __float_as_uint(__ldcg(q + P::kStatus));
-      if (m == -kInfF) continue;  // nothing seen in this part
-      const float N = fmax_nan(M, m), wa = ex2_fast(M - N), wb = ex2_fast(m - N);
-      M = N;
-      L = fmaf(L, wa, l * wb);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        a[e].x = fmaf(a[e].x, wa, v[e].x * wb), a[e].y = fmaf(a[e].y, wa, v[e].y * wb);
-        a[e].z = fmaf(a[e].z, wa, v[e].z * wb), a[e].w = fmaf(a[e].w, wa, v[e].w * wb);
-      }
-    }
-    const bool none = M == -kInfF;
-    const float inv = none ? 0.0f : 1.0f / L;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = (q0 + e * step) * 4;
-      if (d < p.c.head_dim)
-        store4<BF16>(out + d * ES, none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                        : make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv));
-    }
-    if (q0 == 0 && p.lse) p.lse[(s.r.row0 + i) * p.heads + head] = none ? -kInfF : fmaf(M, kLn2, logf(L));
+  if (live * (DP / 4) <= 2 * T)
+    attn_join_rows<BF16, MT, DP, T, 1, 8>(p, s, c0, c1, live, t);
+  else
+    attn_join_rows<BF16, MT, DP, T, 4, 2>(p, s, c0, c1, live, t);
+  if (s.reports && t == 0) {
+    uint32_t any = 0u;
+    for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(attn_part<MT, DP>(p, c, c == c0) + AttnPart<MT, DP>::kStatus));
+    p.status[s.b] = any;
   }
-  if (s.reports && t == 0) p.status[s.b] = any;
 }
 
 // The tensor-memory kernel (bf16, head_dim <= 128).

@@ -6,7 +6,8 @@
 //   O += P V  (P from tensor memory)         accumulated in tensor memory
 //
 // Four softmax warps, four loading warps, one warp that issues the matrix
-// instructions and one that loads the next unit's Q, connected by mbarriers.  The loading warps gather K and V rows
+// instructions, one that loads the next unit's Q and one that walks the line
+// of tiles ahead of them all, connected by mbarriers.  The loading warps gather K and V rows
 // through the page table with 16-byte asynchronous copies into a ring of
 // tiles in the 128-byte swizzle the matrix unit reads, and run ahead over the
 // ends of units.  S has two buffers, so the next tile's scores are computed
@@ -14,6 +15,10 @@
 // moves (and O is rescaled) only when a row's maximum has grown by more than
 // 2^8: the weights stay below 2^8, the sums in fp32, and the result does not
 // depend on the reference.
+//
+// Units that several blocks share are joined by a second kernel, spread over
+// the whole GPU: two long requests leave 19 parts of a unit, which its last
+// block alone took 35 us to join.
 //
 // Every wait is bounded; a wait that gives up raises SV_DEV_TIMEOUT, lets all
 // warps leave, and the block frees its tensor memory.
@@ -29,7 +34,8 @@ namespace {
 
 constexpr int kRows = 128, kKeys = 128;  // a tile
 constexpr int kSoftmaxThreads = 128, kLoadThreads = 128;
-constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 64;  // and a warp to issue, a warp to load Q
+constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 96;  // and a warp each to issue, to load Q, to plan
+constexpr int kReaders = 10;      // warps that read the plan
 constexpr int kUnitPlaces = 1;  // what a unit costs beside its key tiles, in tiles
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kSlack = 8.0f;  // log2 units a row's maximum may pass its reference by
@@ -115,6 +121,11 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // NaN and infini
   return w;
 }
 
+// An arrival that the thread's earlier asynchronous copies make, once they are complete.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // As mbar_try_wait, the thread suspended for up to about `ns`.
 __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
@@ -137,7 +148,6 @@ struct Wide {
   static constexpr int kBlock = kKeys * 128;          // 128 rows of 64 elements
   static constexpr int kTile = kBlock * (DP / 64);    // a K or V tile, or Q
   static constexpr int kRing = DP == 128 ? 6 : 8;     // tiles in the ring
-  static constexpr int kFlight = 4;                   // of them, copies a thread leaves unfinished
   static constexpr int kInfo = 8;                     // tiles whose validity is kept
   static constexpr int kPieces = DP / 8;              // 16-byte pieces of a row
   static constexpr int kS = 0, kO = 256;              // tensor memory columns: two S of 128, then O
@@ -145,9 +155,12 @@ struct Wide {
   static constexpr int kQ = 0;
   static constexpr int kTiles = kTile;
   static constexpr int kValid = kTiles + kRing * kTile;     // uint32 [kInfo][8]: four valid words, four bad
-  static constexpr int kBars = kValid + kInfo * 8 * 4;       // full, empty [kRing], s, p, q, q free, pv [2], soft
-  static constexpr int kMisc = kBars + (2 * kRing + 12) * 8; // sums [10], find [2]; tmem, abort, last, careful
-  static constexpr int kSmem = kMisc + 12 * 8 + 4 * 4;
+  static constexpr int kPlan = kValid + kInfo * 8 * 4;       // AttnSegment [kPlans]
+  static constexpr int kPlans = 4;
+  static constexpr int kBars = kPlan + kPlans * static_cast<int>(sizeof(AttnSegment));
+  // full, empty [kRing], s, p, q, q free, pv [2], soft, (pad), plan, plan free [kPlans]
+  static constexpr int kMisc = kBars + (2 * kRing + 12 + 2 * kPlans) * 8;  // sums [22], find [2]; tmem, abort, careful
+  static constexpr int kSmem = kMisc + 24 * 8 + 4 * 4;
   // 16-byte piece c of row r of a tile
   __device__ static uint32_t piece(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -162,11 +175,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   const uint32_t base = smem_addr(smem);
   uint32_t* s_valid = reinterpret_cast<uint32_t*>(smem + W::kValid);
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem + W::kMisc);
-  int64_t* s_find = s_sum + 10;
+  int64_t* s_find = s_sum + 22;
   int* s_misc = reinterpret_cast<int*>(s_find + 2);
   volatile int* s_abort = s_misc + 1;
-  int* s_last = s_misc + 2;
-  volatile int* s_careful = s_misc + 3;
+  volatile int* s_careful = s_misc + 2;
+  AttnSegment* s_plan = reinterpret_cast<AttnSegment*>(smem + W::kPlan);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   auto bar_full = [&](int i) { return base + W::kBars + i * 8; };
   auto bar_empty = [&](int i) { return base + W::kBars + (NB + i) * 8; };
@@ -178,6 +191,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   // come means that O has the products of tile g - 2, not those of g - 1.
   auto bar_pv = [&](uint32_t g) { return base + W::kBars + (2 * NB + 8 + (g & 1)) * 8; };
   const uint32_t bar_soft = base + W::kBars + (2 * NB + 10) * 8;
+  auto bar_plan = [&](int i) { return base + W::kBars + (2 * NB + 12 + i) * 8; };
+  auto bar_read = [&](int i) { return base + W::kBars + (2 * NB + 12 + W::kPlans + i) * 8; };
   // Units of up to 64 rows have two Qs, one in each half of Q's rows: the products of the lower half read on into what
   // lies behind it, but rows past 64 are nobody's then.
   const int twin = p.max_len * static_cast<int64_t>(p.group) <= 64 ? 1 : 0;
@@ -190,12 +205,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
     for (int i = 0; i < 2; ++i) mbar_init(bar_pv(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(bar_q(i), 32), mbar_init(bar_qfree(i), 1);
     mbar_init(bar_soft, kSoftmaxThreads);
+    for (int i = 0; i < W::kPlans; ++i) mbar_init(bar_plan(i), 1), mbar_init(bar_read(i), kReaders);
     mbar_fence_init();
     *s_abort = 0;
     *s_careful = 0;
   }
   if (warp == 8) {
-    tmem_alloc(base + W::kMisc + 12 * 8, 512);
+    tmem_alloc(base + W::kMisc + 24 * 8, 512);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -206,8 +222,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   grid_dependency_wait();
   allow_dependents();
   const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kWideThreads>(p, t, s_sum, s_find, [] { __syncthreads(); });
-  AttnWalk<kRows, kKeys, kUnitPlaces> walk(p, span);
-
   // A wait that gives up ends every role; the lanes of a warp leave together.
   auto wait_one = [&](uint32_t bar, uint32_t parity) {
     for (int i = 0; i < 64; ++i)  // suspended meanwhile: warps that poll take issue slots from those that work
@@ -218,21 +232,45 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   };
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
 
-  if (warp >= 4 && warp < 8) {
+  // The next segment of the plan, for a whole warp (or the issuing thread alone); false at the end, or after a wait that
+  // gave up.
+  uint32_t plans = 0;
+  auto next = [&](AttnSegment& s, auto waiter) {
+    const int slot = plans % W::kPlans;
+    if (!waiter(bar_plan(slot), (plans / W::kPlans) & 1)) return false;
+    s = s_plan[slot];
+    __syncwarp(__activemask());
+    if (lane == 0) mbar_arrive(bar_read(slot));
+    ++plans;
+    return s.cnt > 0;
+  };
+
+  if (warp == 10) {
+    // ---- The plan: the block's segments in order, a few ahead of their readers; one without tiles ends it.
+    if (lane == 0) {
+      AttnWalk<kRows, kKeys, kUnitPlaces> walk(p, span);
+      AttnSegment s{};
+      for (bool more = true; more; ++plans) {
+        more = walk.next(s);
+        if (!more) s.cnt = 0;
+        const int slot = plans % W::kPlans;
+        if (plans >= W::kPlans && !wait_one(bar_read(slot), (plans / W::kPlans - 1) & 1)) break;
+        s_plan[slot] = s;
+        mbar_arrive(bar_plan(slot));
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
     // ---- Loading warps: tile g's K is group 2 g of the ring, its V group 2 g + 1.  A warp has 32 of a tile's keys, a
     // lane one key's place, handed round by shuffles; the word that places a lane's key of the next tile is on its way
     // while this tile is copied.
     const int lw = warp - 4;
     AttnSegment s{};
-    bool more = walk.next(s);
+    bool more = next(s, wait);
     int tile = s.t0;
     int64_t word = more ? key_word(p, s.r, s.b, tile * kKeys + lw * 32 + lane) : -1;
     uint32_t q = 0;  // groups issued
     bool ok = true;
-    auto landed = [&](uint32_t group) {  // this thread's copies of the group are in place
-      fence_async();
-      mbar_arrive(bar_full(group % NB));
-    };
     const int c = lane % W::kPieces, sub = lane / W::kPieces;
     constexpr int kStep = 32 / W::kPieces;  // rows a warp copies at once
     const bool in_head = c * 8 < p.c.head_dim;
@@ -243,7 +281,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       const uint32_t bad = __ballot_sync(0xffffffffu, x < s.r.len + s.r.n && off < 0);
       const int64_t shift = (static_cast<int64_t>(s.hkv) * p.c.head_stride + c * 8) * 2;
       if (++tile >= s.t0 + s.cnt) {
-        more = walk.next(s);
+        more = next(s, wait);
         tile = s.t0;
       }
       if (more) word = key_word(p, s.r, s.b, tile * kKeys + lw * 32 + lane);
@@ -265,20 +303,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           const bool live = o >= 0 && in_head;
           cp_async16(dst + W::piece(lw * 32 + i + sub, c), live ? src + o * 2 : p.c.k, live);
         }
-        cp_async_commit();
-        if (q + 1 >= W::kFlight) {
-          cp_async_wait<W::kFlight - 1>();
-          landed(q + 1 - W::kFlight);
-        }
+        cp_async_arrive(bar_full(q % NB));  // when this thread's copies so far are in place
       }
     }
+    cp_async_commit();
     cp_async_wait<0>();
-    if (ok)
-      for (uint32_t i = q >= W::kFlight - 1 ? q - (W::kFlight - 1) : 0; i < q; ++i) landed(i);
   } else if (warp == 9) {
     // ---- Q of the next unit, as soon as this unit's last scores are done.  Rows that do not exist are 0.
     AttnSegment s;
-    for (uint32_t units = 0; walk.next(s); ++units) {
+    for (uint32_t units = 0; next(s, wait); ++units) {
       const int slot = q_slot(units);
       if (q_phase(units) > 0 && !wait(bar_qfree(slot), (q_phase(units) - 1) & 1)) break;
       const int rows = s.r.n * p.group - s.rt * kRows;
@@ -307,6 +340,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
         const int slot = q_slot(units);
         const uint32_t group = 2 * n;
         if (!wait_one(bar_full(group % NB), (group / NB) & 1)) return false;
+        fence_async();  // the copies wrote through the generic proxy, the products read through the asynchronous one
         tc_fence_after();
         mbar_arrive(bar_s(n & 1));  // hands the tile's validity on
         const uint32_t k = base + W::kTiles + (group % NB) * W::kTile;
@@ -321,7 +355,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
         if (last) tc_commit(bar_qfree(slot));
         return true;
       };
-      while (ok && walk.next(s)) {
+      while (ok && next(s, wait_one)) {
         if (!wait_one(bar_q(q_slot(units)), q_phase(units) & 1)) break;
         tc_fence_after();
         ok = scores(g, s.cnt == 1);
@@ -335,6 +369,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
             ok = false;
             break;
           }
+          fence_async();
           tc_fence_after();
           const uint32_t v = base + W::kTiles + (group % NB) * W::kTile;
 #pragma unroll
@@ -360,8 +395,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
     const float c = fmaxf(p.scale_log2, 1e-30f);  // a scale of 0 by one too small to tell: 0 times a masked -inf is NaN
     AttnSegment s;
     uint32_t g = 0;
-    bool ok = true;
-    while (ok && walk.next(s)) {
+    bool ok = true, left = false;  // left: a unit that goes on behind this block
+    while (ok && next(s, wait)) {
       const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
       const bool idle = warp * 32 >= rows;              // none of the warp's rows exists
       const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread
@@ -557,24 +592,91 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       }
       if (whole) {
         if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
-        if (s.reports && t == 0) p.status[s.b] = bad;
+        if (s.reports && t == 0) p.status[s.b] = bad | attn_timeout(p);
       } else {
         part[P::kM + t] = m;
         part[P::kL + t] = l;
-        if (t == 0) part[P::kStatus] = __uint_as_float(bad);
-        attn_join<true, kRows, DP, kSoftmaxThreads>(p, span, s, t, s_last, meet);
+        if (t == 0) {
+          part[P::kStatus] = __uint_as_float(bad);
+          if (s.t0 == 0) {
+            left = true;
+            *reinterpret_cast<AttnSplit*>(part + P::kSplit) =
+                AttnSplit{s.r.row0, s.r.n, s.b, s.hkv, s.rt, attn_owner(span, s.u0 + s.nt - 1), s.reports ? 1 : 0, {}};
+          }
+        }
       }
       tc_fence_before();
     }
+    if (t == 0 && !left)
+      reinterpret_cast<AttnSplit*>(attn_part<kRows, DP>(p, blockIdx.x, true) + AttnPart<kRows, DP>::kSplit)->last = 0;
   }
   __syncthreads();
   if (*s_abort) {  // never expected: see SV_DEV_TIMEOUT
+    if (t == 0) atomicExch(p.err, 1u);
     for (int b = t; b < p.batch; b += kWideThreads) p.status[b] = kStTimeout;
   }
   if (warp == 8) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }
+}
+
+// Block (c, i): rows 16 i .. of the unit that begins in block c of the attention kernel and goes on behind it, if any.
+constexpr int kJoinRows = 16;
+
+template <int DP>
+__global__ void __launch_bounds__(kJoinRows * DP / 8) k_attention_join(AttnParams p) {
+  using P = AttnPart<kRows, DP>;
+  constexpr int PARTS = 8, E = 2;  // parts in flight, quads of columns a thread
+  grid_dependency_wait();
+  allow_dependents();
+  const int c0 = blockIdx.x, t = threadIdx.x;
+  const float* first = attn_part<kRows, DP>(p, c0, true);
+  const float* rest = attn_part<kRows, DP>(p, 0, false);
+  const AttnSplit s = *reinterpret_cast<const AttnSplit*>(first + P::kSplit);
+  if (s.last <= c0) return;
+  auto part_of = [&](int c) { return c == c0 ? first : rest + static_cast<int64_t>(c) * 2 * P::kFloats; };
+  const int row = blockIdx.y * kJoinRows + t % kJoinRows, quad = t / kJoinRows;
+  const int grow = s.rt * kRows + row;
+  if (blockIdx.y == 0 && t == 0 && s.reports) {
+    uint32_t any = 0u;
+    for (int c = c0; c <= s.last; ++c) any |= __float_as_uint(part_of(c)[P::kStatus]);
+    p.status[s.b] = any | attn_timeout(p);
+  }
+  if (grow >= s.n * p.group) return;
+  const int i = grow / p.group, head = s.hkv * p.group + grow - i * p.group;
+  float4 a[E];
+  float M = -kInfF, L = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int cb = c0; cb <= s.last; cb += PARTS) {
+    float m[PARTS], l[PARTS];
+    float4 v[PARTS][E];
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j)
+      if (cb + j <= s.last) {
+        const float* q = part_of(cb + j);
+        m[j] = q[P::kM + row], l[j] = q[P::kL + row];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[j][e] = reinterpret_cast<const float4*>(q)[(quad + e * (DP / 8)) * kRows + row];
+      }
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) {
+      if (cb + j > s.last) break;
+      const float N = fmax_nan(M, m[j]), ref = N == -kInfF ? 0.0f : N;
+      const float wa = ex2_fast(M - ref), wb = ex2_fast(m[j] - ref);
+      M = N;
+      L = fmaf(L, wa, l[j] * wb);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        a[e].x = fmaf(a[e].x, wa, v[j][e].x * wb), a[e].y = fmaf(a[e].y, wa, v[j][e].y * wb);
+        a[e].z = fmaf(a[e].z, wa, v[j][e].z * wb), a[e].w = fmaf(a[e].w, wa, v[j][e].w * wb);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    write_row<true>(p, s.row0 + i, head, (quad + e * (DP / 8)) * 4, a[e], M, L);
 }
 
 template <int DP>
@@ -595,8 +697,12 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
   }
   static_assert(Wide<DP>::kSmem <= 227 * 1024, "shared memory of a block");
   const int grid = dev.sms < kAttnMaxBlocks / 2 ? dev.sms : kAttnMaxBlocks / 2;  // parts are laid out for 64-row tiles
-  return launch_pdl(k_attention_wide<DP>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<DP>::kSmem,
-                    stream, p);
+  e = launch_pdl(k_attention_wide<DP>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<DP>::kSmem, stream, p);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
+  const int slices = static_cast<int>(((rows < kRows ? rows : kRows) + kJoinRows - 1) / kJoinRows);
+  return launch_pdl(k_attention_join<DP>, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(slices)),
+                    dim3(kJoinRows * DP / 8), 0, stream, p);
 }
 
 }  // namespace
