@@ -123,6 +123,25 @@ __device__ __forceinline__ void store4(char* p, float4 v) {
   }
 }
 
+// Which of keys x0 .. x0 + 31 new row i of a request sees, among those of `valid`.
+__device__ __forceinline__ uint32_t row_sees_of(const AttnParams& p, const AttnRequest& r, int b, int i, int x0,
+                                                uint32_t valid) {
+  if (i >= r.n) return 0u;
+  const int hist = r.len - x0;  // keys of the history among them
+  if (hist >= 32) return valid;
+  uint32_t see = hist <= 0 ? 0u : (1u << hist) - 1u;
+  if (!p.mask) {
+    const int upto = hist + i + 1;
+    see = upto <= 0 ? 0u : upto >= 32 ? 0xffffffffu : (1u << upto) - 1u;
+  } else {
+    const uint8_t* m = p.mask + (static_cast<int64_t>(b) * p.max_len + i) * p.max_len - hist;
+#pragma unroll 4
+    for (int k = max(hist, 0); k < min(32, hist + r.n); ++k)
+      if (m[k]) see |= 1u << k;
+  }
+  return see & valid;
+}
+
 // A query row's quad of columns, normalised, and (with the first quad) its lse.
 template <bool BF16>
 __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int head, int d, float4 o, float m, float l) {

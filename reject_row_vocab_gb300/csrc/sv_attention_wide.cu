@@ -27,6 +27,8 @@
 #include <cstdint>
 #include <mutex>
 
+#include <cuda.h>
+
 #include "sv_attention.cuh"
 
 namespace sv {
@@ -121,9 +123,20 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // NaN and infini
   return w;
 }
 
-// An arrival that the thread's earlier asynchronous copies make, once they are complete.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+// K and V of the call's layer as [pages][page_size][heads][head_dim] tensors, in boxes of 64 columns of `rows` rows of a
+// page (a power of two that divides the page's; 0: none, the pages are copied row by row).
+struct KvMaps {
+  CUtensorMap k, v;
+  int32_t rows;
+};
+
+__device__ __forceinline__ void box_copy(uint32_t dst, const CUtensorMap* map, int x, int head, int row, int page,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(head), "r"(row), "r"(page), "r"(bar)
+      : "memory");
 }
 
 // As mbar_try_wait, the thread suspended for up to about `ns`.
@@ -137,6 +150,38 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
       : "r"(bar), "r"(parity), "r"(ns)
       : "memory");
   return ok != 0;
+}
+
+// The rest of a wait that did not end at once.  Suspended meanwhile: warps that poll take issue slots from those that
+// work.  (Out of line, like all that seldom runs: what the roles run by turns has to stay in the instruction cache.)
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait_for(bar, parity, 10000)) return true;
+  if (mbar_wait_bounded(bar, parity, abort, kWaitNs)) return true;
+  *abort = 1;
+  return false;
+}
+
+// An arrival that the thread's earlier asynchronous copies make, once they are complete.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The sum of the NaN and infinite values that new row i sees of columns d .. d + 3 of the segment's new rows' V.
+__device__ __noinline__ float4 nonfinite_seen(const AttnParams& p, const AttnSegment& s, int i, int d) {
+  float f[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < s.r.n; ++j) {
+    const int x = s.r.len + j;
+    if (x < s.t0 * kKeys || x >= (s.t0 + s.cnt) * kKeys || !row_sees(p, s.b, i, j)) continue;
+    const int64_t off = key_offset(p, s.r, x, key_word(p, s.r, s.b, x));
+    if (off < 0) continue;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v) + off + s.hkv * p.c.head_stride + d;
+    for (int k = 0; k < 4 && d + k < p.c.head_dim; ++k) {
+      const float x = __uint_as_float(static_cast<uint32_t>(v[k]) << 16);
+      if (!(fabsf(x) < kInfF)) f[k] += x;
+    }
+  }
+  return make_float4(f[0], f[1], f[2], f[3]);
 }
 
 // ---------------------------------------------------------------------------------------------------------------------
@@ -168,7 +213,8 @@ struct Wide {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p) {
+__global__ void __launch_bounds__(kWideThreads, 1)
+    k_attention_wide(const AttnParams p, const __grid_constant__ KvMaps maps) {
   using W = Wide<DP>;
   constexpr int NB = W::kRing;
   extern __shared__ __align__(1024) char smem[];
@@ -224,11 +270,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
   const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kWideThreads>(p, t, s_sum, s_find, [] { __syncthreads(); });
   // A wait that gives up ends every role; the lanes of a warp leave together.
   auto wait_one = [&](uint32_t bar, uint32_t parity) {
-    for (int i = 0; i < 64; ++i)  // suspended meanwhile: warps that poll take issue slots from those that work
-      if (mbar_try_wait_for(bar, parity, 10000)) return true;
-    if (mbar_wait_bounded(bar, parity, s_abort, kWaitNs)) return true;
-    *s_abort = 1;
-    return false;
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, s_abort);
   };
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; };
 
@@ -279,6 +321,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       const int64_t off = key_offset(p, s.r, x, word);
       const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
       const uint32_t bad = __ballot_sync(0xffffffffu, x < s.r.len + s.r.n && off < 0);
+      // a tile of history in boxes: this lane's box of the warp's 32 keys
+      const bool boxes = maps.rows > 0 && (tile + 1) * kKeys <= s.r.len;
+      const int per = boxes ? 32 / maps.rows : 1;
+      const int box_row = boxes ? lane % per * maps.rows : 0, box_col = boxes ? lane / per : 0;
+      const int box_head = s.hkv;
+      const int64_t box_page = __shfl_sync(0xffffffffu, word, box_row);
+      const uint32_t box_key = static_cast<uint32_t>(tile * kKeys + lw * 32 + box_row);
+      const uint32_t box_in = box_key - divide(box_key, p.c.div_mul, p.c.div_shift) * p.c.page_size;
       const int64_t shift = (static_cast<int64_t>(s.hkv) * p.c.head_stride + c * 8) * 2;
       if (++tile >= s.t0 + s.cnt) {
         more = next(s, wait);
@@ -286,6 +336,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       }
       if (more) word = key_word(p, s.r, s.b, tile * kKeys + lw * 32 + lane);
       const uint32_t g = q >> 1;
+#pragma unroll 1
       for (int which = 0; which < 2; ++which, ++q) {
         if (q >= NB && !wait(bar_empty(q % NB), (q / NB - 1) & 1)) {
           ok = false;
@@ -294,6 +345,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
         if (which == 0 && lane == 0) {
           s_valid[(g % W::kInfo) * 8 + lw] = valid;
           s_valid[(g % W::kInfo) * 8 + 4 + lw] = bad;
+        }
+        if (boxes) {
+          // (a page outside the cache is outside the tensor: the box is filled with zeros)
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar_full(q % NB), 32 * 128 * (DP / 64));
+          else
+            mbar_arrive(bar_full(q % NB));
+          __syncwarp();
+          if (box_col < DP / 64)
+            box_copy(base + W::kTiles + (q % NB) * W::kTile + box_col * W::kBlock + (lw * 32 + box_row) * 128,
+                     which ? &maps.v : &maps.k, box_col * 64, box_head, static_cast<int>(box_in),
+                     static_cast<int>(box_page), bar_full(q % NB));
+          continue;
         }
         const char* src = (which ? p.c.v : p.c.k) + shift;
         const uint32_t dst = base + W::kTiles + (q % NB) * W::kTile;
@@ -308,6 +372,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
     }
     cp_async_commit();
     cp_async_wait<0>();
+    if (*s_abort)  // copies in flight end before the block does
+      for (uint32_t i = q > NB ? q - NB : 0; i < q; ++i)
+        for (int n = 0; n < 100 && !mbar_try_wait_for(bar_full(i % NB), (i / NB) & 1, 10000); ++n) {
+        }
   } else if (warp == 9) {
     // ---- Q of the next unit, as soon as this unit's last scores are done.  Rows that do not exist are 0.
     AttnSegment s;
@@ -316,13 +384,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       if (q_phase(units) > 0 && !wait(bar_qfree(slot), (q_phase(units) - 1) & 1)) break;
       const int rows = s.r.n * p.group - s.rt * kRows;
       const int warps = min(kRows, (rows + 31) & ~31);  // rows of the warps that have any
-      const int c = lane % W::kPieces;
-      for (int row = lane / W::kPieces; row < warps; row += 32 / W::kPieces) {
-        const int grow = s.rt * kRows + row;
-        const bool live = row < rows && c * 8 < p.c.head_dim;
-        const int i = grow / p.group;
-        const int64_t at = (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head + c * 8;
-        cp_async16(base + W::kQ + W::piece(slot * 64 + row, c), p.q + (live ? at * 2 : 0), live);
+      const int c = lane % W::kPieces, sub = lane / W::kPieces;
+      const bool in_head = c * 8 < p.c.head_dim;
+      for (int r0 = 0; r0 < warps; r0 += 32) {  // a lane finds one row's place, the warp copies the 32 of them
+        const int grow = s.rt * kRows + r0 + lane, i = grow / p.group;
+        const int64_t at = r0 + lane < rows
+                               ? (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head
+                               : -1;
+#pragma unroll 8
+        for (int j = 0; j < 32; j += 32 / W::kPieces) {
+          const int64_t o = __shfl_sync(0xffffffffu, at, j + sub);
+          const bool live = o >= 0 && in_head;
+          cp_async16(base + W::kQ + W::piece(slot * 64 + r0 + j + sub, c), live ? p.q + (o + c * 8) * 2 : p.q, live);
+        }
       }
       cp_async_commit();
       cp_async_wait<0>();
@@ -441,40 +515,30 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           fence_async();
         }
         if (!idle) {
-          if (masked) {
-            // what this row sees of the tile: valid keys, history, and new rows up to itself or as the mask says
-            if (x0 + kKeys > s.r.len) {
-              const int first = max(s.r.len - x0, 0);  // first new row's place in the tile
-              const bool none = t >= rows;
+          if (masked) {  // what the row does not see of the tile becomes -inf, in place
 #pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                uint32_t see = 0u;
-                if (!p.mask) {
-                  const int upto = s.r.len + my_row + 1 - x0 - w * 32;  // keys seen of these 32
-                  see = none || upto <= 0 ? 0u : upto >= 32 ? 0xffffffffu : (1u << upto) - 1u;
-                } else if (!none) {
-                  const int hist = first - w * 32;
-                  see = hist <= 0 ? 0u : hist >= 32 ? 0xffffffffu : (1u << hist) - 1u;
-                  const int j0 = x0 + w * 32 - s.r.len;
-                  for (int b = max(-j0, 0); b < min(32, s.r.n - j0); ++b)
-                    if (row_sees(p, s.b, my_row, j0 + b)) see |= 1u << b;
-                }
-                vw[w] &= see;
-              }
+            for (int w = 0; w < 4; ++w) vw[w] = row_sees_of(p, s.r, s.b, t < rows ? my_row : s.r.n, x0 + w * 32, vw[w]);
+            uint32_t word = vw[0];
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              float v[32];
+              tmem_ld32(st + h * 32, reinterpret_cast<uint32_t*>(v));
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = (word >> j & 1u) ? v[j] : -kInfF;
+              tmem_st32(st + h * 32, reinterpret_cast<const uint32_t*>(v));
+              word = h == 0 ? vw[1] : h == 1 ? vw[2] : vw[3];
             }
+            tmem_wait_st();
           }
           // The scores are read twice, for the maximum and for the weights: 128 of them do not fit beside the rest.
           float mx[4] = {-kInfF, -kInfF, -kInfF, -kInfF};
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float v[64];
             tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
             tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
             tmem_wait_ld();
-            if (masked) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = (vw[h * 2 + (j >> 5)] >> (j & 31) & 1u) ? v[j] : -kInfF;
-            }
 #pragma unroll
             for (int j = 0; j < 64; ++j) mx[j & 3] = fmax_nan(mx[j & 3], v[j]);
           }
@@ -491,7 +555,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
               break;
             }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < DP / 32; ++h) {
               float o[32];
               tmem_ld32(tmem + lanes + W::kO + h * 32, reinterpret_cast<uint32_t*>(o));
@@ -503,17 +567,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
           }
           const float ref = m == -kInfF ? 0.0f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float v[64];
             uint32_t pk[32];
             tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
             tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
             tmem_wait_ld();
-            if (masked) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = (vw[h * 2 + (j >> 5)] >> (j & 31) & 1u) ? v[j] : -kInfF;
-            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float a = ex2_fast(fmaf(v[2 * j], c, -ref));
@@ -550,25 +610,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) k_attention_wide(AttnParams p
       const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
       const float inv = none ? 0.0f : 1.0f / l;
       if (!idle) {
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < DP / 32; ++h) {
           float o[32];
           tmem_ld32(tmem + lanes + W::kO + h * 32, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
           if (t < rows) {
             if (careful) {
-              for (int j = 0; j < s.r.n; ++j) {
-                const int x = s.r.len + j;
-                if (x < s.t0 * kKeys || x >= (s.t0 + s.cnt) * kKeys || !row_sees(p, s.b, my_row, j)) continue;
-                const int64_t off = key_offset(p, s.r, x, key_word(p, s.r, s.b, x));
-                if (off < 0) continue;
-                const uint16_t* vr = reinterpret_cast<const uint16_t*>(p.c.v) + off + s.hkv * p.c.head_stride + h * 32;
 #pragma unroll
-                for (int d = 0; d < 32; ++d)
-                  if (h * 32 + d < p.c.head_dim) {
-                    const float f = __uint_as_float(static_cast<uint32_t>(vr[d]) << 16);
-                    if (!(fabsf(f) < kInfF)) o[d] += f;
-                  }
+              for (int d = 0; d < 32; d += 4) {
+                const float4 f = nonfinite_seen(p, s, my_row, h * 32 + d);
+                o[d] += f.x, o[d + 1] += f.y, o[d + 2] += f.z, o[d + 3] += f.w;
               }
             }
             if (whole) {
@@ -679,6 +731,44 @@ __global__ void __launch_bounds__(kJoinRows * DP / 8) k_attention_join(AttnParam
     write_row<true>(p, s.row0 + i, head, (quad + e * (DP / 8)) * 4, a[e], M, L);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiledFn>(f) : nullptr;
+  }();
+  return fn;
+}
+
+// Boxes need pages of a multiple of eight rows (the swizzle's period); a layout the driver takes no map of has none.
+KvMaps kv_maps(const KvView& c) {
+  KvMaps m{};
+  int rows = 32;
+  while (rows >= 8 && c.page_size % rows != 0) rows /= 2;
+  const EncodeTiledFn encode = encode_tiled();
+  if (rows < 8 || !encode) return m;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.heads),
+                              static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
+  // an axis of one entry may come without a step
+  auto step = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s : (c.head_dim + 7) / 8 * 8) * 2; };
+  const cuuint64_t strides[3] = {step(c.head_stride), step(c.slot_stride), step(c.page_stride)};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
+  char* const base[2] = {c.k, c.v};
+  CUtensorMap* const map[2] = {&m.k, &m.v};
+  for (int i = 0; i < 2; ++i)
+    if (encode(map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return m;
+  m.rows = rows;
+  return m;
+}
+
 template <int DP>
 cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   static std::mutex mu;
@@ -697,7 +787,8 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
   }
   static_assert(Wide<DP>::kSmem <= 227 * 1024, "shared memory of a block");
   const int grid = dev.sms < kAttnMaxBlocks / 2 ? dev.sms : kAttnMaxBlocks / 2;  // parts are laid out for 64-row tiles
-  e = launch_pdl(k_attention_wide<DP>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<DP>::kSmem, stream, p);
+  e = launch_pdl(k_attention_wide<DP>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<DP>::kSmem, stream, p,
+                 kv_maps(p.c));
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
   const int slices = static_cast<int>(((rows < kRows ? rows : kRows) + kJoinRows - 1) / kJoinRows);
