@@ -12,7 +12,7 @@
 #include <cstdint>
 #include <mutex>
 
-#include "sv_attention.cuh"
+#include "sv_attention_ring.cuh"
 
 namespace sv {
 namespace {
@@ -111,7 +111,6 @@ struct SimtEngine {
       l[i] = fmaf(l[i], a, pr[i]);
 #pragma unroll
       for (int j = 0; j < NQ; ++j) o[i][j].x *= a, o[i][j].y *= a, o[i][j].z *= a, o[i][j].w *= a;
-      if (masked && s[i] == -kInfF) pr[i] = -1.0f;  // not seen: its V has no part, whatever it holds
     }
     *reinterpret_cast<float4*>(pt + lane * MT + warp * 4) = make_float4(pr[0], pr[1], pr[2], pr[3]);
     __syncwarp();
@@ -125,13 +124,12 @@ struct SimtEngine {
         const int byte = d * ES;
         const float4 v = load4(vs + piece(key, byte >> 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!masked || !(w[i] < 0.0f)) {
-            o[i][j].x = fmaf(w[i], v.x, o[i][j].x);
-            o[i][j].y = fmaf(w[i], v.y, o[i][j].y);
-            o[i][j].z = fmaf(w[i], v.z, o[i][j].z);
-            o[i][j].w = fmaf(w[i], v.w, o[i][j].w);
-          }
+        for (int i = 0; i < 4; ++i) {
+          o[i][j].x = fmaf(w[i], v.x, o[i][j].x);
+          o[i][j].y = fmaf(w[i], v.y, o[i][j].y);
+          o[i][j].z = fmaf(w[i], v.z, o[i][j].z);
+          o[i][j].w = fmaf(w[i], v.w, o[i][j].w);
+        }
       }
     }
     __syncwarp();
@@ -185,21 +183,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// A pair of bf16 with NaN and infinities replaced by 0.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-  return w;
-}
-__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
 template <int DP, int WR>
 struct MmaEngine {
   static constexpr bool kBf16 = true;
@@ -283,18 +266,19 @@ struct MmaEngine {
     // valid: a bit for each of the tile's keys
     const bool masked = (valid[0] & valid[1]) != 0xffffffffu || x0 + KT > r.len;
     if (masked) {
+      constexpr int W = NK > 32 ? 2 : 1;  // the words of 32 keys that hold the warp's
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = (rt * MT + row_lo + h * 8) / p.group;
+        uint32_t see[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          see[w] = row_sees_of(p, r, b, row, x0 + (k0 & ~31) + w * 32, valid[(k0 >> 5) + w]) >> (k0 & 31);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int key = k0 + i * 8 + (lane & 3) * 2 + c;
-            bool see = (valid[key >> 5] >> (key & 31) & 1u) != 0u && row < r.n;
-            if (see && x0 + key >= r.len) see = row_sees(p, b, row, x0 + key - r.len);
-            if (!see) s[i][h * 2 + c] = -kInfF;
-          }
+          for (int c = 0; c < 2; ++c)
+            if (!(see[i / 4] >> (i % 4 * 8 + (lane & 3) * 2 + c) & 1u)) s[i][h * 2 + c] = -kInfF;
       }
     }
     float alpha[2];
@@ -326,16 +310,6 @@ struct MmaEngine {
         o[i][2] *= alpha[1], o[i][3] *= alpha[1];
       }
     }
-    // A weight of 0 does not silence a V that is NaN or infinite.  Only new rows can be seen by some rows of the tile
-    // and not by others; where one of them holds such a V, it is taken out of the products and added by itself.
-    bool careful = false;
-    if (masked && r.n > 1) {
-      for (int x = lane; x < NK * (DP / 8); x += 32) {
-        const uint4 u = *reinterpret_cast<const uint4*>(stage + KT * ROW + piece(k0 + x / (DP / 8), x % (DP / 8)));
-        careful = careful || nonfinite_pair(u.x) || nonfinite_pair(u.y) || nonfinite_pair(u.z) || nonfinite_pair(u.w);
-      }
-      careful = __any_sync(0xffffffffu, careful);
-    }
 #pragma unroll
     for (int j = 0; j < NT / 2; ++j) {
       const uint32_t a[4] = {pack_bf16(s[2 * j][0], s[2 * j][1]), pack_bf16(s[2 * j][2], s[2 * j][3]),
@@ -344,37 +318,9 @@ struct MmaEngine {
       for (int dt = 0; dt < DT; dt += 2) {
         uint32_t vb[4];
         ldmatrix4_trans(vs_addr + piece(k0 + j * 16 + (mi & 1) * 8 + mr, dt + (mi >> 1)), vb);
-        if (careful) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vb[i] = finite_pair(vb[i]);
-        }
         mma_bf16(o[dt], a, vb[0], vb[1]);
         mma_bf16(o[dt + 1], a, vb[2], vb[3]);
       }
-    }
-    if (careful) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        for (int kk = 0; kk < 8; ++kk) {
-          const int src = (lane & ~3) | (kk >> 1);
-          const float w0 = __shfl_sync(0xffffffffu, (kk & 1) ? s[i][1] : s[i][0], src);
-          const float w1 = __shfl_sync(0xffffffffu, (kk & 1) ? s[i][3] : s[i][2], src);
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(stage + KT * ROW + piece(k0 + i * 8 + kk, dt) +
-                                                                  (lane & 3) * 4);
-            if (!nonfinite_pair(v)) continue;
-            const float lo = bf16_lo(v), hi = bf16_hi(v);
-            if (finite_pair(v & 0xffffu) != (v & 0xffffu)) {
-              if (w0 != 0.0f) o[dt][0] = fmaf(w0, lo, o[dt][0]);
-              if (w1 != 0.0f) o[dt][2] = fmaf(w1, lo, o[dt][2]);
-            }
-            if (finite_pair(v & 0xffff0000u) != (v & 0xffff0000u)) {
-              if (w0 != 0.0f) o[dt][1] = fmaf(w0, hi, o[dt][1]);
-              if (w1 != 0.0f) o[dt][3] = fmaf(w1, hi, o[dt][3]);
-            }
-          }
-        }
     }
   }
 
@@ -440,7 +386,8 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
     const AttnRequest& r = s.r;
     const int end = s.t0 + s.cnt;
     const int keys = r.len + r.n;
-    uint32_t bad = 0u;  // this thread placed a key outside the cache
+    uint32_t bad = 0u;   // this thread placed a key outside the cache
+    bool found = false;  // it took values that are not finite out of V
 
     E eng;
     // Offsets of a tile's keys: fetched as raw words two tiles before they are needed.
@@ -472,24 +419,35 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
       }
       cp_async_commit();
     };
+#pragma unroll 1
     for (int i = 0; i < S; ++i) {
       fetch(s.t0 + i);
       place(s.t0 + i);
     }
     fetch(s.t0 + S);
     __syncthreads();
+#pragma unroll 1
     for (int i = 0; i < S - 1; ++i) load(s.t0 + i);
     eng.init(p, r, s.hkv, s.rt, extra);
+#pragma unroll 1
     for (int tile = s.t0; tile < end; ++tile) {
       cp_async_wait<S - 2>();
       __syncthreads();
       load(tile + S - 1);
       place(tile + S);
       fetch(tile + S + 1);
+      if (r.n > 1 && (tile + 1) * KT > r.len) {
+        char* v = ring + (tile % S) * E::STAGE + KT * E::ROW;
+#pragma unroll 1
+        for (int x = max(r.len - tile * KT, 0) * PIECES + t; x < KT * PIECES; x += T)
+          if (make_finite<E::kBf16>(reinterpret_cast<uint4*>(v + E::piece(x / PIECES, x % PIECES)))) found = true;
+        __syncthreads();
+      }
       eng.tile(p, r, s.b, s.rt, tile * KT, ring + (tile % S) * E::STAGE, s_valid + (tile % RING) * 4);
     }
     cp_async_wait<0>();
     bad = (__syncthreads_or(static_cast<int>(bad)) ? kStSlotRange : 0u) | r.status;
+    const bool careful = __syncthreads_or(found ? 1 : 0) != 0;
 
     // Finish: the key groups' parts, joined in group order.
     float* s_o = reinterpret_cast<float*>(ring);
@@ -518,9 +476,15 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
         const float4 v = *reinterpret_cast<const float4*>(s_o + (k * MT + row) * DP + d);
         a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
       }
+      if (careful && s.rt * MT + row < r.n * p.group) {
+        const AttnSegment copy = s;
+        const float4 f = nonfinite_seen<E::kBf16, KT>(p, copy, (s.rt * MT + row) / p.group, d);
+        a.x += f.x, a.y += f.y, a.z += f.z, a.w += f.w;
+      }
       return a;
     };
     if (s.cnt == s.nt) {
+#pragma unroll 1
       for (int x = t; x < MT * QUADS; x += T) {
         const int row = x / QUADS, d = (x % QUADS) * 4, grow = s.rt * MT + row;
         if (grow < r.n * p.group) {
@@ -532,13 +496,16 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
     } else {
       using P = AttnPart<MT, DP>;
       float* part = attn_part<MT, DP>(p, blockIdx.x, s.t0 == 0);
+#pragma unroll 1
       for (int x = t; x < MT * QUADS; x += T) {
         const int row = x % MT, quad = x / MT;
         *reinterpret_cast<float4*>(part + x * 4) = joined(row, quad * 4);
       }
       for (int row = t; row < MT; row += T) part[P::kM + row] = s_m[row], part[P::kL + row] = s_l[row];
       if (t == 0) part[P::kStatus] = __uint_as_float(bad);
-      attn_join<E::kBf16, MT, DP, T>(p, span, s, t, &s_last, sync);
+      const AttnSegment copy = s;
+      const AttnSpan span_copy = span;
+      attn_join<E::kBf16, MT, DP, T>(p, span_copy, copy, t, &s_last);
     }
     __syncthreads();  // the ring and the offsets are free again
   }
@@ -576,22 +543,15 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
   return launch_pdl(k_attention<E>, dim3(static_cast<unsigned>(grid)), dim3(E::THREADS), Lay<E>::kSmem, stream, p);
 }
 
-// Row tiles of 16, 32 or 64: the smallest that holds a request's rows, so that few rows leave their warps to the keys.
-template <int DP>
-cudaError_t launch_mma(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
-  if (rows <= 16) return launch<MmaEngine<DP, 1>>(p, dev, stream);
-  if (rows <= 32) return launch<MmaEngine<DP, 2>>(p, dev, stream);
-  return launch<MmaEngine<DP, 4>>(p, dev, stream);
-}
-
 cudaError_t launch_attention(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   const int dim = p.c.head_dim;
-  if (p.c.es == 2 && dim <= 128 && static_cast<int64_t>(p.max_len) * p.group > 32 && p.scale_log2 >= 0.0f)
-    return launch_attention_wide(p, dev, stream);
-  if (p.c.es == 2)
-    return dim <= 64 ? launch_mma<64>(p, dev, stream)
-                     : dim <= 128 ? launch_mma<128>(p, dev, stream) : launch_mma<256>(p, dev, stream);
+  const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
+  if (p.c.es == 2) {
+    if (dim <= 128) return rows <= 16 ? launch_attention_few(p, dev, stream) : launch_attention_wide(p, dev, stream);
+    // row tiles of 16, 32 or 64: the smallest that holds a request's rows, so that few rows leave their warps to the keys
+    return rows <= 16 ? launch<MmaEngine<256, 1>>(p, dev, stream)
+                      : rows <= 32 ? launch<MmaEngine<256, 2>>(p, dev, stream) : launch<MmaEngine<256, 4>>(p, dev, stream);
+  }
   return dim <= 64 ? launch<SimtEngine<64>>(p, dev, stream)
                    : dim <= 128 ? launch<SimtEngine<128>>(p, dev, stream) : launch<SimtEngine<256>>(p, dev, stream);
 }
@@ -602,7 +562,46 @@ size_t part_bytes(int32_t head_dim) {
   return (64 * (dp + 2) + 16) * sizeof(float);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiledFn>(f) : nullptr;
+  }();
+  return fn;
+}
+
 }  // namespace
+
+// Boxes need pages of a multiple of eight rows (the swizzle's period); a layout the driver takes no map of has none.
+KvMaps kv_maps(const KvView& c) {
+  KvMaps m{};
+  int rows = 32;
+  while (rows >= 8 && c.page_size % rows != 0) rows /= 2;
+  const EncodeTiledFn encode = encode_tiled();
+  if (rows < 8 || !encode) return m;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.heads),
+                              static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
+  // an axis of one entry may come without a step
+  auto step = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s : (c.head_dim + 7) / 8 * 8) * 2; };
+  const cuuint64_t strides[3] = {step(c.head_stride), step(c.slot_stride), step(c.page_stride)};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
+  char* const base[2] = {c.k, c.v};
+  CUtensorMap* const map[2] = {&m.k, &m.v};
+  for (int i = 0; i < 2; ++i)
+    if (encode(map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return m;
+  m.rows = rows;
+  return m;
+}
+
 }  // namespace sv
 
 using namespace sv;

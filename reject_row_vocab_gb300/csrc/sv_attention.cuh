@@ -302,6 +302,51 @@ struct AttnWalk {
 };
 
 // ---------------------------------------------------------------------------------------------------------------------
+// NaN and infinities in V.  A weight of 0 does not silence them, and only new rows can be seen by some rows of a tile and
+// not by others: there they are taken out of the products, and added at the end to the rows that see them.
+// ---------------------------------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // two bf16
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// Takes the values that are not finite out of 16 bytes of V; whether there were any.
+template <bool BF16>
+__device__ __forceinline__ bool make_finite(uint4* at) {
+  const uint4 u = *at;
+  uint4 f;
+  if (BF16)
+    f = make_uint4(finite_pair(u.x), finite_pair(u.y), finite_pair(u.z), finite_pair(u.w));
+  else
+    f = make_uint4((u.x & 0x7f800000u) == 0x7f800000u ? 0u : u.x, (u.y & 0x7f800000u) == 0x7f800000u ? 0u : u.y,
+                   (u.z & 0x7f800000u) == 0x7f800000u ? 0u : u.z, (u.w & 0x7f800000u) == 0x7f800000u ? 0u : u.w);
+  if (f.x == u.x && f.y == u.y && f.z == u.z && f.w == u.w) return false;
+  *at = f;
+  return true;
+}
+
+// The sum of the NaN and infinite values that new row i sees of columns d .. d + 3 of the segment's new rows' V.
+template <bool BF16, int KT>
+__device__ __noinline__ float4 nonfinite_seen(const AttnParams& p, const AttnSegment& s, int i, int d) {
+  float f[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < s.r.n; ++j) {
+    const int x = s.r.len + j;
+    if (x < s.t0 * KT || x >= (s.t0 + s.cnt) * KT || !row_sees(p, s.b, i, j)) continue;
+    const int64_t off = key_offset(p, s.r, x, key_word(p, s.r, s.b, x));
+    if (off < 0) continue;
+    const int64_t at = off + s.hkv * p.c.head_stride + d;
+    for (int k = 0; k < 4 && d + k < p.c.head_dim; ++k) {
+      const float v = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.c.v)[at + k]) << 16)
+                           : reinterpret_cast<const float*>(p.c.v)[at + k];
+      if (!(fabsf(v) < kInfF)) f[k] += v;
+    }
+  }
+  return make_float4(f[0], f[1], f[2], f[3]);
+}
+
+// ---------------------------------------------------------------------------------------------------------------------
 // Parts of a unit that several blocks share
 // ---------------------------------------------------------------------------------------------------------------------
 
@@ -335,7 +380,7 @@ __device__ __forceinline__ int attn_owner(const AttnSpan& sp, int64_t place) {
 }
 
 // After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
-// writes the rows.  T threads of which this is thread t; sync() is a barrier among them; s_last is shared.
+// writes the rows.  T threads, a warp or the block, of which this is thread t; s_last is shared.
 // Joins parts c0 .. c1 of a unit and writes its rows: E quads of columns a thread, PARTS parts in flight; a part's m, l
 // and O are fetched together, and the running maximum moves as they come.
 template <bool BF16, int MT, int DP, int T, int E, int PARTS>
@@ -391,11 +436,11 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, const AttnSe
   }
 }
 
-template <bool BF16, int MT, int DP, int T, class Sync>
-__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
-                                          int* s_last, Sync sync) {
+template <bool BF16, int MT, int DP, int T>
+__device__ __noinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
+                                       int* s_last) {
   __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
-  sync();
+  T == 32 ? __syncwarp() : __syncthreads();
   // the unit's blocks are those that own its first and its last tile
   const int c0 = attn_owner(sp, s.u0), c1 = attn_owner(sp, s.u0 + s.nt - 1);
   if (t == 0) {
@@ -403,7 +448,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
     if (last) p.tickets[c0] = 0u;
     *s_last = last ? 1 : 0;
   }
-  sync();
+  T == 32 ? __syncwarp() : __syncthreads();
   if (!*s_last) return;
   // few rows: one quad a thread and eight parts at a time; many: four quads and two parts
   const int live = min(MT, s.r.n * p.group - s.rt * MT);
@@ -418,7 +463,8 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
   }
 }
 
-// The tensor-memory kernel (bf16, head_dim <= 128).
+// bf16, head_dim <= 128: up to 16 rows a unit, and any number of rows on tensor memory.
+cudaError_t launch_attention_few(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_attention_wide(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace sv

@@ -1,0 +1,352 @@
+// Attention over the paged cache for few query rows (a decoded token's heads, a
+// short chain's): bf16, heads of up to 128, tiles of 16 rows and 128 keys.
+//
+// Bound by the bytes of K and V: of the 16 x 8 x 16 matrix instructions' rows
+// most are often empty, and their rate is still not what limits.  So the layout
+// serves the loads: the ring of sv_attention_ring.cuh runs ahead, four warps
+// take 32 keys of a tile each, with their own running (m, l, O) in registers,
+// and meet only at the end of a unit, where one of them joins the four (and, if
+// the unit is split over blocks, the blocks' parts) while the others go on.
+//
+//   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
+#include <cstdint>
+#include <mutex>
+
+#include "sv_attention_ring.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kTakers = 4;                                      // warps that take the tiles
+constexpr int kFewThreads = 32 * (kTakers + kLoadWarps + 2);    // and a warp each to plan, to load Q
+constexpr int kUnitPlaces = 1;                                  // what a unit costs beside its key tiles, in tiles
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DP>
+struct Few {
+  static constexpr int kRing = DP == 128 ? 6 : 12;  // tiles in the ring
+  using R = KvRing<DP, kRing>;
+  static constexpr int DT = DP / 8, KS = DP / 16;
+  static constexpr int kStage = (DT + 1) * 32 * 16;  // a warp's O, m and l
+  // shared memory: the ring; two Qs of 16 rows; two warps' results; the warps' flags; the meeting point; last
+  static constexpr int kQBlock = 2 * kRows * 128;
+  static constexpr int kQ = (R::kBytes + 1023) / 1024 * 1024;
+  static constexpr int kStages = kQ + kQBlock * (DP / 64);
+  static constexpr int kFlags = kStages + 2 * kStage;
+  static constexpr int kMeet = kFlags + kTakers * 8;
+  static constexpr int kSmem = kMeet + 16;
+};
+
+// What the products left out (see sv_attention.cuh), added by a warp to the rows that it has just written: to its part of
+// the unit, or, without one, to the output.
+template <int DP>
+__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, float* part) {
+  __syncwarp();
+  for (int x = threadIdx.x & 31; x < min(rows, kRows) * (DP / 4); x += 32) {
+    const int row = x / (DP / 4), d = x % (DP / 4) * 4, grow = s.rt * kRows + row, i = grow / p.group;
+    if (d >= p.c.head_dim) continue;
+    const float4 f = nonfinite_seen<true, kKeys>(p, s, i, d);
+    if (part) {
+      float4* at = reinterpret_cast<float4*>(part) + (d / 4) * kRows + row;
+      const float4 v = *at;
+      *at = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+    } else {
+      const int head = s.hkv * p.group + grow - i * p.group;
+      char* at = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head + d) * 2;
+      const uint2 u = *reinterpret_cast<const uint2*>(at);
+      store4<true>(at, make_float4(bf16_lo(u.x) + f.x, bf16_hi(u.x) + f.y, bf16_lo(u.y) + f.z, bf16_hi(u.y) + f.w));
+    }
+  }
+  __syncwarp();
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_attention_few(const AttnParams p, const __grid_constant__ KvMaps maps) {
+  using W = Few<DP>;
+  using R = typename W::R;
+  constexpr int DT = W::DT, KS = W::KS;
+  extern __shared__ __align__(1024) char smem[];
+  R ring(smem);
+  const uint32_t base = smem_addr(smem);
+  const uint32_t bar_meet = base + W::kMeet;
+  uint32_t* s_flags = reinterpret_cast<uint32_t*>(smem + W::kFlags);  // [kTakers][2]: keys outside the cache, careful
+  int* s_last = reinterpret_cast<int*>(smem + W::kMeet + 8);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t == 0) {
+    ring.init(kTakers, kTakers + kLoadWarps + 1, kTakers);
+    mbar_init(bar_meet, 32 * kTakers);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
+  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kFewThreads>(p, t, ring.sums(), ring.sums() + 22,
+                                                                          [] { __syncthreads(); });
+  if (warp == 8) {
+    ring.template plan<kRows, kUnitPlaces>(p, span);
+  } else if (warp == 9) {
+    ring.template load_q<kRows>(p, base + W::kQ, W::kQBlock, 2, kRows);
+  } else if (warp >= kTakers) {
+    ring.load(p, maps, warp - kTakers);
+  } else {
+    const int k0 = warp * 32;                 // this warp's keys of a tile
+    const int mi = lane >> 3, mr = lane & 7;  // matrix and row that this lane addresses for ldmatrix
+    uint32_t meets = 0, g = 0;
+    auto meet = [&] {  // a barrier of the taking warps, bounded like every wait
+      mbar_arrive(bar_meet);
+      return ring.wait(bar_meet, meets++ & 1);
+    };
+    auto done = [&](uint32_t bar) {  // this warp needs the buffer no more
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    AttnSegment s;
+    bool ok = true;
+    for (uint32_t unit = 0; ok && ring.next(s); ++unit) {
+      const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
+      const int slot = unit & 1;
+      if (!ring.wait(ring.q_bar(slot), unit >> 1 & 1)) break;
+      const int q_row = slot * kRows + (lane & 15);  // this lane's row of Q for ldmatrix
+      const uint32_t q_at = base + W::kQ + q_row * 128;
+      float m[2] = {-kInfF, -kInfF}, l[2] = {0.0f, 0.0f};
+      float o[DT][4];
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+      uint32_t bad = 0u;
+      bool careful = false;
+#pragma unroll 1
+      for (int i = 0; i < s.cnt; ++i, ++g) {
+        const int x0 = (s.t0 + i) * kKeys + k0;  // the warp's first key
+        if (!ring.wait(ring.full(2 * g), ring.phase(2 * g))) {
+          ok = false;
+          break;
+        }
+        const uint32_t good = ring.valid(g)[warp];
+        bad |= ring.valid(g)[4 + warp];
+        const uint32_t kt = ring.tile(2 * g);
+        float sc[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t qf[4];  // (Q stays in shared memory: O, the scores and Q do not fit the registers together)
+          ldmatrix4(q_at + (ks >> 2) * W::kQBlock + ((((ks & 3) * 2 + (lane >> 4)) ^ (q_row & 7)) << 4), qf);
+#pragma unroll
+          for (int n = 0; n < 4; n += 2) {
+            uint32_t kb[4];
+            ldmatrix4(kt + R::piece(k0 + n * 8 + (mi >> 1) * 8 + mr, ks * 2 + (mi & 1)), kb);
+            mma_bf16(sc[n], qf, kb[0], kb[1]);
+            mma_bf16(sc[n + 1], qf, kb[2], kb[3]);
+          }
+        }
+        done(ring.empty(2 * g));
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[n][c] *= p.scale_log2;
+        if (good != 0xffffffffu || x0 + 32 > s.r.len) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = (s.rt * kRows + (lane >> 2) + h * 8) / p.group;
+            const uint32_t see = row_sees_of(p, s.r, s.b, row, x0, good) >> ((lane & 3) * 2);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (!(see >> (n * 8 + c) & 1u)) sc[n][h * 2 + c] = -kInfF;
+          }
+        }
+        float alpha[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = m[h];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) mx = fmax_nan(mx, fmax_nan(sc[n][h * 2], sc[n][h * 2 + 1]));
+          mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float ref = mx == -kInfF ? 0.0f : mx;
+          alpha[h] = ex2_fast(m[h] - ref);
+          m[h] = mx;
+          l[h] *= alpha[h];
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float x = ex2_fast(sc[n][h * 2 + c] - ref);
+              sc[n][h * 2 + c] = x;
+              l[h] += x;
+            }
+        }
+        // O moves to the new maximum only when one of the warp's rows has a new one
+        if (__any_sync(0xffffffffu, !(alpha[0] == 1.0f && alpha[1] == 1.0f))) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[d][0] *= alpha[0], o[d][1] *= alpha[0];
+            o[d][2] *= alpha[1], o[d][3] *= alpha[1];
+          }
+        }
+        if (!ring.wait(ring.full(2 * g + 1), ring.phase(2 * g + 1))) {
+          ok = false;
+          break;
+        }
+        if (s.r.n > 1 && x0 + 32 > s.r.len) {
+          char* v = ring.tile_mem(2 * g + 1);
+          bool found = false;
+#pragma unroll 1
+          for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < 32 * R::kPieces; x += 32)
+            if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(k0 + x / R::kPieces, x % R::kPieces)))) found = true;
+          careful = __any_sync(0xffffffffu, found) || careful;
+        }
+        const uint32_t vt = ring.tile(2 * g + 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a[4] = {pack_bf16(sc[2 * j][0], sc[2 * j][1]), pack_bf16(sc[2 * j][2], sc[2 * j][3]),
+                                 pack_bf16(sc[2 * j + 1][0], sc[2 * j + 1][1]),
+                                 pack_bf16(sc[2 * j + 1][2], sc[2 * j + 1][3])};
+#pragma unroll
+          for (int d = 0; d < DT; d += 2) {
+            uint32_t vb[4];
+            ldmatrix4_trans(vt + R::piece(k0 + j * 16 + (mi & 1) * 8 + mr, d + (mi >> 1)), vb);
+            mma_bf16(o[d], a, vb[0], vb[1]);
+            mma_bf16(o[d + 1], a, vb[2], vb[3]);
+          }
+        }
+        done(ring.empty(2 * g + 1));
+      }
+      if (!ok) break;
+      done(ring.q_free(slot));
+
+      // The four warps' results, joined in two steps: 1 into 0 and 3 into 2, then 2 into 0.  A lane has the same rows and
+      // columns in every warp.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      }
+      if (lane == 0) s_flags[warp * 2] = bad, s_flags[warp * 2 + 1] = careful ? 1u : 0u;
+      float4* mine = reinterpret_cast<float4*>(smem + W::kStages + (warp >> 1) * W::kStage) + lane;
+      auto leave = [&](float4* to) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) to[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+        to[DT * 32] = make_float4(m[0], m[1], l[0], l[1]);
+      };
+      auto take = [&](const float4* from) {
+        const float4 x = from[DT * 32];
+        float wa[2], wb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mb = h ? x.y : x.x, N = fmax_nan(m[h], mb), ref = N == -kInfF ? 0.0f : N;
+          wa[h] = ex2_fast(m[h] - ref), wb[h] = ex2_fast(mb - ref);
+          m[h] = N;
+          l[h] = fmaf(l[h], wa[h], (h ? x.w : x.z) * wb[h]);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const float4 v = from[d * 32];
+          o[d][0] = fmaf(o[d][0], wa[0], v.x * wb[0]), o[d][1] = fmaf(o[d][1], wa[0], v.y * wb[0]);
+          o[d][2] = fmaf(o[d][2], wa[1], v.z * wb[1]), o[d][3] = fmaf(o[d][3], wa[1], v.w * wb[1]);
+        }
+      };
+      if (warp & 1) leave(mine);
+      if (!meet()) break;
+      if (!(warp & 1)) take(mine);
+      if (warp == 2) leave(mine);  // where warp 3's lay
+      if (!meet()) break;
+      if (warp == 0) {
+        take(reinterpret_cast<const float4*>(smem + W::kStages + W::kStage) + lane);
+        bad = (s_flags[0] | s_flags[2] | s_flags[4] | s_flags[6]) ? kStSlotRange : 0u;
+        bad |= s.r.status;
+        const bool whole = s.cnt == s.nt;
+        using P = AttnPart<kRows, DP>;
+        float* part = attn_part<kRows, DP>(p, blockIdx.x, s.t0 == 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = (lane >> 2) + h * 8, grow = s.rt * kRows + row;
+          if (row >= rows) continue;
+          if (whole) {
+            const int i = grow / p.group, head = s.hkv * p.group + grow - i * p.group;
+            const bool none = m[h] == -kInfF;  // nothing seen, or only scores of -inf
+            const float inv = none ? 0.0f : 1.0f / l[h];
+            char* out = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head + (lane & 3) * 2) * 2;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+              if (d * 8 < p.c.head_dim)
+                *reinterpret_cast<uint32_t*>(out + d * 16) = none ? 0u : pack_bf16(o[d][h * 2] * inv, o[d][h * 2 + 1] * inv);
+            if ((lane & 3) == 0 && p.lse) p.lse[(s.r.row0 + i) * p.heads + head] = none ? -kInfF : fmaf(m[h], kLn2, logf(l[h]));
+          } else {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)  // quads of columns, a quad by two lanes
+              *reinterpret_cast<float2*>(part + ((d * 2 + (lane >> 1 & 1)) * kRows + row) * 4 + (lane & 1) * 2) =
+                  make_float2(o[d][h * 2], o[d][h * 2 + 1]);
+            if ((lane & 3) == 0) part[P::kM + row] = m[h], part[P::kL + row] = l[h];
+          }
+        }
+        if (s_flags[1] | s_flags[3] | s_flags[5] | s_flags[7]) {
+          const AttnSegment copy = s;
+          add_nonfinite<DP>(p, copy, rows, whole ? nullptr : part);
+        }
+        if (whole) {
+          if (s.reports && lane == 0) p.status[s.b] = bad | attn_timeout(p);
+        } else {
+          if (lane == 0) part[P::kStatus] = __uint_as_float(bad);
+          const AttnSegment copy = s;
+          const AttnSpan span_copy = span;
+          attn_join<true, kRows, DP, 32>(p, span_copy, copy, lane, s_last);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  ring.report_abort(p);
+}
+
+template <int DP>
+cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool have[64] = {};
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return e;
+  if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!have[d]) {
+      e = cudaFuncSetAttribute(k_attention_few<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<DP>::kSmem);
+      if (e != cudaSuccess) return e;
+      have[d] = true;
+    }
+  }
+  static_assert(Few<DP>::kSmem <= 227 * 1024, "shared memory of a block");
+  const int grid = dev.sms < kAttnMaxBlocks ? dev.sms : kAttnMaxBlocks;
+  return launch_pdl(k_attention_few<DP>, dim3(static_cast<unsigned>(grid)), dim3(kFewThreads), Few<DP>::kSmem, stream, p,
+                    kv_maps(p.c));
+}
+
+}  // namespace
+
+cudaError_t launch_attention_few(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  return p.c.head_dim <= 64 ? launch<64>(p, dev, stream) : launch<128>(p, dev, stream);
+}
+
+}  // namespace sv
