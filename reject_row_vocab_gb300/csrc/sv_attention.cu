@@ -503,9 +503,7 @@ __global__ void __launch_bounds__(E::THREADS) k_attention(AttnParams p) {
       }
       for (int row = t; row < MT; row += T) part[P::kM + row] = s_m[row], part[P::kL + row] = s_l[row];
       if (t == 0) part[P::kStatus] = __uint_as_float(bad);
-      const AttnSegment copy = s;
-      const AttnSpan span_copy = span;
-      attn_join<E::kBf16, MT, DP, T>(p, span_copy, copy, t, &s_last);
+      attn_join<E::kBf16, MT, DP, T>(p, span, s, t, &s_last);
     }
     __syncthreads();  // the ring and the offsets are free again
   }

@@ -183,10 +183,11 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
 
 // Computed by every block for itself, by T threads of which this is thread t; sync() is a barrier among them.  One
 // scan over the first T requests gives the total and finds the start; only larger batches are gone through again.
-// s_sum [2 T / 32] and s_find [2] are shared.
+// s_sum [2 T / 32] (32 at most) and s_find [2] are shared.
 template <int MT, int KT, int U, int T, class Sync>
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_t* s_sum, int64_t* s_find, Sync sync) {
   constexpr int W = T / 32;
+  static_assert(W <= 16, "s_sum");
   const int lane = t & 31, warp = t >> 5;
   AttnSpan sp{};
   int64_t own = 0, rest = 0;
@@ -437,8 +438,8 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, const AttnSe
 }
 
 template <bool BF16, int MT, int DP, int T>
-__device__ __noinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
-                                       int* s_last) {
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
+                                          int* s_last) {
   __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
   T == 32 ? __syncwarp() : __syncthreads();
   // the unit's blocks are those that own its first and its last tile

@@ -3,10 +3,11 @@
 //
 // Bound by the bytes of K and V: of the 16 x 8 x 16 matrix instructions' rows
 // most are often empty, and their rate is still not what limits.  So the layout
-// serves the loads: the ring of sv_attention_ring.cuh runs ahead, four warps
-// take 32 keys of a tile each, with their own running (m, l, O) in registers,
-// and meet only at the end of a unit, where one of them joins the four (and, if
-// the unit is split over blocks, the blocks' parts) while the others go on.
+// serves the loads: the ring of sv_attention_ring.cuh runs ahead, eight warps
+// take 16 keys of a tile each, with their own running (m, l, O) in registers,
+// and meet only at the end of a unit, where they join by halves, and the first
+// of them writes the rows while the others go on.  If a unit is split over
+// blocks, the planning warp joins the blocks' parts.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>
@@ -18,7 +19,7 @@ namespace sv {
 namespace {
 
 constexpr int kRows = 16;
-constexpr int kTakers = 4;                                      // warps that take the tiles
+constexpr int kTakers = 8;                                      // warps that take the tiles
 constexpr int kFewThreads = 32 * (kTakers + kLoadWarps + 2);    // and a warp each to plan, to load Q
 constexpr int kUnitPlaces = 1;                                  // what a unit costs beside its key tiles, in tiles
 
@@ -44,17 +45,18 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 template <int DP>
 struct Few {
-  static constexpr int kRing = DP == 128 ? 6 : 12;  // tiles in the ring
+  static constexpr int kRing = DP == 128 ? 5 : 10;  // tiles in the ring
   using R = KvRing<DP, kRing>;
   static constexpr int DT = DP / 8, KS = DP / 16;
   static constexpr int kStage = (DT + 1) * 32 * 16;  // a warp's O, m and l
-  // shared memory: the ring; two Qs of 16 rows; two warps' results; the warps' flags; the meeting point; last
+  // shared memory: the ring; two Qs of 16 rows; half the warps' results; the warps' flags; the meeting point; last; split segments
   static constexpr int kQBlock = 2 * kRows * 128;
   static constexpr int kQ = (R::kBytes + 1023) / 1024 * 1024;
   static constexpr int kStages = kQ + kQBlock * (DP / 64);
-  static constexpr int kFlags = kStages + 2 * kStage;
-  static constexpr int kMeet = kFlags + kTakers * 8;
-  static constexpr int kSmem = kMeet + 16;
+  static constexpr int kFlags = kStages + kTakers / 2 * kStage;
+  static constexpr int kMeet = kFlags + 2 * kTakers * 8;
+  static constexpr int kParts = kMeet + 4 * 8;  // (behind two barriers, one for each part)
+  static constexpr int kSmem = kParts + 2 * static_cast<int>(sizeof(AttnSegment));
 };
 
 // What the products left out (see sv_attention.cuh), added by a warp to the rows that it has just written: to its part of
@@ -90,29 +92,41 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   R ring(smem);
   const uint32_t base = smem_addr(smem);
   const uint32_t bar_meet = base + W::kMeet;
-  uint32_t* s_flags = reinterpret_cast<uint32_t*>(smem + W::kFlags);  // [kTakers][2]: keys outside the cache, careful
+  uint32_t* s_flags = reinterpret_cast<uint32_t*>(smem + W::kFlags);  // [2][kTakers][2], by turns: keys outside the cache, careful
+  AttnSegment* s_parts = reinterpret_cast<AttnSegment*>(smem + W::kParts);
+  const uint32_t bar_part = base + W::kMeet + 16;
   int* s_last = reinterpret_cast<int*>(smem + W::kMeet + 8);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
     ring.init(kTakers, kTakers + kLoadWarps + 1, kTakers);
     mbar_init(bar_meet, 32 * kTakers);
+    for (int i = 0; i < 2; ++i) mbar_init(bar_part + i * 8, 1);
     mbar_fence_init();
   }
   __syncthreads();
   grid_dependency_wait();
   allow_dependents();
-  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kFewThreads>(p, t, ring.sums(), ring.sums() + 22,
+  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kFewThreads>(p, t, ring.sums(), ring.find(),
                                                                           [] { __syncthreads(); });
-  if (warp == 8) {
-    ring.template plan<kRows, kUnitPlaces>(p, span);
-  } else if (warp == 9) {
+  if (warp == kTakers + kLoadWarps) {
+    // The plan; then, when the parts that this block leaves of units are written, the join of the units that it ends.
+    const int split = ring.template plan<kRows, kUnitPlaces>(p, span, s_parts);
+#pragma unroll 1
+    for (int i = 0; i < split; ++i) {
+      if (!ring.wait(bar_part + i * 8, 0)) break;
+      attn_join<true, kRows, DP, 32>(p, span, s_parts[i], lane, s_last);
+    }
+  } else if (warp == kTakers + kLoadWarps + 1) {
     ring.template load_q<kRows>(p, base + W::kQ, W::kQBlock, 2, kRows);
   } else if (warp >= kTakers) {
     ring.load(p, maps, warp - kTakers);
   } else {
-    const int k0 = warp * 32;                 // this warp's keys of a tile
-    const int mi = lane >> 3, mr = lane & 7;  // matrix and row that this lane addresses for ldmatrix
-    uint32_t meets = 0, g = 0;
+    const int k0 = warp * 16;                 // this warp's keys of a tile
+    // What this lane addresses for ldmatrix within a tile (piece(row, column)): the pieces of a row further on differ from
+    // it in bits 5 and 6 of the address, or by a block.
+    const int mi = lane >> 3, mr = lane & 7;  // matrix and row
+    const uint32_t k_at = R::piece(k0 + (mi >> 1) * 8 + mr, mi & 1), v_at = R::piece(k0 + (mi & 1) * 8 + mr, mi >> 1);
+    uint32_t meets = 0, g = 0, left = 0;  // left: parts written
     auto meet = [&] {  // a barrier of the taking warps, bounded like every wait
       mbar_arrive(bar_meet);
       return ring.wait(bar_meet, meets++ & 1);
@@ -121,14 +135,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    AttnSegment s;
     bool ok = true;
-    for (uint32_t unit = 0; ok && ring.next(s); ++unit) {
+    for (uint32_t unit = 0; ok; ++unit) {
+      const AttnSegment* const seg = ring.peek();
+      if (!seg) break;
+      const AttnSegment& s = *seg;
       const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
       const int slot = unit & 1;
       if (!ring.wait(ring.q_bar(slot), unit >> 1 & 1)) break;
       const int q_row = slot * kRows + (lane & 15);  // this lane's row of Q for ldmatrix
-      const uint32_t q_at = base + W::kQ + q_row * 128;
+      const uint32_t q_at = base + W::kQ + q_row * 128 + (((lane >> 4) ^ (q_row & 7)) << 4);
       float m[2] = {-kInfF, -kInfF}, l[2] = {0.0f, 0.0f};
       float o[DT][4];
 #pragma unroll
@@ -142,36 +158,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t good = ring.valid(g)[warp];
-        bad |= ring.valid(g)[4 + warp];
-        const uint32_t kt = ring.tile(2 * g);
-        float sc[4][4];
+        const uint32_t good = ring.valid(g)[warp / 2] >> (k0 & 16) & 0xffffu;
+        bad |= ring.valid(g)[4 + warp / 2];
+        const uint32_t kt = ring.tile(2 * g) + k_at;
+        float sc[2][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+        for (int n = 0; n < 2; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t qf[4];  // (Q stays in shared memory: O, the scores and Q do not fit the registers together)
-          ldmatrix4(q_at + (ks >> 2) * W::kQBlock + ((((ks & 3) * 2 + (lane >> 4)) ^ (q_row & 7)) << 4), qf);
-#pragma unroll
-          for (int n = 0; n < 4; n += 2) {
-            uint32_t kb[4];
-            ldmatrix4(kt + R::piece(k0 + n * 8 + (mi >> 1) * 8 + mr, ks * 2 + (mi & 1)), kb);
-            mma_bf16(sc[n], qf, kb[0], kb[1]);
-            mma_bf16(sc[n + 1], qf, kb[2], kb[3]);
-          }
+          ldmatrix4((q_at ^ (ks & 3) << 5) + (ks >> 2) * W::kQBlock, qf);
+          uint32_t kb[4];
+          ldmatrix4((kt ^ (ks & 3) << 5) + (ks >> 2) * R::kBlock, kb);
+          mma_bf16(sc[0], qf, kb[0], kb[1]);
+          mma_bf16(sc[1], qf, kb[2], kb[3]);
         }
         done(ring.empty(2 * g));
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[n][c] *= p.scale_log2;
-        if (good != 0xffffffffu || x0 + 32 > s.r.len) {
+        if (good != 0xffffu || x0 + 16 > s.r.len) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int row = (s.rt * kRows + (lane >> 2) + h * 8) / p.group;
             const uint32_t see = row_sees_of(p, s.r, s.b, row, x0, good) >> ((lane & 3) * 2);
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c)
                 if (!(see >> (n * 8 + c) & 1u)) sc[n][h * 2 + c] = -kInfF;
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int h = 0; h < 2; ++h) {
           float mx = m[h];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) mx = fmax_nan(mx, fmax_nan(sc[n][h * 2], sc[n][h * 2 + 1]));
+          for (int n = 0; n < 2; ++n) mx = fmax_nan(mx, fmax_nan(sc[n][h * 2], sc[n][h * 2 + 1]));
           mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float ref = mx == -kInfF ? 0.0f : mx;
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           m[h] = mx;
           l[h] *= alpha[h];
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float x = ex2_fast(sc[n][h * 2 + c] - ref);
@@ -210,42 +223,39 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           ok = false;
           break;
         }
-        if (s.r.n > 1 && x0 + 32 > s.r.len) {
+        if (s.r.n > 1 && x0 + 16 > s.r.len) {
           char* v = ring.tile_mem(2 * g + 1);
           bool found = false;
 #pragma unroll 1
-          for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < 32 * R::kPieces; x += 32)
+          for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < 16 * R::kPieces; x += 32)
             if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(k0 + x / R::kPieces, x % R::kPieces)))) found = true;
           careful = __any_sync(0xffffffffu, found) || careful;
         }
-        const uint32_t vt = ring.tile(2 * g + 1);
+        const uint32_t vt = ring.tile(2 * g + 1) + v_at;
+        const uint32_t a[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
+                               pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t a[4] = {pack_bf16(sc[2 * j][0], sc[2 * j][1]), pack_bf16(sc[2 * j][2], sc[2 * j][3]),
-                                 pack_bf16(sc[2 * j + 1][0], sc[2 * j + 1][1]),
-                                 pack_bf16(sc[2 * j + 1][2], sc[2 * j + 1][3])};
-#pragma unroll
-          for (int d = 0; d < DT; d += 2) {
-            uint32_t vb[4];
-            ldmatrix4_trans(vt + R::piece(k0 + j * 16 + (mi & 1) * 8 + mr, d + (mi >> 1)), vb);
-            mma_bf16(o[d], a, vb[0], vb[1]);
-            mma_bf16(o[d + 1], a, vb[2], vb[3]);
-          }
+        for (int d = 0; d < DT; d += 2) {
+          uint32_t vb[4];
+          ldmatrix4_trans((vt ^ (d & 6) << 4) + (d >> 3) * R::kBlock, vb);
+          mma_bf16(o[d], a, vb[0], vb[1]);
+          mma_bf16(o[d + 1], a, vb[2], vb[3]);
         }
         done(ring.empty(2 * g + 1));
       }
       if (!ok) break;
       done(ring.q_free(slot));
 
-      // The four warps' results, joined in two steps: 1 into 0 and 3 into 2, then 2 into 0.  A lane has the same rows and
-      // columns in every warp.
+      // The warps' results, joined by halves: warp w + h into warp w for h = 4, 2, 1.  A lane has the same rows and columns
+      // in every warp.  (What h leaves lies where no warp of the step before reads: the steps meet in between.)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       }
-      if (lane == 0) s_flags[warp * 2] = bad, s_flags[warp * 2 + 1] = careful ? 1u : 0u;
-      float4* mine = reinterpret_cast<float4*>(smem + W::kStages + (warp >> 1) * W::kStage) + lane;
+      uint32_t* const flags = s_flags + slot * kTakers * 2;
+      if (lane == 0) flags[warp * 2] = bad, flags[warp * 2 + 1] = careful ? 1u : 0u;
+      auto stage = [&](int i) { return reinterpret_cast<float4*>(smem + W::kStages + i * W::kStage) + lane; };
       auto leave = [&](float4* to) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) to[d * 32] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
@@ -268,15 +278,22 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           o[d][2] = fmaf(o[d][2], wa[1], v.z * wb[1]), o[d][3] = fmaf(o[d][3], wa[1], v.w * wb[1]);
         }
       };
-      if (warp & 1) leave(mine);
-      if (!meet()) break;
-      if (!(warp & 1)) take(mine);
-      if (warp == 2) leave(mine);  // where warp 3's lay
-      if (!meet()) break;
+      ok = true;
+#pragma unroll 1
+      for (int h = kTakers / 2; h > 0; h /= 2) {
+        if (warp >= h && warp < 2 * h) leave(stage(warp - h));
+        ok = meet();
+        if (!ok) break;
+        if (warp < h) take(stage(warp));
+        ok = meet();
+        if (!ok) break;
+      }
+      if (!ok) break;
       if (warp == 0) {
-        take(reinterpret_cast<const float4*>(smem + W::kStages + W::kStage) + lane);
-        bad = (s_flags[0] | s_flags[2] | s_flags[4] | s_flags[6]) ? kStSlotRange : 0u;
-        bad |= s.r.status;
+        uint32_t any = 0u, odd = 0u;
+#pragma unroll
+        for (int w = 0; w < kTakers; ++w) any |= flags[w * 2], odd |= flags[w * 2 + 1];
+        bad = (any ? kStSlotRange : 0u) | s.r.status;
         const bool whole = s.cnt == s.nt;
         using P = AttnPart<kRows, DP>;
         float* part = attn_part<kRows, DP>(p, blockIdx.x, s.t0 == 0);
@@ -302,19 +319,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if ((lane & 3) == 0) part[P::kM + row] = m[h], part[P::kL + row] = l[h];
           }
         }
-        if (s_flags[1] | s_flags[3] | s_flags[5] | s_flags[7]) {
-          const AttnSegment copy = s;
-          add_nonfinite<DP>(p, copy, rows, whole ? nullptr : part);
+        if (odd) {
+          add_nonfinite<DP>(p, s, rows, whole ? nullptr : part);
         }
         if (whole) {
           if (s.reports && lane == 0) p.status[s.b] = bad | attn_timeout(p);
         } else {
           if (lane == 0) part[P::kStatus] = __uint_as_float(bad);
-          const AttnSegment copy = s;
-          const AttnSpan span_copy = span;
-          attn_join<true, kRows, DP, 32>(p, span_copy, copy, lane, s_last);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_part + left++ * 8);
         }
       }
+      ring.release();
     }
   }
   __syncthreads();

@@ -45,7 +45,7 @@ __device__ __forceinline__ void box_copy(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// As mbar_try_wait, the thread suspended for up to about `ns`.
+// As mbar_try_wait, the thread suspended for up to about `ns`: warps that poll take issue slots from those that work.
 __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
   asm volatile(
@@ -58,11 +58,9 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
-// The rest of a wait that did not end at once.  Suspended meanwhile: warps that poll take issue slots from those that
-// work.  (Out of line, like all that seldom runs: what the roles run by turns has to stay in the instruction cache.)
+// The rest of a wait that is long.  (Out of line, like all that seldom runs: what the roles run by turns has to stay in the
+// instruction cache.)
 static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait_for(bar, parity, 10000)) return true;
   if (mbar_wait_bounded(bar, parity, abort, kWaitNs)) return true;
   *abort = 1;
   return false;
@@ -84,8 +82,8 @@ struct KvRing {
   static constexpr int kPlan = kValid + kInfo * 8 * 4;           // AttnSegment [kPlans]
   static constexpr int kBars = kPlan + kPlans * static_cast<int>(sizeof(AttnSegment));
   // full, empty [NB], plan, read [kPlans], q, q free [2]
-  static constexpr int kSums = kBars + (2 * NB + 2 * kPlans + 4) * 8;  // int64 [24]: sums [22], find [2]
-  static constexpr int kAbort = kSums + 24 * 8;
+  static constexpr int kSums = kBars + (2 * NB + 2 * kPlans + 4) * 8;  // int64 [34]: sums [32], find [2]
+  static constexpr int kAbort = kSums + 34 * 8;
   static constexpr int kBytes = kAbort + 16;
 
   char* mem;       // of the ring
@@ -106,6 +104,7 @@ struct KvRing {
   __device__ char* tile_mem(uint32_t group) const { return mem + group % NB * kTile; }
   __device__ uint32_t* valid(uint32_t g) const { return reinterpret_cast<uint32_t*>(mem + kValid) + g % kInfo * 8; }
   __device__ AttnSegment* plan_slot(uint32_t i) const { return reinterpret_cast<AttnSegment*>(mem + kPlan) + i % kPlans; }
+  __device__ int64_t* find() const { return sums() + 32; }
   __device__ int64_t* sums() const { return reinterpret_cast<int64_t*>(mem + kSums); }
   __device__ volatile int* abort() const { return reinterpret_cast<volatile int*>(mem + kAbort); }
   // 16-byte piece c of row r of a tile
@@ -123,7 +122,11 @@ struct KvRing {
 
   // A wait that gives up ends every role; the lanes of a warp leave together.
   __device__ bool wait_one(uint32_t bar, uint32_t parity) const {
-    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort());
+    // (the call is the last resort: registers are saved around it)
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_for(bar, parity, 10000)) return true;
+    return wait_on(bar, parity, abort());
   }
   __device__ bool wait(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; }
 
@@ -139,21 +142,37 @@ struct KvRing {
     return s.cnt > 0;
   }
 
-  // The planning warp: the block's segments in order; one without tiles ends them.
+  // The same, left in the plan until release() (for warps that have no registers to keep it in).
+  __device__ const AttnSegment* peek() const {
+    if (!wait(plan_bar(plans), plans / kPlans & 1)) return nullptr;
+    const AttnSegment* s = plan_slot(plans);
+    return s->cnt > 0 ? s : nullptr;
+  }
+  __device__ void release() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(read_bar(plans));
+    ++plans;
+  }
+
+  // The planning warp: the block's segments in order; one without tiles ends them.  Segments that are only part of their
+  // unit (two at most) are put down in `parts` too; their number is returned to every lane.
   template <int MT, int U>
-  __device__ void plan(const AttnParams& p, const AttnSpan& span) {
+  __device__ int plan(const AttnParams& p, const AttnSpan& span, AttnSegment* parts = nullptr) {
+    int split = 0;
     if (lane == 0) {
       AttnWalk<MT, kKeys, U> walk(p, span);
       AttnSegment s{};
       for (bool more = true; more; ++plans) {
         more = walk.next(s);
         if (!more) s.cnt = 0;
+        if (parts && more && s.cnt < s.nt) parts[split++] = s;
         if (plans >= kPlans && !wait_one(read_bar(plans), (plans / kPlans - 1) & 1)) break;
         *plan_slot(plans) = s;
         mbar_arrive(plan_bar(plans));
       }
     }
     __syncwarp();
+    return __shfl_sync(0xffffffffu, split, 0);
   }
 
   // Loading warp lw.  A warp has 32 of a tile's keys, a lane one key's place, handed round by shuffles; the word that

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
   grid_dependency_wait();
   allow_dependents();
-  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kWideThreads>(p, t, ring.sums(), ring.sums() + 22,
+  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kWideThreads>(p, t, ring.sums(), ring.find(),
                                                                            [] { __syncthreads(); });
 
   if (warp == 10) {
