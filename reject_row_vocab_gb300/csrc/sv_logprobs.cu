@@ -7,13 +7,16 @@
 // One pass: each thread keeps a running (m, s, w) of the elements it has read
 // and rescales it when its maximum grows; a block joins its threads' triples,
 // and the last block of a row joins the blocks' in block order, so results do
-// not depend on the order the blocks finish in.
+// not depend on the order the blocks finish in.  Bound by the instructions: an
+// exponential and about three and a half other issues an element.
 //
 // Top alternatives from the same pass: a thread's running maximum is the
 // largest of its own elements, so the top_k-th largest of the block's thread
-// maxima is a lower bound on the block's top_k-th element.  Only threads whose
-// maximum reaches the bound (about top_k of 256) can hold a top element, and
-// only their elements are looked at again (from L2), by whole warps.  Elements
+// maxima is a lower bound on the block's top_k-th element.  Only batches whose
+// largest logit reaches the bound (about top_k of some thousands; their maxima
+// are put down as they pass) can hold a top element, and only they are read
+// again: all elements of the threads that reach it, 8 percent of the row, cost
+// as much as a fifth of the pass.  Elements
 // are ordered by a 64-bit key - value, then the lower index - so the selection
 // is unique whatever the order of the candidates.
 //
@@ -25,6 +28,7 @@
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cfloat>
 #include <cstdint>
+#include <mutex>
 
 #include "sv_device.cuh"
 #include "sv_internal.h"
@@ -36,10 +40,11 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 64;
 constexpr int kMaxGiven = 1024;
-constexpr int kMaxSplits = 32;
-constexpr int kMaxSplitRows = 1024;           // rows are split only below this many (see row_splits)
-constexpr int kMaxParts = 2 * kMaxSplitRows;  // parts of a call with split rows
+constexpr int kMaxBlocks = 1280;    // of the forward kernel (the workspace is laid out for them)
+constexpr int kMinVectors = 1024;   // 16-byte vectors that a block takes at least
 constexpr int kCandCap = 1024;  // candidates a block sorts in shared memory
+constexpr int kBatch = 4;       // vectors that a thread reads at once
+constexpr int kPeaks = 32;      // groups of batches whose largest logits are kept
 constexpr float kLn2 = 0.693147180559945309417f;
 
 // A logits vector: 16 bytes as floats.
@@ -61,6 +66,19 @@ struct Vec<false> {
   }
 };
 
+// The largest of a vector's logits that are numbers.
+template <bool BF16>
+__device__ __forceinline__ float largest(const uint4& u) {
+  if (BF16) {
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(u.x), "r"(u.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(u.z), "r"(u.w));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return fmaxf(bf16_lo(a), bf16_hi(a));
+  }
+  return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+
 // Order-preserving whole number of a float (-0 as 0); 0 stands for "no element" (-inf and unusable logits).
 __device__ __forceinline__ uint32_t ordered(float x) {
   if (!usable_logit(x) || x == -kInfF) return 0u;
@@ -75,7 +93,7 @@ __device__ __forceinline__ uint64_t top_key(float x, int32_t idx) {
   return o == 0u ? 0ull : (static_cast<uint64_t>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(idx));
 }
 
-// Running sums of a thread, block or row: s = sum 2^((l - m) k), w = sum (l - m) 2^((l - m) k).
+// Running sums of a thread, block or row against a reference m, with t = (l - m) k: s = sum 2^t, w = sum t 2^t.
 struct Run {
   float m, s, w;
 };
@@ -87,16 +105,16 @@ __device__ __forceinline__ void run_merge(Run& a, const Run& b, float k) {
     return;
   }
   const float M = fmaxf(a.m, b.m);
-  const float da = a.m - M, db = b.m - M;
-  const float ea = ex2_fast(da * k), eb = ex2_fast(db * k);
-  // a term that vanished has sums that vanish with it (0 * a large distance is 0, not a stray product)
-  a.w = (ea > 0.0f ? ea * (a.w + a.s * da) : 0.0f) + (eb > 0.0f ? eb * (b.w + b.s * db) : 0.0f);
+  const float da = (a.m - M) * k, db = (b.m - M) * k;
+  const float ea = ex2_fast(da), eb = ex2_fast(db);
+  // a term that vanished has sums that vanish with it (0 times a large distance is 0, not a stray product)
+  a.w = (ea > 0.0f ? ea * fmaf(a.s, da, a.w) : 0.0f) + (eb > 0.0f ? eb * fmaf(b.s, db, b.w) : 0.0f);
   a.s = ea * a.s + eb * b.s;
   a.m = M;
 }
 
-// log2(e) / T; the unscaled distribution for a greedy temperature.  Held at 1e-30 at least: below that every finite
-// logit of ordinary size has the same weight, and a masked entry's distance still has to end in a weight of zero.
+// log2(e) / T, of the unscaled distribution for a greedy temperature.  Held at 1e-30 at least: there every finite logit of
+// ordinary size has the same weight, and a masked entry's distance still has to end in a weight of zero.
 __device__ __forceinline__ float logprob_temperature(const float* row_temp, int64_t i) {
   const float T = row_temp ? row_temp[i] : 1.0f;
   return sampling_temperature(T) ? T : 1.0f;
@@ -119,11 +137,11 @@ struct LogprobParams {
   int32_t* top_ids;
   float* top_logprob;
   uint32_t* flags;
-  int32_t splits;
-  uint32_t* tickets;  // [n], zero between calls
-  Run* part;          // [n, splits]
+  uint32_t* tickets;  // [kMaxBlocks], zero between calls
+  Run* part;          // [kMaxBlocks][2]
   uint32_t* part_flags;
-  uint64_t* part_top;  // [n, splits, top_k]
+  uint64_t* part_top;  // [kMaxBlocks][2][top_k]
+  int64_t min_vectors;  // that a block takes
 };
 
 template <bool BF16>
@@ -143,6 +161,44 @@ __device__ __forceinline__ void run_add(Run& r, float x, float k, uint32_t& flag
   run_merge(r, Run{x, 1.0f, 0.0f}, k);
 }
 
+// A thread's running sums while it streams, against a reference: weights are 2^(l k - c) with c = ref k as rounded, one
+// multiply-add an element; settle() makes up for the rounding, which is the same for all of them.  The reference is the
+// largest logit of the warp's first vectors, and moves only when a logit passes it by 64 log2 units (2^64 times a row's
+// length is far from fp32's end): moving it at every new maximum made up two thirds of the instructions.  Logits below
+// `low` are read as `low`, which has a weight of 0 just as well: their exponent stays finite, and 0 times it is 0.
+template <bool BF16>
+struct Stream {
+  Run r{-kInfF, 0.0f, 0.0f};  // what has been settled
+  float ref = -kInfF, c = 0.0f, low = -kInfF, limit = -kInfF;  // the same in all lanes of a warp
+  uint32_t low2 = 0xff80ff80u;
+  float2 s2{0.0f, 0.0f}, w2{0.0f, 0.0f};
+
+  __device__ __forceinline__ bool packed() const { return fabsf(c) < 1e37f; }  // (a huge logit may have no room)
+
+  __device__ __forceinline__ void settle(float k) {
+    if (ref == -kInfF || !packed()) return;
+    const float off = fmaf(ref, -k, c);  // c - ref k, exactly: 2^(l k - c) 2^off = 2^t and t = (l k - c) + off
+    const float e = ex2_fast(off), s = s2.x + s2.y, w = w2.x + w2.y;
+    run_merge(r, Run{ref, e * s, e * fmaf(s, off, w)}, k);
+    s2 = w2 = make_float2(0.0f, 0.0f);
+  }
+  __device__ __forceinline__ void rise(float to, float k, float unit) {  // a larger reference; unit: 1 / k
+    settle(k);
+    ref = to;
+    c = ref * k;
+    low = fmaf(-300.0f, unit, ref);
+    limit = fmaf(64.0f, unit, ref);
+    if (BF16) {  // low, rounded down
+      uint32_t b = __float_as_uint(low);
+      if (low < 0.0f && (b & 0xffffu)) b += 0x10000u;
+      b >>= 16;
+      low2 = b | b << 16;
+      low = bf16_hi(low2);
+    }
+    if (low == -kInfF) c = kInfF;  // nothing left to read -inf as: element by element
+  }
+};
+
 // The top_k largest of the n keys in `cand` (unique, in any order), sorted into `out` (top_k entries, 0 = none).
 __device__ __forceinline__ void rank_top(const uint64_t* cand, int n, int top_k, uint64_t* out) {
   for (int i = threadIdx.x; i < top_k; i += kLpThreads) out[i] = 0ull;
@@ -156,252 +212,162 @@ __device__ __forceinline__ void rank_top(const uint64_t* cand, int n, int top_k,
   __syncthreads();
 }
 
+// Shared memory of a block.
+struct LogprobShared {
+  Run run[kLpWarps];
+  float max[kLpWarps];
+  uint64_t cand[kCandCap];
+  uint64_t top[kMaxTop];
+  uint64_t key[kLpWarps];
+  alignas(16) uint16_t level[kLpThreads];
+  uint16_t peak[kPeaks][kLpThreads];  // the largest logit of each thread's groups of batches, as 16-bit bounds
+  uint16_t who[kCandCap];             // groups that may hold a top element: thread + 256 group
+  int64_t sums[kLpWarps];
+  int64_t find[2];
+  uint32_t flags, found, last, owners, bound;
+};
+
+// The top_k keys of vectors [lo, hi) of a row (and of its ragged end, tails elements from tail0) into sh.top, given each
+// thread's largest logit of its own vectors lo + t, lo + t + 256, ... (and the end), and sh.peak, where a group is
+// `batches` batches of kBatch of them.
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads) k_token_logprobs(LogprobParams p) {
+__device__ __noinline__ void select_top(const LogprobParams& p, LogprobShared& sh, int64_t row, int lo, int hi, int tail0,
+                                        int tails, float mine_max, int batches) {
   constexpr int N = Vec<BF16>::N;
-  constexpr int U = 4;  // vectors in flight a thread
-  __shared__ Run s_run[kLpWarps];
-  __shared__ uint32_t s_flags, s_count, s_last;
-  __shared__ uint64_t s_cand[kCandCap];
-  __shared__ uint64_t s_top[kMaxTop];
-  __shared__ uint64_t s_key[kLpWarps];
-  __shared__ uint16_t s_who[kLpThreads];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int64_t i = blockIdx.x / p.splits;
-  const int split = static_cast<int>(blockIdx.x - i * p.splits);
-  grid_dependency_wait();
-  allow_dependents();
-  int64_t row = p.row_index ? p.row_index[i] : i;
-  if (row < 0 || row >= p.lg.rows) {  // padding
-    if (split != 0) return;
-    for (int j = t; j < p.num_ids; j += kLpThreads) p.logprob[i * p.num_ids + j] = 0.0f;
-    for (int j = t; j < p.top_k; j += kLpThreads) {
-      p.top_ids[i * p.top_k + j] = -1;
-      p.top_logprob[i * p.top_k + j] = -kInfF;
+  const uint4* vec = reinterpret_cast<const uint4*>(static_cast<const char*>(p.lg.base) + row * p.lg.ld * (BF16 ? 2 : 4));
+  // The largest 16-bit bound that top_k threads' maxima reach, found bit by bit by one warp.
+  const uint32_t mine = ordered(mine_max) >> 16;
+  sh.level[t] = static_cast<uint16_t>(mine);
+  if (t == 0) sh.found = 0u, sh.owners = 0u;
+  __syncthreads();
+  if (warp == 0) {
+    const uint4 x = reinterpret_cast<const uint4*>(sh.level)[lane];
+    const uint32_t v[8] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16,
+                           x.z & 0xffffu, x.z >> 16, x.w & 0xffffu, x.w >> 16};
+    uint32_t thr = 0u;
+#pragma unroll 1
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t to = thr | 1u << bit;
+      uint32_t n = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n += v[e] >= to ? 1u : 0u;
+      if (__reduce_add_sync(0xffffffffu, n) >= static_cast<uint32_t>(p.top_k)) thr = to;
     }
-    if (t == 0) {
-      if (p.entropy) p.entropy[i] = 0.0f;
-      if (p.row_max) p.row_max[i] = -kInfF;
-      if (p.log_z) p.log_z[i] = 0.0f;
-      if (p.flags) p.flags[i] = row == -1 ? 0u : kStBadLayout;
+    if (lane == 0) sh.bound = max(thr, 1u);  // 0 stands for no element
+  }
+  __syncthreads();
+  const uint32_t bound = sh.bound;
+  // no element below it counts (bounds up to that of the lowest number let everything pass)
+  const float least = bound > 0x80u ? from_ordered(bound << 16) : -kInfF;
+  const int span = kLpThreads * kBatch * batches;  // vectors of the line between a thread's groups
+  if (mine >= bound)
+    for (int group = 0; lo + group * span < hi; ++group)
+      if (sh.peak[group][t] >= bound) {
+        const uint32_t at = atomicAdd(&sh.owners, 1u);
+        if (at < kCandCap) sh.who[at] = static_cast<uint16_t>(t + kLpThreads * group);
+      }
+  auto offer = [&](float f, int idx) {
+    if ((ordered(f) >> 16) >= bound) {
+      const uint32_t at = atomicAdd(&sh.found, 1u);
+      if (at < kCandCap) sh.cand[at] = top_key(f, idx);
     }
+  };
+  if (t < tails && mine >= bound) offer(logit_at<BF16>(p.lg, row, tail0 + t), tail0 + t);
+  __syncthreads();
+  const int who = static_cast<int>(sh.owners);
+  const int per = kBatch * batches;  // vectors of a group
+  if (who <= kCandCap) {             // those groups' vectors again
+    for (int y = t; y < who * per; y += kLpThreads) {
+      const int item = y / per, w = sh.who[item];
+      const int x = lo + w / kLpThreads * span + w % kLpThreads + (y - item * per) * kLpThreads;
+      if (x >= hi) continue;
+      const uint4 u = ld_stream16(vec + x);
+      if (largest<BF16>(u) < least) continue;
+      float f[N];
+      Vec<BF16>::unpack(u, f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) offer(f[e], x * N + e);
+    }
+  } else if (t == 0) {
+    sh.found = kCandCap + 1;
+  }
+  __syncthreads();
+  const uint32_t found = sh.found;
+  if (found <= kCandCap) {
+    rank_top(sh.cand, static_cast<int>(found), p.top_k, sh.top);
     return;
   }
-  const float T = logprob_temperature(p.row_temp, i);
-  const float k = logprob_k(T);
-  const int nvec = p.lg.vocab / N;
-  const int lo = static_cast<int>(static_cast<int64_t>(nvec) * split / p.splits);
-  const int hi = static_cast<int>(static_cast<int64_t>(nvec) * (split + 1) / p.splits);
-  const char* base = static_cast<const char*>(p.lg.base) + row * p.lg.ld * (BF16 ? 2 : 4);
-  const uint4* vec = reinterpret_cast<const uint4*>(base);
-  const int tail0 = nvec * N;  // the ragged end belongs to the last block of the row
-  const int tails = split == p.splits - 1 ? p.lg.vocab - tail0 : 0;
+  // More candidates than the sort holds (long runs of equal logits): one block-wide search an alternative.
+  uint64_t last = ~0ull;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint64_t best = 0ull;
+    for (int x = lo + t; x < hi; x += kLpThreads) {
+      float f[N];
+      Vec<BF16>::unpack(ld_stream16(vec + x), f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const uint64_t key = top_key(f[e], x * N + e);
+        if (key < last && key > best) best = key;
+      }
+    }
+    if (t < tails) {
+      const uint64_t key = top_key(logit_at<BF16>(p.lg, row, tail0 + t), tail0 + t);
+      if (key < last && key > best) best = key;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, off));
+    if (lane == 0) sh.key[warp] = best;
+    __syncthreads();
+    best = 0ull;
+    for (int w = 0; w < kLpWarps; ++w) best = max(best, sh.key[w]);
+    if (t == 0) sh.top[j] = best;
+    last = best == 0ull ? 1ull : best;  // nothing left: no key is below 1
+    __syncthreads();
+  }
+}
 
-  if (t == 0) s_flags = 0u, s_count = 0u;
-  __syncthreads();
-  Run r{-kInfF, 0.0f, 0.0f};
-  uint32_t flags = 0u;
-  for (int v = lo + t; v < hi; v += kLpThreads * U) {
-    uint4 u[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int x = v + j * kLpThreads;
-      // beyond the part: all -inf (bf16 pairs 0xff80, fp32 0xff800000)
-      u[j] = x < hi ? ld_stream16(vec + x)
-                    : (BF16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
-                            : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u));
-    }
-    float vm;
-    if (BF16) {
-      uint32_t a = 0xff80ff80u;
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        a = bmax2_nan(a, bmax2_nan(bmax2_nan(u[j].x, u[j].y), bmax2_nan(u[j].z, u[j].w)));
-      vm = fmax_nan(bf16_lo(a), bf16_hi(a));
-    } else {
-      vm = -kInfF;
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        vm = fmax_nan(vm, fmax_nan(fmax_nan(__uint_as_float(u[j].x), __uint_as_float(u[j].y)),
-                                   fmax_nan(__uint_as_float(u[j].z), __uint_as_float(u[j].w))));
-    }
-    if (!(vm <= r.m)) {
-      if (!usable_logit(vm)) {  // a NaN or +inf among them: element by element
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          float f[N];
-          Vec<BF16>::unpack(u[j], f);
-#pragma unroll
-          for (int e = 0; e < N; ++e) run_add(r, f[e], k, flags);
-        }
-        continue;
-      }
-      run_merge(r, Run{vm, 0.0f, 0.0f}, k);  // the new reference
-    }
-    if (r.m > -kInfF) {
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        float f[N];
-        Vec<BF16>::unpack(u[j], f);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float d = fmaxf(f[e] - r.m, -FLT_MAX);  // -inf entries: weight 0, and 0 * d = 0
-          const float x = ex2_fast(d * k);
-          r.s += x;
-          r.w = fmaf(x, d, r.w);
-        }
-      }
-    }
-  }
-  if (t < tails) run_add(r, logit_at<BF16>(p.lg, row, tail0 + t), k, flags);
-
-  // Top alternatives of the part.
-  if (p.top_k > 0) {
-    const uint32_t mine = ordered(r.m) >> 16;
-    uint32_t thr = 0u;  // the largest 16-bit bound that top_k threads' maxima reach
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t cand = thr | (1u << bit);
-      if (__syncthreads_count(mine >= cand) >= p.top_k) thr = cand;
-    }
-    const uint32_t bound = max(thr, 1u);  // 0 stands for no element
-    if (mine >= bound) s_who[atomicAdd(&s_count, 1u)] = static_cast<uint16_t>(t);
-    __syncthreads();
-    const int who = static_cast<int>(s_count);
-    __syncthreads();
-    if (t == 0) s_count = 0u;
-    __syncthreads();
-    for (int c = warp; c < who; c += kLpWarps) {
-      const int owner = s_who[c];
-      for (int x = lo + owner + lane * kLpThreads; x < hi; x += 32 * kLpThreads) {
-        float f[N];
-        Vec<BF16>::unpack(ld_stream16(vec + x), f);
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if ((ordered(f[e]) >> 16) >= bound) {
-            const uint32_t at = atomicAdd(&s_count, 1u);
-            if (at < kCandCap) s_cand[at] = top_key(f[e], x * N + e);
-          }
-      }
-      if (owner < tails && lane == 0) {
-        const float f = logit_at<BF16>(p.lg, row, tail0 + owner);
-        if ((ordered(f) >> 16) >= bound) {
-          const uint32_t at = atomicAdd(&s_count, 1u);
-          if (at < kCandCap) s_cand[at] = top_key(f, tail0 + owner);
-        }
-      }
-    }
-    __syncthreads();
-    const uint32_t found = s_count;
-    if (found <= kCandCap) {
-      rank_top(s_cand, static_cast<int>(found), p.top_k, s_top);
-    } else {
-      // More candidates than the sort holds (long runs of equal logits): one block-wide search an alternative.
-      uint64_t last = ~0ull;
-      for (int j = 0; j < p.top_k; ++j) {
-        uint64_t best = 0ull;
-        for (int x = lo + t; x < hi; x += kLpThreads) {
-          float f[N];
-          Vec<BF16>::unpack(ld_stream16(vec + x), f);
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const uint64_t key = top_key(f[e], x * N + e);
-            if (key < last && key > best) best = key;
-          }
-        }
-        if (t < tails) {
-          const uint64_t key = top_key(logit_at<BF16>(p.lg, row, tail0 + t), tail0 + t);
-          if (key < last && key > best) best = key;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, off));
-        if (lane == 0) s_key[warp] = best;
-        __syncthreads();
-        best = 0ull;
-        for (int w = 0; w < kLpWarps; ++w) best = max(best, s_key[w]);
-        if (t == 0) s_top[j] = best;
-        last = best == 0ull ? 1ull : best;  // nothing left: no key is below 1
-        __syncthreads();
-      }
-    }
-  }
-
-  // Join the threads' sums.
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Run o{__shfl_xor_sync(0xffffffffu, r.m, off), __shfl_xor_sync(0xffffffffu, r.s, off),
-          __shfl_xor_sync(0xffffffffu, r.w, off)};
-    // both sides of an exchange join in the same order, lower lane first
-    if (lane & off) {
-      const Run mine = r;
-      r = o;
-      o = mine;
-    }
-    run_merge(r, o, k);
-  }
-  flags = __reduce_or_sync(0xffffffffu, flags);
-  if (lane == 0) {
-    s_run[warp] = r;
-    if (flags) atomicOr(&s_flags, flags);
-  }
-  __syncthreads();
+// Joins the parts of a row, left by blocks c0 .. c1, into sh.run[0], sh.flags and sh.top.
+__device__ __noinline__ void join_parts(const LogprobParams& p, LogprobShared& sh, int c0, int c1, float k) {
+  const int t = threadIdx.x;
+  auto slot = [&](int c) { return c * 2 + (c == c0 ? 1 : 0); };  // a block's first row began before it, but for the first
   if (t == 0) {
-    r = s_run[0];
-    for (int w = 1; w < kLpWarps; ++w) run_merge(r, s_run[w], k);
-    s_run[0] = r;
+    Run r{-kInfF, 0.0f, 0.0f};
+    uint32_t f = 0u;
+    for (int c = c0; c <= c1; ++c) {
+      const Run* q = p.part + slot(c);
+      run_merge(r, Run{__ldcg(&q->m), __ldcg(&q->s), __ldcg(&q->w)}, k);
+      f |= __ldcg(&p.part_flags[slot(c)]);
+    }
+    sh.run[0] = r;
+    sh.flags = f;
+    sh.found = 0u;
+    sh.key[0] = 0ull;
   }
-
-  if (p.splits > 1) {
-    const int64_t at = i * p.splits + split;
-    for (int j = t; j < p.top_k; j += kLpThreads) p.part_top[at * p.top_k + j] = s_top[j];
-    if (t == 0) {
-      p.part[at] = r;
-      p.part_flags[at] = s_flags;
-    }
-    __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
-    __syncthreads();
-    if (t == 0) s_last = ticket_add(&p.tickets[i], 1u) == static_cast<unsigned>(p.splits - 1) ? 1u : 0u;
-    __syncthreads();
-    if (!s_last) return;
-    // The last block of the row joins the parts in order.
-    if (t == 0) {
-      p.tickets[i] = 0u;
-      r = Run{-kInfF, 0.0f, 0.0f};
-      uint32_t f = 0u;
-      for (int s = 0; s < p.splits; ++s) {
-        const Run* q = p.part + i * p.splits + s;
-        run_merge(r, Run{__ldcg(&q->m), __ldcg(&q->s), __ldcg(&q->w)}, k);
-        f |= __ldcg(&p.part_flags[i * p.splits + s]);
-      }
-      s_run[0] = r;
-      s_flags = f;
-      s_count = 0u;
-    }
-    if (p.top_k > 0) {
-      // A part's last key is a lower bound on the row's top_k-th: the largest of them leaves about top_k keys.
-      const uint64_t* keys = p.part_top + i * p.splits * p.top_k;
-      if (warp == 0) {
-        uint64_t b = lane < p.splits ? __ldcg(&keys[lane * p.top_k + p.top_k - 1]) : 0ull;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, off));
-        if (lane == 0) s_key[0] = b;
-      }
-      __syncthreads();
-      const uint64_t bound = s_key[0];
-      for (int x = t; x < p.splits * p.top_k; x += kLpThreads) {
-        const uint64_t key = __ldcg(&keys[x]);
-        if (key != 0ull && key >= bound) {
-          const uint32_t at = atomicAdd(&s_count, 1u);
-          if (at < kCandCap) s_cand[at] = key;
-        }
-      }
-      __syncthreads();
-      rank_top(s_cand, min(static_cast<int>(s_count), kCandCap), p.top_k, s_top);
+  __syncthreads();
+  if (p.top_k == 0) return;
+  // A part's last key is a lower bound on the row's top_k-th: the largest of them leaves about top_k keys.
+  for (int c = c0 + t; c <= c1; c += kLpThreads)
+    atomicMax(reinterpret_cast<unsigned long long*>(&sh.key[0]),
+              static_cast<unsigned long long>(__ldcg(&p.part_top[static_cast<int64_t>(slot(c)) * p.top_k + p.top_k - 1])));
+  __syncthreads();
+  const uint64_t bound = sh.key[0];
+  for (int x = t; x < (c1 - c0 + 1) * p.top_k; x += kLpThreads) {
+    const uint64_t key = __ldcg(&p.part_top[static_cast<int64_t>(slot(c0 + x / p.top_k)) * p.top_k + x % p.top_k]);
+    if (key != 0ull && key >= bound) {
+      const uint32_t at = atomicAdd(&sh.found, 1u);
+      if (at < kCandCap) sh.cand[at] = key;
     }
   }
   __syncthreads();
+  rank_top(sh.cand, min(static_cast<int>(sh.found), kCandCap), p.top_k, sh.top);
+}
 
-  // Outputs of the row.
-  r = s_run[0];
+// The outputs of row i from sh.run[0], sh.flags and sh.top.
+template <bool BF16>
+__device__ __noinline__ void write_outputs(const LogprobParams& p, LogprobShared& sh, int64_t i, int64_t row, float T) {
+  const int t = threadIdx.x;
+  const Run r = sh.run[0];
   const bool empty = r.m == -kInfF;
   const float lz = empty ? -kInfF : logf(r.s);
   bool range = false;
@@ -420,7 +386,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(LogprobParams p) 
     p.logprob[i * p.num_ids + j] = lp;
   }
   for (int j = t; j < p.top_k; j += kLpThreads) {
-    const uint64_t key = s_top[j];
+    const uint64_t key = sh.top[j];
     p.top_ids[i * p.top_k + j] = key ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
     p.top_logprob[i * p.top_k + j] =
         key ? __fdiv_rn(from_ordered(static_cast<uint32_t>(key >> 32)) - r.m, T) - lz : -kInfF;
@@ -428,29 +394,289 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(LogprobParams p) 
   const int outside = __syncthreads_or(range ? 1 : 0);
   if (t == 0) {
     // the entropy of a distribution is not negative; rounding may leave a value just below 0
-    if (p.entropy) p.entropy[i] = empty ? 0.0f : fmaxf(lz - __fdiv_rn(__fdiv_rn(r.w, r.s), T), 0.0f);
+    if (p.entropy) p.entropy[i] = empty ? 0.0f : fmaxf(fmaf(__fdiv_rn(r.w, r.s), -kLn2, lz), 0.0f);
     if (p.row_max) p.row_max[i] = r.m;
     if (p.log_z) p.log_z[i] = lz;
-    if (p.flags) p.flags[i] = s_flags | (outside ? kStTokenRange : 0u) | (empty ? kStNonFinite : 0u);
+    if (p.flags) p.flags[i] = sh.flags | (outside ? kStTokenRange : 0u) | (empty ? kStNonFinite : 0u);
+  }
+}
+
+__device__ __forceinline__ void write_padding(const LogprobParams& p, int64_t i, uint32_t flags) {
+  for (int j = 0; j < p.num_ids; ++j) p.logprob[i * p.num_ids + j] = 0.0f;
+  for (int j = 0; j < p.top_k; ++j) p.top_ids[i * p.top_k + j] = -1, p.top_logprob[i * p.top_k + j] = -kInfF;
+  if (p.entropy) p.entropy[i] = 0.0f;
+  if (p.row_max) p.row_max[i] = -kInfF;
+  if (p.log_z) p.log_z[i] = 0.0f;
+  if (p.flags) p.flags[i] = flags;
+}
+
+// The vectors of all rows form one line; block c of g takes vectors [c total / g, (c + 1) total / g) of it, so that every
+// block reads as much, however many rows there are and whichever of them are padding.  A row that lies in one block is
+// finished there; of one that several share each leaves its part, and the last to arrive joins them in block order.
+template <bool BF16>
+__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobParams p) {
+  constexpr int N = Vec<BF16>::N;
+  constexpr int U = kBatch;
+  __shared__ LogprobShared sh;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  grid_dependency_wait();
+  allow_dependents();
+  const int nvec = p.lg.vocab / N, tail0 = nvec * N;
+  const int per_row = nvec > 0 ? nvec : 1;  // (a row of less than a vector has its ragged end only)
+
+  // Rows that there are, and the padding.
+  auto padding = [&](int64_t i) {
+    const int64_t r = p.row_index[i];
+    return r < 0 || r >= p.lg.rows;
+  };
+  int64_t rows = p.n;
+  if (p.row_index) {
+    int64_t mine = 0;
+    for (int64_t i = t; i < p.n; i += kLpThreads) mine += padding(i) ? 0 : 1;
+    for (int64_t i = blockIdx.x * kLpThreads + t; i < p.n; i += static_cast<int64_t>(gridDim.x) * kLpThreads)
+      if (padding(i)) write_padding(p, i, p.row_index[i] == -1 ? 0u : kStBadLayout);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    if (lane == 0) sh.sums[warp] = mine;
+    __syncthreads();
+    rows = 0;
+#pragma unroll
+    for (int w = 0; w < kLpWarps; ++w) rows += sh.sums[w];
+    __syncthreads();
+  }
+  const int64_t total = rows * per_row;
+  int64_t g = total / p.min_vectors;
+  if (g > gridDim.x) g = gridDim.x;
+  if (g < 1) g = 1;
+  if (blockIdx.x >= g || total == 0) return;
+  const int64_t start = blockIdx.x * total / g, end = (blockIdx.x + 1) * total / g;
+  int64_t ord = start / per_row;  // rows before this block's first one
+  int64_t i = ord;                // its output
+  if (p.row_index) {              // the ord-th output that is not padding
+    int64_t before = 0;
+    for (int64_t i0 = 0; i0 < p.n; i0 += kLpThreads) {
+      const bool is = i0 + t < p.n && !padding(i0 + t);
+      const uint32_t b = __ballot_sync(0xffffffffu, is);
+      if (lane == 0) sh.sums[warp] = __popc(b);
+      __syncthreads();
+      int64_t at = before;
+#pragma unroll
+      for (int w = 0; w < kLpWarps; ++w) {
+        if (w == warp && is && at + __popc(b & ((1u << lane) - 1u)) == ord) sh.find[0] = i0 + t;
+        at += sh.sums[w];
+      }
+      before = at;
+      __syncthreads();
+      if (before > ord) break;
+    }
+    i = sh.find[0];
+  }
+
+  for (int64_t pos = start; pos < end; ++i) {
+    if (p.row_index && padding(i)) continue;
+    const int64_t row = p.row_index ? p.row_index[i] : i;
+    const int64_t row0 = ord * per_row;  // the row's first place in the line
+    const int lo = static_cast<int>(pos - row0);
+    const int hi = static_cast<int>(min(static_cast<int64_t>(per_row), end - row0));
+    const int vhi = min(hi, nvec);
+    const bool whole = lo == 0 && hi == per_row;
+    const int tails = hi == per_row ? p.lg.vocab - tail0 : 0;  // the ragged end belongs to the row's last block
+    pos = row0 + hi;
+    ++ord;
+    const float T = logprob_temperature(p.row_temp, i);
+    const float k = logprob_k(T), unit = __frcp_rn(k);
+    const uint4* vec = reinterpret_cast<const uint4*>(static_cast<const char*>(p.lg.base) + row * p.lg.ld * (BF16 ? 2 : 4));
+
+    Stream<BF16> st;
+    uint32_t flags = 0u;
+    float top = -kInfF;  // the thread's largest usable logit
+    // batches of a group, so that the groups fit sh.peak; the current one's largest, its batches so far, its number
+    const int batches = ((vhi - lo + kLpThreads * U - 1) / (kLpThreads * U) + kPeaks - 1) / kPeaks;
+    float peak = -kInfF;
+    int had = 0, group = 0;
+    auto batch_done = [&](float m) {
+      top = fmaxf(top, m);
+      if (p.top_k == 0) return;
+      peak = fmaxf(peak, m);
+      if (++had == batches) {
+        sh.peak[group++][t] = static_cast<uint16_t>(ordered(peak) >> 16);
+        peak = -kInfF;
+        had = 0;
+      }
+    };
+    for (int v0 = lo + warp * 32; v0 < vhi; v0 += kLpThreads * U) {
+      uint4 u[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int x = v0 + lane + j * kLpThreads;
+        // beyond the part: all -inf (bf16 pairs 0xff80, fp32 0xff800000)
+        u[j] = x < vhi ? ld_stream16(vec + x)
+                       : (BF16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                               : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u));
+      }
+      float vm;
+      if (BF16) {
+        uint32_t a = 0xff80ff80u;
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          a = bmax2_nan(a, bmax2_nan(bmax2_nan(u[j].x, u[j].y), bmax2_nan(u[j].z, u[j].w)));
+        vm = fmax_nan(bf16_lo(a), bf16_hi(a));
+      } else {
+        vm = -kInfF;
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          vm = fmax_nan(vm, fmax_nan(fmax_nan(__uint_as_float(u[j].x), __uint_as_float(u[j].y)),
+                                     fmax_nan(__uint_as_float(u[j].z), __uint_as_float(u[j].w))));
+      }
+      const bool odd = !usable_logit(vm);  // a NaN or +inf among them
+      if (__any_sync(0xffffffffu, odd || vm > st.limit)) {
+        float to = odd ? -kInfF : vm;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+        if (to > st.limit) st.rise(to, k, unit);
+      }
+      if (odd || !st.packed()) {  // element by element
+        float most = -kInfF;
+#pragma unroll 1
+        for (int j = 0; j < U; ++j) {
+          float f[N];
+          Vec<BF16>::unpack(j == 0 ? u[0] : j == 1 ? u[1] : j == 2 ? u[2] : u[U - 1], f);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            run_add(st.r, f[e], k, flags);
+            if (usable_logit(f[e])) most = fmaxf(most, f[e]);
+          }
+        }
+        batch_done(most);
+        continue;
+      }
+      batch_done(vm);
+      if (st.ref == -kInfF) continue;  // nothing above -inf yet
+      const float2 kk = make_float2(k, k), cc = make_float2(-st.c, -st.c);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (BF16) {
+          u[j].x = bmax2_nan(u[j].x, st.low2), u[j].y = bmax2_nan(u[j].y, st.low2);
+          u[j].z = bmax2_nan(u[j].z, st.low2), u[j].w = bmax2_nan(u[j].w, st.low2);
+        }
+        float f[N];
+        Vec<BF16>::unpack(u[j], f);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          float2 x = make_float2(f[e], f[e + 1]);
+          if (!BF16) x = make_float2(fmaxf(x.x, st.low), fmaxf(x.y, st.low));
+          const float2 y = __ffma2_rn(x, kk, cc);
+          const float2 z = make_float2(ex2_fast(y.x), ex2_fast(y.y));
+          st.s2 = __fadd2_rn(st.s2, z);
+          st.w2 = __ffma2_rn(y, z, st.w2);
+        }
+      }
+    }
+    st.settle(k);
+    if (had > 0) sh.peak[group][t] = static_cast<uint16_t>(ordered(peak) >> 16);
+    Run r = st.r;
+    if (t < tails) {
+      const float l = logit_at<BF16>(p.lg, row, tail0 + t);
+      run_add(r, l, k, flags);
+      if (usable_logit(l)) top = fmaxf(top, l);
+    }
+    if (t == 0) sh.flags = 0u;
+    __syncthreads();
+    if (p.top_k > 0) select_top<BF16>(p, sh, row, lo, vhi, tail0, tails, top, batches);
+
+    // Join the threads' sums.
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      Run o{__shfl_xor_sync(0xffffffffu, r.m, off), __shfl_xor_sync(0xffffffffu, r.s, off),
+            __shfl_xor_sync(0xffffffffu, r.w, off)};
+      // both sides of an exchange join in the same order, lower lane first
+      if (lane & off) {
+        const Run mine = r;
+        r = o;
+        o = mine;
+      }
+      run_merge(r, o, k);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    }
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if (lane == 0) {
+      sh.run[warp] = r;
+      sh.max[warp] = top;
+      if (flags) atomicOr(&sh.flags, flags);
+    }
+    __syncthreads();
+    if (t == 0) {
+      r = sh.run[0];
+#pragma unroll 1
+      for (int w = 1; w < kLpWarps; ++w) run_merge(r, sh.run[w], k), top = fmaxf(top, sh.max[w]);
+      // from here on against the row's (or part's) largest logit
+      if (top > -kInfF) {
+        const float d = (r.m - top) * k;
+        const float e = ex2_fast(d);
+        r = Run{top, e * r.s, e * fmaf(r.s, d, r.w)};
+      }
+      sh.run[0] = r;
+    }
+    if (!whole) {
+      const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 + (lo == 0 ? 1 : 0);
+      for (int j = t; j < p.top_k; j += kLpThreads) p.part_top[at * p.top_k + j] = sh.top[j];
+      if (t == 0) {
+        p.part[at] = r;
+        p.part_flags[at] = sh.flags;
+      }
+      const int c0 = static_cast<int>(((row0 + 1) * g - 1) / total), c1 = static_cast<int>(((row0 + per_row) * g - 1) / total);
+      __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
+      __syncthreads();
+      if (t == 0) {
+        sh.last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0) ? 1u : 0u;
+        if (sh.last) p.tickets[c0] = 0u;
+      }
+      __syncthreads();
+      if (!sh.last) continue;
+      join_parts(p, sh, c0, c1, k);
+    }
+    __syncthreads();
+    write_outputs<BF16>(p, sh, i, row, T);
+    __syncthreads();
   }
 }
 
 struct LogprobWs {
-  size_t tickets, part, flags, top, total;
+  size_t part, flags, top, total;
 };
 
 // The same offsets whatever the number of rows, so that the tickets of one call never lie where another wrote its parts.
 LogprobWs logprob_ws(int32_t top_k) {
   LogprobWs L{};
-  size_t off = sizeof(uint32_t) * kMaxSplitRows;
+  size_t off = sizeof(uint32_t) * kMaxBlocks;
   L.part = off;
-  off = align_up(off + sizeof(Run) * kMaxParts, 256);
+  off = align_up(off + sizeof(Run) * 2 * kMaxBlocks, 256);
   L.flags = off;
-  off = align_up(off + sizeof(uint32_t) * kMaxParts, 256);
+  off = align_up(off + sizeof(uint32_t) * 2 * kMaxBlocks, 256);
   L.top = off;
-  off = align_up(off + sizeof(uint64_t) * kMaxParts * static_cast<size_t>(top_k > 0 ? top_k : 0), 256);
+  off = align_up(off + sizeof(uint64_t) * 2 * kMaxBlocks * static_cast<size_t>(top_k > 0 ? top_k : 0), 256);
   L.total = off;
   return L;
+}
+
+// Resident blocks of a multiprocessor, once for each device.
+template <bool BF16>
+cudaError_t logprob_blocks(int* n) {
+  static std::mutex mu;
+  static int have[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (have[dev] == 0) {
+    int fit = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k_token_logprobs<BF16>, kLpThreads, 0);
+    if (e != cudaSuccess) return e;
+    have[dev] = fit < 1 ? 1 : fit;
+  }
+  *n = have[dev];
+  return cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------------------------------------------------
@@ -589,15 +815,12 @@ sv_status_t check_rows(const void* logits, sv_dtype_t dt, int64_t ld, int64_t ro
   return SV_OK;
 }
 
-// Blocks a row is split over: enough that about `want` blocks run, each with at least 1024 vectors, and no more parts
-// than the join of the top alternatives holds.
-int32_t row_splits(int64_t n, int32_t vocab, bool bf16, int32_t want, int32_t top_k) {
-  if (want > kMaxSplitRows) want = kMaxSplitRows;
+// Blocks a row's gradient is split over: enough that about `want` blocks run, each with at least 1024 vectors.
+int32_t row_splits(int64_t n, int32_t vocab, bool bf16, int32_t want) {
   const int64_t nvec = vocab / (bf16 ? 8 : 4);
   int64_t s = (want + n - 1) / n;
   if (s > nvec / 1024) s = nvec / 1024;
-  if (s > kMaxSplits) s = kMaxSplits;
-  if (top_k > 0 && s > kCandCap / top_k) s = kCandCap / top_k;
+  if (s > 32) s = 32;
   return static_cast<int32_t>(s < 1 ? 1 : s);
 }
 
@@ -621,7 +844,7 @@ sv_status_t spec_verify_token_logprobs(const void* logits, sv_dtype_t dtype, int
   if (n == 0 && rows >= 0) return SV_OK;  // an empty batch has no arrays to check
   const sv_status_t c = check_rows(logits, dtype, ld, rows, vocab);
   if (c != SV_OK) return c;
-  if (n < 0 || n > INT32_MAX / kMaxSplits || (!row_index && n > rows)) return SV_ERR_BAD_SHAPE;
+  if (n < 0 || n > INT32_MAX || (!row_index && n > rows)) return SV_ERR_BAD_SHAPE;
   if (num_ids < 0 || num_ids > kMaxGiven || top_k < 0 || top_k > kMaxTop || ldi < num_ids) return SV_ERR_BAD_SHAPE;
   if (num_ids > 0 && (!ids || !logprob)) return SV_ERR_NULL_ARG;
   if (top_k > 0 && (!top_ids || !top_logprob)) return SV_ERR_NULL_ARG;
@@ -632,12 +855,26 @@ sv_status_t spec_verify_token_logprobs(const void* logits, sv_dtype_t dtype, int
   if (e != cudaSuccess) return cuda_failure(e);
   char* base = static_cast<char*>(ws);
   const bool bf16 = dtype == SV_BF16;
-  LogprobParams p{LogitsView{logits, dtype, ld, rows, vocab},
-                  n, row_index, ids, num_ids, ldi, row_temp, top_k, logprob, entropy, row_max, log_z, top_ids,
-                  top_logprob, flags, row_splits(n, vocab, bf16, 4 * dev.sms, top_k),
-                  reinterpret_cast<uint32_t*>(base + L.tickets), reinterpret_cast<Run*>(base + L.part),
-                  reinterpret_cast<uint32_t*>(base + L.flags), reinterpret_cast<uint64_t*>(base + L.top)};
-  const dim3 grid(static_cast<unsigned>(n * p.splits));
+  int per_sm = 1;
+  e = bf16 ? logprob_blocks<true>(&per_sm) : logprob_blocks<false>(&per_sm);
+  if (e != cudaSuccess) return cuda_failure(e);
+  // one resident wave, less where the rows are not worth it
+  const int64_t vectors = n * (vocab / (bf16 ? 8 : 4));
+  int64_t blocks = static_cast<int64_t>(dev.sms) * per_sm;
+  if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+  // ... and no more parts of a row than the join of the top alternatives holds
+  int64_t least = kMinVectors;
+  if (top_k > 0) {
+    const int64_t parts = kCandCap / top_k - 2, nvec = vocab / (bf16 ? 8 : 4);
+    if (least < (nvec + parts - 1) / parts) least = (nvec + parts - 1) / parts;
+  }
+  if (blocks > vectors / least) blocks = vectors / least;
+  if (blocks < 1) blocks = 1;
+  const LogprobParams p{LogitsView{logits, dtype, ld, rows, vocab},
+                        n, row_index, ids, num_ids, ldi, row_temp, top_k, logprob, entropy, row_max, log_z, top_ids,
+                        top_logprob, flags, reinterpret_cast<uint32_t*>(base), reinterpret_cast<Run*>(base + L.part),
+                        reinterpret_cast<uint32_t*>(base + L.flags), reinterpret_cast<uint64_t*>(base + L.top), least};
+  const dim3 grid(static_cast<unsigned>(blocks));
   e = bf16 ? launch_pdl(k_token_logprobs<true>, grid, dim3(kLpThreads), 0, stream, p)
            : launch_pdl(k_token_logprobs<false>, grid, dim3(kLpThreads), 0, stream, p);
   return e == cudaSuccess ? SV_OK : cuda_failure(e);
@@ -655,7 +892,7 @@ sv_status_t spec_verify_token_logprobs_backward(const void* logits, sv_dtype_t d
   c = check_rows(dlogits, dtype, ldd, rows, vocab);
   if (c != SV_OK) return c;
   if (num_ids < 0 || num_ids > kMaxGiven || top_k < 0 || top_k > kMaxTop || ldi < num_ids ||
-      rows > INT32_MAX / kMaxSplits)
+      rows > INT32_MAX / 32)
     return SV_ERR_BAD_SHAPE;
   if (!row_max || !log_z) return SV_ERR_NULL_ARG;
   if (num_ids > 0 && (!ids || !g_logprob)) return SV_ERR_NULL_ARG;
@@ -672,7 +909,7 @@ sv_status_t spec_verify_token_logprobs_backward(const void* logits, sv_dtype_t d
   if (e != cudaSuccess) return cuda_failure(e);
   const LogprobBwdParams p{LogitsView{logits, dtype, ld, rows, vocab},
                            ids, num_ids, ldi, row_temp, row_max, log_z, entropy, top_ids, top_k, g_logprob,
-                           g_entropy, g_top, dlogits, ldd, row_splits(rows, vocab, bf16, 4 * dev.sms, 0)};
+                           g_entropy, g_top, dlogits, ldd, row_splits(rows, vocab, bf16, 4 * dev.sms)};
   const dim3 grid(static_cast<unsigned>(rows * p.splits));
   e = bf16 ? launch_pdl(k_token_logprobs_bwd<true>, grid, dim3(kLpThreads), 0, stream, p)
            : launch_pdl(k_token_logprobs_bwd<false>, grid, dim3(kLpThreads), 0, stream, p);
