@@ -36,7 +36,7 @@
 namespace sv {
 namespace {
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 128;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 64;
 constexpr int kMaxGiven = 1024;
@@ -44,7 +44,7 @@ constexpr int kMaxBlocks = 1280;    // of the forward kernel (the workspace is l
 constexpr int kMinVectors = 1024;   // 16-byte vectors that a block takes at least
 constexpr int kCandCap = 1024;  // candidates a block sorts in shared memory
 constexpr int kBatch = 4;       // vectors that a thread reads at once
-constexpr int kPeaks = 32;      // groups of batches whose largest logits are kept
+constexpr int kPeaks = 40;      // groups of batches whose largest logits are kept
 constexpr float kLn2 = 0.693147180559945309417f;
 
 // A logits vector: 16 bytes as floats.
@@ -111,6 +111,24 @@ __device__ __forceinline__ void run_merge(Run& a, const Run& b, float k) {
   a.w = (ea > 0.0f ? ea * fmaf(a.s, da, a.w) : 0.0f) + (eb > 0.0f ? eb * fmaf(b.s, db, b.w) : 0.0f);
   a.s = ea * a.s + eb * b.s;
   a.m = M;
+}
+
+// The lanes' triples, in order (both sides of an exchange join the lower lane's first): the same in every lane.  Rolled, as
+// what runs once a row is: its instructions are fetched anew each time.
+__device__ __forceinline__ Run run_join(Run r, float k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int off = 1; off < 32; off <<= 1) {
+    Run o{__shfl_xor_sync(0xffffffffu, r.m, off), __shfl_xor_sync(0xffffffffu, r.s, off),
+          __shfl_xor_sync(0xffffffffu, r.w, off)};
+    if (lane & off) {
+      const Run mine = r;
+      r = o;
+      o = mine;
+    }
+    run_merge(r, o, k);
+  }
+  return r;
 }
 
 // log2(e) / T, of the unscaled distribution for a greedy temperature.  Held at 1e-30 at least: there every finite logit of
@@ -221,14 +239,14 @@ struct LogprobShared {
   uint64_t key[kLpWarps];
   alignas(16) uint16_t level[kLpThreads];
   uint16_t peak[kPeaks][kLpThreads];  // the largest logit of each thread's groups of batches, as 16-bit bounds
-  uint16_t who[kCandCap];             // groups that may hold a top element: thread + 256 group
+  uint16_t who[kCandCap];             // groups that may hold a top element: thread + kLpThreads group
   int64_t sums[kLpWarps];
   int64_t find[2];
   uint32_t flags, found, last, owners, bound;
 };
 
 // The top_k keys of vectors [lo, hi) of a row (and of its ragged end, tails elements from tail0) into sh.top, given each
-// thread's largest logit of its own vectors lo + t, lo + t + 256, ... (and the end), and sh.peak, where a group is
+// thread's largest logit of its own vectors lo + t, lo + t + kLpThreads, ... (and the end), and sh.peak, where a group is
 // `batches` batches of kBatch of them.
 template <bool BF16>
 __device__ __noinline__ void select_top(const LogprobParams& p, LogprobShared& sh, int64_t row, int lo, int hi, int tail0,
@@ -242,17 +260,24 @@ __device__ __noinline__ void select_top(const LogprobParams& p, LogprobShared& s
   if (t == 0) sh.found = 0u, sh.owners = 0u;
   __syncthreads();
   if (warp == 0) {
-    const uint4 x = reinterpret_cast<const uint4*>(sh.level)[lane];
-    const uint32_t v[8] = {x.x & 0xffffu, x.x >> 16, x.y & 0xffffu, x.y >> 16,
-                           x.z & 0xffffu, x.z >> 16, x.w & 0xffffu, x.w >> 16};
-    uint32_t thr = 0u;
+    uint32_t v[kLpWarps], most = 0u, least = 0xffffu;
+#pragma unroll
+    for (int e = 0; e < kLpWarps; ++e) v[e] = sh.level[lane + 32 * e], most = max(most, v[e]), least = min(least, v[e]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    const int differ = (32 - __clz(most ^ least) + 1) & ~1;  // bits below the leading ones that all have
+    uint32_t thr = most >> differ << differ;
+    const uint32_t k = static_cast<uint32_t>(p.top_k);
 #pragma unroll 1
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t to = thr | 1u << bit;
+    for (int bit = differ - 2; bit >= 0; bit -= 2) {  // three candidates a step, their threads counted in ten bits each
       uint32_t n = 0u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) n += v[e] >= to ? 1u : 0u;
-      if (__reduce_add_sync(0xffffffffu, n) >= static_cast<uint32_t>(p.top_k)) thr = to;
+      for (int e = 0; e < kLpWarps; ++e) {
+        const uint32_t d = v[e] >> bit, to = thr >> bit;
+        n += (d >= (to | 1u) ? 1u : 0u) + (d >= (to | 2u) ? 1u << 10 : 0u) + (d >= (to | 3u) ? 1u << 20 : 0u);
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+      thr |= ((n >> 20) >= k ? 3u : (n >> 10 & 0x3ffu) >= k ? 2u : (n & 0x3ffu) >= k ? 1u : 0u) << bit;
     }
     if (lane == 0) sh.bound = max(thr, 1u);  // 0 stands for no element
   }
@@ -262,6 +287,7 @@ __device__ __noinline__ void select_top(const LogprobParams& p, LogprobShared& s
   const float least = bound > 0x80u ? from_ordered(bound << 16) : -kInfF;
   const int span = kLpThreads * kBatch * batches;  // vectors of the line between a thread's groups
   if (mine >= bound)
+#pragma unroll 4
     for (int group = 0; lo + group * span < hi; ++group)
       if (sh.peak[group][t] >= bound) {
         const uint32_t at = atomicAdd(&sh.owners, 1u);
@@ -282,12 +308,14 @@ __device__ __noinline__ void select_top(const LogprobParams& p, LogprobShared& s
       const int item = y / per, w = sh.who[item];
       const int x = lo + w / kLpThreads * span + w % kLpThreads + (y - item * per) * kLpThreads;
       if (x >= hi) continue;
-      const uint4 u = ld_stream16(vec + x);
+      uint4 u = ld_stream16(vec + x);
       if (largest<BF16>(u) < least) continue;
-      float f[N];
-      Vec<BF16>::unpack(u, f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) offer(f[e], x * N + e);
+#pragma unroll 1
+      for (int e = 0; e < N; e += N / 4) {  // word by word
+        offer(BF16 ? bf16_lo(u.x) : __uint_as_float(u.x), x * N + e);
+        if (BF16) offer(bf16_hi(u.x), x * N + e + 1);
+        u.x = u.y, u.y = u.z, u.z = u.w;
+      }
     }
   } else if (t == 0) {
     sh.found = kCandCap + 1;
@@ -331,18 +359,23 @@ __device__ __noinline__ void select_top(const LogprobParams& p, LogprobShared& s
 __device__ __noinline__ void join_parts(const LogprobParams& p, LogprobShared& sh, int c0, int c1, float k) {
   const int t = threadIdx.x;
   auto slot = [&](int c) { return c * 2 + (c == c0 ? 1 : 0); };  // a block's first row began before it, but for the first
-  if (t == 0) {
+  if (t < 32) {  // a lane a part (and the 32nd after it), then the lanes in order
     Run r{-kInfF, 0.0f, 0.0f};
     uint32_t f = 0u;
-    for (int c = c0; c <= c1; ++c) {
+    for (int c = c0 + t; c <= c1; c += 32) {
       const Run* q = p.part + slot(c);
-      run_merge(r, Run{__ldcg(&q->m), __ldcg(&q->s), __ldcg(&q->w)}, k);
+      const Run o{__ldcg(&q->m), __ldcg(&q->s), __ldcg(&q->w)};
       f |= __ldcg(&p.part_flags[slot(c)]);
+      run_merge(r, o, k);
     }
-    sh.run[0] = r;
-    sh.flags = f;
-    sh.found = 0u;
-    sh.key[0] = 0ull;
+    r = run_join(r, k);
+    f = __reduce_or_sync(0xffffffffu, f);
+    if (t == 0) {
+      sh.run[0] = r;
+      sh.flags = f;
+      sh.found = 0u;
+      sh.key[0] = 0ull;
+    }
   }
   __syncthreads();
   if (p.top_k == 0) return;
@@ -414,7 +447,7 @@ __device__ __forceinline__ void write_padding(const LogprobParams& p, int64_t i,
 // block reads as much, however many rows there are and whichever of them are padding.  A row that lies in one block is
 // finished there; of one that several share each leaves its part, and the last to arrive joins them in block order.
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, 7) k_token_logprobs(LogprobParams p) {
   constexpr int N = Vec<BF16>::N;
   constexpr int U = kBatch;
   __shared__ LogprobShared sh;
@@ -448,6 +481,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobParams 
   int64_t g = total / p.min_vectors;
   if (g > gridDim.x) g = gridDim.x;
   if (g < 1) g = 1;
+  // a whole number of blocks a row, where that leaves few of them idle: then no block has parts of two
+  if (rows > 0 && rows <= g && g / rows * rows * 5 >= g * 4) g = g / rows * rows;
   if (blockIdx.x >= g || total == 0) return;
   const int64_t start = blockIdx.x * total / g, end = (blockIdx.x + 1) * total / g;
   int64_t ord = start / per_row;  // rows before this block's first one
@@ -585,19 +620,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(LogprobParams 
     if (p.top_k > 0) select_top<BF16>(p, sh, row, lo, vhi, tail0, tails, top, batches);
 
     // Join the threads' sums.
+    r = run_join(r, k);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      Run o{__shfl_xor_sync(0xffffffffu, r.m, off), __shfl_xor_sync(0xffffffffu, r.s, off),
-            __shfl_xor_sync(0xffffffffu, r.w, off)};
-      // both sides of an exchange join in the same order, lower lane first
-      if (lane & off) {
-        const Run mine = r;
-        r = o;
-        o = mine;
-      }
-      run_merge(r, o, k);
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    }
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0) {
       sh.run[warp] = r;
