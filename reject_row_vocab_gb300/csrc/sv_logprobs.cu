@@ -733,13 +733,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Blocks take a part of a row each; about 32 a multiprocessor (six of them resident), so that the ends of some lie under
+// the streams of others.
+constexpr int kBwdThreads = 256;
+
 template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads) k_token_logprobs_bwd(LogprobBwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 6) k_token_logprobs_bwd(LogprobBwdParams p) {
   constexpr int N = Vec<BF16>::N;
   constexpr int U = 4;
   __shared__ int32_t s_id[kMaxGiven + kMaxTop];  // -1: no part in the gradient
   __shared__ float s_g[kMaxGiven + kMaxTop];
-  __shared__ float s_sum[kLpWarps];
+  __shared__ float s_sum[(kBwdThreads / 32)];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t row = blockIdx.x / p.splits;
   const int split = static_cast<int>(blockIdx.x - row * p.splits);
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_bwd(LogprobBwdPar
   const float k = logprob_k(T), invT = __frcp_rn(T);
   const int given = p.num_ids + p.top_k;
   float G = 0.0f;
-  for (int j = t; j < given; j += kLpThreads) {
+  for (int j = t; j < given; j += kBwdThreads) {
     const bool top = j >= p.num_ids;
     int32_t id = top ? p.top_ids[row * p.top_k + j - p.num_ids] : p.ids[row * p.ldi + j];
     const float g = top ? p.g_top[row * p.top_k + j - p.num_ids] : p.g_logprob[row * p.num_ids + j];
@@ -766,7 +770,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_bwd(LogprobBwdPar
   __syncthreads();
   G = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kLpWarps; ++w) G += s_sum[w];
+  for (int w = 0; w < (kBwdThreads / 32); ++w) G += s_sum[w];
 
   const float gH = p.g_entropy ? p.g_entropy[row] : 0.0f;
   const float A = -(G + (p.g_entropy ? gH * p.entropy[row] : 0.0f)) * invT;
@@ -785,14 +789,14 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_bwd(LogprobBwdPar
   const uint4* vec = reinterpret_cast<const uint4*>(static_cast<const char*>(p.lg.base) + row * p.lg.ld * (BF16 ? 2 : 4));
   char* out = static_cast<char*>(p.dlogits) + row * p.ldd * (BF16 ? 2 : 4);
   uint4* ovec = reinterpret_cast<uint4*>(out);
-  for (int v = lo + t; v < hi; v += kLpThreads * U) {
+  for (int v = lo + t; v < hi; v += kBwdThreads * U) {
     uint4 u[U];
 #pragma unroll
     for (int j = 0; j < U; ++j)
-      if (v + j * kLpThreads < hi) u[j] = ld_stream16(vec + v + j * kLpThreads);
+      if (v + j * kBwdThreads < hi) u[j] = ld_stream16(vec + v + j * kBwdThreads);
 #pragma unroll
     for (int j = 0; j < U; ++j)
-      if (v + j * kLpThreads < hi) {
+      if (v + j * kBwdThreads < hi) {
         float f[N];
         Vec<BF16>::unpack(u[j], f);
 #pragma unroll
@@ -803,7 +807,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_bwd(LogprobBwdPar
                          pack_bf16(f[N - 2], f[N - 1]));
         else
           o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-        __stcs(ovec + v + j * kLpThreads, o);
+        __stcs(ovec + v + j * kBwdThreads, o);
       }
   }
   auto store = [&](int64_t col, float x) {
@@ -817,7 +821,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_bwd(LogprobBwdPar
   if (last && nvec * N + t < p.lg.vocab) store(nvec * N + t, grad(logit_at<BF16>(p.lg, row, nvec * N + t)));
   __syncthreads();
   // The given tokens of this part: written over, whole, and rounded once.
-  for (int j = t; j < given; j += kLpThreads) {
+  for (int j = t; j < given; j += kBwdThreads) {
     const int32_t id = s_id[j];
     if (id < c0 || id >= c1) continue;
     float g = 0.0f;
@@ -934,10 +938,10 @@ sv_status_t spec_verify_token_logprobs_backward(const void* logits, sv_dtype_t d
   if (e != cudaSuccess) return cuda_failure(e);
   const LogprobBwdParams p{LogitsView{logits, dtype, ld, rows, vocab},
                            ids, num_ids, ldi, row_temp, row_max, log_z, entropy, top_ids, top_k, g_logprob,
-                           g_entropy, g_top, dlogits, ldd, row_splits(rows, vocab, bf16, 4 * dev.sms)};
+                           g_entropy, g_top, dlogits, ldd, row_splits(rows, vocab, bf16, 32 * dev.sms)};
   const dim3 grid(static_cast<unsigned>(rows * p.splits));
-  e = bf16 ? launch_pdl(k_token_logprobs_bwd<true>, grid, dim3(kLpThreads), 0, stream, p)
-           : launch_pdl(k_token_logprobs_bwd<false>, grid, dim3(kLpThreads), 0, stream, p);
+  e = bf16 ? launch_pdl(k_token_logprobs_bwd<true>, grid, dim3(kBwdThreads), 0, stream, p)
+           : launch_pdl(k_token_logprobs_bwd<false>, grid, dim3(kBwdThreads), 0, stream, p);
   return e == cudaSuccess ? SV_OK : cuda_failure(e);
 }
 
