@@ -557,9 +557,24 @@ def _on(stream):
     return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call_stream(stream, device) -> int:
     """The handle of the given stream, or of the device's current one."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)  # the same handle without a stream object around it
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _need(t, name: str, dtype, numel: int, device, index: int):
+    """_arg for tensors that are used often: the checks in their cheap forms, the full ones only to say what is wrong."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.numel() >= numel
+            and t.is_contiguous()):
+        return
+    _arg(t, name, dtype, numel, device)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -595,7 +610,7 @@ class PagedKvCache:
         batch, pages = page_table.shape
         _rows_arg(page_table, "page_table", torch.int32, batch, pages, k.device)
         self.k, self.v, self.page_table = k, v, page_table
-        self.device, self.dtype, self.batch = k.device, k.dtype, batch
+        self.device, self.dtype, self.batch, self.index = k.device, k.dtype, batch, k.get_device()
         self.heads, self.head_dim = k.shape[3], k.shape[4]
         st = [x if n > 1 else 0 for x, n in zip(k.stride(), k.shape)]  # an axis of one entry has no step
         self.struct = SvKvCache(k.data_ptr(), v.data_ptr(), SV_BF16 if k.dtype == torch.bfloat16 else SV_F32,
@@ -633,7 +648,13 @@ def attention_workspace(batch: int, max_len: int, cache: PagedKvCache, num_heads
     return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
-def _head_rows(t, name, rows, heads, dim, dtype, device):
+def _head_rows(t, name, rows, heads, dim, dtype, device, index):
+    """Checks t [>= rows, heads, dim]; returns its row and head strides (an axis of one entry has no step)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 3:
+        n, h, d = t.shape
+        a, b, c = t.stride()
+        if n >= rows and h == heads and d == dim and (c == 1 or d == 1):
+            return (a if n > 1 else 0), (b if h > 1 else 0)
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError("%s must be a 3-D torch tensor [rows, heads, head_dim]" % name)
     if t.device != device:
@@ -644,11 +665,6 @@ def _head_rows(t, name, rows, heads, dim, dtype, device):
         raise ValueError("%s is %s; the call needs [%d, %d, %d]" % (name, tuple(t.shape), rows, heads, dim))
     if dim > 1 and t.stride(2) != 1:
         raise ValueError("%s: head_dim must be dense" % name)
-
-
-def _steps(t):
-    """Row and head strides; an axis of one entry has no step."""
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
 
 
 def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len: Optional[int] = None,
@@ -664,14 +680,14 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
     scale defaults to 1 / sqrt(head_dim)."""
     lib = load_library()
     _require_cache(cache)
-    dev = cache.device
+    dev, index = cache.device, cache.index
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D torch tensor [rows, heads, head_dim]")
     rows, heads, dim = q.shape
-    _head_rows(q, "q", rows, heads, cache.head_dim, cache.dtype, dev)
-    _arg(seq_lens, "seq_lens", torch.int64, 0, dev)
+    q_steps = _head_rows(q, "q", rows, heads, cache.head_dim, cache.dtype, dev, index)
     if seq_lens is None:
         raise ValueError("seq_lens is required")
+    _need(seq_lens, "seq_lens", torch.int64, 0, dev, index)
     batch = seq_lens.numel()
     if cache.batch < batch:
         raise ValueError("page_table has %d rows; the call reads %d" % (cache.batch, batch))
@@ -679,26 +695,34 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
         if cu_seqlens is not None:
             raise ValueError("max_len is required with cu_seqlens")
         max_len = rows // batch if batch else 1
-    if cu_seqlens is None and batch and rows < batch * max_len:
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, dev, index)
+    elif rows < batch * max_len:
         raise ValueError("q has %d rows; the call reads %d" % (rows, batch * max_len))
-    _arg(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, dev)
-    _arg(row_slots, "row_slots", torch.int64, rows, dev)
-    _arg(mask, "mask", torch.uint8, batch * max_len * max_len, dev)
+    if row_slots is not None:
+        _need(row_slots, "row_slots", torch.int64, rows, dev, index)
+    if mask is not None:
+        _need(mask, "mask", torch.uint8, batch * max_len * max_len, dev, index)
     if out is None or ws is None:
         with _on(stream):
             if out is None:
                 out = AttentionOutputs.allocate(rows, heads, dim, batch, cache.dtype, dev)
             if ws is None:
                 ws = attention_workspace(batch, max_len, cache, heads)
-    _head_rows(out.out, "out.out", rows, heads, dim, cache.dtype, dev)
-    _arg(out.lse, "out.lse", torch.float32, rows * heads, dev)
-    _arg(out.dev_status, "out.dev_status", torch.int32, batch, dev)
-    _check_ws(ws, dev)
-    _check("spec_verify_paged_attention", lib.spec_verify_paged_attention(
-        q.data_ptr(), *_steps(q), heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
+    o, lse, status = out.out, out.lse, out.dev_status
+    o_steps = _head_rows(o, "out.out", rows, heads, dim, cache.dtype, dev, index)
+    if lse is not None:
+        _need(lse, "out.lse", torch.float32, rows * heads, dev, index)
+    if status is not None:
+        _need(status, "out.dev_status", torch.int32, batch, dev, index)
+    _need(ws, "ws", torch.uint8, 0, dev, index)
+    code = lib.spec_verify_paged_attention(
+        q.data_ptr(), q_steps[0], q_steps[1], heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
         seq_lens.data_ptr(), _addr(row_slots), _addr(mask), dim ** -0.5 if scale is None else scale,
-        out.out.data_ptr(), *_steps(out.out), _addr(out.lse), _addr(out.dev_status),
-        ws.data_ptr(), ws.numel(), _call_stream(stream, dev)))
+        o.data_ptr(), o_steps[0], o_steps[1], _addr(lse), _addr(status), ws.data_ptr(), ws.numel(),
+        _call_stream(stream, dev))
+    if code:
+        _check("spec_verify_paged_attention", code)
     return out
 
 
@@ -708,22 +732,24 @@ def kv_commit(cache: PagedKvCache, commit_cu, commit_src_slot, commit_dst_pos, *
     (VerifyOutputs.commit_cu / commit_src_slot / commit_dst_pos).  Returns the requests' status bits [batch]."""
     lib = load_library()
     _require_cache(cache)
-    dev = cache.device
+    dev, index = cache.device, cache.index
     if commit_cu is None or commit_src_slot is None or commit_dst_pos is None:
         raise ValueError("commit_cu, commit_src_slot and commit_dst_pos are required")
-    _arg(commit_cu, "commit_cu", torch.int32, 1, dev)
+    _need(commit_cu, "commit_cu", torch.int32, 1, dev, index)
     batch = commit_cu.numel() - 1
     if cache.batch < batch:
         raise ValueError("page_table has %d rows; the call reads %d" % (cache.batch, batch))
-    _arg(commit_src_slot, "commit_src_slot", torch.int64, 0, dev)
-    _arg(commit_dst_pos, "commit_dst_pos", torch.int64, 0, dev)
+    _need(commit_src_slot, "commit_src_slot", torch.int64, 0, dev, index)
+    _need(commit_dst_pos, "commit_dst_pos", torch.int64, 0, dev, index)
     if dev_status is None:
         with _on(stream):
             dev_status = torch.empty(batch, dtype=torch.int32, device=dev)
-    _arg(dev_status, "dev_status", torch.int32, batch, dev)
-    _check("spec_verify_kv_commit", lib.spec_verify_kv_commit(
+    _need(dev_status, "dev_status", torch.int32, batch, dev, index)
+    code = lib.spec_verify_kv_commit(
         cache.ref, batch, max_len, min(commit_src_slot.numel(), commit_dst_pos.numel()), commit_cu.data_ptr(),
-        _addr(commit_src_slot), _addr(commit_dst_pos), _addr(dev_status), _call_stream(stream, dev)))
+        commit_src_slot.data_ptr(), commit_dst_pos.data_ptr(), dev_status.data_ptr(), _call_stream(stream, dev))
+    if code:
+        _check("spec_verify_kv_commit", code)
     return dev_status
 
 
@@ -754,14 +780,17 @@ def logprobs_workspace(n: int, vocab: int, top_k: int = 0, device=None) -> torch
     return torch.zeros(b, dtype=torch.uint8, device=device or "cuda")
 
 
-def _given_ids(ids, n, device):
-    """ids as [n, num_ids] with dense rows; a 1-D array is one id a row."""
+def _given_ids(ids, n, device, index):
+    """ids as [n, num_ids] with dense rows (a 1-D array is one id a row): the tensor, num_ids and the row stride."""
     if not isinstance(ids, torch.Tensor) or ids.dim() not in (1, 2):
         raise ValueError("ids must be a 1-D or 2-D torch tensor")
     if ids.dim() == 1:
         ids = ids.unsqueeze(1)
-    _rows_arg(ids, "ids", torch.int32, n, 0, device)
-    return ids, ids.shape[1], (ids.stride(0) if n > 1 else max(ids.shape[1], 1))
+    m, num = ids.shape
+    a, b = ids.stride()
+    if not (ids.dtype is torch.int32 and ids.get_device() == index and m >= n and (b == 1 or num <= 1)):
+        _rows_arg(ids, "ids", torch.int32, n, 0, device)
+    return ids, num, (a if n > 1 else max(num, 1))
 
 
 def token_logprobs(logits, ids, *, top_k: int = 0, row_index=None, row_temp=None, out=None, ws=None,
@@ -774,34 +803,34 @@ def token_logprobs(logits, ids, *, top_k: int = 0, row_index=None, row_temp=None
     lib = load_library()
     _require_cuda(logits)
     rows, V = logits.shape
-    dev = logits.device
+    dev, index = logits.device, logits.get_device()
     if row_index is None:
         n = rows
     else:
-        _arg(row_index, "row_index", torch.int32, 0, dev)
+        _need(row_index, "row_index", torch.int32, 0, dev, index)
         n = row_index.numel()
-    ids, num_ids, ldi = _given_ids(ids, n, dev)
-    _arg(row_temp, "row_temp", torch.float32, n, dev)
+    ids, num_ids, ldi = _given_ids(ids, n, dev, index)
+    f32, i32 = torch.float32, torch.int32
+    if row_temp is not None:
+        _need(row_temp, "row_temp", f32, n, dev, index)
     if out is None or ws is None:
         with _on(stream):
             if out is None:
                 out = LogprobOutputs.allocate(n, num_ids, top_k, dev)
             if ws is None:
                 ws = logprobs_workspace(n, V, top_k, dev)
-    f32 = torch.float32
-    _arg(out.logprob, "out.logprob", f32, n * num_ids, dev)
-    _arg(out.entropy, "out.entropy", f32, n, dev)
-    _arg(out.row_max, "out.row_max", f32, n, dev)
-    _arg(out.log_z, "out.log_z", f32, n, dev)
-    _arg(out.top_ids, "out.top_ids", torch.int32, n * top_k, dev)
-    _arg(out.top_logprob, "out.top_logprob", f32, n * top_k, dev)
-    _arg(out.flags, "out.flags", torch.int32, n, dev)
-    _check_ws(ws, dev)
-    _check("spec_verify_token_logprobs", lib.spec_verify_token_logprobs(
+    res = (out.logprob, out.entropy, out.row_max, out.log_z, out.top_ids, out.top_logprob, out.flags)
+    for t, name, dtype, numel in zip(res, ("logprob", "entropy", "row_max", "log_z", "top_ids", "top_logprob", "flags"),
+                                     (f32, f32, f32, f32, i32, f32, i32), (n * num_ids, n, n, n, n * top_k, n * top_k, n)):
+        if t is not None:
+            _need(t, "out." + name, dtype, numel, dev, index)
+    _need(ws, "ws", torch.uint8, 0, dev, index)
+    code = lib.spec_verify_token_logprobs(
         logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, n, _addr(row_index), ids.data_ptr(), num_ids,
-        ldi, _addr(row_temp), top_k, _addr(out.logprob), _addr(out.entropy), _addr(out.row_max), _addr(out.log_z),
-        _addr(out.top_ids), _addr(out.top_logprob), _addr(out.flags), ws.data_ptr(), ws.numel(),
-        _call_stream(stream, dev)))
+        ldi, _addr(row_temp), top_k, *[None if t is None else t.data_ptr() for t in res], ws.data_ptr(), ws.numel(),
+        _call_stream(stream, dev))
+    if code:
+        _check("spec_verify_token_logprobs", code)
     return out
 
 
@@ -815,30 +844,32 @@ def token_logprobs_backward(logits, ids, kept: LogprobOutputs, g_logprob, *, g_e
     lib = load_library()
     _require_cuda(logits)
     rows, V = logits.shape
-    dev, f32 = logits.device, torch.float32
-    ids, num_ids, ldi = _given_ids(ids, rows, dev)
-    _arg(g_logprob, "g_logprob", f32, rows * num_ids, dev)
-    _arg(g_entropy, "g_entropy", f32, rows, dev)
-    top_k = 0
+    dev, index, f32 = logits.device, logits.get_device(), torch.float32
+    ids, num_ids, ldi = _given_ids(ids, rows, dev, index)
+    top_ids, top_k = None, 0
     if g_top is not None:
         if not isinstance(g_top, torch.Tensor) or g_top.dim() != 2:
             raise ValueError("g_top must be a 2-D torch tensor")
-        top_k = g_top.shape[1]
-        _arg(g_top, "g_top", f32, rows * top_k, dev)
-        _arg(kept.top_ids, "kept.top_ids", torch.int32, rows * top_k, dev)
-        if kept.top_ids is not None and (kept.top_ids.dim() != 2 or kept.top_ids.shape[1] != top_k):
-            raise ValueError("kept.top_ids must have g_top's %d columns" % top_k)
-    _arg(row_temp, "row_temp", f32, rows, dev)
-    _arg(kept.row_max, "kept.row_max", f32, rows, dev)
-    _arg(kept.log_z, "kept.log_z", f32, rows, dev)
-    _arg(kept.entropy, "kept.entropy", f32, rows, dev)
+        top_ids, top_k = kept.top_ids, g_top.shape[1]
+        _need(g_top, "g_top", f32, rows * top_k, dev, index)
+        if top_ids is not None:
+            _need(top_ids, "kept.top_ids", torch.int32, rows * top_k, dev, index)
+            if top_ids.dim() != 2 or top_ids.shape[1] != top_k:
+                raise ValueError("kept.top_ids must have g_top's %d columns" % top_k)
+    for t, name, numel in ((g_logprob, "g_logprob", rows * num_ids), (g_entropy, "g_entropy", rows),
+                           (row_temp, "row_temp", rows), (kept.row_max, "kept.row_max", rows),
+                           (kept.log_z, "kept.log_z", rows), (kept.entropy, "kept.entropy", rows)):
+        if t is not None:
+            _need(t, name, f32, numel, dev, index)
     if out is None:
         per = 16 // logits.element_size()
         with _on(stream):
             out = torch.empty(rows, -(-V // per) * per, dtype=logits.dtype, device=dev)[:, :V]
     _rows_arg(out, "out", logits.dtype, rows, V, dev)
-    _check("spec_verify_token_logprobs_backward", lib.spec_verify_token_logprobs_backward(
+    code = lib.spec_verify_token_logprobs_backward(
         logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, ids.data_ptr(), num_ids, ldi, _addr(row_temp),
-        _addr(kept.row_max), _addr(kept.log_z), _addr(kept.entropy), _addr(kept.top_ids) if top_k else None, top_k,
-        _addr(g_logprob), _addr(g_entropy), _addr(g_top), out.data_ptr(), _row_step(out), _call_stream(stream, dev)))
+        _addr(kept.row_max), _addr(kept.log_z), _addr(kept.entropy), _addr(top_ids), top_k, _addr(g_logprob),
+        _addr(g_entropy), _addr(g_top), out.data_ptr(), _row_step(out), _call_stream(stream, dev))
+    if code:
+        _check("spec_verify_token_logprobs_backward", code)
     return out
