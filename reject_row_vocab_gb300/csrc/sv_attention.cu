@@ -161,186 +161,6 @@ struct SimtEngine {
 };
 
 // ---------------------------------------------------------------------------------------------------------------------
-// Engine: bf16 matrix instructions (16 x 8 x 16, fp32 accumulators).  WR row groups of 16 rows times WK key groups of
-// KT / WK keys, a warp each; a warp keeps the scores, weights and O of its rows in registers, so the only exchange is
-// the join of the key groups at the end of a unit.  Few rows are spread over the keys, many over the rows.
-// ---------------------------------------------------------------------------------------------------------------------
-
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <int DP, int WR>
-struct MmaEngine {
-  static constexpr bool kBf16 = true;
-  static constexpr int kDP = DP;
-  static constexpr int WK = 4 / WR, MT = 16 * WR, KT = 64, THREADS = 128;
-  static constexpr int ROW = DP * 2, STAGE = 2 * KT * ROW;
-  static constexpr int STAGES = DP == 64 ? 5 : 3;
-  static constexpr int EXTRA = MT * ROW;  // Q
-  static constexpr int NK = KT / WK;      // keys of a warp
-  static constexpr int NT = NK / 8, DT = DP / 8, KS = DP / 16;
-  static constexpr bool kQRegs = DP <= 128;  // Q stays in registers (wider heads fetch it from shared memory)
-
-  float m[2], l[2];
-  float o[DT][4];
-  uint32_t qf[kQRegs ? KS : 1][4];
-  uint32_t q_addr;  // this lane's row of Q for ldmatrix
-
-  __device__ static int piece(int row, int c) { return row * ROW + ((c ^ (row & 7)) << 4); }
-  __device__ static int row_group() { return (threadIdx.x >> 5) % WR; }
-  __device__ static int key_group() { return (threadIdx.x >> 5) / WR; }
-
-  __device__ void load_q(int ks, uint32_t (&a)[4]) const {
-    const int lane = threadIdx.x & 31;
-    const int row = row_group() * 16 + (lane & 15);
-    ldmatrix4(q_addr + piece(row, ks * 2 + (lane >> 4)), a);
-  }
-
-  __device__ void init(const AttnParams& p, const AttnRequest& r, int hkv, int rt, char* extra) {
-    const int rows = r.n * p.group;
-    for (int x = threadIdx.x; x < MT * (DP / 8); x += THREADS) {
-      const int row = x / (DP / 8), c = x % (DP / 8), grow = rt * MT + row;
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (grow < rows && c * 8 < p.c.head_dim) {
-        const int64_t at = (r.row0 + grow / p.group) * p.q_row + (hkv * p.group + grow % p.group) * p.q_head + c * 8;
-        u = *reinterpret_cast<const uint4*>(p.q + at * 2);
-      }
-      *reinterpret_cast<uint4*>(extra + piece(row, c)) = u;
-    }
-    q_addr = smem_addr(extra);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) m[i] = -kInfF, l[i] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    __syncthreads();
-    if (kQRegs)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) load_q(ks, qf[kQRegs ? ks : 0]);
-  }
-
-  __device__ void tile(const AttnParams& p, const AttnRequest& r, int b, int rt, int x0, const char* stage,
-                       const uint32_t* valid) {
-    const int lane = threadIdx.x & 31;
-    const int k0 = key_group() * NK;  // first key of the warp within the tile
-    const uint32_t ks_addr = smem_addr(stage), vs_addr = ks_addr + KT * ROW;
-    const int mi = lane >> 3, mr = lane & 7;
-    float s[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      uint32_t a[4];
-      if (kQRegs) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = qf[kQRegs ? ks : 0][i];
-      } else {
-        load_q(ks, a);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; nt += 2) {
-        uint32_t kb[4];
-        ldmatrix4(ks_addr + piece(k0 + nt * 8 + (mi >> 1) * 8 + mr, ks * 2 + (mi & 1)), kb);
-        mma_bf16(s[nt], a, kb[0], kb[1]);
-        mma_bf16(s[nt + 1], a, kb[2], kb[3]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[i][c] *= p.scale_log2;
-    const int row_lo = row_group() * 16 + (lane >> 2);
-    // valid: a bit for each of the tile's keys
-    const bool masked = (valid[0] & valid[1]) != 0xffffffffu || x0 + KT > r.len;
-    if (masked) {
-      constexpr int W = NK > 32 ? 2 : 1;  // the words of 32 keys that hold the warp's
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = (rt * MT + row_lo + h * 8) / p.group;
-        uint32_t see[W];
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-          see[w] = row_sees_of(p, r, b, row, x0 + (k0 & ~31) + w * 32, valid[(k0 >> 5) + w]) >> (k0 & 31);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (!(see[i / 4] >> (i % 4 * 8 + (lane & 3) * 2 + c) & 1u)) s[i][h * 2 + c] = -kInfF;
-      }
-    }
-    float alpha[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = m[h];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) mx = fmax_nan(mx, fmax_nan(s[i][h * 2], s[i][h * 2 + 1]));
-      mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float ref = mx == -kInfF ? 0.0f : mx;
-      alpha[h] = ex2_fast(m[h] - ref);
-      m[h] = mx;
-      l[h] *= alpha[h];
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float x = ex2_fast(s[i][h * 2 + c] - ref);
-          s[i][h * 2 + c] = x;
-          l[h] += x;
-        }
-    }
-    // O moves to the new maximum only when one of the warp's rows has a new one.
-    if (__any_sync(0xffffffffu, !(alpha[0] == 1.0f && alpha[1] == 1.0f))) {
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        o[i][0] *= alpha[0], o[i][1] *= alpha[0];
-        o[i][2] *= alpha[1], o[i][3] *= alpha[1];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j) {
-      const uint32_t a[4] = {pack_bf16(s[2 * j][0], s[2 * j][1]), pack_bf16(s[2 * j][2], s[2 * j][3]),
-                             pack_bf16(s[2 * j + 1][0], s[2 * j + 1][1]), pack_bf16(s[2 * j + 1][2], s[2 * j + 1][3])};
-#pragma unroll
-      for (int dt = 0; dt < DT; dt += 2) {
-        uint32_t vb[4];
-        ldmatrix4_trans(vs_addr + piece(k0 + j * 16 + (mi & 1) * 8 + mr, dt + (mi >> 1)), vb);
-        mma_bf16(o[dt], a, vb[0], vb[1]);
-        mma_bf16(o[dt + 1], a, vb[2], vb[3]);
-      }
-    }
-  }
-
-  __device__ void dump(float* so, float* sm, float* sl) {
-    const int lane = threadIdx.x & 31, wk = key_group();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float sum = l[h];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int row = wk * MT + row_group() * 16 + (lane >> 2) + h * 8;
-      if ((lane & 3) == 0) sm[row] = m[h], sl[row] = sum;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-        *reinterpret_cast<float2*>(so + row * DP + dt * 8 + (lane & 3) * 2) = make_float2(o[dt][h * 2], o[dt][h * 2 + 1]);
-    }
-  }
-};
-
-// ---------------------------------------------------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------------------------------------------------
 
@@ -544,12 +364,7 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
 cudaError_t launch_attention(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   const int dim = p.c.head_dim;
   const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
-  if (p.c.es == 2) {
-    if (dim <= 128) return rows <= 16 ? launch_attention_few(p, dev, stream) : launch_attention_wide(p, dev, stream);
-    // row tiles of 16, 32 or 64: the smallest that holds a request's rows, so that few rows leave their warps to the keys
-    return rows <= 16 ? launch<MmaEngine<256, 1>>(p, dev, stream)
-                      : rows <= 32 ? launch<MmaEngine<256, 2>>(p, dev, stream) : launch<MmaEngine<256, 4>>(p, dev, stream);
-  }
+  if (p.c.es == 2) return rows <= 16 ? launch_attention_few(p, dev, stream) : launch_attention_wide(p, dev, stream);
   return dim <= 64 ? launch<SimtEngine<64>>(p, dev, stream)
                    : dim <= 128 ? launch<SimtEngine<128>>(p, dev, stream) : launch<SimtEngine<256>>(p, dev, stream);
 }
@@ -579,20 +394,20 @@ EncodeTiledFn encode_tiled() {
 // Boxes need pages of a multiple of eight rows (the swizzle's period); a layout the driver takes no map of has none.
 KvMaps kv_maps(const KvView& c) {
   KvMaps m{};
-  int rows = 32;
+  int rows = kKeys;
   while (rows >= 8 && c.page_size % rows != 0) rows /= 2;
   const EncodeTiledFn encode = encode_tiled();
   if (rows < 8 || !encode) return m;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.heads),
                               static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
   // an axis of one entry may come without a step
-  auto step = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s : (c.head_dim + 7) / 8 * 8) * 2; };
+  auto step = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s * c.es : (c.head_dim * c.es + 15) / 16 * 16); };
   const cuuint64_t strides[3] = {step(c.head_stride), step(c.slot_stride), step(c.page_stride)};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {128u / c.es, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
   char* const base[2] = {c.k, c.v};
   CUtensorMap* const map[2] = {&m.k, &m.v};
   for (int i = 0; i < 2; ++i)
-    if (encode(map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base[i], dims, strides, box, ones,
+    if (encode(map[i], c.es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base[i], dims, strides, box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return m;

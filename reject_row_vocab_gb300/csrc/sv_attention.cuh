@@ -103,6 +103,27 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Matrix instructions' fragments: four 8 x 8 blocks of 16-bit values, and the product of 16 x 16 by 16 x 8 on top of c.
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // Whether new row i sees new row j of the same request.
 __device__ __forceinline__ bool row_sees(const AttnParams& p, int b, int i, int j) {
   if (!p.mask) return j <= i;
@@ -380,8 +401,6 @@ __device__ __forceinline__ int attn_owner(const AttnSpan& sp, int64_t place) {
   return static_cast<int>(n / sp.total);
 }
 
-// After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
-// writes the rows.  T threads, a warp or the block, of which this is thread t; s_last is shared.
 // Joins parts c0 .. c1 of a unit and writes its rows: E quads of columns a thread, PARTS parts in flight; a part's m, l
 // and O are fetched together, and the running maximum moves as they come.
 template <bool BF16, int MT, int DP, int T, int E, int PARTS>
@@ -437,6 +456,8 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, const AttnSe
   }
 }
 
+// After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
+// writes the rows.  T threads, a warp or the block, of which this is thread t; s_last is shared.
 template <bool BF16, int MT, int DP, int T>
 __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
                                           int* s_last) {

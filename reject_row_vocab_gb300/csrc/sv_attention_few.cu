@@ -1,5 +1,5 @@
 // Attention over the paged cache for few query rows (a decoded token's heads, a
-// short chain's): bf16, heads of up to 128, tiles of 16 rows and 128 keys.
+// short chain's): bf16, tiles of 16 rows and 128 keys.
 //
 // Bound by the bytes of K and V: of the 16 x 8 x 16 matrix instructions' rows
 // most are often empty, and their rate is still not what limits.  So the layout
@@ -23,36 +23,21 @@ constexpr int kTakers = 8;                                      // warps that ta
 constexpr int kFewThreads = 32 * (kTakers + kLoadWarps + 2);    // and a warp each to plan, to load Q
 constexpr int kUnitPlaces = 1;                                  // what a unit costs beside its key tiles, in tiles
 
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <int DP>
+// Heads of up to 64 (CB 1), 128 (CB 2) and 256 (CB 2, H 2) columns.  With H of 2 a warp has the scores of 32 keys and one
+// entry's columns of O: the scores are taken twice, O would not fit the registers otherwise.
+template <int CB, int H>
 struct Few {
-  static constexpr int kRing = DP == 128 ? 5 : 10;  // tiles in the ring
-  using R = KvRing<DP, kRing>;
-  static constexpr int DT = DP / 8, KS = DP / 16;
+  static constexpr int kRing = CB == 2 ? 5 : 10;  // entries in the ring
+  using R = KvRing<2, CB, kRing, H>;
+  static constexpr int kCols = CB * 64, kDP = kCols * H;
+  static constexpr int kGroups = kTakers / H;        // key groups
+  static constexpr int kOwn = kKeys / kGroups;       // keys of a warp
+  static constexpr int DT = kCols / 8, KS = kCols / 16, NT = kOwn / 8;
   static constexpr int kStage = (DT + 1) * 32 * 16;  // a warp's O, m and l
   // shared memory: the ring; two Qs of 16 rows; half the warps' results; the warps' flags; the meeting point; last; split segments
   static constexpr int kQBlock = 2 * kRows * 128;
   static constexpr int kQ = (R::kBytes + 1023) / 1024 * 1024;
-  static constexpr int kStages = kQ + kQBlock * (DP / 64);
+  static constexpr int kStages = kQ + kQBlock * CB * H;
   static constexpr int kFlags = kStages + kTakers / 2 * kStage;
   static constexpr int kMeet = kFlags + 2 * kTakers * 8;
   static constexpr int kParts = kMeet + 4 * 8;  // (behind two barriers, one for each part)
@@ -60,12 +45,12 @@ struct Few {
 };
 
 // What the products left out (see sv_attention.cuh), added by a warp to the rows that it has just written: to its part of
-// the unit, or, without one, to the output.
-template <int DP>
-__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, float* part) {
+// the unit, or, without one, to the output.  Columns d0 .. d0 + COLS - 1.
+template <int COLS>
+__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, int d0, float* part) {
   __syncwarp();
-  for (int x = threadIdx.x & 31; x < min(rows, kRows) * (DP / 4); x += 32) {
-    const int row = x / (DP / 4), d = x % (DP / 4) * 4, grow = s.rt * kRows + row, i = grow / p.group;
+  for (int x = threadIdx.x & 31; x < min(rows, kRows) * (COLS / 4); x += 32) {
+    const int row = x / (COLS / 4), d = d0 + x % (COLS / 4) * 4, grow = s.rt * kRows + row, i = grow / p.group;
     if (d >= p.c.head_dim) continue;
     const float4 f = nonfinite_seen<true, kKeys>(p, s, i, d);
     if (part) {
@@ -82,12 +67,12 @@ __device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegmen
   __syncwarp();
 }
 
-template <int DP>
+template <int CB, int H>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_attention_few(const AttnParams p, const __grid_constant__ KvMaps maps) {
-  using W = Few<DP>;
+  using W = Few<CB, H>;
   using R = typename W::R;
-  constexpr int DT = W::DT, KS = W::KS;
+  constexpr int DT = W::DT, KS = W::KS, NT = W::NT, DP = W::kDP;
   extern __shared__ __align__(1024) char smem[];
   R ring(smem);
   const uint32_t base = smem_addr(smem);
@@ -100,7 +85,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (t == 0) {
     ring.init(kTakers, kTakers + kLoadWarps + 1, kTakers);
     mbar_init(bar_meet, 32 * kTakers);
-    for (int i = 0; i < 2; ++i) mbar_init(bar_part + i * 8, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar_part + i * 8, H);
     mbar_fence_init();
   }
   __syncthreads();
@@ -121,7 +106,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else if (warp >= kTakers) {
     ring.load(p, maps, warp - kTakers);
   } else {
-    const int k0 = warp * 16;                 // this warp's keys of a tile
+    const int group = warp % W::kGroups, part_of_row = warp / W::kGroups;  // its keys, its columns of O
+    const int k0 = group * W::kOwn, d0 = part_of_row * W::kCols;
     // What this lane addresses for ldmatrix within a tile (piece(row, column)): the pieces of a row further on differ from
     // it in bits 5 and 6 of the address, or by a block.
     const int mi = lane >> 3, mr = lane & 7;  // matrix and row
@@ -154,37 +140,47 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < s.cnt; ++i, ++g) {
         const int x0 = (s.t0 + i) * kKeys + k0;  // the warp's first key
-        if (!ring.wait(ring.full(2 * g), ring.phase(2 * g))) {
+        if (!ring.wait(ring.full(2 * H * g), ring.phase(2 * H * g))) {
           ok = false;
           break;
         }
-        const uint32_t good = ring.valid(g)[warp / 2] >> (k0 & 16) & 0xffffu;
-        bad |= ring.valid(g)[4 + warp / 2];
-        const uint32_t kt = ring.tile(2 * g) + k_at;
-        float sc[2][4];
+        const uint32_t all = W::kOwn == 32 ? 0xffffffffu : 0xffffu;
+        const uint32_t good = ring.valid(g)[k0 / 32] >> (k0 & 31) & all;
+        bad |= ring.valid(g)[4 + k0 / 32];
+        float sc[NT][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t qf[4];  // (Q stays in shared memory: O, the scores and Q do not fit the registers together)
-          ldmatrix4((q_at ^ (ks & 3) << 5) + (ks >> 2) * W::kQBlock, qf);
-          uint32_t kb[4];
-          ldmatrix4((kt ^ (ks & 3) << 5) + (ks >> 2) * R::kBlock, kb);
-          mma_bf16(sc[0], qf, kb[0], kb[1]);
-          mma_bf16(sc[1], qf, kb[2], kb[3]);
+        for (int h = 0; h < H; ++h) {
+          const uint32_t group_k = 2 * H * g + h;
+          if (h > 0 && !ring.wait(ring.full(group_k), ring.phase(group_k))) ok = false;
+          const uint32_t kt = ring.tile(group_k) + k_at;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t qf[4];  // (Q stays in shared memory: O, the scores and Q do not fit the registers together)
+            ldmatrix4((q_at ^ (ks & 3) << 5) + (h * CB + (ks >> 2)) * W::kQBlock, qf);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+              uint32_t kb[4];
+              ldmatrix4((kt ^ (ks & 3) << 5) + (ks >> 2) * R::kBlock + n * 1024, kb);
+              mma_bf16(sc[n], qf, kb[0], kb[1]);
+              mma_bf16(sc[n + 1], qf, kb[2], kb[3]);
+            }
+          }
+          done(ring.empty(group_k));
         }
-        done(ring.empty(2 * g));
+        if (!ok) break;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[n][c] *= p.scale_log2;
-        if (good != 0xffffu || x0 + 16 > s.r.len) {
+        if (good != all || x0 + W::kOwn > s.r.len) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int row = (s.rt * kRows + (lane >> 2) + h * 8) / p.group;
             const uint32_t see = row_sees_of(p, s.r, s.b, row, x0, good) >> ((lane & 3) * 2);
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c)
                 if (!(see >> (n * 8 + c) & 1u)) sc[n][h * 2 + c] = -kInfF;
@@ -195,7 +191,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int h = 0; h < 2; ++h) {
           float mx = m[h];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) mx = fmax_nan(mx, fmax_nan(sc[n][h * 2], sc[n][h * 2 + 1]));
+          for (int n = 0; n < NT; ++n) mx = fmax_nan(mx, fmax_nan(sc[n][h * 2], sc[n][h * 2 + 1]));
           mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float ref = mx == -kInfF ? 0.0f : mx;
@@ -203,7 +199,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           m[h] = mx;
           l[h] *= alpha[h];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float x = ex2_fast(sc[n][h * 2 + c] - ref);
@@ -219,29 +215,41 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             o[d][2] *= alpha[1], o[d][3] *= alpha[1];
           }
         }
-        if (!ring.wait(ring.full(2 * g + 1), ring.phase(2 * g + 1))) {
-          ok = false;
-          break;
-        }
-        if (s.r.n > 1 && x0 + 16 > s.r.len) {
-          char* v = ring.tile_mem(2 * g + 1);
-          bool found = false;
-#pragma unroll 1
-          for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < 16 * R::kPieces; x += 32)
-            if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(k0 + x / R::kPieces, x % R::kPieces)))) found = true;
-          careful = __any_sync(0xffffffffu, found) || careful;
-        }
-        const uint32_t vt = ring.tile(2 * g + 1) + v_at;
-        const uint32_t a[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
-                               pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
 #pragma unroll
-        for (int d = 0; d < DT; d += 2) {
-          uint32_t vb[4];
-          ldmatrix4_trans((vt ^ (d & 6) << 4) + (d >> 3) * R::kBlock, vb);
-          mma_bf16(o[d], a, vb[0], vb[1]);
-          mma_bf16(o[d + 1], a, vb[2], vb[3]);
+        for (int h = 0; h < H; ++h) {
+          const uint32_t group_v = 2 * H * g + H + h;
+          if (!ring.wait(ring.full(group_v), ring.phase(group_v))) {
+            ok = false;
+            break;
+          }
+          if (h != part_of_row) {  // (a warp that does not need the entry has still to know that it came)
+            done(ring.empty(group_v));
+            continue;
+          }
+          if (s.r.n > 1 && x0 + W::kOwn > s.r.len) {
+            char* v = ring.tile_mem(group_v);
+            bool found = false;
+#pragma unroll 1
+            for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < W::kOwn * R::kPieces; x += 32)
+              if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(k0 + x / R::kPieces, x % R::kPieces)))) found = true;
+            careful = __any_sync(0xffffffffu, found) || careful;
+          }
+          const uint32_t vt = ring.tile(group_v) + v_at;
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+            const uint32_t a[4] = {pack_bf16(sc[n][0], sc[n][1]), pack_bf16(sc[n][2], sc[n][3]),
+                                   pack_bf16(sc[n + 1][0], sc[n + 1][1]), pack_bf16(sc[n + 1][2], sc[n + 1][3])};
+#pragma unroll
+            for (int d = 0; d < DT; d += 2) {
+              uint32_t vb[4];
+              ldmatrix4_trans((vt ^ (d & 6) << 4) + (d >> 3) * R::kBlock + n * 1024, vb);
+              mma_bf16(o[d], a, vb[0], vb[1]);
+              mma_bf16(o[d + 1], a, vb[2], vb[3]);
+            }
+          }
+          done(ring.empty(group_v));
         }
-        done(ring.empty(2 * g + 1));
+        if (!ok) break;
       }
       if (!ok) break;
       done(ring.q_free(slot));
@@ -280,16 +288,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       };
       ok = true;
 #pragma unroll 1
-      for (int h = kTakers / 2; h > 0; h /= 2) {
-        if (warp >= h && warp < 2 * h) leave(stage(warp - h));
+      for (int h = W::kGroups / 2; h > 0; h /= 2) {
+        if (group >= h && group < 2 * h) leave(stage(part_of_row * (W::kGroups / 2) + group - h));
         ok = meet();
         if (!ok) break;
-        if (warp < h) take(stage(warp));
+        if (group < h) take(stage(part_of_row * (W::kGroups / 2) + group));
         ok = meet();
         if (!ok) break;
       }
       if (!ok) break;
-      if (warp == 0) {
+      if (group == 0) {
         uint32_t any = 0u, odd = 0u;
 #pragma unroll
         for (int w = 0; w < kTakers; ++w) any |= flags[w * 2], odd |= flags[w * 2 + 1];
@@ -305,27 +313,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const int i = grow / p.group, head = s.hkv * p.group + grow - i * p.group;
             const bool none = m[h] == -kInfF;  // nothing seen, or only scores of -inf
             const float inv = none ? 0.0f : 1.0f / l[h];
-            char* out = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head + (lane & 3) * 2) * 2;
+            char* out = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head + d0 + (lane & 3) * 2) * 2;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-              if (d * 8 < p.c.head_dim)
+              if (d0 + d * 8 < p.c.head_dim)
                 *reinterpret_cast<uint32_t*>(out + d * 16) = none ? 0u : pack_bf16(o[d][h * 2] * inv, o[d][h * 2 + 1] * inv);
-            if ((lane & 3) == 0 && p.lse) p.lse[(s.r.row0 + i) * p.heads + head] = none ? -kInfF : fmaf(m[h], kLn2, logf(l[h]));
+            if (d0 == 0 && (lane & 3) == 0 && p.lse) p.lse[(s.r.row0 + i) * p.heads + head] = none ? -kInfF : fmaf(m[h], kLn2, logf(l[h]));
           } else {
 #pragma unroll
             for (int d = 0; d < DT; ++d)  // quads of columns, a quad by two lanes
-              *reinterpret_cast<float2*>(part + ((d * 2 + (lane >> 1 & 1)) * kRows + row) * 4 + (lane & 1) * 2) =
+              *reinterpret_cast<float2*>(part + ((d0 / 4 + d * 2 + (lane >> 1 & 1)) * kRows + row) * 4 + (lane & 1) * 2) =
                   make_float2(o[d][h * 2], o[d][h * 2 + 1]);
-            if ((lane & 3) == 0) part[P::kM + row] = m[h], part[P::kL + row] = l[h];
+            if (d0 == 0 && (lane & 3) == 0) part[P::kM + row] = m[h], part[P::kL + row] = l[h];
           }
         }
         if (odd) {
-          add_nonfinite<DP>(p, s, rows, whole ? nullptr : part);
+          add_nonfinite<W::kCols>(p, s, rows, d0, whole ? nullptr : part);
         }
         if (whole) {
-          if (s.reports && lane == 0) p.status[s.b] = bad | attn_timeout(p);
+          if (s.reports && warp == 0 && lane == 0) p.status[s.b] = bad | attn_timeout(p);
         } else {
-          if (lane == 0) part[P::kStatus] = __uint_as_float(bad);
+          if (warp == 0 && lane == 0) part[P::kStatus] = __uint_as_float(bad);
           __threadfence();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_part + left++ * 8);
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   ring.report_abort(p);
 }
 
-template <int DP>
+template <int CB, int H>
 cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   static std::mutex mu;
   static bool have[64] = {};
@@ -349,21 +357,22 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!have[d]) {
-      e = cudaFuncSetAttribute(k_attention_few<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<DP>::kSmem);
+      e = cudaFuncSetAttribute(k_attention_few<CB, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<CB, H>::kSmem);
       if (e != cudaSuccess) return e;
       have[d] = true;
     }
   }
-  static_assert(Few<DP>::kSmem <= 227 * 1024, "shared memory of a block");
+  static_assert(Few<CB, H>::kSmem <= 227 * 1024, "shared memory of a block");
   const int grid = dev.sms < kAttnMaxBlocks ? dev.sms : kAttnMaxBlocks;
-  return launch_pdl(k_attention_few<DP>, dim3(static_cast<unsigned>(grid)), dim3(kFewThreads), Few<DP>::kSmem, stream, p,
+  return launch_pdl(k_attention_few<CB, H>, dim3(static_cast<unsigned>(grid)), dim3(kFewThreads), Few<CB, H>::kSmem, stream, p,
                     kv_maps(p.c));
 }
 
 }  // namespace
 
 cudaError_t launch_attention_few(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  return p.c.head_dim <= 64 ? launch<64>(p, dev, stream) : launch<128>(p, dev, stream);
+  const int dim = p.c.head_dim;
+  return dim <= 64 ? launch<1, 1>(p, dev, stream) : dim <= 128 ? launch<2, 1>(p, dev, stream) : launch<2, 2>(p, dev, stream);
 }
 
 }  // namespace sv

@@ -1,10 +1,14 @@
-// The ring that carries K and V to the attention kernels for bf16, and the warps around it: one that walks the line of
-// tiles ahead of the others (the plan), four that load, one that fetches the next unit's Q.  The kernels differ in who
-// consumes the tiles.
+// The ring that carries K and V to the attention kernels, and the warps around it: one that walks the line of tiles ahead
+// of the others (the plan), four that load, one that fetches the next unit's Q.  The kernels differ in who consumes the
+// tiles.
 //
-// A tile is 128 keys by DP (64 or 128) columns in blocks of 64 columns, 128 bytes a row, in the 128-byte swizzle that TMA
-// writes and the matrix unit reads: piece c (16 bytes) of row r lies at (c ^ r) % 8 of its row.  Tile g's K is group 2 g
-// of the ring, its V group 2 g + 1.
+// A tile is 128 keys.  Its rows are cut into H entries of CB blocks of 128 bytes (64 columns of bf16, 32 of fp32) in the
+// 128-byte swizzle that TMA writes and the matrix unit reads: piece c (16 bytes) of row r lies at (c ^ r) % 8 of its
+// block's row.  The entries of tile g are groups 2 H g + h (K) and 2 H g + H + h (V) of the ring.
+//
+// The history's rows come in boxes of a page's rows, all of an entry's issued by one warp: what a warp does for an entry
+// (find the pages, wait for room, issue) takes about a microsecond, and four entries are on their way at once.  New rows,
+// the history's last, odd page sizes' and all beside them are gathered row by row, by all loading warps together.
 #pragma once
 
 #include <cstdint>
@@ -18,7 +22,7 @@ namespace sv {
 constexpr int kKeys = 128;        // keys of a tile
 constexpr int kLoadWarps = 4;
 constexpr int kLoadThreads = 32 * kLoadWarps;
-constexpr int kPlans = 4;         // segments the plan is ahead by
+constexpr int kPlans = 8;         // segments the plan is ahead by
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -29,7 +33,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// K and V of the call's layer as [pages][page_size][heads][head_dim] tensors, in boxes of 64 columns of `rows` rows of a
+// K and V of the call's layer as [pages][page_size][heads][head_dim] tensors, in boxes of 128 bytes of `rows` rows of a
 // page (a power of two that divides the page's; 0: none, the pages are copied row by row).
 struct KvMaps {
   CUtensorMap k, v;
@@ -71,18 +75,23 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int DP, int NB>
+__device__ __forceinline__ void mbar_arrive_times(uint32_t bar, uint32_t times) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(times) : "memory");
+}
+
+template <int ES, int CB, int NB, int H, bool EARLY = false>
 struct KvRing {
-  static constexpr int kBlock = kKeys * 128;        // 128 rows of 64 columns
-  static constexpr int kTile = kBlock * (DP / 64);
-  static constexpr int kPieces = DP / 8;            // 16-byte pieces of a row
-  static constexpr int kInfo = 8;                   // tiles whose validity is kept
+  static constexpr int kBlock = kKeys * 128;        // 128 rows of 128 bytes
+  static constexpr int kTile = kBlock * CB;         // an entry
+  static constexpr int kPieces = CB * 8;            // 16-byte pieces of an entry's row
+  static constexpr int kEach = 16 / ES;             // elements of a piece
+  static constexpr int kInfo = 16;                  // tiles whose validity is kept
   // shared memory of the ring: the tiles, and behind them
   static constexpr int kValid = NB * kTile;                      // uint32 [kInfo][8]: four valid words, four bad
   static constexpr int kPlan = kValid + kInfo * 8 * 4;           // AttnSegment [kPlans]
   static constexpr int kBars = kPlan + kPlans * static_cast<int>(sizeof(AttnSegment));
-  // full, empty [NB], plan, read [kPlans], q, q free [2]
-  static constexpr int kSums = kBars + (2 * NB + 2 * kPlans + 4) * 8;  // int64 [34]: sums [32], find [2]
+  // full, empty [NB], plan, read [kPlans], q, q free [2], open [2 NB]
+  static constexpr int kSums = kBars + (4 * NB + 2 * kPlans + 4) * 8;  // int64 [34]: sums [32], find [2]
   static constexpr int kAbort = kSums + 34 * 8;
   static constexpr int kBytes = kAbort + 16;
 
@@ -99,6 +108,7 @@ struct KvRing {
   __device__ uint32_t read_bar(uint32_t i) const { return base + kBars + (2 * NB + kPlans + i % kPlans) * 8; }
   __device__ uint32_t q_bar(int i) const { return base + kBars + (2 * NB + 2 * kPlans + i) * 8; }
   __device__ uint32_t q_free(int i) const { return base + kBars + (2 * NB + 2 * kPlans + 2 + i) * 8; }
+  __device__ uint32_t open(uint32_t i) const { return base + kBars + (2 * NB + 2 * kPlans + 4 + i % (2 * NB)) * 8; }
   __device__ static uint32_t phase(uint32_t group) { return group / NB & 1; }
   __device__ uint32_t tile(uint32_t group) const { return base + group % NB * kTile; }
   __device__ char* tile_mem(uint32_t group) const { return mem + group % NB * kTile; }
@@ -114,8 +124,10 @@ struct KvRing {
 
   // By one thread: empties: arrivals that free a tile, readers: warps that read the plan, q_frees: arrivals that free a Q.
   __device__ void init(int empties, int readers, int q_frees) const {
-    for (int i = 0; i < NB; ++i) mbar_init(full(i), kLoadThreads), mbar_init(empty(i), empties);
+    for (int i = 0; i < NB; ++i) mbar_init(full(i), 2 * kLoadThreads), mbar_init(empty(i), empties);
+    for (int i = 0; i < 2 * NB; ++i) mbar_init(open(i), 1);
     for (int i = 0; i < kPlans; ++i) mbar_init(plan_bar(i), 1), mbar_init(read_bar(i), readers);
+    for (int i = 0; i < kInfo * 8; ++i) valid(0)[i] = 0u;
     for (int i = 0; i < 2; ++i) mbar_init(q_bar(i), 32), mbar_init(q_free(i), q_frees);
     *abort() = 0;
   }
@@ -175,85 +187,219 @@ struct KvRing {
     return __shfl_sync(0xffffffffu, split, 0);
   }
 
-  // Loading warp lw.  A warp has 32 of a tile's keys, a lane one key's place, handed round by shuffles; the word that
-  // places a lane's key of the next tile is on its way while this tile is copied.
-  __device__ void load(const AttnParams& p, const KvMaps& maps, int lw) {
+  // What a loading warp knows of its next tile: the words that place the keys are long on their way.
+  struct Ahead {
+    int64_t word, box_word;  // of this lane's key, of this lane's box
+    uint32_t g;              // tiles before it
+    int x0, hkv;             // first key, cache head
+    int len, n;              // the request's; n 0: no more tiles
+    int boxed, row0, each;   // rows [0, boxed) come in boxes, the warp gathers rows row0 .. row0 + each - 1
+  };
+
+  // Rows of K or V, 32 keys' places being the lanes' `off`: the first `each` of them to the shared rows from dst on.
+  __device__ void gather(const AttnParams& p, uint32_t dst, const char* from, int h, int hkv, int64_t off, int each) const {
+    const int c = lane % kPieces, sub = lane / kPieces;
+    constexpr int kStep = 32 / kPieces;  // rows a warp copies at once
+    const char* src = from + (static_cast<int64_t>(hkv) * p.c.head_stride + c * kEach) * ES + h * CB * 128;
+    const bool in_head = (h * kPieces + c) * kEach < p.c.head_dim;
+    auto copy = [&](int i) {
+      const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
+      const bool live = o >= 0 && in_head;
+      cp_async16(dst + piece(i + sub, c), live ? src + o * ES : p.c.k, live);
+    };
+    if (each == 32) {
+#pragma unroll 8
+      for (int i = 0; i < 32; i += kStep) copy(i);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < each; i += kStep) copy(i);
+    }
+  }
+
+  // The end of a loading warp that went through `groups` groups: copies in flight end before the block does.
+  __device__ void drain(uint32_t groups) const {
+    cp_async_commit();
+    cp_async_wait<0>();
+    if (*abort())
+      for (uint32_t i = groups > NB ? groups - NB : 0; i < groups; ++i)
+        for (int n = 0; n < 100 && !mbar_try_wait_for(full(i), phase(i), 10000); ++n) {
+        }
+  }
+
+  // Loading warp lw where there are no boxes: a quarter of each tile's keys, a lane one key's place.
+  __device__ void load_rows(const AttnParams& p, int lw) {
     AttnSegment s{};
     bool more = next(s);
     int t = s.t0;
     int64_t word = more ? key_word(p, s.r, s.b, t * kKeys + lw * 32 + lane) : -1;
-    uint32_t q = 0;  // groups issued
-    bool ok = true;
-    const int c = lane % kPieces, sub = lane / kPieces;
-    constexpr int kStep = 32 / kPieces;  // rows a warp copies at once
-    const bool in_head = c * 8 < p.c.head_dim;
-    while (more && ok) {
-      const int x = t * kKeys + lw * 32 + lane;
+    uint32_t q = 0;  // groups gone through
+    for (bool ok = true; more && ok;) {
+      const int x = t * kKeys + lw * 32 + lane, hkv = s.hkv;
       const int64_t off = key_offset(p, s.r, x, word);
       const uint32_t good = __ballot_sync(0xffffffffu, off >= 0);
       const uint32_t bad = __ballot_sync(0xffffffffu, x < s.r.len + s.r.n && off < 0);
-      // a tile of history in boxes: this lane's box of the warp's 32 keys
-      const bool boxes = maps.rows > 0 && (t + 1) * kKeys <= s.r.len;
-      const int per = boxes ? 32 / maps.rows : 1;
-      const int box_row = boxes ? lane % per * maps.rows : 0, box_col = boxes ? lane / per : 0;
-      const int box_head = s.hkv;
-      const int64_t box_page = __shfl_sync(0xffffffffu, word, box_row);
-      const uint32_t box_key = static_cast<uint32_t>(t * kKeys + lw * 32 + box_row);
-      const uint32_t box_in = box_key - divide(box_key, p.c.div_mul, p.c.div_shift) * p.c.page_size;
-      const int64_t shift = (static_cast<int64_t>(s.hkv) * p.c.head_stride + c * 8) * 2;
+      const uint32_t g = q / (2 * H);
       if (++t >= s.t0 + s.cnt) {
         more = next(s);
         t = s.t0;
       }
       if (more) word = key_word(p, s.r, s.b, t * kKeys + lw * 32 + lane);
 #pragma unroll 1
-      for (int which = 0; which < 2; ++which, ++q) {
+      for (int e = 0; e < 2 * H; ++e, ++q) {
         if (q >= NB && !wait(empty(q), phase(q - NB))) {
           ok = false;
           break;
         }
-        if (which == 0 && lane == 0) {
-          valid(q >> 1)[lw] = good;
-          valid(q >> 1)[4 + lw] = bad;
-        }
-        const uint32_t dst = tile(q);
-        if (boxes) {
-          // (a page outside the cache is outside the tensor: the box is filled with zeros)
-          if (lane == 0)
-            mbar_arrive_expect_tx(full(q), 32 * 128 * (DP / 64));
-          else
-            mbar_arrive(full(q));
-          __syncwarp();
-          if (box_col < DP / 64)
-            box_copy(dst + box_col * kBlock + (lw * 32 + box_row) * 128, which ? &maps.v : &maps.k, box_col * 64, box_head,
-                     static_cast<int>(box_in), static_cast<int>(box_page), full(q));
-          continue;
-        }
-        const char* src = (which ? p.c.v : p.c.k) + shift;
-#pragma unroll 8
-        for (int i = 0; i < 32; i += kStep) {
-          const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
-          const bool live = o >= 0 && in_head;
-          cp_async16(dst + piece(lw * 32 + i + sub, c), live ? src + o * 2 : p.c.k, live);
-        }
+        if (e == 0 && lane == 0) valid(g)[lw] = good, valid(g)[4 + lw] = bad;
+        gather(p, tile(q) + lw * 32 * 128, e >= H ? p.c.v : p.c.k, e % H, hkv, off, 32);
         cp_async_arrive(full(q));  // when this thread's copies so far are in place
+        mbar_arrive(full(q));
       }
     }
-    cp_async_commit();
-    cp_async_wait<0>();
-    if (*abort())  // copies in flight end before the block does
-      for (uint32_t i = q > NB ? q - NB : 0; i < q; ++i)
-        for (int n = 0; n < 100 && !mbar_try_wait_for(full(i), phase(i), 10000); ++n) {
-        }
+    drain(q);
   }
 
-  // The warp that fetches Q: rows of up to MT query rows a unit (rows that do not exist are 0), 64-column blocks of
-  // `block` bytes at `at`, in the tiles' swizzle; slots Qs in turn, `slot_rows` rows apart.
+  // Loading warp lw with boxes.  A group is owned by the warp that is its number modulo the loading warps: it issues the
+  // boxes.  Rows that do not come in boxes are gathered by all of the warps.
+  // (A wait by parity is good where the barrier's phase before is known to be over, and where the next one cannot come
+  // before the wait is done.  No group comes that a warp has not had its part in.  That a group's place is free follows a
+  // wait for a group at most four before it; with that group, the place's own phase before is over, if the consumer frees
+  // K and V in order, or at most K of the tile behind V's before V.  Where the places are too few for that (EARLY), the
+  // owner waits, and opens the group to the others; the openings are gone through by every warp, and are twice as many as
+  // the places.)
+  __device__ void load(const AttnParams& p, const KvMaps& maps, int lw) {
+    if (maps.rows == 0) return load_rows(p, lw);
+    static_assert(NB >= kLoadWarps && kLoadWarps == 4, "parity of the places, owners of the groups");
+    AttnSegment s{};
+    bool more = next(s);
+    int t = s.t0;
+    uint32_t tiles = 0;
+    const int nb = kKeys / maps.rows;  // boxes of a block
+    const int box_row = lane % nb * maps.rows, box_col = lane / nb;
+    auto ahead = [&](Ahead& a) {
+      a.n = 0;
+      for (; more; ++t, ++tiles) {
+        if (t >= s.t0 + s.cnt) {
+          more = next(s);
+          t = s.t0;
+          if (!more) return;
+        }
+        a.x0 = t * kKeys;
+        a.boxed = max(min(s.r.len - a.x0, kKeys), 0) / maps.rows * maps.rows;
+        // (boxes alone: with one entry a row, two of the four warps own them)
+        if (a.boxed < kKeys || H > 1 || (tiles & 1) == (lw >> 1)) break;
+      }
+      if (!more) return;
+      ++t;
+      a.g = tiles++, a.hkv = s.hkv, a.len = s.r.len, a.n = s.r.n;
+      a.each = ((kKeys - a.boxed) / kLoadWarps + 7) & ~7;  // (eight rows are the swizzle's period)
+      a.row0 = min(a.boxed + lw * a.each, kKeys);
+      a.each = min(a.each, kKeys - a.row0);
+      if (a.boxed > 0) a.box_word = key_word(p, s.r, s.b, a.x0 + box_row);
+      if (a.boxed < kKeys) a.word = key_word(p, s.r, s.b, a.x0 + a.row0 + lane);
+    };
+    const int c = lane % kPieces, sub = lane / kPieces;
+    constexpr int kStep = 32 / kPieces;  // rows a warp copies at once
+    uint32_t last = 0, opened = 0;              // groups before the next tile's; openings so far
+    bool ok = true;
+    Ahead now;
+    ahead(now);
+    while (now.n > 0 && ok) {
+      const Ahead a = now;
+      ahead(now);
+      last = (a.g + 1) * 2 * H;
+      const bool whole = a.boxed == kKeys;
+      uint32_t good = 0u;  // lane j < 4: of keys 32 j .. 32 j + 31, those in boxes
+      if (a.boxed > 0) {
+        const uint32_t found = __ballot_sync(0xffffffffu, a.box_word >= 0 && a.box_word < p.c.pages && box_row < a.boxed);
+        for (int x = 0; x < 32; x += min(maps.rows, 32))
+          if (found >> ((lane & 3) * 32 + x) / maps.rows & 1u)
+            good |= (maps.rows >= 32 ? 0xffffffffu : (1u << maps.rows) - 1u) << x;
+      }
+      int64_t off = -1;
+      uint32_t there = 0u, missing = 0u;  // of the warp's own rows
+      if (!whole) {
+        AttnRequest r{};
+        r.len = a.len, r.n = a.n;
+        const int x = a.x0 + a.row0 + lane;
+        if (lane < a.each) off = key_offset(p, r, x, a.word);
+        there = __ballot_sync(0xffffffffu, off >= 0);
+        missing = __ballot_sync(0xffffffffu, lane < a.each && x < a.len + a.n && off < 0);
+      }
+      const uint32_t key = static_cast<uint32_t>(a.x0 + box_row);
+      const int in = static_cast<int>(key - divide(key, p.c.div_mul, p.c.div_shift) * p.c.page_size);
+#pragma unroll 1
+      for (int e = 0; e < 2 * H; ++e) {
+        const uint32_t q = a.g * 2 * H + e;
+        const int h = e % H;
+        const bool is_v = e >= H, own = q % kLoadWarps == lw;
+        if (!own && whole) continue;
+        if (q >= NB && (own || !EARLY) && !wait(empty(q), phase(q - NB))) {
+          ok = false;
+          break;
+        }
+        if (own) {
+          if (e == 0 && lane < 4) {
+            const int rest = a.boxed - lane * 32;  // of the word's keys, those that come in boxes
+            const uint32_t boxes = rest >= 32 ? 0xffffffffu : rest <= 0 ? 0u : (1u << rest) - 1u;
+            if (boxes) {
+              atomicOr(valid(a.g) + lane, good);
+              atomicOr(valid(a.g) + 4 + lane, boxes & ~good);
+            }
+          }
+          // words are put together from 0: here those of a tile whose place was read long ago
+          if (e == 0 && lane < 8) valid(a.g + kInfo / 2)[lane] = 0u;
+          if (a.boxed > 0) {
+            // (a page outside the cache is outside the tensor: the box is filled with zeros)
+            if (lane == 0) mbar_expect_tx(full(q), a.boxed * 128 * CB);
+            __syncwarp();
+            if (box_col < CB && box_row < a.boxed)
+              box_copy(tile(q) + box_col * kBlock + box_row * 128, is_v ? &maps.v : &maps.k,
+                       (h * CB + box_col) * (128 / ES), a.hkv, in, static_cast<int>(a.box_word), full(q));
+          }
+          if (whole) {
+            mbar_arrive_times(full(q), 2 * kLoadWarps);
+            continue;
+          }
+        }
+        if (EARLY && q >= NB) {
+          __syncwarp();
+          if (own && lane == 0) mbar_arrive(open(opened));
+          if (!wait(open(opened), opened / (2 * NB) & 1)) {
+            ok = false;
+            break;
+          }
+          ++opened;
+        }
+        if (e == 0 && lane == 0) {
+          uint32_t* v = valid(a.g) + (a.row0 >> 5);
+          const int shift = a.row0 & 31;
+          if (there << shift) atomicOr(v, there << shift);
+          if (missing << shift) atomicOr(v + 4, missing << shift);
+          if (shift && there >> (32 - shift)) atomicOr(v + 1, there >> (32 - shift));
+          if (shift && missing >> (32 - shift)) atomicOr(v + 5, missing >> (32 - shift));
+        }
+        if (a.x0 + a.row0 < a.len + a.n) {
+          gather(p, tile(q) + a.row0 * 128, is_v ? p.c.v : p.c.k, h, a.hkv, off, a.each);
+        } else if (is_v) {  // a weight of 0 times what lay there before has to be 0 (a score of it is masked)
+#pragma unroll 1
+          for (int i = 0; i < a.each; i += kStep)
+            *reinterpret_cast<uint4*>(tile_mem(q) + piece(a.row0 + i + sub, c)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        cp_async_arrive(full(q));  // when this thread's copies so far are in place
+        mbar_arrive(full(q));
+      }
+    }
+    drain(last);
+  }
+
+  // The warp that fetches Q: rows of up to MT query rows a unit (rows that do not exist are 0), 128-byte blocks of `block`
+  // bytes at `at`, in the tiles' swizzle; slots Qs in turn, `slot_rows` rows apart.
   template <int MT>
   __device__ void load_q(const AttnParams& p, uint32_t at, int block, int slots, int slot_rows) {
+    constexpr int kRowPieces = kPieces * H, kLanes = kRowPieces < 32 ? kRowPieces : 32;  // lanes on a row
     AttnSegment s;
-    const int c = lane % kPieces, sub = lane / kPieces;
-    const bool in_head = c * 8 < p.c.head_dim;
+    const int c0 = lane % kLanes, sub = lane / kLanes;
     for (uint32_t unit = 0; next(s); ++unit) {
       const int slot = static_cast<int>(unit % slots);
       const uint32_t turn = unit / slots;
@@ -262,16 +408,19 @@ struct KvRing {
       const int upto = min(MT, (rows + 31) & ~31);  // rows of the warps that have any
       for (int r0 = 0; r0 < upto; r0 += 32) {       // a lane finds one row's place, the warp copies the 32 of them
         const int grow = s.rt * MT + r0 + lane, i = grow / p.group;
-        const int64_t from = r0 + lane < rows
+        const int64_t from = r0 + lane < min(rows, MT)
                                  ? (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head
                                  : -1;
 #pragma unroll 8
-        for (int j = 0; j < (MT < 32 ? MT : 32); j += 32 / kPieces) {
+        for (int j = 0; j < (MT < 32 ? MT : 32); j += 32 / kLanes) {
           const int64_t o = __shfl_sync(0xffffffffu, from, j + sub);
-          const bool live = o >= 0 && in_head;
           const int row = slot * slot_rows + r0 + j + sub;
-          cp_async16(at + (c >> 3) * block + row * 128 + (((c & 7) ^ (row & 7)) << 4), live ? p.q + (o + c * 8) * 2 : p.q,
-                     live);
+#pragma unroll
+          for (int c = c0; c < kRowPieces; c += kLanes) {
+            const bool live = o >= 0 && c * kEach < p.c.head_dim;
+            cp_async16(at + (c >> 3) * block + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                       live ? p.q + (o + c * kEach) * ES : p.q, live);
+          }
         }
       }
       cp_async_commit();
@@ -290,7 +439,7 @@ struct KvRing {
   }
 };
 
-// The maps of a call's layer (bf16).
+// The maps of a call's layer.
 KvMaps kv_maps(const KvView& c);
 
 }  // namespace sv

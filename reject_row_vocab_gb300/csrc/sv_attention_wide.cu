@@ -1,5 +1,5 @@
 // Attention over the paged cache for many query rows, on the fifth-generation
-// tensor cores: bf16, heads of up to 128, tiles of 128 rows and 128 keys.
+// tensor cores: bf16, tiles of 128 rows and 128 keys.
 //
 //   S = Q K^T (128 x 128, tensor memory)     one thread issues the products
 //   P = 2^(c S - m), l += sum P              one thread a row: no exchange
@@ -113,25 +113,29 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // Layout
 // ---------------------------------------------------------------------------------------------------------------------
 
-template <int DP>
+// Heads of up to 64 (CB 1), 128 (CB 2) and 256 (CB 2, H 2) columns.
+template <int CB, int H>
 struct Wide {
-  static constexpr int kRing = DP == 128 ? 6 : 8;  // tiles in the ring
-  using R = KvRing<DP, kRing>;
+  static constexpr int kRing = H == 2 ? 4 : CB == 2 ? 6 : 8;  // entries in the ring
+  using R = KvRing<2, CB, kRing, H, kRing == 4>;
+  static constexpr int kCols = CB * 64, kDP = kCols * H;
   static constexpr int kS = 0, kO = 256;           // tensor memory columns: two S of 128, then O
-  // shared memory: Q (a tile), the ring, s, p, pv [2], soft, and tmem, careful
-  static constexpr int kBars = R::kTile + R::kBytes;
+  // shared memory: Q (as a tile's K), the ring, s, p, pv [2], soft, and tmem, careful
+  static constexpr int kQBytes = R::kTile * H;
+  static constexpr int kBars = kQBytes + R::kBytes;
   static constexpr int kMisc = kBars + 7 * 8 + 8;
   static constexpr int kSmem = kMisc + 16;
 };
 
-template <int DP>
+template <int CB, int H>
 __global__ void __launch_bounds__(kWideThreads, 1)
     k_attention_wide(const AttnParams p, const __grid_constant__ KvMaps maps) {
-  using W = Wide<DP>;
+  using W = Wide<CB, H>;
   using R = typename W::R;
+  constexpr int DP = W::kDP;
   extern __shared__ __align__(1024) char smem[];
   const uint32_t base = smem_addr(smem);  // Q lies first
-  R ring(smem + R::kTile);
+  R ring(smem + W::kQBytes);
   int* s_misc = reinterpret_cast<int*>(smem + W::kMisc);
   volatile int* s_careful = s_misc + 1;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -182,19 +186,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const uint32_t qk = instruction(kKeys, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
       auto scores = [&](uint32_t n, bool last) {
         const int slot = static_cast<int>(units % twins);
-        const uint32_t group = 2 * n;
-        if (!ring.wait_one(ring.full(group), ring.phase(group))) return false;
-        fence_async();  // the copies wrote through the generic proxy, the products read through the asynchronous one
-        tc_fence_after();
-        mbar_arrive(bar_s(n));  // hands the tile's validity on
-        const uint32_t k = ring.tile(group);
+#pragma unroll 1
+        for (int h = 0; h < H; ++h) {
+          const uint32_t group = 2 * H * n + h;
+          if (!ring.wait_one(ring.full(group), ring.phase(group))) return false;
+          fence_async();  // the copies wrote through the generic proxy, the products read through the asynchronous one
+          tc_fence_after();
+          if (h == 0) mbar_arrive(bar_s(n));  // hands the tile's validity on
+          const uint32_t k = ring.tile(group);
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
-          const uint32_t at = (i >> 2) * R::kBlock + (i & 3) * 32;
-          mma_ss(tmem + W::kS + (n & 1) * 128, operand(base + slot * 64 * 128 + at, 16), operand(k + at, 16),
-                 qk, i > 0);
+          for (int i = 0; i < W::kCols / 16; ++i) {
+            const uint32_t at = (i >> 2) * R::kBlock + (i & 3) * 32;
+            mma_ss(tmem + W::kS + (n & 1) * 128, operand(base + slot * 64 * 128 + h * R::kTile + at, 16),
+                   operand(k + at, 16), qk, h > 0 || i > 0);
+          }
+          tc_commit(ring.empty(group));
         }
-        tc_commit(ring.empty(group));
         tc_commit(bar_s(n));
         if (last) tc_commit(ring.q_free(slot));
         return true;
@@ -204,23 +211,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tc_fence_after();
         ok = scores(g, s.cnt == 1);
         for (int i = 0; ok && i < s.cnt; ++i) {
-          const uint32_t n = g + i, group = 2 * n + 1;
+          const uint32_t n = g + i;
           if (i + 1 < s.cnt && !scores(n + 1, i + 2 == s.cnt)) {
             ok = false;
             break;
           }
-          if (!ring.wait_one(ring.full(group), ring.phase(group)) || !ring.wait_one(bar_p(n), half(n))) {
-            ok = false;
-            break;
-          }
-          fence_async();
-          tc_fence_after();
-          const uint32_t v = ring.tile(group);
+#pragma unroll 1
+          for (int h = 0; h < H; ++h) {
+            const uint32_t group = 2 * H * n + H + h;
+            if (!ring.wait_one(ring.full(group), ring.phase(group)) || (h == 0 && !ring.wait_one(bar_p(n), half(n)))) {
+              ok = false;
+              break;
+            }
+            fence_async();
+            tc_fence_after();
+            const uint32_t v = ring.tile(group);
 #pragma unroll
-          for (int j = 0; j < kKeys / 16; ++j)
-            mma_ts(tmem + W::kO, tmem + W::kS + (n & 1) * 128 + j * 8, operand(v + j * 2048, R::kBlock),
-                   instruction(DP, true), i > 0 || j > 0);
-          tc_commit(ring.empty(group));
+            for (int j = 0; j < kKeys / 16; ++j)
+              mma_ts(tmem + W::kO + h * W::kCols, tmem + W::kS + (n & 1) * 128 + j * 8, operand(v + j * 2048, R::kBlock),
+                     instruction(W::kCols, true), i > 0 || j > 0);
+            tc_commit(ring.empty(group));
+          }
+          if (!ok) break;
           tc_commit(bar_pv(n));
         }
         g += s.cnt;
@@ -263,17 +275,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const bool masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xffffffffu || x0 + kKeys > s.r.len;
         if (masked && s.r.n > 1 && x0 + kKeys > s.r.len) {
           mixed = true;
-          const uint32_t group = 2 * g + 1;
-          if (!ring.wait(ring.full(group), ring.phase(group))) {
-            ok = false;
-            break;
-          }
-          char* v = ring.tile_mem(group);
           const int from = max(s.r.len - x0, 0);
           bool found = false;
-          for (int x = from * R::kPieces + t; x < kKeys * R::kPieces; x += kSoftmaxThreads) {
-            if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(x / R::kPieces, x % R::kPieces)))) found = true;
+#pragma unroll 1
+          for (int h = 0; ok && h < H; ++h) {
+            const uint32_t group = 2 * H * g + H + h;
+            ok = ring.wait(ring.full(group), ring.phase(group));
+            char* v = ring.tile_mem(group);
+            for (int x = from * R::kPieces + t; ok && x < kKeys * R::kPieces; x += kSoftmaxThreads) {
+              if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(x / R::kPieces, x % R::kPieces)))) found = true;
+            }
           }
+          if (!ok) break;
           if (found) *s_careful = 1;
           fence_async();
         }
@@ -492,8 +505,9 @@ __global__ void __launch_bounds__(kJoinRows * DP / 8) k_attention_join(AttnParam
     write_row<true>(p, s.row0 + i, head, (quad + e * (DP / 8)) * 4, a[e], M, L);
 }
 
-template <int DP>
+template <int CB, int H>
 cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+  constexpr int DP = Wide<CB, H>::kDP;
   static std::mutex mu;
   static bool have[64] = {};
   int d = 0;
@@ -503,14 +517,14 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!have[d]) {
-      e = cudaFuncSetAttribute(k_attention_wide<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<DP>::kSmem);
+      e = cudaFuncSetAttribute(k_attention_wide<CB, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<CB, H>::kSmem);
       if (e != cudaSuccess) return e;
       have[d] = true;
     }
   }
-  static_assert(Wide<DP>::kSmem <= 227 * 1024, "shared memory of a block");
+  static_assert(Wide<CB, H>::kSmem <= 227 * 1024, "shared memory of a block");
   const int grid = dev.sms < kAttnMaxBlocks / 2 ? dev.sms : kAttnMaxBlocks / 2;  // parts are laid out for 64-row tiles
-  e = launch_pdl(k_attention_wide<DP>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<DP>::kSmem, stream, p,
+  e = launch_pdl(k_attention_wide<CB, H>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), Wide<CB, H>::kSmem, stream, p,
                  kv_maps(p.c));
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
@@ -522,7 +536,8 @@ cudaError_t launch(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_attention_wide(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-  return p.c.head_dim <= 64 ? launch<64>(p, dev, stream) : launch<128>(p, dev, stream);
+  const int dim = p.c.head_dim;
+  return dim <= 64 ? launch<1, 1>(p, dev, stream) : dim <= 128 ? launch<2, 1>(p, dev, stream) : launch<2, 2>(p, dev, stream);
 }
 
 }  // namespace sv
