@@ -485,8 +485,9 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
   }
 }
 
-// bf16, head_dim <= 128: up to 16 rows a unit, and any number of rows on tensor memory.
+// bf16 with up to 16 rows a unit, bf16 with any number of rows on tensor memory, fp32.
 cudaError_t launch_attention_few(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_attention_wide(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_attention_f32(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
 
 }  // namespace sv

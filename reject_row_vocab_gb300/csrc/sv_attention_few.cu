@@ -44,29 +44,6 @@ struct Few {
   static constexpr int kSmem = kParts + 2 * static_cast<int>(sizeof(AttnSegment));
 };
 
-// What the products left out (see sv_attention.cuh), added by a warp to the rows that it has just written: to its part of
-// the unit, or, without one, to the output.  Columns d0 .. d0 + COLS - 1.
-template <int COLS>
-__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, int d0, float* part) {
-  __syncwarp();
-  for (int x = threadIdx.x & 31; x < min(rows, kRows) * (COLS / 4); x += 32) {
-    const int row = x / (COLS / 4), d = d0 + x % (COLS / 4) * 4, grow = s.rt * kRows + row, i = grow / p.group;
-    if (d >= p.c.head_dim) continue;
-    const float4 f = nonfinite_seen<true, kKeys>(p, s, i, d);
-    if (part) {
-      float4* at = reinterpret_cast<float4*>(part) + (d / 4) * kRows + row;
-      const float4 v = *at;
-      *at = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
-    } else {
-      const int head = s.hkv * p.group + grow - i * p.group;
-      char* at = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head + d) * 2;
-      const uint2 u = *reinterpret_cast<const uint2*>(at);
-      store4<true>(at, make_float4(bf16_lo(u.x) + f.x, bf16_hi(u.x) + f.y, bf16_lo(u.y) + f.z, bf16_hi(u.y) + f.w));
-    }
-  }
-  __syncwarp();
-}
-
 template <int CB, int H>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_attention_few(const AttnParams p, const __grid_constant__ KvMaps maps) {
@@ -328,7 +305,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
         }
         if (odd) {
-          add_nonfinite<W::kCols>(p, s, rows, d0, whole ? nullptr : part);
+          add_nonfinite<true, kRows, W::kCols>(p, s, rows, d0, whole ? nullptr : part);
         }
         if (whole) {
           if (s.reports && warp == 0 && lane == 0) p.status[s.b] = bad | attn_timeout(p);

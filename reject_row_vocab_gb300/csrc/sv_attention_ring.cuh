@@ -439,6 +439,35 @@ struct KvRing {
   }
 };
 
+// The NaN and infinite values that the products left out, added by a warp to the rows that it has just written: to its
+// part of the unit, or, without one, to the output.  Units of MT rows, columns d0 .. d0 + COLS - 1.
+template <bool BF16, int MT, int COLS>
+__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, int d0, float* part) {
+  __syncwarp();
+  for (int x = threadIdx.x & 31; x < min(rows, MT) * (COLS / 4); x += 32) {
+    const int row = x / (COLS / 4), d = d0 + x % (COLS / 4) * 4, grow = s.rt * MT + row, i = grow / p.group;
+    if (d >= p.c.head_dim) continue;
+    const float4 f = nonfinite_seen<BF16, kKeys>(p, s, i, d);
+    if (part) {
+      float4* at = reinterpret_cast<float4*>(part) + (d / 4) * MT + row;
+      const float4 v = *at;
+      *at = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+    } else {
+      const int head = s.hkv * p.group + grow - i * p.group;
+      char* at = p.out + ((s.r.row0 + i) * p.o_row + head * p.o_head + d) * (BF16 ? 2 : 4);
+      float4 v;
+      if (BF16) {
+        const uint2 u = *reinterpret_cast<const uint2*>(at);
+        v = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+      } else {
+        v = *reinterpret_cast<const float4*>(at);
+      }
+      store4<BF16>(at, make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w));
+    }
+  }
+  __syncwarp();
+}
+
 // The maps of a call's layer.
 KvMaps kv_maps(const KvView& c);
 
