@@ -456,32 +456,36 @@ __device__ __forceinline__ void attn_join_rows(const AttnParams& p, const AttnSe
   }
 }
 
-// After the part is written: take the unit's ticket; the last block to come joins the parts, in block order, and
-// writes the rows.  T threads, a warp or the block, of which this is thread t; s_last is shared.
+// At the end of a block of T threads: the units that it has left parts of.  Each has a ticket; the last of its blocks to come
+// joins the parts, in block order, and writes the rows.  Two quads of columns a thread and eight parts at a time: a single
+// request of 100000 leaves about 19 parts of a unit, and what their join waits for is the memory, part after part.
+// segments [count], s_last: shared.
 template <bool BF16, int MT, int DP, int T>
-__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment& s, int t,
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& sp, const AttnSegment* segments, int count,
                                           int* s_last) {
-  __threadfence();  // each thread's own writes, before the barrier that lets thread 0 take the ticket for all
-  T == 32 ? __syncwarp() : __syncthreads();
-  // the unit's blocks are those that own its first and its last tile
-  const int c0 = attn_owner(sp, s.u0), c1 = attn_owner(sp, s.u0 + s.nt - 1);
-  if (t == 0) {
-    const bool last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0);
-    if (last) p.tickets[c0] = 0u;
-    *s_last = last ? 1 : 0;
-  }
-  T == 32 ? __syncwarp() : __syncthreads();
-  if (!*s_last) return;
-  // few rows: one quad a thread and eight parts at a time; many: four quads and two parts
-  const int live = min(MT, s.r.n * p.group - s.rt * MT);
-  if (live * (DP / 4) <= 2 * T)
-    attn_join_rows<BF16, MT, DP, T, 1, 8>(p, s, c0, c1, live, t);
-  else
-    attn_join_rows<BF16, MT, DP, T, 4, 2>(p, s, c0, c1, live, t);
-  if (s.reports && t == 0) {
-    uint32_t any = 0u;
-    for (int c = c0; c <= c1; ++c) any |= __float_as_uint(__ldcg(attn_part<MT, DP>(p, c, c == c0) + AttnPart<MT, DP>::kStatus));
-    p.status[s.b] = any;
+  const int t = threadIdx.x;
+#pragma unroll 1
+  for (int x = 0; x < count; ++x) {
+    const AttnSegment& s = segments[x];
+    // the unit's blocks are those that own its first and its last tile
+    const int c0 = attn_owner(sp, s.u0), c1 = attn_owner(sp, s.u0 + s.nt - 1);
+    if (t == 0) {
+      __threadfence();  // the block's parts, written before its last barrier
+      const bool last = ticket_add(&p.tickets[c0], 1u) == static_cast<unsigned>(c1 - c0);
+      if (last) p.tickets[c0] = 0u;
+      *s_last = last ? 1 : 0;
+    }
+    __syncthreads();
+    if (*s_last) {
+      attn_join_rows<BF16, MT, DP, T, 2, 8>(p, s, c0, c1, min(MT, s.r.n * p.group - s.rt * MT), t);
+      if (s.reports && t == 0) {
+        uint32_t any = 0u;
+        for (int c = c0; c <= c1; ++c)
+          any |= __float_as_uint(__ldcg(attn_part<MT, DP>(p, c, c == c0) + AttnPart<MT, DP>::kStatus));
+        p.status[s.b] = any | attn_timeout(p);
+      }
+    }
+    __syncthreads();  // s_last is free again
   }
 }
 

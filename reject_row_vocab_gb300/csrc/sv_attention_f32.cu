@@ -35,7 +35,7 @@ struct Plain {
   static constexpr int kPairs = H < 2 ? 1 : H / 2;  // a lane's quads of columns: one of each pair of entries
   static constexpr int kQRows = 8;                  // rows a Q has (the swizzle's period)
   // shared memory: the ring; two Qs; half the warps' results; each warp's weights [16][R] and row scales [R]; the warps' m,
-  // l and flags; the unit's m and l; meeting point, last, parts' barriers; split segments
+  // l and flags; the unit's m and l; meeting point, last, split; split segments
   static constexpr int kQBlock = 2 * kQRows * 128;
   static constexpr int kQ = (Ring::kBytes + 1023) / 1024 * 1024;
   static constexpr int kStage = R * kPairs * 32 * 16;
@@ -45,7 +45,7 @@ struct Plain {
   static constexpr int kM = kWeights + kTakers * kWarpWeights;  // m, then l: [2 by turns][kTakers][R] each
   static constexpr int kFlags = kM + 4 * kTakers * R * 4;
   static constexpr int kMeet = kFlags + 2 * kTakers * 8;
-  static constexpr int kParts = kMeet + 4 * 8;
+  static constexpr int kParts = kMeet + 2 * 8;
   static constexpr int kSmem = kParts + 2 * static_cast<int>(sizeof(AttnSegment));
 };
 
@@ -57,15 +57,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
   extern __shared__ __align__(1024) char smem[];
   Ring ring(smem);
   const uint32_t base = smem_addr(smem);
-  const uint32_t bar_meet = base + W::kMeet, bar_part = base + W::kMeet + 16;
+  const uint32_t bar_meet = base + W::kMeet;
   int* s_last = reinterpret_cast<int*>(smem + W::kMeet + 8);
+  int* s_split = s_last + 1;  // segments of the block that are only part of their unit
   uint32_t* s_flags = reinterpret_cast<uint32_t*>(smem + W::kFlags);  // [2][kTakers][2], by turns: keys outside the cache, careful
   AttnSegment* s_parts = reinterpret_cast<AttnSegment*>(smem + W::kParts);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
     ring.init(kTakers, kTakers + kLoadWarps + 1, kTakers);
     mbar_init(bar_meet, 32 * kTakers);
-    for (int i = 0; i < 2; ++i) mbar_init(bar_part + i * 8, 1);
     mbar_fence_init();
   }
   __syncthreads();
@@ -73,13 +73,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
   allow_dependents();
   const AttnSpan span = attn_span<R, kKeys, kUnitPlaces, kThreads>(p, t, ring.sums(), ring.find(), [] { __syncthreads(); });
   if (warp == kTakers + kLoadWarps) {
-    // The plan; then, when the parts that this block leaves of units are written, the join of the units that it ends.
     const int split = ring.template plan<R, kUnitPlaces>(p, span, s_parts);
-#pragma unroll 1
-    for (int i = 0; i < split; ++i) {
-      if (!ring.wait(bar_part + i * 8, 0)) break;
-      attn_join<false, R, DP, 32>(p, span, s_parts[i], lane, s_last);
-    }
+    if (lane == 0) *s_split = split;
   } else if (warp == kTakers + kLoadWarps + 1) {
     ring.template load_q<R>(p, base + W::kQ, W::kQBlock, 2, W::kQRows);
   } else if (warp >= kTakers) {
@@ -96,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
     const int piece = H == 1 ? lane & 15 : lane, odd = H == 1 ? lane >> 4 : 0;
     float* const pw = reinterpret_cast<float*>(smem + W::kWeights + warp * W::kWarpWeights);  // [kOwn][R]
     float* const scales = pw + kOwn * R;                                                      // [R]
-    uint32_t meets = 0, g = 0, left = 0;  // left: parts written
+    uint32_t meets = 0, g = 0;
     auto meet = [&] {                     // a barrier of the taking warps, bounded like every wait
       mbar_arrive(bar_meet);
       return ring.wait(bar_meet, meets++ & 1);
@@ -370,16 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
           if (s.reports && lane == 0) p.status[s.b] = bad | attn_timeout(p);
         } else {
           if (lane == 0) part[P::kStatus] = __uint_as_float(bad);
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_part + left++ * 8);
         }
       }
       ring.release();
     }
   }
   __syncthreads();
-  ring.report_abort(p);
+  if (*ring.abort())
+    ring.report_abort(p);
+  else
+    attn_join<false, R, DP, kThreads>(p, span, s_parts, *s_split, s_last);
 }
 
 template <int H, int R>

@@ -40,7 +40,7 @@ struct Few {
   static constexpr int kStages = kQ + kQBlock * CB * H;
   static constexpr int kFlags = kStages + kTakers / 2 * kStage;
   static constexpr int kMeet = kFlags + 2 * kTakers * 8;
-  static constexpr int kParts = kMeet + 4 * 8;  // (behind two barriers, one for each part)
+  static constexpr int kParts = kMeet + 2 * 8;
   static constexpr int kSmem = kParts + 2 * static_cast<int>(sizeof(AttnSegment));
 };
 
@@ -56,13 +56,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const uint32_t bar_meet = base + W::kMeet;
   uint32_t* s_flags = reinterpret_cast<uint32_t*>(smem + W::kFlags);  // [2][kTakers][2], by turns: keys outside the cache, careful
   AttnSegment* s_parts = reinterpret_cast<AttnSegment*>(smem + W::kParts);
-  const uint32_t bar_part = base + W::kMeet + 16;
   int* s_last = reinterpret_cast<int*>(smem + W::kMeet + 8);
+  int* s_split = s_last + 1;  // segments of the block that are only part of their unit
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
     ring.init(kTakers, kTakers + kLoadWarps + 1, kTakers);
     mbar_init(bar_meet, 32 * kTakers);
-    for (int i = 0; i < 2; ++i) mbar_init(bar_part + i * 8, H);
     mbar_fence_init();
   }
   __syncthreads();
@@ -71,13 +70,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, kFewThreads>(p, t, ring.sums(), ring.find(),
                                                                           [] { __syncthreads(); });
   if (warp == kTakers + kLoadWarps) {
-    // The plan; then, when the parts that this block leaves of units are written, the join of the units that it ends.
     const int split = ring.template plan<kRows, kUnitPlaces>(p, span, s_parts);
-#pragma unroll 1
-    for (int i = 0; i < split; ++i) {
-      if (!ring.wait(bar_part + i * 8, 0)) break;
-      attn_join<true, kRows, DP, 32>(p, span, s_parts[i], lane, s_last);
-    }
+    if (lane == 0) *s_split = split;
   } else if (warp == kTakers + kLoadWarps + 1) {
     ring.template load_q<kRows>(p, base + W::kQ, W::kQBlock, 2, kRows);
   } else if (warp >= kTakers) {
@@ -89,7 +83,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // it in bits 5 and 6 of the address, or by a block.
     const int mi = lane >> 3, mr = lane & 7;  // matrix and row
     const uint32_t k_at = R::piece(k0 + (mi >> 1) * 8 + mr, mi & 1), v_at = R::piece(k0 + (mi & 1) * 8 + mr, mi >> 1);
-    uint32_t meets = 0, g = 0, left = 0;  // left: parts written
+    uint32_t meets = 0, g = 0;
     auto meet = [&] {  // a barrier of the taking warps, bounded like every wait
       mbar_arrive(bar_meet);
       return ring.wait(bar_meet, meets++ & 1);
@@ -311,16 +305,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (s.reports && warp == 0 && lane == 0) p.status[s.b] = bad | attn_timeout(p);
         } else {
           if (warp == 0 && lane == 0) part[P::kStatus] = __uint_as_float(bad);
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_part + left++ * 8);
         }
       }
       ring.release();
     }
   }
   __syncthreads();
-  ring.report_abort(p);
+  if (*ring.abort())
+    ring.report_abort(p);
+  else
+    attn_join<true, kRows, DP, kFewThreads>(p, span, s_parts, *s_split, s_last);
 }
 
 template <int CB, int H>
