@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
           if (s.r.n > 1 && x0 + kOwn > s.r.len) {
             bool found = false;
 #pragma unroll 1
-            for (int y = max(s.r.len - x0, 0) * Ring::kPieces * E + lane; y < kOwn * Ring::kPieces * E; y += 32) {
+            for (int y = max(s.r.len - x0, 0) * Ring::kPieces * E + lane; y < min(s.r.len + s.r.n - x0, kOwn) * Ring::kPieces * E;
+                 y += 32) {
               const int c = y % (Ring::kPieces * E);
               if (make_finite<false>(reinterpret_cast<uint4*>(ring.tile_mem(group + c / Ring::kPieces) +
                                                               Ring::piece(k0 + y / (Ring::kPieces * E), c % Ring::kPieces))))

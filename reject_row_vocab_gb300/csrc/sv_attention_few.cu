@@ -21,7 +21,7 @@ namespace {
 constexpr int kRows = 16;
 constexpr int kTakers = 8;                                      // warps that take the tiles
 constexpr int kFewThreads = 32 * (kTakers + kLoadWarps + 2);    // and a warp each to plan, to load Q
-constexpr int kUnitPlaces = 1;                                  // what a unit costs beside its key tiles, in tiles
+constexpr int kUnitPlaces = 2;                                  // what a unit costs beside its key tiles, in tiles
 
 // Heads of up to 64 (CB 1), 128 (CB 2) and 256 (CB 2, H 2) columns.  With H of 2 a warp has the scores of 32 keys and one
 // entry's columns of O: the scores are taken twice, O would not fit the registers otherwise.
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             char* v = ring.tile_mem(group_v);
             bool found = false;
 #pragma unroll 1
-            for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < W::kOwn * R::kPieces; x += 32)
+            for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < min(s.r.len + s.r.n - x0, W::kOwn) * R::kPieces; x += 32)
               if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(k0 + x / R::kPieces, x % R::kPieces)))) found = true;
             careful = __any_sync(0xffffffffu, found) || careful;
           }

@@ -17,8 +17,8 @@
 // depend on the reference.
 //
 // Units that several blocks share are joined by a second kernel, spread over
-// the whole GPU: two long requests leave 19 parts of a unit, which its last
-// block alone took 35 us to join.
+// the whole GPU.  (By the last of the unit's blocks alone, two long requests
+// took 90 us instead of 63, a 64-request block 127 instead of 118.)
 //
 // Every wait is bounded; a wait that gives up raises SV_DEV_TIMEOUT, lets all
 // warps leave, and the block frees its tensor memory.
@@ -36,7 +36,7 @@ constexpr int kRows = 128;  // query rows of a tile
 constexpr int kSoftmaxThreads = 128;
 constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 96;  // and a warp each to issue, to load Q, to plan
 constexpr int kReaders = 10;                                       // warps that read the plan
-constexpr int kUnitPlaces = 1;                                     // what a unit costs beside its key tiles, in tiles
+constexpr int kUnitPlaces = 4;                                     // what a unit costs beside its key tiles, in tiles
 constexpr float kSlack = 8.0f;  // log2 units a row's maximum may pass its reference by
 
 // ---------------------------------------------------------------------------------------------------------------------
@@ -275,14 +275,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const bool masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xffffffffu || x0 + kKeys > s.r.len;
         if (masked && s.r.n > 1 && x0 + kKeys > s.r.len) {
           mixed = true;
-          const int from = max(s.r.len - x0, 0);
+          const int from = max(s.r.len - x0, 0), upto = min(s.r.len + s.r.n - x0, kKeys);  // the new rows
           bool found = false;
 #pragma unroll 1
           for (int h = 0; ok && h < H; ++h) {
             const uint32_t group = 2 * H * g + H + h;
             ok = ring.wait(ring.full(group), ring.phase(group));
             char* v = ring.tile_mem(group);
-            for (int x = from * R::kPieces + t; ok && x < kKeys * R::kPieces; x += kSoftmaxThreads) {
+            for (int x = from * R::kPieces + t; ok && x < upto * R::kPieces; x += kSoftmaxThreads) {
               if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(x / R::kPieces, x % R::kPieces)))) found = true;
             }
           }
@@ -297,12 +297,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             uint32_t word = vw[0];
 #pragma unroll 1
             for (int h = 0; h < 4; ++h) {
-              float v[32];
-              tmem_ld32(st + h * 32, reinterpret_cast<uint32_t*>(v));
-              tmem_wait_ld();
+              if (!__all_sync(0xffffffffu, word == 0xffffffffu)) {
+                float v[32];
+                if (__any_sync(0xffffffffu, word != 0u)) {
+                  tmem_ld32(st + h * 32, reinterpret_cast<uint32_t*>(v));
+                  tmem_wait_ld();
+                }
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = (word >> j & 1u) ? v[j] : -kInfF;
-              tmem_st32(st + h * 32, reinterpret_cast<const uint32_t*>(v));
+                for (int j = 0; j < 32; ++j) v[j] = (word >> j & 1u) ? v[j] : -kInfF;
+                tmem_st32(st + h * 32, reinterpret_cast<const uint32_t*>(v));
+              }
               word = h == 0 ? vw[1] : h == 1 ? vw[2] : vw[3];
             }
             tmem_wait_st();
@@ -447,13 +451,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
-// Block (c, i): rows 16 i .. of the unit that begins in block c of the attention kernel and goes on behind it, if any.
-constexpr int kJoinRows = 16;
+// Block (c, i): rows 8 i .. of the unit that begins in block c of the attention kernel and goes on behind it, if any.
+// (Rows a block, quads a thread, parts in flight; two requests of 60000 to 100000 and a block of 64 requests: 16, 2, 8: 66
+// and 119 us; 8, 2, 4: 63 and 118; 8, 2, 10: 62 and 119; 4, 2, 8: 62 and 120; 8, 1, 20: 63 and 127.)
+constexpr int kJoinRows = 8;
 
 template <int DP>
 __global__ void __launch_bounds__(kJoinRows * DP / 8) k_attention_join(AttnParams p) {
   using P = AttnPart<kRows, DP>;
-  constexpr int PARTS = 8, E = 2;  // parts in flight, quads of columns a thread
+  constexpr int PARTS = 4, E = 2;  // parts in flight, quads of columns a thread
   grid_dependency_wait();
   allow_dependents();
   const int c0 = blockIdx.x, t = threadIdx.x;
