@@ -483,6 +483,9 @@ __global__ void __launch_bounds__(kLpThreads, 7) k_token_logprobs(LogprobParams 
   if (g < 1) g = 1;
   // a whole number of blocks a row, where that leaves few of them idle: then no block has parts of two
   if (rows > 0 && rows <= g && g / rows * rows * 5 >= g * 4) g = g / rows * rows;
+  // ... or of rows a block
+  const int64_t each = rows > g ? (rows + g - 1) / g : 1;
+  if (each > 1 && rows % each == 0 && rows / each * 5 >= g * 4) g = rows / each;
   if (blockIdx.x >= g || total == 0) return;
   const int64_t start = blockIdx.x * total / g, end = (blockIdx.x + 1) * total / g;
   int64_t ord = start / per_row;  // rows before this block's first one
