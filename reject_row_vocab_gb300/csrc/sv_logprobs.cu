@@ -8,7 +8,9 @@
 // and rescales it when its maximum grows; a block joins its threads' triples,
 // and the last block of a row joins the blocks' in block order, so results do
 // not depend on the order the blocks finish in.  Bound by the instructions: an
-// exponential and about three and a half other issues an element.
+// exponential and about three and a half other issues an element.  Measured:
+// 1024 rows of 151936 bf16, 20 alternatives: 65 us, 4.8 TB/s; without
+// alternatives 57 us; 5 rows of 32000 fp32, 5 alternatives: 13 us, latency.
 //
 // Top alternatives from the same pass: a thread's running maximum is the
 // largest of its own elements, so the top_k-th largest of the block's thread
@@ -24,6 +26,8 @@
 //   dl = p (A + B t) + (the row's given tokens)/T,
 //   A = -(G + gH H)/T,  B = -gH ln 2 / T:
 // two multiply-adds and an exponential an element between a read and a write.
+// Bound by the bytes.  Measured: 1024 rows of 151936 bf16 with an entropy term:
+// 98 us, 6.4 TB/s; 80 rows of 32003 fp32: 11 us.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cfloat>
