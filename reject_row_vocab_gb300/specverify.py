@@ -577,6 +577,14 @@ def _need(t, name: str, dtype, numel: int, device, index: int):
     _arg(t, name, dtype, numel, device)
 
 
+def _need_all(args, dtype, device, index: int):
+    """_need for (tensor or None, name, numel) arguments of one type."""
+    for t, name, numel in args:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+                                  and t.numel() >= numel and t.is_contiguous()):
+            _arg(t, name, dtype, numel, device)
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -788,9 +796,9 @@ def _given_ids(ids, n, device, index):
         ids = ids.unsqueeze(1)
     m, num = ids.shape
     a, b = ids.stride()
-    if not (ids.dtype is torch.int32 and ids.get_device() == index and m >= n and (b == 1 or num <= 1)):
+    if not (m >= n and (b == 1 or num <= 1) and ids.dtype is torch.int32 and ids.get_device() == index):
         _rows_arg(ids, "ids", torch.int32, n, 0, device)
-    return ids, num, (a if n > 1 else max(num, 1))
+    return ids, num, (a if n > 1 else num or 1)
 
 
 def token_logprobs(logits, ids, *, top_k: int = 0, row_index=None, row_temp=None, out=None, ws=None,
@@ -811,8 +819,6 @@ def token_logprobs(logits, ids, *, top_k: int = 0, row_index=None, row_temp=None
         n = row_index.numel()
     ids, num_ids, ldi = _given_ids(ids, n, dev, index)
     f32, i32 = torch.float32, torch.int32
-    if row_temp is not None:
-        _need(row_temp, "row_temp", f32, n, dev, index)
     if out is None or ws is None:
         with _on(stream):
             if out is None:
@@ -820,10 +826,10 @@ def token_logprobs(logits, ids, *, top_k: int = 0, row_index=None, row_temp=None
             if ws is None:
                 ws = logprobs_workspace(n, V, top_k, dev)
     res = (out.logprob, out.entropy, out.row_max, out.log_z, out.top_ids, out.top_logprob, out.flags)
-    for t, name, dtype, numel in zip(res, ("logprob", "entropy", "row_max", "log_z", "top_ids", "top_logprob", "flags"),
-                                     (f32, f32, f32, f32, i32, f32, i32), (n * num_ids, n, n, n, n * top_k, n * top_k, n)):
-        if t is not None:
-            _need(t, "out." + name, dtype, numel, dev, index)
+    _need_all(((row_temp, "row_temp", n), (res[0], "out.logprob", n * num_ids), (res[1], "out.entropy", n),
+               (res[2], "out.row_max", n), (res[3], "out.log_z", n), (res[5], "out.top_logprob", n * top_k)),
+              f32, dev, index)
+    _need_all(((res[4], "out.top_ids", n * top_k), (res[6], "out.flags", n)), i32, dev, index)
     _need(ws, "ws", torch.uint8, 0, dev, index)
     code = lib.spec_verify_token_logprobs(
         logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, n, _addr(row_index), ids.data_ptr(), num_ids,
@@ -856,20 +862,24 @@ def token_logprobs_backward(logits, ids, kept: LogprobOutputs, g_logprob, *, g_e
             _need(top_ids, "kept.top_ids", torch.int32, rows * top_k, dev, index)
             if top_ids.dim() != 2 or top_ids.shape[1] != top_k:
                 raise ValueError("kept.top_ids must have g_top's %d columns" % top_k)
-    for t, name, numel in ((g_logprob, "g_logprob", rows * num_ids), (g_entropy, "g_entropy", rows),
-                           (row_temp, "row_temp", rows), (kept.row_max, "kept.row_max", rows),
-                           (kept.log_z, "kept.log_z", rows), (kept.entropy, "kept.entropy", rows)):
-        if t is not None:
-            _need(t, name, f32, numel, dev, index)
+    row_max, log_z, entropy = kept.row_max, kept.log_z, kept.entropy
+    _need_all(((g_logprob, "g_logprob", rows * num_ids), (g_entropy, "g_entropy", rows), (row_temp, "row_temp", rows),
+               (row_max, "kept.row_max", rows), (log_z, "kept.log_z", rows), (entropy, "kept.entropy", rows)),
+              f32, dev, index)
     if out is None:
         per = 16 // logits.element_size()
         with _on(stream):
             out = torch.empty(rows, -(-V // per) * per, dtype=logits.dtype, device=dev)[:, :V]
-    _rows_arg(out, "out", logits.dtype, rows, V, dev)
+    if not (isinstance(out, torch.Tensor) and out.shape == logits.shape and out.dtype is logits.dtype
+            and out.get_device() == index and (out.stride(1) == 1 or V == 1)):
+        _rows_arg(out, "out", logits.dtype, rows, V, dev)
+    row_temp, row_max, log_z, entropy, top_ids, g_logprob, g_entropy, g_top = [
+        None if t is None else t.data_ptr()
+        for t in (row_temp, row_max, log_z, entropy, top_ids, g_logprob, g_entropy, g_top)]
     code = lib.spec_verify_token_logprobs_backward(
-        logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, ids.data_ptr(), num_ids, ldi, _addr(row_temp),
-        _addr(kept.row_max), _addr(kept.log_z), _addr(kept.entropy), _addr(top_ids), top_k, _addr(g_logprob),
-        _addr(g_entropy), _addr(g_top), out.data_ptr(), _row_step(out), _call_stream(stream, dev))
+        logits.data_ptr(), _dtype(logits), _row_step(logits), rows, V, ids.data_ptr(), num_ids, ldi, row_temp,
+        row_max, log_z, entropy, top_ids, top_k, g_logprob, g_entropy, g_top, out.data_ptr(), _row_step(out),
+        _call_stream(stream, dev))
     if code:
         _check("spec_verify_token_logprobs_backward", code)
     return out
