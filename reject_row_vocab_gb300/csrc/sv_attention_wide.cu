@@ -128,7 +128,7 @@ struct Wide {
   using R = KvRing<2, CB, kRing, H, kRing == 4>;
   static constexpr int kCols = CB * 64, kDP = kCols * H;
   static constexpr int kS = 0, kO = 256;           // tensor memory columns: two S of 128, then O
-  // shared memory: Q (as a tile's K), the ring, s, p, pv [2], soft, and tmem, careful
+  // shared memory: Q (as a tile's K), the ring, s, p, pv [2], soft, and tmem, careful [2]
   static constexpr int kQBytes = R::kTile * H;
   static constexpr int kBars = kQBytes + R::kBytes;
   static constexpr int kMisc = kBars + 7 * 8 + 8;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t base = smem_addr(smem);  // Q lies first
   R ring(smem + W::kQBytes);
   int* s_misc = reinterpret_cast<int*>(smem + W::kMisc);
-  volatile int* s_careful = s_misc + 1;
+  volatile uint32_t* s_careful = reinterpret_cast<volatile uint32_t*>(s_misc + 1);  // [2]: units that found NaN or infinities
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   auto bar_s = [&](uint32_t g) { return base + W::kBars + (g & 1) * 8; };
   auto bar_p = [&](uint32_t g) { return base + W::kBars + (2 + (g & 1)) * 8; };
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_init(bar_s(i), 2), mbar_init(bar_p(i), kSoftmaxThreads), mbar_init(bar_pv(i), 1);
     mbar_init(bar_soft, kSoftmaxThreads);
     mbar_fence_init();
-    *s_careful = 0;
+    s_careful[0] = s_careful[1] = 0u;
   }
   if (warp == 8) {
     tmem_alloc(base + W::kMisc, 512);
@@ -258,18 +258,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     // a negative scale's sign is in the products; a scale of 0 by one too small to tell (0 times a masked -inf is NaN)
     const float c = fmaxf(fabsf(p.scale_log2), 1e-30f);
-    AttnSegment s;
-    uint32_t g = 0;
+    uint32_t g = 0, units = 0;     // tiles and units so far, this one among them
     bool ok = true, left = false;  // left: a unit that goes on behind this block
-    while (ok && ring.next(s)) {
+    while (const AttnSegment* const seg = ring.peek()) {
+      const AttnSegment& s = *seg;
+      ++units;
       const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
       const bool idle = warp * 32 >= rows;              // none of the warp's rows exists
-      const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread
+      const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread, and its head
+      const int head = s.hkv * p.group + (s.rt * kRows + t) - my_row * p.group;
       float m = -kInfF, l = 0.0f;
       uint32_t bad = 0u;
       bool mixed = false;  // a tile whose keys some rows see and others do not
-      for (int i = 0; i < s.cnt; ++i, ++g) {
-        const int x0 = (s.t0 + i) * kKeys;
+      const int cnt = s.cnt, t0 = s.t0;
+      for (int i = 0; i < cnt; ++i, ++g) {
+        const int x0 = (t0 + i) * kKeys;
         const uint32_t st = tmem + lanes + W::kS + (g & 1) * 128;
         if (!ring.wait(bar_s(g), half(g))) {
           ok = false;
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
           }
           if (!ok) break;
-          if (found) *s_careful = 1;
+          if (found) s_careful[units & 1] = units;
           fence_async();
         }
         if (!idle) {
@@ -385,15 +388,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       bool careful = false;
       if (mixed) {
         meet();
-        careful = *s_careful != 0;
-        meet();
-        if (t == 0) *s_careful = 0;
+        careful = s_careful[units & 1] == units;  // (a unit's products wait for every thread: none is two units ahead)
       }
       bad = (bad ? kStSlotRange : 0u) | s.r.status;
       const bool whole = s.cnt == s.nt;
       using P = AttnPart<kRows, DP>;
       float* part = whole ? nullptr : attn_part<kRows, DP>(p, blockIdx.x, s.t0 == 0);
-      const int head = s.hkv * p.group + (s.rt * kRows + t) % p.group;
       char* out = p.out + ((s.r.row0 + my_row) * p.o_row + head * p.o_head) * 2;
       const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
       const float inv = none ? 0.0f : 1.0f / l;
@@ -407,8 +407,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (careful) {
 #pragma unroll
               for (int d = 0; d < 32; d += 4) {
-                const AttnSegment copy = s;
-                const float4 f = nonfinite_seen<true, kKeys>(p, copy, my_row, h * 32 + d);
+                const float4 f = nonfinite_seen<true, kKeys>(p, s, my_row, h * 32 + d);
                 o[d] += f.x, o[d + 1] += f.y, o[d + 2] += f.z, o[d + 3] += f.w;
               }
             }
@@ -447,6 +446,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       }
       tc_fence_before();
+      ring.release();
     }
     if (t == 0 && !left)
       reinterpret_cast<AttnSplit*>(attn_part<kRows, DP>(p, blockIdx.x, true) + AttnPart<kRows, DP>::kSplit)->last = 0;
