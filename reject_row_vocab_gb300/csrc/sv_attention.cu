@@ -61,15 +61,11 @@ KvMaps kv_maps(const KvView& c) {
   auto step = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s * c.es : (c.head_dim * c.es + 15) / 16 * 16); };
   const cuuint64_t strides[3] = {step(c.head_stride), step(c.slot_stride), step(c.page_stride)};
   const cuuint32_t box[4] = {128u / c.es, 1, static_cast<cuuint32_t>(rows), 1}, ones[4] = {1, 1, 1, 1};
-  // Lines of L2 are fetched in pairs where a head's row is whole pairs; other rows would bring their neighbours along
-  // (64 requests, heads of 64: 139 us with pairs, 129 without; of 96: 211 and 164; of 128: 175 and 178).
-  const CUtensorMapL2promotion lines =
-      c.head_dim * c.es % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   char* const base[2] = {c.k, c.v};
   CUtensorMap* const map[2] = {&m.k, &m.v};
   for (int i = 0; i < 2; ++i)
     if (encode(map[i], c.es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base[i], dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, lines,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return m;
   m.rows = rows;
