@@ -13,7 +13,7 @@
 // operands of one type); their sum l is of the unrounded ones, in fp32.
 //
 // Measured: one token of 128 requests of up to 8192, 32 heads of 128 on 8 in the
-// cache: 321 us, 6.7 TB/s; 64 requests, heads of 256: 336 us, 6.6 TB/s; one of a
+// cache: 317 us, 6.8 TB/s; 64 requests, heads of 256: 332 us, 6.6 TB/s; one of a
 // single request of 100000: 76 us, 5.4 TB/s; of 500: 12 us, latency.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
@@ -28,7 +28,7 @@ namespace {
 constexpr int kRows = 16;
 constexpr int kTakers = 8;                                      // warps that take the tiles
 constexpr int kFewThreads = 32 * (kTakers + kLoadWarps + 2);    // and a warp each to plan, to load Q
-constexpr int kUnitPlaces = 2;  // what a unit costs beside its key tiles, in tiles (128 requests: 1: 332 us, 2: 320, 4: 321)
+constexpr int kUnitPlaces = 2;  // what a unit costs beside its key tiles, in tiles (1 to 3 measure alike)
 
 // Heads of up to 64 (CB 1), 128 (CB 2) and 256 (CB 2, H 2) columns.  With H of 2 a warp has the scores of 32 keys and one
 // entry's columns of O: the scores are taken twice, O would not fit the registers otherwise.
