@@ -55,6 +55,9 @@ KvMaps kv_maps(const KvView& c) {
   while (rows >= 8 && c.page_size % rows != 0) rows /= 2;
   const EncodeTiledFn encode = encode_tiled();
   if (rows < 8 || !encode) return m;
+  // entries that share their memory (an axis repeated without a step) have no map either
+  if ((c.heads > 1 && c.head_stride == 0) || (c.page_size > 1 && c.slot_stride == 0) || (c.pages > 1 && c.page_stride == 0))
+    return m;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.heads),
                               static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
   // an axis of one entry may come without a step

@@ -77,3 +77,20 @@ def test_repeats_are_bit_equal(dtype, dim, rows, page):
     for _ in range(8):
         again = c.run(sv)
         assert torch.equal(first.out, again.out) and torch.equal(first.lse, again.lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("axis", ["pages", "heads"])
+def test_entries_that_share_their_memory(dtype, rows, axis):
+    # one page, or one head, repeated without a step
+    c = AttentionCase([300, 170], rows, 4, 2, 64, 16, dtype, seed=rows, poison=False)
+    one = (slice(None), slice(0, 1)) if axis == "pages" else (slice(None), slice(None), slice(None), slice(0, 1))
+    shape = c.k.shape
+    c.k, c.v = c.k[one].contiguous().expand(shape), c.v[one].contiguous().expand(shape)
+    k, v = c.k[one].cuda().expand(shape), c.v[one].cuda().expand(shape)
+    assert 0 in k.stride()
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    cache = sv.PagedKvCache(k, v, dev(c.table))
+    got = sv.paged_attention(c.q.cuda(), cache, dev(np.asarray(c.lens, np.int64)), max_len=c.max_len, scale=c.scale)
+    check_attention(c, got)
