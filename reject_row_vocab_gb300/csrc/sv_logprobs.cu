@@ -184,40 +184,67 @@ __device__ __forceinline__ void run_add(Run& r, float x, float k, uint32_t& flag
 }
 
 // A thread's running sums while it streams, against a reference: weights are 2^(l k - c) with c = ref k as rounded, one
-// multiply-add an element; settle() makes up for the rounding, which is the same for all of them.  The reference is the
-// largest logit of the warp's first vectors, and moves only when a logit passes it by 64 log2 units (2^64 times a row's
-// length is far from fp32's end): moving it at every new maximum made up two thirds of the instructions.  Logits below
-// `low` are read as `low`, which has a weight of 0 just as well: their exponent stays finite, and 0 times it is 0.
+// multiply-add an element; settle() makes up for the rounding, which is the same for all of them.  That needs a rounding
+// within the exponent's range: it is past it from |ref| k = 2^31 on, as in a row masked with -1e10 or at temperatures below
+// 1e-8.  A reference that is `far` is therefore subtracted before the product, an operation a pair of elements more (1024
+// rows of 151936 took 66.7 us that way throughout, and take 64.4).  The reference is the largest logit of the
+// warp's first vectors, and moves only when a logit passes it by 64 log2 units (2^64 times a row's length is far from fp32's
+// end): moving it at every new maximum made up two thirds of the instructions.  Logits below `low` are read as `low`, which
+// has a weight of 0 just as well: their exponent stays finite, and 0 times it is 0.
 template <bool BF16>
 struct Stream {
   Run r{-kInfF, 0.0f, 0.0f};  // what has been settled
   float ref = -kInfF, c = 0.0f, low = -kInfF, limit = -kInfF;  // the same in all lanes of a warp
   uint32_t low2 = 0xff80ff80u;
+  bool far = false;
+  bool packed = true;  // false: no number below the reference has a finite exponent: element by element
   float2 s2{0.0f, 0.0f}, w2{0.0f, 0.0f};
 
-  __device__ __forceinline__ bool packed() const { return fabsf(c) < 1e37f; }  // (a huge logit may have no room)
-
   __device__ __forceinline__ void settle(float k) {
-    if (ref == -kInfF || !packed()) return;
-    const float off = fmaf(ref, -k, c);  // c - ref k, exactly: 2^(l k - c) 2^off = 2^t and t = (l k - c) + off
+    if (ref == -kInfF || !packed) return;
+    const float off = far ? 0.0f : fmaf(ref, -k, c);  // c - ref k, exactly: 2^(l k - c) 2^off = 2^t and t = (l k - c) + off
     const float e = ex2_fast(off), s = s2.x + s2.y, w = w2.x + w2.y;
     run_merge(r, Run{ref, e * s, e * fmaf(s, off, w)}, k);
     s2 = w2 = make_float2(0.0f, 0.0f);
   }
-  __device__ __forceinline__ void rise(float to, float k, float unit) {  // a larger reference; unit: 1 / k
+  // A larger reference; unit: 1 / k.  Both ends are rounded down: where 300 or 64 units are less than the reference's last
+  // place, `low` is the number below it, and `limit` the reference itself.
+  __device__ __forceinline__ void rise(float to, float k, float unit) {
     settle(k);
     ref = to;
     c = ref * k;
-    low = fmaf(-300.0f, unit, ref);
-    limit = fmaf(64.0f, unit, ref);
-    if (BF16) {  // low, rounded down
+    far = !(fabsf(c) < 0x1p24f);  // the rounding of c is one half at most
+    low = __fmaf_rd(-300.0f, unit, ref);
+    limit = __fmaf_rd(64.0f, unit, ref);
+    if (BF16) {
       uint32_t b = __float_as_uint(low);
       if (low < 0.0f && (b & 0xffffu)) b += 0x10000u;
       b >>= 16;
       low2 = b | b << 16;
       low = bf16_hi(low2);
     }
-    if (low == -kInfF) c = kInfF;  // nothing left to read -inf as: element by element
+    packed = (ref - low) * k < 1e37f;
+  }
+  // A vector's elements (two at a time), all of them numbers.
+  template <bool FAR>
+  __device__ __forceinline__ void add(uint4 u, float k) {
+    constexpr int N = Vec<BF16>::N;
+    const float2 kk = make_float2(k, k), cc = make_float2(-c, -c), from = make_float2(-ref, -ref);
+    if (BF16) {
+      u.x = bmax2_nan(u.x, low2), u.y = bmax2_nan(u.y, low2);
+      u.z = bmax2_nan(u.z, low2), u.w = bmax2_nan(u.w, low2);
+    }
+    float f[N];
+    Vec<BF16>::unpack(u, f);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      float2 x = make_float2(f[e], f[e + 1]);
+      if (!BF16) x = make_float2(fmaxf(x.x, low), fmaxf(x.y, low));
+      const float2 y = FAR ? __fmul2_rn(__fadd2_rn(x, from), kk) : __ffma2_rn(x, kk, cc);
+      const float2 z = make_float2(ex2_fast(y.x), ex2_fast(y.y));
+      s2 = __fadd2_rn(s2, z);
+      w2 = __ffma2_rn(y, z, w2);
+    }
   }
 };
 
@@ -431,7 +458,8 @@ __device__ __noinline__ void write_outputs(const LogprobParams& p, LogprobShared
   const int outside = __syncthreads_or(range ? 1 : 0);
   if (t == 0) {
     // the entropy of a distribution is not negative; rounding may leave a value just below 0
-    if (p.entropy) p.entropy[i] = empty ? 0.0f : fmaxf(fmaf(__fdiv_rn(r.w, r.s), -kLn2, lz), 0.0f);
+    const float h = fmaf(__fdiv_rn(r.w, r.s), -kLn2, lz);
+    if (p.entropy) p.entropy[i] = empty || h < 0.0f ? 0.0f : h;
     if (p.row_max) p.row_max[i] = r.m;
     if (p.log_z) p.log_z[i] = lz;
     if (p.flags) p.flags[i] = sh.flags | (outside ? kStTokenRange : 0u) | (empty ? kStNonFinite : 0u);
@@ -577,7 +605,7 @@ __global__ void __launch_bounds__(kLpThreads, 7) k_token_logprobs(LogprobParams 
         for (int off = 16; off > 0; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
         if (to > st.limit) st.rise(to, k, unit);
       }
-      if (odd || !st.packed()) {  // element by element
+      if (odd || !st.packed) {  // element by element
         float most = -kInfF;
 #pragma unroll 1
         for (int j = 0; j < U; ++j) {
@@ -594,24 +622,12 @@ __global__ void __launch_bounds__(kLpThreads, 7) k_token_logprobs(LogprobParams 
       }
       batch_done(vm);
       if (st.ref == -kInfF) continue;  // nothing above -inf yet
-      const float2 kk = make_float2(k, k), cc = make_float2(-st.c, -st.c);
+      if (st.far) {
+#pragma unroll 1
+        for (int j = 0; j < U; ++j) st.template add<true>(j == 0 ? u[0] : j == 1 ? u[1] : j == 2 ? u[2] : u[U - 1], k);
+      } else {
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        if (BF16) {
-          u[j].x = bmax2_nan(u[j].x, st.low2), u[j].y = bmax2_nan(u[j].y, st.low2);
-          u[j].z = bmax2_nan(u[j].z, st.low2), u[j].w = bmax2_nan(u[j].w, st.low2);
-        }
-        float f[N];
-        Vec<BF16>::unpack(u[j], f);
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          float2 x = make_float2(f[e], f[e + 1]);
-          if (!BF16) x = make_float2(fmaxf(x.x, st.low), fmaxf(x.y, st.low));
-          const float2 y = __ffma2_rn(x, kk, cc);
-          const float2 z = make_float2(ex2_fast(y.x), ex2_fast(y.y));
-          st.s2 = __fadd2_rn(st.s2, z);
-          st.w2 = __ffma2_rn(y, z, st.w2);
-        }
+        for (int j = 0; j < U; ++j) st.template add<false>(u[j], k);
       }
     }
     st.settle(k);
