@@ -796,14 +796,18 @@ __global__ void __launch_bounds__(kBwdThreads, 6) k_token_logprobs_bwd(LogprobBw
   for (int w = 0; w < (kBwdThreads / 32); ++w) G += s_sum[w];
 
   const float gH = p.g_entropy ? p.g_entropy[row] : 0.0f;
-  const float A = -(G + (p.g_entropy ? gH * p.entropy[row] : 0.0f)) * invT;
+  // Exponents are held kLift higher, and the factors 2^kLift lower: a probability under 2^-126, where the exponential is
+  // flushed to 0, may still have a factor of some thousands (1/T, its logarithm and the entropy).
+  constexpr float kLift = 16.0f, kLower = 0x1p-16f;
   const float B = -gH * kLn2 * invT;
-  const float lz2 = lz * 1.44269504088896340736f;
+  const float A = fmaf(-kLift, B, -(G + (p.g_entropy ? gH * p.entropy[row] : 0.0f)) * invT) * kLower;
+  const float Bl = B * kLower;
+  const float lz2 = fmaf(lz, 1.44269504088896340736f, -kLift);
   // p (A + B t) for one logit; 0 for one that is not a usable, finite logit
   auto grad = [&](float l) {
     const float d = (l - M) * k - lz2;
     const float x = fmaxf(d, -200.0f);  // 2^-200 is 0 in fp32, and keeps 0 * t from becoming NaN
-    const float y = ex2_fast(x) * fmaf(B, x, A);
+    const float y = ex2_fast(x) * fmaf(Bl, x, A);
     return (usable_logit(l) && !empty) ? y : 0.0f;
   };
   const int nvec = p.lg.vocab / N;

@@ -71,7 +71,7 @@ def test_largest_logits(dtype, temp):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("low", [-1e9, -1e10, -1e30])
-@pytest.mark.parametrize("temp", [1.0])
+@pytest.mark.parametrize("temp", [1.0, 0.1])
 def test_gradient_of_masked_rows(dtype, low, temp):
     V = 3001
     rng = np.random.default_rng(4)
@@ -85,3 +85,11 @@ def test_gradient_at_the_smallest_temperatures(dtype, temp):
     rng = np.random.default_rng(5)
     x = _logits(4, 3001, dtype, 6)
     _grad(x, rng.integers(0, 3001, (4, 2)), rng.normal(size=(4, 2)), temp=[temp] * 4)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("temp", [0.3, 0.1, 0.05])
+def test_gradient_of_probabilities_at_the_end_of_fp32(dtype, temp):
+    rng = np.random.default_rng(6)
+    _grad(_logits(8, 20011, dtype, 9), rng.integers(0, 20011, (8, 2)), rng.normal(size=(8, 2)), temp=[temp] * 8,
+          g_ent=rng.normal(size=8))
