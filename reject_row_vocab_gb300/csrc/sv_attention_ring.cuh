@@ -8,7 +8,9 @@
 //
 // The history's rows come in boxes of a page's rows, all of an entry's issued by one warp: what a warp does for an entry
 // (find the pages, wait for room, issue) takes about a microsecond, and four entries are on their way at once.  New rows,
-// the history's last, odd page sizes' and all beside them are gathered row by row, by all loading warps together.
+// the history's last, odd page sizes' and all beside them are gathered row by row, by all loading warps together.  (Rows that
+// are gathered, the zeros behind them and the values taken out of V are written through the generic proxy, boxes through the
+// asynchronous one: a place that the former wrote is fenced before a box goes there.  The barriers alone do not order the two.)
 #pragma once
 
 #include <cstdint>
@@ -301,6 +303,7 @@ struct KvRing {
     const int c = lane % kPieces, sub = lane / kPieces;
     constexpr int kStep = 32 / kPieces;  // rows a warp copies at once
     uint32_t last = 0, opened = 0;              // groups before the next tile's; openings so far
+    uint32_t gathered = 0;                      // groups up to the end of the last tile that had gathered rows
     bool ok = true;
     Ahead now;
     ahead(now);
@@ -309,6 +312,7 @@ struct KvRing {
       ahead(now);
       last = (a.g + 1) * 2 * H;
       const bool whole = a.boxed == kKeys;
+      if (!whole) gathered = last;
       uint32_t good = 0u;  // lane j < 4: of keys 32 j .. 32 j + 31, those in boxes
       if (a.boxed > 0) {
         const uint32_t found = __ballot_sync(0xffffffffu, a.box_word >= 0 && a.box_word < p.c.pages && box_row < a.boxed);
@@ -350,6 +354,7 @@ struct KvRing {
           // words are put together from 0: here those of a tile whose place was read long ago
           if (e == 0 && lane < 8) valid(a.g + kInfo / 2)[lane] = 0u;
           if (a.boxed > 0) {
+            if (q >= NB && q - NB < gathered) fence_async();  // by the lanes that issue the boxes, behind their wait
             // (a page outside the cache is outside the tensor: the box is filled with zeros)
             if (lane == 0) mbar_expect_tx(full(q), a.boxed * 128 * CB);
             __syncwarp();
