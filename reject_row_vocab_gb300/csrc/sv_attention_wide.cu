@@ -289,6 +289,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           mixed = true;
           const int from = max(s.r.len - x0, 0), upto = min(s.r.len + s.r.n - x0, kKeys);  // the new rows
           bool found = false;
+          // With one tile's entries in the ring V(g) lies where V(g - 1) did, which S(g) does not wait for: the phase before
+          // the one waited for here is known to be over once V(g - 1) has been used.  (A unit's first tile comes after the
+          // end of the unit before; larger rings have V(g - 2) or an older one in the place, and S(g) comes behind its use.)
+          if (R::kEntries == 2 * H && i > 0 && !ring.wait(bar_pv(g - 1), half(g - 1))) {
+            ok = false;
+            break;
+          }
 #pragma unroll 1
           for (int h = 0; ok && h < H; ++h) {
             const uint32_t group = 2 * H * g + H + h;

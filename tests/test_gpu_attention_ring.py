@@ -13,7 +13,7 @@ from reject_row_vocab_gb300 import _build  # noqa: E402
 
 _build.build()
 from reject_row_vocab_gb300 import specverify as sv  # noqa: E402
-from tests.serving_cases import BF16, F32, AttentionCase, check_attention  # noqa: E402
+from tests.serving_cases import BF16, F32, AttentionCase, attention_bounds, check_attention  # noqa: E402
 
 
 def _lens(n, seed):
@@ -37,3 +37,37 @@ def test_boxes_where_gathered_rows_were(dtype, rows, dim):
     # (the oracle goes key by key: a part of the requests)
     small = AttentionCase(_lens(24, rows), rows, 4, 2, dim, 16, dtype, seed=dim + 1)
     check_attention(small, small.run(sv))
+
+
+def check_rows(case, got, keep):
+    """check_attention for the rows `keep` alone."""
+    o = case.oracle()
+    tol, lse_tol = attention_bounds(o, case.q.shape[2], case.dtype)
+    out, lse = got.out.double().cpu().numpy(), got.lse.double().cpu().numpy()
+    assert np.isfinite(out[keep]).all()
+    assert (np.abs(out - o["out"])[keep] <= tol[keep]).all()
+    assert np.array_equal(np.isneginf(lse[keep]), np.isneginf(o["lse"][keep]))
+    fine = np.isfinite(o["lse"][keep])
+    assert (np.abs(lse[keep][fine] - o["lse"][keep][fine]) <= lse_tol[keep][fine]).all()
+    assert np.array_equal(got.dev_status.cpu().numpy().view(np.uint32), o["status"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim", [64, 128, 136, 256])
+@pytest.mark.parametrize("rows", [4, 20])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_of_unseen_rows_behind_long_histories(dtype, dim, rows, bad):
+    # every request's third row holds what only it sees, behind histories of several tiles
+    c = AttentionCase([900, 260, 37, 128, 511, 0, 1300], rows, 8, 2, dim, 16, dtype, tree=True, staged=True, seed=dim + rows)
+    R = rows * len(c.lens)
+    for b in range(len(c.lens)):
+        c.mask[b, :, 2] = 0
+        c.mask[b, 2, 2] = 1
+        s = int(c.row_slots[b * rows + 2])
+        c.k[0, s // 16, s % 16] = bad
+        c.v[0, s // 16, s % 16, :, ::3] = bad
+    got = c.run(sv)
+    check_rows(c, got, [r for r in range(R) if r % rows != 2])
+    for _ in range(3):
+        again = c.run(sv)
+        assert torch.equal(torch.nan_to_num(got.out), torch.nan_to_num(again.out))
