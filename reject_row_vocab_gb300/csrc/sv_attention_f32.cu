@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
                                                               Ring::piece(k0 + y / (Ring::kPieces * E), c % Ring::kPieces))))
                 found = true;
             }
+            __syncwarp();  // what a lane took out, another reads (a vote orders no memory)
             careful = __any_sync(0xffffffffu, found) || careful;
           }
           const char* vt = ring.tile_mem(group + (H == 1 ? 0 : lane >> 4)) + (piece >> 3 & 1) * Ring::kBlock + k0 * 128;

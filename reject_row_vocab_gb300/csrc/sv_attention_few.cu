@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
             for (int x = max(s.r.len - x0, 0) * R::kPieces + lane; x < min(s.r.len + s.r.n - x0, W::kOwn) * R::kPieces; x += 32)
               if (make_finite<true>(reinterpret_cast<uint4*>(v + R::piece(k0 + x / R::kPieces, x % R::kPieces)))) found = true;
+            __syncwarp();  // what a lane took out, another reads (a vote orders no memory)
             careful = __any_sync(0xffffffffu, found) || careful;
           }
           const uint32_t vt = ring.tile(group_v) + v_at;

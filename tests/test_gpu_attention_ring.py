@@ -71,3 +71,20 @@ def test_values_of_unseen_rows_behind_long_histories(dtype, dim, rows, bad):
     for _ in range(3):
         again = c.run(sv)
         assert torch.equal(torch.nan_to_num(got.out), torch.nan_to_num(again.out))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads", [2, 8])
+def test_every_other_row_holds_no_number(dtype, dim, heads):
+    # a lane takes the values out that other lanes of its warp read next
+    for rows in (4, 8):
+        c = AttentionCase([120, 0, 640, 57] * 4, rows, heads, 2, dim, 16, dtype, tree=True, staged=True, seed=dim + rows)
+        c.mask[:] = 0
+        c.mask[:, ::2, ::2] = np.tril(np.ones((rows // 2, rows // 2), np.uint8))
+        for s in c.row_slots.reshape(-1, rows)[:, 1::2].ravel():
+            c.k[0, s // 16, s % 16], c.v[0, s // 16, s % 16] = float("nan"), float("-inf")
+        first = c.run(sv)
+        check_rows(c, first, list(range(len(c.q))))
+        for _ in range(5):
+            assert torch.equal(first.out, c.run(sv).out)
