@@ -337,6 +337,9 @@ struct AttnWalk {
 // not by others: there they are taken out of the products, and added at the end to the rows that see them.
 // ---------------------------------------------------------------------------------------------------------------------
 
+// Whether a row of the request may not see one of its new rows.  (A single row sees itself, unless a mask says otherwise.)
+__device__ __forceinline__ bool new_rows_differ(const AttnParams& p, const AttnRequest& r) { return r.n > 1 || p.mask; }
+
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // two bf16
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
   if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;

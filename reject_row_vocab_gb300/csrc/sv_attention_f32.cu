@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
           for (int e = 0; e < E; ++e)
             if (!ring.wait(ring.full(group + e), ring.phase(group + e))) ok = false;
           if (!ok) break;
-          if (s.r.n > 1 && x0 + kOwn > s.r.len) {
+          if (new_rows_differ(p, s.r) && x0 + kOwn > s.r.len) {
             bool found = false;
 #pragma unroll 1
             for (int y = max(s.r.len - x0, 0) * Ring::kPieces * E + lane; y < min(s.r.len + s.r.n - x0, kOwn) * Ring::kPieces * E;

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             done(ring.empty(group_v));
             continue;
           }
-          if (s.r.n > 1 && x0 + W::kOwn > s.r.len) {
+          if (new_rows_differ(p, s.r) && x0 + W::kOwn > s.r.len) {
             char* v = ring.tile_mem(group_v);
             bool found = false;
 #pragma unroll 1

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
         bad |= vb.x | vb.y | vb.z | vb.w;
         const bool masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xffffffffu || x0 + kKeys > s.r.len;
-        if (masked && s.r.n > 1 && x0 + kKeys > s.r.len) {
+        if (masked && new_rows_differ(p, s.r) && x0 + kKeys > s.r.len) {
           mixed = true;
           const int from = max(s.r.len - x0, 0), upto = min(s.r.len + s.r.n - x0, kKeys);  // the new rows
           bool found = false;

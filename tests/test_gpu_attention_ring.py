@@ -88,3 +88,17 @@ def test_every_other_row_holds_no_number(dtype, dim, heads):
         check_rows(c, first, list(range(len(c.q))))
         for _ in range(5):
             assert torch.equal(first.out, c.run(sv).out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("heads", [4, 40])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_single_row_that_does_not_see_itself(dtype, heads, bad):
+    for ragged in (False, True):
+        c = AttentionCase([300, 0, 37, 128], [1, 2, 1, 1] if ragged else 1, heads, 2, 128, 16, dtype, tree=True, staged=True,
+                          ragged=ragged, seed=heads)
+        c.mask[:] = 0
+        for s in c.row_slots:
+            c.k[0, s // 16, s % 16] = bad
+            c.v[0, s // 16, s % 16, :, ::3] = bad
+        check_rows(c, c.run(sv), list(range(len(c.q))))
