@@ -462,6 +462,9 @@ sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int
  * writes, so its sources and destinations may overlap (drafts staged in
  * place); those of different requests must not.  A request commits at most
  * max_len (<= 1024) entries, and the lists hold list_len entries.
+ * Every entry of the cache must have memory of its own: SV_ERR_UNSUPPORTED when
+ * an axis is repeated (a stride of 0) or its stride is less than the axes with
+ * smaller ones span, and when K and V share memory (they may be interleaved).
  * dev_status [batch] (may be NULL): SV_DEV_BAD_LAYOUT when the request's range
  * is invalid (nothing is moved), SV_DEV_SLOT_RANGE when an entry's slot or
  * position lies outside the cache (that entry is not moved).

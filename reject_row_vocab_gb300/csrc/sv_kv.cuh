@@ -64,6 +64,40 @@ inline sv_status_t check_cache(const sv_kv_cache_t* c, KvView* v) {
   return SV_OK;
 }
 
+// Whether every entry of K and V has memory of its own (a call that writes to the cache needs that).  The steps have to be
+// nested: each at least what the axes with smaller ones span.  Then K and V meet if and only if some combination of steps
+// comes within a row of the distance between them, and of each axis, from the largest step down, only the two multiples
+// about what is left can.
+inline bool entries_apart(const KvView& c) {
+  struct Axis {
+    __int128 step;
+    int64_t n;
+  } axes[4] = {};
+  int count = 0;
+  auto add = [&](int64_t step, int64_t n) {
+    if (n < 2) return;
+    int i = count++;
+    for (; i > 0 && axes[i - 1].step > static_cast<__int128>(step) * c.es; --i) axes[i] = axes[i - 1];
+    axes[i] = Axis{static_cast<__int128>(step) * c.es, n};
+  };
+  add(c.head_stride, c.heads), add(c.slot_stride, c.page_size), add(c.page_stride, c.pages), add(c.layer_stride, c.layers);
+  const __int128 row = static_cast<__int128>(c.head_dim) * c.es;
+  __int128 span = row;
+  for (int i = 0; i < count; ++i) {
+    if (axes[i].step < span) return false;
+    span += axes[i].step * (axes[i].n - 1);
+  }
+  auto meets = [&](auto&& self, int i, __int128 apart) -> bool {
+    if (i < 0) return -row < apart && apart < row;
+    const __int128 most = axes[i].n - 1;
+    const __int128 d = apart / axes[i].step;
+    for (__int128 m = d - 1; m <= d + 1; ++m)
+      if (-most <= m && m <= most && self(self, i - 1, apart - m * axes[i].step)) return true;
+    return false;
+  };
+  return !meets(meets, count - 1, static_cast<__int128>(reinterpret_cast<intptr_t>(c.v)) - reinterpret_cast<intptr_t>(c.k));
+}
+
 // Element offset (within a layer and head 0) of a slot, or -1 outside the cache.
 __device__ __forceinline__ int64_t kv_slot_offset(const KvView& c, int64_t slot) {
   if (slot < 0 || slot >= static_cast<int64_t>(c.pages) * c.page_size) return -1;

@@ -115,6 +115,7 @@ extern "C" sv_status_t spec_verify_kv_commit(const sv_kv_cache_t* cache, int32_t
   if (c.layers > 32767) return SV_ERR_BAD_SHAPE;
   if (batch == 0) return SV_OK;
   if (!commit_cu || (list_len > 0 && (!commit_src_slot || !commit_dst_pos))) return SV_ERR_NULL_ARG;
+  if (!entries_apart(c)) return SV_ERR_UNSUPPORTED;  // a block would read what another has already moved
   DeviceInfo dev{};
   cudaError_t e = device_info(&dev);
   if (e != cudaSuccess) return cuda_failure(e);
