@@ -66,36 +66,37 @@ inline sv_status_t check_cache(const sv_kv_cache_t* c, KvView* v) {
 
 // Whether every entry of K and V has memory of its own (a call that writes to the cache needs that).  The steps have to be
 // nested: each at least what the axes with smaller ones span.  Then K and V meet if and only if some combination of steps
-// comes within a row of the distance between them, and of each axis, from the largest step down, only the two multiples
-// about what is left can.
+// comes within a row of the distance between them, and of each axis, from the largest step down, only the multiples about
+// what is left can.
 inline bool entries_apart(const KvView& c) {
   struct Axis {
-    __int128 step;
-    int64_t n;
+    int64_t step, n;  // bytes, entries
   } axes[4] = {};
   int count = 0;
   auto add = [&](int64_t step, int64_t n) {
     if (n < 2) return;
     int i = count++;
-    for (; i > 0 && axes[i - 1].step > static_cast<__int128>(step) * c.es; --i) axes[i] = axes[i - 1];
-    axes[i] = Axis{static_cast<__int128>(step) * c.es, n};
+    for (; i > 0 && axes[i - 1].step > step; --i) axes[i] = axes[i - 1];
+    axes[i] = Axis{step, n};
   };
-  add(c.head_stride, c.heads), add(c.slot_stride, c.page_size), add(c.page_stride, c.pages), add(c.layer_stride, c.layers);
-  const __int128 row = static_cast<__int128>(c.head_dim) * c.es;
-  __int128 span = row;
+  add(c.head_stride * c.es, c.heads), add(c.slot_stride * c.es, c.page_size);
+  add(c.page_stride * c.es, c.pages), add(c.layer_stride * c.es, c.layers);
+  const int64_t row = c.head_dim * c.es;
+  int64_t span = row;
   for (int i = 0; i < count; ++i) {
-    if (axes[i].step < span) return false;
+    if (axes[i].step < span || axes[i].step > (INT64_MAX - span) / axes[i].n) return false;
     span += axes[i].step * (axes[i].n - 1);
   }
-  auto meets = [&](auto&& self, int i, __int128 apart) -> bool {
-    if (i < 0) return -row < apart && apart < row;
-    const __int128 most = axes[i].n - 1;
-    const __int128 d = apart / axes[i].step;
-    for (__int128 m = d - 1; m <= d + 1; ++m)
-      if (-most <= m && m <= most && self(self, i - 1, apart - m * axes[i].step)) return true;
+  const int64_t apart = reinterpret_cast<intptr_t>(c.v) - reinterpret_cast<intptr_t>(c.k);
+  if (apart >= span || apart <= -span) return true;
+  auto meets = [&](auto&& self, int i, int64_t left) -> bool {
+    if (i < 0) return -row < left && left < row;
+    const int64_t most = axes[i].n - 1, d = left / axes[i].step;
+    for (int64_t m = d - 1; m <= d + 1; ++m)
+      if (-most <= m && m <= most && self(self, i - 1, left - m * axes[i].step)) return true;
     return false;
   };
-  return !meets(meets, count - 1, static_cast<__int128>(reinterpret_cast<intptr_t>(c.v)) - reinterpret_cast<intptr_t>(c.k));
+  return !meets(meets, count - 1, apart);
 }
 
 // Element offset (within a layer and head 0) of a slot, or -1 outside the cache.
