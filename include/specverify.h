@@ -431,9 +431,10 @@ typedef struct {
  *   s_x = scale * (q . k_x)   out = sum_x softmax(s)_x v_x   lse = ln sum_x exp(s_x)
  *
  * with fp32 statistics and sums; out (cache dtype, its own row and head
- * strides, not smaller than head_dim) is rounded once.  lse [total_rows, num_heads] fp32 may be NULL.  A
- * row that sees nothing, or only scores of -inf, has out 0 and lse -inf.  K/V
- * of entries a row does not see do not influence it, whatever they hold.
+ * strides, the larger at least what the other axis spans) is rounded once.
+ * lse [total_rows, num_heads] fp32 may be NULL.  A row that sees nothing, or
+ * only scores of -inf, has out 0 and lse -inf.  K/V of entries a row does not
+ * see do not influence it, whatever they hold.
  *
  * dev_status [batch]: SV_DEV_BAD_LAYOUT for an invalid row range (the request's
  * rows are left unwritten) or a negative seq_lens[b] (taken as 0);

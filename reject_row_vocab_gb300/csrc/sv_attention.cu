@@ -101,9 +101,17 @@ sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int
   if (static_cast<int64_t>(max_len) * num_heads > (1 << 24)) return SV_ERR_BAD_SHAPE;
   if (!cu_seqlens && total_rows < static_cast<int64_t>(batch) * max_len) return SV_ERR_BAD_SHAPE;
   if (q_row_stride < 0 || q_head_stride < 0 || out_row_stride < 0 || out_head_stride < 0) return SV_ERR_BAD_SHAPE;
-  // rows or heads of the output that lay over one another would be written in no order
-  if ((num_heads > 1 && out_head_stride < c.head_dim) || (total_rows > 1 && out_row_stride < c.head_dim))
-    return SV_ERR_BAD_SHAPE;
+  // rows or heads of the output that lay over one another would be written in no order: the larger of the two steps has to
+  // be at least what the other axis spans
+  const bool row_last = out_row_stride >= out_head_stride;
+  const int64_t steps[2] = {row_last ? out_head_stride : out_row_stride, row_last ? out_row_stride : out_head_stride};
+  const int64_t counts[2] = {row_last ? num_heads : total_rows, row_last ? total_rows : num_heads};
+  int64_t span = c.head_dim;
+  for (int i = 0; i < 2; ++i) {
+    if (counts[i] < 2) continue;
+    if (steps[i] < span || steps[i] > (INT64_MAX - span) / counts[i]) return SV_ERR_BAD_SHAPE;
+    span += steps[i] * (counts[i] - 1);
+  }
   if (batch == 0) return SV_OK;
   if (!q || !out || !seq_lens || !dev_status) return SV_ERR_NULL_ARG;
   if (!aligned16(q) || !aligned16(out) || (q_row_stride * c.es) % 16 != 0 || (q_head_stride * c.es) % 16 != 0 ||

@@ -102,3 +102,12 @@ def test_a_single_row_that_does_not_see_itself(dtype, heads, bad):
             c.k[0, s // 16, s % 16] = bad
             c.v[0, s // 16, s % 16, :, ::3] = bad
         check_rows(c, c.run(sv), list(range(len(c.q))))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [1, 20])
+def test_an_output_of_heads_before_rows(dtype, rows):
+    c = AttentionCase([300, 37], rows, 8, 2, 64, 16, dtype, seed=rows)
+    out = sv.AttentionOutputs.allocate(2 * rows, 8, 64, 2, dtype)
+    out.out = torch.empty(8, 2 * rows, 64, dtype=dtype, device="cuda").transpose(0, 1)
+    check_attention(c, c.run(sv, out=out))
