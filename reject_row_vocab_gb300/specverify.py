@@ -681,8 +681,8 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
     """Attention of each request's new rows q [rows, heads, head_dim] over its committed positions in the cache and
     over the new rows themselves.
 
-    seq_lens [batch] int64: committed positions, without the new rows.  A request has max_len new rows
-    (rows / batch when not given; 1 is plain decoding), or cu_seqlens [batch + 1] int32 gives ragged ones of 1..max_len.
+    seq_lens [batch] int64: committed positions, without the new rows.  A request has max_len new rows (rows / batch, a
+    whole number, when not given; 1 is plain decoding), or cu_seqlens [batch + 1] int32 gives ragged ones of 1..max_len.
     row_slots [rows] int64: where the new rows' K/V lie (None: at positions seq_lens + j).  mask [batch, max_len,
     max_len] uint8: which new rows a row sees (None: itself and earlier ones), as build_tree returns it.
     scale defaults to 1 / sqrt(head_dim)."""
@@ -702,6 +702,8 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
     if max_len is None:
         if cu_seqlens is not None:
             raise ValueError("max_len is required with cu_seqlens")
+        if batch and (rows % batch or not rows):
+            raise ValueError("q's %d rows do not divide among %d requests: max_len is required" % (rows, batch))
         max_len = rows // batch if batch else 1
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, dev, index)

@@ -28,3 +28,18 @@ def test_a_binding_passes_overlapping_outputs_on_to_the_library(cpu_binding):  #
     out.out = buf.as_strided((6, 4, 16), (16, 16, 1))
     _attn(out=out)
     assert cpu_binding.calls[0][1][15:17] == (16, 16)
+
+
+@pytest.mark.parametrize("rows", [4, 5, 7, 2])
+def test_rows_that_no_request_would_own(cpu_binding, rows):  # noqa: F811
+    # three requests and no max_len: the rows have to divide among them
+    q = torch.zeros(rows, 4, 16, dtype=BF16)
+    with pytest.raises(ValueError, match="max_len"):
+        _attn(q=q, max_len=None)
+    assert cpu_binding.calls == []
+
+
+def test_rows_left_over_on_purpose(cpu_binding):  # noqa: F811
+    _attn(q=torch.zeros(7, 4, 16, dtype=BF16), max_len=2)
+    _attn(q=torch.zeros(9, 4, 16, dtype=BF16), max_len=None)
+    assert [c[1][8] for c in cpu_binding.calls] == [2, 3]
