@@ -2,7 +2,7 @@
 // tensor cores: bf16, tiles of 128 rows and 128 keys.
 //
 //   S = Q K^T (128 x 128, tensor memory)     one thread issues the products
-//   P = 2^(c S - m), l += sum P              one thread a row: no exchange
+//   P = 2^(c (S - m)), l += sum P            one thread a row: no exchange
 //   O += P V  (P from tensor memory)         accumulated in tensor memory
 //
 // Four softmax warps, four loading warps, one warp that issues the matrix
@@ -47,6 +47,7 @@ constexpr int kReaders = 10;                                       // warps that
 // the trees).
 constexpr int kUnitPlaces = 2;
 constexpr float kSlack = 8.0f;  // log2 units a row's maximum may pass its reference by
+constexpr float kNear = 128.0f;  // and a reference may have with its factor rounded
 
 // ---------------------------------------------------------------------------------------------------------------------
 // Tensor memory and matrix instructions
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const bool idle = warp * 32 >= rows;              // none of the warp's rows exists
       const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread, and its head
       const int head = s.hkv * p.group + (s.rt * kRows + t) - my_row * p.group;
-      float m = -kInfF, l = 0.0f;
+      float m = -kInfF, l = 0.0f;  // m: a score without its factor c
       uint32_t bad = 0u;
       bool mixed = false;  // a tile whose keys some rows see and others do not
       const int cnt = s.cnt, t0 = s.t0;
@@ -341,12 +342,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
             for (int j = 0; j < 64; ++j) mx[j & 3] = fmax_nan(mx[j & 3], v[j]);
           }
-          const float top = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3])) * c;
-          const bool grow = !(top <= m + kSlack);  // also a first finite maximum, and NaN
+          const float top = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3]));
+          const bool grow = !(top <= m) && !((top - m) * c <= kSlack);  // also a first finite maximum, and NaN
           if (i == 0) {
             m = top;
           } else if (__any_sync(0xffffffffu, grow)) {
-            const float a = grow ? ex2_fast(m - top) : 1.0f;
+            const float a = grow ? ex2_fast((m - top) * c) : 1.0f;
             if (grow) m = top;
             l *= a;
             if (!ring.wait(bar_pv(g - 1), half(g - 1))) {
@@ -364,7 +365,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               tmem_st32(tmem + lanes + W::kO + h * 32, reinterpret_cast<const uint32_t*>(o));
             }
           }
-          const float ref = m == -kInfF ? 0.0f : m;
+          // c S - c m, one multiply-add with c m rounded (by 2^-18 at most), as long as c m is small enough; where a row's is
+          // not, the warp's rows are moved to their references first, in place: at 2^31 the rounding alone would be past the
+          // exponent's range.
+          float ref = m == -kInfF ? 0.0f : m * c;
+          if (__any_sync(0xffffffffu, !(fabsf(ref) < kNear))) {
+            const float from = m == -kInfF ? 0.0f : m;
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              float v[32];
+              tmem_ld32(st + h * 32, reinterpret_cast<uint32_t*>(v));
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] -= from;
+              tmem_st32(st + h * 32, reinterpret_cast<const uint32_t*>(v));
+            }
+            tmem_wait_st();
+            ref = 0.0f;
+          }
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -439,10 +457,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       }
       if (whole) {
-        if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m, kLn2, logf(l));
+        if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m * c, kLn2, logf(l));
         if (s.reports && t == 0) p.status[s.b] = bad | attn_timeout(p);
       } else {
-        part[P::kM + t] = m;
+        part[P::kM + t] = m * c;
         part[P::kL + t] = l;
         if (t == 0) {
           part[P::kStatus] = __uint_as_float(bad);

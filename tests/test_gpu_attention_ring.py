@@ -39,9 +39,11 @@ def test_boxes_where_gathered_rows_were(dtype, rows, dim):
     check_attention(small, small.run(sv))
 
 
-def check_rows(case, got, keep):
-    """check_attention for the rows `keep` alone."""
+def check_rows(case, got, keep, exact_scores=False):
+    """check_attention for the rows `keep` alone; exact_scores: fp32 holds all of their scores' sums exactly."""
     o = case.oracle()
+    if exact_scores:
+        o["smax"][:] = 0.0
     tol, lse_tol = attention_bounds(o, case.q.shape[2], case.dtype)
     out, lse = got.out.double().cpu().numpy(), got.lse.double().cpu().numpy()
     assert np.isfinite(out[keep]).all()
@@ -111,3 +113,17 @@ def test_an_output_of_heads_before_rows(dtype, rows):
     out = sv.AttentionOutputs.allocate(2 * rows, 8, 64, 2, dtype)
     out.out = torch.empty(8, 2 * rows, 64, dtype=dtype, device="cuda").transpose(0, 1)
     check_attention(c, c.run(sv, out=out))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [1, 3, 18])
+@pytest.mark.parametrize("power", [10, 24, 31, 40, 80, 120])
+def test_largest_scores(dtype, rows, power):
+    # scores of a whole number times 2^power: the weights are 0, or shared by the keys that have the largest one
+    c = AttentionCase([300, 37, 0, 1300], rows, 8, 2, 64, 16, dtype, seed=power + rows, poison=False)
+    g = torch.Generator().manual_seed(power)
+    c.q = torch.zeros_like(c.q)
+    c.q[..., 5] = 2.0 ** power * (1 - 2 * torch.randint(0, 2, c.q.shape[:2], generator=g)).to(dtype)
+    c.k[..., 5] = torch.randint(-40, 41, c.k.shape[:-1], generator=g).to(dtype)
+    for c.scale in (1.0, -2.0):
+        check_rows(c, c.run(sv), list(range(len(c.q))), exact_scores=True)
