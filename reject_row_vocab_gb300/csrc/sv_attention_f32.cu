@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_f32(const AttnParams 
           }
         }
         if (!whole && lane < R) part[P::kM + lane] = M, part[P::kL + lane] = L;
-        if (odd_ones) add_nonfinite<false, R, DP>(p, s, rows, 0, whole ? nullptr : part);
+        if (odd_ones) add_nonfinite<false, R, DP>(p, s, rows, 0, __ballot_sync(0xffffffffu, none), whole ? nullptr : part);
         if (whole) {
           if (s.reports && lane == 0) p.status[s.b] = bad | attn_timeout(p);
         } else {

@@ -307,7 +307,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
         }
         if (odd) {
-          add_nonfinite<true, kRows, W::kCols>(p, s, rows, d0, whole ? nullptr : part);
+          uint32_t none = 0u;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) none |= __reduce_or_sync(0xffffffffu, m[h] == -kInfF ? 1u << ((lane >> 2) + h * 8) : 0u);
+          add_nonfinite<true, kRows, W::kCols>(p, s, rows, d0, none, whole ? nullptr : part);
         }
         if (whole) {
           if (s.reports && warp == 0 && lane == 0) p.status[s.b] = bad | attn_timeout(p);

@@ -446,13 +446,14 @@ struct KvRing {
 };
 
 // The NaN and infinite values that the products left out, added by a warp to the rows that it has just written: to its
-// part of the unit, or, without one, to the output.  Units of MT rows, columns d0 .. d0 + COLS - 1.
+// part of the unit, or, without one, to the output, where rows of `none` (a bit each) saw scores of -inf alone and stay 0.
+// Units of MT rows, columns d0 .. d0 + COLS - 1.
 template <bool BF16, int MT, int COLS>
-__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, int d0, float* part) {
+__device__ __noinline__ void add_nonfinite(const AttnParams& p, const AttnSegment& s, int rows, int d0, uint32_t none, float* part) {
   __syncwarp();
   for (int x = threadIdx.x & 31; x < min(rows, MT) * (COLS / 4); x += 32) {
     const int row = x / (COLS / 4), d = d0 + x % (COLS / 4) * 4, grow = s.rt * MT + row, i = grow / p.group;
-    if (d >= p.c.head_dim) continue;
+    if (d >= p.c.head_dim || (!part && (none >> row & 1u))) continue;
     const float4 f = nonfinite_seen<BF16, kKeys>(p, s, i, d);
     if (part) {
       float4* at = reinterpret_cast<float4*>(part) + (d / 4) * MT + row;

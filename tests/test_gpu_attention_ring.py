@@ -127,3 +127,23 @@ def test_largest_scores(dtype, rows, power):
     c.k[..., 5] = torch.randint(-40, 41, c.k.shape[:-1], generator=g).to(dtype)
     for c.scale in (1.0, -2.0):
         check_rows(c, c.run(sv), list(range(len(c.q))), exact_scores=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [1, 3, 18])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_only_scores_of_minus_infinity_give_zero(dtype, rows, bad):
+    # no history; every new row sees new row 0 (and the last one itself), whose scores are -inf and whose V holds no number
+    c = AttentionCase([0, 0], rows, 8, 2, 64, 16, dtype, tree=True, staged=True, seed=rows)
+    c.q[..., 5] = 1.0
+    c.mask[:] = 0
+    c.mask[:, :, 0] = 1
+    c.mask[:, rows - 1, rows - 1] = 1
+    for s in c.row_slots.reshape(2, rows)[:, 0]:
+        c.k[0, s // 16, s % 16] = 0.0
+        c.k[0, s // 16, s % 16, :, 5] = -float("inf")
+        c.v[0, s // 16, s % 16, :, ::3] = bad
+    got = c.run(sv)
+    for b in range(2):
+        for i in range(rows - 1 if rows > 1 else 1):
+            assert torch.isneginf(got.lse[b * rows + i]).all() and (got.out[b * rows + i] == 0).all(), (b, i)
