@@ -225,9 +225,10 @@ struct Stream {
     }
     packed = (ref - low) * k < 1e37f;
   }
-  // A vector's elements (two at a time), all of them numbers.
+  // A vector's elements (two at a time), all of them numbers, to sums of the batch: a row in one block gives a thread some
+  // 600 elements for each half, and beside a likely token's weight the last bits of the many small ones would be lost.
   template <bool FAR>
-  __device__ __forceinline__ void add(uint4 u, float k) {
+  __device__ __forceinline__ void add(uint4 u, float k, float2& bs, float2& bw) const {
     constexpr int N = Vec<BF16>::N;
     const float2 kk = make_float2(k, k), cc = make_float2(-c, -c), from = make_float2(-ref, -ref);
     if (BF16) {
@@ -242,8 +243,8 @@ struct Stream {
       if (!BF16) x = make_float2(fmaxf(x.x, low), fmaxf(x.y, low));
       const float2 y = FAR ? __fmul2_rn(__fadd2_rn(x, from), kk) : __ffma2_rn(x, kk, cc);
       const float2 z = make_float2(ex2_fast(y.x), ex2_fast(y.y));
-      s2 = __fadd2_rn(s2, z);
-      w2 = __ffma2_rn(y, z, w2);
+      bs = __fadd2_rn(bs, z);
+      bw = __ffma2_rn(y, z, bw);
     }
   }
 };
@@ -622,13 +623,17 @@ __global__ void __launch_bounds__(kLpThreads, 7) k_token_logprobs(LogprobParams 
       }
       batch_done(vm);
       if (st.ref == -kInfF) continue;  // nothing above -inf yet
+      float2 s2 = make_float2(0.0f, 0.0f), w2 = make_float2(0.0f, 0.0f);
       if (st.far) {
 #pragma unroll 1
-        for (int j = 0; j < U; ++j) st.template add<true>(j == 0 ? u[0] : j == 1 ? u[1] : j == 2 ? u[2] : u[U - 1], k);
+        for (int j = 0; j < U; ++j)
+          st.template add<true>(j == 0 ? u[0] : j == 1 ? u[1] : j == 2 ? u[2] : u[U - 1], k, s2, w2);
       } else {
 #pragma unroll
-        for (int j = 0; j < U; ++j) st.template add<false>(u[j], k);
+        for (int j = 0; j < U; ++j) st.template add<false>(u[j], k, s2, w2);
       }
+      st.s2 = __fadd2_rn(st.s2, s2);
+      st.w2 = __fadd2_rn(st.w2, w2);
     }
     st.settle(k);
     if (had > 0) sh.peak[group][t] = static_cast<uint16_t>(ordered(peak) >> 16);

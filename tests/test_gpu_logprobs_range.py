@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from test_gpu_logprobs import BF16, F32, _check, _grad, _logits  # noqa: E402
+from test_gpu_logprobs import BF16, F32, _check, _grad, _logits, dw, sv  # noqa: E402
 
 MASKS = [-1e4, -65504.0, -1e8, -1e9, -1e10, -1e12, -1e20, -1e30, -3e38]
 
@@ -93,3 +93,23 @@ def test_gradient_of_probabilities_at_the_end_of_fp32(dtype, temp):
     rng = np.random.default_rng(6)
     _grad(_logits(8, 20011, dtype, 9), rng.integers(0, 20011, (8, 2)), rng.normal(size=(8, 2)), temp=[temp] * 8,
           g_ent=rng.normal(size=8))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_small_weights_beside_large_ones(dtype):
+    # 256 tokens of weight 1, one early in each of the sums that 128 threads hold, and 151680 of 2^-24.9, each below the last
+    # place of a sum that has one of the others; every row in one block
+    V, n = 151936, 1024
+    x = torch.full((1, V), -17.25)
+    per = 8 if dtype == BF16 else 4
+    x[0, (per * torch.arange(128)[:, None] + torch.arange(2)).ravel()] = 0.0
+    d = dw.padded_rows(x.to(dtype), "cuda")
+    got = sv.token_logprobs(d, torch.zeros(n, 1, dtype=torch.int32, device="cuda"),
+                            row_index=torch.zeros(n, dtype=torch.int32, device="cuda"))
+    rest = 151680 * np.exp(-17.25)
+    want = np.log(256 + rest)
+    # a sum's 64 elements, the ten such sums of a row, and the join of 128 threads, each 2^-24; an exponential 2^-21
+    tol = (64 + 10 + 64) * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -23 * want
+    assert (got.log_z.double().cpu() - want).abs().max() <= tol
+    entropy = want + 17.25 * rest / (256 + rest)
+    assert (got.entropy.double().cpu() - entropy).abs().max() <= tol * (1 + 17.25)
