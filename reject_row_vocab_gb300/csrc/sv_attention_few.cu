@@ -9,8 +9,10 @@
 // of them writes the rows while the others go on.  The units that a block
 // shares with others are joined at its end, by all its threads.
 //
-// The weights are rounded to bf16 for the product with V (the matrix unit takes
-// operands of one type); their sum l is of the unrounded ones, in fp32.
+// The matrix unit takes operands of one type, so the weights go to the product
+// with V as two bf16 values, their rounding and the rounding of what it leaves
+// (16 bits together: the instructions are not what limits, 128 requests take 322
+// us with one value and 323 with two); their sum l is in fp32.
 //
 // Measured: one token of 128 requests of up to 8192, 32 heads of 128 on 8 in the
 // cache: 317 us, 6.8 TB/s; 64 requests, heads of 256: 332 us, 6.6 TB/s; one of a
@@ -218,12 +220,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           for (int n = 0; n < NT; n += 2) {
             const uint32_t a[4] = {pack_bf16(sc[n][0], sc[n][1]), pack_bf16(sc[n][2], sc[n][3]),
                                    pack_bf16(sc[n + 1][0], sc[n + 1][1]), pack_bf16(sc[n + 1][2], sc[n + 1][3])};
+            uint32_t rest[4];  // what the rounding leaves
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              rest[i] = pack_bf16(sc[n + (i >> 1)][(i & 1) * 2] - bf16_lo(a[i]), sc[n + (i >> 1)][(i & 1) * 2 + 1] - bf16_hi(a[i]));
 #pragma unroll
             for (int d = 0; d < DT; d += 2) {
               uint32_t vb[4];
               ldmatrix4_trans((vt ^ (d & 6) << 4) + (d >> 3) * R::kBlock + n * 1024, vb);
               mma_bf16(o[d], a, vb[0], vb[1]);
               mma_bf16(o[d + 1], a, vb[2], vb[3]);
+              mma_bf16(o[d], rest, vb[0], vb[1]);
+              mma_bf16(o[d + 1], rest, vb[2], vb[3]);
             }
           }
           done(ring.empty(group_v));

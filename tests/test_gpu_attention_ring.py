@@ -147,3 +147,17 @@ def test_only_scores_of_minus_infinity_give_zero(dtype, rows, bad):
     for b in range(2):
         for i in range(rows - 1 if rows > 1 else 1):
             assert torch.isneginf(got.lse[b * rows + i]).all() and (got.out[b * rows + i] == 0).all(), (b, i)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 4])
+def test_weights_of_few_rows_keep_more_than_eight_bits(dim, rows):
+    # outputs near 0, sums of terms that cancel: weights rounded once, by 2^-9, would miss them by far more than their own
+    # last place
+    c = AttentionCase([5, 300, 1100], rows, 4, 1, dim, 16, BF16, seed=dim + rows)
+    o = c.oracle()
+    got = c.run(sv).out.double().cpu().numpy()
+    # an fp32 computation's bound, the weights' two roundings (2^-9 of 2^-9), and the result's one
+    fp32, _ = attention_bounds(o, dim, F32)
+    tol = fp32 + 2.0 ** -17 * o["mag"] + 2.0 ** -8 * np.abs(o["out"])
+    assert (np.abs(got - o["out"]) <= tol).all(), float((np.abs(got - o["out"]) / tol).max())
