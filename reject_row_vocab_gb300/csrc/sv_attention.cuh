@@ -9,9 +9,9 @@
 // has places [c T / g, (c + 1) T / g) of it.  The line goes through the cache
 // heads one by one, and through the requests within a head: so blocks side by
 // side in time read the heads of the same positions, which lie side by side in
-// memory (one token of 128 requests, 8 heads of 96: 275 us, with a request's
-// heads one after the other 352; of 128: 317 and 327; blocks of 16 rows of 64
-// requests: 101 and 104).  So every block gets the same work whatever the
+// memory (one token of 128 requests, 8 heads of 96: 275 us when both were
+// measured, with a request's heads one after the other 352; of 128: 317 and 327;
+// blocks of 16 rows of 64 requests: 101 and 104).  So every block gets the same work whatever the
 // requests' lengths are, a long history is split over many blocks and a short
 // one is not split at all.  A unit that lies in one block is finished there;
 // otherwise each block leaves its part (m, l, O), and the parts are joined in

@@ -14,9 +14,9 @@
 // (m, l, O), joined at the end of a unit.
 //
 // Measured: one token of 64 requests of up to 8192, 32 heads of 128 on 8 in the
-// cache: 340 us, 6.5 TB/s; 64 heads on 8: 367 us; blocks of 16 rows of 32
-// requests of up to 4000, 64 rows a request and cache head: 745 us, 24 TFLOP/s; ragged
-// blocks of 1 to 8 rows of 24 requests of up to 900, heads of 64: 23 us, latency.
+// cache: 339 us, 6.5 TB/s; 64 heads on 8: 366 us; blocks of 16 rows of 32 requests
+// of up to 4000, 64 rows a request and cache head: 742 us, 24 TFLOP/s; ragged
+// blocks of 1 to 8 rows of 24 requests of up to 900, heads of 64: 24 us, latency.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>

@@ -11,12 +11,13 @@
 //
 // The matrix unit takes operands of one type, so the weights go to the product
 // with V as two bf16 values, their rounding and the rounding of what it leaves
-// (16 bits together: the instructions are not what limits, 128 requests take 322
-// us with one value and 323 with two); their sum l is in fp32.
+// (16 bits together); their sum l is in fp32.  The second value costs little where
+// the bytes are what limits: heads of 128 321.9 us with one and 322.9 with two, of
+// 256 327 and 335, of 96 276 and 283, of 64 224 and 228.
 //
 // Measured: one token of 128 requests of up to 8192, 32 heads of 128 on 8 in the
-// cache: 317 us, 6.8 TB/s; 64 requests, heads of 256: 332 us, 6.6 TB/s; one of a
-// single request of 100000: 76 us, 5.4 TB/s; of 500: 12 us, latency.
+// cache: 318 to 323 us, 6.7 TB/s; 64 requests, heads of 256: 335 us, 6.6 TB/s; one
+// of a single request of 100000: 76 us, 5.4 TB/s; of 500: 12 us, latency.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>

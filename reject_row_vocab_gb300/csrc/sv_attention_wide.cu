@@ -25,9 +25,11 @@
 // Bound by the bytes of K and V where histories are long, by the chain from
 // scores to weights to sums at each unit's ends where they are short.
 // Measured: blocks of 16 rows of 64 requests of up to 4000, 32 heads of 128 on 8
-// in the cache: 101 us, 5.6 TB/s; 32 requests, heads of 256: 108 us; 5 rows of two requests of 60000 to 100000: 64
-// us, 5.0 TB/s (22 of them outside the stream); trees of 17 nodes of 16 requests
-// in pages of one slot: 22 us.
+// in the cache: 102 us, 5.6 TB/s; 32 requests, heads of 256: 107 us; 5 rows of
+// two requests of 60000 to 100000: 64 us, 5.0 TB/s (18 of them outside the
+// stream); trees of 17 nodes of 16 requests in pages of one slot: 22 us; a
+// causal block of 1024 rows of one request: 72 us without history, 148 (513
+// TFLOP/s) behind 4000, all key tiles gone through by every tile of rows.
 //
 // Units that several blocks share are joined by a second kernel, spread over
 // the whole GPU.  (By the last of the unit's blocks alone, two long requests
@@ -49,8 +51,8 @@ constexpr int kRows = 128;  // query rows of a tile
 constexpr int kSoftmaxThreads = 128;
 constexpr int kWideThreads = kSoftmaxThreads + kLoadThreads + 96;  // and a warp each to issue, to load Q, to plan
 constexpr int kReaders = 10;                                       // warps that read the plan
-// What a unit costs beside its key tiles, in tiles (1 to 5 measure alike: 101 us for the 64-request block, 21.5 to 23 for
-// the trees).
+// What a unit costs beside its key tiles, in tiles (1 to 5 measure alike: 101 to 102 us for the 64-request block, 21.5 to 23
+// for the trees).
 constexpr int kUnitPlaces = 2;
 constexpr float kSlack = 8.0f;  // log2 units a row's maximum may pass its reference by
 constexpr float kNear = 128.0f;  // and a reference may have with its factor rounded

@@ -13,7 +13,7 @@
 // chain of loads that leads to the places (64 requests, 32 layers: 31 us).
 //
 // Measured: 384 rows of 2 KB of K and of V in 32 layers, 64 requests: 25 us, 4.0
-// TB/s read and written (256 requests: 83 us, 4.7); 28 layers of one request: 6.
+// TB/s read and written (256 requests: 83 us, 4.8); 28 layers of one request: 6.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>

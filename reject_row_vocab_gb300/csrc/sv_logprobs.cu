@@ -7,10 +7,12 @@
 // One pass: each thread keeps a running (m, s, w) of the elements it has read
 // and rescales it when its maximum grows; a block joins its threads' triples,
 // and the last block of a row joins the blocks' in block order, so results do
-// not depend on the order the blocks finish in.  Bound by the instructions: an
-// exponential and about three and a half other issues an element.  Measured:
-// 1024 rows of 151936 bf16, 20 alternatives: 65 us, 4.8 TB/s; without
-// alternatives 57 us; 5 rows of 32000 fp32, 5 alternatives: 13 us, latency.
+// not depend on the order the blocks finish in.  An element costs an exponential
+// and about three and a half other issues, a batch of vectors is asked for only
+// when the one before is used up: issue slots and DRAM are each about half
+// used, and most waits are for memory.  Measured: 1024 rows of 151936 bf16, 20
+// alternatives: 65 us, 4.8 TB/s; without alternatives 57 us; 5 rows of 32000
+// fp32, 5 alternatives: 13 us, latency.
 //
 // Top alternatives from the same pass: a thread's running maximum is the
 // largest of its own elements, so the top_k-th largest of the block's thread
@@ -186,8 +188,8 @@ __device__ __forceinline__ void run_add(Run& r, float x, float k, uint32_t& flag
 // A thread's running sums while it streams, against a reference: weights are 2^(l k - c) with c = ref k as rounded, one
 // multiply-add an element; settle() makes up for the rounding, which is the same for all of them.  That needs a rounding
 // within the exponent's range: it is past it from |ref| k = 2^31 on, as in a row masked with -1e10 or at temperatures below
-// 1e-8.  A reference that is `far` is therefore subtracted before the product, an operation a pair of elements more (1024
-// rows of 151936 took 66.7 us that way throughout, and take 64.4).  The reference is the largest logit of the
+// 1e-8.  A reference that is `far` is therefore subtracted before the product, an operation a pair of elements more (all
+// rows done that way: 66.7 us for 1024 of 151936, where this took 64.4).  The reference is the largest logit of the
 // warp's first vectors, and moves only when a logit passes it by 64 log2 units (2^64 times a row's length is far from fp32's
 // end): moving it at every new maximum made up two thirds of the instructions.  Logits below `low` are read as `low`, which
 // has a weight of 0 just as well: their exponent stays finite, and 0 times it is 0.
