@@ -739,7 +739,9 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
 def kv_commit(cache: PagedKvCache, commit_cu, commit_src_slot, commit_dst_pos, *, max_len: int, dev_status=None,
               stream=None) -> torch.Tensor:
     """Moves the committed rows' K/V to their positions, in every layer, from a verification's commit lists
-    (VerifyOutputs.commit_cu / commit_src_slot / commit_dst_pos).  Returns the requests' status bits [batch]."""
+    (VerifyOutputs.commit_cu / commit_src_slot / commit_dst_pos).  Returns the requests' status bits [batch].
+
+    Every entry of the cache needs memory of its own: expanded axes, and k and v in the same memory, are refused."""
     lib = load_library()
     _require_cache(cache)
     dev, index = cache.device, cache.index
