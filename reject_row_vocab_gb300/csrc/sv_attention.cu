@@ -18,7 +18,7 @@ namespace sv {
 namespace {
 
 // bf16: units of 16 rows on matrix instructions of a warp where a request's rows of a cache head fit them, else units of
-// 128 on tensor memory.  (64 requests of 200 to 400, 8 cache heads of 128: 16 rows 38 us and 45, 32 rows 62 and 46; of up to
+// 128 on tensor memory.  (64 requests of 200 to 400, 8 cache heads of 128: 16 rows 39 us and 45, 32 rows 62 and 46; of up to
 // 4000: 16 rows 103 and 100, 32 rows 183 and 101.)  fp32: plain arithmetic.
 cudaError_t launch_attention(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream) {
   if (p.c.es == 4) return launch_attention_f32(p, dev, stream);

@@ -10,14 +10,16 @@
 // shares with others are joined at its end, by all its threads.
 //
 // The matrix unit takes operands of one type, so the weights go to the product
-// with V as two bf16 values, their rounding and the rounding of what it leaves
-// (16 bits together); their sum l is in fp32.  The second value costs little where
-// the bytes are what limits: heads of 128 321.9 us with one and 322.9 with two, of
-// 256 327 and 335, of 96 276 and 283, of 64 224 and 228.
+// with V as two bf16 values, their upper half and the rounding of what it leaves
+// (16 bits together); their sum l is in fp32.  Where the weight is above 0 both
+// are: an infinity of V times one of 0, or of the other sign, would be NaN.  The
+// second value costs little where the bytes are what limits: heads of 128 321.9
+// us with one and 323.5 with two, of 256 327 and 330, of 96 276 and 284, of 64
+// 224 and 231.
 //
 // Measured: one token of 128 requests of up to 8192, 32 heads of 128 on 8 in the
-// cache: 318 to 323 us, 6.7 TB/s; 64 requests, heads of 256: 335 us, 6.6 TB/s; one
-// of a single request of 100000: 76 us, 5.4 TB/s; of 500: 12 us, latency.
+// cache: 318 to 323 us, 6.7 TB/s; 64 requests, heads of 256: 330 us, 6.7 TB/s; one
+// of a single request of 100000: 77 us, 5.3 TB/s; of 500: 12 us, latency.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>
@@ -219,12 +221,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const uint32_t vt = ring.tile(group_v) + v_at;
 #pragma unroll
           for (int n = 0; n < NT; n += 2) {
-            const uint32_t a[4] = {pack_bf16(sc[n][0], sc[n][1]), pack_bf16(sc[n][2], sc[n][3]),
-                                   pack_bf16(sc[n + 1][0], sc[n + 1][1]), pack_bf16(sc[n + 1][2], sc[n + 1][3])};
-            uint32_t rest[4];  // what the rounding leaves
+            uint32_t a[4], rest[4];  // the weights' upper halves, and what is left
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              rest[i] = pack_bf16(sc[n + (i >> 1)][(i & 1) * 2] - bf16_lo(a[i]), sc[n + (i >> 1)][(i & 1) * 2 + 1] - bf16_hi(a[i]));
+            for (int i = 0; i < 4; ++i) {
+              const float x = sc[n + (i >> 1)][(i & 1) * 2], y = sc[n + (i >> 1)][(i & 1) * 2 + 1];
+              a[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+              // (a weight above 0 is 2^-126 at least)
+              rest[i] = pack_bf16(fmaxf(x - bf16_lo(a[i]), fminf(x, 0x1p-126f)), fmaxf(y - bf16_hi(a[i]), fminf(y, 0x1p-126f)));
+            }
 #pragma unroll
             for (int d = 0; d < DT; d += 2) {
               uint32_t vb[4];
