@@ -533,6 +533,156 @@ sv_status_t spec_verify_token_logprobs_backward(const void* logits, sv_dtype_t d
                                                 const float* g_logprob, const float* g_entropy, const float* g_top,
                                                 void* dlogits, int64_t ldd, cudaStream_t stream);
 
+/*
+ * A paged KV cache held in 4 bits: 16 neighbouring columns of a head share a
+ * scale, and a value is the scale times a code.  Codes are e2m1 (a sign bit,
+ * and 0, 0.5, 1, 1.5, 2, 3, 4 or 6); a scale is one byte, a positive half float's
+ * upper bits without the sign (five exponent bits, three of mantissa), at most
+ * 10240 (larger patterns are read as that).  Values are exact in bf16 and fp32.
+ *
+ * data is [layers, pages, heads, block]: the block of a page and head holds K's
+ * codes and V's codes ([page_size, head_dim / 2] bytes each, the even column in
+ * the lower half of a byte), K's scales and V's scales ([page_size, head_dim /
+ * 16] bytes each), and is padded to a multiple of 16 bytes:
+ * spec_verify_packed_kv_block_bytes(page_size, head_dim), 0 for sizes that
+ * have none.  head_dim is a multiple of 32, at most 256.  The strides are in
+ * bytes, multiples of 16, like the base pointer.  Slots, positions and the page
+ * table are those of sv_kv_cache_t.  dtype is that of the rows that go with the
+ * cache: new keys and values, queries, outputs.
+ */
+typedef struct {
+  void* data;
+  sv_dtype_t dtype;
+  int32_t layers;
+  int32_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int64_t layer_stride;
+  int64_t page_stride;
+  int64_t head_stride;
+  const int32_t* page_table; /* [batch, ld_table], device */
+  int32_t max_pages;
+  int64_t ld_table;
+} sv_packed_kv_cache_t;
+
+size_t spec_verify_packed_kv_block_bytes(int32_t page_size, int32_t head_dim);
+
+/*
+ * Rows of a batch and their places in a cache.  Request b owns rows [b *
+ * max_len, (b + 1) * max_len), or, with cu_seqlens [batch + 1], rows
+ * [cu_seqlens[b], cu_seqlens[b+1]) of total_rows, 0..max_len of them; rows of
+ * no request are left alone.  Its row j lies at slot row_slots[row], or, when
+ * row_slots is NULL, at position seq_lens[b] + j.
+ */
+typedef struct {
+  int32_t batch;
+  int32_t max_len;
+  int64_t total_rows;
+  const int32_t* cu_seqlens; /* [batch + 1] or NULL   */
+  const int64_t* seq_lens;   /* [batch] or NULL       */
+  const int64_t* row_slots;  /* [total_rows] or NULL  */
+} sv_rows_t;
+
+/*
+ * A rotation by position: pair i < pairs of a head's columns turns by the angle
+ * position * inv_freq[i].  A pair is columns (i, i + pairs), or (2 i, 2 i + 1)
+ * when interleaved; columns from 2 * pairs on are left as they are.  The
+ * rotated columns are also multiplied by magnitude (1 for none).  Angles are
+ * reduced in 64 bits: far positions lose nothing.
+ */
+typedef struct {
+  const float* inv_freq; /* [pairs], device */
+  int32_t pairs;
+  int32_t interleaved;
+  float magnitude;
+} sv_rotation_t;
+
+/*
+ * New rows of a layer go into the cache, their keys rotated on the way, and
+ * their queries are rotated beside them (what a model's layer does between its
+ * projections and spec_verify_paged_attention; [E2D] §2.4: position ids come
+ * from the depth in the draft tree, so they are given apart from the places).
+ *
+ *   (x, y) -> magnitude (x cos a - y sin a, y cos a + x sin a)   for each pair
+ *
+ * k and v: [rows, heads, head_dim] of the cache's dtype, q and q_out: [rows,
+ * num_heads, head_dim], each with its own row and head strides in elements (rows
+ * and strides multiples of 16 bytes).  positions [total_rows] (int64; NULL:
+ * seq_lens[b] + j) are what rows are rotated by; rotation NULL: nothing is
+ * rotated.  q NULL: only keys and values.  q_out may be q itself; any other
+ * overlap of q_out with q, k, v or the cache, and of these with the cache, is
+ * refused (SV_ERR_UNSUPPORTED), as are a cache whose entries share memory and
+ * rows or heads of q_out that lie over one another.  seq_lens may be NULL when
+ * row_slots and positions are given.
+ *
+ * Arithmetic is fp32, rounded once to the dtype; values are copied as they are.
+ * The 4-bit cache takes the rotated fp32 values: each group's scale is the one
+ * nearest to its largest magnitude / 6, each code the one nearest to its value,
+ * both half way to the even one.  Magnitudes above 61440 are stored as 61440, a
+ * NaN as 0.  Two rows of a call must not have the same place.
+ *
+ * dev_status [batch] is OR-ed into (zero it first): SV_DEV_BAD_LAYOUT for an
+ * invalid row range or a negative seq_lens[b] (nothing of the request is
+ * written), SV_DEV_SLOT_RANGE when a row's place lies outside the cache (it is
+ * not stored; its query is rotated all the same), SV_DEV_NONFINITE when a NaN
+ * or an infinity went into the 4-bit cache.
+ */
+sv_status_t spec_verify_kv_append(const sv_kv_cache_t* cache, int32_t layer, const sv_rows_t* rows,
+                                  const int64_t* positions, const sv_rotation_t* rotation, const void* k,
+                                  int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                                  int64_t v_head_stride, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                  int32_t num_heads, void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                                  uint32_t* dev_status, cudaStream_t stream);
+
+sv_status_t spec_verify_packed_kv_append(const sv_packed_kv_cache_t* cache, int32_t layer, const sv_rows_t* rows,
+                                         const int64_t* positions, const sv_rotation_t* rotation, const void* k,
+                                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                                         int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads, void* q_out,
+                                         int64_t out_row_stride, int64_t out_head_stride, uint32_t* dev_status,
+                                         cudaStream_t stream);
+
+/*
+ * The entries of given rows' places as they lie in the cache (of the 4-bit
+ * cache: the values that they stand for), in num_layers layers from `layer` on:
+ * what spec_verify_kv_append with the same rows has stored.  k and v:
+ * [num_layers, rows, heads, head_dim] of the cache's dtype, with the same
+ * strides in elements (head_dim dense; multiples of 16 bytes); rows, heads and
+ * layers must not lie over one another, nor k over v or either over the cache
+ * (SV_ERR_UNSUPPORTED).  A row whose place lies outside the cache is 0.
+ * dev_status [batch] is OR-ed into, with the bits of spec_verify_kv_append.
+ */
+sv_status_t spec_verify_kv_read(const sv_kv_cache_t* cache, int32_t layer, int32_t num_layers, const sv_rows_t* rows,
+                                void* k, void* v, int64_t layer_stride, int64_t row_stride, int64_t head_stride,
+                                uint32_t* dev_status, cudaStream_t stream);
+
+sv_status_t spec_verify_packed_kv_read(const sv_packed_kv_cache_t* cache, int32_t layer, int32_t num_layers,
+                                       const sv_rows_t* rows, void* k, void* v, int64_t layer_stride,
+                                       int64_t row_stride, int64_t head_stride, uint32_t* dev_status,
+                                       cudaStream_t stream);
+
+/*
+ * spec_verify_paged_attention over a 4-bit cache (q and out bf16), with the same arguments,
+ * results and workspace.  Scores are products with the values that the cache
+ * stands for; statistics and sums are fp32.
+ */
+sv_status_t spec_verify_packed_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                         int32_t num_heads, const sv_packed_kv_cache_t* cache, int32_t layer,
+                                         int32_t batch, int64_t total_rows, int32_t max_len,
+                                         const int32_t* cu_seqlens, const int64_t* seq_lens, const int64_t* row_slots,
+                                         const uint8_t* mask, float scale, void* out, int64_t out_row_stride,
+                                         int64_t out_head_stride, float* lse, uint32_t* dev_status, void* ws,
+                                         size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * spec_verify_kv_commit in a 4-bit cache: codes and scales are moved as they
+ * are.  SV_ERR_UNSUPPORTED when blocks share memory.
+ */
+sv_status_t spec_verify_packed_kv_commit(const sv_packed_kv_cache_t* cache, int32_t batch, int32_t max_len,
+                                         int64_t list_len, const int32_t* commit_cu, const int64_t* commit_src_slot,
+                                         const int64_t* commit_dst_pos, uint32_t* dev_status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -75,27 +75,12 @@ KvMaps kv_maps(const KvView& c) {
   return m;
 }
 
-}  // namespace sv
-
-using namespace sv;
-
-extern "C" {
-
-size_t spec_verify_attention_workspace_bytes(int32_t /*batch*/, int32_t /*max_len*/, int32_t /*num_heads*/,
-                                             int32_t /*kv_heads*/, int32_t head_dim) {
-  return align_up(kAttnCounterBytes + 2 * static_cast<size_t>(kAttnMaxBlocks) * part_bytes(head_dim), 256);
-}
-
-sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads,
-                                        const sv_kv_cache_t* cache, int32_t layer, int32_t batch, int64_t total_rows,
-                                        int32_t max_len, const int32_t* cu_seqlens, const int64_t* seq_lens,
-                                        const int64_t* row_slots, const uint8_t* mask, float scale, void* out,
-                                        int64_t out_row_stride, int64_t out_head_stride, float* lse,
-                                        uint32_t* dev_status, void* ws, size_t ws_bytes, cudaStream_t stream) {
-  if (batch < 0 || batch > 65535 || max_len < 1 || total_rows < 0 || total_rows > INT32_MAX) return SV_ERR_BAD_SHAPE;
-  KvView c{};
-  const sv_status_t s = check_cache(cache, &c);
-  if (s != SV_OK) return s;
+// The checks of a call that follow those of its cache, and what its kernels are given (nothing for a batch of 0).
+sv_status_t attention_params(const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads, const KvView& c,
+                             int32_t layer, int32_t batch, int64_t total_rows, int32_t max_len, const int32_t* cu_seqlens,
+                             const int64_t* seq_lens, const int64_t* row_slots, const uint8_t* mask, float scale, void* out,
+                             int64_t out_row_stride, int64_t out_head_stride, float* lse, uint32_t* dev_status, void* ws,
+                             size_t ws_bytes, AttnParams* p, DeviceInfo* dev) {
   if (layer < 0 || layer >= c.layers || num_heads < 1 || num_heads % c.heads != 0 || !std::isfinite(scale))
     return SV_ERR_BAD_SHAPE;
   if (static_cast<int64_t>(max_len) * num_heads > (1 << 24)) return SV_ERR_BAD_SHAPE;
@@ -120,19 +105,47 @@ sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int
   if (!ws || ws_bytes < spec_verify_attention_workspace_bytes(batch, max_len, num_heads, c.heads, c.head_dim) ||
       (reinterpret_cast<uintptr_t>(ws) & 255) != 0)
     return SV_ERR_WORKSPACE_TOO_SMALL;
-  DeviceInfo dev{};
-  cudaError_t e = device_info(&dev);
+  const cudaError_t e = device_info(dev);
   if (e != cudaSuccess) return cuda_failure(e);
-  c.k += layer * c.layer_stride * c.es;
-  c.v += layer * c.layer_stride * c.es;
   char* base = static_cast<char*>(ws);
-  const AttnParams p{static_cast<const char*>(q),
-                     q_row_stride, q_head_stride, static_cast<char*>(out), out_row_stride, out_head_stride, lse, c,
-                     cu_seqlens, seq_lens, row_slots, mask, dev_status, batch, max_len, num_heads,
-                     num_heads / c.heads, total_rows, scale * 1.44269504088896340736f,
-                     reinterpret_cast<uint32_t*>(base), reinterpret_cast<uint32_t*>(base) + kAttnMaxBlocks,
-                     reinterpret_cast<float*>(base + kAttnCounterBytes)};
-  e = launch_attention(p, dev, stream);
+  *p = AttnParams{static_cast<const char*>(q),
+                  q_row_stride, q_head_stride, static_cast<char*>(out), out_row_stride, out_head_stride, lse, c,
+                  cu_seqlens, seq_lens, row_slots, mask, dev_status, batch, max_len, num_heads,
+                  num_heads / c.heads, total_rows, scale * 1.44269504088896340736f,
+                  reinterpret_cast<uint32_t*>(base), reinterpret_cast<uint32_t*>(base) + kAttnMaxBlocks,
+                  reinterpret_cast<float*>(base + kAttnCounterBytes)};
+  return SV_OK;
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+size_t spec_verify_attention_workspace_bytes(int32_t /*batch*/, int32_t /*max_len*/, int32_t /*num_heads*/,
+                                             int32_t /*kv_heads*/, int32_t head_dim) {
+  return align_up(kAttnCounterBytes + 2 * static_cast<size_t>(kAttnMaxBlocks) * part_bytes(head_dim), 256);
+}
+
+sv_status_t spec_verify_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads,
+                                        const sv_kv_cache_t* cache, int32_t layer, int32_t batch, int64_t total_rows,
+                                        int32_t max_len, const int32_t* cu_seqlens, const int64_t* seq_lens,
+                                        const int64_t* row_slots, const uint8_t* mask, float scale, void* out,
+                                        int64_t out_row_stride, int64_t out_head_stride, float* lse,
+                                        uint32_t* dev_status, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!attention_sizes(batch, max_len, total_rows)) return SV_ERR_BAD_SHAPE;
+  KvView c{};
+  sv_status_t s = check_cache(cache, &c);
+  if (s != SV_OK) return s;
+  AttnParams p{};
+  DeviceInfo dev{};
+  s = attention_params(q, q_row_stride, q_head_stride, num_heads, c, layer, batch, total_rows, max_len, cu_seqlens, seq_lens,
+                       row_slots, mask, scale, out, out_row_stride, out_head_stride, lse, dev_status, ws, ws_bytes, &p, &dev);
+  if (s != SV_OK || batch == 0) return s;
+  p.c.k += layer * c.layer_stride * c.es;
+  p.c.v += layer * c.layer_stride * c.es;
+  const cudaError_t e = launch_attention(p, dev, stream);
   return e == cudaSuccess ? SV_OK : cuda_failure(e);
 }
 

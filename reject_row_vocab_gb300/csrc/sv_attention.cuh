@@ -501,6 +501,15 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnSpan& s
   }
 }
 
+inline bool attention_sizes(int32_t batch, int32_t max_len, int64_t total_rows) {
+  return batch >= 0 && batch <= 65535 && max_len >= 1 && total_rows >= 0 && total_rows <= INT32_MAX;
+}
+sv_status_t attention_params(const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads, const KvView& c,
+                             int32_t layer, int32_t batch, int64_t total_rows, int32_t max_len, const int32_t* cu_seqlens,
+                             const int64_t* seq_lens, const int64_t* row_slots, const uint8_t* mask, float scale, void* out,
+                             int64_t out_row_stride, int64_t out_head_stride, float* lse, uint32_t* dev_status, void* ws,
+                             size_t ws_bytes, AttnParams* p, DeviceInfo* dev);
+
 // bf16 with up to 16 rows a unit, bf16 with any number of rows on tensor memory, fp32.
 cudaError_t launch_attention_few(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t launch_attention_wide(const AttnParams& p, const DeviceInfo& dev, cudaStream_t stream);

@@ -84,6 +84,7 @@ __device__ __forceinline__ void mbar_arrive_times(uint32_t bar, uint32_t times) 
 template <int ES, int CB, int NB, int H, bool EARLY = false>
 struct KvRing {
   static constexpr int kEntries = NB;
+  static constexpr int kHalves = H;
   static constexpr int kBlock = kKeys * 128;        // 128 rows of 128 bytes
   static constexpr int kTile = kBlock * CB;         // an entry
   static constexpr int kPieces = CB * 8;            // 16-byte pieces of an entry's row
@@ -125,9 +126,10 @@ struct KvRing {
     return static_cast<uint32_t>((c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4));
   }
 
-  // By one thread: empties: arrivals that free a tile, readers: warps that read the plan, q_frees: arrivals that free a Q.
-  __device__ void init(int empties, int readers, int q_frees) const {
-    for (int i = 0; i < NB; ++i) mbar_init(full(i), 2 * kLoadThreads), mbar_init(empty(i), empties);
+  // By one thread: empties: arrivals that free a tile, readers: warps that read the plan, q_frees: arrivals that free a Q,
+  // fulls: arrivals that fill a tile.
+  __device__ void init(int empties, int readers, int q_frees, int fulls = 2 * kLoadThreads) const {
+    for (int i = 0; i < NB; ++i) mbar_init(full(i), fulls), mbar_init(empty(i), empties);
     for (int i = 0; i < 2 * NB; ++i) mbar_init(open(i), 1);
     for (int i = 0; i < kPlans; ++i) mbar_init(plan_bar(i), 1), mbar_init(read_bar(i), readers);
     for (int i = 0; i < kInfo * 8; ++i) valid(0)[i] = 0u;

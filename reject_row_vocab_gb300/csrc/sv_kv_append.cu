@@ -1,0 +1,425 @@
+// New rows go into the paged cache with their keys rotated on the way, and
+// their queries are rotated beside them ([E2D] §2.4: a draft tree's position
+// ids come from the depth, its places from where the rows are staged).
+//
+//   a = position * inv_freq[i]
+//   (x, y) -> magnitude (x cos a - y sin a, y cos a + x sin a)
+//
+// A warp takes one row (a part of its heads where there are few rows), a lane
+// eight columns of a head: a pair's other half is in the lane itself or one
+// shuffle away, and the row's sines and cosines are computed once, by the
+// warp, and kept in registers for all heads.  The angle is reduced to a part of
+// a turn in 64 bits, where the product of a position and a frequency is exact.
+//
+// The 4-bit cache: 16 columns are two lanes, one shuffle gives their largest
+// magnitude.
+//
+//   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
+#include <cmath>
+#include <type_traits>
+#include <cstdint>
+
+#include "sv_rows.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kAppendWarps = 4;
+constexpr int kMaxPairs = 128;
+constexpr int kUnroll = 4;
+
+enum Pairing { kNeighbours = 0, kHalves = 1, kHalvesOdd = 2 };  // halves: of a multiple of eight pairs, of any number
+
+struct HeadRows {
+  const char* p;
+  int64_t row, head;  // strides in elements
+};
+
+struct AppendParams {
+  RowsView r;
+  const int64_t* positions;
+  const float* inv_freq;
+  int32_t pairs;
+  float magnitude;
+  HeadRows q, k, v;
+  char* q_out;
+  int64_t o_row, o_head;
+  int32_t q_heads, kv_heads, dim;
+  uint32_t* status;
+  int32_t passes, chunks, per;  // a row's passes over its heads, dealt out to `chunks` warps
+};
+
+// Sine and cosine of position * f.
+__device__ __forceinline__ float2 turn_by(int64_t position, float f) {
+  double t = static_cast<double>(position) * (static_cast<double>(f) * 0.15915494309189533577);  // turns
+  t = 2.0 * (t - rint(t));  // half turns, -1 .. 1
+  const float hi = static_cast<float>(t), lo = static_cast<float>(t - hi) * 3.14159265f;
+  float s, c;
+  sincospif(hi, &s, &c);
+  return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
+}
+
+template <int ES>
+struct Eight {  // eight values of a row
+  uint32_t w[ES * 2];
+};
+
+template <int ES>
+__device__ __forceinline__ float value_of(const Eight<ES>& e, int i) {
+  if (ES == 4) return __uint_as_float(e.w[i]);
+  return i & 1 ? bf16_hi(e.w[i >> 1]) : bf16_lo(e.w[i >> 1]);
+}
+
+template <int ES>
+__device__ __forceinline__ void load8(Eight<ES>& e, const char* p, bool first, bool second) {
+  uint4 a = make_uint4(0u, 0u, 0u, 0u);
+  if (first) a = *reinterpret_cast<const uint4*>(p);
+  e.w[0] = a.x, e.w[1] = a.y, e.w[2] = a.z, e.w[3] = a.w;
+  if (ES == 4) {
+    a = make_uint4(0u, 0u, 0u, 0u);
+    if (second) a = *reinterpret_cast<const uint4*>(p + 16);
+    e.w[ES * 2 - 4] = a.x, e.w[ES * 2 - 3] = a.y, e.w[ES * 2 - 2] = a.z, e.w[ES * 2 - 1] = a.w;
+  }
+}
+
+template <int ES>
+__device__ __forceinline__ void store8(char* p, const Eight<ES>& e, bool second) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(e.w[0], e.w[1], e.w[2], e.w[3]);
+  if (ES == 4 && second)
+    *reinterpret_cast<uint4*>(p + 16) = make_uint4(e.w[ES * 2 - 4], e.w[ES * 2 - 3], e.w[ES * 2 - 2], e.w[ES * 2 - 1]);
+}
+
+template <int ES>
+__device__ __forceinline__ Eight<ES> round8(const float (&x)[8]) {
+  Eight<ES> e;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (ES == 4)
+      e.w[i] = __float_as_uint(x[i]);
+    else if (i % 2 == 0)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(e.w[i / 2]) : "f"(x[i + 1]), "f"(x[i]));
+  return e;
+}
+
+template <int ES, class C, Pairing PAIRING>
+__global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const AppendParams p, const C c) {
+  constexpr bool kPacked = std::is_same<C, PackedView>::value;
+  __shared__ float2 s_turn[kAppendWarps][kMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lanes = (p.dim + 7) / 8, heads = 32 / lanes;  // lanes of a head, heads of a pass
+  const int of = lane / lanes, d0 = (lane - of * lanes) * 8;
+  const int slots = p.q_heads + 2 * p.kv_heads;
+  const bool wide = ES == 2 || d0 + 4 < p.dim;  // the lane's second 16 bytes exist
+  const int n = p.pairs;
+  const bool turned = d0 < 2 * n;  // some of the lane's columns are rotated
+  grid_dependency_wait();
+  allow_dependents();
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  flag_requests(p.r, p.status, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, threads);
+  const int64_t items = rows_count(p.r) * p.chunks;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp; item < items; item += threads / 32) {
+    const int64_t row = p.chunks == 1 ? item : item / p.chunks;
+    const int chunk = static_cast<int>(item - row * p.chunks);
+    const int first = chunk * p.per, last = min(first + p.per, p.passes);
+    // The lane's columns of a pass: the address, and which head (a query's, then the keys', then the values').
+    auto from = [&](int pass, int* slot) -> const char* {
+      const int s = pass * heads + of;
+      *slot = of < heads && pass < last && s < slots ? s : -1;
+      if (*slot < 0) return nullptr;
+      const HeadRows& h = s < p.q_heads ? p.q : s < p.q_heads + p.kv_heads ? p.k : p.v;
+      const int head = s < p.q_heads ? s : s < p.q_heads + p.kv_heads ? s - p.q_heads : s - p.q_heads - p.kv_heads;
+      return h.p + (row * h.row + head * h.head + d0) * ES;
+    };
+    Eight<ES> raw[kUnroll];
+    int slot[kUnroll];
+    const char* at[kUnroll];
+    auto load = [&](int pass0) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        at[u] = from(pass0 + u, &slot[u]);
+        load8<ES>(raw[u], at[u], slot[u] >= 0, slot[u] >= 0 && wide);
+      }
+    };
+    load(first);  // (on its way while the row's place is looked up)
+    int j;
+    const int b = row_request(p.r, row, lane, &j);
+    if (b < 0) continue;
+    const int64_t len = p.r.seq_lens ? p.r.seq_lens[b] : 0;
+    if (len < 0) continue;
+    const Place place = p.r.row_slots ? slot_place(c, p.r.row_slots[row]) : position_place(c, b, len + j);
+    if (place.page < 0 && chunk == 0 && lane == 0) atomicOr(p.status + b, kStSlotRange);
+    float co[8], si[8];
+    if (n > 0 && first * heads < p.q_heads + p.kv_heads) {
+      const int64_t pos = p.positions ? p.positions[row] : len + j;
+      for (int i = lane; i < n; i += 32) s_turn[warp][i] = turn_by(pos, p.inv_freq[i]);
+      __syncwarp();
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = d0 + e;
+          const bool high = PAIRING == kNeighbours ? e & 1 : d >= n;  // the pair's second column
+          int i = PAIRING == kNeighbours ? d / 2 : high ? d - n : d;
+          if (i >= n) i = 0;  // (a column that is left as it is)
+          const float2 t = s_turn[warp][i];
+          co[e] = t.x * p.magnitude, si[e] = (high ? t.y : -t.y) * p.magnitude;
+        }
+      }
+      __syncwarp();
+    }
+    uint32_t odd = 0u;  // a value that is not finite went into the 4-bit cache
+    for (int pass0 = first; pass0 < last; pass0 += kUnroll) {
+      if (pass0 > first) load(pass0);
+      float x[kUnroll][8];
+      bool rotated[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        rotated[u] = turned && slot[u] >= 0 && slot[u] < p.q_heads + p.kv_heads;
+        float y[8];
+        if (PAIRING == kHalves) {
+          Eight<ES> other;
+          const int step = n / 8, at_lane = d0 < n ? lane + step : d0 < 2 * n ? lane - step : lane;
+#pragma unroll
+          for (int i = 0; i < ES * 2; ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[u].w[i], at_lane & 31);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = value_of<ES>(other, e);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[u][e] = value_of<ES>(raw[u], e);
+          if (PAIRING == kNeighbours) y[e] = value_of<ES>(raw[u], e ^ 1);
+        }
+        if (PAIRING == kHalvesOdd && rotated[u]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int d = d0 + e;
+            y[e] = 0.0f;
+            if (d < 2 * n) {
+              const char* o = at[u] + (d < n ? n + e : e - n) * ES;
+              y[e] = ES == 4 ? *reinterpret_cast<const float*>(o)
+                             : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(o)) << 16);
+            }
+          }
+        }
+        if (rotated[u]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (d0 + e < 2 * n) x[u][e] = fmaf(x[u][e], co[e], y[e] * si[e]);
+        }
+      }
+      if (PAIRING == kHalvesOdd) __syncwarp();  // (q_out may be q: other lanes' reads come first)
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int s = slot[u];
+        if (s >= 0 && s < p.q_heads) {
+          char* to = p.q_out + (row * p.o_row + s * p.o_head + d0) * ES;
+          store8<ES>(to, rotated[u] ? round8<ES>(x[u]) : raw[u], wide);
+        }
+        if ((pass0 + u) * heads + heads <= p.q_heads) continue;  // (a pass of queries alone)
+        const bool is_v = s >= p.q_heads + p.kv_heads;
+        const int head = is_v ? s - p.q_heads - p.kv_heads : s - p.q_heads;
+        if constexpr (!kPacked) {
+          if (s >= p.q_heads && place.page >= 0) {
+            char* to = (is_v ? c.v : c.k) +
+                       (place.page * c.page_stride + place.in * c.slot_stride + head * c.head_stride + d0) * ES;
+            store8<ES>(to, rotated[u] ? round8<ES>(x[u]) : raw[u], wide);
+          }
+        } else {
+          float top = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (s >= p.q_heads && !(fabsf(x[u][e]) < kInfF)) odd = kStNonFinite;
+            x[u][e] = x[u][e] == x[u][e] ? fminf(fmaxf(x[u][e], -61440.0f), 61440.0f) : 0.0f;
+            top = fmaxf(top, fabsf(x[u][e]));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // (a head's lanes are a multiple of four)
+          const uint32_t byte = scale_byte(top);
+          const float scale = scale_value(byte), inv = byte ? 1.0f / scale : 0.0f;
+          float quot[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) quot[e] = scaled(x[u][e], scale, inv);
+          const uint32_t codes = pack_codes(quot);
+          if (s >= p.q_heads && place.page >= 0) {
+            char* block = c.data + place.page * c.page_stride + head * c.head_stride;
+            const int v_codes = packed_v_codes(c.page_size, c.head_dim);
+            *reinterpret_cast<uint32_t*>(block + (is_v ? v_codes : 0) + place.in * (c.head_dim / 2) + d0 / 2) = codes;
+            if ((lane & 1) == 0)
+              block[(is_v ? packed_v_scales(c.page_size, c.head_dim) : packed_k_scales(c.page_size, c.head_dim)) +
+                    place.in * (c.head_dim / 16) + d0 / 16] = static_cast<char>(byte);
+          }
+        }
+      }
+    }
+    if (kPacked && place.page >= 0 && __any_sync(0xffffffffu, odd != 0u) && lane == 0) atomicOr(p.status + b, kStNonFinite);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host checks
+// ---------------------------------------------------------------------------
+
+// A [rows, heads, dim] array in bytes.
+struct Span {
+  const char* p;
+  int64_t row, rows, head, heads, bytes;  // steps and counts; bytes of a head's row
+  int64_t end() const { return (rows > 0 ? (rows - 1) * row : 0) + (heads - 1) * head + bytes; }
+};
+
+// Whether two arrays have no byte in common, as far as that shows: ranges that do not meet, or parts of the rows (or of the
+// heads) of one larger array.
+bool apart(const Span& a, const Span& b) {
+  if (a.p + a.end() <= b.p || b.p + b.end() <= a.p) return true;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t step = i ? a.head : a.row, other = i ? b.head : b.row;
+    const int64_t in_a = i ? (a.rows - 1) * a.row + a.bytes : (a.heads - 1) * a.head + a.bytes;
+    const int64_t in_b = i ? (b.rows - 1) * b.row + b.bytes : (b.heads - 1) * b.head + b.bytes;
+    if (step <= 0 || step != other) continue;
+    int64_t d = (b.p - a.p) % step;
+    if (d < 0) d += step;
+    if (in_a <= d && d + in_b <= step) return true;
+  }
+  return false;
+}
+
+bool meets_range(const Span& a, const char* lo, int64_t bytes) { return a.p < lo + bytes && lo < a.p + a.end(); }
+
+sv_status_t check_array(const void* p, int64_t row, int64_t head, int es) {
+  if (row < 0 || head < 0) return SV_ERR_BAD_SHAPE;
+  if (!p) return SV_ERR_NULL_ARG;
+  return aligned16(p) && (row * es) % 16 == 0 && (head * es) % 16 == 0 ? SV_OK : SV_ERR_MISALIGNED;
+}
+
+// The caches' memory as ranges, and whether their entries lie apart.
+struct Memory {
+  const char* at[2];
+  int64_t bytes[2];
+};
+bool memory_of(const KvView& c, Memory* m) {
+  StepAxis axes[4] = {{c.head_stride * c.es, c.heads}, {c.slot_stride * c.es, c.page_size},
+                      {c.page_stride * c.es, c.pages}, {c.layer_stride * c.es, c.layers}};
+  int64_t span = 0;
+  if (!entries_apart(c) || !steps_nested(axes, 4, static_cast<int64_t>(c.head_dim) * c.es, &span)) return false;
+  *m = Memory{{c.k, c.v}, {span, span}};
+  return true;
+}
+bool memory_of(const PackedView& c, Memory* m) {
+  StepAxis axes[3] = {{c.head_stride, c.heads}, {c.page_stride, c.pages}, {c.layer_stride, c.layers}};
+  int64_t span = 0;
+  if (!steps_nested(axes, 3, packed_block_bytes(c.page_size, c.head_dim), &span)) return false;
+  *m = Memory{{c.data, c.data}, {span, span}};
+  return true;
+}
+
+void to_layer(KvView* c, int layer) {
+  c->k += layer * c->layer_stride * c->es;
+  c->v += layer * c->layer_stride * c->es;
+}
+void to_layer(PackedView* c, int layer) { c->data += layer * c->layer_stride; }
+
+template <int ES, class C>
+cudaError_t launch_append(const AppendParams& p, const C& c, Pairing pairing, unsigned grid, cudaStream_t stream) {
+  auto kernel = pairing == kNeighbours ? k_kv_append<ES, C, kNeighbours>
+                : pairing == kHalves   ? k_kv_append<ES, C, kHalves>
+                                       : k_kv_append<ES, C, kHalvesOdd>;
+  return launch_pdl(kernel, dim3(grid), dim3(32 * kAppendWarps), 0, stream, p, c);
+}
+
+template <class C>
+sv_status_t append_entry(C c, int es, int32_t layer, const sv_rows_t* rows, const int64_t* positions,
+                         const sv_rotation_t* rotation, const HeadRows& k, const HeadRows& v, const HeadRows& q,
+                         int32_t num_heads, void* q_out, int64_t o_row, int64_t o_head, uint32_t* dev_status,
+                         cudaStream_t stream) {
+  RowsView r{};
+  sv_status_t s = check_rows(rows, &r);
+  if (s != SV_OK) return s;
+  if (layer < 0 || layer >= c.layers) return SV_ERR_BAD_SHAPE;
+  if (q.p && (num_heads < 1 || num_heads > (1 << 20))) return SV_ERR_BAD_SHAPE;
+  if (!q.p) num_heads = 0;
+  if (rotation && (rotation->pairs < 0 || 2 * static_cast<int64_t>(rotation->pairs) > c.head_dim ||
+                   !std::isfinite(rotation->magnitude)))
+    return SV_ERR_BAD_SHAPE;
+  if (r.batch == 0 || rows_count(r) == 0) return SV_OK;
+  if (!dev_status || (rotation && rotation->pairs > 0 && !rotation->inv_freq)) return SV_ERR_NULL_ARG;
+  if (!r.seq_lens && (!r.row_slots || (rotation && !positions))) return SV_ERR_NULL_ARG;
+  if ((s = check_array(k.p, k.row, k.head, es)) != SV_OK || (s = check_array(v.p, v.row, v.head, es)) != SV_OK) return s;
+  if (q.p && ((s = check_array(q.p, q.row, q.head, es)) != SV_OK || (s = check_array(q_out, o_row, o_head, es)) != SV_OK)) return s;
+  const int64_t bytes = static_cast<int64_t>(c.head_dim) * es;
+  const Span sk{k.p, k.row * es, r.total, k.head * es, c.heads, bytes}, sv{v.p, v.row * es, r.total, v.head * es, c.heads, bytes};
+  Memory m{};
+  if (!memory_of(c, &m)) return SV_ERR_UNSUPPORTED;
+  for (int i = 0; i < 2; ++i)
+    if (meets_range(sk, m.at[i], m.bytes[i]) || meets_range(sv, m.at[i], m.bytes[i])) return SV_ERR_UNSUPPORTED;
+  if (q.p) {
+    const Span sq{q.p, q.row * es, r.total, q.head * es, num_heads, bytes};
+    const Span so{static_cast<const char*>(q_out), o_row * es, r.total, o_head * es, num_heads, bytes};
+    StepAxis axes[2] = {{so.row, so.rows}, {so.head, so.heads}};
+    int64_t span;
+    if (!steps_nested(axes, 2, bytes, &span)) return SV_ERR_UNSUPPORTED;
+    const bool same = sq.p == so.p && (r.total < 2 || sq.row == so.row) && (num_heads < 2 || sq.head == so.head);
+    if ((!same && !apart(so, sq)) || !apart(so, sk) || !apart(so, sv)) return SV_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i)
+      if (meets_range(so, m.at[i], m.bytes[i]) || meets_range(sq, m.at[i], m.bytes[i])) return SV_ERR_UNSUPPORTED;
+  }
+  DeviceInfo dev{};
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_failure(e);
+  to_layer(&c, layer);
+  const int lanes = (c.head_dim + 7) / 8, heads = 32 / lanes;
+  const int64_t passes = (num_heads + 2 * static_cast<int64_t>(c.heads) + heads - 1) / heads;
+  // As many warps a row as it takes to give every multiprocessor sixteen.
+  const int64_t count = rows_count(r), want = 16 * static_cast<int64_t>(dev.sms);
+  int64_t chunks = (want + count - 1) / count;
+  chunks = chunks > passes ? passes : chunks;
+  const int64_t per = (passes + chunks - 1) / chunks;
+  chunks = (passes + per - 1) / per;
+  const int n = rotation ? rotation->pairs : 0;
+  const AppendParams p{r, positions, rotation ? rotation->inv_freq : nullptr, n, rotation ? rotation->magnitude : 1.0f, q, k, v,
+                       static_cast<char*>(q_out), o_row, o_head, num_heads, c.heads, c.head_dim, dev_status,
+                       static_cast<int32_t>(passes), static_cast<int32_t>(chunks), static_cast<int32_t>(per)};
+  const int64_t blocks = (count * chunks + kAppendWarps - 1) / kAppendWarps, most = 64 * static_cast<int64_t>(dev.sms);
+  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  const Pairing pairing = n == 0 || rotation->interleaved ? kNeighbours : n % 8 == 0 ? kHalves : kHalvesOdd;
+  e = es == 2 ? launch_append<2>(p, c, pairing, grid, stream) : launch_append<4>(p, c, pairing, grid, stream);
+  return e == cudaSuccess ? SV_OK : cuda_failure(e);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+sv_status_t spec_verify_kv_append(const sv_kv_cache_t* cache, int32_t layer, const sv_rows_t* rows,
+                                  const int64_t* positions, const sv_rotation_t* rotation, const void* k,
+                                  int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                                  int64_t v_head_stride, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                  int32_t num_heads, void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                                  uint32_t* dev_status, cudaStream_t stream) {
+  KvView c{};
+  const sv_status_t s = check_cache(cache, &c);
+  if (s != SV_OK) return s;
+  return append_entry(c, c.es, layer, rows, positions, rotation,
+                      HeadRows{static_cast<const char*>(k), k_row_stride, k_head_stride},
+                      HeadRows{static_cast<const char*>(v), v_row_stride, v_head_stride},
+                      HeadRows{static_cast<const char*>(q), q_row_stride, q_head_stride}, num_heads, q_out,
+                      out_row_stride, out_head_stride, dev_status, stream);
+}
+
+sv_status_t spec_verify_packed_kv_append(const sv_packed_kv_cache_t* cache, int32_t layer, const sv_rows_t* rows,
+                                         const int64_t* positions, const sv_rotation_t* rotation, const void* k,
+                                         int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                                         int64_t v_row_stride, int64_t v_head_stride, const void* q,
+                                         int64_t q_row_stride, int64_t q_head_stride, int32_t num_heads, void* q_out,
+                                         int64_t out_row_stride, int64_t out_head_stride, uint32_t* dev_status,
+                                         cudaStream_t stream) {
+  PackedView c{};
+  const sv_status_t s = check_packed_cache(cache, &c);
+  if (s != SV_OK) return s;
+  return append_entry(c, c.dtype == SV_BF16 ? 2 : 4, layer, rows, positions, rotation,
+                      HeadRows{static_cast<const char*>(k), k_row_stride, k_head_stride},
+                      HeadRows{static_cast<const char*>(v), v_row_stride, v_head_stride},
+                      HeadRows{static_cast<const char*>(q), q_row_stride, q_head_stride}, num_heads, q_out,
+                      out_row_stride, out_head_stride, dev_status, stream);
+}
+
+}  // extern "C"

@@ -33,7 +33,9 @@ ENTRY_POINTS = ("spec_verify_workspace_bytes", "spec_verify_status_string", "spe
                 "spec_verify_sparse_workspace_bytes", "spec_verify_rejection_chain_sparse", "spec_verify_build_tree",
                 "spec_verify_sample_match_chain", "spec_verify_attention_workspace_bytes",
                 "spec_verify_paged_attention", "spec_verify_kv_commit", "spec_verify_logprobs_workspace_bytes",
-                "spec_verify_token_logprobs", "spec_verify_token_logprobs_backward")
+                "spec_verify_token_logprobs", "spec_verify_token_logprobs_backward", "spec_verify_kv_append",
+                "spec_verify_kv_read", "spec_verify_packed_kv_block_bytes", "spec_verify_packed_kv_append",
+                "spec_verify_packed_kv_read", "spec_verify_packed_attention", "spec_verify_packed_kv_commit")
 
 
 class SpecVerifyError(RuntimeError):
@@ -54,6 +56,24 @@ class SvKvCache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
                 ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
                 ("max_pages", ctypes.c_int32), ("ld_table", ctypes.c_int64)]
+
+
+class SvPackedKvCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("layers", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int32),
+                ("ld_table", ctypes.c_int64)]
+
+
+class SvRows(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_len", ctypes.c_int32), ("total_rows", ctypes.c_int64),
+                ("cu_seqlens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("row_slots", ctypes.c_void_p)]
+
+
+class SvRotation(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
 
 
 _lib = None
@@ -102,7 +122,14 @@ def load_library():
                                         P, P, SZ, P], ctypes.c_int),
         "spec_verify_token_logprobs_backward": ([P, ctypes.c_int, I64, I64, I32, P, I32, I64, P, P, P, P, P, I32, P, P,
                                                  P, P, I64, P], ctypes.c_int),
+        "spec_verify_kv_append": ([P, I32, P, P, P, P, I64, I64, P, I64, I64, P, I64, I64, I32, P, I64, I64, P, P],
+                                  ctypes.c_int),
+        "spec_verify_kv_read": ([P, I32, I32, P, P, P, I64, I64, I64, P, P], ctypes.c_int),
+        "spec_verify_packed_kv_block_bytes": ([I32, I32], SZ),
     }
+    for name in ("kv_append", "kv_read", "kv_commit"):
+        sig["spec_verify_packed_" + name] = sig["spec_verify_" + name]
+    sig["spec_verify_packed_attention"] = sig["spec_verify_paged_attention"]
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -557,6 +584,25 @@ def _on(stream):
     return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
+class _OtherDevice:
+    """The call's device, where it is not the current one."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        torch.cuda.set_device(self.was)
+        return False
+
+
+def _on_device(index):
+    return _CURRENT if index < 0 or torch.cuda.current_device() == index else _OtherDevice(index)
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -619,7 +665,7 @@ class PagedKvCache:
         _rows_arg(page_table, "page_table", torch.int32, batch, pages, k.device)
         self.k, self.v, self.page_table = k, v, page_table
         self.device, self.dtype, self.batch, self.index = k.device, k.dtype, batch, k.get_device()
-        self.heads, self.head_dim = k.shape[3], k.shape[4]
+        self.layers, self.heads, self.head_dim = k.shape[0], k.shape[3], k.shape[4]
         st = [x if n > 1 else 0 for x, n in zip(k.stride(), k.shape)]  # an axis of one entry has no step
         self.struct = SvKvCache(k.data_ptr(), v.data_ptr(), SV_BF16 if k.dtype == torch.bfloat16 else SV_F32,
                                 k.shape[0], k.shape[1], k.shape[2], k.shape[3], k.shape[4], st[0], st[1], st[2], st[3],
@@ -627,10 +673,60 @@ class PagedKvCache:
         self.ref = ctypes.byref(self.struct)
 
 
-def _require_cache(cache: PagedKvCache):
-    if not isinstance(cache, PagedKvCache):
-        raise TypeError("cache must be a PagedKvCache")
-    if not cache.k.is_cuda:
+class PackedKvCache:
+    """A paged KV cache held in 4 bits: data [layers, pages, heads, block bytes] uint8 (the last axis dense, other strides
+    multiples of 16) and page_table [batch, max_pages] int32 (dense rows).
+
+    A block holds a page's entries of one head: block_bytes(page_size, head_dim) bytes of it are used.  head_dim is a multiple
+    of 32.  dtype (bf16 or fp32) is that of the rows that go with the cache: keys and values that kv_append takes and kv_read
+    gives back; paged_attention takes bf16.  Stands wherever a PagedKvCache does; make it once and use it for every call."""
+
+    def __init__(self, data: torch.Tensor, page_table: torch.Tensor, *, page_size: int, head_dim: int,
+                 dtype: torch.dtype = torch.bfloat16):
+        if not isinstance(data, torch.Tensor) or data.dim() != 4:
+            raise ValueError("data must be a 4-D torch tensor [layers, pages, heads, block bytes]")
+        if data.dtype != torch.uint8:
+            raise TypeError("data must be torch.uint8, got %s" % data.dtype)
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("dtype must be bfloat16 or float32, got %s" % dtype)
+        need = PackedKvCache.block_bytes(page_size, head_dim)
+        if data.shape[3] < need or data.stride(3) != 1:
+            raise ValueError("data's blocks must be dense and hold %d bytes (got %d)" % (need, data.shape[3]))
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be a 2-D torch tensor")
+        batch, pages = page_table.shape
+        _rows_arg(page_table, "page_table", torch.int32, batch, pages, data.device)
+        self.data, self.page_table = data, page_table
+        self.device, self.dtype, self.batch, self.index = data.device, dtype, batch, data.get_device()
+        self.layers, self.heads, self.head_dim, self.page_size = data.shape[0], data.shape[2], head_dim, page_size
+        st = [x if n > 1 else 0 for x, n in zip(data.stride(), data.shape)]  # an axis of one entry has no step
+        self.struct = SvPackedKvCache(data.data_ptr(), SV_BF16 if dtype == torch.bfloat16 else SV_F32, data.shape[0],
+                                      data.shape[1], page_size, data.shape[2], head_dim, st[0], st[1], st[2],
+                                      page_table.data_ptr(), pages, page_table.stride(0) if batch > 1 else max(pages, 1))
+        self.ref = ctypes.byref(self.struct)
+
+    @staticmethod
+    def block_bytes(page_size: int, head_dim: int) -> int:
+        """Bytes of a page's entries of one head, K and V."""
+        n = int(load_library().spec_verify_packed_kv_block_bytes(page_size, head_dim))
+        if n == 0:
+            raise ValueError("no 4-bit cache of page_size %d and head_dim %d (a multiple of 32, at most 256)"
+                             % (page_size, head_dim))
+        return n
+
+    @staticmethod
+    def allocate(layers: int, pages: int, heads: int, page_size: int, head_dim: int, page_table: torch.Tensor,
+                 dtype: torch.dtype = torch.bfloat16) -> "PackedKvCache":
+        """A cache of zeros on page_table's device."""
+        data = torch.zeros(layers, pages, heads, PackedKvCache.block_bytes(page_size, head_dim), dtype=torch.uint8,
+                           device=page_table.device)
+        return PackedKvCache(data, page_table, page_size=page_size, head_dim=head_dim, dtype=dtype)
+
+
+def _require_cache(cache):
+    if not isinstance(cache, (PagedKvCache, PackedKvCache)):
+        raise TypeError("cache must be a PagedKvCache or a PackedKvCache")
+    if cache.device.type != "cuda":
         raise ValueError("the cache must be on a CUDA device (got %s): the library has no CPU path" % cache.device)
 
 
@@ -649,7 +745,7 @@ class AttentionOutputs:
                                 dev_status=torch.empty(batch, dtype=torch.int32, device=d))
 
 
-def attention_workspace(batch: int, max_len: int, cache: PagedKvCache, num_heads: int) -> torch.Tensor:
+def attention_workspace(batch: int, max_len: int, cache, num_heads: int) -> torch.Tensor:
     """A zero-filled workspace of paged_attention calls (the library keeps its counters zero between calls)."""
     n = int(load_library().spec_verify_attention_workspace_bytes(batch, max_len, num_heads, cache.heads,
                                                                  cache.head_dim))
@@ -675,7 +771,7 @@ def _head_rows(t, name, rows, heads, dim, dtype, device, index):
         raise ValueError("%s: head_dim must be dense" % name)
 
 
-def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len: Optional[int] = None,
+def paged_attention(q, cache, seq_lens, *, layer: int = 0, max_len: Optional[int] = None,
                     cu_seqlens=None, row_slots=None, mask=None, scale: Optional[float] = None, out=None, ws=None,
                     stream=None) -> AttentionOutputs:
     """Attention of each request's new rows q [rows, heads, head_dim] over its committed positions in the cache and
@@ -685,7 +781,7 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
     whole number, when not given; 1 is plain decoding), or cu_seqlens [batch + 1] int32 gives ragged ones of 1..max_len.
     row_slots [rows] int64: where the new rows' K/V lie (None: at positions seq_lens + j).  mask [batch, max_len,
     max_len] uint8: which new rows a row sees (None: itself and earlier ones), as build_tree returns it.
-    scale defaults to 1 / sqrt(head_dim)."""
+    cache: a PagedKvCache, or a PackedKvCache with bf16 rows.  scale defaults to 1 / sqrt(head_dim)."""
     lib = load_library()
     _require_cache(cache)
     dev, index = cache.device, cache.index
@@ -726,17 +822,19 @@ def paged_attention(q, cache: PagedKvCache, seq_lens, *, layer: int = 0, max_len
     if status is not None:
         _need(status, "out.dev_status", torch.int32, batch, dev, index)
     _need(ws, "ws", torch.uint8, 0, dev, index)
-    code = lib.spec_verify_paged_attention(
-        q.data_ptr(), q_steps[0], q_steps[1], heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
-        seq_lens.data_ptr(), _addr(row_slots), _addr(mask), dim ** -0.5 if scale is None else scale,
-        o.data_ptr(), o_steps[0], o_steps[1], _addr(lse), _addr(status), ws.data_ptr(), ws.numel(),
-        _call_stream(stream, dev))
+    fn = lib.spec_verify_packed_attention if isinstance(cache, PackedKvCache) else lib.spec_verify_paged_attention
+    with _on_device(index):
+        code = fn(
+            q.data_ptr(), q_steps[0], q_steps[1], heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
+            seq_lens.data_ptr(), _addr(row_slots), _addr(mask), dim ** -0.5 if scale is None else scale,
+            o.data_ptr(), o_steps[0], o_steps[1], _addr(lse), _addr(status), ws.data_ptr(), ws.numel(),
+            _call_stream(stream, dev))
     if code:
-        _check("spec_verify_paged_attention", code)
+        _check("spec_verify_packed_attention" if isinstance(cache, PackedKvCache) else "spec_verify_paged_attention", code)
     return out
 
 
-def kv_commit(cache: PagedKvCache, commit_cu, commit_src_slot, commit_dst_pos, *, max_len: int, dev_status=None,
+def kv_commit(cache, commit_cu, commit_src_slot, commit_dst_pos, *, max_len: int, dev_status=None,
               stream=None) -> torch.Tensor:
     """Moves the committed rows' K/V to their positions, in every layer, from a verification's commit lists
     (VerifyOutputs.commit_cu / commit_src_slot / commit_dst_pos).  Returns the requests' status bits [batch].
@@ -757,12 +855,200 @@ def kv_commit(cache: PagedKvCache, commit_cu, commit_src_slot, commit_dst_pos, *
         with _on(stream):
             dev_status = torch.empty(batch, dtype=torch.int32, device=dev)
     _need(dev_status, "dev_status", torch.int32, batch, dev, index)
-    code = lib.spec_verify_kv_commit(
-        cache.ref, batch, max_len, min(commit_src_slot.numel(), commit_dst_pos.numel()), commit_cu.data_ptr(),
-        commit_src_slot.data_ptr(), commit_dst_pos.data_ptr(), dev_status.data_ptr(), _call_stream(stream, dev))
+    fn = lib.spec_verify_packed_kv_commit if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_commit
+    with _on_device(index):
+        code = fn(
+            cache.ref, batch, max_len, min(commit_src_slot.numel(), commit_dst_pos.numel()), commit_cu.data_ptr(),
+            commit_src_slot.data_ptr(), commit_dst_pos.data_ptr(), dev_status.data_ptr(), _call_stream(stream, dev))
     if code:
-        _check("spec_verify_kv_commit", code)
+        _check("spec_verify_packed_kv_commit" if isinstance(cache, PackedKvCache) else "spec_verify_kv_commit", code)
     return dev_status
+
+
+class Rotation:
+    """A rotation by position: pair i of a head's columns turns by position * inv_freq[i] (fp32, on the cache's device).
+
+    A pair is columns (i, i + pairs), or (2 i, 2 i + 1) when interleaved; the rotated columns are multiplied by magnitude, and
+    columns from 2 * pairs on are left as they are.  Make it once and use it for every call."""
+
+    def __init__(self, inv_freq: torch.Tensor, *, interleaved: bool = False, magnitude: float = 1.0):
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a 1-D torch tensor")
+        _arg(inv_freq, "inv_freq", torch.float32, 0, inv_freq.device)
+        self.inv_freq, self.pairs, self.interleaved, self.magnitude = inv_freq, inv_freq.numel(), interleaved, magnitude
+        self.struct = SvRotation(inv_freq.data_ptr(), self.pairs, 1 if interleaved else 0, magnitude)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots):
+    """The rows of a call on a cache: checks their arrays; returns the batch and the library's description.  rows None: as many
+    as the requests have."""
+    dev, index = cache.device, cache.index
+    if seq_lens is not None:
+        _need(seq_lens, "seq_lens", torch.int64, 0, dev, index)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, 1, dev, index)
+        batch = cu_seqlens.numel() - 1
+        if max_len is None:
+            raise ValueError("max_len is required with cu_seqlens")
+        if rows is None:
+            raise ValueError("rows is required with cu_seqlens")
+        if seq_lens is not None:
+            _need(seq_lens, "seq_lens", torch.int64, batch, dev, index)
+    elif seq_lens is not None:
+        batch = seq_lens.numel()
+        if max_len is None:
+            if rows is None:
+                raise ValueError("max_len is required")
+            if batch and (rows % batch or not rows):
+                raise ValueError("%d rows do not divide among %d requests: max_len is required" % (rows, batch))
+            max_len = rows // batch if batch else 1
+    else:
+        if rows is None:
+            raise ValueError("seq_lens or cu_seqlens is required")
+        max_len = 1 if max_len is None else max_len
+        if max_len < 1 or rows % max_len:
+            raise ValueError("%d rows are no whole number of requests of %d" % (rows, max_len))
+        batch = rows // max_len
+    if rows is None:
+        rows = batch * max_len
+    if cu_seqlens is None and rows < batch * max_len:
+        raise ValueError("there are %d rows; the call reads %d" % (rows, batch * max_len))
+    if row_slots is not None:
+        _need(row_slots, "row_slots", torch.int64, rows, dev, index)
+    else:
+        if seq_lens is None:
+            raise ValueError("seq_lens is required without row_slots")
+        if cache.batch < batch:
+            raise ValueError("page_table has %d rows; the call reads %d" % (cache.batch, batch))
+    return batch, rows, SvRows(batch, max_len, rows, _addr(cu_seqlens), _addr(seq_lens), _addr(row_slots))
+
+
+@dataclass
+class KvAppendOutputs:
+    q: Optional[torch.Tensor]   # [rows, heads, head_dim], the rotated queries
+    dev_status: torch.Tensor    # [batch] int32 storage of uint32 bits, OR-ed into
+
+    @staticmethod
+    def allocate(rows: int, heads: int, head_dim: int, batch: int, dtype=torch.bfloat16, device=None) -> "KvAppendOutputs":
+        d = device or "cuda"
+        return KvAppendOutputs(q=torch.empty(rows, heads, head_dim, dtype=dtype, device=d) if heads else None,
+                               dev_status=torch.zeros(batch, dtype=torch.int32, device=d))
+
+
+def kv_append(cache, k, v, *, layer: int = 0, seq_lens=None, max_len: Optional[int] = None, cu_seqlens=None, row_slots=None,
+              positions=None, rotation: Optional[Rotation] = None, q=None, out=None, stream=None) -> KvAppendOutputs:
+    """Puts new rows k, v [rows, heads, head_dim] of a layer into the cache, the keys rotated by position, and rotates their
+    queries q [rows, query heads, head_dim].
+
+    A request has max_len rows (rows / batch when not given), or cu_seqlens [batch + 1] int32 gives ragged ones of 0..max_len;
+    rows behind the last request are left alone.  Row j of request b goes to position seq_lens[b] + j, or to slot row_slots
+    [rows] int64; it is rotated by positions [rows] int64, or by seq_lens[b] + j.  Two rows must not have the same place.
+    out: KvAppendOutputs; its q may be q itself.  dev_status is OR-ed into: it collects what many calls report until it is
+    zeroed.  cache: a PagedKvCache or a PackedKvCache (which takes the rotated fp32 values, rounded once to 4 bits)."""
+    lib = load_library()
+    _require_cache(cache)
+    dev, index = cache.device, cache.index
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a 3-D torch tensor [rows, heads, head_dim]")
+    rows, dim = k.shape[0], cache.head_dim
+    ks = _head_rows(k, "k", rows, cache.heads, dim, cache.dtype, dev, index)
+    vs = _head_rows(v, "v", rows, cache.heads, dim, cache.dtype, dev, index)
+    batch, _, desc = _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots)
+    if positions is not None:
+        _need(positions, "positions", torch.int64, rows, dev, index)
+    elif rotation is not None and seq_lens is None:
+        raise ValueError("positions are required without seq_lens")
+    heads, qs, os = 0, (0, 0), (0, 0)
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a 3-D torch tensor [rows, heads, head_dim]")
+        heads = q.shape[1]
+        qs = _head_rows(q, "q", rows, heads, dim, cache.dtype, dev, index)
+    if rotation is not None:
+        if not isinstance(rotation, Rotation):
+            raise TypeError("rotation must be a Rotation")
+        if rotation.inv_freq.get_device() != index:
+            raise ValueError("rotation is on %s; the call runs on %s (the cache's device)" % (rotation.inv_freq.device, dev))
+    if out is None:
+        with _on(stream):
+            out = KvAppendOutputs.allocate(rows, heads, dim, batch, cache.dtype, dev)
+    if q is not None:
+        if out.q is None:
+            raise ValueError("out.q is required with q")
+        os = _head_rows(out.q, "out.q", rows, heads, dim, cache.dtype, dev, index)
+    _need(out.dev_status, "out.dev_status", torch.int32, batch, dev, index)
+    fn = lib.spec_verify_packed_kv_append if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_append
+    with _on_device(index):
+        code = fn(cache.ref, layer, ctypes.byref(desc), _addr(positions), None if rotation is None else rotation.ref,
+                  k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1], heads,
+                  None if q is None else out.q.data_ptr(), os[0], os[1], out.dev_status.data_ptr(), _call_stream(stream, dev))
+    if code:
+        _check("spec_verify_packed_kv_append" if isinstance(cache, PackedKvCache) else "spec_verify_kv_append", code)
+    return out
+
+
+@dataclass
+class KvReadOutputs:
+    k: torch.Tensor             # [rows, heads, head_dim], or [layers, rows, heads, head_dim]
+    v: torch.Tensor
+    dev_status: torch.Tensor    # [batch] int32 storage of uint32 bits, OR-ed into
+
+    @staticmethod
+    def allocate(rows: int, heads: int, head_dim: int, batch: int, dtype=torch.bfloat16, device=None,
+                 layers: Optional[int] = None) -> "KvReadOutputs":
+        d = device or "cuda"
+        shape = (rows, heads, head_dim) if layers is None else (layers, rows, heads, head_dim)
+        return KvReadOutputs(k=torch.empty(shape, dtype=dtype, device=d), v=torch.empty(shape, dtype=dtype, device=d),
+                             dev_status=torch.zeros(batch, dtype=torch.int32, device=d))
+
+
+def kv_read(cache, *, layer: Optional[int] = None, seq_lens=None, max_len: Optional[int] = None, cu_seqlens=None,
+            row_slots=None, rows: Optional[int] = None, out=None, stream=None) -> KvReadOutputs:
+    """The cache's entries of the given rows' places (as kv_append places rows) as dense rows of the cache's dtype: of one
+    layer k, v [rows, heads, head_dim], or, without layer, of every layer [layers, rows, heads, head_dim].
+
+    rows: how many there are (needed with cu_seqlens where neither out nor row_slots tells).  A request's whole history is
+    seq_lens of zeros and its lengths in cu_seqlens.  A row whose place lies outside the cache is 0; rows of no request are
+    left as they are in out.  dev_status is OR-ed into."""
+    lib = load_library()
+    _require_cache(cache)
+    dev, index = cache.device, cache.index
+    if rows is None:
+        if out is not None and isinstance(out.k, torch.Tensor):
+            rows = out.k.shape[-3]
+        elif row_slots is not None and isinstance(row_slots, torch.Tensor):
+            rows = row_slots.numel()
+    batch, rows, desc = _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots)
+    layers = cache.layers if layer is None else 1
+    if out is None:
+        with _on(stream):
+            out = KvReadOutputs.allocate(rows, cache.heads, cache.head_dim, batch, cache.dtype, dev,
+                                         layers if layer is None else None)
+    ks, vs = out.k, out.v
+    if layer is None:
+        for t, name in ((ks, "out.k"), (vs, "out.v")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != layers:
+                raise ValueError("%s must be [%d layers, rows, heads, head_dim]" % (name, layers))
+        step = ks.stride(0) if layers > 1 else 0
+        if layers > 1 and vs.stride(0) != step:
+            raise ValueError("out.k and out.v must have the same strides")
+        if layers < 1:
+            raise ValueError("the cache has no layers")
+        ks, vs = ks[0], vs[0]
+    else:
+        step = 0
+    st = _head_rows(ks, "out.k", rows, cache.heads, cache.head_dim, cache.dtype, dev, index)
+    if _head_rows(vs, "out.v", rows, cache.heads, cache.head_dim, cache.dtype, dev, index) != st:
+        raise ValueError("out.k and out.v must have the same strides")
+    _need(out.dev_status, "out.dev_status", torch.int32, batch, dev, index)
+    fn = lib.spec_verify_packed_kv_read if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_read
+    with _on_device(index):
+        code = fn(cache.ref, 0 if layer is None else layer, layers, ctypes.byref(desc), out.k.data_ptr(), out.v.data_ptr(),
+                  step, st[0], st[1], out.dev_status.data_ptr(), _call_stream(stream, dev))
+    if code:
+        _check("spec_verify_packed_kv_read" if isinstance(cache, PackedKvCache) else "spec_verify_kv_read", code)
+    return out
 
 
 @dataclass
