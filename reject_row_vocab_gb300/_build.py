@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["sv_api.cu", "sv_stats.cu", "sv_accept.cu", "sv_sample.cu", "sv_noalloc.cu", "sv_sched.cu", "sv_tree_build.cu",
            "sv_attention.cu", "sv_attention_few.cu", "sv_attention_wide.cu", "sv_attention_f32.cu", "sv_kv_commit.cu", "sv_logprobs.cu",
-           "sv_attention_packed.cu", "sv_attention_packed_wide.cu", "sv_kv_append.cu", "sv_kv_read.cu", "sv_packed_commit.cu"]
+           "sv_attention_packed.cu", "sv_attention_packed_few.cu", "sv_attention_packed_wide.cu",
+           "sv_kv_append.cu", "sv_kv_read.cu", "sv_packed_commit.cu"]
 HEADERS = ["sv_internal.h", "sv_device.cuh", "sv_commit.cuh", "sv_kv.cuh", "sv_attention.cuh", "sv_attention_ring.cuh",
            "sv_attention_wide.cuh", "sv_packed.cuh", "sv_rows.cuh", "sv_attention_packed.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -26,6 +26,8 @@ extern "C" sv_status_t spec_verify_packed_attention(
                        row_slots, mask, scale, out, out_row_stride, out_head_stride, lse, dev_status, ws, ws_bytes, &p, &dev);
   if (s != SV_OK || batch == 0) return s;
   c.data += layer * c.layer_stride;
-  const cudaError_t e = launch_packed_attention_wide(p, c, dev, stream);
+  const int64_t rows = static_cast<int64_t>(max_len) * p.group;
+  const cudaError_t e = rows <= (c.head_dim <= 128 ? 16 : 8) ? launch_packed_attention_few(p, c, dev, stream)
+                                                             : launch_packed_attention_wide(p, c, dev, stream);
   return e == cudaSuccess ? SV_OK : cuda_failure(e);
 }

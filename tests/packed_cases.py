@@ -34,6 +34,15 @@ class PackedAttentionCase(AttentionCase):
         self.data, self.dtable = data, dev(self.table)
         return sv.PackedKvCache(data, self.dtable, page_size=self.page, head_dim=self.q.shape[2])
 
+    def oracle(self):
+        """With what weights in half floats may add to a correct computation's error: a weight's own 2^-12 is below the 2^-8 that
+        the bounds count for it, but a small one is a whole number of steps of 2^-24, half of one off, where the largest weight of
+        the row is 2^6 at least (a reference is set that far below a maximum).  So each of the keys seen may add 2^-31 of its |v|."""
+        o = super().oracle()
+        most = np.nan_to_num(self.v[self.layer].abs().numpy()).max()
+        o["mag"] = o["mag"] + 2.0 ** -31 * o["count"][:, None, None] * most / 2.0 ** -8
+        return o
+
     def run(self, sv, out=None, ws=None, stream=None, scale=None):
         dev = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
         return sv.paged_attention(self.q.cuda(), self.cache(sv), dev(np.asarray(self.lens, np.int64)), layer=self.layer,

@@ -60,6 +60,25 @@ def test_lengths(sv, lens, rows):
     run(sv, PackedAttentionCase(lens, rows, 4, 1, 128, 16))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 12])
+def test_many_tiles_a_block(sv, dim, rows):
+    """Places are used again and again, by warps that take parts of some tiles only (one request's bytes for many)."""
+    case = PackedAttentionCase([6000], rows, 32, 8, dim, 16)
+    cache = case.cache(sv)
+    n = 24
+    table = cache.page_table.expand(n, -1).contiguous()
+    many = sv.PackedKvCache(cache.data, table, page_size=16, head_dim=dim)
+    q = case.q.cuda().repeat(n, 1, 1)
+    lens = torch.tensor([6000 - 7 * i for i in range(n)], device="cuda")
+    got = sv.paged_attention(q, many, lens, max_len=rows, mask=torch.zeros(n, rows, rows, dtype=torch.uint8, device="cuda"))
+    for i in (0, 5, n - 1):
+        case.lens, case.mask = [6000 - 7 * i], np.zeros((1, rows, rows), np.uint8)
+        one = sv.AttentionOutputs(out=got.out[i * rows:(i + 1) * rows], lse=got.lse[i * rows:(i + 1) * rows], dev_status=got.dev_status[i:i + 1])
+        check_attention(case, one)
+    assert (got.dev_status == 0).all()
+
+
 @pytest.mark.parametrize("dim", [64, 256])
 def test_long_history_of_wide_and_narrow_heads(sv, dim):
     run(sv, PackedAttentionCase([7000, 300], 1, 8, 2, dim, 16))
