@@ -27,6 +27,7 @@
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "sv_attention_packed.cuh"
 
@@ -43,9 +44,8 @@ constexpr float kSlack = 14.0f;  // ... and scores may pass it by this much: wei
 template <int D, int NT>
 struct Few4 {
   static constexpr int kRows = 8 * NT;
-  // Sixteen warps have 128 registers each, twelve 168: enough for 8 rows of 128 columns, and for more.
-  static constexpr bool kLarge = D == 256 || NT == 2;
-  static constexpr int kTakers = kLarge ? 8 : 10, kStageWarps = kLarge ? 2 : 4;
+  static constexpr int kTakers = kSlices, kStageWarps = 2;
+  static constexpr int kTogether = D * NT <= 128 ? 2 : 1;  // tiles that a warp takes at once: as many as its registers hold
   static constexpr int kThreads = 32 * (kTakers + kStageWarps + 2);  // and a warp each to plan, to load Q
   static constexpr int kPlaces = D == 64 ? 12 : D == 256 ? 4 : 8;
   using Stage = PackedStage<kPlaces, kStageWarps, packed_tile_bytes(D)>;
@@ -60,8 +60,7 @@ struct Few4 {
   static constexpr int kLeft = kQ + 2 * kRows * kQRow;
   static constexpr int kFlags = kLeft + kTakers * kLeave;
   static constexpr int kMisc = kFlags + kTakers * 4 + (kTakers * 4) % 16;  // left free barrier, last, split, count
-  static constexpr int kAt = kMisc + 32;  // int2 [kSlices]: where a slice's codes and scales lie in a tile
-  static constexpr int kParts = kAt + kSlices * 8;
+  static constexpr int kParts = kMisc + 32;
   static constexpr int kSmem = kParts + 2 * static_cast<int>(sizeof(AttnSegment));
 };
 
@@ -131,10 +130,6 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
     *s_count = 0u;
     mbar_fence_init();
   }
-  if (t < kSlices) {
-    const int x = t * kSlice, in = x & ((1 << tiles.rows_log) - 1), at = (x >> tiles.rows_log) * tiles.block;
-    reinterpret_cast<int2*>(smem + W::kAt)[t] = make_int2(at + in * (p.c.head_dim / 2), at + in * (p.c.head_dim / 16));
-  }
   __syncthreads();
   grid_dependency_wait();
   allow_dependents();
@@ -167,21 +162,25 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
     const int g8 = lane >> 2, t4 = lane & 3;  // a fragment's row, and its pair of columns
     const int rows_log = tiles.rows_log, block = tiles.block, in_block = (1 << rows_log) - 1;
     const int code_row = dim / 2, scale_row = dim / 16;
-    const int v_codes = packed_v_codes(in_block + 1, dim), k_scales = packed_k_scales(in_block + 1, dim);
-    const int v_scales = packed_v_scales(in_block + 1, dim);
-    // Where key x of a slice lies behind its first key, and what that is for keys 1 and 8 further on.
+    // Where key x of a tile lies, and how far keys 1 and 8 further on are from the first of a slice.
     auto code_at = [&](int x) { return (x >> rows_log) * block + (x & in_block) * code_row; };
     auto scale_at = [&](int x) { return (x >> rows_log) * block + (x & in_block) * scale_row; };
     const int code8 = code_at(8), scale8 = scale_at(8), code1 = code_at(1), scale1 = scale_at(1);
-    // K: keys g8 and g8 + 8, this lane's columns (16 or 32 from k_col on; of 256 columns 32 more, 128 further on).
+    const int x_own = warp * kSlice;  // the warp's keys of every tile
+    // K: keys g8 and g8 + 8, this lane's columns (16 or 32 from k_col on; of 256 columns 32 more, 128 further on).  Columns
+    // that a head does not have are others' codes times 0.
     constexpr int kCols = D == 64 ? 16 : 32;
     const int k_col = t4 * kCols;
     const bool k_live = k_col < dim, k_live2 = D == 256 && k_col + 128 < dim;
-    const int k_code = code_at(g8) + k_col / 2, k_scale = k_scales + scale_at(g8) + k_col / 16;
+    const uint32_t k_code = base + code_at(x_own + g8) + (k_live ? k_col / 2 : 0);
+    const uint32_t k_scale = base + packed_k_scales(in_block + 1, dim) + scale_at(x_own + g8) + (k_live ? k_col / 16 : 0);
+    const uint32_t k_one = k_live ? 128u : 0u, k_one2 = k_live2 ? 128u : 0u;
     // V: keys 2 t4, + 1, + 8, + 9, columns v_col .. v_col + D / 8 - 1.
     const int v_col = g8 * (D / 8);
     const bool v_live = v_col < dim;
-    const int v_code = v_codes + code_at(2 * t4) + v_col / 2, v_scale = v_scales + scale_at(2 * t4) + v_col / 16;
+    const uint32_t v_code = base + packed_v_codes(in_block + 1, dim) + code_at(x_own + 2 * t4) + (v_live ? v_col / 2 : 0);
+    const uint32_t v_scale = base + packed_v_scales(in_block + 1, dim) + scale_at(x_own + 2 * t4) + (v_live ? v_col / 16 : 0);
+    const uint32_t v_one = v_live ? 128u : 0u;
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t unit = 0; ok; ++unit) {
@@ -232,114 +231,107 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
         for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
       }
       uint32_t bad = 0u;
-      int mine = warp;  // this warp's next slice, counted from the tile's first
-#pragma unroll 1
-      for (int i = 0; i < s.cnt; ++i, ++g) {
-        if (!plan.wait(stage.full(g), stage.phase(g))) {
-          ok = false;
-          break;
-        }
-        const int sl = mine;
-        if (sl >= kSlices) {  // (none of this tile; its place is not free before this warp knows of it)
-          if (lane == 0) mbar_arrive(stage.empty(g));
-          mine -= kSlices;
-          continue;
-        }
-        mine += kTakers - kSlices;
-        const int x0 = (s.t0 + i) * kKeys + sl * kSlice;  // the slice's first key
-        const uint32_t good = reinterpret_cast<const uint16_t*>(stage.info(g))[sl];  // keys that are there
-        if (good != 0xffffu) bad |= stage.info(g)[4 + sl / 2];
-        const int2 slice_at = reinterpret_cast<const int2*>(smem + W::kAt)[sl];
-        const uint32_t at = base + g % W::kPlaces * W::Stage::kTile;
-        const uint32_t code0 = at + slice_at.x, scale0 = at + slice_at.y;
-        // All of the slice that this lane needs.
-        uint32_t kw[2][KW] = {}, ks[2][D == 256 ? 2 : 1] = {}, vw[4][VW] = {}, vs[4] = {};
-        if (k_live) {
+      // N tiles from tile i of the segment on, side by side.
+      auto take = [&](auto count, int i) {
+        constexpr int N = decltype(count)::value;
+        uint32_t kw[N][2][KW], ks[N][2][D == 256 ? 2 : 1], vw[N][4][VW], vs[N][4], good[N];
+#pragma unroll
+        for (int z = 0; z < N; ++z) {
+          const uint32_t tile = g + z;
+          if (!plan.wait(stage.full(tile), stage.phase(tile))) return false;
+          good[z] = reinterpret_cast<const uint16_t*>(stage.info(tile))[warp];  // keys that are there
+          if (good[z] != 0xffffu) bad |= stage.info(tile)[4 + warp / 2];
+          const uint32_t at = tile % W::kPlaces * W::Stage::kTile;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a = code0 + k_code + h * code8, b = scale0 + k_scale + h * scale8;
+            const uint32_t a = at + k_code + h * code8, b = at + k_scale + h * scale8;
             if constexpr (D == 256) {
-              uint32_t w4[4];
-              lds_words<4>(a, w4);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) kw[h][j] = w4[j];
-              ks[h][0] = lds_u16(b);
-              if (k_live2) {
-                lds_words<4>(a + 64, w4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) kw[h][KW - 4 + j] = w4[j];
-                ks[h][D == 256 ? 1 : 0] = lds_u16(b + 8);
-              }
+              lds_words<KW>(a, kw[z][h], k_live2 ? 64 : 0);
+              ks[z][h][0] = lds_u16(b);
+              ks[z][h][D == 256 ? 1 : 0] = lds_u16(b + (k_live2 ? 8 : 0));
             } else {
-              lds_words<KW>(a, kw[h]);
-              ks[h][0] = D == 64 ? lds_u8(b) : lds_u16(b);
+              lds_words<KW>(a, kw[z][h]);
+              ks[z][h][0] = D == 64 ? lds_u8(b) : lds_u16(b);
             }
           }
-        }
-        if (v_live) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const uint32_t a = code0 + v_code + (h & 1) * code1 + (h >> 1) * code8;
-            const uint32_t b = scale0 + v_scale + (h & 1) * scale1 + (h >> 1) * scale8;
-            lds_words<VW>(a, vw[h]);
-            vs[h] = D == 256 ? lds_u16(b) : lds_u8(b);
+            lds_words<VW>(at + v_code + (h & 1) * code1 + (h >> 1) * code8, vw[z][h]);
+            const uint32_t b = at + v_scale + (h & 1) * scale1 + (h >> 1) * scale8;
+            vs[z][h] = D == 256 ? lds_u16(b) : lds_u8(b);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(stage.empty(g));
-        if (x0 >= s.r.len + s.r.n) continue;
-        // Scores: two chains of products.
-        float sc[NT][2][4];
+        if (lane == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc[n][0][j] = sc[n][1][j] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint32_t a[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            unpack_codes(kw[h][w], a[h]);
-            const uint32_t byte2 = ks[h][w >> 2];
-            const uint32_t s2 = scale_pair(D == 64 || (w & 2) == 0 ? __byte_perm(byte2, 0u, 0x0404) : __byte_perm(byte2, 0u, 0x1414));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[h][j] = mul_half2(a[h][j], s2);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16(sc[n][0], a[0][0], a[1][0], a[0][1], a[1][1], qf[n][w][0], qf[n][w][1]);
-            mma_f16(sc[n][1], a[0][2], a[1][2], a[0][3], a[1][3], qf[n][w][2], qf[n][w][3]);
-          }
+          for (int z = 0; z < N; ++z) mbar_arrive(stage.empty(g + z));
         }
+        const int x0 = (s.t0 + i) * kKeys + x_own;  // the first tile's first key
+        if (x0 >= s.r.len + s.r.n) return true;
+        // Scores: two chains of products a tile.
+        float sc[N][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc[n][0][j] = (sc[n][0][j] + sc[n][1][j]) * factor[n][j & 1];
-        if (good != 0xffffu || x0 + kSlice > s.r.len) {
+        for (int z = 0; z < N; ++z) {
+          float other[NT][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t see = row_sees_of(p, s.r, s.b, (s.rt * kRows + n * 8 + 2 * t4 + c) / p.group, x0, good);
-              if (!(see >> g8 & 1u)) sc[n][0][c] = -kInfF;
-              if (!(see >> (g8 + 8) & 1u)) sc[n][0][2 + c] = -kInfF;
+            for (int j = 0; j < 4; ++j) sc[z][n][j] = other[n][j] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              unpack_codes(kw[z][h][w], a[h]);
+              const uint32_t s2 = scale_pair(__byte_perm(ks[z][h][w >> 2], 0u, D == 64 || (w & 2) == 0 ? 0x4040 : 0x4141),
+                                             w < 4 ? k_one : k_one2);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) a[h][j] = mul_half2(a[h][j], s2);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(sc[z][n], a[0][0], a[1][0], a[0][1], a[1][1], qf[n][w][0], qf[n][w][1]);
+              mma_f16(other[n], a[0][2], a[1][2], a[0][3], a[1][3], qf[n][w][2], qf[n][w][3]);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[z][n][j] = (sc[z][n][j] + other[n][j]) * factor[n][j & 1];
         }
+#pragma unroll
+        for (int z = 0; z < N; ++z)
+          if (good[z] != 0xffffu || x0 + z * kKeys + kSlice > s.r.len) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t see =
+                    row_sees_of(p, s.r, s.b, (s.rt * kRows + n * 8 + 2 * t4 + c) / p.group, x0 + z * kKeys, good[z]);
+                if (!(see >> g8 & 1u)) sc[z][n][c] = -kInfF;
+                if (!(see >> (g8 + 8) & 1u)) sc[z][n][2 + c] = -kInfF;
+              }
+          }
+        float top[NT][2];
         bool grow = false;  // also at a first finite score, and at NaN
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) grow = grow || !(fmax_nan(sc[n][0][c], sc[n][0][2 + c]) <= m[n][c] + kSlack);
+          for (int c = 0; c < 2; ++c) {
+            top[n][c] = fmax_nan(sc[0][n][c], sc[0][n][2 + c]);
+#pragma unroll
+            for (int z = 1; z < N; ++z) top[n][c] = fmax_nan(top[n][c], fmax_nan(sc[z][n][c], sc[z][n][2 + c]));
+            grow = grow || !(top[n][c] <= m[n][c] + kSlack);
+          }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float top = fmax_nan(sc[n][0][c], sc[n][0][2 + c]);
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, x));
-              if (!(top <= m[n][c] + kSlack)) {
-                const float to = top - kTop, a = ex2_fast(m[n][c] - to);
+              for (int x = 4; x < 32; x <<= 1) top[n][c] = fmax_nan(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], x));
+              if (!(top[n][c] <= m[n][c] + kSlack)) {
+                const float to = top[n][c] - kTop, a = ex2_fast(m[n][c] - to);
                 m[n][c] = to;
                 l[n][c] *= a;
 #pragma unroll
@@ -347,45 +339,58 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
               }
             }
         }
-        uint32_t pt[NT][2];
+        uint32_t pt[N][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float w[4];
+          const float ref[2] = {m[n][0] == -kInfF ? 0.0f : m[n][0], m[n][1] == -kInfF ? 0.0f : m[n][1]};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ref = m[n][j & 1] == -kInfF ? 0.0f : m[n][j & 1];
-            w[j] = ex2_fast(sc[n][0][j] - ref);
+          for (int z = 0; z < N; ++z) {
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = ex2_fast(sc[z][n][j] - ref[j & 1]);
+            l[n][0] += w[0] + w[2];
+            l[n][1] += w[1] + w[3];
+            pt[z][n][0] = turn8(pack_half(w[0], w[1]));
+            pt[z][n][1] = turn8(pack_half(w[2], w[3]));
           }
-          l[n][0] += w[0] + w[2];
-          l[n][1] += w[1] + w[3];
-          pt[n][0] = turn8(pack_half(w[0], w[1]));
-          pt[n][1] = turn8(pack_half(w[2], w[3]));
         }
         // V: word w of a pair of keys holds eight columns of both.
-        const uint32_t sa = scale_pair(__byte_perm(vs[0], vs[1], D == 256 ? 0x4000 : 0x4101));
-        const uint32_t sb = scale_pair(__byte_perm(vs[2], vs[3], D == 256 ? 0x4000 : 0x4101));
-        uint32_t sa2 = sa, sb2 = sb;
-        if constexpr (D == 256) {
-          sa2 = scale_pair(__byte_perm(vs[0], vs[1], 0x5010));
-          sb2 = scale_pair(__byte_perm(vs[2], vs[3], 0x5010));
-        }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          uint32_t even[2][4], odd[2][4];  // by pair of keys: the codes' even and odd columns
+        for (int z = 0; z < N; ++z) {
+          uint32_t s2[D == 256 ? 2 : 1][2];  // by group of columns, by pair of keys
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a = vw[2 * h][w], b = vw[2 * h + 1][w];
-            const uint32_t s2 = w < 2 ? (h ? sb : sa) : (h ? sb2 : sa2);
-            unpack_codes((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
-            unpack_codes(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) even[h][j] = mul_half2(even[h][j], s2), odd[h][j] = mul_half2(odd[h][j], s2);
+            s2[0][h] = scale_pair(__byte_perm(vs[z][2 * h], vs[z][2 * h + 1], D == 256 ? 0x7430 : 0x1410), v_one);
+            if constexpr (D == 256) s2[1][h] = scale_pair(__byte_perm(vs[z][2 * h], vs[z][2 * h + 1], 0x7531), v_one);
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int w = 0; w < VW; ++w) {
+            uint32_t even[2][4], odd[2][4];  // by pair of keys: the codes' even and odd columns
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_f16(o[n][w * 4 + j], even[0][j], odd[0][j], even[1][j], odd[1][j], pt[n][0], pt[n][1]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a = vw[z][2 * h][w], b = vw[z][2 * h + 1][w];
+              unpack_codes((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
+              unpack_codes(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) even[h][j] = mul_half2(even[h][j], s2[w / 2][h]), odd[h][j] = mul_half2(odd[h][j], s2[w / 2][h]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(o[n][w * 4 + j], even[0][j], odd[0][j], even[1][j], odd[1][j], pt[z][n][0], pt[z][n][1]);
+          }
+        }
+        return true;
+      };
+#pragma unroll 1
+      for (int i = 0; ok && i < s.cnt;) {
+        if (W::kTogether == 2 && i + 2 <= s.cnt) {
+          ok = take(std::integral_constant<int, W::kTogether>{}, i);
+          i += 2, g += 2;
+        } else {
+          ok = take(std::integral_constant<int, 1>{}, i);
+          ++i, ++g;
         }
       }
       if (!ok) break;

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const ReadParams p,
         if constexpr (kPacked) {
           uint32_t h[4];
           unpack_codes(code[u], h);
-          const uint32_t s2 = scale_pair(byte[u] << 8 | byte[u] << 24);
+          const uint32_t s2 = scale_pair(byte[u] | byte[u] << 16);
           float x[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

@@ -118,11 +118,11 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two scales as a pair of half floats, from bytes 1 and 3 of w (its others are ignored).  Bytes that no call writes, above the
-// largest scale, count as it: every pattern stands for a number.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t w) {
-  uint32_t h = (w & 0xff00ff00u) >> 1, r;
-  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(kMostScale << 7 | kMostScale << 23));
+// Two scales as a pair of half floats, from bytes 0 and 2 of w (the others 0), times `one` / 128: a shift that may also silence
+// them.  Bytes that no call writes, above the largest scale, count as it: every pattern stands for a number.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, uint32_t one = 128u) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w * one), "r"(kMostScale << 7 | kMostScale << 23));
   return r;
 }
 
