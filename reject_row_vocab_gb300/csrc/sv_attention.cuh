@@ -209,11 +209,11 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
 
 // Computed by every block for itself, by T threads of which this is thread t; sync() is a barrier among them.  One
 // scan over the first T requests gives the total and finds the start; only larger batches are gone through again.
-// s_sum [2 T / 32] (2 MAXW at most) and s_find [2] are shared.
-template <int MT, int KT, int U, int T, int MAXW = 16, class Sync>
+// s_sum [2 T / 32] (32 at most) and s_find [2] are shared.
+template <int MT, int KT, int U, int T, class Sync>
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, int t, int64_t* s_sum, int64_t* s_find, Sync sync) {
   constexpr int W = T / 32;
-  static_assert(W <= MAXW, "s_sum");
+  static_assert(W <= 16, "s_sum");
   const int lane = t & 31, warp = t >> 5;
   AttnSpan sp{};
   int64_t own = 0, rest = 0;

@@ -58,9 +58,8 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src, int by
 }
 
 // The places for tiles, and the warps that fill them.  A wait by parity needs the barrier's phase before to be known to be over,
-// and the next one not to come before the wait is done.  So tile g has place g % NS and is loaded by warp g % NL (NS is a
-// multiple of NL: a place's phases pass by one loading warp), and every taking warp waits for every tile and frees every place,
-// those of tiles that it takes nothing of among them.
+// and the next one not to come before the wait is done.  So tile g has place g % NS, and a place is always loaded by the same
+// warp (g % NL, NS a multiple of NL) and taken by the same ones.
 template <int NS, int NL, int TILE>
 struct PackedStage {
   static_assert(NS % NL == 0, "a place belongs to one loading warp");
@@ -84,9 +83,19 @@ struct PackedStage {
     for (int i = 0; i < NS; ++i) mbar_init(full(i), 64), mbar_init(empty(i), empties);
   }
 
-  // Loading warp lw.  plan: the warps' way along the line of tiles (KvRing, or PlanQueue).
+  // Loading warp lw.  plan: the warps' way along the line of tiles.
   template <class Plan>
   __device__ void load(Plan& plan, const AttnParams& p, const PackedTiles& k, int lw) const {
+    if (k.rows_log >= 2)
+      load_tiles<1>(plan, p, k, lw);
+    else
+      load_tiles<4>(plan, p, k, lw);
+  }
+
+  // WORDS: pages that a lane has of a tile: one where the blocks are 32 at most, each of them a bulk copy; four of blocks of one
+  // or two entries, which are copied 16 bytes a lane.
+  template <int WORDS, class Plan>
+  __device__ __forceinline__ void load_tiles(Plan& plan, const AttnParams& p, const PackedTiles& k, int lw) const {
     const PackedView& c = k.c;
     const int lane = threadIdx.x & 31;
     const int code_row = c.head_dim / 2, scale_row = c.head_dim / 16;
@@ -97,38 +106,39 @@ struct PackedStage {
     bool more = plan.next(s);
     int t = s.t0;
     uint32_t g = 0;          // the tile that t is
+    int turn = 0;            // g % NL
     uint32_t gathered = 0u;  // places whose tile before had gathered rows: a bit each
     uint32_t last = 0;       // tiles up to this warp's last one
     // A tile, and the pages of its blocks lane, lane + 32, ...: the table's words are on their way a tile ahead, and are not
     // touched before they are needed.
     struct Tile {
-      int32_t page[4];
+      int32_t page[WORDS];
       uint32_t g;
-      int x0, in, keys, hist, hkv, b;  // keys from x0 on, the committed ones among them; keys 0: no more tiles
+      int x0, keys, hist, hkv, b;  // keys from x0 on, the committed ones among them; keys 0: no more tiles
       int64_t row0;
     };
     auto ahead = [&](Tile& a) {
       a.keys = 0;
-      for (;; ++t, ++g) {
+      for (;;) {
         if (more && t >= s.t0 + s.cnt) {
           more = plan.next(s);
           t = s.t0;
         }
         if (!more) return;
-        if (static_cast<int>(g % NL) == lw) break;
+        if (turn == lw) break;
+        ++t, ++g, turn = turn + 1 == NL ? 0 : turn + 1;
       }
       a.g = g, a.x0 = t * kKeys, a.hkv = s.hkv, a.b = s.b, a.row0 = s.r.row0;
       a.keys = s.r.len + s.r.n - a.x0, a.hist = s.r.len - a.x0;
       const uint32_t first = divide(static_cast<uint32_t>(a.x0), c.div_mul, c.div_shift);
-      a.in = static_cast<int>(static_cast<uint32_t>(a.x0) - first * c.page_size);  // 0 but where a tile is a part of a page
       const int32_t* table = c.table + a.b * c.ld_table + first;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < WORDS; ++i) {
         const int n = i * 32 + lane;
         a.page[i] = -1;
         if (n < blocks && (n << k.rows_log) < a.keys && first + n < static_cast<uint32_t>(c.max_pages)) a.page[i] = table[n];
       }
-      ++t, ++g;
+      ++t, ++g, turn = turn + 1 == NL ? 0 : turn + 1;
     };
     Tile now;
     ahead(now);
@@ -137,18 +147,14 @@ struct PackedStage {
       ahead(now);
       // (rows that lie apart: the request's last tiles', or all)
       const bool apart = k.copies == 0 || (p.row_slots && a.hist < kKeys && a.keys > a.hist);
-      uint32_t found[4];
+      uint32_t found[WORDS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        found[i] = 0u;
-        if (i * 32 < blocks) found[i] = __ballot_sync(0xffffffffu, a.page[i] >= 0 && a.page[i] < c.pages);
-      }
+      for (int i = 0; i < WORDS; ++i) found[i] = __ballot_sync(0xffffffffu, a.page[i] >= 0 && a.page[i] < c.pages);
+      const uint32_t place = a.g % NS, to = base + place * TILE, bar = full(a.g), bit = 1u << place;
       if (a.g >= NS && !plan.wait(empty(a.g), phase(a.g - NS))) break;
       last = a.g + 1;
-      const uint32_t bit = 1u << (a.g % NS), bar = full(a.g);
-      if (gathered & bit) fence_async();  // what lanes wrote here, before copies go over it (after the wait, by those that copy)
-      gathered = apart ? gathered | bit : gathered & ~bit;
-      const uint32_t to = base + a.g % NS * TILE;
+      if (gathered & bit) fence_async();  // what lanes wrote here, before bulk copies go over it (after the wait, by those that copy)
+      gathered = apart || WORDS > 1 ? gathered | bit : gathered & ~bit;
       if (apart) {
         load_apart(p, k, a.b, a.x0, a.keys, a.hist, a.hkv, a.row0, to, bar, info(a.g));
         continue;
@@ -158,32 +164,54 @@ struct PackedStage {
       const uint32_t range = upto >= 32 ? 0xffffffffu : upto <= 0 ? 0u : (1u << upto) - 1u;
       uint32_t good = range;
       const int need = min(blocks, (a.keys + (1 << k.rows_log) - 1) >> k.rows_log);  // blocks with keys
-      const int have = __popc(found[0]) + __popc(found[1]) + __popc(found[2]) + __popc(found[3]);
+      int have = 0;
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) have += __popc(found[i]);
       if (have < need) {
 #pragma unroll 1
         for (int x = 0; x < 32; ++x) {
           const int n = ((lane & 3) * 32 + x) >> k.rows_log;
-          const uint32_t word = n < 32 ? found[0] : n < 64 ? found[1] : n < 96 ? found[2] : found[3];
+          uint32_t word = found[0];
+#pragma unroll
+          for (int i = 1; i < WORDS; ++i) word = n >> 5 == i ? found[i] : word;
           if (!(word >> (n & 31) & 1u)) good &= ~(1u << x);
         }
       }
       if (lane < 4) info(a.g)[lane] = good, info(a.g)[4 + lane] = range & ~good;
+      const char* head = c.data + a.hkv * c.head_stride;
+      if (WORDS > 1) {
+        const int each = k.block / 16;
+        const uint32_t mul = ((1u << 20) + each - 1) / each;  // exact for x below 2^20 / each: each at most 36, x 2335
+#pragma unroll 2
+        for (int y = 0; y < need * each; y += 32) {
+          const int x = y + lane, n = static_cast<int>(x * mul >> 20);
+          int32_t page = -1;
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) {
+            const int32_t v = __shfl_sync(0xffffffffu, a.page[i], n & 31);
+            if (n >> 5 == i && (found[i] >> (n & 31) & 1u)) page = v;
+          }
+          if (page >= 0) cp_async16(to + x * 16, head + page * c.page_stride + (x - n * each) * 16, true);
+        }
+        cp_async_arrive(bar);  // when this lane's copies are in place
+        mbar_arrive(bar);
+        __syncwarp();
+        continue;
+      }
       if (lane == 0 && have > 0) mbar_expect_tx(bar, static_cast<uint32_t>(have * bytes));
       __syncwarp();
-      const char* head = c.data + a.hkv * c.head_stride;
       if (k.copies == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (found[i] >> lane & 1u)
-            bulk_copy_g2s(to + (i * 32 + lane) * k.block, head + a.page[i] * c.page_stride, bytes, bar);
+        if (found[0] >> lane & 1u) bulk_copy_g2s(to + lane * k.block, head + a.page[0] * c.page_stride, bytes, bar);
       } else if (have > 0) {  // a part of one page: its four arrays, a lane each
         const char* from = head + __shfl_sync(0xffffffffu, a.page[0], 0) * c.page_stride;
+        const int in = static_cast<int>(static_cast<uint32_t>(a.x0) -
+                                        divide(static_cast<uint32_t>(a.x0), c.div_mul, c.div_shift) * c.page_size);
         const int n_code = kKeys * code_row, n_scale = kKeys * scale_row;
         if (lane < 4) {
           const int at = lane == 0 ? 0 : lane == 1 ? packed_v_codes(c.page_size, c.head_dim)
                          : lane == 2 ? packed_k_scales(c.page_size, c.head_dim) : packed_v_scales(c.page_size, c.head_dim);
           const int dst = lane == 0 ? 0 : lane == 1 ? n_code : lane == 2 ? 2 * n_code : 2 * n_code + n_scale;
-          bulk_copy_g2s(to + dst, from + at + static_cast<int64_t>(a.in) * (lane < 2 ? code_row : scale_row), lane < 2 ? n_code : n_scale,
+          bulk_copy_g2s(to + dst, from + at + static_cast<int64_t>(in) * (lane < 2 ? code_row : scale_row), lane < 2 ? n_code : n_scale,
                         bar);
         }
       }
@@ -276,7 +304,7 @@ struct PackedStage {
 struct PlanQueue {
   static constexpr int kPlan = 0;  // AttnSegment [kPlans]
   static constexpr int kBars = kPlan + kPlans * static_cast<int>(sizeof(AttnSegment));  // plan, read [kPlans], q, q free [2]
-  static constexpr int kWarps = 18;                           // of a block, at most
+  static constexpr int kWarps = 16;                           // of a block, at most
   static constexpr int kSums = kBars + (2 * kPlans + 4) * 8;  // int64: sums [2 kWarps], find [2]
   static constexpr int kAbort = kSums + (2 * kWarps + 2) * 8;
   static constexpr int kBytes = (kAbort + 16 + 127) / 128 * 128;
@@ -329,23 +357,49 @@ struct PlanQueue {
     ++plans;
   }
   // The planning warp: the block's segments in order; one without tiles ends them.  Those that are only part of their unit (two
-  // at most) are put down in `parts` too; their number is returned to every lane.
-  template <int MT, int U>
-  __device__ int plan(const AttnParams& p, const AttnSpan& span, AttnSegment* parts) {
+  // at most) are put down in `parts` too; their number is returned to every lane.  load_q(s, slot) is what fetches a unit's Q: by
+  // turns with the plan, whichever has room.
+  template <int MT, int U, class LoadQ>
+  __device__ int plan_and_load(const AttnParams& p, const AttnSpan& span, AttnSegment* parts, LoadQ load_q) {
     int split = 0;
-    if (lane == 0) {
-      AttnWalk<MT, kKeys, U> walk(p, span);
-      AttnSegment s{};
-      for (bool more = true; more; ++plans) {
-        more = walk.next(s);
-        if (!more) s.cnt = 0;
-        if (more && s.cnt < s.nt) parts[split++] = s;
-        if (plans >= kPlans && !wait_one(read_bar(plans), (plans / kPlans - 1) & 1)) break;
-        *slot(plans) = s;
-        mbar_arrive(plan_bar(plans));
+    uint32_t planned = 0, loaded = 0;  // segments; of them, those whose Q is there
+    bool ended = false;
+    AttnWalk<MT, kKeys, U> walk(p, span);
+    const uint64_t start = global_ns();
+    uint64_t moved = start;
+    while (!(ended && loaded + 1 == planned)) {  // (the last one has no Q)
+      const bool room = !ended && (planned < kPlans || mbar_try_wait(read_bar(planned), (planned / kPlans - 1) & 1));
+      if (__all_sync(0xffffffffu, room)) {
+        int more = 0;
+        if (lane == 0) {
+          AttnSegment s{};
+          more = walk.next(s);
+          if (!more) s.cnt = 0;
+          if (more && s.cnt < s.nt) parts[split++] = s;
+          *slot(planned) = s;
+          mbar_arrive(plan_bar(planned));
+        }
+        ended = __shfl_sync(0xffffffffu, more, 0) == 0;
+        ++planned;
+        moved = global_ns();
+        continue;
+      }
+      if (loaded + (ended ? 1 : 0) < planned) {
+        const bool free = loaded < 2 || mbar_try_wait_for(q_free(loaded & 1), (loaded / 2 - 1) & 1, 2000);
+        if (__all_sync(0xffffffffu, free)) {
+          load_q(*slot(loaded), loaded & 1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(read_bar(loaded));
+          ++loaded;
+          moved = global_ns();
+          continue;
+        }
+      }
+      if (__any_sync(0xffffffffu, *abort() != 0 || global_ns() - moved > kWaitNs)) {
+        *abort() = 1;
+        break;
       }
     }
-    __syncwarp();
     return __shfl_sync(0xffffffffu, split, 0);
   }
   // At the end, by every thread after the block's last barrier (never expected: see SV_DEV_TIMEOUT).

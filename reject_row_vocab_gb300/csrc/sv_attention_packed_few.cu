@@ -20,8 +20,8 @@
 // that a half float has room for; so there is no exchange between lanes in a
 // usual tile.
 //
-// A tile's slices of 16 keys go round the taking warps.  A warp that is through
-// with a unit leaves its (m, l, O) in shared memory and goes on; the last one
+// A tile's slices of 16 keys are dealt out to the warps of a team; teams take
+// tiles in turn.  A warp that is through with a unit leaves its (m, l, O) in shared memory and goes on; the last one
 // joins them and writes the rows, or the block's part of the unit.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
@@ -44,10 +44,14 @@ constexpr float kSlack = 14.0f;  // ... and scores may pass it by this much: wei
 template <int D, int NT>
 struct Few4 {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kTakers = kSlices, kStageWarps = 2;
-  static constexpr int kTogether = D * NT <= 128 ? 2 : 1;  // tiles that a warp takes at once: as many as its registers hold
-  static constexpr int kThreads = 32 * (kTakers + kStageWarps + 2);  // and a warp each to plan, to load Q
-  static constexpr int kPlaces = D == 64 ? 12 : D == 256 ? 4 : 8;
+  // A tile is taken by kWarps warps, kTogether slices each: as many as their registers hold.  Tile g is that of team g % kTeams.
+  static constexpr bool kLarge = D == 256 || NT == 2;
+  static constexpr int kTogether = kLarge ? 1 : 2, kWarps = kSlices / kTogether, kTeams = kLarge ? 1 : 3;
+  static constexpr int kTakers = kWarps * kTeams;
+  static constexpr int kHelpers = 4, kStageWarps = D == 256 ? 2 : 3;  // those that load tiles; the last helper plans and fetches Q
+  static constexpr int kThreads = 32 * (kHelpers + kTakers);
+  static constexpr int kPlaces = D == 256 ? 4 : NT == 2 ? 6 : 9;
+  static_assert(kPlaces % kTeams == 0, "a place belongs to one team");
   using Stage = PackedStage<kPlaces, kStageWarps, packed_tile_bytes(D)>;
   static constexpr int KW = D / 32;   // words of codes that a lane has of a key's K
   static constexpr int VW = D / 64;   // and of a key's V
@@ -65,8 +69,7 @@ struct Few4 {
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -107,9 +110,10 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   return r;
 }
 
-template <int D, int NT>
+// DENSE: heads of D columns in pages of a multiple of 16, whose steps in shared memory are constants.
+template <int D, int NT, bool DENSE>
 __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
-    k_packed_few(const AttnParams p, const __grid_constant__ PackedTiles tiles) {
+    k_packed_few(const __grid_constant__ AttnParams p, const __grid_constant__ PackedTiles tiles) {
   using W = Few4<D, NT>;
   constexpr int KW = W::KW, VW = W::VW, MT = W::MT, kRows = W::kRows, kTakers = W::kTakers;
   extern __shared__ __align__(128) char smem[];
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
   AttnSegment* s_parts = reinterpret_cast<AttnSegment*>(smem + W::kParts);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
-    stage.init(kTakers);
+    stage.init(W::kWarps);
     plan.init(kTakers + W::kStageWarps + 1, kTakers);
     mbar_init(bar_left, 1);
     *s_count = 0u;
@@ -133,40 +137,38 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
   __syncthreads();
   grid_dependency_wait();
   allow_dependents();
-  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, W::kThreads, PlanQueue::kWarps>(p, t, plan.sums(), plan.find(),
-                                                                                             [] { __syncthreads(); });
+  const AttnSpan span = attn_span<kRows, kKeys, kUnitPlaces, W::kThreads>(p, t, plan.sums(), plan.find(), [] { __syncthreads(); });
   const int dim = p.c.head_dim;
-  if (warp == kTakers + W::kStageWarps) {
-    const int split = plan.template plan<kRows, kUnitPlaces>(p, span, s_parts);
-    if (lane == 0) *s_split = split;
-  } else if (warp == kTakers + W::kStageWarps + 1) {
-    // Q, a unit ahead: rows that do not exist are 0.
-    AttnSegment s;
-    for (uint32_t unit = 0; plan.next(s); ++unit) {
-      const int at = unit & 1, rows = s.r.n * p.group - s.rt * kRows;
-      if (unit >= 2 && !plan.wait(plan.q_free(at), (unit / 2 - 1) & 1)) break;
-      for (int x = lane; x < kRows * (D / 8); x += 32) {
-        const int row = x / (D / 8), piece = x % (D / 8), grow = s.rt * kRows + row, i = grow / p.group;
-        const bool live = row < rows && piece * 8 < dim;
-        const int64_t from = (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head + piece * 8;
-        cp_async16(base + W::kQ + (at * kRows + row) * W::kQRow + piece * 16, live ? p.q + from * 2 : p.q, live);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      mbar_arrive(plan.q_bar(at));
+  if (warp < W::kHelpers) {
+    if (warp < W::kStageWarps) {
+      stage.load(plan, p, tiles, warp);
+    } else if (warp == W::kHelpers - 1) {
+      const int split = plan.template plan_and_load<kRows, kUnitPlaces>(p, span, s_parts, [&](const AttnSegment& s, int at) {
+        // rows that do not exist are 0
+        const int rows = s.r.n * p.group - s.rt * kRows;
+        for (int x = lane; x < kRows * (D / 8); x += 32) {
+          const int row = x / (D / 8), piece = x % (D / 8), grow = s.rt * kRows + row, i = grow / p.group;
+          const bool live = row < rows && piece * 8 < dim;
+          const int64_t from = (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head + piece * 8;
+          cp_async16(base + W::kQ + (at * kRows + row) * W::kQRow + piece * 16, live ? p.q + from * 2 : p.q, live);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        mbar_arrive(plan.q_bar(at));
+      });
+      if (lane == 0) *s_split = split;
     }
-    cp_async_wait<0>();
-  } else if (warp >= kTakers) {
-    stage.load(plan, p, tiles, warp - kTakers);
   } else {
+    const int taker = warp - W::kHelpers, team = taker / W::kWarps, x_own = taker % W::kWarps * W::kTogether * kSlice;
     const int g8 = lane >> 2, t4 = lane & 3;  // a fragment's row, and its pair of columns
     const int rows_log = tiles.rows_log, block = tiles.block, in_block = (1 << rows_log) - 1;
-    const int code_row = dim / 2, scale_row = dim / 16;
-    // Where key x of a tile lies, and how far keys 1 and 8 further on are from the first of a slice.
+    const int code_row = DENSE ? D / 2 : dim / 2, scale_row = DENSE ? D / 16 : dim / 16;
+    // Where key x of a tile lies, and how far keys 1, 8 and 16 further on are from a slice's first.
     auto code_at = [&](int x) { return (x >> rows_log) * block + (x & in_block) * code_row; };
     auto scale_at = [&](int x) { return (x >> rows_log) * block + (x & in_block) * scale_row; };
-    const int code8 = code_at(8), scale8 = scale_at(8), code1 = code_at(1), scale1 = scale_at(1);
-    const int x_own = warp * kSlice;  // the warp's keys of every tile
+    const int code8 = DENSE ? 8 * code_row : code_at(8), scale8 = DENSE ? 8 * scale_row : scale_at(8);
+    const int code1 = DENSE ? code_row : code_at(1), scale1 = DENSE ? scale_row : scale_at(1);
+    const int code16 = code_at(kSlice), scale16 = scale_at(kSlice);
     // K: keys g8 and g8 + 8, this lane's columns (16 or 32 from k_col on; of 256 columns 32 more, 128 further on).  Columns
     // that a head does not have are others' codes times 0.
     constexpr int kCols = D == 64 ? 16 : 32;
@@ -181,7 +183,9 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
     const uint32_t v_code = base + packed_v_codes(in_block + 1, dim) + code_at(x_own + 2 * t4) + (v_live ? v_col / 2 : 0);
     const uint32_t v_scale = base + packed_v_scales(in_block + 1, dim) + scale_at(x_own + 2 * t4) + (v_live ? v_col / 16 : 0);
     const uint32_t v_one = v_live ? 128u : 0u;
-    uint32_t g = 0;
+    uint32_t g = 0;             // tiles of the segments before
+    int place = team;           // of the team's next tile, and its phase there
+    uint32_t parity = 0u;
     bool ok = true;
     for (uint32_t unit = 0; ok; ++unit) {
       const AttnSegment* const seg = plan.peek();
@@ -223,28 +227,41 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(plan.q_free(q_slot));
-      float m[NT][2], l[NT][2], o[NT][MT][4];
+      // Of rows 2 t4 and 2 t4 + 1: the reference (0 at first), what scores may reach before it moves, the sum, O.
+      float ref[NT][2], most[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -kInfF, l[n][0] = l[n][1] = 0.0f;
+        ref[n][0] = ref[n][1] = l[n][0] = l[n][1] = 0.0f, most[n][0] = most[n][1] = -kInfF;
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
       }
       uint32_t bad = 0u;
-      // N tiles from tile i of the segment on, side by side.
-      auto take = [&](auto count, int i) {
-        constexpr int N = decltype(count)::value;
+      // The warp's slices of tile i of the segment, side by side.
+      constexpr int N = W::kTogether;
+      const int cnt = s.cnt, len = s.r.len, end = s.r.len + s.r.n, first = s.t0 * kKeys + x_own;
+#pragma unroll 1
+      for (int i = (team + W::kTeams - static_cast<int>(g % W::kTeams)) % W::kTeams; i < cnt; i += W::kTeams) {
+        if (!plan.wait(stage.full(place), parity)) {
+          ok = false;
+          break;
+        }
         uint32_t kw[N][2][KW], ks[N][2][D == 256 ? 2 : 1], vw[N][4][VW], vs[N][4], good[N];
+        const uint32_t tile_at = place * W::Stage::kTile, info = base + W::Stage::kInfo + place * 32 + x_own / 8;
+        if constexpr (N == 2) {  // keys that are there, and that are not
+          uint32_t both, none;
+          asm volatile("ld.shared.u32 %0, [%2];\n\tld.shared.u32 %1, [%2 + 16];" : "=r"(both), "=r"(none) : "r"(info));
+          good[0] = both & 0xffffu, good[N - 1] = both >> 16;
+          bad |= none;
+        } else {
+          good[0] = lds_u16(info);
+          bad |= lds_u16(info + 16);
+        }
 #pragma unroll
         for (int z = 0; z < N; ++z) {
-          const uint32_t tile = g + z;
-          if (!plan.wait(stage.full(tile), stage.phase(tile))) return false;
-          good[z] = reinterpret_cast<const uint16_t*>(stage.info(tile))[warp];  // keys that are there
-          if (good[z] != 0xffffu) bad |= stage.info(tile)[4 + warp / 2];
-          const uint32_t at = tile % W::kPlaces * W::Stage::kTile;
+          const uint32_t at_code = tile_at + z * code16, at_scale = tile_at + z * scale16;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a = at + k_code + h * code8, b = at + k_scale + h * scale8;
+            const uint32_t a = at_code + k_code + h * code8, b = at_scale + k_scale + h * scale8;
             if constexpr (D == 256) {
               lds_words<KW>(a, kw[z][h], k_live2 ? 64 : 0);
               ks[z][h][0] = lds_u16(b);
@@ -256,29 +273,29 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
           }
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            lds_words<VW>(at + v_code + (h & 1) * code1 + (h >> 1) * code8, vw[z][h]);
-            const uint32_t b = at + v_scale + (h & 1) * scale1 + (h >> 1) * scale8;
+            lds_words<VW>(at_code + v_code + (h & 1) * code1 + (h >> 1) * code8, vw[z][h]);
+            const uint32_t b = at_scale + v_scale + (h & 1) * scale1 + (h >> 1) * scale8;
             vs[z][h] = D == 256 ? lds_u16(b) : lds_u8(b);
           }
         }
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0) mbar_arrive(stage.empty(place));
+        place += W::kTeams;
+        if (place >= W::kPlaces) place -= W::kPlaces, parity ^= 1u;
+        const int x0 = first + i * kKeys;  // the first key
+        if (x0 >= end) continue;
+        // Scores: two chains of products a slice.
+        float sc[N][NT][4], other[N][NT][4];
 #pragma unroll
-          for (int z = 0; z < N; ++z) mbar_arrive(stage.empty(g + z));
-        }
-        const int x0 = (s.t0 + i) * kKeys + x_own;  // the first tile's first key
-        if (x0 >= s.r.len + s.r.n) return true;
-        // Scores: two chains of products a tile.
-        float sc[N][NT][4];
-#pragma unroll
-        for (int z = 0; z < N; ++z) {
-          float other[NT][4];
+        for (int z = 0; z < N; ++z)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sc[z][n][j] = other[n][j] = 0.0f;
+            for (int j = 0; j < 4; ++j) sc[z][n][j] = other[z][n][j] = 0.0f;
 #pragma unroll
-          for (int w = 0; w < KW; ++w) {
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int z = 0; z < N; ++z) {
             uint32_t a[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -291,23 +308,24 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma_f16(sc[z][n], a[0][0], a[1][0], a[0][1], a[1][1], qf[n][w][0], qf[n][w][1]);
-              mma_f16(other[n], a[0][2], a[1][2], a[0][3], a[1][3], qf[n][w][2], qf[n][w][3]);
+              mma_f16(other[z][n], a[0][2], a[1][2], a[0][3], a[1][3], qf[n][w][2], qf[n][w][3]);
             }
           }
 #pragma unroll
+        for (int z = 0; z < N; ++z)
+#pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sc[z][n][j] = (sc[z][n][j] + other[n][j]) * factor[n][j & 1];
-        }
+            for (int j = 0; j < 4; ++j) sc[z][n][j] = (sc[z][n][j] + other[z][n][j]) * factor[n][j & 1];
 #pragma unroll
         for (int z = 0; z < N; ++z)
-          if (good[z] != 0xffffu || x0 + z * kKeys + kSlice > s.r.len) {
+          if (good[z] != 0xffffu || x0 + z * kSlice + kSlice > len) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const uint32_t see =
-                    row_sees_of(p, s.r, s.b, (s.rt * kRows + n * 8 + 2 * t4 + c) / p.group, x0 + z * kKeys, good[z]);
+                    row_sees_of(p, s.r, s.b, (s.rt * kRows + n * 8 + 2 * t4 + c) / p.group, x0 + z * kSlice, good[z]);
                 if (!(see >> g8 & 1u)) sc[z][n][c] = -kInfF;
                 if (!(see >> (g8 + 8) & 1u)) sc[z][n][2 + c] = -kInfF;
               }
@@ -321,7 +339,7 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
             top[n][c] = fmax_nan(sc[0][n][c], sc[0][n][2 + c]);
 #pragma unroll
             for (int z = 1; z < N; ++z) top[n][c] = fmax_nan(top[n][c], fmax_nan(sc[z][n][c], sc[z][n][2 + c]));
-            grow = grow || !(top[n][c] <= m[n][c] + kSlack);
+            grow = grow || !(top[n][c] <= most[n][c]);
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -330,9 +348,9 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top[n][c] = fmax_nan(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], x));
-              if (!(top[n][c] <= m[n][c] + kSlack)) {
-                const float to = top[n][c] - kTop, a = ex2_fast(m[n][c] - to);
-                m[n][c] = to;
+              if (!(top[n][c] <= most[n][c])) {
+                const float to = top[n][c] - kTop, a = most[n][c] == -kInfF ? 0.0f : ex2_fast(ref[n][c] - to);
+                ref[n][c] = to, most[n][c] = to + kSlack;
                 l[n][c] *= a;
 #pragma unroll
                 for (int d = 0; d < MT; ++d) o[n][d][c] *= a, o[n][d][2 + c] *= a;
@@ -342,12 +360,11 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
         uint32_t pt[N][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float ref[2] = {m[n][0] == -kInfF ? 0.0f : m[n][0], m[n][1] == -kInfF ? 0.0f : m[n][1]};
 #pragma unroll
           for (int z = 0; z < N; ++z) {
             float w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = ex2_fast(sc[z][n][j] - ref[j & 1]);
+            for (int j = 0; j < 4; ++j) w[j] = ex2_fast(sc[z][n][j] - ref[n][j & 1]);
             l[n][0] += w[0] + w[2];
             l[n][1] += w[1] + w[3];
             pt[z][n][0] = turn8(pack_half(w[0], w[1]));
@@ -355,16 +372,18 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
           }
         }
         // V: word w of a pair of keys holds eight columns of both.
+        uint32_t s2[N][D == 256 ? 2 : 1][2];  // scales, by group of columns, by pair of keys
 #pragma unroll
-        for (int z = 0; z < N; ++z) {
-          uint32_t s2[D == 256 ? 2 : 1][2];  // by group of columns, by pair of keys
+        for (int z = 0; z < N; ++z)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            s2[0][h] = scale_pair(__byte_perm(vs[z][2 * h], vs[z][2 * h + 1], D == 256 ? 0x7430 : 0x1410), v_one);
-            if constexpr (D == 256) s2[1][h] = scale_pair(__byte_perm(vs[z][2 * h], vs[z][2 * h + 1], 0x7531), v_one);
+            s2[z][0][h] = scale_pair(__byte_perm(vs[z][2 * h], vs[z][2 * h + 1], D == 256 ? 0x7430 : 0x1410), v_one);
+            if constexpr (D == 256) s2[z][1][h] = scale_pair(__byte_perm(vs[z][2 * h], vs[z][2 * h + 1], 0x7531), v_one);
           }
 #pragma unroll
-          for (int w = 0; w < VW; ++w) {
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int z = 0; z < N; ++z) {
             uint32_t even[2][4], odd[2][4];  // by pair of keys: the codes' even and odd columns
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -372,7 +391,8 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
               unpack_codes((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
               unpack_codes(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) even[h][j] = mul_half2(even[h][j], s2[w / 2][h]), odd[h][j] = mul_half2(odd[h][j], s2[w / 2][h]);
+              for (int j = 0; j < 4; ++j)
+                even[h][j] = mul_half2(even[h][j], s2[z][w / 2][h]), odd[h][j] = mul_half2(odd[h][j], s2[z][w / 2][h]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -380,19 +400,8 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
               for (int n = 0; n < NT; ++n)
                 mma_f16(o[n][w * 4 + j], even[0][j], odd[0][j], even[1][j], odd[1][j], pt[z][n][0], pt[z][n][1]);
           }
-        }
-        return true;
-      };
-#pragma unroll 1
-      for (int i = 0; ok && i < s.cnt;) {
-        if (W::kTogether == 2 && i + 2 <= s.cnt) {
-          ok = take(std::integral_constant<int, W::kTogether>{}, i);
-          i += 2, g += 2;
-        } else {
-          ok = take(std::integral_constant<int, 1>{}, i);
-          ++i, ++g;
-        }
       }
+      g += s.cnt;
       if (!ok) break;
 
       // What the warp has is left to the unit's last warp.  A lane has the same rows and columns in every warp.
@@ -404,14 +413,15 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
           for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
       if (unit > 0 && !plan.wait(bar_left, (unit - 1) & 1)) break;
       auto left = [&](int w) { return reinterpret_cast<float4*>(smem + W::kLeft + w * W::kLeave) + lane; };
-      float4* to = left(warp);
+      float4* to = left(taker);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int d = 0; d < MT; ++d) to[(n * (MT + 1) + d) * 32] = make_float4(o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]);
-        to[(n * (MT + 1) + MT) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+        const float m[2] = {most[n][0] == -kInfF ? -kInfF : ref[n][0], most[n][1] == -kInfF ? -kInfF : ref[n][1]};
+        to[(n * (MT + 1) + MT) * 32] = make_float4(m[0], m[1], l[n][0], l[n][1]);
       }
-      if (lane == 0) s_flags[warp] = bad;
+      if (lane == 0) s_flags[taker] = bad;
       __syncwarp();
       unsigned before = 0u;
       if (lane == 0) asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_addr(s_count)) : "memory");
@@ -500,9 +510,10 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
     attn_join<true, kRows, D, W::kThreads>(p, span, s_parts, *s_split, s_last);
 }
 
-template <int D, int NT>
-cudaError_t launch(const AttnParams& p, const PackedView& c, const DeviceInfo& dev, cudaStream_t stream) {
+template <int D, int NT, bool DENSE>
+cudaError_t launch_as(const AttnParams& p, const PackedView& c, const DeviceInfo& dev, cudaStream_t stream) {
   using W = Few4<D, NT>;
+  const auto kernel = k_packed_few<D, NT, DENSE>;
   static std::mutex mu;
   static bool have[64] = {};
   int d = 0;
@@ -512,14 +523,20 @@ cudaError_t launch(const AttnParams& p, const PackedView& c, const DeviceInfo& d
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!have[d]) {
-      e = cudaFuncSetAttribute(k_packed_few<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kSmem);
       if (e != cudaSuccess) return e;
       have[d] = true;
     }
   }
   static_assert(W::kSmem <= 227 * 1024, "shared memory of a block");
   const int grid = dev.sms < kAttnMaxBlocks ? dev.sms : kAttnMaxBlocks;
-  return launch_pdl(k_packed_few<D, NT>, dim3(static_cast<unsigned>(grid)), dim3(W::kThreads), W::kSmem, stream, p, packed_tiles(c));
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(W::kThreads), W::kSmem, stream, p, packed_tiles(c));
+}
+
+template <int D, int NT>
+cudaError_t launch(const AttnParams& p, const PackedView& c, const DeviceInfo& dev, cudaStream_t stream) {
+  const bool dense = c.head_dim == D && c.page_size % kSlice == 0 && (c.page_size % kKeys == 0 || kKeys % c.page_size == 0);
+  return dense ? launch_as<D, NT, true>(p, c, dev, stream) : launch_as<D, NT, false>(p, c, dev, stream);
 }
 
 }  // namespace
