@@ -104,9 +104,8 @@ struct PackedStage {
     const int bytes = k.copies == 1 ? k.block : kKeys * (code_row + scale_row) * 2;
     AttnSegment s{};
     bool more = plan.next(s);
-    int t = s.t0;
-    uint32_t g = 0;          // the tile that t is
-    int turn = 0;            // g % NL
+    int t = s.t0 + lw;       // this warp's next tile, if the segment has that many, and its number
+    uint32_t g = lw;
     uint32_t gathered = 0u;  // places whose tile before had gathered rows: a bit each
     uint32_t last = 0;       // tiles up to this warp's last one
     // A tile, and the pages of its blocks lane, lane + 32, ...: the table's words are on their way a tile ahead, and are not
@@ -119,15 +118,12 @@ struct PackedStage {
     };
     auto ahead = [&](Tile& a) {
       a.keys = 0;
-      for (;;) {
-        if (more && t >= s.t0 + s.cnt) {
-          more = plan.next(s);
-          t = s.t0;
-        }
-        if (!more) return;
-        if (turn == lw) break;
-        ++t, ++g, turn = turn + 1 == NL ? 0 : turn + 1;
+      while (more && t >= s.t0 + s.cnt) {
+        const int past = t - s.t0 - s.cnt;
+        more = plan.next(s);
+        t = s.t0 + past;
       }
+      if (!more) return;
       a.g = g, a.x0 = t * kKeys, a.hkv = s.hkv, a.b = s.b, a.row0 = s.r.row0;
       a.keys = s.r.len + s.r.n - a.x0, a.hist = s.r.len - a.x0;
       const uint32_t first = divide(static_cast<uint32_t>(a.x0), c.div_mul, c.div_shift);
@@ -138,7 +134,7 @@ struct PackedStage {
         a.page[i] = -1;
         if (n < blocks && (n << k.rows_log) < a.keys && first + n < static_cast<uint32_t>(c.max_pages)) a.page[i] = table[n];
       }
-      ++t, ++g, turn = turn + 1 == NL ? 0 : turn + 1;
+      t += NL, g += NL;
     };
     Tile now;
     ahead(now);

@@ -46,11 +46,11 @@ struct Few4 {
   static constexpr int kRows = 8 * NT;
   // A tile is taken by kWarps warps, kTogether slices each: as many as their registers hold.  Tile g is that of team g % kTeams.
   static constexpr bool kLarge = D == 256 || NT == 2;
-  static constexpr int kTogether = kLarge ? 1 : 2, kWarps = kSlices / kTogether, kTeams = kLarge ? 1 : 3;
+  static constexpr int kTogether = kLarge ? 1 : 2, kWarps = kSlices / kTogether, kTeams = kLarge ? 1 : 2;
   static constexpr int kTakers = kWarps * kTeams;
   static constexpr int kHelpers = 4, kStageWarps = D == 256 ? 2 : 3;  // those that load tiles; the last helper plans and fetches Q
   static constexpr int kThreads = 32 * (kHelpers + kTakers);
-  static constexpr int kPlaces = D == 256 ? 4 : NT == 2 ? 6 : 9;
+  static constexpr int kPlaces = D == 256 ? 4 : 6;
   static_assert(kPlaces % kTeams == 0, "a place belongs to one team");
   using Stage = PackedStage<kPlaces, kStageWarps, packed_tile_bytes(D)>;
   static constexpr int KW = D / 32;   // words of codes that a lane has of a key's K
@@ -167,21 +167,24 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
     auto code_at = [&](int x) { return (x >> rows_log) * block + (x & in_block) * code_row; };
     auto scale_at = [&](int x) { return (x >> rows_log) * block + (x & in_block) * scale_row; };
     const int code8 = DENSE ? 8 * code_row : code_at(8), scale8 = DENSE ? 8 * scale_row : scale_at(8);
-    const int code1 = DENSE ? code_row : code_at(1), scale1 = DENSE ? scale_row : scale_at(1);
+    const int code1 = (t4 & 1 ? -1 : 1) * (DENSE ? code_row : code_at(1)), scale1 = (t4 & 1 ? -1 : 1) * (DENSE ? scale_row : scale_at(1));
     const int code16 = code_at(kSlice), scale16 = scale_at(kSlice);
-    // K: keys g8 and g8 + 8, this lane's columns (16 or 32 from k_col on; of 256 columns 32 more, 128 further on).  Columns
+    // Row m of a product's 16 is key m ^ (m >> 1 & 1) of the slice: so lanes that read K together read neighbouring keys, and those
+    // that read V together keys of both parities, which lie in different banks.
+    const int key = g8 ^ (g8 >> 1 & 1);
+    // K: keys key and key + 8, this lane's columns (16 or 32 from k_col on; of 256 columns 32 more, 128 further on).  Columns
     // that a head does not have are others' codes times 0.
     constexpr int kCols = D == 64 ? 16 : 32;
     const int k_col = t4 * kCols;
     const bool k_live = k_col < dim, k_live2 = D == 256 && k_col + 128 < dim;
-    const uint32_t k_code = base + code_at(x_own + g8) + (k_live ? k_col / 2 : 0);
-    const uint32_t k_scale = base + packed_k_scales(in_block + 1, dim) + scale_at(x_own + g8) + (k_live ? k_col / 16 : 0);
+    const uint32_t k_code = base + code_at(x_own + key) + (k_live ? k_col / 2 : 0);
+    const uint32_t k_scale = base + packed_k_scales(in_block + 1, dim) + scale_at(x_own + key) + (k_live ? k_col / 16 : 0);
     const uint32_t k_one = k_live ? 128u : 0u, k_one2 = k_live2 ? 128u : 0u;
-    // V: keys 2 t4, + 1, + 8, + 9, columns v_col .. v_col + D / 8 - 1.
+    // V: the keys of rows 2 t4, + 1, + 8, + 9, columns v_col .. v_col + D / 8 - 1.
     const int v_col = g8 * (D / 8);
     const bool v_live = v_col < dim;
-    const uint32_t v_code = base + packed_v_codes(in_block + 1, dim) + code_at(x_own + 2 * t4) + (v_live ? v_col / 2 : 0);
-    const uint32_t v_scale = base + packed_v_scales(in_block + 1, dim) + scale_at(x_own + 2 * t4) + (v_live ? v_col / 16 : 0);
+    const uint32_t v_code = base + packed_v_codes(in_block + 1, dim) + code_at(x_own + 2 * t4 + (t4 & 1)) + (v_live ? v_col / 2 : 0);
+    const uint32_t v_scale = base + packed_v_scales(in_block + 1, dim) + scale_at(x_own + 2 * t4 + (t4 & 1)) + (v_live ? v_col / 16 : 0);
     const uint32_t v_one = v_live ? 128u : 0u;
     uint32_t g = 0;             // tiles of the segments before
     int place = team;           // of the team's next tile, and its phase there
@@ -278,11 +281,14 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
             vs[z][h] = D == 256 ? lds_u16(b) : lds_u8(b);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(stage.empty(place));
-        place += W::kTeams;
-        if (place >= W::kPlaces) place -= W::kPlaces, parity ^= 1u;
         const int x0 = first + i * kKeys;  // the first key
+        auto done = [&] {  // all that the warp needs of the tile is in its registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(stage.empty(place));
+          place += W::kTeams;
+          if (place >= W::kPlaces) place -= W::kPlaces, parity ^= 1u;
+        };
+        done();
         if (x0 >= end) continue;
         // Scores: two chains of products a slice.
         float sc[N][NT][4], other[N][NT][4];
@@ -326,8 +332,8 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
               for (int c = 0; c < 2; ++c) {
                 const uint32_t see =
                     row_sees_of(p, s.r, s.b, (s.rt * kRows + n * 8 + 2 * t4 + c) / p.group, x0 + z * kSlice, good[z]);
-                if (!(see >> g8 & 1u)) sc[z][n][c] = -kInfF;
-                if (!(see >> (g8 + 8) & 1u)) sc[z][n][2 + c] = -kInfF;
+                if (!(see >> key & 1u)) sc[z][n][c] = -kInfF;
+                if (!(see >> (key + 8) & 1u)) sc[z][n][2 + c] = -kInfF;
               }
           }
         float top[NT][2];
