@@ -45,6 +45,19 @@ inline PackedTiles packed_tiles(const PackedView& c) {
   return t;
 }
 
+// A query row's way to half floats and back: its largest magnitude (the bits of a bf16 without the sign) goes to 2^14 .. 2^15, as far
+// as a factor goes; and the factor of its scores, scale / up.
+struct RowScale {
+  float up, factor;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top, float scale) {
+  const int e = min(static_cast<int>(top >> 7), 254), shift = min(14 + 127 - e, 126), half = shift / 2;
+  // (back by two factors: one alone may be too large or too small)
+  return RowScale{__uint_as_float(static_cast<uint32_t>(shift + 127) << 23),
+                  scale * __uint_as_float(static_cast<uint32_t>(127 - half) << 23) *
+                      __uint_as_float(static_cast<uint32_t>(127 - (shift - half)) << 23)};
+}
+
 // Bytes of a tile of heads of up to 64, 128 or 256 columns (blocks of one entry are padded: 80 bytes for 64 columns).
 constexpr int packed_tile_bytes(int dim) { return kKeys * (dim <= 64 ? 80 : dim <= 128 ? 144 : 288); }
 
@@ -315,7 +328,7 @@ struct PlanQueue {
   __device__ uint32_t read_bar(uint32_t i) const { return base + kBars + (kPlans + i % kPlans) * 8; }
   __device__ uint32_t q_bar(int i) const { return base + kBars + (2 * kPlans + i) * 8; }
   __device__ uint32_t q_free(int i) const { return base + kBars + (2 * kPlans + 2 + i) * 8; }
-  __device__ AttnSegment* slot(uint32_t i) const { return reinterpret_cast<AttnSegment*>(mem + kPlan) + i % kPlans; }
+  __device__ AttnSegment* plan_slot(uint32_t i) const { return reinterpret_cast<AttnSegment*>(mem + kPlan) + i % kPlans; }
   __device__ int64_t* sums() const { return reinterpret_cast<int64_t*>(mem + kSums); }
   __device__ int64_t* find() const { return sums() + 2 * kWarps; }
   __device__ volatile int* abort() const { return reinterpret_cast<volatile int*>(mem + kAbort); }
@@ -336,7 +349,7 @@ struct PlanQueue {
   __device__ bool wait(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; }
   __device__ bool next(AttnSegment& s) {
     if (!wait(plan_bar(plans), plans / kPlans & 1)) return false;
-    s = *slot(plans);
+    s = *plan_slot(plans);
     __syncwarp();
     if (lane == 0) mbar_arrive(read_bar(plans));
     ++plans;
@@ -344,59 +357,13 @@ struct PlanQueue {
   }
   __device__ const AttnSegment* peek() const {
     if (!wait(plan_bar(plans), plans / kPlans & 1)) return nullptr;
-    const AttnSegment* s = slot(plans);
+    const AttnSegment* s = plan_slot(plans);
     return s->cnt > 0 ? s : nullptr;
   }
   __device__ void release() {
     __syncwarp();
     if (lane == 0) mbar_arrive(read_bar(plans));
     ++plans;
-  }
-  // The planning warp: the block's segments in order; one without tiles ends them.  Those that are only part of their unit (two
-  // at most) are put down in `parts` too; their number is returned to every lane.  load_q(s, slot) is what fetches a unit's Q: by
-  // turns with the plan, whichever has room.
-  template <int MT, int U, class LoadQ>
-  __device__ int plan_and_load(const AttnParams& p, const AttnSpan& span, AttnSegment* parts, LoadQ load_q) {
-    int split = 0;
-    uint32_t planned = 0, loaded = 0;  // segments; of them, those whose Q is there
-    bool ended = false;
-    AttnWalk<MT, kKeys, U> walk(p, span);
-    const uint64_t start = global_ns();
-    uint64_t moved = start;
-    while (!(ended && loaded + 1 == planned)) {  // (the last one has no Q)
-      const bool room = !ended && (planned < kPlans || mbar_try_wait(read_bar(planned), (planned / kPlans - 1) & 1));
-      if (__all_sync(0xffffffffu, room)) {
-        int more = 0;
-        if (lane == 0) {
-          AttnSegment s{};
-          more = walk.next(s);
-          if (!more) s.cnt = 0;
-          if (more && s.cnt < s.nt) parts[split++] = s;
-          *slot(planned) = s;
-          mbar_arrive(plan_bar(planned));
-        }
-        ended = __shfl_sync(0xffffffffu, more, 0) == 0;
-        ++planned;
-        moved = global_ns();
-        continue;
-      }
-      if (loaded + (ended ? 1 : 0) < planned) {
-        const bool free = loaded < 2 || mbar_try_wait_for(q_free(loaded & 1), (loaded / 2 - 1) & 1, 2000);
-        if (__all_sync(0xffffffffu, free)) {
-          load_q(*slot(loaded), loaded & 1);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(read_bar(loaded));
-          ++loaded;
-          moved = global_ns();
-          continue;
-        }
-      }
-      if (__any_sync(0xffffffffu, *abort() != 0 || global_ns() - moved > kWaitNs)) {
-        *abort() = 1;
-        break;
-      }
-    }
-    return __shfl_sync(0xffffffffu, split, 0);
   }
   // At the end, by every thread after the block's last barrier (never expected: see SV_DEV_TIMEOUT).
   __device__ void report_abort(const AttnParams& p) const {

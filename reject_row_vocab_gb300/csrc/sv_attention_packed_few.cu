@@ -78,12 +78,6 @@ __device__ __forceinline__ uint32_t turn8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // N words (1, 2, 4 or 8: of two pieces that lie `far` bytes apart) from shared memory.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N], int far = 0) {
@@ -143,7 +137,7 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
     if (warp < W::kStageWarps) {
       stage.load(plan, p, tiles, warp);
     } else if (warp == W::kHelpers - 1) {
-      const int split = plan.template plan_and_load<kRows, kUnitPlaces>(p, span, s_parts, [&](const AttnSegment& s, int at) {
+      const int split = plan_and_load<kRows, kUnitPlaces>(plan, p, span, s_parts, 2, [&](const AttnSegment& s, int at) {
         // rows that do not exist are 0
         const int rows = s.r.n * p.group - s.rt * kRows;
         for (int x = lane; x < kRows * (D / 8); x += 32) {
@@ -214,19 +208,13 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the row's largest magnitude to 2^14 .. 2^15 (of numbers too small for that as far as a factor goes)
-        const int e = min(static_cast<int>(top >> 7), 254), shift = min(14 + 127 - e, 126);
-        const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+        const RowScale f = row_scale(top, p.scale_log2);
 #pragma unroll
         for (int w = 0; w < KW; ++w)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qf[n][w][i] = pack_half(bf16_lo(qf[n][w][i]) * up, bf16_hi(qf[n][w][i]) * up);
-        // (two factors: 2^-shift alone may be too large or too small for one)
-        const int half = shift / 2;
-        const float down = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - half) << 23) *
-                           __uint_as_float(static_cast<uint32_t>(127 - (shift - half)) << 23);
+          for (int i = 0; i < 4; ++i) qf[n][w][i] = pack_half(bf16_lo(qf[n][w][i]) * f.up, bf16_hi(qf[n][w][i]) * f.up);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) factor[n][c] = __shfl_sync(0xffffffffu, down, (2 * t4 + c) * 4);
+        for (int c = 0; c < 2; ++c) factor[n][c] = __shfl_sync(0xffffffffu, f.factor, (2 * t4 + c) * 4);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(plan.q_free(q_slot));

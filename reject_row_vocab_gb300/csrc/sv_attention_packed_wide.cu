@@ -1,11 +1,18 @@
 // Attention over the 4-bit cache for many query rows: the kernel of
-// sv_attention_wide.cu on tiles that the loading warps unpack to bf16 (which
-// holds the cache's values exactly).
+// sv_attention_wide.cu on tiles that eight of its warps unpack to half floats,
+// which hold the cache's values exactly.
 //
-// Eight loading warps take 16 keys of a tile each.  A lane has one key's 32
-// columns (16 bytes of codes, two scales) of each block of 64: it fetches them
-// a tile ahead, and writes 64 bytes of bf16 in the swizzle that the matrix unit
-// reads.
+// Each unpacking warp has 16 keys of a tile; a lane has 32 columns of one key
+// in each block of 64: 16 bytes of codes, two scales, 64 bytes of half floats in
+// the swizzle that the matrix unit reads.  Its operands have one type, so the
+// queries are half floats too: the same warps bring each row of a unit's Q to
+// their range by a power of two, which the row's factor of the scores takes
+// back.  The weights are half floats, below 2^14 with the sums in fp32 (their
+// rounding, 2^-12, is below that of the output).
+//
+// A tile's bytes come by bulk copies (sv_attention_packed.cuh), some tiles ahead.
+// Heads of more than 128 columns have no room for that: there the unpacking warps
+// fetch a tile ahead into registers.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include "sv_attention_packed.cuh"
@@ -14,72 +21,205 @@
 namespace sv {
 namespace {
 
-// Four pairs of bf16 from eight codes: a code's half float, its exponent moved to bf16's place, is the value times 2^-112,
-// which the scale brings back.
-__device__ __forceinline__ uint4 unpack_bf16(uint32_t w, uint32_t scale2) {
+constexpr int kUnpackWarps = 8;
+
+// Eight codes times a scale (both halves).
+__device__ __forceinline__ uint4 unpack_half(uint32_t w, uint32_t scale2) {
   uint32_t h[4];
   unpack_codes(w, h);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t m = ((h[i] >> 3) & 0x0fff0fffu) | (h[i] & 0x80008000u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(m), "r"(scale2));
-  }
+  for (int i = 0; i < 4; ++i) h[i] = mul_half2(h[i], scale2);
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// A scale times 2^112 in both halves.
-__device__ __forceinline__ uint32_t bf16_scale2(uint32_t byte) {
-  uint32_t r;
-  const float s = scale_value(byte) * 0x1p112f;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(s));
-  return r;
+// 32 columns of one key, of codes `w` and two scales, to half floats at pieces c0 .. c0 + 3 of row r of a tile.
+template <class R>
+__device__ __forceinline__ void store_half(char* tile, int r, int c0, uint4 w, uint32_t scales) {
+  const uint32_t s0 = scale_pair(__byte_perm(scales, 0u, 0x4040)), s1 = scale_pair(__byte_perm(scales, 0u, 0x4141));
+  *reinterpret_cast<uint4*>(tile + R::piece(r, c0)) = unpack_half(w.x, s0);
+  *reinterpret_cast<uint4*>(tile + R::piece(r, c0 + 1)) = unpack_half(w.y, s0);
+  *reinterpret_cast<uint4*>(tile + R::piece(r, c0 + 2)) = unpack_half(w.z, s1);
+  *reinterpret_cast<uint4*>(tile + R::piece(r, c0 + 3)) = unpack_half(w.w, s1);
 }
 
-struct PackedSource {
-  using Args = PackedView;
-  static constexpr int kWarps = 8, kFulls = kWarps;
-  static constexpr bool kFinite = true;
+// STAGED: through shared memory, by a warp that loads.
+template <bool STAGED>
+struct HalfSource {
+  using Args = PackedTiles;
+  static constexpr int kWarps = kUnpackWarps + (STAGED ? 1 : 0), kFulls = kUnpackWarps;
+  static constexpr bool kHalf = true;
+  template <int CB, int H>
+  static __host__ __device__ constexpr int entries() { return CB == 2 ? 4 : 8; }
+  template <int CB, int H>
+  using Stage = PackedStage<CB == 2 ? 3 : 4, 1, packed_tile_bytes(CB * 64 * H)>;
+  // The source's shared memory: the places, the rows' factors of the last eight units (the unpacking warps are at most six tiles
+  // ahead of the softmax warps: a tile of K needs the place of one four before it, whose product is issued behind the weights two
+  // before that), the barriers of converted Qs.
+  template <int CB, int H>
+  static __host__ __device__ constexpr int factors() { return STAGED ? Stage<CB, H>::kBytes : 0; }
+  template <int CB, int H>
+  static __host__ __device__ constexpr int ready() { return factors<CB, H>() + 8 * kRows * 4; }
+  template <int CB, int H>
+  static __host__ __device__ constexpr int extra_bytes() { return ready<CB, H>() + 16; }
 
-  template <class R>
-  static __device__ void load(R& ring, const AttnParams& p, const Args& c, int lw) {
-    constexpr int kEntries = R::kPieces / 8;  // blocks of 64 columns in an entry
-    constexpr int H = R::kHalves, kBlocks = kEntries * H;
+  template <int CB, int H>
+  static __device__ __forceinline__ void init(char* extra) {
+    if constexpr (STAGED) Stage<CB, H>(extra).init(kUnpackWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(extra) + ready<CB, H>() + i * 8, kUnpackWarps);
+  }
+  template <int CB, int H>
+  static __device__ __forceinline__ uint32_t q_ready(char* extra, int slot) {
+    return smem_addr(extra) + ready<CB, H>() + slot * 8;
+  }
+  template <int CB, int H>
+  static __device__ __forceinline__ float row_factor(char* extra, uint32_t unit, int t) {
+    return reinterpret_cast<const volatile float*>(extra + factors<CB, H>())[unit % 8 * kRows + t];
+  }
+
+  // A warp's share of a unit's Q: rows of bf16 to half floats, in place.
+  template <int CB, int H, class R>
+  static __device__ __forceinline__ bool convert_q(R& ring, const AttnParams& p, char* q, char* extra, const AttnSegment& s, uint32_t unit, int twins,
+                                                   int lw) {
+    constexpr int kPieces = R::kPieces * H, kAtOnce = 32 / kPieces;
+    const int slot = static_cast<int>(unit % twins), lane = ring.lane;
+    if (!ring.wait(ring.q_bar(slot), unit / twins & 1)) return false;
+    const int rows = min(s.r.n * p.group - s.rt * kRows, kRows), c = lane % kPieces;
+    float* const factor = reinterpret_cast<float*>(extra + factors<CB, H>()) + unit % 8 * kRows;
+    for (int r0 = lw * kAtOnce; r0 < rows; r0 += kUnpackWarps * kAtOnce) {
+      const int r = r0 + lane / kPieces, row = slot * 64 + r;
+      uint4* const at = reinterpret_cast<uint4*>(q + (c >> 3) * R::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (r < rows) w[0] = at->x, w[1] = at->y, w[2] = at->z, w[3] = at->w;
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+      top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+      for (int x = 1; x < kPieces; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const RowScale f = row_scale(top, fabsf(p.scale_log2));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_half(bf16_lo(w[i]) * f.up, bf16_hi(w[i]) * f.up);
+      if (r < rows) {
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c == 0) factor[r] = fmaxf(f.factor, 1e-45f);
+      }
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(extra) + ready<CB, H>() + slot * 8);
+    return true;
+  }
+
+  template <int CB, int H, class R>
+  static __device__ __forceinline__ void load(R& ring, const AttnParams& p, const Args& k, char* q, char* extra, int twins, int lw) {
+    if constexpr (STAGED) {
+      const Stage<CB, H> stage(extra);
+      if (lw == kUnpackWarps)
+        stage.load(ring, p, k, 0);
+      else
+        unpack<CB, H>(ring, p, k, stage, q, extra, twins, lw);
+    } else {
+      fetch<CB, H>(ring, p, k.c, q, extra, twins, lw);
+    }
+  }
+
+  // A tile from its place: K, then V.
+  template <int CB, int H, class R, class S>
+  static __device__ __forceinline__ void unpack(R& ring, const AttnParams& p, const Args& k, const S& stage, char* q, char* extra, int twins,
+                                                int lw) {
+    constexpr int kEntries = R::kEntries;
+    static_assert(H == 1, "one entry for K and one for V");
     const int lane = ring.lane, mine = lw * 16 + (lane >> 1);  // this lane's key of a tile
+    const int dim = k.c.head_dim, in_block = (1 << k.rows_log) - 1, at_block = (mine >> k.rows_log) * k.block;
+    const int code_at = at_block + (mine & in_block) * (dim / 2) + (lane & 1) * 16;
+    const int scale_at = at_block + (mine & in_block) * (dim / 16) + (lane & 1) * 2;
+    const int codes[2] = {code_at, code_at + packed_v_codes(in_block + 1, dim)};
+    const int scales[2] = {scale_at + packed_k_scales(in_block + 1, dim), scale_at + packed_v_scales(in_block + 1, dim)};
+    AttnSegment s;
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t unit = 0; ok && ring.next(s); ++unit) {
+      if (!convert_q<CB, H>(ring, p, q, extra, s, unit, twins, lw)) break;
+#pragma unroll 1
+      for (int i = 0; i < s.cnt; ++i, ++g) {
+        if (!ring.wait(stage.full(g), stage.phase(g))) {
+          ok = false;
+          break;
+        }
+        const char* place = stage.tile(g);
+        uint4 w[2][CB];
+        uint32_t b[2][CB];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int n = 0; n < CB; ++n) {
+            const bool live = n * 64 + (lane & 1) * 32 < dim;
+            w[e][n] = *reinterpret_cast<const uint4*>(place + codes[e] + (live ? n * 32 : 0));
+            b[e][n] = *reinterpret_cast<const uint16_t*>(place + scales[e] + (live ? n * 4 : 0));
+            if (!live) b[e][n] = 0u;  // columns that a head does not have are 0
+          }
+        const uint32_t good = reinterpret_cast<const uint16_t*>(stage.info(g))[lw];
+        const uint32_t bad = reinterpret_cast<const uint16_t*>(stage.info(g))[8 + lw];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(stage.empty(g));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t entry = 2 * g + e;
+          if (entry >= kEntries && !ring.wait(ring.empty(entry), R::phase(entry - kEntries))) {
+            ok = false;
+            break;
+          }
+          if (e == 0 && lane == 0) {
+            reinterpret_cast<uint16_t*>(ring.valid(g))[lw] = static_cast<uint16_t>(good);
+            reinterpret_cast<uint16_t*>(ring.valid(g) + 4)[lw] = static_cast<uint16_t>(bad);
+          }
+#pragma unroll
+          for (int n = 0; n < CB; ++n) store_half<R>(ring.tile_mem(entry), mine, n * 8 + (lane & 1) * 4, w[e][n], b[e][n]);
+          fence_async();  // (the matrix unit reads through the asynchronous proxy)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ring.full(entry));
+        }
+        if (!ok) break;
+      }
+    }
+  }
+
+  // A tile from the cache: the next one's bytes are fetched while this one's are unpacked.
+  template <int CB, int H, class R>
+  static __device__ __forceinline__ void fetch(R& ring, const AttnParams& p, const PackedView& c, char* q_mem, char* extra, int twins, int lw) {
+    constexpr int kBlocks = CB * H;
+    const int lane = ring.lane, mine = lw * 16 + (lane >> 1);
     const int v_codes = packed_v_codes(c.page_size, c.head_dim), k_scales = packed_k_scales(c.page_size, c.head_dim);
     const int v_scales = packed_v_scales(c.page_size, c.head_dim);
     struct Tile {
-      uint4 codes[2][kBlocks];       // of K, of V
-      uint32_t scales[2][kBlocks];   // two bytes
-      uint32_t good, bad;            // a bit for each of the warp's keys
+      uint4 codes[2][kBlocks];      // of K, of V
+      uint32_t scales[2][kBlocks];  // two bytes
+      uint32_t good, bad;           // two bits for each of the warp's keys
+      bool first;                   // of its unit
     };
     AttnSegment s{};
     bool more = ring.next(s);
     int t = s.t0;
+    uint32_t unit = 0;
+    bool ok = !more || convert_q<CB, H>(ring, p, q_mem, extra, s, unit, twins, lw);
     int64_t word = more ? key_word(p, s.r, s.b, t * kKeys + mine) : -1;
-    // The next tile's bytes; false behind the last tile.
-    auto fetch = [&](Tile& f) {
-      if (!more) return false;
-      const int x = t * kKeys + mine, hkv = s.hkv, keys = s.r.len + s.r.n;
+    auto ahead = [&](Tile& f) {  // the next tile's bytes; false behind the last tile
+      if (!more || !ok) return false;
+      const int x = t * kKeys + mine, keys = s.r.len + s.r.n;
       const Place at = packed_place(p, c, s.r, x, word);
       const bool there = at.page >= 0;
-      const uint32_t good = __ballot_sync(0xffffffffu, there), bad = __ballot_sync(0xffffffffu, x < keys && !there);
-      f.good = good, f.bad = bad;
-      if (++t >= s.t0 + s.cnt) {
-        more = ring.next(s);
-        t = s.t0;
-      }
-      if (more) word = key_word(p, s.r, s.b, t * kKeys + mine);
-      const char* block = c.data + at.page * c.page_stride + hkv * c.head_stride;
+      f.good = __ballot_sync(0xffffffffu, there), f.bad = __ballot_sync(0xffffffffu, x < keys && !there);
+      const char* block = c.data + at.page * c.page_stride + s.hkv * c.head_stride;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           const int d = i * 64 + (lane & 1) * 32;
-          f.codes[k][i] = make_uint4(0u, 0u, 0u, 0u);
-          f.scales[k][i] = 0u;
+          f.codes[e][i] = make_uint4(0u, 0u, 0u, 0u);
+          f.scales[e][i] = 0u;
           if (there && d < c.head_dim) {
-            f.codes[k][i] = *reinterpret_cast<const uint4*>(block + (k ? v_codes : 0) + at.in * (c.head_dim / 2) + d / 2);
-            f.scales[k][i] = *reinterpret_cast<const uint16_t*>(block + (k ? v_scales : k_scales) +
+            f.codes[e][i] = *reinterpret_cast<const uint4*>(block + (e ? v_codes : 0) + at.in * (c.head_dim / 2) + d / 2);
+            f.scales[e][i] = *reinterpret_cast<const uint16_t*>(block + (e ? v_scales : k_scales) +
                                                                 at.in * (c.head_dim / 16) + d / 16);
           }
         }
@@ -87,10 +227,19 @@ struct PackedSource {
     };
     uint32_t q = 0;
     Tile next_tile;
-    bool have = fetch(next_tile);
-    for (bool ok = true; have && ok;) {
+    bool have = ahead(next_tile);
+    while (have && ok) {
       const Tile f = next_tile;
-      have = fetch(next_tile);
+      // The walk's next tile.  (A unit's Q is converted before its first tile is unpacked, and after the last of the unit before:
+      // only then is its place sure to be given back.)
+      bool turn = false;
+      if (++t >= s.t0 + s.cnt) {
+        more = ring.next(s);
+        t = s.t0;
+        turn = more;
+      }
+      if (more) word = key_word(p, s.r, s.b, t * kKeys + mine);
+      have = ahead(next_tile);
       const uint32_t g = q / (2 * H);
 #pragma unroll
       for (int e = 0; e < 2 * H; ++e, ++q) {
@@ -98,8 +247,7 @@ struct PackedSource {
           ok = false;
           break;
         }
-        if (e == 0 && lane < 16) {
-          // (a key is two lanes' bits)
+        if (e == 0 && lane < 16) {  // (a key is two lanes' bits)
           const uint32_t there = __ballot_sync(0xffffu, f.good >> (2 * lane) & 1u);
           const uint32_t missing = __ballot_sync(0xffffu, f.bad >> (2 * lane) & 1u);
           if (lane == 0) {
@@ -107,24 +255,16 @@ struct PackedSource {
             reinterpret_cast<uint16_t*>(ring.valid(g) + 4)[lw] = static_cast<uint16_t>(missing);
           }
         }
-        char* tile = ring.tile_mem(q);
-        constexpr int kK = 0;
-        const int which = e >= H ? 1 : kK;
 #pragma unroll
-        for (int i = 0; i < kEntries; ++i) {
-          const int n = (e % H) * kEntries + i;
-          const uint4 w = f.codes[which][n];
-          const uint32_t s0 = bf16_scale2(f.scales[which][n] & 0xffu), s1 = bf16_scale2(f.scales[which][n] >> 8);
-          const int c0 = i * 8 + (lane & 1) * 4;
-          *reinterpret_cast<uint4*>(tile + R::piece(mine, c0)) = unpack_bf16(w.x, s0);
-          *reinterpret_cast<uint4*>(tile + R::piece(mine, c0 + 1)) = unpack_bf16(w.y, s0);
-          *reinterpret_cast<uint4*>(tile + R::piece(mine, c0 + 2)) = unpack_bf16(w.z, s1);
-          *reinterpret_cast<uint4*>(tile + R::piece(mine, c0 + 3)) = unpack_bf16(w.w, s1);
+        for (int i = 0; i < CB; ++i) {
+          const int n = (e % H) * CB + i;
+          store_half<R>(ring.tile_mem(q), mine, i * 8 + (lane & 1) * 4, f.codes[e >= H ? 1 : 0][n], f.scales[e >= H ? 1 : 0][n]);
         }
-        fence_async();  // (the matrix unit reads through the asynchronous proxy)
+        fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(ring.full(q));
       }
+      if (ok && turn) ok = convert_q<CB, H>(ring, p, q_mem, extra, s, ++unit, twins, lw);
     }
   }
 };
@@ -132,10 +272,11 @@ struct PackedSource {
 }  // namespace
 
 cudaError_t launch_packed_attention_wide(const AttnParams& p, const PackedView& c, const DeviceInfo& dev, cudaStream_t stream) {
+  const PackedTiles tiles = packed_tiles(c);
   const int dim = c.head_dim;
-  return dim <= 64    ? launch_wide<1, 1, PackedSource>(p, c, dev, stream)
-         : dim <= 128 ? launch_wide<2, 1, PackedSource>(p, c, dev, stream)
-                      : launch_wide<2, 2, PackedSource>(p, c, dev, stream);
+  return dim <= 64    ? launch_wide<1, 1, HalfSource<true>>(p, tiles, dev, stream)
+         : dim <= 128 ? launch_wide<2, 1, HalfSource<true>>(p, tiles, dev, stream)
+                      : launch_wide<2, 2, HalfSource<false>>(p, tiles, dev, stream);
 }
 
 }  // namespace sv

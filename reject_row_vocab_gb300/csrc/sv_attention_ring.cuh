@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // K and V of the call's layer as [pages][page_size][heads][head_dim] tensors, in boxes of 128 bytes of `rows` rows of a
 // page (a power of two that divides the page's; 0: none, the pages are copied row by row).
 struct KvMaps {
@@ -405,38 +411,44 @@ struct KvRing {
   // bytes at `at`, in the tiles' swizzle; slots Qs in turn, `slot_rows` rows apart.
   template <int MT>
   __device__ void load_q(const AttnParams& p, uint32_t at, int block, int slots, int slot_rows) {
-    constexpr int kRowPieces = kPieces * H, kLanes = kRowPieces < 32 ? kRowPieces : 32;  // lanes on a row
     AttnSegment s;
-    const int c0 = lane % kLanes, sub = lane / kLanes;
     for (uint32_t unit = 0; next(s); ++unit) {
       const int slot = static_cast<int>(unit % slots);
       const uint32_t turn = unit / slots;
       if (turn > 0 && !wait(q_free(slot), (turn - 1) & 1)) break;
-      const int rows = s.r.n * p.group - s.rt * MT;
-      const int upto = min(MT, (rows + 31) & ~31);  // rows of the warps that have any
-      for (int r0 = 0; r0 < upto; r0 += 32) {       // a lane finds one row's place, the warp copies the 32 of them
-        const int grow = s.rt * MT + r0 + lane, i = grow / p.group;
-        const int64_t from = r0 + lane < min(rows, MT)
-                                 ? (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head
-                                 : -1;
-#pragma unroll 8
-        for (int j = 0; j < (MT < 32 ? MT : 32); j += 32 / kLanes) {
-          const int64_t o = __shfl_sync(0xffffffffu, from, j + sub);
-          const int row = slot * slot_rows + r0 + j + sub;
-#pragma unroll
-          for (int c = c0; c < kRowPieces; c += kLanes) {
-            const bool live = o >= 0 && c * kEach < p.c.head_dim;
-            cp_async16(at + (c >> 3) * block + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                       live ? p.q + (o + c * kEach) * ES : p.q, live);
-          }
-        }
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_async();
-      mbar_arrive(q_bar(slot));
+      fetch_q<MT>(p, s, at, block, slot, slot_rows);
     }
     cp_async_wait<0>();
+  }
+
+  // A unit's Q, by a warp.
+  template <int MT>
+  __device__ void fetch_q(const AttnParams& p, const AttnSegment& s, uint32_t at, int block, int slot, int slot_rows) {
+    constexpr int kRowPieces = kPieces * H, kLanes = kRowPieces < 32 ? kRowPieces : 32;  // lanes on a row
+    const int c0 = lane % kLanes, sub = lane / kLanes;
+    const int rows = s.r.n * p.group - s.rt * MT;
+    const int upto = min(MT, (rows + 31) & ~31);  // rows of the warps that have any
+    for (int r0 = 0; r0 < upto; r0 += 32) {       // a lane finds one row's place, the warp copies the 32 of them
+      const int grow = s.rt * MT + r0 + lane, i = grow / p.group;
+      const int64_t from = r0 + lane < min(rows, MT)
+                               ? (s.r.row0 + i) * p.q_row + (s.hkv * p.group + grow - i * p.group) * p.q_head
+                               : -1;
+#pragma unroll 8
+      for (int j = 0; j < (MT < 32 ? MT : 32); j += 32 / kLanes) {
+        const int64_t o = __shfl_sync(0xffffffffu, from, j + sub);
+        const int row = slot * slot_rows + r0 + j + sub;
+#pragma unroll
+        for (int c = c0; c < kRowPieces; c += kLanes) {
+          const bool live = o >= 0 && c * kEach < p.c.head_dim;
+          cp_async16(at + (c >> 3) * block + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                     live ? p.q + (o + c * kEach) * ES : p.q, live);
+        }
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_async();
+    mbar_arrive(q_bar(slot));
   }
 
   // At the end, by every thread after the block's last barrier (never expected: see SV_DEV_TIMEOUT).
@@ -446,6 +458,54 @@ struct KvRing {
     for (int b = threadIdx.x; b < p.batch; b += blockDim.x) p.status[b] = kStTimeout;
   }
 };
+
+// One warp that plans (KvRing::plan) and fetches Q, by turns, whichever has room: load_q(s, slot) fetches a unit's Q into one of
+// `slots`.  Segments that are only part of their unit (two at most) are put down in `parts`, if given; their number is returned
+// to every lane.
+template <int MT, int U, class Queue, class LoadQ>
+__device__ __forceinline__ int plan_and_load(Queue& queue, const AttnParams& p, const AttnSpan& span, AttnSegment* parts, uint32_t slots,
+                                             LoadQ load_q) {
+  int split = 0;
+  uint32_t planned = 0, loaded = 0;  // segments; of them, those whose Q is there
+  bool ended = false;
+  AttnWalk<MT, kKeys, U> walk(p, span);
+  uint64_t moved = global_ns();
+  while (!(ended && loaded + 1 == planned)) {  // (the last one has no Q)
+    const bool room = !ended && (planned < kPlans || mbar_try_wait(queue.read_bar(planned), (planned / kPlans - 1) & 1));
+    if (__all_sync(0xffffffffu, room)) {
+      int more = 0;
+      if (queue.lane == 0) {
+        AttnSegment s{};
+        more = walk.next(s);
+        if (!more) s.cnt = 0;
+        if (parts && more && s.cnt < s.nt) parts[split++] = s;
+        *queue.plan_slot(planned) = s;
+        mbar_arrive(queue.plan_bar(planned));
+      }
+      ended = __shfl_sync(0xffffffffu, more, 0) == 0;
+      ++planned;
+      moved = global_ns();
+      continue;
+    }
+    if (loaded + (ended ? 1 : 0) < planned) {
+      const uint32_t slot = loaded % slots, turn = loaded / slots;
+      const bool free = turn == 0 || mbar_try_wait_for(queue.q_free(slot), (turn - 1) & 1, 2000);
+      if (__all_sync(0xffffffffu, free)) {
+        load_q(*queue.plan_slot(loaded), static_cast<int>(slot));
+        __syncwarp();
+        if (queue.lane == 0) mbar_arrive(queue.read_bar(loaded));
+        ++loaded;
+        moved = global_ns();
+        continue;
+      }
+    }
+    if (__any_sync(0xffffffffu, *queue.abort() != 0 || global_ns() - moved > kWaitNs)) {
+      *queue.abort() = 1;
+      break;
+    }
+  }
+  return __shfl_sync(0xffffffffu, split, 0);
+}
 
 // The NaN and infinite values that the products left out, added by a warp to the rows that it has just written: to its
 // part of the unit, or, without one, to the output, where rows of `none` (a bit each) saw scores of -inf alone and stay 0.

@@ -72,9 +72,9 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 constexpr uint32_t kNegateA = 1u << 13;
-// bf16 x bf16 -> fp32, 128 rows, n columns; b_mn: B's contiguous axis is N (V as it lies), not K.
-__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+// bf16 x bf16 (or half x half) -> fp32, 128 rows, n columns; b_mn: B's contiguous axis is N (V as it lies), not K.
+__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn, bool half) {
+  return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -97,9 +97,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // ---------------------------------------------------------------------------------------------------------------------
 
 // Heads of up to 64 (CB 1), 128 (CB 2) and 256 (CB 2, H 2) columns.
-template <int CB, int H>
+template <int CB, int H, class Source>
 struct Wide {
-  static constexpr int kRing = H == 2 ? 4 : CB == 2 ? 6 : 8;  // entries in the ring
+  static constexpr int kRing = Source::template entries<CB, H>();  // in the ring
   using R = KvRing<2, CB, kRing, H, kRing == 4>;
   static constexpr int kCols = CB * 64, kDP = kCols * H;
   static constexpr int kS = 0, kO = 256;           // tensor memory columns: two S of 128, then O
@@ -107,29 +107,33 @@ struct Wide {
   static constexpr int kQBytes = R::kTile * H;
   static constexpr int kBars = kQBytes + R::kBytes;
   static constexpr int kMisc = kBars + 7 * 8 + 8;
-  static constexpr int kSmem = kMisc + 16;
+  static constexpr int kExtra = (kMisc + 16 + 127) / 128 * 128;  // the source's own
+  static constexpr int kSmem = kExtra + Source::template extra_bytes<CB, H>();
 };
 
 // Rows of a cache of whole numbers.
 struct RowSource {
   using Args = KvMaps;
   static constexpr int kWarps = kLoadWarps, kFulls = 2 * kLoadThreads;  // loading warps; arrivals that fill an entry
-  static constexpr bool kFinite = false;                                // V may hold NaN and infinities
-  template <class R>
-  static __device__ __forceinline__ void load(R& ring, const AttnParams& p, const Args& maps, int lw) {
-    ring.load(p, maps, lw);
-  }
+  // Half floats in the tiles (their values are finite, Q's rows have factors of their own, and one warp plans and fetches Q), or bf16.
+  static constexpr bool kHalf = false;
+  template <int CB, int H>
+  static __host__ __device__ constexpr int entries() { return H == 2 ? 4 : CB == 2 ? 6 : 8; }
+  template <int CB, int H>
+  static __host__ __device__ constexpr int extra_bytes() { return 0; }
 };
 
 // Softmax warps, loading warps, and a warp each to issue, to load Q, to plan.
 template <class Source>
-constexpr int kWideThreads = kSoftmaxThreads + 32 * Source::kWarps + 96;
+constexpr int kWideThreads = kSoftmaxThreads + 32 * Source::kWarps + (Source::kHalf ? 64 : 96);
+// Of half floats: a new reference lies this far below the maximum, in powers of two (weights reach 2^14; a half float's least is 2^-24).
+constexpr float kTopHalf = 6.0f;
 
 template <int CB, int H, class Source>
 __global__ void __launch_bounds__(kWideThreads<Source>, 1)
-    k_attention_wide(const AttnParams p, const __grid_constant__ typename Source::Args source) {
-  using W = Wide<CB, H>;
-  constexpr int kIssue = 4 + Source::kWarps, kQueries = kIssue + 1, kPlanner = kIssue + 2;  // those warps
+    k_attention_wide(const __grid_constant__ AttnParams p, const __grid_constant__ typename Source::Args source) {
+  using W = Wide<CB, H, Source>;
+  constexpr int kIssue = 4 + Source::kWarps, kQueries = Source::kHalf ? -1 : kIssue + 1, kPlanner = kIssue + (Source::kHalf ? 1 : 2);
   using R = typename W::R;
   constexpr int DP = W::kDP;
   extern __shared__ __align__(1024) char smem[];
@@ -151,6 +155,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
 
   if (t == 0) {
     ring.init(1, kIssue + 2, 1, Source::kFulls);
+    if constexpr (Source::kHalf) Source::template init<CB, H>(smem + W::kExtra);
     for (int i = 0; i < 2; ++i) mbar_init(bar_s(i), 2), mbar_init(bar_p(i), kSoftmaxThreads), mbar_init(bar_pv(i), 1);
     mbar_init(bar_soft, kSoftmaxThreads);
     mbar_fence_init();
@@ -171,9 +176,17 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
                                                                                    [] { __syncthreads(); });
 
   if (warp == kPlanner) {
-    ring.template plan<kRows, kUnitPlaces>(p, span);
+    if constexpr (Source::kHalf)
+      plan_and_load<kRows, kUnitPlaces>(ring, p, span, nullptr, twins, [&](const AttnSegment& s, int slot) {
+        ring.template fetch_q<kRows>(p, s, base, R::kBlock, slot, 64);
+      });
+    else
+      ring.template plan<kRows, kUnitPlaces>(p, span);
   } else if (warp >= 4 && warp < kIssue) {
-    Source::load(ring, p, source, warp - 4);
+    if constexpr (Source::kHalf)
+      Source::template load<CB, H>(ring, p, source, smem, smem + W::kExtra, twins, warp - 4);
+    else
+      ring.load(p, source, warp - 4);
   } else if (warp == kQueries) {
     ring.template load_q<kRows>(p, base, R::kBlock, twins, 64);
   } else if (warp == kIssue) {
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
       AttnSegment s;
       uint32_t g = 0, units = 0;
       bool ok = true;
-      const uint32_t qk = instruction(kKeys, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
+      const uint32_t qk = instruction(kKeys, false, Source::kHalf) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
       auto scores = [&](uint32_t n, bool last) {
         const int slot = static_cast<int>(units % twins);
 #pragma unroll 1
@@ -206,7 +219,10 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         return true;
       };
       while (ok && ring.template next<true>(s)) {
-        if (!ring.wait_one(ring.q_bar(static_cast<int>(units % twins)), units / twins & 1)) break;
+        const int q_slot = static_cast<int>(units % twins);
+        uint32_t q_here = ring.q_bar(q_slot);
+        if constexpr (Source::kHalf) q_here = Source::template q_ready<CB, H>(smem + W::kExtra, q_slot);
+        if (!ring.wait_one(q_here, units / twins & 1)) break;
         tc_fence_after();
         ok = scores(g, s.cnt == 1);
         for (int i = 0; ok && i < s.cnt; ++i) {
@@ -228,7 +244,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
 #pragma unroll
             for (int j = 0; j < kKeys / 16; ++j)
               mma_ts(tmem + W::kO + h * W::kCols, tmem + W::kS + (n & 1) * 128 + j * 8, operand(v + j * 2048, R::kBlock),
-                     instruction(W::kCols, true), i > 0 || j > 0);
+                     instruction(W::kCols, true, Source::kHalf), i > 0 || j > 0);
             tc_commit(ring.empty(group));
           }
           if (!ok) break;
@@ -248,7 +264,8 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
     };
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     // a negative scale's sign is in the products; a scale of 0 by the smallest number (0 times a masked -inf is NaN)
-    const float c = fmaxf(fabsf(p.scale_log2), 1e-45f);
+    float c = fmaxf(fabsf(p.scale_log2), 1e-45f);
+    constexpr float kLow = Source::kHalf ? kTopHalf : 0.0f;  // the reference of the weights lies this far below c m
     uint32_t g = 0, units = 0;     // tiles and units so far, this one among them
     bool ok = true, left = false;  // left: a unit that goes on behind this block
     while (const AttnSegment* const seg = ring.peek()) {
@@ -270,12 +287,15 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           break;
         }
         tc_fence_after();
+        if constexpr (Source::kHalf) {  // the row's factor is there with its scores
+          if (i == 0) c = Source::template row_factor<CB, H>(smem + W::kExtra, units - 1, t);
+        }
         const uint4 vv = *reinterpret_cast<const uint4*>(ring.valid(g));
         const uint4 vb = *reinterpret_cast<const uint4*>(ring.valid(g) + 4);
         uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
         bad |= vb.x | vb.y | vb.z | vb.w;
         const bool masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xffffffffu || x0 + kKeys > s.r.len;
-        if (!Source::kFinite && masked && new_rows_differ(p, s.r) && x0 + kKeys > s.r.len) {
+        if (!Source::kHalf && masked && new_rows_differ(p, s.r) && x0 + kKeys > s.r.len) {
           mixed = true;
           const int from = max(s.r.len - x0, 0), upto = min(s.r.len + s.r.n - x0, kKeys);  // the new rows
           bool found = false;
@@ -372,6 +392,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
             tmem_wait_st();
             ref = 0.0f;
           }
+          ref -= kLow;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -386,7 +407,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
               const float b = ex2_fast(fmaf(v[2 * j + 1], c, -ref));
               sum[(2 * j) & 3] += a;
               sum[(2 * j + 1) & 3] += b;
-              pk[j] = pack_bf16(a, b);
+              pk[j] = Source::kHalf ? pack_half(a, b) : pack_bf16(a, b);
             }
             tmem_st32(st + h * 32, pk);
           }
@@ -419,7 +440,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           tmem_ld32(tmem + lanes + W::kO + h * 32, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
           if (t < rows) {
-            if (!Source::kFinite && careful) {
+            if (!Source::kHalf && careful) {
 #pragma unroll
               for (int d = 0; d < 32; d += 4) {
                 const float4 f = nonfinite_seen<true, kKeys>(p, s, my_row, h * 32 + d);
@@ -446,10 +467,10 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         }
       }
       if (whole) {
-        if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m * c, kLn2, logf(l));
+        if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m * c - kLow, kLn2, logf(l));
         if (s.reports && t == 0) p.status[s.b] = bad | attn_timeout(p);
       } else {
-        part[P::kM + t] = m * c;
+        part[P::kM + t] = m * c - kLow;
         part[P::kL + t] = l;
         if (t == 0) {
           part[P::kStatus] = __uint_as_float(bad);
@@ -536,7 +557,7 @@ __global__ void __launch_bounds__(kJoinRows * DP / 8) k_attention_join(AttnParam
 
 template <int CB, int H, class Source>
 cudaError_t launch_wide(const AttnParams& p, const typename Source::Args& source, const DeviceInfo& dev, cudaStream_t stream) {
-  constexpr int DP = Wide<CB, H>::kDP;
+  constexpr int DP = Wide<CB, H, Source>::kDP;
   static std::mutex mu;
   static bool have[64] = {};
   int d = 0;
@@ -546,15 +567,15 @@ cudaError_t launch_wide(const AttnParams& p, const typename Source::Args& source
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!have[d]) {
-      e = cudaFuncSetAttribute(k_attention_wide<CB, H, Source>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<CB, H>::kSmem);
+      e = cudaFuncSetAttribute(k_attention_wide<CB, H, Source>, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<CB, H, Source>::kSmem);
       if (e != cudaSuccess) return e;
       have[d] = true;
     }
   }
-  static_assert(Wide<CB, H>::kSmem <= 227 * 1024, "shared memory of a block");
+  static_assert(Wide<CB, H, Source>::kSmem <= 227 * 1024, "shared memory of a block");
   const int grid = dev.sms < kAttnMaxBlocks / 2 ? dev.sms : kAttnMaxBlocks / 2;  // parts are laid out for 64-row tiles
   e = launch_pdl(k_attention_wide<CB, H, Source>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads<Source>),
-                 Wide<CB, H>::kSmem, stream, p, source);
+                 Wide<CB, H, Source>::kSmem, stream, p, source);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.max_len) * p.group;
   const int slices = static_cast<int>(((rows < kRows ? rows : kRows) + kJoinRows - 1) / kJoinRows);
