@@ -54,42 +54,64 @@ struct HalfSource {
   using Stage = PackedStage<CB == 2 ? 3 : 4, 1, packed_tile_bytes(CB * 64 * H)>;
   // The source's shared memory: the places, the rows' factors of the last eight units (the unpacking warps are at most six tiles
   // ahead of the softmax warps: a tile of K needs the place of one four before it, whose product is issued behind the weights two
-  // before that), the barriers of converted Qs.
+  // before that), what threads of one row tell each other, the
+  // barriers of a converted Q and of a unit's end.
   template <int CB, int H>
   static __host__ __device__ constexpr int factors() { return STAGED ? Stage<CB, H>::kBytes : 0; }
   template <int CB, int H>
-  static __host__ __device__ constexpr int ready() { return factors<CB, H>() + 8 * kRows * 4; }
+  static __host__ __device__ constexpr int ready() { return factors<CB, H>() + 8 * kRows * 4 + kRows * 8; }
   template <int CB, int H>
   static __host__ __device__ constexpr int extra_bytes() { return ready<CB, H>() + 16; }
 
   template <int CB, int H>
   static __device__ __forceinline__ void init(char* extra) {
     if constexpr (STAGED) Stage<CB, H>(extra).init(kUnpackWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(extra) + ready<CB, H>() + i * 8, kUnpackWarps);
+    mbar_init(smem_addr(extra) + ready<CB, H>(), kUnpackWarps);
+    mbar_init(unit_done<CB, H>(extra), kSoftmaxThreads);
   }
   template <int CB, int H>
-  static __device__ __forceinline__ uint32_t q_ready(char* extra, int slot) {
-    return smem_addr(extra) + ready<CB, H>() + slot * 8;
+  static __device__ __forceinline__ uint32_t q_ready(char* extra) {
+    return smem_addr(extra) + ready<CB, H>();
+  }
+  template <int CB, int H>
+  static __device__ __forceinline__ uint32_t unit_done(char* extra) {
+    return smem_addr(extra) + ready<CB, H>() + 8;
+  }
+  template <int CB, int H>
+  static __device__ __forceinline__ float2* pairs(char* extra) {
+    return reinterpret_cast<float2*>(extra + factors<CB, H>() + 8 * kRows * 4);
+  }
+  // 8 KB each: the lower half of a block of Q's second copy, which is not used between a unit's last product and its end.
+  template <int CB, int H>
+  static __device__ __forceinline__ float4* exchange(char* q, int i) {
+    constexpr int kFar = CB * H > 1 ? kKeys * 128 : 0;
+    return reinterpret_cast<float4*>(q + 64 * 128 + i * kFar);
   }
   template <int CB, int H>
   static __device__ __forceinline__ float row_factor(char* extra, uint32_t unit, int t) {
     return reinterpret_cast<const volatile float*>(extra + factors<CB, H>())[unit % 8 * kRows + t];
   }
 
-  // A warp's share of a unit's Q: rows of bf16 to half floats, in place.
+  // A warp's share of a unit's Q: rows of bf16 to half floats, in place, and (of units of up to 64 rows) once more 64 rows
+  // further on, where the end of the unit before has to be over.
   template <int CB, int H, class R>
-  static __device__ __forceinline__ bool convert_q(R& ring, const AttnParams& p, char* q, char* extra, const AttnSegment& s, uint32_t unit, int twins,
-                                                   int lw) {
+  static __device__ __forceinline__ bool convert_q(R& ring, const AttnParams& p, char* q, char* extra, const AttnSegment& s, uint32_t unit,
+                                                   bool split, int lw) {
     constexpr int kPieces = R::kPieces * H, kAtOnce = 32 / kPieces;
-    const int slot = static_cast<int>(unit % twins), lane = ring.lane;
-    if (!ring.wait(ring.q_bar(slot), unit / twins & 1)) return false;
-    const int rows = min(s.r.n * p.group - s.rt * kRows, kRows), c = lane % kPieces;
+    const int lane = ring.lane;
+    if (!ring.wait(ring.q_bar(0), unit & 1)) return false;
+    if (split && unit > 0 && !ring.wait(unit_done<CB, H>(extra), (unit - 1) & 1)) return false;
+    // (with the rows of 0 that fill the last warp's)
+    const int rows = min((s.r.n * p.group - s.rt * kRows + 31) & ~31, kRows), c = lane % kPieces;
     float* const factor = reinterpret_cast<float*>(extra + factors<CB, H>()) + unit % 8 * kRows;
     for (int r0 = lw * kAtOnce; r0 < rows; r0 += kUnpackWarps * kAtOnce) {
-      const int r = r0 + lane / kPieces, row = slot * 64 + r;
-      uint4* const at = reinterpret_cast<uint4*>(q + (c >> 3) * R::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+      const int r = r0 + lane / kPieces;
+      char* const at = q + (c >> 3) * R::kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
       uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (r < rows) w[0] = at->x, w[1] = at->y, w[2] = at->z, w[3] = at->w;
+      if (r < rows) {
+        const uint4 u = *reinterpret_cast<const uint4*>(at);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+      }
       uint32_t top = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
@@ -100,32 +122,33 @@ struct HalfSource {
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = pack_half(bf16_lo(w[i]) * f.up, bf16_hi(w[i]) * f.up);
       if (r < rows) {
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (split) *reinterpret_cast<uint4*>(at + 64 * 128) = make_uint4(w[0], w[1], w[2], w[3]);
         if (c == 0) factor[r] = fmaxf(f.factor, 1e-45f);
       }
     }
     fence_async();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(extra) + ready<CB, H>() + slot * 8);
+    if (lane == 0) mbar_arrive(q_ready<CB, H>(extra));
     return true;
   }
 
   template <int CB, int H, class R>
-  static __device__ __forceinline__ void load(R& ring, const AttnParams& p, const Args& k, char* q, char* extra, int twins, int lw) {
+  static __device__ __forceinline__ void load(R& ring, const AttnParams& p, const Args& k, char* q, char* extra, bool split, int lw) {
     if constexpr (STAGED) {
       const Stage<CB, H> stage(extra);
       if (lw == kUnpackWarps)
         stage.load(ring, p, k, 0);
       else
-        unpack<CB, H>(ring, p, k, stage, q, extra, twins, lw);
+        unpack<CB, H>(ring, p, k, stage, q, extra, split, lw);
     } else {
-      fetch<CB, H>(ring, p, k.c, q, extra, twins, lw);
+      fetch<CB, H>(ring, p, k.c, q, extra, split, lw);
     }
   }
 
   // A tile from its place: K, then V.
   template <int CB, int H, class R, class S>
-  static __device__ __forceinline__ void unpack(R& ring, const AttnParams& p, const Args& k, const S& stage, char* q, char* extra, int twins,
+  static __device__ __forceinline__ void unpack(R& ring, const AttnParams& p, const Args& k, const S& stage, char* q, char* extra, bool split,
                                                 int lw) {
     constexpr int kEntries = R::kEntries;
     static_assert(H == 1, "one entry for K and one for V");
@@ -139,7 +162,6 @@ struct HalfSource {
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t unit = 0; ok && ring.next(s); ++unit) {
-      if (!convert_q<CB, H>(ring, p, q, extra, s, unit, twins, lw)) break;
 #pragma unroll 1
       for (int i = 0; i < s.cnt; ++i, ++g) {
         if (!ring.wait(stage.full(g), stage.phase(g))) {
@@ -179,6 +201,8 @@ struct HalfSource {
           __syncwarp();
           if (lane == 0) mbar_arrive(ring.full(entry));
         }
+        // (Q behind the first tile, which has not to wait for it)
+        if (ok && i == 0) ok = convert_q<CB, H>(ring, p, q, extra, s, unit, split, lw);
         if (!ok) break;
       }
     }
@@ -186,7 +210,7 @@ struct HalfSource {
 
   // A tile from the cache: the next one's bytes are fetched while this one's are unpacked.
   template <int CB, int H, class R>
-  static __device__ __forceinline__ void fetch(R& ring, const AttnParams& p, const PackedView& c, char* q_mem, char* extra, int twins, int lw) {
+  static __device__ __forceinline__ void fetch(R& ring, const AttnParams& p, const PackedView& c, char* q_mem, char* extra, bool split, int lw) {
     constexpr int kBlocks = CB * H;
     const int lane = ring.lane, mine = lw * 16 + (lane >> 1);
     const int v_codes = packed_v_codes(c.page_size, c.head_dim), k_scales = packed_k_scales(c.page_size, c.head_dim);
@@ -201,7 +225,7 @@ struct HalfSource {
     bool more = ring.next(s);
     int t = s.t0;
     uint32_t unit = 0;
-    bool ok = !more || convert_q<CB, H>(ring, p, q_mem, extra, s, unit, twins, lw);
+    bool ok = !more || convert_q<CB, H>(ring, p, q_mem, extra, s, unit, split, lw);
     int64_t word = more ? key_word(p, s.r, s.b, t * kKeys + mine) : -1;
     auto ahead = [&](Tile& f) {  // the next tile's bytes; false behind the last tile
       if (!more || !ok) return false;
@@ -264,7 +288,7 @@ struct HalfSource {
         __syncwarp();
         if (lane == 0) mbar_arrive(ring.full(q));
       }
-      if (ok && turn) ok = convert_q<CB, H>(ring, p, q_mem, extra, s, ++unit, twins, lw);
+      if (ok && turn) ok = convert_q<CB, H>(ring, p, q_mem, extra, s, ++unit, split, lw);
     }
   }
 };

@@ -151,7 +151,12 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
   auto half = [](uint32_t g) { return g >> 1 & 1; };  // parity of tile g at a pair of barriers
   // Units of up to 64 rows have two Qs, one in each half of Q's rows: the products of the lower half read on into what
   // lies behind it, but rows past 64 are nobody's then.
-  const int twins = p.max_len * static_cast<int64_t>(p.group) <= 64 ? 2 : 1;
+  const bool small = p.max_len * static_cast<int64_t>(p.group) <= 64;
+  const int twins = small && !Source::kHalf ? 2 : 1;
+  // With half floats they have Q in both halves instead, and two threads a row: the second takes the tiles' upper 64 keys, with a
+  // reference, a sum and an O of its own (its weights of the lower keys are 0, as are the first one's of the upper); they are put
+  // together at the end of the unit.  (The softmax warps are what limits there; the matrix unit multiplies 128 rows anyway.)
+  const bool split = small && Source::kHalf;
 
   if (t == 0) {
     ring.init(1, kIssue + 2, 1, Source::kFulls);
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
       ring.template plan<kRows, kUnitPlaces>(p, span);
   } else if (warp >= 4 && warp < kIssue) {
     if constexpr (Source::kHalf)
-      Source::template load<CB, H>(ring, p, source, smem, smem + W::kExtra, twins, warp - 4);
+      Source::template load<CB, H>(ring, p, source, smem, smem + W::kExtra, split, warp - 4);
     else
       ring.load(p, source, warp - 4);
   } else if (warp == kQueries) {
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
       while (ok && ring.template next<true>(s)) {
         const int q_slot = static_cast<int>(units % twins);
         uint32_t q_here = ring.q_bar(q_slot);
-        if constexpr (Source::kHalf) q_here = Source::template q_ready<CB, H>(smem + W::kExtra, q_slot);
+        if constexpr (Source::kHalf) q_here = Source::template q_ready<CB, H>(smem + W::kExtra);
         if (!ring.wait_one(q_here, units / twins & 1)) break;
         tc_fence_after();
         ok = scores(g, s.cnt == 1);
@@ -268,13 +273,15 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
     constexpr float kLow = Source::kHalf ? kTopHalf : 0.0f;  // the reference of the weights lies this far below c m
     uint32_t g = 0, units = 0;     // tiles and units so far, this one among them
     bool ok = true, left = false;  // left: a unit that goes on behind this block
+    const int half_of = split ? t >> 6 : 0, mine = split ? t & 63 : t;  // this thread's half of a tile's keys, its row
+    const int h0 = half_of, h1 = split ? half_of + 1 : 2;               // 64 keys each
     while (const AttnSegment* const seg = ring.peek()) {
       const AttnSegment& s = *seg;
       ++units;
       const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
-      const bool idle = warp * 32 >= rows;              // none of the warp's rows exists
-      const int my_row = (s.rt * kRows + t) / p.group;  // new row of this thread, and its head
-      const int head = s.hkv * p.group + (s.rt * kRows + t) - my_row * p.group;
+      const bool idle = (mine & ~31) >= rows;           // none of the warp's rows exists
+      const int my_row = (s.rt * kRows + mine) / p.group;  // new row of this thread, and its head
+      const int head = s.hkv * p.group + (s.rt * kRows + mine) - my_row * p.group;
       float m = -kInfF, l = 0.0f;  // m: a score without its factor c
       uint32_t bad = 0u;
       bool mixed = false;  // a tile whose keys some rows see and others do not
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         }
         tc_fence_after();
         if constexpr (Source::kHalf) {  // the row's factor is there with its scores
-          if (i == 0) c = Source::template row_factor<CB, H>(smem + W::kExtra, units - 1, t);
+          if (i == 0) c = Source::template row_factor<CB, H>(smem + W::kExtra, units - 1, mine);
         }
         const uint4 vv = *reinterpret_cast<const uint4*>(ring.valid(g));
         const uint4 vb = *reinterpret_cast<const uint4*>(ring.valid(g) + 4);
@@ -322,10 +329,11 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         if (!idle) {
           if (masked) {  // what the row does not see of the tile becomes -inf, in place
 #pragma unroll
-            for (int w = 0; w < 4; ++w) vw[w] = row_sees_of(p, s.r, s.b, t < rows ? my_row : s.r.n, x0 + w * 32, vw[w]);
-            uint32_t word = vw[0];
+            for (int w = 0; w < 4; ++w) if (w >= 2 * h0 && w < 2 * h1)
+                vw[w] = row_sees_of(p, s.r, s.b, mine < rows ? my_row : s.r.n, x0 + w * 32, vw[w]);
+            uint32_t word = h0 ? vw[2] : vw[0];
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 2 * h0; h < 2 * h1; ++h) {
               if (!__all_sync(0xffffffffu, word == 0xffffffffu)) {
                 float v[32];
                 if (__any_sync(0xffffffffu, word != 0u)) {
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           // The scores are read twice, for the maximum and for the weights: 128 of them do not fit beside the rest.
           float mx[4] = {-kInfF, -kInfF, -kInfF, -kInfF};
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          for (int h = h0; h < h1; ++h) {
             float v[64];
             tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
             tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           if (__any_sync(0xffffffffu, !(fabsf(ref) < kNear))) {
             const float from = m == -kInfF ? 0.0f : m;
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 2 * h0; h < 2 * h1; ++h) {
               float v[32];
               tmem_ld32(st + h * 32, reinterpret_cast<uint32_t*>(v));
               tmem_wait_ld();
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           ref -= kLow;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          for (int h = h0; h < h1; ++h) {
             float v[64];
             uint32_t pk[32];
             tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
@@ -410,6 +418,12 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
               pk[j] = Source::kHalf ? pack_half(a, b) : pack_bf16(a, b);
             }
             tmem_st32(st + h * 32, pk);
+          }
+          if (split) {  // the other half of the keys is the other thread's
+            uint32_t none[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) none[j] = 0u;
+            tmem_st32(st + (1 - h0) * 32, none);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
@@ -431,15 +445,48 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
       using P = AttnPart<kRows, DP>;
       float* part = whole ? nullptr : attn_part<kRows, DP>(p, blockIdx.x, s.t0 == 0);
       char* out = p.out + ((s.r.row0 + my_row) * p.o_row + head * p.o_head) * 2;
-      const bool none = m == -kInfF;  // nothing seen, or only scores of -inf
+      float top = m * c - kLow, weight = 1.0f;  // the reference, and what O is to be multiplied by
+      if constexpr (Source::kHalf) {
+        if (split) {
+          float2* const pairs = Source::template pairs<CB, H>(smem + W::kExtra);
+          pairs[t] = make_float2(top, l);
+          meet();
+          const float2 other = pairs[t ^ 64];
+          const float both = fmax_nan(top, other.x), from = both == -kInfF ? 0.0f : both;
+          weight = ex2_fast(top - from);
+          l = fmaf(l, weight, other.y * ex2_fast(other.x - from));
+          top = both;
+        }
+      }
+      const bool none = (split ? top : m) == -kInfF;  // nothing seen, or only scores of -inf
       const float inv = none ? 0.0f : 1.0f / l;
-      if (!idle) {
+      if (!idle || split) {
 #pragma unroll 1
         for (int h = 0; h < DP / 32; ++h) {
           float o[32];
           tmem_ld32(tmem + lanes + W::kO + h * 32, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
-          if (t < rows) {
+          if constexpr (Source::kHalf) {
+            if (split) {  // 32 columns go through shared memory (two places, in turn): the second thread's to the first
+              float4* const row = Source::template exchange<CB, H>(smem, h & 1) + mine * 8;
+              if (half_of) {
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                  row[d ^ (mine & 7)] = make_float4(o[4 * d] * weight, o[4 * d + 1] * weight, o[4 * d + 2] * weight, o[4 * d + 3] * weight);
+              }
+              meet();
+              if (!half_of) {
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                  const float4 v = row[d ^ (mine & 7)];
+                  o[4 * d] = fmaf(o[4 * d], weight, v.x), o[4 * d + 1] = fmaf(o[4 * d + 1], weight, v.y);
+                  o[4 * d + 2] = fmaf(o[4 * d + 2], weight, v.z), o[4 * d + 3] = fmaf(o[4 * d + 3], weight, v.w);
+                }
+              }
+              if (CB * H == 1) meet();  // (there is one place)
+            }
+          }
+          if (mine < rows && !half_of) {
             if (!Source::kHalf && careful) {
 #pragma unroll
               for (int d = 0; d < 32; d += 4) {
@@ -460,18 +507,17 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
             } else {
 #pragma unroll
               for (int d = 0; d < 32; d += 4)
-                reinterpret_cast<float4*>(part)[(h * 8 + d / 4) * kRows + t] =
+                reinterpret_cast<float4*>(part)[(h * 8 + d / 4) * kRows + mine] =
                     make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
             }
           }
         }
       }
       if (whole) {
-        if (t < rows && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(m * c - kLow, kLn2, logf(l));
+        if (mine < rows && !half_of && p.lse) p.lse[(s.r.row0 + my_row) * p.heads + head] = none ? -kInfF : fmaf(top, kLn2, logf(l));
         if (s.reports && t == 0) p.status[s.b] = bad | attn_timeout(p);
       } else {
-        part[P::kM + t] = m * c - kLow;
-        part[P::kL + t] = l;
+        if (!half_of) part[P::kM + mine] = top, part[P::kL + mine] = l;
         if (t == 0) {
           part[P::kStatus] = __uint_as_float(bad);
           if (s.t0 == 0) {
@@ -482,6 +528,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         }
       }
       tc_fence_before();
+      if constexpr (Source::kHalf) mbar_arrive(Source::template unit_done<CB, H>(smem + W::kExtra));
       ring.release();
     }
     if (t == 0 && !left)
