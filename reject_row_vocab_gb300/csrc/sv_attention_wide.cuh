@@ -65,11 +65,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand in the 128-byte swizzle.  Stride: bytes between groups of eight rows (1024); lead: bytes between
-// 64-element blocks of the contiguous axis (used where that axis is the operand's M or N).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lead >> 4) & 0x3fffu) << 16) |
-         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operand in the 128-byte swizzle: its lower word, which a part of the operand `bytes` further on only adds
+// bytes / 16 to, and the operand.  (One thread issues all products, so what it computes for each of them counts.)  Stride: bytes
+// between groups of eight rows (1024); lead: bytes between 64-element blocks of the contiguous axis (used where that axis is the
+// operand's M or N).
+__device__ __forceinline__ uint32_t operand_at(uint32_t addr, uint32_t lead) { return (addr >> 4) + ((lead >> 4) << 16); }
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t bytes) {
+  constexpr uint32_t kUpper = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return static_cast<uint64_t>(kUpper) << 32 | (at + (bytes >> 4));
 }
 constexpr uint32_t kNegateA = 1u << 13;
 // bf16 x bf16 (or half x half) -> fp32, 128 rows, n columns; b_mn: B's contiguous axis is N (V as it lies), not K.
@@ -210,12 +213,12 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           fence_async();  // the copies wrote through the generic proxy, the products read through the asynchronous one
           tc_fence_after();
           if (h == 0) mbar_arrive(bar_s(n));  // hands the tile's validity on
-          const uint32_t k = ring.tile(group);
+          const uint32_t q_at = operand_at(base + slot * 64 * 128 + h * R::kTile, 16), k_at = operand_at(ring.tile(group), 16);
+          const uint32_t to = tmem + W::kS + (n & 1) * 128;
 #pragma unroll
           for (int i = 0; i < W::kCols / 16; ++i) {
             const uint32_t at = (i >> 2) * R::kBlock + (i & 3) * 32;
-            mma_ss(tmem + W::kS + (n & 1) * 128, operand(base + slot * 64 * 128 + h * R::kTile + at, 16),
-                   operand(k + at, 16), qk, h > 0 || i > 0);
+            mma_ss(to, operand(q_at, at), operand(k_at, at), qk, h > 0 || i > 0);
           }
           tc_commit(ring.empty(group));
         }
@@ -245,10 +248,11 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
             }
             fence_async();
             tc_fence_after();
-            const uint32_t v = ring.tile(group);
+            const uint32_t v_at = operand_at(ring.tile(group), R::kBlock);
+            const uint32_t to = tmem + W::kO + h * W::kCols, weights = tmem + W::kS + (n & 1) * 128;
 #pragma unroll
             for (int j = 0; j < kKeys / 16; ++j)
-              mma_ts(tmem + W::kO + h * W::kCols, tmem + W::kS + (n & 1) * 128 + j * 8, operand(v + j * 2048, R::kBlock),
+              mma_ts(to, weights + j * 8, operand(v_at, j * 2048),
                      instruction(W::kCols, true, Source::kHalf), i > 0 || j > 0);
             tc_commit(ring.empty(group));
           }
