@@ -589,7 +589,7 @@ typedef struct {
  * position * inv_freq[i].  A pair is columns (i, i + pairs), or (2 i, 2 i + 1)
  * when interleaved; columns from 2 * pairs on are left as they are.  The
  * rotated columns are also multiplied by magnitude (1 for none).  Angles are
- * reduced in 64 bits: far positions lose nothing.
+ * reduced in more than fp32: far positions lose nothing.
  */
 typedef struct {
   const float* inv_freq; /* [pairs], device */

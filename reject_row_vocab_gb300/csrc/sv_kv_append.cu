@@ -9,7 +9,7 @@
 // eight columns of a head: a pair's other half is in the lane itself or one
 // shuffle away, and the row's sines and cosines are computed once, by the
 // warp, and kept in registers for all heads.  The angle is reduced to a part of
-// a turn in 64 bits, where the product of a position and a frequency is exact.
+// a turn in twice the bits of a float.
 //
 // The 4-bit cache: 16 columns are two lanes, one shuffle gives their largest
 // magnitude.
@@ -49,14 +49,29 @@ struct AppendParams {
   int32_t passes, chunks, per;  // a row's passes over its heads, dealt out to `chunks` warps
 };
 
-// Sine and cosine of position * f.
-__device__ __forceinline__ float2 turn_by(int64_t position, float f) {
-  double t = static_cast<double>(position) * (static_cast<double>(f) * 0.15915494309189533577);  // turns
-  t = 2.0 * (t - rint(t));  // half turns, -1 .. 1
-  const float hi = static_cast<float>(t), lo = static_cast<float>(t - hi) * 3.14159265f;
+// Sine and cosine of position * f, from half turns hi + lo.
+__device__ __forceinline__ float2 turn_of(float hi, float lo) {
   float s, c;
   sincospif(hi, &s, &c);
+  lo *= 3.14159265f;
   return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
+}
+// Positions below 2^22, in pairs of floats: f / 2 pi to 2^-49 of itself, the product exactly, whole turns taken off.  (The 64-bit
+// unit does two lanes a clock: 8192 rows took 8 us of it.)
+__device__ __forceinline__ float2 turn_by(float position, float f) {
+  constexpr float kHi = 0.15915494f;                                                      // 1 / 2 pi
+  constexpr float kLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(kHi));  // and what it lacks
+  const float h = f * kHi, l = fmaf(f, kLo, fmaf(f, kHi, -h));
+  const float x = h * position, low = fmaf(l, position, fmaf(h, position, -x));
+  const float part = x - rintf(x), t = part + low;
+  return turn_of(2.0f * t, 2.0f * (low - (t - part)));
+}
+// Any position, in 64 bits.
+__device__ __noinline__ float2 turn_by_far(int64_t position, float f) {
+  double t = static_cast<double>(position) * (static_cast<double>(f) * 0.15915494309189533577);  // turns
+  t = 2.0 * (t - rint(t));
+  const float hi = static_cast<float>(t);
+  return turn_of(hi, static_cast<float>(t - hi));
 }
 
 template <int ES>
@@ -102,7 +117,7 @@ __device__ __forceinline__ Eight<ES> round8(const float (&x)[8]) {
 }
 
 template <int ES, class C, Pairing PAIRING>
-__global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const AppendParams p, const C c) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const AppendParams p, const C c) {
   constexpr bool kPacked = std::is_same<C, PackedView>::value;
   __shared__ float2 s_turn[kAppendWarps][kMaxPairs];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -140,7 +155,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const AppendPar
         load8<ES>(raw[u], at[u], slot[u] >= 0, slot[u] >= 0 && wide);
       }
     };
-    load(first);  // (on its way while the row's place is looked up)
+    load(first);  // (on its way while the row's place is looked up, like the frequencies)
+    float freq[kMaxPairs / 32];
+    const bool turns = n > 0 && first * heads < p.q_heads + p.kv_heads;
+#pragma unroll
+    for (int i = 0; i < kMaxPairs / 32; ++i) freq[i] = turns && i * 32 + lane < n ? p.inv_freq[i * 32 + lane] : 0.0f;
     int j;
     const int b = row_request(p.r, row, lane, &j);
     if (b < 0) continue;
@@ -149,9 +168,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const AppendPar
     const Place place = p.r.row_slots ? slot_place(c, p.r.row_slots[row]) : position_place(c, b, len + j);
     if (place.page < 0 && chunk == 0 && lane == 0) atomicOr(p.status + b, kStSlotRange);
     float co[8], si[8];
-    if (n > 0 && first * heads < p.q_heads + p.kv_heads) {
+    if (turns) {
       const int64_t pos = p.positions ? p.positions[row] : len + j;
-      for (int i = lane; i < n; i += 32) s_turn[warp][i] = turn_by(pos, p.inv_freq[i]);
+      const bool far = pos <= -(1 << 22) || pos >= 1 << 22;
+#pragma unroll
+      for (int i = 0; i < kMaxPairs / 32; ++i)
+        if (i * 32 + lane < n) s_turn[warp][i * 32 + lane] = far ? turn_by_far(pos, freq[i]) : turn_by(static_cast<float>(pos), freq[i]);
       __syncwarp();
       if (turned) {
 #pragma unroll
@@ -169,12 +191,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const AppendPar
     uint32_t odd = 0u;  // a value that is not finite went into the 4-bit cache
     for (int pass0 = first; pass0 < last; pass0 += kUnroll) {
       if (pass0 > first) load(pass0);
-      float x[kUnroll][8];
-      bool rotated[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        rotated[u] = turned && slot[u] >= 0 && slot[u] < p.q_heads + p.kv_heads;
-        float y[8];
+        const int s = slot[u];
+        const bool rotated = turned && s >= 0 && s < p.q_heads + p.kv_heads;
+        float x[8], y[8];
         if (PAIRING == kHalves) {
           Eight<ES> other;
           const int step = n / 8, at_lane = d0 < n ? lane + step : d0 < 2 * n ? lane - step : lane;
@@ -185,59 +206,53 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const AppendPar
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[u][e] = value_of<ES>(raw[u], e);
+          x[e] = value_of<ES>(raw[u], e);
           if (PAIRING == kNeighbours) y[e] = value_of<ES>(raw[u], e ^ 1);
         }
-        if (PAIRING == kHalvesOdd && rotated[u]) {
+        if (PAIRING == kHalvesOdd) {
+          if (rotated) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int d = d0 + e;
-            y[e] = 0.0f;
-            if (d < 2 * n) {
-              const char* o = at[u] + (d < n ? n + e : e - n) * ES;
-              y[e] = ES == 4 ? *reinterpret_cast<const float*>(o)
-                             : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(o)) << 16);
+            for (int e = 0; e < 8; ++e) {
+              const int d = d0 + e;
+              y[e] = 0.0f;
+              if (d < 2 * n) {
+                const char* o = at[u] + (d < n ? n + e : e - n) * ES;
+                y[e] = ES == 4 ? *reinterpret_cast<const float*>(o)
+                               : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(o)) << 16);
+              }
             }
           }
+          __syncwarp();  // (q_out may be q: other lanes' reads of the head come first)
         }
-        if (rotated[u]) {
+        if (rotated) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (d0 + e < 2 * n) x[u][e] = fmaf(x[u][e], co[e], y[e] * si[e]);
+            if (d0 + e < 2 * n) x[e] = fmaf(x[e], co[e], y[e] * si[e]);
         }
-      }
-      if (PAIRING == kHalvesOdd) __syncwarp();  // (q_out may be q: other lanes' reads come first)
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int s = slot[u];
-        if (s >= 0 && s < p.q_heads) {
-          char* to = p.q_out + (row * p.o_row + s * p.o_head + d0) * ES;
-          store8<ES>(to, rotated[u] ? round8<ES>(x[u]) : raw[u], wide);
-        }
+        if (s >= 0 && s < p.q_heads)
+          store8<ES>(p.q_out + (row * p.o_row + s * p.o_head + d0) * ES, rotated ? round8<ES>(x) : raw[u], wide);
         if ((pass0 + u) * heads + heads <= p.q_heads) continue;  // (a pass of queries alone)
         const bool is_v = s >= p.q_heads + p.kv_heads;
         const int head = is_v ? s - p.q_heads - p.kv_heads : s - p.q_heads;
         if constexpr (!kPacked) {
-          if (s >= p.q_heads && place.page >= 0) {
-            char* to = (is_v ? c.v : c.k) +
-                       (place.page * c.page_stride + place.in * c.slot_stride + head * c.head_stride + d0) * ES;
-            store8<ES>(to, rotated[u] ? round8<ES>(x[u]) : raw[u], wide);
-          }
+          if (s >= p.q_heads && place.page >= 0)
+            store8<ES>((is_v ? c.v : c.k) +
+                           (place.page * c.page_stride + place.in * c.slot_stride + head * c.head_stride + d0) * ES,
+                       rotated ? round8<ES>(x) : raw[u], wide);
         } else {
           float top = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (s >= p.q_heads && !(fabsf(x[u][e]) < kInfF)) odd = kStNonFinite;
-            x[u][e] = x[u][e] == x[u][e] ? fminf(fmaxf(x[u][e], -61440.0f), 61440.0f) : 0.0f;
-            top = fmaxf(top, fabsf(x[u][e]));
+            if (s >= p.q_heads && !(fabsf(x[e]) < kInfF)) odd = kStNonFinite;
+            x[e] = x[e] == x[e] ? fminf(fmaxf(x[e], -61440.0f), 61440.0f) : 0.0f;
+            top = fmaxf(top, fabsf(x[e]));
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // (a head's lanes are a multiple of four)
           const uint32_t byte = scale_byte(top);
           const float scale = scale_value(byte), inv = byte ? 1.0f / scale : 0.0f;
-          float quot[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) quot[e] = scaled(x[u][e], scale, inv);
-          const uint32_t codes = pack_codes(quot);
+          for (int e = 0; e < 8; ++e) x[e] = scaled(x[e], scale, inv);
+          const uint32_t codes = pack_codes(x);
           if (s >= p.q_heads && place.page >= 0) {
             char* block = c.data + place.page * c.page_stride + head * c.head_stride;
             const int v_codes = packed_v_codes(c.page_size, c.head_dim);
