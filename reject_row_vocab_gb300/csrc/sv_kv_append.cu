@@ -74,15 +74,39 @@ __device__ __noinline__ float2 turn_by_far(int64_t position, float f) {
   return turn_of(hi, static_cast<float>(t - hi));
 }
 
+// Eight values of a row as they lie, and as pairs of floats.
 template <int ES>
-struct Eight {  // eight values of a row
+struct Eight {
   uint32_t w[ES * 2];
 };
+struct Pairs {
+  uint64_t v[4];
+};
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 template <int ES>
-__device__ __forceinline__ float value_of(const Eight<ES>& e, int i) {
-  if (ES == 4) return __uint_as_float(e.w[i]);
-  return i & 1 ? bf16_hi(e.w[i >> 1]) : bf16_lo(e.w[i >> 1]);
+__device__ __forceinline__ Pairs pairs_of(const Eight<ES>& e) {
+  Pairs p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p.v[i] = ES == 4 ? pair(__uint_as_float(e.w[ES * i / 2]), __uint_as_float(e.w[ES * i / 2 + 1])) : pair(bf16_lo(e.w[i]), bf16_hi(e.w[i]));
+  return p;
 }
 
 template <int ES>
@@ -105,16 +129,52 @@ __device__ __forceinline__ void store8(char* p, const Eight<ES>& e, bool second)
 }
 
 template <int ES>
-__device__ __forceinline__ Eight<ES> round8(const float (&x)[8]) {
+__device__ __forceinline__ Eight<ES> round8(const Pairs& x) {
   Eight<ES> e;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpair(x.v[i], lo, hi);
     if (ES == 4)
-      e.w[i] = __float_as_uint(x[i]);
-    else if (i % 2 == 0)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(e.w[i / 2]) : "f"(x[i + 1]), "f"(x[i]));
+      e.w[ES * i / 2] = __float_as_uint(lo), e.w[ES * i / 2 + 1] = __float_as_uint(hi);
+    else
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(e.w[i]) : "f"(hi), "f"(lo));
+  }
   return e;
 }
+
+// Eight values (of a head's lanes, a multiple of four, all of them) into the 4-bit cache: codes, scale; whether all are finite.
+__device__ __forceinline__ bool quantize8(const Pairs& x, uint32_t* codes, uint32_t* byte) {
+  float v[8], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(x.v[i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmax_nan(top, fabsf(v[e]));
+  const bool fine = top < kInfF;
+  if (!fine) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] == v[e] ? v[e] : 0.0f;
+  }
+  if (!(top <= 61440.0f)) {
+    top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(v[e], -61440.0f), 61440.0f), top = fmaxf(top, fabsf(v[e]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  *byte = scale_byte(top);
+  const float scale = scale_value(*byte), inv = *byte ? __frcp_rn(scale) : 0.0f;
+  // quotients, corrected by their remainders (see scaled())
+  const uint64_t s2 = pair(-scale, -scale), i2 = pair(inv, inv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t y = pair(v[2 * i], v[2 * i + 1]), a = mul_pair(y, i2);
+    unpair(fma_pair(fma_pair(a, s2, y), i2, a), v[2 * i], v[2 * i + 1]);
+  }
+  *codes = pack_codes(v);
+  return fine;
+}
+
+enum Part { kQuery, kKey, kValue };
 
 template <int ES, class C, Pairing PAIRING>
 __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const AppendParams p, const C c) {
@@ -123,10 +183,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = (p.dim + 7) / 8, heads = 32 / lanes;  // lanes of a head, heads of a pass
   const int of = lane / lanes, d0 = (lane - of * lanes) * 8;
-  const int slots = p.q_heads + 2 * p.kv_heads;
   const bool wide = ES == 2 || d0 + 4 < p.dim;  // the lane's second 16 bytes exist
   const int n = p.pairs;
-  const bool turned = d0 < 2 * n;  // some of the lane's columns are rotated
+  const bool turned = d0 < 2 * n;                                         // some of the lane's columns are rotated
+  const int partner = (d0 < n ? lane + n / 8 : turned ? lane - n / 8 : lane) & 31;  // lane of the pairs' other halves
+  const int q_passes = (p.q_heads + heads - 1) / heads, kv_passes = (p.kv_heads + heads - 1) / heads;
   grid_dependency_wait();
   allow_dependents();
   const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -136,28 +197,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
     const int64_t row = p.chunks == 1 ? item : item / p.chunks;
     const int chunk = static_cast<int>(item - row * p.chunks);
     const int first = chunk * p.per, last = min(first + p.per, p.passes);
-    // The lane's columns of a pass: the address, and which head (a query's, then the keys', then the values').
-    auto from = [&](int pass, int* slot) -> const char* {
-      const int s = pass * heads + of;
-      *slot = of < heads && pass < last && s < slots ? s : -1;
-      if (*slot < 0) return nullptr;
-      const HeadRows& h = s < p.q_heads ? p.q : s < p.q_heads + p.kv_heads ? p.k : p.v;
-      const int head = s < p.q_heads ? s : s < p.q_heads + p.kv_heads ? s - p.q_heads : s - p.q_heads - p.kv_heads;
-      return h.p + (row * h.row + head * h.head + d0) * ES;
-    };
-    Eight<ES> raw[kUnroll];
-    int slot[kUnroll];
-    const char* at[kUnroll];
-    auto load = [&](int pass0) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        at[u] = from(pass0 + u, &slot[u]);
-        load8<ES>(raw[u], at[u], slot[u] >= 0, slot[u] >= 0 && wide);
-      }
-    };
-    load(first);  // (on its way while the row's place is looked up, like the frequencies)
-    float freq[kMaxPairs / 32];
-    const bool turns = n > 0 && first * heads < p.q_heads + p.kv_heads;
+    const bool turns = n > 0 && first < q_passes + kv_passes;
+    float freq[kMaxPairs / 32];  // (on their way while the row's place is looked up)
 #pragma unroll
     for (int i = 0; i < kMaxPairs / 32; ++i) freq[i] = turns && i * 32 + lane < n ? p.inv_freq[i * 32 + lane] : 0.0f;
     int j;
@@ -167,7 +208,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
     if (len < 0) continue;
     const Place place = p.r.row_slots ? slot_place(c, p.r.row_slots[row]) : position_place(c, b, len + j);
     if (place.page < 0 && chunk == 0 && lane == 0) atomicOr(p.status + b, kStSlotRange);
-    float co[8], si[8];
+    Pairs co, si;
     if (turns) {
       const int64_t pos = p.positions ? p.positions[row] : len + j;
       const bool far = pos <= -(1 << 22) || pos >= 1 << 22;
@@ -177,94 +218,129 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
       __syncwarp();
       if (turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = d0 + e;
-          const bool high = PAIRING == kNeighbours ? e & 1 : d >= n;  // the pair's second column
-          int i = PAIRING == kNeighbours ? d / 2 : high ? d - n : d;
-          if (i >= n) i = 0;  // (a column that is left as it is)
-          const float2 t = s_turn[warp][i];
-          co[e] = t.x * p.magnitude, si[e] = (high ? t.y : -t.y) * p.magnitude;
+        for (int e = 0; e < 8; e += 2) {
+          float2 t[2];
+          float sign[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int d = d0 + e + f;
+            const bool high = PAIRING == kNeighbours ? f : d >= n;  // the pair's second column
+            int i = PAIRING == kNeighbours ? d / 2 : high ? d - n : d;
+            if (i >= n) i = 0;  // (a column that is left as it is)
+            t[f] = s_turn[warp][i];
+            sign[f] = high ? p.magnitude : -p.magnitude;
+          }
+          co.v[e / 2] = pair(t[0].x * p.magnitude, t[1].x * p.magnitude);
+          si.v[e / 2] = pair(t[0].y * sign[0], t[1].y * sign[1]);
         }
       }
       __syncwarp();
     }
-    uint32_t odd = 0u;  // a value that is not finite went into the 4-bit cache
-    for (int pass0 = first; pass0 < last; pass0 += kUnroll) {
-      if (pass0 > first) load(pass0);
+    bool odd = false;  // a value that is not finite went into the 4-bit cache
+    // Passes [lo, hi) over the heads of one part, `steps` bytes of a source's pass and of its destination's apart.
+    auto part = [&](auto which, int lo, int hi, const HeadRows& from, int total) {
+      constexpr Part kPart = decltype(which)::value;
+      constexpr bool kInto = kPart != kQuery;  // into the cache
+      lo = max(lo, 0);
+      if (lo >= hi || (kInto && place.page < 0)) return;
+      const int head0 = lo * heads + of;
+      const char* src = from.p + (row * from.row + head0 * from.head + d0) * ES;
+      const int64_t src_step = heads * from.head * ES;
+      char* dst;
+      int64_t dst_step;
+      int scale_at = 0;
+      if constexpr (!kInto) {
+        dst = p.q_out + (row * p.o_row + head0 * p.o_head + d0) * ES, dst_step = heads * p.o_head * ES;
+      } else if constexpr (!kPacked) {
+        dst = (kPart == kValue ? c.v : c.k) +
+              (place.page * c.page_stride + place.in * c.slot_stride + head0 * c.head_stride + d0) * ES;
+        dst_step = heads * c.head_stride * ES;
+      } else {
+        const int codes = (kPart == kValue ? packed_v_codes(c.page_size, c.head_dim) : 0) + place.in * (c.head_dim / 2) + d0 / 2;
+        scale_at = (kPart == kValue ? packed_v_scales(c.page_size, c.head_dim) : packed_k_scales(c.page_size, c.head_dim)) +
+                   place.in * (c.head_dim / 16) + d0 / 16 - codes;
+        dst = c.data + place.page * c.page_stride + head0 * c.head_stride + codes, dst_step = heads * c.head_stride;
+      }
+      const int live = of < heads ? (total - of + heads - 1) / heads : 0;  // passes in which this lane has a head
+      for (int pass0 = lo; pass0 < hi; pass0 += kUnroll) {
+        Eight<ES> raw[kUnroll];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int s = slot[u];
-        const bool rotated = turned && s >= 0 && s < p.q_heads + p.kv_heads;
-        float x[8], y[8];
-        if (PAIRING == kHalves) {
-          Eight<ES> other;
-          const int step = n / 8, at_lane = d0 < n ? lane + step : d0 < 2 * n ? lane - step : lane;
-#pragma unroll
-          for (int i = 0; i < ES * 2; ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[u].w[i], at_lane & 31);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = value_of<ES>(other, e);
+        for (int u = 0; u < kUnroll; ++u) {
+          const bool have = pass0 + u < min(hi, live);
+          load8<ES>(raw[u], src + u * src_step, have, have && wide);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = value_of<ES>(raw[u], e);
-          if (PAIRING == kNeighbours) y[e] = value_of<ES>(raw[u], e ^ 1);
-        }
-        if (PAIRING == kHalvesOdd) {
-          if (rotated) {
+        for (int u = 0; u < kUnroll; ++u) {
+          if (pass0 + u >= hi) break;
+          const bool have = pass0 + u < live;
+          Eight<ES> out = raw[u];
+          Pairs x;
+          if (kPart != kValue || (kPacked && kInto)) x = pairs_of(raw[u]);
+          if (kPart != kValue && n > 0) {
+            Pairs y = x;
+            if (PAIRING == kHalves) {
+              Eight<ES> other;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int d = d0 + e;
-              y[e] = 0.0f;
-              if (d < 2 * n) {
-                const char* o = at[u] + (d < n ? n + e : e - n) * ES;
-                y[e] = ES == 4 ? *reinterpret_cast<const float*>(o)
-                               : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(o)) << 16);
+              for (int i = 0; i < ES * 2; ++i) other.w[i] = __shfl_sync(0xffffffffu, raw[u].w[i], partner);
+              y = pairs_of(other);
+            } else if (PAIRING == kNeighbours) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float lo_, hi_;
+                unpair(x.v[i], lo_, hi_);
+                y.v[i] = pair(hi_, lo_);
               }
+            } else {
+              if (turned && have) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int d = d0 + e;
+                  f[e] = 0.0f;
+                  if (d < 2 * n) {
+                    const char* o = src + u * src_step + (d < n ? n + e : e - n) * ES;
+                    f[e] = ES == 4 ? *reinterpret_cast<const float*>(o)
+                                   : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(o)) << 16);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y.v[i] = pair(f[2 * i], f[2 * i + 1]);
+              }
+              __syncwarp();  // (q_out may be q: other lanes' reads of the head come first)
+            }
+            if (turned) {
+              const Pairs was = x;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x.v[i] = fma_pair(x.v[i], co.v[i], mul_pair(y.v[i], si.v[i]));
+              if (2 * n - d0 < 8) {  // columns behind the last pair are left as they are
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float a0, a1, b0, b1;
+                  unpair(x.v[i], a0, a1), unpair(was.v[i], b0, b1);
+                  x.v[i] = pair(d0 + 2 * i < 2 * n ? a0 : b0, d0 + 2 * i + 1 < 2 * n ? a1 : b1);
+                }
+              }
+              if (!kPacked || !kInto) out = round8<ES>(x);
             }
           }
-          __syncwarp();  // (q_out may be q: other lanes' reads of the head come first)
-        }
-        if (rotated) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (d0 + e < 2 * n) x[e] = fmaf(x[e], co[e], y[e] * si[e]);
-        }
-        if (s >= 0 && s < p.q_heads)
-          store8<ES>(p.q_out + (row * p.o_row + s * p.o_head + d0) * ES, rotated ? round8<ES>(x) : raw[u], wide);
-        if ((pass0 + u) * heads + heads <= p.q_heads) continue;  // (a pass of queries alone)
-        const bool is_v = s >= p.q_heads + p.kv_heads;
-        const int head = is_v ? s - p.q_heads - p.kv_heads : s - p.q_heads;
-        if constexpr (!kPacked) {
-          if (s >= p.q_heads && place.page >= 0)
-            store8<ES>((is_v ? c.v : c.k) +
-                           (place.page * c.page_stride + place.in * c.slot_stride + head * c.head_stride + d0) * ES,
-                       rotated ? round8<ES>(x) : raw[u], wide);
-        } else {
-          float top = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (s >= p.q_heads && !(fabsf(x[e]) < kInfF)) odd = kStNonFinite;
-            x[e] = x[e] == x[e] ? fminf(fmaxf(x[e], -61440.0f), 61440.0f) : 0.0f;
-            top = fmaxf(top, fabsf(x[e]));
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // (a head's lanes are a multiple of four)
-          const uint32_t byte = scale_byte(top);
-          const float scale = scale_value(byte), inv = byte ? 1.0f / scale : 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = scaled(x[e], scale, inv);
-          const uint32_t codes = pack_codes(x);
-          if (s >= p.q_heads && place.page >= 0) {
-            char* block = c.data + place.page * c.page_stride + head * c.head_stride;
-            const int v_codes = packed_v_codes(c.page_size, c.head_dim);
-            *reinterpret_cast<uint32_t*>(block + (is_v ? v_codes : 0) + place.in * (c.head_dim / 2) + d0 / 2) = codes;
-            if ((lane & 1) == 0)
-              block[(is_v ? packed_v_scales(c.page_size, c.head_dim) : packed_k_scales(c.page_size, c.head_dim)) +
-                    place.in * (c.head_dim / 16) + d0 / 16] = static_cast<char>(byte);
+          if constexpr (kPacked && kInto) {
+            uint32_t codes, byte;
+            odd = !quantize8(x, &codes, &byte) && have || odd;
+            if (have) {
+              *reinterpret_cast<uint32_t*>(dst + u * dst_step) = codes;
+              if ((lane & 1) == 0) dst[u * dst_step + scale_at] = static_cast<char>(byte);
+            }
+          } else {
+            if (have) store8<ES>(dst + u * dst_step, out, wide);
           }
         }
+        src += kUnroll * src_step, dst += kUnroll * dst_step;
       }
-    }
-    if (kPacked && place.page >= 0 && __any_sync(0xffffffffu, odd != 0u) && lane == 0) atomicOr(p.status + b, kStNonFinite);
+    };
+    part(std::integral_constant<Part, kQuery>{}, first, min(last, q_passes), p.q, p.q_heads);
+    part(std::integral_constant<Part, kKey>{}, first - q_passes, min(last - q_passes, kv_passes), p.k, p.kv_heads);
+    part(std::integral_constant<Part, kValue>{}, first - q_passes - kv_passes, min(last - q_passes - kv_passes, kv_passes), p.v, p.kv_heads);
+    if (kPacked && __any_sync(0xffffffffu, odd) && lane == 0) atomicOr(p.status + b, kStNonFinite);
   }
 }
 
@@ -379,7 +455,7 @@ sv_status_t append_entry(C c, int es, int32_t layer, const sv_rows_t* rows, cons
   if (e != cudaSuccess) return cuda_failure(e);
   to_layer(&c, layer);
   const int lanes = (c.head_dim + 7) / 8, heads = 32 / lanes;
-  const int64_t passes = (num_heads + 2 * static_cast<int64_t>(c.heads) + heads - 1) / heads;
+  const int64_t passes = (num_heads + heads - 1) / heads + 2 * static_cast<int64_t>((c.heads + heads - 1) / heads);
   // As many warps a row as it takes to give every multiprocessor sixteen.
   const int64_t count = rows_count(r), want = 16 * static_cast<int64_t>(dev.sms);
   int64_t chunks = (want + count - 1) / count;
