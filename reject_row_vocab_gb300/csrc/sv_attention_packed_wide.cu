@@ -11,8 +11,10 @@
 // rounding, 2^-12, is below that of the output).
 //
 // A tile's bytes come by bulk copies (sv_attention_packed.cuh), some tiles ahead.
-// Heads of more than 128 columns have no room for that: there the unpacking warps
-// fetch a tile ahead into registers.
+// Heads of more than 128 columns have no room for that, and pages of one or two
+// entries no blocks worth a copy: there the unpacking warps fetch a tile ahead into
+// registers (trees of 16 requests in pages of one slot: 24 us, by way of shared
+// memory 41; 64 blocks of 16 rows in pages of 64 the other way round, 137 and 109).
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include "sv_attention_packed.cuh"
@@ -298,6 +300,10 @@ struct HalfSource {
 cudaError_t launch_packed_attention_wide(const AttnParams& p, const PackedView& c, const DeviceInfo& dev, cudaStream_t stream) {
   const PackedTiles tiles = packed_tiles(c);
   const int dim = c.head_dim;
+  if (tiles.copies == 0 || tiles.rows_log < 2)
+    return dim <= 64    ? launch_wide<1, 1, HalfSource<false>>(p, tiles, dev, stream)
+           : dim <= 128 ? launch_wide<2, 1, HalfSource<false>>(p, tiles, dev, stream)
+                        : launch_wide<2, 2, HalfSource<false>>(p, tiles, dev, stream);
   return dim <= 64    ? launch_wide<1, 1, HalfSource<true>>(p, tiles, dev, stream)
          : dim <= 128 ? launch_wide<2, 1, HalfSource<true>>(p, tiles, dev, stream)
                       : launch_wide<2, 2, HalfSource<false>>(p, tiles, dev, stream);

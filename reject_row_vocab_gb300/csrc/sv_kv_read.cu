@@ -4,8 +4,8 @@
 // a look at the cache needs; [E2D] §5.6.6: the committed slots.)
 //
 // Bound by the bytes of the output.  A warp takes one row, or a part of its
-// heads and layers; a lane has eight columns of a head: 16 bytes of bf16, four
-// bytes of codes.
+// heads and layers; a lane has eight columns of a head, or, of codes, a group of
+// 16 with its scale.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>
@@ -28,14 +28,19 @@ struct ReadParams {
   int32_t passes, chunks, per;
 };
 
+// Columns of a lane: of the 4-bit cache a group's (8 bytes of codes and its scale), else eight.
+template <class C>
+constexpr int kLaneCols = std::is_same<C, PackedView>::value ? 16 : 8;
+
 template <int ES, class C>
 __global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const ReadParams p, const C c) {
   constexpr bool kPacked = std::is_same<C, PackedView>::value;
+  constexpr int kCols = kLaneCols<C>, kPieces = kCols * ES / 16;  // 16-byte pieces of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lanes = (p.dim + 7) / 8, heads = 32 / lanes;
-  const int of = lane / lanes, d0 = (lane - of * lanes) * 8;
-  const bool wide = ES == 2 || d0 + 4 < p.dim;
-  const int slots = p.layers * 2 * p.heads;
+  const int lanes = (p.dim + kCols - 1) / kCols, heads = 32 / lanes;
+  const int of = lane / lanes, d0 = (lane - of * lanes) * kCols;
+  const int live = of < heads ? (p.heads - of + heads - 1) / heads : 0;  // passes over the heads in which this lane has one
+  const int rounds = (p.heads + heads - 1) / heads;                      // passes over the heads
   grid_dependency_wait();
   allow_dependents();
   const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -53,62 +58,77 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const ReadParams p,
     const bool there = place.page >= 0;
     if (!there && chunk == 0 && lane == 0) atomicOr(p.status + b, kStSlotRange);
     const int first = chunk * p.per, last = min(first + p.per, p.passes);
+    // This lane's columns of head `of` of layer 0: in K's memory and V's, and in the outputs.
+    const char *from[2] = {nullptr, nullptr}, *scale[2] = {nullptr, nullptr};
+    int64_t layer_step, head_step;
+    if constexpr (kPacked) {
+      const char* block = c.data + static_cast<int64_t>(there ? place.page : 0) * c.page_stride + of * c.head_stride;
+      const int code = place.in * (c.head_dim / 2) + d0 / 2, group = place.in * (c.head_dim / 16) + d0 / 16;
+      from[0] = block + code, from[1] = from[0] + packed_v_codes(c.page_size, c.head_dim);
+      scale[0] = block + packed_k_scales(c.page_size, c.head_dim) + group;
+      scale[1] = block + packed_v_scales(c.page_size, c.head_dim) + group;
+      layer_step = c.layer_stride, head_step = heads * c.head_stride;
+    } else {
+      const int64_t at = (static_cast<int64_t>(there ? place.page : 0) * c.page_stride + place.in * c.slot_stride + of * c.head_stride + d0) * ES;
+      from[0] = c.k + at, from[1] = c.v + at;
+      layer_step = c.layer_stride * ES, head_step = heads * c.head_stride * ES;
+    }
+    const int64_t out_at = (row * p.o_row + of * p.o_head + d0) * ES, out_layer = p.o_layer * ES, out_head = heads * p.o_head * ES;
+    // A pass is a round over the heads of K or V of a layer.
+    int layer = first / (2 * rounds), round = first - layer * 2 * rounds, which = round >= rounds ? 1 : 0;
+    round -= which * rounds;
     for (int pass0 = first; pass0 < last; pass0 += kReadUnroll) {
-      uint4 a[kReadUnroll], a2[kReadUnroll];
-      uint32_t code[kReadUnroll], byte[kReadUnroll];
+      uint4 a[kReadUnroll][kPieces];
+      uint2 code[kReadUnroll];
+      uint32_t byte[kReadUnroll];
       char* to[kReadUnroll];
 #pragma unroll
       for (int u = 0; u < kReadUnroll; ++u) {
-        const int s = (pass0 + u) * heads + of;
-        to[u] = nullptr;
-        a[u] = a2[u] = make_uint4(0u, 0u, 0u, 0u);
-        code[u] = byte[u] = 0u;
-        if (of >= heads || pass0 + u >= last || s >= slots) continue;
-        const int which = s / p.heads, head = s - which * p.heads, layer = which >> 1;
-        const bool is_v = which & 1;
-        to[u] = (is_v ? p.v : p.k) + (layer * p.o_layer + row * p.o_row + head * p.o_head + d0) * ES;
-        if (!there) continue;
-        if constexpr (kPacked) {
-          const char* block = c.data + layer * c.layer_stride + place.page * c.page_stride + head * c.head_stride;
-          code[u] = *reinterpret_cast<const uint32_t*>(block + (is_v ? packed_v_codes(c.page_size, c.head_dim) : 0) +
-                                                       place.in * (c.head_dim / 2) + d0 / 2);
-          byte[u] = static_cast<unsigned char>(
-              block[(is_v ? packed_v_scales(c.page_size, c.head_dim) : packed_k_scales(c.page_size, c.head_dim)) +
-                    place.in * (c.head_dim / 16) + d0 / 16]);
-        } else {
-          const char* at = (is_v ? c.v : c.k) +
-                           (layer * c.layer_stride + place.page * c.page_stride + place.in * c.slot_stride +
-                            head * c.head_stride + d0) * ES;
-          a[u] = *reinterpret_cast<const uint4*>(at);
-          if (ES == 4 && wide) a2[u] = *reinterpret_cast<const uint4*>(at + 16);
+        const bool have = pass0 + u < last && round < live;
+        to[u] = have ? (which ? p.v : p.k) + out_at + layer * out_layer + round * out_head : nullptr;
+        code[u] = make_uint2(0u, 0u), byte[u] = 0u;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) a[u][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (have && there) {
+          const int64_t at = layer * layer_step + round * head_step;
+          const char* f = (which ? from[1] : from[0]) + at;
+          if constexpr (kPacked) {
+            code[u] = *reinterpret_cast<const uint2*>(f);
+            byte[u] = static_cast<unsigned char>((which ? scale[1] : scale[0])[at]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+              if (d0 * ES + i * 16 < p.dim * ES) a[u][i] = *reinterpret_cast<const uint4*>(f + i * 16);
+          }
         }
+        if (++round == rounds) round = 0, which ^= 1, layer += which ^ 1;
       }
 #pragma unroll
       for (int u = 0; u < kReadUnroll; ++u) {
         if (!to[u]) continue;
         if constexpr (kPacked) {
-          uint32_t h[4];
-          unpack_codes(code[u], h);
           const uint32_t s2 = scale_pair(byte[u] | byte[u] << 16);
-          float x[8];
+          uint32_t w[kCols * ES / 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v = mul_half2(h[i], s2);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t f[4];
+            unpack_codes(h ? code[u].y : code[u].x, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t v = mul_half2(f[i], s2);
+              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v));
+              if (ES == 4)
+                w[(h * 4 + i) * ES / 2] = __float_as_uint(x.x), w[(h * 4 + i) * ES / 2 + 1] = __float_as_uint(x.y);
+              else
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h * 4 + i]) : "f"(x.y), "f"(x.x));
+            }
           }
-          uint32_t w[ES * 2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (ES == 4)
-              w[i] = __float_as_uint(x[i]);
-            else if (i % 2 == 0)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i / 2]) : "f"(x[i + 1]), "f"(x[i]));
-          a[u] = make_uint4(w[0], w[1], w[2], w[3]);
-          if (ES == 4) a2[u] = make_uint4(w[ES * 2 - 4], w[ES * 2 - 3], w[ES * 2 - 2], w[ES * 2 - 1]);
+          for (int i = 0; i < kPieces; ++i) a[u][i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
-        *reinterpret_cast<uint4*>(to[u]) = a[u];
-        if (ES == 4 && wide) *reinterpret_cast<uint4*>(to[u] + 16) = a2[u];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (d0 * ES + i * 16 < p.dim * ES) *reinterpret_cast<uint4*>(to[u] + i * 16) = a[u][i];
       }
     }
   }
@@ -157,8 +177,8 @@ sv_status_t read_entry(C c, int es, int32_t layer, int32_t num_layers, const sv_
   cudaError_t e = device_info(&dev);
   if (e != cudaSuccess) return cuda_failure(e);
   to_layer(&c, layer);
-  const int lanes = (c.head_dim + 7) / 8, heads = 32 / lanes;
-  const int64_t passes = (static_cast<int64_t>(num_layers) * 2 * c.heads + heads - 1) / heads;
+  const int lanes = (c.head_dim + kLaneCols<C> - 1) / kLaneCols<C>, heads = 32 / lanes;
+  const int64_t passes = static_cast<int64_t>(num_layers) * 2 * ((c.heads + heads - 1) / heads);
   const int64_t count = rows_count(r), want = 32 * static_cast<int64_t>(dev.sms);
   int64_t chunks = (want + count - 1) / count;
   chunks = chunks > passes ? passes : chunks;

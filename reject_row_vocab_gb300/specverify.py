@@ -599,8 +599,11 @@ class _OtherDevice:
         return False
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on_device(index):
-    return _CURRENT if index < 0 or torch.cuda.current_device() == index else _OtherDevice(index)
+    return _CURRENT if index < 0 or _current_device() == index else _OtherDevice(index)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -876,16 +879,15 @@ class Rotation:
             raise ValueError("inv_freq must be a 1-D torch tensor")
         _arg(inv_freq, "inv_freq", torch.float32, 0, inv_freq.device)
         self.inv_freq, self.pairs, self.interleaved, self.magnitude = inv_freq, inv_freq.numel(), interleaved, magnitude
+        self.index = inv_freq.get_device()
         self.struct = SvRotation(inv_freq.data_ptr(), self.pairs, 1 if interleaved else 0, magnitude)
         self.ref = ctypes.byref(self.struct)
 
 
-def _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots):
-    """The rows of a call on a cache: checks their arrays; returns the batch and the library's description.  rows None: as many
-    as the requests have."""
+def _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots, positions=None):
+    """The rows of a call on a cache: checks their arrays; returns the batch, the rows and the library's description.  rows None:
+    as many as the requests have."""
     dev, index = cache.device, cache.index
-    if seq_lens is not None:
-        _need(seq_lens, "seq_lens", torch.int64, 0, dev, index)
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", torch.int32, 1, dev, index)
         batch = cu_seqlens.numel() - 1
@@ -893,9 +895,8 @@ def _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots):
             raise ValueError("max_len is required with cu_seqlens")
         if rows is None:
             raise ValueError("rows is required with cu_seqlens")
-        if seq_lens is not None:
-            _need(seq_lens, "seq_lens", torch.int64, batch, dev, index)
     elif seq_lens is not None:
+        _need(seq_lens, "seq_lens", torch.int64, 0, dev, index)
         batch = seq_lens.numel()
         if max_len is None:
             if rows is None:
@@ -903,6 +904,10 @@ def _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots):
             if batch and (rows % batch or not rows):
                 raise ValueError("%d rows do not divide among %d requests: max_len is required" % (rows, batch))
             max_len = rows // batch if batch else 1
+        if rows is None:
+            rows = batch * max_len
+        elif rows < batch * max_len:
+            raise ValueError("there are %d rows; the call reads %d" % (rows, batch * max_len))
     else:
         if rows is None:
             raise ValueError("seq_lens or cu_seqlens is required")
@@ -910,18 +915,16 @@ def _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots):
         if max_len < 1 or rows % max_len:
             raise ValueError("%d rows are no whole number of requests of %d" % (rows, max_len))
         batch = rows // max_len
-    if rows is None:
-        rows = batch * max_len
-    if cu_seqlens is None and rows < batch * max_len:
-        raise ValueError("there are %d rows; the call reads %d" % (rows, batch * max_len))
-    if row_slots is not None:
-        _need(row_slots, "row_slots", torch.int64, rows, dev, index)
-    else:
+    _need_all(((seq_lens, "seq_lens", batch), (row_slots, "row_slots", rows), (positions, "positions", rows)), torch.int64, dev,
+              index)
+    if row_slots is None:
         if seq_lens is None:
             raise ValueError("seq_lens is required without row_slots")
         if cache.batch < batch:
             raise ValueError("page_table has %d rows; the call reads %d" % (cache.batch, batch))
-    return batch, rows, SvRows(batch, max_len, rows, _addr(cu_seqlens), _addr(seq_lens), _addr(row_slots))
+    return batch, rows, SvRows(batch, max_len, rows, None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                               None if seq_lens is None else seq_lens.data_ptr(),
+                               None if row_slots is None else row_slots.data_ptr())
 
 
 @dataclass
@@ -954,10 +957,8 @@ def kv_append(cache, k, v, *, layer: int = 0, seq_lens=None, max_len: Optional[i
     rows, dim = k.shape[0], cache.head_dim
     ks = _head_rows(k, "k", rows, cache.heads, dim, cache.dtype, dev, index)
     vs = _head_rows(v, "v", rows, cache.heads, dim, cache.dtype, dev, index)
-    batch, _, desc = _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots)
-    if positions is not None:
-        _need(positions, "positions", torch.int64, rows, dev, index)
-    elif rotation is not None and seq_lens is None:
+    batch, _, desc = _cache_rows(cache, rows, seq_lens, max_len, cu_seqlens, row_slots, positions)
+    if positions is None and rotation is not None and seq_lens is None:
         raise ValueError("positions are required without seq_lens")
     heads, qs, os = 0, (0, 0), (0, 0)
     if q is not None:
@@ -968,7 +969,7 @@ def kv_append(cache, k, v, *, layer: int = 0, seq_lens=None, max_len: Optional[i
     if rotation is not None:
         if not isinstance(rotation, Rotation):
             raise TypeError("rotation must be a Rotation")
-        if rotation.inv_freq.get_device() != index:
+        if rotation.index != index:
             raise ValueError("rotation is on %s; the call runs on %s (the cache's device)" % (rotation.inv_freq.device, dev))
     if out is None:
         with _on(stream):
@@ -1003,6 +1004,18 @@ class KvReadOutputs:
                              dev_status=torch.zeros(batch, dtype=torch.int32, device=d))
 
 
+def _layer_rows(t, name, layers, rows, cache):
+    """Checks t [layers, >= rows, heads, dim] of a cache; returns its layer, row and head strides."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != layers or layers < 1:
+        raise ValueError("%s must be [%d layers, rows, heads, head_dim]" % (name, layers))
+    _, n, h, d = t.shape
+    a, b, c, e = t.stride()
+    if not (t.dtype is cache.dtype and t.get_device() == cache.index and n >= rows and h == cache.heads and d == cache.head_dim
+            and (e == 1 or d == 1)):
+        _head_rows(t[0], name, rows, cache.heads, cache.head_dim, cache.dtype, cache.device, cache.index)
+    return (a if layers > 1 else 0), (b if n > 1 else 0), (c if h > 1 else 0)
+
+
 def kv_read(cache, *, layer: Optional[int] = None, seq_lens=None, max_len: Optional[int] = None, cu_seqlens=None,
             row_slots=None, rows: Optional[int] = None, out=None, stream=None) -> KvReadOutputs:
     """The cache's entries of the given rows' places (as kv_append places rows) as dense rows of the cache's dtype: of one
@@ -1025,27 +1038,19 @@ def kv_read(cache, *, layer: Optional[int] = None, seq_lens=None, max_len: Optio
         with _on(stream):
             out = KvReadOutputs.allocate(rows, cache.heads, cache.head_dim, batch, cache.dtype, dev,
                                          layers if layer is None else None)
-    ks, vs = out.k, out.v
     if layer is None:
-        for t, name in ((ks, "out.k"), (vs, "out.v")):
-            if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[0] != layers:
-                raise ValueError("%s must be [%d layers, rows, heads, head_dim]" % (name, layers))
-        step = ks.stride(0) if layers > 1 else 0
-        if layers > 1 and vs.stride(0) != step:
-            raise ValueError("out.k and out.v must have the same strides")
-        if layers < 1:
-            raise ValueError("the cache has no layers")
-        ks, vs = ks[0], vs[0]
+        st = _layer_rows(out.k, "out.k", layers, rows, cache)
+        same = _layer_rows(out.v, "out.v", layers, rows, cache) == st
     else:
-        step = 0
-    st = _head_rows(ks, "out.k", rows, cache.heads, cache.head_dim, cache.dtype, dev, index)
-    if _head_rows(vs, "out.v", rows, cache.heads, cache.head_dim, cache.dtype, dev, index) != st:
+        st = (0,) + _head_rows(out.k, "out.k", rows, cache.heads, cache.head_dim, cache.dtype, dev, index)
+        same = (0,) + _head_rows(out.v, "out.v", rows, cache.heads, cache.head_dim, cache.dtype, dev, index) == st
+    if not same:
         raise ValueError("out.k and out.v must have the same strides")
     _need(out.dev_status, "out.dev_status", torch.int32, batch, dev, index)
     fn = lib.spec_verify_packed_kv_read if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_read
     with _on_device(index):
         code = fn(cache.ref, 0 if layer is None else layer, layers, ctypes.byref(desc), out.k.data_ptr(), out.v.data_ptr(),
-                  step, st[0], st[1], out.dev_status.data_ptr(), _call_stream(stream, dev))
+                  st[0], st[1], st[2], out.dev_status.data_ptr(), _call_stream(stream, dev))
     if code:
         _check("spec_verify_packed_kv_read" if isinstance(cache, PackedKvCache) else "spec_verify_kv_read", code)
     return out
