@@ -5,16 +5,18 @@
 // Each unpacking warp has 16 keys of a tile; a lane has 32 columns of one key
 // in each block of 64: 16 bytes of codes, two scales, 64 bytes of half floats in
 // the swizzle that the matrix unit reads.  Its operands have one type, so the
-// queries are half floats too: the same warps bring each row of a unit's Q to
-// their range by a power of two, which the row's factor of the scores takes
-// back.  The weights are half floats, below 2^14 with the sums in fp32 (their
+// queries are half floats too: each row of a unit's Q is brought to their range by
+// a power of two, which the row's factor of the scores takes back (by the softmax
+// warps, to tensor memory; of heads of more than 128 columns, for which that has no
+// room, by the unpacking warps in shared memory).  The weights are half floats, below 2^14 with the sums in fp32 (their
 // rounding, 2^-12, is below that of the output).
 //
 // A tile's bytes come by bulk copies (sv_attention_packed.cuh), some tiles ahead.
 // Heads of more than 128 columns have no room for that, and pages of one or two
 // entries no blocks worth a copy: there the unpacking warps fetch a tile ahead into
 // registers (trees of 16 requests in pages of one slot: 24 us, by way of shared
-// memory 41; 64 blocks of 16 rows in pages of 64 the other way round, 137 and 109).
+// memory 41; 64 blocks of 16 rows in pages of 64 the other way round, 137 and 109,
+// both with Q in shared memory).
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include "sv_attention_packed.cuh"
@@ -54,21 +56,24 @@ struct HalfSource {
   static __host__ __device__ constexpr int entries() { return CB == 2 ? 4 : 8; }
   template <int CB, int H>
   using Stage = PackedStage<CB == 2 ? 3 : 4, 1, packed_tile_bytes(CB * 64 * H)>;
-  // The source's shared memory: the places, the rows' factors of the last eight units (the unpacking warps are at most six tiles
-  // ahead of the softmax warps: a tile of K needs the place of one four before it, whose product is issued behind the weights two
-  // before that), what threads of one row tell each other, the
-  // barriers of a converted Q and of a unit's end.
+  // The source's shared memory: the places; what threads of one row tell each other, and 8 KB through which the second thread's O
+  // goes to the first (where Q is in shared memory, its second copy is used for that); the rows' factors of the last eight
+  // units, where Q is in shared memory (the unpacking warps are at most six tiles ahead of the softmax warps: a tile of K needs the
+  // place of one four before it, whose product is issued behind the weights two before that); the barriers of a converted Q and
+  // of a unit's end.
   template <int CB, int H>
-  static __host__ __device__ constexpr int factors() { return STAGED ? Stage<CB, H>::kBytes : 0; }
+  static __host__ __device__ constexpr int pairs_at() { return STAGED ? Stage<CB, H>::kBytes : 0; }
   template <int CB, int H>
-  static __host__ __device__ constexpr int ready() { return factors<CB, H>() + 8 * kRows * 4 + kRows * 8; }
+  static __host__ __device__ constexpr int factors() { return pairs_at<CB, H>() + kRows * 8; }
+  template <int CB, int H>
+  static __host__ __device__ constexpr int ready() { return factors<CB, H>() + (H == 1 ? 64 * 128 : 8 * kRows * 4); }
   template <int CB, int H>
   static __host__ __device__ constexpr int extra_bytes() { return ready<CB, H>() + 16; }
 
   template <int CB, int H>
   static __device__ __forceinline__ void init(char* extra) {
     if constexpr (STAGED) Stage<CB, H>(extra).init(kUnpackWarps);
-    mbar_init(smem_addr(extra) + ready<CB, H>(), kUnpackWarps);
+    mbar_init(smem_addr(extra) + ready<CB, H>(), H == 1 ? kSoftmaxThreads : kUnpackWarps);
     mbar_init(unit_done<CB, H>(extra), kSoftmaxThreads);
   }
   template <int CB, int H>
@@ -81,13 +86,16 @@ struct HalfSource {
   }
   template <int CB, int H>
   static __device__ __forceinline__ float2* pairs(char* extra) {
-    return reinterpret_cast<float2*>(extra + factors<CB, H>() + 8 * kRows * 4);
+    return reinterpret_cast<float2*>(extra + pairs_at<CB, H>());
   }
-  // 8 KB each: the lower half of a block of Q's second copy, which is not used between a unit's last product and its end.
+  // Of H = 2 there are two places: the second copy's rows of two blocks of Q, which are not used between a unit's last product and its end.
   template <int CB, int H>
-  static __device__ __forceinline__ float4* exchange(char* q, int i) {
-    constexpr int kFar = CB * H > 1 ? kKeys * 128 : 0;
-    return reinterpret_cast<float4*>(q + 64 * 128 + i * kFar);
+  static __device__ __forceinline__ float4* exchange(char* q, char* extra, int i) {
+    return reinterpret_cast<float4*>(H == 1 ? extra + factors<CB, H>() : q + 64 * 128 + i * kKeys * 128);
+  }
+  static __device__ __forceinline__ float2 row_range(uint32_t top, float scale) {
+    const RowScale f = row_scale(top, scale);
+    return make_float2(f.up, f.factor);
   }
   template <int CB, int H>
   static __device__ __forceinline__ float row_factor(char* extra, uint32_t unit, int t) {
@@ -142,7 +150,7 @@ struct HalfSource {
       if (lw == kUnpackWarps)
         stage.load(ring, p, k, 0);
       else
-        unpack<CB, H>(ring, p, k, stage, q, extra, split, lw);
+        unpack<CB, H>(ring, k, stage, lw);
     } else {
       fetch<CB, H>(ring, p, k.c, q, extra, split, lw);
     }
@@ -150,10 +158,9 @@ struct HalfSource {
 
   // A tile from its place: K, then V.
   template <int CB, int H, class R, class S>
-  static __device__ __forceinline__ void unpack(R& ring, const AttnParams& p, const Args& k, const S& stage, char* q, char* extra, bool split,
-                                                int lw) {
+  static __device__ __forceinline__ void unpack(R& ring, const Args& k, const S& stage, int lw) {
     constexpr int kEntries = R::kEntries;
-    static_assert(H == 1, "one entry for K and one for V");
+    static_assert(H == 1, "one entry for K and one for V; Q is in tensor memory");
     const int lane = ring.lane, mine = lw * 16 + (lane >> 1);  // this lane's key of a tile
     const int dim = k.c.head_dim, in_block = (1 << k.rows_log) - 1, at_block = (mine >> k.rows_log) * k.block;
     const int code_at = at_block + (mine & in_block) * (dim / 2) + (lane & 1) * 16;
@@ -163,7 +170,7 @@ struct HalfSource {
     AttnSegment s;
     uint32_t g = 0;
     bool ok = true;
-    for (uint32_t unit = 0; ok && ring.next(s); ++unit) {
+    while (ok && ring.next(s)) {
 #pragma unroll 1
       for (int i = 0; i < s.cnt; ++i, ++g) {
         if (!ring.wait(stage.full(g), stage.phase(g))) {
@@ -203,8 +210,6 @@ struct HalfSource {
           __syncwarp();
           if (lane == 0) mbar_arrive(ring.full(entry));
         }
-        // (Q behind the first tile, which has not to wait for it)
-        if (ok && i == 0) ok = convert_q<CB, H>(ring, p, q, extra, s, unit, split, lw);
         if (!ok) break;
       }
     }
@@ -227,7 +232,7 @@ struct HalfSource {
     bool more = ring.next(s);
     int t = s.t0;
     uint32_t unit = 0;
-    bool ok = !more || convert_q<CB, H>(ring, p, q_mem, extra, s, unit, split, lw);
+    bool ok = H == 1 || !more || convert_q<CB, H>(ring, p, q_mem, extra, s, unit, split, lw);
     int64_t word = more ? key_word(p, s.r, s.b, t * kKeys + mine) : -1;
     auto ahead = [&](Tile& f) {  // the next tile's bytes; false behind the last tile
       if (!more || !ok) return false;
@@ -290,7 +295,7 @@ struct HalfSource {
         __syncwarp();
         if (lane == 0) mbar_arrive(ring.full(q));
       }
-      if (ok && turn) ok = convert_q<CB, H>(ring, p, q_mem, extra, s, ++unit, split, lw);
+      if (H > 1 && ok && turn) ok = convert_q<CB, H>(ring, p, q_mem, extra, s, ++unit, split, lw);
     }
   }
 };

@@ -171,6 +171,10 @@ struct KvRing {
     const AttnSegment* s = plan_slot(plans);
     return s->cnt > 0 ? s : nullptr;
   }
+  // Whether another segment follows the one that peek() gives.
+  __device__ bool another() const {
+    return wait(plan_bar(plans + 1), (plans + 1) / kPlans & 1) && plan_slot(plans + 1)->cnt > 0;
+  }
   __device__ void release() {
     __syncwarp();
     if (lane == 0) mbar_arrive(read_bar(plans));

@@ -105,7 +105,11 @@ struct Wide {
   static constexpr int kRing = Source::template entries<CB, H>();  // in the ring
   using R = KvRing<2, CB, kRing, H, kRing == 4>;
   static constexpr int kCols = CB * 64, kDP = kCols * H;
-  static constexpr int kS = 0, kO = 256;           // tensor memory columns: two S of 128, then O
+  static constexpr int kS = 0, kO = 256, kQ = kO + kDP;  // tensor memory columns: two S of 128, then O, and Q where there is room
+  // Half floats' Q lies in tensor memory, where a thread of the softmax warps writes its row: the products read it there instead of
+  // over the shared memory's bus, which limits, and it is written between a unit's last scores and its end.  (64 blocks of 16 rows
+  // over 4 bits: 100 us, Q converted in shared memory by the unpacking warps 109.)
+  static constexpr bool kTmemQ = Source::kHalf && H == 1;
   // shared memory: Q (as a tile's K), the ring, s, p, pv [2], soft, and tmem, careful [2]
   static constexpr int kQBytes = R::kTile * H;
   static constexpr int kBars = kQBytes + R::kBytes;
@@ -155,14 +159,16 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
   // Units of up to 64 rows have two Qs, one in each half of Q's rows: the products of the lower half read on into what
   // lies behind it, but rows past 64 are nobody's then.
   const bool small = p.max_len * static_cast<int64_t>(p.group) <= 64;
-  const int twins = small && !Source::kHalf ? 2 : 1;
-  // With half floats they have Q in both halves instead, and two threads a row: the second takes the tiles' upper 64 keys, with a
-  // reference, a sum and an O of its own (its weights of the lower keys are 0, as are the first one's of the upper); they are put
-  // together at the end of the unit.  (The softmax warps are what limits there; the matrix unit multiplies 128 rows anyway.)
+  const int twins = small && (!Source::kHalf || W::kTmemQ) ? 2 : 1;
+  // With half floats each row of Q is there twice, 64 rows apart (in tensor memory, or in shared memory, which then holds one Q), and
+  // two threads have a row: the second takes the tiles' upper 64 keys, with a reference, a sum and an O of its own (its weights of the
+  // lower keys are 0, as are the first one's of the upper); they are put together at the end of the unit.  (The softmax warps are
+  // what limits there; the matrix unit multiplies 128 rows anyway.  64 blocks of 16 rows over 4 bits: 109 us, a thread a row 112;
+  // two long requests 57 and 66.)
   const bool split = small && Source::kHalf;
 
   if (t == 0) {
-    ring.init(1, kIssue + 2, 1, Source::kFulls);
+    ring.init(1, kIssue + 2, W::kTmemQ ? 4 : 1, Source::kFulls);
     if constexpr (Source::kHalf) Source::template init<CB, H>(smem + W::kExtra);
     for (int i = 0; i < 2; ++i) mbar_init(bar_s(i), 2), mbar_init(bar_p(i), kSoftmaxThreads), mbar_init(bar_pv(i), 1);
     mbar_init(bar_soft, kSoftmaxThreads);
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
       AttnSegment s;
       uint32_t g = 0, units = 0;
       bool ok = true;
-      const uint32_t qk = instruction(kKeys, false, Source::kHalf) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
+      const uint32_t qk = instruction(kKeys, false, Source::kHalf) | (p.scale_log2 < 0.0f && !W::kTmemQ ? kNegateA : 0u);
       auto scores = [&](uint32_t n, bool last) {
         const int slot = static_cast<int>(units % twins);
 #pragma unroll 1
@@ -218,19 +224,22 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
 #pragma unroll
           for (int i = 0; i < W::kCols / 16; ++i) {
             const uint32_t at = (i >> 2) * R::kBlock + (i & 3) * 32;
-            mma_ss(to, operand(q_at, at), operand(k_at, at), qk, h > 0 || i > 0);
+            if constexpr (W::kTmemQ)
+              mma_ts(to, tmem + W::kQ + i * 8, operand(k_at, at), qk, i > 0);
+            else
+              mma_ss(to, operand(q_at, at), operand(k_at, at), qk, h > 0 || i > 0);
           }
           tc_commit(ring.empty(group));
         }
         tc_commit(bar_s(n));
-        if (last) tc_commit(ring.q_free(slot));
+        if (last && !W::kTmemQ) tc_commit(ring.q_free(slot));
         return true;
       };
       while (ok && ring.template next<true>(s)) {
         const int q_slot = static_cast<int>(units % twins);
         uint32_t q_here = ring.q_bar(q_slot);
         if constexpr (Source::kHalf) q_here = Source::template q_ready<CB, H>(smem + W::kExtra);
-        if (!ring.wait_one(q_here, units / twins & 1)) break;
+        if (!ring.wait_one(q_here, (W::kTmemQ ? units : units / twins) & 1)) break;
         tc_fence_after();
         ok = scores(g, s.cnt == 1);
         for (int i = 0; ok && i < s.cnt; ++i) {
@@ -279,9 +288,50 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
     bool ok = true, left = false;  // left: a unit that goes on behind this block
     const int half_of = split ? t >> 6 : 0, mine = split ? t & 63 : t;  // this thread's half of a tile's keys, its row
     const int h0 = half_of, h1 = split ? half_of + 1 : 2;               // 64 keys each
-    while (const AttnSegment* const seg = ring.peek()) {
+    // With Q in tensor memory: the thread's row of unit n's, brought to half floats' range, and the factor of its scores.
+    float c_next = c;
+    auto put_q = [&](uint32_t n) {
+      if constexpr (W::kTmemQ) {
+        const int slot = static_cast<int>(n % twins), r = slot * 64 + mine;
+        if (!ring.wait(ring.q_bar(slot), n / twins & 1)) return false;
+        const char* const row = smem + r * 128;
+        auto piece = [&](int x) { return *reinterpret_cast<const uint4*>(row + (x >> 3) * R::kBlock + (((x & 7) ^ (r & 7)) << 4)); };
+        uint32_t top = 0u;
+#pragma unroll
+        for (int x = 0; x < W::kCols / 8; ++x) {
+          const uint4 u = piece(x);
+          top = __vmaxu2(__vmaxu2(top, u.x & 0x7fff7fffu), u.y & 0x7fff7fffu);
+          top = __vmaxu2(__vmaxu2(top, u.z & 0x7fff7fffu), u.w & 0x7fff7fffu);
+        }
+        const float2 f = Source::row_range(max(top & 0xffffu, top >> 16), fabsf(p.scale_log2));
+        const float up = p.scale_log2 < 0.0f ? -f.x : f.x;
+        c_next = fmaxf(f.y, 1e-45f);
+#pragma unroll 1
+        for (int h = 0; h < W::kCols / 64; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint4 u = piece(h * 8 + x);
+            w[4 * x] = pack_half(bf16_lo(u.x) * up, bf16_hi(u.x) * up), w[4 * x + 1] = pack_half(bf16_lo(u.y) * up, bf16_hi(u.y) * up);
+            w[4 * x + 2] = pack_half(bf16_lo(u.z) * up, bf16_hi(u.z) * up), w[4 * x + 3] = pack_half(bf16_lo(u.w) * up, bf16_hi(u.w) * up);
+          }
+          tmem_st32(tmem + lanes + W::kQ + h * 32, w);
+        }
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(ring.q_free(slot));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(Source::template q_ready<CB, H>(smem + W::kExtra));
+      }
+      return true;
+    };
+    if (W::kTmemQ && ring.peek()) ok = put_q(0);
+    while (ok) {
+      const AttnSegment* const seg = ring.peek();
+      if (!seg) break;
       const AttnSegment& s = *seg;
       ++units;
+      if (W::kTmemQ) c = c_next;
       const int rows = s.r.n * p.group - s.rt * kRows;  // rows of the unit from this tile on
       const bool idle = (mine & ~31) >= rows;           // none of the warp's rows exists
       const int my_row = (s.rt * kRows + mine) / p.group;  // new row of this thread, and its head
@@ -298,7 +348,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           break;
         }
         tc_fence_after();
-        if constexpr (Source::kHalf) {  // the row's factor is there with its scores
+        if constexpr (Source::kHalf && !W::kTmemQ) {  // the row's factor is there with its scores
           if (i == 0) c = Source::template row_factor<CB, H>(smem + W::kExtra, units - 1, mine);
         }
         const uint4 vv = *reinterpret_cast<const uint4*>(ring.valid(g));
@@ -436,6 +486,8 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         mbar_arrive(bar_p(g));
       }
       if (!ok) break;
+      // The next unit's Q, now that this one's last scores are there: its products begin while this one's end.
+      if (W::kTmemQ && ring.another() && !put_q(units)) break;
       // The unit's last product is done: this thread's row of O.
       if (!ring.wait(bar_pv(g - 1), half(g - 1))) break;
       tc_fence_after();
@@ -472,7 +524,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
           tmem_wait_ld();
           if constexpr (Source::kHalf) {
             if (split) {  // 32 columns go through shared memory (two places, in turn): the second thread's to the first
-              float4* const row = Source::template exchange<CB, H>(smem, h & 1) + mine * 8;
+              float4* const row = Source::template exchange<CB, H>(smem, smem + W::kExtra, h & 1) + mine * 8;
               if (half_of) {
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
@@ -487,7 +539,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
                   o[4 * d + 2] = fmaf(o[4 * d + 2], weight, v.z), o[4 * d + 3] = fmaf(o[4 * d + 3], weight, v.w);
                 }
               }
-              if (CB * H == 1) meet();  // (there is one place)
+              if (W::kTmemQ) meet();  // (there is one place)
             }
           }
           if (mine < rows && !half_of) {
@@ -532,7 +584,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
         }
       }
       tc_fence_before();
-      if constexpr (Source::kHalf) mbar_arrive(Source::template unit_done<CB, H>(smem + W::kExtra));
+      if constexpr (Source::kHalf && !W::kTmemQ) mbar_arrive(Source::template unit_done<CB, H>(smem + W::kExtra));
       ring.release();
     }
     if (t == 0 && !left)
