@@ -617,9 +617,10 @@ typedef struct {
  * row_slots and positions are given.
  *
  * Arithmetic is fp32, rounded once to the dtype; values are copied as they are.
- * The 4-bit cache takes the rotated fp32 values: each group's scale is the one
- * nearest to its largest magnitude / 6, each code the one nearest to its value,
- * both half way to the even one.  Magnitudes above 61440 are stored as 61440, a
+ * The 4-bit cache takes the rotated values before any rounding: each group's
+ * scale is the one nearest to its largest magnitude / 6, each code the one nearest
+ * to its value, both half way to the even one, decided in 64 bits where fp32
+ * leaves open which that is.  Magnitudes above 61440 are stored as 61440, a
  * NaN as 0.  Two rows of a call must not have the same place.
  *
  * dev_status [batch] is OR-ed into (zero it first): SV_DEV_BAD_LAYOUT for an

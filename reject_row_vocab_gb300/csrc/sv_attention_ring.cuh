@@ -90,7 +90,6 @@ __device__ __forceinline__ void mbar_arrive_times(uint32_t bar, uint32_t times) 
 template <int ES, int CB, int NB, int H, bool EARLY = false>
 struct KvRing {
   static constexpr int kEntries = NB;
-  static constexpr int kHalves = H;
   static constexpr int kBlock = kKeys * 128;        // 128 rows of 128 bytes
   static constexpr int kTile = kBlock * CB;         // an entry
   static constexpr int kPieces = CB * 8;            // 16-byte pieces of an entry's row

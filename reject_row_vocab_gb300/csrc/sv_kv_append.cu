@@ -12,7 +12,10 @@
 // a turn in twice the bits of a float.
 //
 // The 4-bit cache: 16 columns are two lanes, one shuffle gives their largest
-// magnitude.
+// magnitude.  Which scale and which code is nearest hangs on which side of a
+// border a value lies, and a rotation in fp32 gets that wrong for one value in a
+// million.  So its keys are turned in pairs of floats, sines and cosines included
+// (2^-37 and better), and rounded to odd, which keeps every border on its side.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cmath>
@@ -49,29 +52,91 @@ struct AppendParams {
   int32_t passes, chunks, per;  // a row's passes over its heads, dealt out to `chunks` warps
 };
 
-// Sine and cosine of position * f, from half turns hi + lo.
-__device__ __forceinline__ float2 turn_of(float hi, float lo) {
-  float s, c;
-  sincospif(hi, &s, &c);
-  lo *= 3.14159265f;
-  return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
-}
-// Positions below 2^22, in pairs of floats: f / 2 pi to 2^-49 of itself, the product exactly, whole turns taken off.  (The 64-bit
-// unit does two lanes a clock: 8192 rows took 8 us of it.)
-__device__ __forceinline__ float2 turn_by(float position, float f) {
+// Part of a turn, hi + lo, of position * f.  Positions below 2^22 in pairs of floats: f / 2 pi to 2^-49 of itself, the product
+// exactly, whole turns taken off.  (The 64-bit unit does two lanes a clock: 8192 rows took 8 us of it.)
+__device__ __forceinline__ float2 part_of_turn(float position, float f) {
   constexpr float kHi = 0.15915494f;                                                      // 1 / 2 pi
   constexpr float kLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(kHi));  // and what it lacks
   const float h = f * kHi, l = fmaf(f, kLo, fmaf(f, kHi, -h));
   const float x = h * position, low = fmaf(l, position, fmaf(h, position, -x));
   const float part = x - rintf(x), t = part + low;
-  return turn_of(2.0f * t, 2.0f * (low - (t - part)));
+  return make_float2(t, low - (t - part));
 }
-// Any position, in 64 bits.
-__device__ __noinline__ float2 turn_by_far(int64_t position, float f) {
+// Of any position, in 64 bits.
+__device__ __noinline__ float2 part_of_turn_far(int64_t position, float f) {
   double t = static_cast<double>(position) * (static_cast<double>(f) * 0.15915494309189533577);  // turns
-  t = 2.0 * (t - rint(t));
+  t = t - rint(t);
   const float hi = static_cast<float>(t);
-  return turn_of(hi, static_cast<float>(t - hi));
+  return make_float2(hi, static_cast<float>(t - hi));
+}
+// Cosine and sine.
+__device__ __forceinline__ float2 turn_of(float2 t) {
+  float s, c;
+  sincospif(2.0f * t.x, &s, &c);
+  const float lo = t.y * 6.28318531f;
+  return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
+}
+
+// Sums and products of floats as pairs of floats (Dekker, Knuth): the rounded result in x, what it lacks in y.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v)));
+}
+__device__ __forceinline__ float2 two_product(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return make_float2(p, __fmaf_rn(a, b, -p));
+}
+
+// Cosine and sine of k / 64 of a turn, in pairs of floats.
+struct TurnTable {
+  float4 v[64];
+};
+constexpr double taylor(double x, int first) {  // of the sine (1) or the cosine (0), |x| <= pi / 4
+  double term = first ? x : 1.0, sum = term;
+  for (int i = first + 1; i < 24; i += 2) term *= -x * x / (i * (i + 1.0)), sum += term;
+  return sum;
+}
+constexpr TurnTable turn_table() {
+  TurnTable t{};
+  for (int k = 0; k < 64; ++k) {
+    const int quarter = (k + 8) / 16, i = k - quarter * 16;  // the nearest quarter of a turn, and the rest
+    const double x = i * (6.28318530717958647693 / 64.0), c0 = taylor(x, 0), s0 = taylor(x, 1);
+    const int q = quarter % 4;
+    const double c = q == 0 ? c0 : q == 1 ? -s0 : q == 2 ? -c0 : s0, s = q == 0 ? s0 : q == 1 ? c0 : q == 2 ? -s0 : -c0;
+    const float ch = static_cast<float>(c), sh = static_cast<float>(s);
+    t.v[k] = float4{ch, static_cast<float>(c - ch), sh, static_cast<float>(s - sh)};
+  }
+  return t;
+}
+__device__ const TurnTable kTurnTable = turn_table();
+
+// Cosine (x, y) and sine (z, w) in pairs of floats: those of the nearest 64th of a turn, turned by the rest a, |a| < 0.05:
+// sin a = a - a^3 / 6 + a^5 / 120 - .., cos a - 1 = - a^2 / 2 + a^4 / 24 - ..
+__device__ __forceinline__ float4 turn_in_pairs(float2 t) {
+  const float k = rintf(t.x * 64.0f), r = __fmaf_rn(k, -1.0f / 64.0f, t.x);
+  const float4 at = kTurnTable.v[static_cast<int>(k) & 63];
+  constexpr float kHi = 6.2831855f;  // 2 pi
+  constexpr float kLo = static_cast<float>(6.28318530717958647693 - static_cast<double>(kHi));
+  float2 a = two_product(r, kHi);
+  a.y = __fmaf_rn(t.y, kHi, __fmaf_rn(r, kLo, a.y));
+  const float2 z = two_product(a.x, a.x);
+  const float sin_lo = __fmaf_rn(__fmul_rn(a.x, z.x), __fmaf_rn(z.x, __fmaf_rn(z.x, -1.0f / 5040.0f, 1.0f / 120.0f), -1.0f / 6.0f),
+                                 __fmaf_rn(a.y, __fmul_rn(-0.5f, z.x), a.y));
+  const float cos_hi = __fmul_rn(-0.5f, z.x);  // (cos a) - 1
+  const float cos_lo = __fmaf_rn(__fmul_rn(z.x, z.x), __fmaf_rn(z.x, -1.0f / 720.0f, 1.0f / 24.0f),
+                                 __fmaf_rn(-0.5f, z.y, __fmul_rn(-a.x, a.y)));
+  // (own + own_lo) cos a + (other + other_lo) sin a
+  auto add = [&](float own, float own_lo, float other, float other_lo) {
+    const float2 u = two_product(other, a.x), w = two_product(own, cos_hi);
+    const float2 x = two_sum(u.x, w.x), y = two_sum(own, x.x);
+    float low = __fmaf_rn(other, sin_lo, __fmul_rn(own, cos_lo));
+    low = __fmaf_rn(other_lo, a.x, __fmaf_rn(own_lo, cos_hi, low));
+    low = __fadd_rn(__fadd_rn(own_lo, low), __fadd_rn(__fadd_rn(u.y, w.y), __fadd_rn(x.y, y.y)));
+    const float hi = __fadd_rn(y.x, low);
+    return make_float2(hi, __fsub_rn(low, __fsub_rn(hi, y.x)));
+  };
+  const float2 c = add(at.x, at.y, -at.z, -at.w), s = add(at.z, at.w, at.x, at.y);
+  return make_float4(c.x, c.y, s.x, s.y);
 }
 
 // Eight values of a row as they lie, and as pairs of floats.
@@ -98,6 +163,42 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair_rz(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// x c + y s with c and s in pairs of floats (c_lo, s_lo what they lack), rounded to odd: towards 0, and, where that lost
+// something, to an odd last bit.  What has at most 23 bits lies on the same side of the result as of the exact sum.
+__device__ __forceinline__ uint64_t turn_to_odd(uint64_t x, uint64_t c, uint64_t c_lo, uint64_t y, uint64_t s, uint64_t s_lo) {
+  const uint64_t minus = pair(-1.0f, -1.0f);
+  // The product p = x c, the sum p + y s, and what each lacks: of the sum y s - (sum - p), and what that difference lost of p.
+  const uint64_t p = mul_pair(x, c), p_lo = fma_pair(x, c, mul_pair(p, minus));
+  const uint64_t sum = fma_pair(y, s, p), v = sub_pair(sum, p);
+  const uint64_t lost = add_pair(fma_pair(y, s, mul_pair(v, minus)), sub_pair(p, sub_pair(sum, v)));
+  const uint64_t low = fma_pair(y, s_lo, fma_pair(x, c_lo, add_pair(p_lo, lost)));
+  const uint64_t cut = add_pair_rz(sum, low), rest = sub_pair(low, sub_pair(cut, sum));
+  float w[2], r[2], n[2];
+  unpair(cut, w[0], w[1]), unpair(rest, r[0], r[1]), unpair(sum, n[0], n[1]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = __uint_as_float(__float_as_uint(w[i]) | (r[i] != 0.0f ? 1u : 0u));
+    if (!(fabsf(n[i]) < 1e30f)) w[i] = n[i];  // (not a number, or a product on the way to none)
+  }
+  return pair(w[0], w[1]);
 }
 
 template <int ES>
@@ -163,7 +264,8 @@ __device__ __forceinline__ bool quantize8(const Pairs& x, uint32_t* codes, uint3
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   *byte = scale_byte(top);
   const float scale = scale_value(*byte), inv = *byte ? __frcp_rn(scale) : 0.0f;
-  // quotients, corrected by their remainders (see scaled())
+  // Quotients: v times the rounded 1 / scale, whose remainder is exact and corrects it (Markstein's division), so that a value half
+  // way between two codes is seen to be there.  (0 for a scale of 0.)
   const uint64_t s2 = pair(-scale, -scale), i2 = pair(inv, inv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -180,6 +282,9 @@ template <int ES, class C, Pairing PAIRING>
 __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const AppendParams p, const C c) {
   constexpr bool kPacked = std::is_same<C, PackedView>::value;
   __shared__ float2 s_turn[kAppendWarps][kMaxPairs];
+  // Of the 4-bit cache: what s_turn lacks, and then what a column's cosine and (signed) sine lack.
+  __shared__ float2 s_lack[kPacked ? kAppendWarps : 1][kPacked ? kMaxPairs : 1];
+  __shared__ float4 s_low[kPacked ? kAppendWarps : 1][2][kPacked ? 2 * kMaxPairs / 4 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lanes = (p.dim + 7) / 8, heads = 32 / lanes;  // lanes of a head, heads of a pass
   const int of = lane / lanes, d0 = (lane - of * lanes) * 8;
@@ -214,24 +319,44 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
       const bool far = pos <= -(1 << 22) || pos >= 1 << 22;
 #pragma unroll
       for (int i = 0; i < kMaxPairs / 32; ++i)
-        if (i * 32 + lane < n) s_turn[warp][i * 32 + lane] = far ? turn_by_far(pos, freq[i]) : turn_by(static_cast<float>(pos), freq[i]);
+        if (i * 32 + lane < n) {
+          const float2 t = far ? part_of_turn_far(pos, freq[i]) : part_of_turn(static_cast<float>(pos), freq[i]);
+          if constexpr (kPacked) {
+            const float4 u = turn_in_pairs(t);
+            s_turn[warp][i * 32 + lane] = make_float2(u.x, u.z), s_lack[warp][i * 32 + lane] = make_float2(u.y, u.w);
+          } else {
+            s_turn[warp][i * 32 + lane] = turn_of(t);
+          }
+        }
       __syncwarp();
       if (turned) {
+        float low_c[8], low_s[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          float2 t[2];
-          float sign[2];
+          float c[2], s[2];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int d = d0 + e + f;
             const bool high = PAIRING == kNeighbours ? f : d >= n;  // the pair's second column
             int i = PAIRING == kNeighbours ? d / 2 : high ? d - n : d;
             if (i >= n) i = 0;  // (a column that is left as it is)
-            t[f] = s_turn[warp][i];
-            sign[f] = high ? p.magnitude : -p.magnitude;
+            const float2 t = s_turn[warp][i];
+            const float sign = high ? p.magnitude : -p.magnitude;
+            c[f] = t.x * p.magnitude, s[f] = t.y * sign;
+            if constexpr (kPacked) {
+              const float2 l = s_lack[warp][i];
+              low_c[e + f] = fmaf(l.x, p.magnitude, fmaf(t.x, p.magnitude, -c[f]));
+              low_s[e + f] = fmaf(l.y, sign, fmaf(t.y, sign, -s[f]));
+            }
           }
-          co.v[e / 2] = pair(t[0].x * p.magnitude, t[1].x * p.magnitude);
-          si.v[e / 2] = pair(t[0].y * sign[0], t[1].y * sign[1]);
+          co.v[e / 2] = pair(c[0], c[1]), si.v[e / 2] = pair(s[0], s[1]);
+        }
+        if (kPacked && of == 0) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            s_low[warp][0][(d0 + e) / 4] = make_float4(low_c[e], low_c[e + 1], low_c[e + 2], low_c[e + 3]);
+            s_low[warp][1][(d0 + e) / 4] = make_float4(low_s[e], low_s[e + 1], low_s[e + 2], low_s[e + 3]);
+          }
         }
       }
       __syncwarp();
@@ -310,8 +435,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
             }
             if (turned) {
               const Pairs was = x;
+              if constexpr (kPacked && kPart == kKey) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) x.v[i] = fma_pair(x.v[i], co.v[i], mul_pair(y.v[i], si.v[i]));
+                for (int i = 0; i < 4; i += 2) {
+                  const float4 c = s_low[warp][0][d0 / 4 + i / 2], s = s_low[warp][1][d0 / 4 + i / 2];
+                  x.v[i] = turn_to_odd(x.v[i], co.v[i], pair(c.x, c.y), y.v[i], si.v[i], pair(s.x, s.y));
+                  x.v[i + 1] = turn_to_odd(x.v[i + 1], co.v[i + 1], pair(c.z, c.w), y.v[i + 1], si.v[i + 1], pair(s.z, s.w));
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x.v[i] = fma_pair(x.v[i], co.v[i], mul_pair(y.v[i], si.v[i]));
+              }
               if (2 * n - d0 < 8) {  // columns behind the last pair are left as they are
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {

@@ -24,7 +24,6 @@
 
 namespace sv {
 
-constexpr int kScaleGroup = 16;
 constexpr uint32_t kMostScale = 0xe2u;  // 10240: the largest scale with 6 * scale below 2^16
 
 struct PackedView {
@@ -141,13 +140,6 @@ __device__ __forceinline__ uint32_t scale_byte(float top) {
   const float lo = scale_value(b), hi = scale_value(b + 1);
   const float mid = 3.0f * (lo + hi);  // six times the middle
   return top > mid || (top == mid && (b & 1u)) ? b + 1 : b;
-}
-
-// x / s (|x| <= 61440, inv = 1 / s rounded, 0 for a scale of 0): the quotient's remainder is exact and corrects it (Markstein's
-// division), so that a value half way between two codes is seen to be there.
-__device__ __forceinline__ float scaled(float x, float s, float inv) {
-  const float a = x * inv;
-  return fmaf(fmaf(-a, s, x), inv, a);
 }
 
 // The codes of eight quotients: each the nearest code, half way to the even one, 6 at most.

@@ -948,7 +948,7 @@ def kv_append(cache, k, v, *, layer: int = 0, seq_lens=None, max_len: Optional[i
     rows behind the last request are left alone.  Row j of request b goes to position seq_lens[b] + j, or to slot row_slots
     [rows] int64; it is rotated by positions [rows] int64, or by seq_lens[b] + j.  Two rows must not have the same place.
     out: KvAppendOutputs; its q may be q itself.  dev_status is OR-ed into: it collects what many calls report until it is
-    zeroed.  cache: a PagedKvCache or a PackedKvCache (which takes the rotated fp32 values, rounded once to 4 bits)."""
+    zeroed.  cache: a PagedKvCache or a PackedKvCache (which takes the rotated values rounded once, to 4 bits)."""
     lib = load_library()
     _require_cache(cache)
     dev, index = cache.device, cache.index

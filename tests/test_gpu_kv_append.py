@@ -199,6 +199,24 @@ def test_every_scale_and_tie_of_bf16(sv):
     run(sv, case)
 
 
+@pytest.mark.parametrize("dtype,pairs,interleaved,magnitude", [(BF16, 64, False, 1.0), (BF16, 64, True, 1.25), (F32, 64, False, 1.0),
+                                                               (F32, 19, True, 1.0), (BF16, 29, False, 0.75)])
+def test_keys_are_stored_as_exact_rotations_would_be(sv, dtype, pairs, interleaved, magnitude):
+    """Every scale and code of a million rotated keys, those among them that a rotation in fp32 puts on a border's other side.  (64-bit
+    angles are off by 2^-40 here: a key that close to a border is one in 10^10.)"""
+    case = AppendCase([0, 3000, 100000], 700, 1, 4, 128, 16, dtype, is_packed=True, staged=True, pairs=pairs, interleaved=interleaved,
+                      magnitude=magnitude, seed=pairs)
+    d = case.make(sv)
+    got = case.append(sv, d)
+    o = case.oracle()
+    assert (got.dev_status == 0).all() and (o["slot"] >= 0).all()
+    parts = packed.unblock(d["data"].cpu().numpy(), 16, 128)
+    codes, scales = (t[0].reshape(-1, 4, t.shape[-1])[o["slot"]] for t in parts[:2])
+    _, want_scales, want = packed.quantize(o["k"])
+    assert np.array_equal(scales, want_scales)
+    assert np.array_equal(packed.values(codes, scales), want)
+
+
 @BOTH
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dim,page,staged", [(64, 16, False), (128, 1, True), (256, 5, False), (96, 16, True)])
