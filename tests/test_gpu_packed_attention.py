@@ -193,3 +193,99 @@ def test_outputs_with_strides(sv):
                                   lse=None, dev_status=torch.empty(2, dtype=torch.int32, device="cuda"))
         got = case.run(sv, out=out)
         assert torch.equal(got.out, case.run(sv).out)
+
+
+@pytest.mark.parametrize("rows", [[1, 2, 1], [20, 3, 7]])
+def test_rows_of_no_request_are_left(sv, rows):
+    case = PackedAttentionCase([40, 300, 9], rows, 4, 2, 64, 16, ragged=True)
+    n = case.q.shape[0]
+    want = run(sv, case)
+    case.q = torch.cat([case.q, torch.full((3, 4, 64), float("nan"), dtype=BF16)])
+    out = sv.AttentionOutputs(out=torch.full((n + 3, 4, 64), 5.0, dtype=BF16, device="cuda"),
+                              lse=torch.full((n + 3, 4), 5.0, device="cuda"), dev_status=torch.empty(3, dtype=torch.int32, device="cuda"))
+    got = case.run(sv, out=out)
+    assert torch.equal(got.out[:n], want.out) and torch.equal(got.lse[:n], want.lse)
+    assert (got.out[n:] == 5.0).all() and (got.lse[n:] == 5.0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_graphs_that_share_a_workspace(sv, rows):
+    """Two captured calls on one workspace, replayed by turns, with an eager one between them."""
+    cases = [PackedAttentionCase(lens, rows, 8, 2, 128, 16, seed=i) for i, lens in enumerate(([3000, 40], [100, 5000]))]
+    want = [run(sv, c) for c in cases]
+    ws = sv.attention_workspace(2, rows, cases[0].cache(sv), 8)
+    calls, graphs = [], []
+    for c in cases:
+        d = {"q": c.q.cuda(), "cache": c.cache(sv), "lens": torch.tensor(c.lens, device="cuda"),
+             "mask": None if c.mask is None else torch.from_numpy(c.mask).cuda(),
+             "slots": None if c.row_slots is None else torch.from_numpy(c.row_slots).cuda(), "scale": c.scale,
+             "out": sv.AttentionOutputs.allocate(2 * rows, 8, 128, 2)}
+        call = lambda d=d: sv.paged_attention(d["q"], d["cache"], d["lens"], max_len=rows, row_slots=d["slots"], mask=d["mask"],
+                                              scale=d["scale"], out=d["out"], ws=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        calls.append((call, d)), graphs.append(g)
+    for i in (0, 1, 1, 0):
+        calls[i][1]["out"].out.fill_(7.0)
+        graphs[i].replay()
+        assert torch.equal(calls[i][1]["out"].out, want[i].out) and torch.equal(calls[i][1]["out"].lse, want[i].lse)
+        calls[1 - i][0]()
+        assert torch.equal(calls[1 - i][1]["out"].out, want[1 - i].out)
+
+
+def test_calls_at_once(sv):
+    """On two streams, each with a workspace of its own."""
+    cases = [PackedAttentionCase([9000, 40], rows, 8, 2, 128, 16, seed=rows) for rows in (1, 20)]
+    want = [run(sv, c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    made = [(c.q.cuda(), c.cache(sv), torch.tensor(c.lens, device="cuda"), sv.attention_workspace(2, c.max_len, c.cache(sv), 8)) for c in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            q, cache, lens, ws = made[i]
+            outs[i].append(sv.paged_attention(q, cache, lens, max_len=c.max_len, scale=c.scale, ws=ws, stream=s))
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        for o in got:
+            assert torch.equal(o.out, w.out) and torch.equal(o.lse, w.lse)
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("page", [1, 16, 128, 200])
+def test_large_offsets(sv, rows, page):
+    """Pages more than 2^32 bytes into the cache give what near ones do; a commit moves entries there."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 16 << 30:
+        pytest.skip("needs 16 GB")
+    n = 260
+    need = -(-n // page)
+    near = torch.arange(need, dtype=torch.int32, device="cuda")[None].contiguous()
+    block = sv.PackedKvCache.block_bytes(page, 64)
+    step = -(-(5 << 30) // (2 * need * 16)) * 16  # bytes from one page to the next
+    g = torch.Generator(device="cuda").manual_seed(page)
+    data = torch.randint(0, 256, (1, 2 * need, 2, block), dtype=torch.uint8, device="cuda", generator=g)
+    parts = packed.unblock(data.cpu().numpy(), page, 64)
+    for a in (parts[1], parts[3]):
+        a[:] = a % 16 + 96  # moderate scales
+    data = torch.from_numpy(packed.blocks(*parts)).cuda()
+    far_mem = torch.zeros(2 * need * step + 2 * block, dtype=torch.uint8, device="cuda")
+    far_data = torch.as_strided(far_mem, (1, 2 * need, 2, block), (0, step, block, 1))
+    far_data.copy_(data)
+    table = near + need
+    q = torch.randn(rows, 8, 64, device="cuda", generator=g).to(BF16)
+    lens = torch.tensor([n - rows], device="cuda")
+    got = []
+    for d in (data, far_data):
+        cache = sv.PackedKvCache(d, table, page_size=page, head_dim=64)
+        o = sv.paged_attention(q, cache, lens, max_len=rows)
+        cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+        src = torch.tensor([(2 * need - 1) * page, need * page, 2], device="cuda")
+        st = sv.kv_commit(cache, cu, src, torch.tensor([3, 4, 5], device="cuda"), max_len=3)
+        got.append((o, cache.data.contiguous(), st))
+    (a, ca, sa), (b, cb, sb) = got
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse) and (a.dev_status == 0).all() and (b.dev_status == 0).all()
+    assert torch.equal(ca, cb) and not torch.equal(ca, data.new_zeros(1).expand_as(ca)) and sa.item() == 0 and sb.item() == 0
