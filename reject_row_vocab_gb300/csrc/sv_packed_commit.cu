@@ -8,6 +8,11 @@
 // much of an entry's scales of a head as its alignment allows (8 bytes of heads of
 // 128).  Places are found once for the layers that a block goes through.
 //
+// Bound by the chain lists, places, rows, and by pieces of 64 and 8 bytes: 384 rows of
+// 64 requests in 32 layers, 8 heads of 128, take 19 us (28 MB there and back; with
+// the sectors that the pieces touch it is 57).  Blocks of 512 threads take 21 us, a
+// quarter of the blocks 23.
+//
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>
 
