@@ -57,7 +57,7 @@ __device__ __forceinline__ void store_half(char* tile, int r, int c0, uint4 w, u
 template <bool STAGED>
 struct HalfSource {
   using Args = PackedTiles;
-  static constexpr int kWarps = kUnpackWarps + (STAGED ? 1 : 0), kFulls = kUnpackWarps;
+  static constexpr int kWarps = kUnpackWarps + (STAGED ? 1 : 0), kFulls = STAGED ? kUnpackWarps / 2 : kUnpackWarps;
   static constexpr bool kHalf = true;
   template <int CB, int H>
   static __host__ __device__ constexpr int entries() { return CB == 2 ? 4 : 8; }
@@ -163,17 +163,22 @@ struct HalfSource {
     }
   }
 
-  // A tile from its place: K, then V.
+  // A tile from its place, K by one half of the warps, V by the other.  (K's place is free again when its scores are there, V's only
+  // behind the weights: by the same warps in turn, the next K waits for that, and 64 blocks of 16 rows take 100 us.)
   template <int CB, int H, class R, class S>
   static __device__ __forceinline__ void unpack(R& ring, const Args& k, const S& stage, int lw) {
     constexpr int kEntries = R::kEntries;
-    static_assert(H == 1, "one entry for K and one for V; Q is in tensor memory");
-    const int lane = ring.lane, mine = lw * 16 + (lane >> 1);  // this lane's key of a tile
-    const int dim = k.c.head_dim, in_block = (1 << k.rows_log) - 1, at_block = (mine >> k.rows_log) * k.block;
-    const int code_at = at_block + (mine & in_block) * (dim / 2) + (lane & 1) * 16;
-    const int scale_at = at_block + (mine & in_block) * (dim / 16) + (lane & 1) * 2;
-    const int codes[2] = {code_at, code_at + packed_v_codes(in_block + 1, dim)};
-    const int scales[2] = {scale_at + packed_k_scales(in_block + 1, dim), scale_at + packed_v_scales(in_block + 1, dim)};
+    static_assert(H == 1 && kEntries % 2 == 0, "one entry for K and one for V, in places of their own; Q is in tensor memory");
+    const int lane = ring.lane, dim = k.c.head_dim, in_block = (1 << k.rows_log) - 1;
+    const int is_v = lw / kFulls, quarter = lw % kFulls;  // 32 keys, 16 at once
+    int code[2], scale[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int key = quarter * 32 + r * 16 + (lane >> 1), at_block = (key >> k.rows_log) * k.block;
+      code[r] = at_block + (key & in_block) * (dim / 2) + (lane & 1) * 16 + (is_v ? packed_v_codes(in_block + 1, dim) : 0);
+      scale[r] = at_block + (key & in_block) * (dim / 16) + (lane & 1) * 2 +
+                 (is_v ? packed_v_scales(in_block + 1, dim) : packed_k_scales(in_block + 1, dim));
+    }
     AttnSegment s;
     uint32_t g = 0;
     bool ok = true;
@@ -188,36 +193,31 @@ struct HalfSource {
         uint4 w[2][CB];
         uint32_t b[2][CB];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int n = 0; n < CB; ++n) {
             const bool live = n * 64 + (lane & 1) * 32 < dim;
-            w[e][n] = *reinterpret_cast<const uint4*>(place + codes[e] + (live ? n * 32 : 0));
-            b[e][n] = *reinterpret_cast<const uint16_t*>(place + scales[e] + (live ? n * 4 : 0));
-            if (!live) b[e][n] = 0u;  // columns that a head does not have are 0
+            w[r][n] = *reinterpret_cast<const uint4*>(place + code[r] + (live ? n * 32 : 0));
+            b[r][n] = *reinterpret_cast<const uint16_t*>(place + scale[r] + (live ? n * 4 : 0));
+            if (!live) b[r][n] = 0u;  // columns that a head does not have are 0
           }
-        const uint32_t good = reinterpret_cast<const uint16_t*>(stage.info(g))[lw];
-        const uint32_t bad = reinterpret_cast<const uint16_t*>(stage.info(g))[8 + lw];
+        const uint32_t good = stage.info(g)[quarter], bad = stage.info(g)[4 + quarter];
         __syncwarp();
         if (lane == 0) mbar_arrive(stage.empty(g));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t entry = 2 * g + e;
-          if (entry >= kEntries && !ring.wait(ring.empty(entry), R::phase(entry - kEntries))) {
-            ok = false;
-            break;
-          }
-          if (e == 0 && lane == 0) {
-            reinterpret_cast<uint16_t*>(ring.valid(g))[lw] = static_cast<uint16_t>(good);
-            reinterpret_cast<uint16_t*>(ring.valid(g) + 4)[lw] = static_cast<uint16_t>(bad);
-          }
-#pragma unroll
-          for (int n = 0; n < CB; ++n) store_half<R>(ring.tile_mem(entry), mine, n * 8 + (lane & 1) * 4, w[e][n], b[e][n]);
-          fence_async();  // (the matrix unit reads through the asynchronous proxy)
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ring.full(entry));
+        const uint32_t entry = 2 * g + is_v;
+        if (entry >= kEntries && !ring.wait(ring.empty(entry), R::phase(entry - kEntries))) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
+        if (!is_v && lane == 0) ring.valid(g)[quarter] = good, ring.valid(g)[4 + quarter] = bad;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int n = 0; n < CB; ++n)
+            store_half<R>(ring.tile_mem(entry), quarter * 32 + r * 16 + (lane >> 1), n * 8 + (lane & 1) * 4, w[r][n], b[r][n]);
+        fence_async();  // (the matrix unit reads through the asynchronous proxy)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.full(entry));
       }
     }
   }
