@@ -152,13 +152,11 @@ struct KvRing {
   }
   __device__ bool wait(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, wait_one(bar, parity)) != 0; }
 
-  // The next segment of the plan, for a whole warp (or, with ONE, for its first lane alone); false at the end, or after a
-  // wait that gave up.
-  template <bool ONE = false>
+  // The next segment of the plan, for a whole warp; false at the end, or after a wait that gave up.
   __device__ bool next(AttnSegment& s) {
-    if (!(ONE ? wait_one(plan_bar(plans), plans / kPlans & 1) : wait(plan_bar(plans), plans / kPlans & 1))) return false;
+    if (!wait(plan_bar(plans), plans / kPlans & 1)) return false;
     s = *plan_slot(plans);
-    if (!ONE) __syncwarp();
+    __syncwarp();
     if (lane == 0) mbar_arrive(read_bar(plans));
     ++plans;
     return s.cnt > 0;

@@ -80,19 +80,26 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool b_mn, bool half) 
   return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kRows >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// By a whole warp, of which the lane with `issues` acts: so the compiler sees operands and control flow that are the same in all
+// lanes, and keeps them in uniform registers, which is where the instruction takes them from.
+__device__ __forceinline__ void mma_ss(bool issues, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(issues ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(bool issues, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(issues ? 1u : 0u)
       : "memory");
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r)::"memory");
+  return r != 0u;
 }
 
 // ---------------------------------------------------------------------------------------------------------------------
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
   R ring(smem + W::kQBytes);
   int* s_misc = reinterpret_cast<int*>(smem + W::kMisc);
   volatile uint32_t* s_careful = reinterpret_cast<volatile uint32_t*>(s_misc + 1);  // [2]: units that found NaN or infinities
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0);
   auto bar_s = [&](uint32_t g) { return base + W::kBars + (g & 1) * 8; };
   auto bar_p = [&](uint32_t g) { return base + W::kBars + (2 + (g & 1)) * 8; };
   // Two, in turn: a wait by parity is only good where the barrier's phase before is known to be over, and that S(g) has
@@ -204,73 +211,79 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
   } else if (warp == kQueries) {
     ring.template load_q<kRows>(p, base, R::kBlock, twins, 64);
   } else if (warp == kIssue) {
-    // ---- The issuing thread.
-    if (lane == 0) {
-      AttnSegment s;
-      uint32_t g = 0, units = 0;
-      bool ok = true;
-      const uint32_t qk = instruction(kKeys, false, Source::kHalf) | (p.scale_log2 < 0.0f && !W::kTmemQ ? kNegateA : 0u);
-      auto scores = [&](uint32_t n, bool last) {
-        const int slot = static_cast<int>(units % twins);
+    // ---- The issuing warp: one lane acts, all go along.
+    AttnSegment s;
+    uint32_t g = 0, units = 0;
+    bool ok = true;
+    const bool issues = elected();
+    const uint32_t qk = instruction(kKeys, false, Source::kHalf) | (p.scale_log2 < 0.0f && !W::kTmemQ ? kNegateA : 0u);
+    const uint32_t tmem_at = __shfl_sync(0xffffffffu, tmem, 0);
+    auto commit = [&](uint32_t bar) {
+      if (issues) tc_commit(bar);
+    };
+    // (rows of half floats are fenced by the warps that write them)
+    auto see = [&] {
+      if constexpr (!Source::kHalf) fence_async();  // the copies wrote through the generic proxy, the products read through the asynchronous one
+      tc_fence_after();
+    };
+    auto scores = [&](uint32_t n, bool last) {
+      const uint32_t slot = units % twins;
+#pragma unroll 1
+      for (int h = 0; h < H; ++h) {
+        const uint32_t group = 2 * H * n + h;
+        if (!ring.wait(ring.full(group), ring.phase(group))) return false;
+        see();
+        if (h == 0 && issues) mbar_arrive(bar_s(n));  // hands the tile's validity on
+        const uint32_t q_at = operand_at(base + slot * 64 * 128 + h * R::kTile, 16), k_at = operand_at(ring.tile(group), 16);
+        const uint32_t to = tmem_at + W::kS + (n & 1) * 128;
+#pragma unroll
+        for (int i = 0; i < W::kCols / 16; ++i) {
+          const uint32_t at = (i >> 2) * R::kBlock + (i & 3) * 32;
+          if constexpr (W::kTmemQ)
+            mma_ts(issues, to, tmem_at + W::kQ + i * 8, operand(k_at, at), qk, i > 0);
+          else
+            mma_ss(issues, to, operand(q_at, at), operand(k_at, at), qk, h > 0 || i > 0);
+        }
+        commit(ring.empty(group));
+      }
+      commit(bar_s(n));
+      if (last && !W::kTmemQ) commit(ring.q_free(slot));
+      return true;
+    };
+    while (ok && ring.next(s)) {
+      const int cnt = __shfl_sync(0xffffffffu, s.cnt, 0);
+      const uint32_t q_slot = units % twins;
+      uint32_t q_here = ring.q_bar(q_slot);
+      if constexpr (Source::kHalf) q_here = Source::template q_ready<CB, H>(smem + W::kExtra);
+      if (!ring.wait(q_here, (W::kTmemQ ? units : units / twins) & 1)) break;
+      tc_fence_after();
+      ok = scores(g, cnt == 1);
+      for (int i = 0; ok && i < cnt; ++i) {
+        const uint32_t n = g + i;
+        if (i + 1 < cnt && !scores(n + 1, i + 2 == cnt)) {
+          ok = false;
+          break;
+        }
 #pragma unroll 1
         for (int h = 0; h < H; ++h) {
-          const uint32_t group = 2 * H * n + h;
-          if (!ring.wait_one(ring.full(group), ring.phase(group))) return false;
-          fence_async();  // the copies wrote through the generic proxy, the products read through the asynchronous one
-          tc_fence_after();
-          if (h == 0) mbar_arrive(bar_s(n));  // hands the tile's validity on
-          const uint32_t q_at = operand_at(base + slot * 64 * 128 + h * R::kTile, 16), k_at = operand_at(ring.tile(group), 16);
-          const uint32_t to = tmem + W::kS + (n & 1) * 128;
-#pragma unroll
-          for (int i = 0; i < W::kCols / 16; ++i) {
-            const uint32_t at = (i >> 2) * R::kBlock + (i & 3) * 32;
-            if constexpr (W::kTmemQ)
-              mma_ts(to, tmem + W::kQ + i * 8, operand(k_at, at), qk, i > 0);
-            else
-              mma_ss(to, operand(q_at, at), operand(k_at, at), qk, h > 0 || i > 0);
-          }
-          tc_commit(ring.empty(group));
-        }
-        tc_commit(bar_s(n));
-        if (last && !W::kTmemQ) tc_commit(ring.q_free(slot));
-        return true;
-      };
-      while (ok && ring.template next<true>(s)) {
-        const int q_slot = static_cast<int>(units % twins);
-        uint32_t q_here = ring.q_bar(q_slot);
-        if constexpr (Source::kHalf) q_here = Source::template q_ready<CB, H>(smem + W::kExtra);
-        if (!ring.wait_one(q_here, (W::kTmemQ ? units : units / twins) & 1)) break;
-        tc_fence_after();
-        ok = scores(g, s.cnt == 1);
-        for (int i = 0; ok && i < s.cnt; ++i) {
-          const uint32_t n = g + i;
-          if (i + 1 < s.cnt && !scores(n + 1, i + 2 == s.cnt)) {
+          const uint32_t group = 2 * H * n + H + h;
+          if (!ring.wait(ring.full(group), ring.phase(group)) || (h == 0 && !ring.wait(bar_p(n), half(n)))) {
             ok = false;
             break;
           }
-#pragma unroll 1
-          for (int h = 0; h < H; ++h) {
-            const uint32_t group = 2 * H * n + H + h;
-            if (!ring.wait_one(ring.full(group), ring.phase(group)) || (h == 0 && !ring.wait_one(bar_p(n), half(n)))) {
-              ok = false;
-              break;
-            }
-            fence_async();
-            tc_fence_after();
-            const uint32_t v_at = operand_at(ring.tile(group), R::kBlock);
-            const uint32_t to = tmem + W::kO + h * W::kCols, weights = tmem + W::kS + (n & 1) * 128;
+          see();
+          const uint32_t v_at = operand_at(ring.tile(group), R::kBlock);
+          const uint32_t to = tmem_at + W::kO + h * W::kCols, weights = tmem_at + W::kS + (n & 1) * 128;
 #pragma unroll
-            for (int j = 0; j < kKeys / 16; ++j)
-              mma_ts(to, weights + j * 8, operand(v_at, j * 2048),
-                     instruction(W::kCols, true, Source::kHalf), i > 0 || j > 0);
-            tc_commit(ring.empty(group));
-          }
-          if (!ok) break;
-          tc_commit(bar_pv(n));
+          for (int j = 0; j < kKeys / 16; ++j)
+            mma_ts(issues, to, weights + j * 8, operand(v_at, j * 2048), instruction(W::kCols, true, Source::kHalf), i > 0 || j > 0);
+          commit(ring.empty(group));
         }
-        g += s.cnt;
-        ++units;
+        if (!ok) break;
+        commit(bar_pv(n));
       }
+      g += cnt;
+      ++units;
     }
     __syncwarp();
   } else {
