@@ -62,6 +62,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
             tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 64; ++j) mx[j & 3] = fmax_nan(mx[j & 3], v[j]);
+            for (int j = 0; j < 32; ++j) mx[j & 3] = fmax_nan(mx[j & 3], v[2 * j], v[2 * j + 1]);
           }
           const float top = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3]));
           const bool grow = !(top <= m) && !((top - m) * c <= kSlack);  // also a first finite maximum, and NaN
@@ -468,23 +475,27 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
             ref = 0.0f;
           }
           ref -= kLow;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t sum[2] = {0u, 0u};  // of each fourth weight, in pairs
+          const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
 #pragma unroll 1
           for (int h = h0; h < h1; ++h) {
             float v[64];
-            uint32_t pk[32];
             tmem_ld32(st + h * 64, reinterpret_cast<uint32_t*>(v));
             tmem_ld32(st + h * 64 + 32, reinterpret_cast<uint32_t*>(v) + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float a = ex2_fast(fmaf(v[2 * j], c, -ref));
-              const float b = ex2_fast(fmaf(v[2 * j + 1], c, -ref));
-              sum[(2 * j) & 3] += a;
-              sum[(2 * j + 1) & 3] += b;
-              pk[j] = Source::kHalf ? pack_half(a, b) : pack_bf16(a, b);
+            for (int part = 0; part < 2; ++part) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float a, b;
+                unpair(fma_pair(pair(v[part * 32 + 2 * j], v[part * 32 + 2 * j + 1]), c2, ref2), a, b);
+                a = ex2_fast(a), b = ex2_fast(b);
+                sum[j & 1] = add_pair(sum[j & 1], pair(a, b));
+                pk[j] = Source::kHalf ? pack_half(a, b) : pack_bf16(a, b);
+              }
+              tmem_st16(st + h * 32 + part * 16, pk);
             }
-            tmem_st32(st + h * 32, pk);
           }
           if (split) {  // the other half of the keys is the other thread's
             uint32_t none[32];
@@ -492,7 +503,9 @@ __global__ void __launch_bounds__(kWideThreads<Source>, 1)
             for (int j = 0; j < 32; ++j) none[j] = 0u;
             tmem_st32(st + (1 - h0) * 32, none);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float of[4];
+          unpair(sum[0], of[0], of[1]), unpair(sum[1], of[2], of[3]);
+          l += (of[0] + of[1]) + (of[2] + of[3]);
           tmem_wait_st();
         }
         tc_fence_before();
