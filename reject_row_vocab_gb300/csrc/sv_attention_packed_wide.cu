@@ -18,12 +18,13 @@
 // memory 41; 64 blocks of 16 rows in pages of 64 the other way round, 137 and 109,
 // both with Q in shared memory).
 //
-// Bound by a tile's way through shared memory: 18 KB arrive, are read, written as 64
-// KB of half floats and read again by the products, beside 1100 clocks of the matrix
-// unit, which multiplies 128 rows whether there are as many or not.  Measured: blocks
-// of 16 rows of 64 requests of up to 4000, 32 heads of 128 on 8, pages of 64: 100 us (102
-// over bf16, for 3.6 times the bytes); trees of 17 nodes of 16 requests in pages of
-// one slot: 22 us; 5 rows of two requests of 60000 to 100000: 55 us (64).
+// Bound by the softmax warps' chain, about 1700 clocks a tile (64 keys a thread), beside
+// 1100 of the matrix unit, which multiplies 128 rows whether there are as many or not,
+// and by a unit's end (5400 clocks: two threads' halves of a row are put together by
+// way of 8 KB).  Measured: blocks of 16 rows of 64 requests of up to 4000, 32 heads of
+// 128 on 8, pages of 64: 86 us (102 over bf16, for 3.6 times the bytes); trees of 17
+// nodes of 16 requests in pages of one slot: 22 us; 5 rows of two requests of 60000 to
+// 100000: 49 us (64).
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include "sv_attention_packed.cuh"
@@ -164,7 +165,7 @@ struct HalfSource {
   }
 
   // A tile from its place, K by one half of the warps, V by the other.  (K's place is free again when its scores are there, V's only
-  // behind the weights: by the same warps in turn, the next K waits for that, and 64 blocks of 16 rows take 100 us.)
+  // behind the weights: by the same warps in turn, the next K waits for that: 64 blocks of 16 rows took 100 us that way and 96 this.)
   template <int CB, int H, class R, class S>
   static __device__ __forceinline__ void unpack(R& ring, const Args& k, const S& stage, int lw) {
     constexpr int kEntries = R::kEntries;

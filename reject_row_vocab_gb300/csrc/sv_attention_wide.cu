@@ -1,12 +1,13 @@
 // Attention over the paged cache for many query rows, on the fifth-generation
 // tensor cores: bf16, tiles of 128 rows and 128 keys.
 //
-//   S = Q K^T (128 x 128, tensor memory)     one thread issues the products
+//   S = Q K^T (128 x 128, tensor memory)     one warp issues the products
 //   P = 2^(c (S - m)), l += sum P            one thread a row: no exchange
 //   O += P V  (P from tensor memory)         accumulated in tensor memory
 //
 // Four softmax warps, four loading warps, one warp that issues the matrix
-// instructions, one that loads the next unit's Q and one that walks the line
+// instructions (a lane of it, with what they take in uniform registers: by one
+// thread alone an instruction took 70 clocks to issue, about as long as to run), one that loads the next unit's Q and one that walks the line
 // of tiles ahead of them all, connected by mbarriers.  The loading warps bring
 // K and V through the page table into a ring of tiles in the 128-byte swizzle
 // the matrix unit reads, and run ahead over the ends of units.  S has two

@@ -73,7 +73,7 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand in the 128-byte swizzle: its lower word, which a part of the operand `bytes` further on only adds
-// bytes / 16 to, and the operand.  (One thread issues all products, so what it computes for each of them counts.)  Stride: bytes
+// bytes / 16 to, and the operand.  (One warp issues all products, so what it computes for each of them counts.)  Stride: bytes
 // between groups of eight rows (1024); lead: bytes between 64-element blocks of the contiguous axis (used where that axis is the
 // operand's M or N).
 __device__ __forceinline__ uint32_t operand_at(uint32_t addr, uint32_t lead) { return (addr >> 4) + ((lead >> 4) << 16); }
