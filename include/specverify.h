@@ -650,8 +650,8 @@ sv_status_t spec_verify_packed_kv_append(const sv_packed_kv_cache_t* cache, int3
  * what spec_verify_kv_append with the same rows has stored.  k and v:
  * [num_layers, rows, heads, head_dim] of the cache's dtype, with the same
  * strides in elements (head_dim dense; multiples of 16 bytes); rows, heads and
- * layers must not lie over one another, nor k over v or either over the cache
- * (SV_ERR_UNSUPPORTED).  A row whose place lies outside the cache is 0.
+ * layers must not lie over one another, and the address ranges of k, v and the
+ * cache must not meet (SV_ERR_UNSUPPORTED).  A row whose place lies outside the cache is 0.
  * dev_status [batch] is OR-ed into, with the bits of spec_verify_kv_append.
  */
 sv_status_t spec_verify_kv_read(const sv_kv_cache_t* cache, int32_t layer, int32_t num_layers, const sv_rows_t* rows,
