@@ -483,6 +483,7 @@ __device__ __forceinline__ int plan_and_load(Queue& queue, const AttnParams& p, 
         *queue.plan_slot(planned) = s;
         mbar_arrive(queue.plan_bar(planned));
       }
+      __syncwarp();  // load_q's other lanes read the segment without a wait on its barrier; a shuffle alone orders no memory
       ended = __shfl_sync(0xffffffffu, more, 0) == 0;
       ++planned;
       moved = global_ns();

@@ -5,7 +5,7 @@ import torch
 
 from oracle import packed
 from tests.packed_cases import PackedAttentionCase
-from tests.serving_cases import BF16, AttentionCase, check_attention
+from tests.serving_cases import BF16, AttentionCase, attention_bounds, check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -77,6 +77,38 @@ def test_many_tiles_a_block(sv, dim, rows):
         one = sv.AttentionOutputs(out=got.out[i * rows:(i + 1) * rows], lse=got.lse[i * rows:(i + 1) * rows], dev_status=got.dev_status[i:i + 1])
         check_attention(case, one)
     assert (got.dev_status == 0).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 12, 40])
+def test_many_units_a_block(sv, dim, rows):
+    """Units of one tile or two in quick turn, a dozen a block or more: the plan's places are used again, and each unit's queries are
+    those of its own request and head.  (One request's bytes for all; the new rows are hidden.)"""
+    n, heads, G = 500, 8, 4
+    case = PackedAttentionCase([200], rows, heads, G, dim, 16)
+    cache = case.cache(sv)
+    many = sv.PackedKvCache(cache.data, cache.page_table.expand(n, -1).contiguous(), page_size=16, head_dim=dim)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    q = (2.0 * torch.randn(n * rows, heads, dim, device="cuda", generator=g)).to(BF16)
+    lens = torch.tensor([1 + 37 * b % 200 for b in range(n)], device="cuda")
+    call = lambda: sv.paged_attention(q, many, lens, max_len=rows, scale=case.scale,
+                                      mask=torch.zeros(n, rows, rows, dtype=torch.uint8, device="cuda"))
+    got, again = call(), call()
+    assert torch.equal(got.out, again.out) and torch.equal(got.lse, again.lse) and (got.dev_status == 0).all()
+    x = torch.arange(200)
+    slot = torch.from_numpy(case.table[0])[x // 16].long() * 16 + x % 16
+    k, v = (t[0].reshape(-1, G, dim)[slot].cuda().repeat_interleave(heads // G, 1) for t in (case.k, case.v))
+    s = torch.einsum("rhd,xhd->rhx", q.double(), k) * case.scale
+    s.masked_fill_((x.cuda() >= lens.repeat_interleave(rows)[:, None])[:, None], float("-inf"))
+    w = torch.softmax(s, -1)
+    host = lambda t: t.cpu().numpy()
+    count = host(lens.repeat_interleave(rows))
+    o = {"out": host(torch.einsum("rhx,xhd->rhd", w, v)), "lse": host(torch.logsumexp(s, -1)), "count": count,
+         "smax": host(torch.einsum("rhd,xhd->rhx", q.double().abs(), k.abs()).amax(-1) * case.scale),
+         "mag": host(torch.einsum("rhx,xhd->rhd", w, v.abs())) + 2.0 ** -23 * count[:, None, None] * host(v.abs().max())}
+    tol, lse_tol = attention_bounds(o, dim, BF16)  # (with what small weights in half floats may add, as in PackedAttentionCase)
+    assert (np.abs(host(got.out.double()) - o["out"]) <= tol).all()
+    assert (np.abs(host(got.lse.double()) - o["lse"]) <= lse_tol).all()
 
 
 @pytest.mark.parametrize("dim", [64, 256])
