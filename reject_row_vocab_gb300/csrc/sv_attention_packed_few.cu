@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(Few4<D, NT>::kThreads, 1)
               for (int x = 4; x < 32; x <<= 1) top[n][c] = fmax_nan(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], x));
               if (!(top[n][c] <= most[n][c])) {
                 const float to = top[n][c] - kTop, a = most[n][c] == -kInfF ? 0.0f : ex2_fast(ref[n][c] - to);
-                ref[n][c] = to, most[n][c] = to + kSlack;
+                // (rounded down: of a score beyond 2^25 the next float may be 16 higher, whose weight a half float has no room for)
+                ref[n][c] = to, most[n][c] = __fadd_rd(to, kSlack);
                 l[n][c] *= a;
 #pragma unroll
                 for (int d = 0; d < MT; ++d) o[n][d][c] *= a, o[n][d][2 + c] *= a;

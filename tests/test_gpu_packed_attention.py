@@ -172,6 +172,43 @@ def test_tiny_scales_of_a_cache_of_whole_numbers(sv, rows, scale):
     run(sv, case)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 20])
+@pytest.mark.parametrize("base,first,later", [(25, 8.0, 16.0), (26, 8.0, 16.0), (27, 16.0, 32.0), (28, 32.0, 64.0)])
+def test_huge_scores_that_rise(sv, dim, rows, base, first, later):
+    """Scores (in powers of two) of 2^base + first in a history's first half, and + later in its second: there a float is a multiple
+    of 4 to 32, and so are a reference and what scores may pass it by.  All of them are exact, so the weights are known."""
+    n, heads, G, keys = 24, 32, 8, 1536
+    case = PackedAttentionCase([keys], rows, heads, G, dim, 16)
+    k = np.zeros((keys, G, dim))
+    k[..., 0], k[..., 1] = 4096.0, 6144.0  # (the second of a group fixes its scale: 1024, and 1)
+    k[:keys // 2, :, 16], k[keys // 2:, :, 16], k[..., 17] = 2.0, 4.0, 6.0
+    x = np.arange(keys)
+    slot = case.table[0][x // 16].astype(np.int64) * 16 + x % 16
+    parts = list(packed.unblock(case.blocks, 16, dim))
+    codes, scales, value = packed.quantize(k)
+    assert np.array_equal(value, k)
+    for i, new in ((0, codes), (1, scales)):
+        parts[i][0].reshape(-1, G, new.shape[-1])[slot] = new
+    case.blocks = packed.blocks(*parts)
+    cache = case.cache(sv)
+    many = sv.PackedKvCache(cache.data, cache.page_table.expand(n, -1).contiguous(), page_size=16, head_dim=dim)
+    q = torch.zeros(n * rows, heads, dim, dtype=BF16, device="cuda")
+    q[..., 0], q[..., 16] = 2.0 ** (base - 12), first / 2.0
+    scale = np.float32(np.log(2.0))
+    assert np.float32(scale * np.float32(1.4426950408889634)) == 1.0
+    got = sv.paged_attention(q, many, torch.full((n,), keys, device="cuda"), max_len=rows, scale=float(scale),
+                             mask=torch.zeros(n, rows, rows, dtype=torch.uint8, device="cuda"))
+    w = np.where(x < keys // 2, 2.0 ** (first - later), 1.0)
+    v = case.v[0].numpy().reshape(-1, G, dim)[slot].repeat(heads // G, 1)
+    out, mag = np.einsum("x,xhd->hd", w, v) / w.sum(), np.einsum("x,xhd->hd", w, np.abs(v)) / w.sum()
+    # the sums of 1536 weights and products in fp32, two exponentials, the weights (2^-11 of themselves) and the result rounded
+    tol = (2 * keys * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -11) * mag + 2.0 ** -8 * np.abs(out)
+    assert (np.abs(got.out.double().cpu().numpy() - out) <= tol).all()
+    lse = (2.0 ** base + later) * np.log(2.0) + np.log(w.sum())
+    assert (np.abs(got.lse.double().cpu().numpy() - lse) <= 2.0 ** -22 * lse).all()
+
+
 @pytest.mark.parametrize("rows", [1, 20])
 def test_queries_of_mixed_size(sv, rows):
     case = PackedAttentionCase([40, 300], rows, 4, 2, 64, 16)
