@@ -77,11 +77,40 @@ def values(codes, scales):
     return np.where(codes >= 8, -1.0, 1.0) * MAGNITUDES[codes & 7] * s
 
 
+def _two_pi(bits):
+    """2 pi times 2^bits, from Machin's 16 arctan(1/5) - 4 arctan(1/239) in whole numbers."""
+    def arctan_of_one_over(n):
+        one = 1 << (bits + 20)
+        term, total, i = one // n, 0, 1
+        while term:
+            total += term // i if i % 4 == 1 else -(term // i)
+            term //= n * n
+            i += 2
+        return total
+    return (32 * arctan_of_one_over(5) - 8 * arctan_of_one_over(239)) >> 20
+
+
+def angles(positions, inv_freq):
+    """position * inv_freq [rows, pairs], where fp64 does not hold that exactly less whole turns, by whole numbers."""
+    pos, f = np.asarray(positions, np.int64), np.asarray(inv_freq, np.float64)
+    out = pos[:, None].astype(np.float64) * f
+    for r in np.nonzero(np.abs(pos.astype(np.float64)) >= 2.0 ** 29)[0]:  # (a float has 24 bits)
+        for i, x in enumerate(f):
+            a, b = float(x).as_integer_ratio()
+            n = (int(pos[r]) * a << 256) // b
+            n -= (2 * n + _TURN) // (2 * _TURN) * _TURN  # less the nearest number of turns
+            out[r, i] = float(n) / 2.0 ** 256
+    return out
+
+
+_TURN = _two_pi(256)
+
+
 def rotate(x, positions, inv_freq, interleaved=False, magnitude=1.0):
     """x [rows, heads, dim]: pairs of columns as complex numbers, turned; and |x| + |y| of each column's pair (0: left alone)."""
     x = np.asarray(x, np.float64)
     n = len(inv_freq)
-    angle = np.asarray(positions, np.float64)[:, None, None] * np.asarray(inv_freq, np.float64)
+    angle = angles(positions, inv_freq)[:, None]
     turn = magnitude * (np.cos(angle) + 1j * np.sin(angle))
     out, mag = x.copy(), np.zeros_like(x)
     a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))

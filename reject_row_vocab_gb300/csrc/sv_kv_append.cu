@@ -69,9 +69,19 @@ __device__ __forceinline__ float2 part_of_turn(float position, float f) {
   const float part = x - rintf(x), t = part + low;
   return make_float2(t, low - (t - part));
 }
-// Of any position, in 64 bits.
+// Of any position, in pairs of doubles: f / 2 pi to 2^-104 of itself, a position's upper and lower 32 bits by themselves (2^63
+// has 2^60 whole turns).
 __device__ __noinline__ float2 part_of_turn_far(int64_t position, float f) {
-  double t = static_cast<double>(position) * (static_cast<double>(f) * 0.15915494309189533577);  // turns
+  constexpr double kHi = 0.15915494309189535;     // 1 / 2 pi
+  constexpr double kLo = -9.839338337591243e-18;  // and what it lacks
+  const double w = static_cast<double>(f), h = w * kHi, l = fma(w, kLo, fma(w, kHi, -h));
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double p = i ? static_cast<double>(static_cast<uint32_t>(position)) : static_cast<double>(position >> 32) * 4294967296.0;
+    const double x = h * p, low = fma(l, p, fma(h, p, -x));
+    t += (x - rint(x)) + (low - rint(low));
+  }
   t = t - rint(t);
   const float hi = static_cast<float>(t);
   return make_float2(hi, static_cast<float>(t - hi));

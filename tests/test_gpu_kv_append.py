@@ -81,6 +81,16 @@ def test_angles_of_far_positions(sv):
 
 
 @BOTH
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_farthest_positions(sv, is_packed, dtype):
+    """Positions of 2^31 and beyond, to the ends of 64 bits."""
+    rng = np.random.default_rng(3)
+    pos = np.array([2 ** 31 + 5, -(2 ** 33) - 1, 2 ** 40 + 12345, 2 ** 52 + 3, 2 ** 53 + 1, -(2 ** 60) + 11, 2 ** 63 - 1, -(2 ** 63)] +
+                   [int(x) for x in rng.integers(2 ** 31, 2 ** 62, 24)], np.int64)
+    run(sv, AppendCase([0] * 32, 1, 4, 2, 64, 16, dtype, is_packed=is_packed, positions=pos))
+
+
+@BOTH
 def test_without_rotation_and_without_queries(sv, is_packed):
     case = AppendCase([7, 3], 2, 2, 2, 64, 16, BF16, is_packed=is_packed, rotation=False)
     d = case.make(sv)

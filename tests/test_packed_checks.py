@@ -339,3 +339,16 @@ def test_rotation_against_its_formula():
         k, _ = packed.rotate(x[1:2], [13], f, inter)
         q0, _ = packed.rotate(x[:1], [4], f, inter)
         assert np.allclose((q * k)[..., :8].sum(), (q0 * x[1:2])[..., :8].sum())
+
+
+def test_angles_of_far_positions_against_rational_numbers():
+    """Fewer whole turns by subtraction alone: the angle of n is twice that of n / 2, from one that fp64 holds exactly."""
+    f = (10000.0 ** (-np.arange(8) / 8)).astype(np.float32)
+    near = np.array([3, 2 ** 28 + 1, -(2 ** 28) - 7, 2 ** 29 - 1], np.int64)
+    assert np.array_equal(packed.angles(near, f), near[:, None] * f.astype(np.float64))
+    for p in near:
+        z = np.exp(1j * packed.angles([p], f))
+        for k in range(1, 33):
+            z = z * z  # (twice the error each time)
+            far = packed.angles([int(p) << k], f)
+            assert (k < 3 or p == 3 or np.abs(far).max() <= np.pi) and np.abs(np.exp(1j * far) - z).max() <= 2.0 ** (k - 51)
