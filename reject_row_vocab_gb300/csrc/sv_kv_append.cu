@@ -180,11 +180,13 @@ __device__ __forceinline__ uint64_t sub_pair(uint64_t a, uint64_t b) {
 // something, to an odd last bit.  What has at most 23 bits lies on the same side of the result as of the exact sum.
 __device__ __forceinline__ uint64_t turn_to_odd(uint64_t x, uint64_t c, uint64_t c_lo, uint64_t y, uint64_t s, uint64_t s_lo) {
   const uint64_t minus = pair(-1.0f, -1.0f);
-  // The product p = x c, the sum p + y s, and what each lacks: of the sum y s - (sum - p), and what that difference lost of p.
+  // The products, their sum, and what each lacks (Dekker, Knuth).  The sum is one of two floats: where they cancel, a product added
+  // without rounding leaves bits below both, and what such a sum lacks is not found by the steps for two floats.
   const uint64_t p = mul_pair(x, c), p_lo = fma_pair(x, c, mul_pair(p, minus));
-  const uint64_t sum = fma_pair(y, s, p), v = sub_pair(sum, p);
-  const uint64_t lost = add_pair(fma_pair(y, s, mul_pair(v, minus)), sub_pair(p, sub_pair(sum, v)));
-  const uint64_t low = fma_pair(y, s_lo, fma_pair(x, c_lo, add_pair(p_lo, lost)));
+  const uint64_t q = mul_pair(y, s), q_lo = fma_pair(y, s, mul_pair(q, minus));
+  const uint64_t sum = add_pair(p, q), v = sub_pair(sum, p);
+  const uint64_t lost = add_pair(sub_pair(p, sub_pair(sum, v)), sub_pair(q, v));
+  const uint64_t low = add_pair(lost, fma_pair(y, s_lo, fma_pair(x, c_lo, add_pair(p_lo, q_lo))));
   const uint64_t cut = add_pair_rz(sum, low), rest = sub_pair(low, sub_pair(cut, sum));
   float w[2], r[2], n[2];
   unpair(cut, w[0], w[1]), unpair(rest, r[0], r[1]), unpair(sum, n[0], n[1]);

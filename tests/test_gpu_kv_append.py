@@ -227,6 +227,42 @@ def test_keys_are_stored_as_exact_rotations_would_be(sv, dtype, pairs, interleav
     assert np.array_equal(packed.values(codes, scales), want)
 
 
+@pytest.mark.parametrize("dim,pairs,interleaved", [(32, 8, True), (64, 16, False), (64, 13, False)])
+@pytest.mark.parametrize("start", [100, 2 ** 22, 2 ** 30 + 1, 2 ** 44 + 3])
+def test_keys_next_to_a_border(sv, dim, pairs, interleaved, start):
+    """Values that lie 2^-34 to 2^-33 beside the middle of two codes, at near and far positions.  (What may be off by rounding: sines
+    and cosines by 2^-37 each, of pairs of up to 4 together.)"""
+    rng = np.random.default_rng(pairs + start)
+    case = AppendCase([0] * 64, 1, 1, 1, dim, 16, F32, is_packed=True, staged=True, pairs=pairs, interleaved=interleaved,
+                      positions=start + np.arange(64))
+    case.inv_freq = rng.uniform(0.3, 1.0, pairs).astype(np.float32)
+    case.inv_freq[-1] = 0.0  # a pair that nothing turns, (6, 0), gives the group of columns 0 .. 15 its scale of 1
+    first, second = (np.arange(pairs) * 2, np.arange(pairs) * 2 + 1) if interleaved else (np.arange(pairs), np.arange(pairs) + pairs)
+    angle = packed.angles(case.positions, case.inv_freq)
+    key, planted = case.qkv[:, 1].numpy(), np.zeros((64, pairs), bool)
+    key[:, first[-1]], key[:, second[-1]] = 6.0, 0.0
+    for r in range(64):
+        for i in range(pairs - 1):
+            c, s, border = np.cos(angle[r, i]), np.sin(angle[r, i]), rng.choice([0.25, 0.75, 1.25])
+            x = rng.uniform(0.5, 1.5, 4000).astype(np.float32).astype(np.float64)
+            y = ((x * c - border) / s).astype(np.float32).astype(np.float64) if abs(s) > 0.1 else x
+            off = np.abs((x * c - border) - y * s)
+            good = np.nonzero((off >= 2.0 ** -34) & (off <= 2.0 ** -33) & (np.abs(x) + np.abs(y) <= 4.0))[0]
+            j = good[0] if len(good) else 0
+            planted[r, i] = len(good) > 0
+            key[r, first[i]], key[r, second[i]] = x[j], y[j] if len(good) else 0.0
+    assert planted.mean() > 0.5
+    d = case.make(sv)
+    assert (case.append(sv, d).dev_status == 0).all()
+    o = case.oracle()
+    assert (np.abs(np.abs(o["k"][:, 0, first][planted][:, None] - [0.25, 0.75, 1.25]).min(1) - 1.5 * 2.0 ** -34) <= 2.0 ** -34).all()
+    parts = packed.unblock(d["data"].cpu().numpy(), 16, dim)
+    codes, scales = (t[0].reshape(-1, 1, t.shape[-1])[o["slot"]] for t in parts[:2])
+    want_codes, want_scales, want = packed.quantize(o["k"])
+    assert np.array_equal(scales, want_scales) and (packed.SCALES[scales[:, 0, 0]] == 1.0).all()
+    assert np.array_equal(packed.values(codes, scales), want)
+
+
 @BOTH
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dim,page,staged", [(64, 16, False), (128, 1, True), (256, 5, False), (96, 16, True)])
