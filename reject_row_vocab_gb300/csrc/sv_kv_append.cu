@@ -59,6 +59,16 @@ struct AppendParams {
   int32_t passes, chunks, per;  // a row's passes over its heads, dealt out to `chunks` warps
 };
 
+// Sums and products of floats as pairs of floats (Dekker, Knuth): the rounded result in x, what it lacks in y.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v)));
+}
+__device__ __forceinline__ float2 two_product(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return make_float2(p, __fmaf_rn(a, b, -p));
+}
+
 // Part of a turn, hi + lo, of position * f.  Positions below 2^22 in pairs of floats: f / 2 pi to 2^-49 of itself, the product
 // exactly, whole turns taken off.  (The 64-bit unit does two lanes a clock: 8192 rows took 8 us of it.)
 __device__ __forceinline__ float2 part_of_turn(float position, float f) {
@@ -68,6 +78,21 @@ __device__ __forceinline__ float2 part_of_turn(float position, float f) {
   const float x = h * position, low = fmaf(l, position, fmaf(h, position, -x));
   const float part = x - rintf(x), t = part + low;
   return make_float2(t, low - (t - part));
+}
+// The same to 2^-47 of a radian: f / 2 pi to 2^-70 of itself in three floats, its products with the position exactly as far as that
+// counts, and their sum in a pair.  (Above, what one float holds beside the first product is rounded to 2^-48 of all turns: 2^-31
+// of a radian at 100 000, 2^-26 at 2^22.)
+__device__ __forceinline__ float2 part_of_turn_in_pairs(float position, float f) {
+  constexpr double kTurn = 0.15915494309189535, kTurnLack = -9.839338337591243e-18;  // 1 / 2 pi
+  constexpr float kHi = static_cast<float>(kTurn);
+  constexpr float kMid = static_cast<float>(kTurn - static_cast<double>(kHi));
+  constexpr float kLo = static_cast<float>(kTurn - static_cast<double>(kHi) - static_cast<double>(kMid) + kTurnLack);
+  const float h = __fmul_rn(f, kHi);
+  const float2 m = two_product(f, kMid), l = two_sum(__fmaf_rn(f, kHi, -h), m.x);
+  const float rest = __fadd_rn(l.y, __fmaf_rn(f, kLo, m.y));
+  const float2 x = two_product(h, position), y = two_product(l.x, position), low = two_sum(x.y, y.x);
+  const float2 t = two_sum(__fsub_rn(x.x, rintf(x.x)), low.x);
+  return make_float2(t.x, __fadd_rn(t.y, __fadd_rn(low.y, __fmaf_rn(rest, position, y.y))));
 }
 // Of any position, in pairs of doubles: f / 2 pi to 2^-104 of itself, a position's upper and lower 32 bits by themselves (2^63
 // has 2^60 whole turns).
@@ -92,16 +117,6 @@ __device__ __forceinline__ float2 turn_of(float2 t) {
   sincospif(2.0f * t.x, &s, &c);
   const float lo = t.y * 6.28318531f;
   return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
-}
-
-// Sums and products of floats as pairs of floats (Dekker, Knuth): the rounded result in x, what it lacks in y.
-__device__ __forceinline__ float2 two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
-  return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v)));
-}
-__device__ __forceinline__ float2 two_product(float a, float b) {
-  const float p = __fmul_rn(a, b);
-  return make_float2(p, __fmaf_rn(a, b, -p));
 }
 
 // Cosine and sine of k / 64 of a turn, in pairs of floats.
@@ -317,7 +332,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 5) k_kv_append(const Append
 #pragma unroll
       for (int i = 0; i < kMaxPairs / 32; ++i)
         if (i * 32 + lane < n) {
-          const float2 t = far ? part_of_turn_far(pos, freq[i]) : part_of_turn(static_cast<float>(pos), freq[i]);
+          const float2 t = far       ? part_of_turn_far(pos, freq[i])
+                           : kPacked ? part_of_turn_in_pairs(static_cast<float>(pos), freq[i])
+                                     : part_of_turn(static_cast<float>(pos), freq[i]);
           if constexpr (kPacked) {
             const float4 u = turn_in_pairs(t);
             s_turn[warp][i * 32 + lane] = make_float2(u.x, u.z), s_lack[warp][i * 32 + lane] = make_float2(u.y, u.w);

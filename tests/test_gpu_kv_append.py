@@ -228,7 +228,7 @@ def test_keys_are_stored_as_exact_rotations_would_be(sv, dtype, pairs, interleav
 
 
 @pytest.mark.parametrize("dim,pairs,interleaved", [(32, 8, True), (64, 16, False), (64, 13, False)])
-@pytest.mark.parametrize("start", [100, 2 ** 22, 2 ** 30 + 1, 2 ** 44 + 3])
+@pytest.mark.parametrize("start", [100, 4000, 20_000, 100_000, 10 ** 6, 2 ** 22 - 64, 2 ** 22, 2 ** 30 + 1, 2 ** 44 + 3])
 def test_keys_next_to_a_border(sv, dim, pairs, interleaved, start):
     """Values that lie 2^-34 to 2^-33 beside the middle of two codes, at near and far positions.  (What may be off by rounding: sines
     and cosines by 2^-37 each, of pairs of up to 4 together.)"""
