@@ -602,8 +602,12 @@ class _OtherDevice:
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on_device(index):
-    return _CURRENT if index < 0 or _current_device() == index else _OtherDevice(index)
+def _run_on(index, fn, *args):
+    """The library's call, on its tensors' device."""
+    if index < 0 or _current_device() == index:  # (nearly always: a context entered for nothing costs a small call a tenth of its time)
+        return fn(*args)
+    with _OtherDevice(index):
+        return fn(*args)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -652,6 +656,8 @@ class PagedKvCache:
 
     Holds the tensors and the library's description of them; make it once and use it for every call."""
 
+    packed = False
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor):
         for t, name in ((k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor) or t.dim() != 5:
@@ -683,6 +689,8 @@ class PackedKvCache:
     A block holds a page's entries of one head: block_bytes(page_size, head_dim) bytes of it are used.  head_dim is a multiple
     of 32.  dtype (bf16 or fp32) is that of the rows that go with the cache: keys and values that kv_append takes and kv_read
     gives back; paged_attention takes bf16.  Stands wherever a PagedKvCache does; make it once and use it for every call."""
+
+    packed = True
 
     def __init__(self, data: torch.Tensor, page_table: torch.Tensor, *, page_size: int, head_dim: int,
                  dtype: torch.dtype = torch.bfloat16):
@@ -727,9 +735,9 @@ class PackedKvCache:
 
 
 def _require_cache(cache):
-    if not isinstance(cache, (PagedKvCache, PackedKvCache)):
+    if type(cache) is not PagedKvCache and not isinstance(cache, (PagedKvCache, PackedKvCache)):
         raise TypeError("cache must be a PagedKvCache or a PackedKvCache")
-    if cache.device.type != "cuda":
+    if cache.index < 0:
         raise ValueError("the cache must be on a CUDA device (got %s): the library has no CPU path" % cache.device)
 
 
@@ -825,15 +833,14 @@ def paged_attention(q, cache, seq_lens, *, layer: int = 0, max_len: Optional[int
     if status is not None:
         _need(status, "out.dev_status", torch.int32, batch, dev, index)
     _need(ws, "ws", torch.uint8, 0, dev, index)
-    fn = lib.spec_verify_packed_attention if isinstance(cache, PackedKvCache) else lib.spec_verify_paged_attention
-    with _on_device(index):
-        code = fn(
-            q.data_ptr(), q_steps[0], q_steps[1], heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
-            seq_lens.data_ptr(), _addr(row_slots), _addr(mask), dim ** -0.5 if scale is None else scale,
-            o.data_ptr(), o_steps[0], o_steps[1], _addr(lse), _addr(status), ws.data_ptr(), ws.numel(),
-            _call_stream(stream, dev))
+    fn = lib.spec_verify_packed_attention if cache.packed else lib.spec_verify_paged_attention
+    code = _run_on(
+        index, fn, q.data_ptr(), q_steps[0], q_steps[1], heads, cache.ref, layer, batch, rows, max_len, _addr(cu_seqlens),
+        seq_lens.data_ptr(), _addr(row_slots), _addr(mask), dim ** -0.5 if scale is None else scale,
+        o.data_ptr(), o_steps[0], o_steps[1], _addr(lse), _addr(status), ws.data_ptr(), ws.numel(),
+        _call_stream(stream, dev))
     if code:
-        _check("spec_verify_packed_attention" if isinstance(cache, PackedKvCache) else "spec_verify_paged_attention", code)
+        _check("spec_verify_packed_attention" if cache.packed else "spec_verify_paged_attention", code)
     return out
 
 
@@ -858,13 +865,12 @@ def kv_commit(cache, commit_cu, commit_src_slot, commit_dst_pos, *, max_len: int
         with _on(stream):
             dev_status = torch.empty(batch, dtype=torch.int32, device=dev)
     _need(dev_status, "dev_status", torch.int32, batch, dev, index)
-    fn = lib.spec_verify_packed_kv_commit if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_commit
-    with _on_device(index):
-        code = fn(
-            cache.ref, batch, max_len, min(commit_src_slot.numel(), commit_dst_pos.numel()), commit_cu.data_ptr(),
-            commit_src_slot.data_ptr(), commit_dst_pos.data_ptr(), dev_status.data_ptr(), _call_stream(stream, dev))
+    fn = lib.spec_verify_packed_kv_commit if cache.packed else lib.spec_verify_kv_commit
+    code = _run_on(
+        index, fn, cache.ref, batch, max_len, min(commit_src_slot.numel(), commit_dst_pos.numel()), commit_cu.data_ptr(),
+        commit_src_slot.data_ptr(), commit_dst_pos.data_ptr(), dev_status.data_ptr(), _call_stream(stream, dev))
     if code:
-        _check("spec_verify_packed_kv_commit" if isinstance(cache, PackedKvCache) else "spec_verify_kv_commit", code)
+        _check("spec_verify_packed_kv_commit" if cache.packed else "spec_verify_kv_commit", code)
     return dev_status
 
 
@@ -979,13 +985,13 @@ def kv_append(cache, k, v, *, layer: int = 0, seq_lens=None, max_len: Optional[i
             raise ValueError("out.q is required with q")
         os = _head_rows(out.q, "out.q", rows, heads, dim, cache.dtype, dev, index)
     _need(out.dev_status, "out.dev_status", torch.int32, batch, dev, index)
-    fn = lib.spec_verify_packed_kv_append if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_append
-    with _on_device(index):
-        code = fn(cache.ref, layer, ctypes.byref(desc), _addr(positions), None if rotation is None else rotation.ref,
-                  k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1], heads,
-                  None if q is None else out.q.data_ptr(), os[0], os[1], out.dev_status.data_ptr(), _call_stream(stream, dev))
+    fn = lib.spec_verify_packed_kv_append if cache.packed else lib.spec_verify_kv_append
+    code = _run_on(
+        index, fn, cache.ref, layer, ctypes.byref(desc), _addr(positions), None if rotation is None else rotation.ref,
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _addr(q), qs[0], qs[1], heads,
+        None if q is None else out.q.data_ptr(), os[0], os[1], out.dev_status.data_ptr(), _call_stream(stream, dev))
     if code:
-        _check("spec_verify_packed_kv_append" if isinstance(cache, PackedKvCache) else "spec_verify_kv_append", code)
+        _check("spec_verify_packed_kv_append" if cache.packed else "spec_verify_kv_append", code)
     return out
 
 
@@ -1047,12 +1053,12 @@ def kv_read(cache, *, layer: Optional[int] = None, seq_lens=None, max_len: Optio
     if not same:
         raise ValueError("out.k and out.v must have the same strides")
     _need(out.dev_status, "out.dev_status", torch.int32, batch, dev, index)
-    fn = lib.spec_verify_packed_kv_read if isinstance(cache, PackedKvCache) else lib.spec_verify_kv_read
-    with _on_device(index):
-        code = fn(cache.ref, 0 if layer is None else layer, layers, ctypes.byref(desc), out.k.data_ptr(), out.v.data_ptr(),
-                  st[0], st[1], st[2], out.dev_status.data_ptr(), _call_stream(stream, dev))
+    fn = lib.spec_verify_packed_kv_read if cache.packed else lib.spec_verify_kv_read
+    code = _run_on(
+        index, fn, cache.ref, 0 if layer is None else layer, layers, ctypes.byref(desc), out.k.data_ptr(), out.v.data_ptr(),
+        st[0], st[1], st[2], out.dev_status.data_ptr(), _call_stream(stream, dev))
     if code:
-        _check("spec_verify_packed_kv_read" if isinstance(cache, PackedKvCache) else "spec_verify_kv_read", code)
+        _check("spec_verify_packed_kv_read" if cache.packed else "spec_verify_kv_read", code)
     return out
 
 

@@ -352,3 +352,16 @@ def test_angles_of_far_positions_against_rational_numbers():
             z = z * z  # (twice the error each time)
             far = packed.angles([int(p) << k], f)
             assert (k < 3 or p == 3 or np.abs(far).max() <= np.pi) and np.abs(np.exp(1j * far) - z).max() <= 2.0 ** (k - 51)
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """Another device than the current one is entered and left again, a refused call's too; the current one is not touched."""
+    now, moves = [1], []
+    monkeypatch.setattr(sv, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "set_device", lambda d: (moves.append(d), now.__setitem__(0, d)))
+    assert sv._run_on(1, lambda *a: (now[0], a), 5, 6) == (1, (5, 6)) and moves == []
+    assert sv._run_on(0, lambda *a: (now[0], a), 7) == (0, (7,)) and moves == [0, 1]
+    with pytest.raises(ctypes.ArgumentError):
+        sv._run_on(0, sv.load_library().spec_verify_packed_kv_block_bytes, "16", 64)
+    assert moves == [0, 1, 0, 1] and now == [1]
