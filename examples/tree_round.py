@@ -1,9 +1,9 @@
 """Rounds of tree speculative decoding with a toy model of one attention layer, all on the library's calls.
 
-Each round: a draft head proposes a tree a request; the rows' keys and values go to staged slots of the paged cache;
-`paged_attention` gives the verify rows' attention under the tree's mask; `greedy_tree` accepts a path; `kv_commit` moves the
-accepted rows' keys and values into place; `token_logprobs` gives the committed tokens' log probabilities with the most likely
-alternatives; and the draft head takes a step on the committed tokens, its gradient from `token_logprobs_backward`.
+Each round: a draft head proposes a tree a request; `kv_append` puts the rows' keys and values into staged slots of the paged
+cache; `paged_attention` gives the verify rows' attention under the tree's mask; `greedy_tree` accepts a path; `kv_commit`
+moves the accepted rows' keys and values into place; `token_logprobs` gives the committed tokens' log probabilities with the
+most likely alternatives; and the draft head takes a step on the committed tokens, its gradient from `token_logprobs_backward`.
 
     python examples/tree_round.py
 """
@@ -51,15 +51,16 @@ def run(prompts, rounds=8, vocab=1000, page=16, top_k=3, lr=0.5, seed=0, device=
     order = torch.randperm(B * room, generator=torch.Generator().manual_seed(seed))
     cache = sv.PagedKvCache(k, v, order.to(torch.int32).view(B, room).to(device))
     row_slots = torch.arange(B * N, device=device) + B * room * page
-    flat_k, flat_v = k.view(-1, m.kv_heads, m.dim), v.view(-1, m.kv_heads, m.dim)
 
     # the prompts' keys and values, all but the last token, which is the first anchor
-    for b, p in enumerate(prompts):
-        at = torch.arange(len(p) - 1, device=device)
-        _, kk, vv = m.qkv(m.hidden(torch.tensor(p[:-1], device=device, dtype=torch.long), at))
-        slots = cache.page_table[b, at // page].long() * page + at % page
-        flat_k[slots], flat_v[slots] = kk, vv
-    seq_lens = torch.tensor([len(p) - 1 for p in prompts], dtype=torch.int64, device=device)
+    lens = [len(p) - 1 for p in prompts]
+    ids = torch.tensor([t for p in prompts for t in p[:-1]], device=device, dtype=torch.long)
+    at = torch.tensor([i for n in lens for i in range(n)], device=device, dtype=torch.long)
+    cu = torch.tensor([sum(lens[:b]) for b in range(B + 1)], dtype=torch.int32, device=device)
+    _, kk, vv = m.qkv(m.hidden(ids, at))
+    filled = sv.kv_append(cache, kk, vv, seq_lens=torch.zeros(B, dtype=torch.int64, device=device), cu_seqlens=cu,
+                          max_len=max(lens + [1]))
+    seq_lens = torch.tensor(lens, dtype=torch.int64, device=device)
     anchor = torch.tensor([p[-1] for p in prompts], device=device)
 
     parents = torch.tensor([PARENTS] * B, dtype=torch.int32, device=device)
@@ -79,7 +80,8 @@ def run(prompts, rounds=8, vocab=1000, page=16, top_k=3, lr=0.5, seed=0, device=
             guess = (m.hidden(tokens[:, up].long(), tree["positions"][:, up]) @ draft_head).topk(2).indices
             tokens[:, node] = guess[:, PARENTS[:node].count(up)]
         x = m.hidden(tokens.view(-1).long(), tree["positions"].view(-1))
-        q, flat_k[row_slots], flat_v[row_slots] = m.qkv(x)
+        q, kk, vv = m.qkv(x)
+        sv.kv_append(cache, kk, vv, seq_lens=seq_lens, max_len=N, row_slots=row_slots, out=filled)
 
         sv.paged_attention(q, cache, seq_lens, max_len=N, row_slots=row_slots, mask=tree["mask"], out=attn_out, ws=attn_ws)
         logits = (x + attn_out.out.view(B * N, -1) @ m.o) @ m.head
@@ -99,7 +101,7 @@ def run(prompts, rounds=8, vocab=1000, page=16, top_k=3, lr=0.5, seed=0, device=
         draft_head -= lr * xd.t() @ grad / xd.square().sum(1).mean()
         losses.append(float(-kept.logprob.sum() / count))
 
-        bits = torch.cat([status, attn_out.dev_status, done.dev_status, lp.flags])
+        bits = torch.cat([filled.dev_status, status, attn_out.dev_status, done.dev_status, lp.flags])
         assert int(bits.abs().sum()) == 0, "data errors"
         for b, n in enumerate(done.num_out.tolist()):
             tokens_of[b] += done.out_tokens[b, :n].tolist()
