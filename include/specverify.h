@@ -548,7 +548,9 @@ sv_status_t spec_verify_token_logprobs_backward(const void* logits, sv_dtype_t d
  * have none.  head_dim is a multiple of 32, at most 256.  The strides are in
  * bytes, multiples of 16, like the base pointer.  Slots, positions and the page
  * table are those of sv_kv_cache_t.  dtype is that of the rows that go with the
- * cache: new keys and values, queries, outputs.
+ * cache: new keys and values, queries, outputs (attention takes bf16 alone).
+ * Pages whose size divides 128, or is a multiple of it, are brought in block by
+ * block; all others row by row, which takes attention up to six times as long.
  */
 typedef struct {
   void* data;
@@ -589,7 +591,8 @@ typedef struct {
  * position * inv_freq[i].  A pair is columns (i, i + pairs), or (2 i, 2 i + 1)
  * when interleaved; columns from 2 * pairs on are left as they are.  The
  * rotated columns are also multiplied by magnitude (1 for none).  Angles are
- * reduced in more than fp32: far positions lose nothing.
+ * reduced in more than fp32, to 2^-25 of a radian or better for inv_freq up to 1:
+ * far positions, to the ends of 64 bits, lose nothing.
  */
 typedef struct {
   const float* inv_freq; /* [pairs], device */
@@ -619,9 +622,10 @@ typedef struct {
  * Arithmetic is fp32, rounded once to the dtype; values are copied as they are.
  * The 4-bit cache takes the rotated values before any rounding: each group's
  * scale is the one nearest to its largest magnitude / 6, each code the one nearest
- * to its value, both half way to the even one, decided in 64 bits where fp32
- * leaves open which that is.  Magnitudes above 61440 are stored as 61440, a
- * NaN as 0.  Two rows of a call must not have the same place.
+ * to its value, both half way to the even one.  Keys are rotated in twice the
+ * bits of fp32 for that: the choice is that of the exact rotation wherever it is
+ * further than 2^-37 (|x| + |y|) magnitude from the middle of two (inv_freq up to 1).
+ * Magnitudes above 61440 are stored as 61440, a NaN as 0.  Two rows of a call must not have the same place.
  *
  * dev_status [batch] is OR-ed into (zero it first): SV_DEV_BAD_LAYOUT for an
  * invalid row range or a negative seq_lens[b] (nothing of the request is

@@ -4,7 +4,9 @@
 // A tile is 128 keys of a cache head.  It lies in shared memory as the cache's own blocks, one after the other: a page's block
 // is one bulk copy, K and V, codes and scales.  Of pages of a multiple of 128 entries a tile is a part, in four copies (codes
 // and scales of K and of V), as a block of 128.  Rows that lie apart (new rows staged elsewhere; all rows where 128 and the page
-// size do not divide one another) are gathered to the places that they would have.  Whatever lies in places of keys that are not
+// size do not divide one another) are gathered to the places that they would have, which takes a warp 40 turns a tile: one token of
+// 128 requests of 64 to 8192 in pages of 48 to 200 such entries 1000 us (153 in pages of 16), blocks of 16 rows of 64 requests 103
+// us (86).  Whatever lies in places of keys that are not
 // there stands for finite numbers (every pattern of bits does): scores with it are masked, and its weights are 0.
 #pragma once
 

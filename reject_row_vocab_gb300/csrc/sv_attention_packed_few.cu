@@ -25,10 +25,11 @@
 // shared memory and goes on; the last one joins them and writes the rows, or
 // the block's part of the unit.
 //
-// Bound by its instructions: 330 for a slice of 16 keys (64 conversions, 64 products
-// with scales), which two warps on each scheduler issue at every other clock, the
-// bytes being there in time (the same pages again and again, out of L2, take as
-// long).  One token of 128 requests of 64 to 8192, 32 heads of 128 on 8: 153 us,
+// Bound by its instructions' order: of the 330 for a slice of 16 keys (64 conversions, 64
+// products with scales) most wait for the one before, and two warps on each
+// scheduler, all that the registers hold, issue one at every other clock (no pipe is
+// busy for more than 42 % of the time).  The bytes are there in time (the same pages
+// again and again, out of L2, take as long).  One token of 128 requests of 64 to 8192, 32 heads of 128 on 8: 153 us,
 // 4.0 TB/s (over bf16 320, for 3.6 times the bytes); bringing the tiles in alone
 // takes 110 us.  Two slices a warp side by side: 153, one
 // after the other by twelve warps 157, one by sixteen 166; one team of four warps 171;

@@ -1,5 +1,5 @@
 // Attention over the 4-bit cache for many query rows: the kernel of
-// sv_attention_wide.cu on tiles that eight of its warps unpack to half floats,
+// sv_attention_wide.cuh on tiles that eight of its warps unpack to half floats,
 // which hold the cache's values exactly.
 //
 // Each unpacking warp has 16 keys of a tile; a lane has 32 columns of one key
@@ -22,9 +22,11 @@
 // 1100 of the matrix unit, which multiplies 128 rows whether there are as many or not,
 // and by a unit's end (5400 clocks: two threads' halves of a row are put together by
 // way of 8 KB).  Measured: blocks of 16 rows of 64 requests of up to 4000, 32 heads of
-// 128 on 8, pages of 64: 86 us (102 over bf16, for 3.6 times the bytes); trees of 17
+// 128 on 8, pages of 64: 86 us (100 over bf16, for 3.6 times the bytes); trees of 17
 // nodes of 16 requests in pages of one slot: 22 us; 5 rows of two requests of 60000 to
-// 100000: 49 us (64).
+// 100000: 49 us (63); a causal block of 1024 rows of one request, pages of 16: 51 us
+// without history, 118 behind 4000 (heads of 256: 90 and 300), K and V unpacked again for
+// every tile of rows and all key tiles gone through.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include "sv_attention_packed.cuh"

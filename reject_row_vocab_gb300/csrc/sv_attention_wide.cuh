@@ -1,6 +1,48 @@
-// The kernel for many query rows, on the fifth-generation tensor cores (described in sv_attention_wide.cu): what it does with
-// tiles of K and V that lie in the ring, and the join of parts.  Where the tiles come from is the Source: a bf16 cache's rows as
-// they are, or a 4-bit cache's values in bf16 (sv_attention_packed_wide.cu).
+// Attention over the paged cache for many query rows, on the fifth-generation
+// tensor cores: tiles of 128 rows and 128 keys.  Where the tiles come from is the
+// Source: a bf16 cache's rows as they are (sv_attention_wide.cu, and what follows), or
+// a 4-bit cache's values in half floats (sv_attention_packed_wide.cu).
+//
+//   S = Q K^T (128 x 128, tensor memory)     one warp issues the products
+//   P = 2^(c (S - m)), l += sum P            one thread a row: no exchange
+//   O += P V  (P from tensor memory)         accumulated in tensor memory
+//
+// Four softmax warps, four loading warps, one warp that issues the matrix
+// instructions (a lane of it, with what they take in uniform registers: by one
+// thread alone an instruction took 70 clocks to issue, about as long as to run),
+// one that loads the next unit's Q and one that walks the line of tiles ahead of
+// them all, connected by mbarriers.  The loading warps bring
+// K and V through the page table into a ring of tiles in the 128-byte swizzle
+// the matrix unit reads, and run ahead over the ends of units.  S has two
+// buffers, so the next tile's scores are computed while this one's weights are
+// taken; P overwrites its own S.  The reference m moves (and O is rescaled) only
+// when a row's maximum has grown by more than 2^8: the weights stay below 2^8,
+// the sums in fp32, and the result does not depend on the reference.
+//
+// The weights are rounded to bf16 for the product with V (its operands have one
+// type); l sums the unrounded ones, in fp32.  That leaves an error of 0.0022 of
+// the outputs' norm, where rounding the outputs alone leaves 0.0017.  Two bf16
+// values a weight, as the kernel for few rows has, would give 0.0017 here too,
+// but lengthen the softmax warps' chain: 64 requests of 16 rows took 131 us
+// instead of 102, two long ones 70 instead of 64.  (Half floats: below.)
+//
+// Bound by the bytes of K and V where histories are long, by the chain from
+// scores to weights to sums at each unit's ends where they are short.
+// Measured: blocks of 16 rows of 64 requests of up to 4000, 32 heads of 128 on 8
+// in the cache: 100 us, 5.7 TB/s; 32 requests, heads of 256: 107 us; 5 rows of
+// two requests of 60000 to 100000: 63 us, 5.0 TB/s (17 of them outside the
+// stream); trees of 17 nodes of 16 requests in pages of one slot: 21 us; a
+// causal block of 1024 rows of one request: 72 us without history, 148 (513
+// TFLOP/s) behind 4000, all key tiles gone through by every tile of rows.
+//
+// Units that several blocks share are joined by a second kernel, spread over
+// the whole GPU.  (By the last of the unit's blocks alone, two long requests
+// took 90 us instead of 63, a 64-request block 127 instead of 118.)
+//
+// Every wait is bounded; a wait that gives up raises SV_DEV_TIMEOUT, lets all
+// warps leave, and the block frees its tensor memory.
+//
+//   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #pragma once
 
 #include <cstdint>
@@ -144,7 +186,7 @@ struct RowSource {
   static __host__ __device__ constexpr int extra_bytes() { return 0; }
 };
 
-// Softmax warps, loading warps, and a warp each to issue, to load Q, to plan.
+// Softmax warps, loading warps, and a warp each to issue, to load Q and to plan (with half floats one does both).
 template <class Source>
 constexpr int kWideThreads = kSoftmaxThreads + 32 * Source::kWarps + (Source::kHalf ? 64 : 96);
 // Of half floats: a new reference lies this far below the maximum, in powers of two (weights reach 2^14; a half float's least is 2^-24).

@@ -9,20 +9,24 @@
 // eight columns of a head: a pair's other half is in the lane itself or one
 // shuffle away, and the row's sines and cosines are computed once, by the
 // warp, and kept in registers for all heads.  The angle is reduced to a part of
-// a turn in twice the bits of a float.
+// a turn in more than a float's bits: to 2^-25 of a radian up to position 2^22, to
+// 2^-43 beyond.
 //
 // The 4-bit cache: 16 columns are two lanes, one shuffle gives their largest
 // magnitude.  Which scale and which code is nearest hangs on which side of a
 // border a value lies, and a rotation in fp32 gets that wrong for one value in a
-// million.  So its keys are turned in pairs of floats, sines and cosines included
-// (2^-37 and better), and rounded to odd, which keeps every border on its side.
+// million.  So its keys are turned in pairs of floats: angles to 2^-43 of a radian at
+// any position, sines and cosines to 2^-37, products and their sum to 2^-46.  The sum is
+// rounded to odd, which keeps it on its side of every border that the exact one is
+// further than 2^-37 (|x| + |y|) from.
 //
-// Bound by the rows' bytes: 8192 rows of 32 + 8 + 8 heads of 128 in bf16, 39 us
-// (5.3 TB/s); over 4 bits by its instructions (half of the issue slots, with as much
-// time again spent on steps that wait for one another): 57 us alone, 49 with keys
-// turned in fp32.  Five blocks of four warps and four passes in flight are the best
-// of both (two passes: 51 and 63 us; four blocks: 51 and 64).  A row's heads go to as
-// many warps as give every multiprocessor sixteen: one token takes 8 us of the GPU.
+// Bound by the rows' bytes: 8192 rows of 32 + 8 + 8 heads of 128 in bf16, 40 us
+// (5.2 TB/s); over 4 bits by steps that wait for one another, twenty warps a
+// multiprocessor not being enough to hide them (52 % of the issue slots are used, the
+// ALU 37 %): 51.5 us, 45.4 with keys turned in fp32.  Five blocks of four warps and
+// four passes in flight are the best of both (two passes: 47 and 57.6 us; four blocks:
+// 45 and 57).  A row's heads go to as many warps as give every multiprocessor
+// sixteen: one token takes 8 us of the GPU.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cmath>
@@ -81,7 +85,7 @@ __device__ __forceinline__ float2 part_of_turn(float position, float f) {
 }
 // The same to 2^-47 of a radian: f / 2 pi to 2^-70 of itself in three floats, its products with the position exactly as far as that
 // counts, and their sum in a pair.  (Above, what one float holds beside the first product is rounded to 2^-48 of all turns: 2^-31
-// of a radian at 100 000, 2^-26 at 2^22.)
+// of a radian at 100 000, 2^-25 at 2^22.)
 __device__ __forceinline__ float2 part_of_turn_in_pairs(float position, float f) {
   constexpr double kTurn = 0.15915494309189535, kTurnLack = -9.839338337591243e-18;  // 1 / 2 pi
   constexpr float kHi = static_cast<float>(kTurn);

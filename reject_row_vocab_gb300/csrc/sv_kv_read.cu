@@ -5,10 +5,11 @@
 //
 // Bound by the bytes of the output.  A warp takes one row, or a part of its
 // heads and layers; a lane has eight columns of a head, or, of codes, a group of
-// 16 with its scale.  8192 rows of 8 heads of 128 out of 4 bits: 17.5 us (43 MB: 2.5
+// 16 with its scale.  8192 rows of 8 heads of 128 out of 4 bits: 15 us (43 MB: 2.9
 // TB/s; the floor is 6.4), of which looking up a row's place and the start take
-// half; 384 rows of 32 layers 25 us.  Four passes in flight: eight take 20.5 and 27 us,
-// two as long as four; twice the warps a row 20.5.
+// half, and as long out of bf16 (67 MB, 4.5 TB/s); 384 rows of 32 layers out of 4 bits
+// 21 us.  Four passes in flight: eight take 15.9 and 23.3 us, two 14.5 and 21.7 (and
+// 16.5 out of bf16); twice the warps a row 16.6 and 20.7.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>

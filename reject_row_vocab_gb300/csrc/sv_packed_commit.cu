@@ -9,9 +9,9 @@
 // 128).  Places are found once for the layers that a block goes through.
 //
 // Bound by the chain lists, places, rows, and by pieces of 64 and 8 bytes: 384 rows of
-// 64 requests in 32 layers, 8 heads of 128, take 19 us (28 MB there and back; with
-// the sectors that the pieces touch it is 57).  Blocks of 512 threads take 21 us, a
-// quarter of the blocks 23.
+// 64 requests in 32 layers, 8 heads of 128, take 16.8 us (28 MB there and back; with
+// the sectors that the pieces touch it is 57), the block's barrier for each layer among
+// them.  Blocks of 512 threads and a quarter of the blocks take 21.5 us.
 //
 //   [E2D] "从 EAGLE 到 DFlash 2：SGLang 与 SpecForge 的投机解码训练和推理"
 #include <cstdint>

@@ -688,7 +688,9 @@ class PackedKvCache:
 
     A block holds a page's entries of one head: block_bytes(page_size, head_dim) bytes of it are used.  head_dim is a multiple
     of 32.  dtype (bf16 or fp32) is that of the rows that go with the cache: keys and values that kv_append takes and kv_read
-    gives back; paged_attention takes bf16.  Stands wherever a PagedKvCache does; make it once and use it for every call."""
+    gives back.  paged_attention takes bf16: a cache of fp32 rows cannot be attended to.  Pages of 16, 32, 64 or a multiple of 128
+    entries are the fast ones for attention (those that neither divide 128 nor are a multiple of it are gathered row by row).  Stands
+    wherever a PagedKvCache does; make it once and use it for every call."""
 
     packed = True
 
