@@ -604,7 +604,8 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 
 def _run_on(index, fn, *args):
     """The library's call, on its tensors' device."""
-    if index < 0 or _current_device() == index:  # (nearly always: a context entered for nothing costs a small call a tenth of its time)
+    # (nearly always the current one: a context entered for nothing costs a small call a tenth of its time)
+    if index < 0 or _current_device() == index:
         return fn(*args)
     with _OtherDevice(index):
         return fn(*args)
